@@ -16,7 +16,14 @@
  *   pkv_paged_attention_prefill  causal attention of a prompt's (or a prompt chunk's)
  *                                new tokens over the cache;
  *   pkv_decode_append            a decode step of one new token per sequence whose
- *                                cache write can run inside the decode kernel.
+ *                                cache write can run inside the decode kernel;
+ *   pkv_rotary_and_cache         rotary positions for queries and keys, the keys and
+ *                                values written to the cache in the same pass;
+ *   pkv_quantize_and_cache       the cache write into a token-scaled 8-bit integer cache
+ *                                (one scale per token and KV head, found on the way);
+ *   pkv_read_cache               cached tokens read back as values;
+ *   pkv_paged_attention_decode_quantized  decode over a token-scaled cache;
+ *   pkv_paged_attention_tree     attention of drafted token trees over the cache.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -35,6 +42,9 @@
  *   descriptor's `scale` (stored code * scale = value), or one scale per KV head in
  *   `head_scales` (ultralytics.com glossary "PagedAttention", section "관련 기법": an
  *   FP8 cache halves the memory of a 16-bit one); other dtypes ignore `scale`.
+ *   Token-scaled caches: PKV_I8 codes with one fp32 scale per (slot, KV head) in two
+ *   arrays beside the caches (code * scale = value); only the calls that take those
+ *   arrays (k_scales, v_scales) accept them.
  *   Queries and outputs: PKV_F32 or PKV_BF16, the output in the query's dtype.
  *   Supported head_dim: 64 and 128.  Supported block_size: 2, 4, 8, 16, 32.
  * Streams.  `stream` is a cudaStream_t (NULL = the legacy default stream) of the
@@ -69,7 +79,8 @@ typedef enum pkv_dtype {
   PKV_BF16 = 1,
   PKV_FP8_E4M3 = 2,
   PKV_I32 = 3,
-  PKV_I64 = 4
+  PKV_I64 = 4,
+  PKV_I8 = 5
 } pkv_dtype;
 
 typedef enum pkv_status {
@@ -84,7 +95,8 @@ typedef enum pkv_status {
 #define PKV_DEVERR_TABLE_ENTRY 0x1u  /* block-table entry outside [0, num_blocks) */
 #define PKV_DEVERR_SLOT 0x2u         /* slot >= num_blocks * block_size */
 #define PKV_DEVERR_COPY_PAIR 0x4u    /* copy pair outside [0, num_blocks) */
-#define PKV_DEVERR_CONTEXT_LEN 0x8u  /* context_len < 0 or > max_blocks_per_seq * block_size */
+#define PKV_DEVERR_CONTEXT_LEN 0x8u  /* context_len < 0 or > max_blocks_per_seq * block_size, or
+                                        query rows that do not fit it, the batch or the mask */
 #define PKV_DEVERR_TIMEOUT 0x10u     /* a bounded wait for an async copy ran out */
 #define PKV_DEVERR_COPY_OVERLAP 0x20u /* copy pairs: a destination repeated or also a source
                                         (checked only with PKV_OPT_DEBUG_SYNC on) */
@@ -317,6 +329,181 @@ pkv_status pkv_reshape_and_cache_amax(const pkv_tensor* key, const pkv_tensor* v
                                       const pkv_tensor* key_cache, const pkv_tensor* value_cache,
                                       const pkv_tensor* slot_mapping, float* k_amax, float* v_amax,
                                       pkv_stream stream);
+
+/*
+ * Rotary positions: how pkv_rotary_and_cache turns queries and keys.  Filled by
+ * pkv_rotary_init, or by hand for frequencies of the caller's own.  A plain host struct,
+ * read during the call only.
+ *
+ * Pair i (i < rotary_dim / 2) of a head at position p is turned by the angle
+ * a = p * frequency[i]:  (x, y) -> magnitude * (x cos a - y sin a, y cos a + x sin a).
+ * The pair is columns (i, i + rotary_dim / 2), or (2i, 2i + 1) if interleaved; columns
+ * from rotary_dim on are copied.  The angle is reduced in 64-bit fixed point (a whole
+ * turn = 2^64), so far positions lose nothing.
+ */
+typedef struct pkv_rotary {
+  int32_t rotary_dim;   /* even, 0 (no rotation) to head_dim */
+  int32_t interleaved;  /* 0 or 1 */
+  double magnitude;     /* factor on cosine and sine; 1 unless the scaling asks for another */
+  double frequency[64]; /* radians per position, for each pair */
+} pkv_rotary;
+
+/* How the frequencies f_i = base^(-2 i / rotary_dim) are changed for contexts longer than
+ * the `original` positions that a model was trained on, by `factor`:
+ *   NONE    unchanged;
+ *   LINEAR  f / factor (positions interpolated);
+ *   BASE    base replaced by base * factor^(d / (d - 2)), d = rotary_dim (> 2);
+ *   BANDS   by the turns r = original * f / 2 pi that a pair makes over the original
+ *           context: f / factor where r <= 1, f where r >= 4, between them a blend linear
+ *           in r;
+ *   RAMP    by the pair's index: f below the index of the pair that makes 32 turns, f /
+ *           factor above that of the pair that makes one turn, between them a blend linear
+ *           in the index (both rounded outwards and kept in 0 .. d - 1, at least 0.001
+ *           apart); magnitude = 0.1 ln(factor) + 1. */
+typedef enum pkv_rotary_scaling {
+  PKV_ROTARY_NONE = 0,
+  PKV_ROTARY_LINEAR = 1,
+  PKV_ROTARY_BASE = 2,
+  PKV_ROTARY_BANDS = 3,
+  PKV_ROTARY_RAMP = 4
+} pkv_rotary_scaling;
+
+/* Fill *rotary on the host.  rotary_dim even, 0 to 128; base finite and > 1; factor finite
+ * and >= 1, `original` > 0 for BANDS and RAMP; otherwise PKV_ERR_INVALID_ARG. */
+pkv_status pkv_rotary_init(pkv_rotary* rotary, int32_t rotary_dim, int32_t interleaved, double base,
+                           int32_t scaling, double factor, int64_t original);
+
+/*
+ * pkv_rotary_and_cache — rotate the new tokens' queries and keys by their positions and
+ * write the rotated keys and the values to the cache, in one pass.
+ *
+ * For token t: query_out[t, h] = rotate(query[t, h], positions[t]) for every query head,
+ * and, with slot = slot_mapping[t] >= 0, the cache write of pkv_reshape_and_cache with
+ * rotate(key[t, h], positions[t]) in place of the key.  The rotation is computed in
+ * binary32 and rounded once, to the query's dtype or to what the cache stores.  A token
+ * with slot < 0 has its query rotated and nothing written.
+ *
+ * query_out, query [num_tokens, num_heads, head_dim] f32 or bf16, last dim contiguous;
+ *                  query_out may be query itself (same pointer and strides), otherwise
+ *                  the two must not overlap.  num_heads may be 0.
+ * key, value       [num_tokens, num_kv_heads, head_dim], the query's dtype, same strides.
+ * positions        [num_tokens] int32 or int64, contiguous; any value, negative ones too.
+ * key_cache,
+ * value_cache      as for pkv_reshape_and_cache: the key's dtype or e4m3; or PKV_I8 with
+ *                  k_scales and v_scales as for pkv_quantize_and_cache (NULL otherwise).
+ * slot_mapping     [num_tokens] int64, contiguous, distinct slots.
+ * rotary           host pointer; rotary_dim <= head_dim; finite frequencies and magnitude.
+ * Base pointers and strides of query, query_out, key and value: multiples of 16 bytes.
+ */
+pkv_status pkv_rotary_and_cache(const pkv_tensor* query_out, const pkv_tensor* query, const pkv_tensor* key,
+                                const pkv_tensor* value, const pkv_tensor* positions,
+                                const pkv_tensor* key_cache, const pkv_tensor* value_cache,
+                                const pkv_tensor* k_scales, const pkv_tensor* v_scales,
+                                const pkv_tensor* slot_mapping, const pkv_rotary* rotary,
+                                pkv_stream stream);
+
+/*
+ * pkv_quantize_and_cache — write new tokens' K and V into a token-scaled 8-bit cache.
+ *
+ * For token t with slot = slot_mapping[t] >= 0, block b = slot / bs, offset o = slot % bs,
+ * KV head h and x = key[t, h, :] (V alike):
+ *   s = max_d |x_d| / 127            (IEEE binary32)
+ *   key_cache[b, h, o, d] = clamp(rint(x_d / s), -127, 127)   (binary32 quotient, ties to even)
+ *   k_scales[b, h, o] = s
+ * Unlike an e4m3 cache it needs no scale beforehand, and a token's error is at most half
+ * a step, max|x| / 254.  A row whose s would be below the smallest normal binary32 number
+ * (max |x| < 1.5e-36, a row of zeros among them) is stored as zeros with s = 0; a row
+ * holding an infinity or a NaN as zeros with s = NaN, so that what reads it shows it.
+ *
+ * key, value           as for pkv_reshape_and_cache, f32 or bf16.
+ * key_cache,
+ * value_cache          PKV_I8, the cache layout above.
+ * k_scales, v_scales   [num_blocks, num_kv_heads, block_size] f32, last dim contiguous,
+ *                      same strides.
+ * slot_mapping         [num_tokens] int64, contiguous, distinct slots.
+ */
+pkv_status pkv_quantize_and_cache(const pkv_tensor* key, const pkv_tensor* value, const pkv_tensor* key_cache,
+                                  const pkv_tensor* value_cache, const pkv_tensor* k_scales,
+                                  const pkv_tensor* v_scales, const pkv_tensor* slot_mapping,
+                                  pkv_stream stream);
+
+/*
+ * pkv_read_cache — read cached tokens back: the inverse of the cache writes.
+ *
+ * For token t with slot = slot_mapping[t] >= 0: key[t, h, :] = the values that the cache
+ * holds at the slot (code * scale in binary32 for an 8-bit cache), rounded once to key's
+ * dtype; V alike.  slot < 0 leaves the token's rows as they were.  Reading a token and
+ * writing it elsewhere moves it: bit for bit between caches of one 16- or 32-bit type
+ * read in that type; for a token-scaled cache read in f32 the codes are the same and the
+ * scale within one unit in its last place.  Slots may repeat.
+ *
+ * key, value           [num_tokens, num_kv_heads, head_dim] f32 or bf16 (written), same
+ *                      dtype, shape and strides, last dim contiguous, 16-byte aligned.
+ * key_cache,
+ * value_cache          any cache dtype; PKV_I8 with k_scales and v_scales (NULL otherwise).
+ * slot_mapping         [num_tokens] int64, contiguous.
+ */
+pkv_status pkv_read_cache(const pkv_tensor* key, const pkv_tensor* value, const pkv_tensor* key_cache,
+                          const pkv_tensor* value_cache, const pkv_tensor* k_scales,
+                          const pkv_tensor* v_scales, const pkv_tensor* slot_mapping, pkv_stream stream);
+
+/*
+ * pkv_paged_attention_decode_quantized — pkv_paged_attention_decode_window over a
+ * token-scaled cache: K_s[j] = codes * k_scales of position j's slot, V_s[j] alike.
+ *
+ * key_cache and value_cache are PKV_I8, k_scales and v_scales as for
+ * pkv_quantize_and_cache; the other arguments as for the window decode (sliding_window 0:
+ * the full context).  A context length out of range sets PKV_DEVERR_CONTEXT_LEN and leaves
+ * the sequence's row as it was.  Workspace: the decode workspace, as described for
+ * pkv_paged_attention_decode, its need given by pkv_tree_workspace_bytes (num_tokens = num_seqs).
+ */
+pkv_status pkv_paged_attention_decode_quantized(const pkv_tensor* out, const pkv_tensor* query,
+                                                const pkv_tensor* key_cache, const pkv_tensor* value_cache,
+                                                const pkv_tensor* k_scales, const pkv_tensor* v_scales,
+                                                const pkv_tensor* block_tables,
+                                                const pkv_tensor* context_lens, int32_t num_kv_heads,
+                                                float scale, int32_t block_size,
+                                                int32_t max_blocks_per_seq, int32_t sliding_window,
+                                                pkv_stream stream);
+
+/*
+ * pkv_paged_attention_tree — attention of drafted tokens (the nodes of a tree per
+ * sequence) over the cache: the verification step of speculative decoding.
+ *
+ * Sequence s has L = context_lens[s] tokens in the cache, the last n = qsl[s+1] - qsl[s]
+ * of them drafted (already written, in node order), qsl = query_start_loc.  Query row
+ * r = qsl[s] + i is node i; with P = L - n it attends to every position j < P and to
+ * position P + c for each node c < n whose bit is set in its mask (bit c % 64 of word
+ * c / 64; a node sees itself only if its own bit is set):
+ *   out[r, h, :] = sum_j softmax_j(scale * query[r, h, :] . K_s[j]) * V_s[j]
+ * A row that attends to nothing is zero.  K and V of positions that a row does not attend
+ * to have no part in it, whatever they hold.  n = 0 is allowed; n > L, L past the table,
+ * n > 64 * mask_words or rows outside the batch set PKV_DEVERR_CONTEXT_LEN and leave the
+ * sequence's rows as they were, as are rows behind the last sequence's.
+ *
+ * out, query     [num_tokens, num_heads, head_dim] f32 or bf16, last dim contiguous; rows
+ *                of each sequence packed in order.
+ * key_cache,
+ * value_cache    any cache dtype; PKV_I8 with k_scales and v_scales (NULL otherwise).
+ * block_tables   [num_seqs, max_blocks_per_seq] int32; context_lens [num_seqs] int32;
+ * query_start_loc [num_seqs + 1] int32, contiguous, non-decreasing, starting at 0.
+ * tree_mask      [num_tokens, mask_words] int64, last dim contiguous, 1 to 16 words; bits
+ *                from n on are ignored.
+ * Shares the decode workspace and its rules (growth, capture, overlapping calls).
+ * Results do not depend on timing: a call's outputs are the same bits every time.
+ */
+pkv_status pkv_paged_attention_tree(const pkv_tensor* out, const pkv_tensor* query, const pkv_tensor* key_cache,
+                                    const pkv_tensor* value_cache, const pkv_tensor* k_scales,
+                                    const pkv_tensor* v_scales, const pkv_tensor* block_tables,
+                                    const pkv_tensor* context_lens, const pkv_tensor* query_start_loc,
+                                    const pkv_tensor* tree_mask, int32_t num_kv_heads, float scale,
+                                    int32_t block_size, int32_t max_blocks_per_seq, pkv_stream stream);
+
+/* Most workspace bytes that pkv_paged_attention_tree or pkv_paged_attention_decode_quantized
+ * needs with these sizes (num_tokens = query rows); 0 for non-positive sizes or num_heads
+ * not a multiple of num_kv_heads. */
+int64_t pkv_tree_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t num_heads, int32_t num_kv_heads,
+                                 int32_t head_dim);
 
 /*
  * pkv_copy_blocks — copy whole physical blocks of one cache tensor.

@@ -26,7 +26,9 @@ DEVERR = {"table_entry": 0x1, "slot": 0x2, "copy_pair": 0x4, "context_len": 0x8,
 OPTIONS = {"partition_tokens": 0, "debug_sync": 1, "dry_run": 2, "decode_kernel": 3,
            "dynamic_share": 4, "dynamic_chunk": 5, "fused_append": 6,
            "prefill_kernel": 7}
-_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2, torch.int32: 3, torch.int64: 4}
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2, torch.int32: 3, torch.int64: 4,
+           torch.int8: 5}
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
 
 
 class PkvError(RuntimeError):
@@ -40,6 +42,12 @@ class PkvTensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("ndim", ctypes.c_int32),
                 ("shape", ctypes.c_int64 * 4), ("stride", ctypes.c_int64 * 4), ("scale", ctypes.c_float),
                 ("head_scales", ctypes.c_void_p)]
+
+
+class PkvRotary(ctypes.Structure):
+    """pkv_rotary: how rotary_and_cache turns queries and keys (see :func:`rotary`)."""
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_double),
+                ("frequency", ctypes.c_double * 64)]
 
 
 _lock = threading.Lock()
@@ -68,12 +76,23 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.pkv_paged_attention_prefill.argtypes = [d, d, d, d, d, d, d, i32, f32, i32, i32, vp]
         lib.pkv_decode_append.argtypes = [d, d, d, d, d, d, d, d, d, i32, f32, i32, i32, i32, vp]
         lib.pkv_paged_attention_decode_window.argtypes = [d, d, d, d, d, d, i32, f32, i32, i32, i32, vp]
+        lib.pkv_rotary_init.argtypes = [ctypes.POINTER(PkvRotary), i32, i32, ctypes.c_double, i32, ctypes.c_double,
+                                        i64]
+        lib.pkv_rotary_and_cache.argtypes = [d] * 10 + [ctypes.POINTER(PkvRotary), vp]
+        lib.pkv_quantize_and_cache.argtypes = [d] * 7 + [vp]
+        lib.pkv_read_cache.argtypes = [d] * 7 + [vp]
+        lib.pkv_paged_attention_decode_quantized.argtypes = [d] * 8 + [i32, f32, i32, i32, i32, vp]
+        lib.pkv_paged_attention_tree.argtypes = [d] * 10 + [i32, f32, i32, i32, vp]
+        lib.pkv_tree_workspace_bytes.restype = i64
+        lib.pkv_tree_workspace_bytes.argtypes = [i32] * 5
         lib.pkv_noalloc_scratch_bytes.restype = i64
         lib.pkv_noalloc_scratch_bytes.argtypes = []
         for fn in ("pkv_paged_attention_decode", "pkv_paged_attention_decode_noalloc",
                    "pkv_reshape_and_cache", "pkv_decode_step", "pkv_copy_blocks",
                    "pkv_paged_attention_decode_window", "pkv_reshape_and_cache_amax",
-                   "pkv_paged_attention_prefill", "pkv_decode_append",
+                   "pkv_paged_attention_prefill", "pkv_decode_append", "pkv_rotary_init",
+                   "pkv_rotary_and_cache", "pkv_quantize_and_cache", "pkv_read_cache",
+                   "pkv_paged_attention_decode_quantized", "pkv_paged_attention_tree",
                    "pkv_set_option", "pkv_reserve_workspace", "pkv_read_device_errors"):
             getattr(lib, fn).restype = ctypes.c_int
         lib.pkv_last_error.restype = ctypes.c_char_p
@@ -297,6 +316,106 @@ def copy_blocks(cache, src_dst_pairs, stream=None) -> None:
         pairs = pairs.reshape(0, 2)
     descs = [_ref(cache), _ref(pairs)]
     _check(lib.pkv_copy_blocks(*descs, _stream(stream)))
+
+
+def rotary(rotary_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+           factor: float = 1.0, original_max_position: int = 0, frequencies=None,
+           magnitude: Optional[float] = None) -> PkvRotary:
+    """The rotation that rotary_and_cache applies: made once, passed to every call.  The
+    first ``rotary_dim`` columns of a head are rotated, in pairs half of them apart or
+    (``interleaved``) next to each other.  ``scaling`` (none, linear, base, bands, ramp)
+    stretches the frequencies by ``factor`` past ``original_max_position`` as pkv_rotary_init
+    describes; ``frequencies`` (radians per position, one per pair) and ``magnitude`` replace
+    what that gives."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"unknown rotary scaling {scaling!r} (known: {', '.join(ROTARY_SCALINGS)})")
+    r = PkvRotary()
+    _check(load_library().pkv_rotary_init(ctypes.byref(r), int(rotary_dim), int(bool(interleaved)), float(base),
+                                          ROTARY_SCALINGS[scaling], float(factor), int(original_max_position)))
+    if frequencies is not None:
+        freqs = [float(f) for f in frequencies]
+        if len(freqs) != rotary_dim // 2:
+            raise ValueError("frequencies must hold rotary_dim / 2 values")
+        r.frequency[:len(freqs)] = freqs
+    if magnitude is not None:
+        r.magnitude = float(magnitude)
+    return r
+
+
+def _opt_ref(t: Optional[torch.Tensor]):
+    return None if t is None else _ref(t)
+
+
+def rotary_and_cache(query_out, query, key, value, positions, key_cache, value_cache, slot_mapping,
+                     rotary: PkvRotary, k_scale: float = 1.0, v_scale: float = 1.0, stream=None,
+                     k_head_scales=None, v_head_scales=None, k_token_scales=None, v_token_scales=None) -> torch.Tensor:
+    """Rotate the new tokens' queries into ``query_out`` (returned; may be ``query``) and
+    write the rotated keys and the values into their cache slots, in one pass.
+    ``k_token_scales`` / ``v_token_scales`` [num_blocks, Hk, block_size] go with an int8
+    cache, which is then written as by quantize_and_cache."""
+    lib = load_library()
+    _check(lib.pkv_rotary_and_cache(
+        _ref(query_out), _ref(query), _ref(key), _ref(value), _ref(positions), _ref(key_cache, k_scale, k_head_scales),
+        _ref(value_cache, v_scale, v_head_scales), _opt_ref(k_token_scales), _opt_ref(v_token_scales),
+        _ref(slot_mapping), ctypes.byref(rotary), _stream(stream)))
+    return query_out
+
+
+def quantize_and_cache(key, value, key_cache, value_cache, k_token_scales, v_token_scales, slot_mapping,
+                       stream=None) -> None:
+    """Write the new tokens' K/V into an int8 cache (in place), each (token, KV head) row
+    with a scale of its own, max |x| / 127, stored beside the codes."""
+    lib = load_library()
+    _check(lib.pkv_quantize_and_cache(_ref(key), _ref(value), _ref(key_cache), _ref(value_cache),
+                                      _ref(k_token_scales), _ref(v_token_scales), _ref(slot_mapping),
+                                      _stream(stream)))
+
+
+def read_cache(key, value, key_cache, value_cache, slot_mapping, k_scale: float = 1.0, v_scale: float = 1.0,
+               stream=None, k_head_scales=None, v_head_scales=None, k_token_scales=None, v_token_scales=None):
+    """Read the tokens at ``slot_mapping`` back from the cache into ``key`` and ``value``
+    (float32 or bfloat16, returned); rows of negative slots stay as they were."""
+    lib = load_library()
+    _check(lib.pkv_read_cache(_ref(key), _ref(value), _ref(key_cache, k_scale, k_head_scales),
+                              _ref(value_cache, v_scale, v_head_scales), _opt_ref(k_token_scales),
+                              _opt_ref(v_token_scales), _ref(slot_mapping), _stream(stream)))
+    return key, value
+
+
+def paged_attention_decode_quantized(out, query, key_cache, value_cache, k_token_scales, v_token_scales, block_tables,
+                                     context_lens, num_kv_heads: int, scale: float, block_size: int,
+                                     max_blocks_per_seq: int, sliding_window: int = 0, stream=None) -> torch.Tensor:
+    """Single-token decode attention over an int8 cache with one scale per (slot, KV head),
+    into ``out`` (returned); ``sliding_window`` as for paged_attention_decode."""
+    lib = load_library()
+    _check(lib.pkv_paged_attention_decode_quantized(
+        _ref(out), _ref(query), _ref(key_cache), _ref(value_cache), _ref(k_token_scales), _ref(v_token_scales),
+        _ref(block_tables), _ref(context_lens), int(num_kv_heads), float(scale), int(block_size),
+        int(max_blocks_per_seq), int(sliding_window), _stream(stream)))
+    return out
+
+
+def paged_attention_tree(out, query, key_cache, value_cache, block_tables, context_lens, query_start_loc, tree_mask,
+                         num_kv_heads: int, scale: float, block_size: int, max_blocks_per_seq: int,
+                         k_scale: float = 1.0, v_scale: float = 1.0, stream=None, k_head_scales=None,
+                         v_head_scales=None, k_token_scales=None, v_token_scales=None) -> torch.Tensor:
+    """Attention of drafted tokens over the paged cache, into ``out`` (returned): rows
+    query_start_loc[s] .. query_start_loc[s+1]-1 are sequence s's drafted nodes, the last of
+    its context_lens[s] cached positions; each sees all positions before the nodes and, of
+    the nodes, those whose bit is set in its row of ``tree_mask`` (int64 [rows, words])."""
+    lib = load_library()
+    _check(lib.pkv_paged_attention_tree(
+        _ref(out), _ref(query), _ref(key_cache, k_scale, k_head_scales), _ref(value_cache, v_scale, v_head_scales),
+        _opt_ref(k_token_scales), _opt_ref(v_token_scales), _ref(block_tables), _ref(context_lens),
+        _ref(query_start_loc), _ref(tree_mask), int(num_kv_heads), float(scale), int(block_size),
+        int(max_blocks_per_seq), _stream(stream)))
+    return out
+
+
+def tree_workspace_bytes(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim) -> int:
+    """Most workspace bytes of a tree (or quantised decode) call with these sizes, for
+    reserve_workspace before a stream capture."""
+    return int(load_library().pkv_tree_workspace_bytes(num_seqs, num_tokens, num_heads, num_kv_heads, head_dim))
 
 
 def set_option(name: str, value: int) -> None:

@@ -10,6 +10,7 @@
 #include <string>
 
 #include "pkv.h"
+#include "pkv_host.h"
 #include "pkv_internal.h"
 
 namespace pkv {
@@ -31,6 +32,8 @@ std::atomic<int64_t> g_opt_prefill_kernel{0};
 
 thread_local std::string t_last_error;
 
+}  // namespace
+
 pkv_status fail(pkv_status st, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -41,24 +44,20 @@ pkv_status fail(pkv_status st, const char* fmt, ...) {
   return st;
 }
 
-pkv_status cuda_fail(cudaError_t e, const char* what) {
+static pkv_status cuda_fail(cudaError_t e, const char* what) {
   return fail(PKV_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
+namespace {
+
 constexpr int kMaxDevices = 64;
 
-struct DeviceState {
-  bool ready = false;
-  unsigned int* err = nullptr;  // address of g_error_word on this device
-  int num_sms = 0;
-  void* ws = nullptr;           // decode workspace
-  size_t ws_bytes = 0;
-  // Held from a workspace check to the end of the launch that uses the workspace, so
-  // a growth on one host thread cannot free a buffer another thread is queueing work on.
-  std::mutex ws_use;
-};
 DeviceState g_dev[kMaxDevices];
 std::mutex g_dev_mutex;
+
+}  // namespace
+
+bool dry_run() { return g_opt_dry_run.load() != 0; }
 
 pkv_status device_state(DeviceState** out) {
   int dev = 0;
@@ -137,6 +136,7 @@ int elt_bytes(int dtype) {
     case PKV_FP8_E4M3: return 1;
     case PKV_I32: return 4;
     case PKV_I64: return 8;
+    case PKV_I8: return 1;
     default: return 0;
   }
 }
@@ -148,11 +148,12 @@ const char* dtype_name(int dtype) {
     case PKV_FP8_E4M3: return "fp8_e4m3";
     case PKV_I32: return "i32";
     case PKV_I64: return "i64";
+    case PKV_I8: return "i8";
     default: return "?";
   }
 }
 
-int64_t numel(const pkv_tensor* t) {
+static int64_t numel(const pkv_tensor* t) {
   int64_t n = 1;
   for (int i = 0; i < t->ndim; ++i) n *= t->shape[i];
   return n;
@@ -172,17 +173,17 @@ pkv_status check_basic(const pkv_tensor* t, const char* name, int ndim) {
   return PKV_OK;
 }
 
-pkv_status check_dtype(const pkv_tensor* t, const char* name, int a, int b = -1, int c = -1) {
+pkv_status check_dtype(const pkv_tensor* t, const char* name, int a, int b, int c) {
   if (t->dtype == a || t->dtype == b || t->dtype == c) return PKV_OK;
   return fail(PKV_ERR_UNSUPPORTED, "%s: dtype %s is not supported here", name, dtype_name(t->dtype));
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-pkv_status check_cache(const pkv_tensor* c, const char* name) {
+pkv_status check_cache(const pkv_tensor* c, const char* name, bool i8) {
   pkv_status st = check_basic(c, name, 4);
   if (st) return st;
-  if ((st = check_dtype(c, name, PKV_F32, PKV_BF16, PKV_FP8_E4M3))) return st;
+  if (!(i8 && c->dtype == PKV_I8) && (st = check_dtype(c, name, PKV_F32, PKV_BF16, PKV_FP8_E4M3))) return st;
   const int64_t D = c->shape[3];
   if (c->shape[2] > 1 && c->stride[2] != D)
     return fail(PKV_ERR_INVALID_ARG, "%s: the (block_size, head_dim) tile must be contiguous (stride[2] == head_dim)", name);
@@ -210,14 +211,12 @@ bool same_layout(const pkv_tensor* a, const pkv_tensor* b) {
 bool supported_head_dim(int64_t d) { return d == 64 || d == 128; }
 bool supported_block_size(int64_t bs) { return bs == 2 || bs == 4 || bs == 8 || bs == 16 || bs == 32; }
 
-int choose_partition_tokens(int64_t max_ctx) {
+static int choose_partition_tokens(int64_t max_ctx) {
   const int64_t opt = g_opt_partition_tokens.load();
   if (opt > 0) return int(opt);
   if (max_ctx <= 512) return int(((max_ctx > 0 ? max_ctx : 1) + 255) / 256 * 256);
   return 512;
 }
-
-}  // namespace
 
 void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
