@@ -9,7 +9,7 @@
 
 namespace pkv {
 
-enum DType { kF32 = 0, kBF16 = 1, kE4M3 = 2, kI32 = 3, kI64 = 4, kI8 = 5 };
+enum DType { kF32 = 0, kBF16 = 1, kE4M3 = 2, kI32 = 3, kI64 = 4 };
 
 // Counts kernel launches made by the library (pkv_launch_count()).
 void note_launch();
@@ -41,58 +41,6 @@ struct CacheWriteParams {
   unsigned int* err;         // per-device error word
 };
 cudaError_t launch_reshape_and_cache(const CacheWriteParams& p, cudaStream_t stream);
-
-// ---- rotary_and_cache, quantize_and_cache, read_cache ----------------------------------
-struct TokenParams {
-  CacheWriteParams w;          // key / value, caches, slots (no amax)
-  float* k_token_scales;       // i8 cache: [NB, Hk, bs] scales (or null)
-  float* v_token_scales;
-  int64_t ts_block, ts_head;   // their strides, elements
-  const void* query;           // [T, Hq, D], the key's dtype
-  void* query_out;
-  int64_t q_stride_t, q_stride_h, qo_stride_t, qo_stride_h;
-  int num_heads;               // 0: no query
-  const void* positions;       // [T]
-  bool positions64;
-  int rotary_dim;              // 0: no rotation
-  bool interleaved;
-  float magnitude;
-  uint64_t turns[64];          // pair i turns by turns[i] / 2^64 of a circle per position
-};
-cudaError_t launch_token_write(const TokenParams& p, cudaStream_t stream);
-cudaError_t launch_token_read(const TokenParams& p, cudaStream_t stream);
-
-// ---- attention of drafted trees / decode over token-scaled caches -----------------------
-struct TreeParams {
-  void* out;                   // [T, Hq, D]
-  const void* query;
-  int q_dtype;                 // and out's
-  int64_t out_stride_t, out_stride_h, q_stride_t, q_stride_h;
-  const void* key_cache;       // [NB, Hk, bs, D]
-  const void* value_cache;
-  int kv_dtype;
-  int64_t cs_block, cs_head;   // elements
-  const float* k_token_scales; // i8 cache: [NB, Hk, bs]
-  const float* v_token_scales;
-  int64_t ts_block, ts_head;
-  const float* k_head_scales;  // e4m3 cache: [Hk] (or null)
-  const float* v_head_scales;
-  const int32_t* block_tables;
-  int64_t bt_stride;
-  const int32_t* context_lens;
-  int64_t cl_stride;
-  const int32_t* query_start_loc;  // null: one row per sequence
-  const int64_t* tree_mask;        // null: rows see the whole context (with the window)
-  int64_t mask_stride;
-  int mask_words;
-  int num_seqs, num_tokens, num_heads, num_kv_heads, group, head_dim, block_size, max_blocks_per_seq;
-  int64_t num_blocks;
-  float qk_scale_log2;         // scale * log2(e) * k_scale
-  float v_scale;
-  int sliding_window;
-  unsigned int* err;
-};
-cudaError_t launch_tree_core(const TreeParams& p, cudaStream_t stream);
 
 // ---- copy_blocks ------------------------------------------------------------------
 struct CopyBlocksParams {
@@ -186,7 +134,7 @@ pkv_status decode_prepare(const pkv_tensor* out, const pkv_tensor* query, const 
                           int32_t block_size, int32_t max_blocks_per_seq, int32_t sliding_window,
                           DecodeParams* p, size_t* ws_bytes, bool* nothing_to_do);
 void decode_set_workspace(DecodeParams* p, void* ws);
-// finish_call (pkv_host.h) for the current device.
+// Maps a launch result to a status (and, with debug sync on, checks the device).
 pkv_status finish_launch(cudaError_t launch_err, cudaStream_t stream, const char* what);
 // Records `msg` as the calling thread's last error and returns `st`.
 pkv_status set_error(pkv_status st, const char* msg);

@@ -5,6 +5,7 @@
 #include <cmath>
 
 #include "pkv_host.h"
+#include "token_internal.h"
 
 namespace pkv {
 namespace {
@@ -199,13 +200,21 @@ pkv_status tree_prepare(const pkv_tensor* out, const pkv_tensor* query, const pk
   return PKV_OK;
 }
 
+// Blocks of the tensor-core kernel: one per SM.
+int tree_grid(int num_sms) { return num_sms < int(TreeSplit::kMaxGrid) ? num_sms : int(TreeSplit::kMaxGrid); }
+
 pkv_status tree_launch(TreeParams& p, cudaStream_t stream, const char* what) {
   if (dry_run() || p.num_seqs == 0 || p.num_tokens == 0 || p.num_heads == 0) return PKV_OK;
   DeviceState* s;
   pkv_status st = device_state(&s);
   if (st) return st;
   p.err = s->err;
-  return finish_call(s, launch_tree_core(p, stream), stream, what);
+  if (!tree_tc_supported(p)) return finish_call(s, launch_tree_core(p, stream), stream, what);
+  const int grid = tree_grid(s->num_sms);
+  const int rows = tree_tc_rows(p.num_tokens, p.group, !p.query_start_loc);
+  std::unique_lock<std::mutex> use(s->ws_use);
+  if ((st = ensure_workspace(s, tree_tc_workspace(grid, rows, p.head_dim), stream))) return st;
+  return finish_call(s, launch_tree_tc(p, grid, rows, s->ws, stream), stream, what);
 }
 
 }  // namespace
@@ -379,7 +388,13 @@ int64_t pkv_tree_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t n
   if (num_seqs <= 0 || num_tokens <= 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
       num_heads % num_kv_heads)
     return 0;
-  return 0;
+  const int group = num_heads / num_kv_heads;
+  if (group > 128) return 0;
+  int num_sms = 0, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    num_sms = int(TreeSplit::kMaxGrid);
+  return int64_t(tree_tc_workspace(tree_grid(num_sms), tree_tc_rows(num_tokens, group, false), head_dim));
 }
 
 }  // extern "C"

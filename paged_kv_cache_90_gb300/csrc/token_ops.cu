@@ -8,7 +8,7 @@
 // shuffles away and loads are 16 bytes wide.  The write with rotation and the one
 // without are the same kernel.
 #include "device_common.cuh"
-#include "pkv_internal.h"
+#include "token_internal.h"
 
 namespace pkv {
 

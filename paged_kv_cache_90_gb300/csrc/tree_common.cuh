@@ -3,7 +3,7 @@
 #pragma once
 
 #include "device_common.cuh"
-#include "pkv_internal.h"
+#include "token_internal.h"
 
 namespace pkv {
 namespace tree {

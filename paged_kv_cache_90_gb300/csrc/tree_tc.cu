@@ -1,0 +1,878 @@
+// tree_tc.cu — attention of drafted token trees over the paged cache on the
+// fifth-generation tensor cores (tcgen05 MMAs, accumulators in tensor memory).
+//
+// A KV head's K and V are read once for all the rows that use them: the group's g query
+// heads times up to TQ = 128 / g (rounded down) drafted nodes make a row tile of 128 MMA
+// rows (row r = node r / g, head r % g; the rest idle), and two row tiles share a pass
+// over the keys.  With few rows the call is a stream of the cache and HBM bounds it; with
+// 256 rows to a KV head the tensor work of a key tile (2 x 2 x 128 x 128 x D
+// multiply-adds) takes as long as its bytes.
+//
+// Work split.  An item is (sequence, KV head, pair of row tiles); its work is its key
+// tiles of 128 positions.  The items' tiles, laid end to end, are cut into equal
+// contiguous ranges, one per SM, so one long context occupies the whole GPU and many
+// short ones balance.  An item inside one range writes its output; one cut by a border
+// leaves, per part, the rows' maximum, sum and unnormalised output in binary32, which a
+// second small kernel folds in order (so the result never depends on timing).
+//
+// A step is one (key tile, row tile):
+//   S = Q K^T        M 128, N 128, K = D: both from shared memory (128-byte swizzle), S in
+//                    one of two tensor-memory buffers, by the step's parity
+//   P = 2^(S c - m)  written back over S as bf16 pairs by a softmax warpgroup, a row per
+//                    thread; masked positions become zero here
+//   O += P V         M 128, N = D, K = 128 keys: P from tensor memory, V from shared memory
+// The MMA thread issues S of step x + 1 before P V of step x, so the tensor cores work
+// while a softmax runs.  Two softmax warpgroups: each owns one Q buffer and one O
+// accumulator.  A pair's two row tiles go to the two of them; single row tiles alternate,
+// so that one item's output is written while the next one's softmax runs.
+//
+// P is rounded to bf16 for the product (half a step, 2^-9 of a weight on average; the
+// other operand is bf16); scores, maximum, sum and output stay in binary32.  The
+// reference maximum moves only when a row's maximum grows by more than 2^8, as in the
+// decode kernel.
+//
+// Warps: 0 streams K tiles, 2 V tiles (TMA, two-deep rings), 3 the queries; 1 issues the
+// MMAs; 4-7 and 8-11 are the softmax warpgroups.  Every wait is bounded; when one runs
+// out the block sets an error bit and a flag that makes every role stop, lets its copies
+// and MMAs land and frees the tensor memory.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "decode_mma_launch.cuh"
+#include "tcgen05.cuh"
+#include "tree_common.cuh"
+
+namespace pkv {
+namespace tree_tc {
+
+constexpr int kBM = 128;  // rows per row tile
+constexpr int kBN = 128;  // positions per key tile
+constexpr int kThreads = 384;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kGap = 8.f;  // growth of a row's maximum (log2) that moves its reference
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;             // 64-column halves of an operand (128-byte rows)
+  static constexpr uint32_t kHalfBytes = kBM * 128;  // 16 KB
+  static constexpr uint32_t kOpBytes = kHalves * kHalfBytes;
+  // from the 1024-aligned base: Q[2] | K[2] | V[2] | barriers and small state
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kK = 2 * kOpBytes;
+  static constexpr uint32_t kV = kK + 2 * kOpBytes;
+  static constexpr uint32_t kState = kV + 2 * kOpBytes;
+  static constexpr uint32_t kStateBytes = 2048;
+  static constexpr size_t kSmem = kState + kStateBytes + 1024;  // (+ alignment)
+  // tensor memory: S of even and odd steps (128 columns each), then O of the two slots
+  static constexpr uint32_t kS = 0, kO = 2 * kBN;
+};
+
+// Barriers.  A wait names a phase by its parity, so its barrier may be at most one phase
+// away: those that a softmax warpgroup waits for count its own slot's steps (S: two per
+// slot, by the parity of the slot's step), since a warpgroup may wait for a step while the
+// other one is still several steps behind it.
+enum Bar { kQFull = 0, kQEmpty = 2, kKFull = 4, kKEmpty = 6, kVFull = 8, kVEmpty = 10, kSFull = 12, kPFull = 16,
+           kODone = 18, kOFree = 20, kDrain = 22, kNumBars = 23 };
+
+// Small shared state behind the operands.
+struct State {
+  uint64_t bars[kNumBars + 1];
+  volatile int abort;
+  uint32_t tmem;
+  int first_seq;             // the range's first sequence
+  int64_t first_off;         // and its offset in that sequence's work
+  int64_t total;             // all tiles
+  int64_t warp_sum[kThreads / 32];
+  // drafted positions with an infinity or a NaN in V, 32 to a word from the first tile
+  // that holds drafted nodes on (1024 nodes touch at most 9 tiles), per item (index mod 4)
+  uint32_t bad_rows[4][36];
+};
+static_assert(sizeof(State) <= 2048, "state");
+
+__device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+  return done != 0;
+}
+// Bounded wait that gives up when another role has; `spin`: without suspending the thread.
+__device__ __forceinline__ bool wait(State* st, int bar, uint32_t parity, bool spin = false) {
+  const uint32_t polls = spin ? kWaitPolls << 4 : kWaitPolls;
+  for (uint32_t i = 0; i < polls; ++i) {
+    if (spin ? test_wait(&st->bars[bar], parity) : mbar_try_wait(&st->bars[bar], parity)) return true;
+    if ((i & 255u) == 255u && st->abort) return false;
+  }
+  st->abort = 1;
+  return false;
+}
+
+// The same by a whole warp: all its lanes see one answer.
+__device__ __forceinline__ bool wait_warp(State* st, int bar, uint32_t parity, bool spin = false) {
+  return __all_sync(0xffffffffu, wait(st, bar, parity, spin));
+}
+
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// A sequence's work in tiles: key tiles x row-tile pairs x KV heads.
+struct SeqWork {
+  tree::Extent e;
+  int base;    // first position of its first tile: the block that holds e.lo
+  int tiles;   // key tiles of an item (at least one where there are rows)
+  int pairs;   // row-tile pairs
+  __device__ __forceinline__ void load(const TreeParams& p, int s, bool* bad) {
+    e = tree::extent(p, s, bad);
+    base = e.lo - e.lo % p.block_size;
+    tiles = max(1, (e.L - base + kBN - 1) / kBN);
+    const int tq = kBM / p.group, rt = (e.n + tq - 1) / tq;
+    pairs = (rt + 1) >> 1;
+  }
+  __device__ __forceinline__ int64_t total(const TreeParams& p) const {
+    return int64_t(tiles) * pairs * p.num_kv_heads;  // (no rows: no pairs)
+  }
+};
+
+// Walks the item parts of a block's range; every role walks the same sequence.
+struct Walk {
+  SeqWork q;
+  int s, kvh, pair;
+  int j0, j1;      // the part's key tiles
+  int nt;          // row tiles of the pair (1 or 2)
+  int64_t left;    // tiles left in the range, this part's included
+  __device__ __forceinline__ bool valid() const { return left > 0; }
+  __device__ __forceinline__ bool begins() const { return j0 == 0; }
+  __device__ __forceinline__ bool ends() const { return j1 == q.tiles; }
+  __device__ __forceinline__ void part(const TreeParams& p) {
+    j1 = int(min(int64_t(q.tiles), j0 + left));
+    const int tq = kBM / p.group, rt = (q.e.n + tq - 1) / tq;
+    nt = min(2, rt - 2 * pair);
+  }
+  __device__ __forceinline__ void start(const TreeParams& p, int seq, int64_t off, int64_t count) {
+    left = count;
+    if (count <= 0) return;
+    bool bad;
+    s = seq;
+    q.load(p, s, &bad);
+    const int item = int(off / q.tiles);
+    j0 = int(off - int64_t(item) * q.tiles);
+    kvh = item / q.pairs;
+    pair = item - kvh * q.pairs;
+    part(p);
+  }
+  __device__ __forceinline__ void next(const TreeParams& p) {
+    left -= j1 - j0;
+    if (left <= 0) return;
+    j0 = 0;
+    if (++pair == q.pairs) {
+      pair = 0;
+      if (++kvh == p.num_kv_heads) {
+        kvh = 0;
+        bool bad;
+        do {
+          q.load(p, ++s, &bad);  // (tiles are left, so a later sequence has some)
+        } while (q.pairs == 0 && s + 1 < p.num_seqs);
+      }
+    }
+    part(p);
+  }
+};
+
+// Bits c0 .. c0 + 31 of a row's mask: 1 for positions before the drafted nodes (c < 0), 0
+// behind them (c >= n).
+__device__ __forceinline__ uint32_t mask_bits(const int64_t* mask, int c0, int n) {
+  if (c0 >= n) return 0u;
+  uint32_t past = 0u;
+  int sh = 0;
+  if (c0 < 0) {
+    if (c0 <= -32) return 0xffffffffu;
+    sh = -c0;
+    past = (1u << sh) - 1u;
+    c0 = 0;
+  }
+  if (!mask) return past;  // (no mask: every position is before the nodes, n = 0 of them)
+  const int w = c0 >> 6, o = c0 & 63;
+  uint64_t b = uint64_t(__ldg(mask + w)) >> o;
+  if (o > 32 && 64 * (w + 1) < n) b |= uint64_t(__ldg(mask + w + 1)) << (64 - o);
+  const int valid = n - c0;
+  uint32_t bits = uint32_t(b);
+  if (valid < 32) bits &= (1u << valid) - 1u;
+  return past | (bits << sh);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+               const __grid_constant__ CUtensorMap tmv, const __grid_constant__ TreeParams p, const TreeSplit sp) {
+  using C = Cfg<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  State* st = reinterpret_cast<State*>(smem + C::kState);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = p.group, TQ = kBM / g;
+  const uint32_t sbase = smem_addr(smem);
+
+  if (tid == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      const bool warps4 = (i >= kPFull && i < kPFull + 2) || (i >= kOFree && i < kOFree + 2);
+      mbar_init(&st->bars[i], warps4 ? 4 : 1);  // (one arrival per softmax warp)
+    }
+    st->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) tc::alloc(&st->tmem, kTmemCols);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing of the caller's is read before
+  asm volatile("griddepcontrol.launch_dependents;");
+
+  // ---- the block's range of the flattened tiles: every thread adds up a run of sequences,
+  // then the one whose run holds the range's start finds the sequence -------------------
+  {
+    const int per = (p.num_seqs + kThreads - 1) / kThreads;
+    const int s0 = min(p.num_seqs, tid * per), s1 = min(p.num_seqs, s0 + per);
+    int64_t sum = 0;
+    for (int s = s0; s < s1; ++s) {
+      SeqWork w;
+      bool bad;
+      w.load(p, s, &bad);
+      if (bad && blockIdx.x == 0) raise_device_error(p.err, kErrContextLen);
+      sum += w.total(p);
+    }
+    int64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) st->warp_sum[warp] = incl;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += st->warp_sum[w];
+      total += st->warp_sum[w];
+    }
+    const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t from = share * blockIdx.x;
+    int64_t at = before + incl - sum;  // where this thread's run starts
+    if (from >= at && from < at + sum) {
+      for (int s = s0; s < s1; ++s) {
+        SeqWork w;
+        bool bad;
+        w.load(p, s, &bad);
+        const int64_t n = w.total(p);
+        if (from < at + n) {
+          st->first_seq = s;
+          st->first_off = from - at;
+          break;
+        }
+        at += n;
+      }
+    }
+    if (tid == 0) st->total = total;
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = st->tmem;
+  const int64_t total = st->total;
+  const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t from = share * blockIdx.x;
+  const int64_t count = max(int64_t(0), min(share, total - from));
+  Walk it;
+  it.start(p, st->first_seq, st->first_off, count);
+
+  if (warp == 0 || warp == 2) {
+    // ---- K (warp 0) and V (warp 2) tiles: lane i issues copy i of a tile (one box of
+    // `box` positions x one 64-column half), its table entry fetched a tile ahead ---------
+    const bool isv = warp == 2;
+    const int bs = p.block_size, box = min(bs, 16);
+    const int eb = isv ? kVEmpty : kKEmpty, fb = isv ? kVFull : kKFull;
+    const uint32_t region = sbase + (isv ? C::kV : C::kK);
+    const CUtensorMap* map = isv ? &tmv : &tmk;
+    const int bx = lane / C::kHalves, half = lane % C::kHalves;
+    int kt = 0;
+    bool ok = true;
+    for (; ok && it.valid(); it.next(p)) {
+      const int32_t* row = p.block_tables + int64_t(it.s) * p.bt_stride;
+      // (positions before e.lo share its block; the tile's other boxes end at L)
+      auto entry = [&](int j) -> int {
+        const int key = it.q.base + j * kBN + bx * box;
+        if (bx * box >= kBN || key >= it.q.e.L) return 0;
+        const int e = __ldg(row + key / bs);
+        if (e >= 0 && int64_t(e) < p.num_blocks) return e;
+        raise_device_error(p.err, kErrTableEntry);
+        return 0;
+      };
+      int e = entry(it.j0);
+      for (int j = it.j0; j < it.j1; ++j, ++kt) {
+        const int e_next = j + 1 < it.j1 ? entry(j + 1) : 0;
+        const int slot = kt & 1, pos = it.q.base + j * kBN;
+        const int nbox = max(0, min(kBN, it.q.e.L - pos) + box - 1) / box;
+        if (lane == 0 && kt >= 2) ok = wait(st, eb + slot, uint32_t((kt - 2) >> 1) & 1u);
+        ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&st->bars[fb + slot], uint32_t(nbox * box) * 128u * C::kHalves);
+        __syncwarp();
+        if (bx < nbox)
+          tma_4d(region + slot * C::kOpBytes + half * C::kHalfBytes + uint32_t(bx * box * 128), map, 64 * half,
+                 (pos + bx * box) & (bs - 1), it.kvh, e, &st->bars[fb + slot]);
+        e = e_next;
+      }
+    }
+    // the copies in flight land before the block may exit
+    if (lane == 0)
+      for (int k = max(0, kt - 2); k < kt; ++k) (void)mbar_wait_bounded(&st->bars[fb + (k & 1)], uint32_t(k >> 1) & 1u);
+  } else if (warp == 3) {
+    // ---- queries: the row tiles of each item, alternating between the two slots; and what
+    // the fold needs of an item that goes on in the next block's range --------------------
+    if (lane == 0) {
+      int oc = 0, uses0 = 0, uses1 = 0;  // of the slots
+      bool ok = true;
+      int64_t at = from;
+      TreeSplit::Tail tail = {0, 0, 0, 0};
+      for (; ok && it.valid(); it.next(p)) {
+        for (int qt = 0; ok && qt < it.nt; ++qt, ++oc) {
+          const int slot = oc & 1, n = slot ? uses1 : uses0;
+          if (n > 0) ok = wait(st, kQEmpty + slot, uint32_t(n - 1) & 1u);
+          if (!ok) break;
+          if (slot) ++uses1; else ++uses0;
+          mbar_arrive_expect_tx(&st->bars[kQFull + slot], uint32_t(g * sp.q_nodes) * 128u * C::kHalves);
+          for (int h = 0; h < C::kHalves; ++h)
+            tma_3d(sbase + C::kQ + slot * C::kOpBytes + h * C::kHalfBytes, &tmq, 64 * h, it.kvh * g,
+                   it.q.e.q0 + (2 * it.pair + qt) * TQ, &st->bars[kQFull + slot]);
+        }
+        if (it.begins() && !it.ends()) {
+          const int node0 = 2 * it.pair * TQ;
+          tail.row0 = it.q.e.q0 + node0;
+          tail.nodes = min(2 * TQ, it.q.e.n - node0);
+          tail.kvh = it.kvh;
+          tail.last = int((at + it.q.tiles - 1) / share);
+        }
+        at += it.j1 - it.j0;
+      }
+      sp.tails[blockIdx.x] = tail;
+      if (uses0) (void)mbar_wait_bounded(&st->bars[kQFull], uint32_t(uses0 - 1) & 1u);
+      if (uses1) (void)mbar_wait_bounded(&st->bars[kQFull + 1], uint32_t(uses1 - 1) & 1u);
+    }
+  } else if (warp == 1) {
+    // ---- MMAs (one thread): two cursors over the steps, S ahead of P V; whichever can go
+    // next goes ---------------------------------------------------------------------------
+    if (lane == 0) {
+      constexpr uint32_t idS = tc::idesc_bf16(kBM, kBN, 0, 0);
+      constexpr uint32_t idO = tc::idesc_bf16(kBM, D, 0, 1);
+      struct Cursor {
+        Walk w;
+        int j, qt, x, kt, oc, uses0, uses1, steps0, steps1;
+        __device__ __forceinline__ int slot() const { return (oc + qt) & 1; }
+        __device__ __forceinline__ int step() const { return slot() ? steps1 : steps0; }
+        __device__ __forceinline__ int uses() const { return slot() ? uses1 : uses0; }  // of the slot before
+        __device__ __forceinline__ void advance(const TreeParams& p) {
+          ++x;
+          if (slot()) ++steps1; else ++steps0;
+          if (++qt < w.nt) return;
+          qt = 0;
+          ++kt;
+          if (++j < w.j1) return;
+          if (w.nt == 2 || (oc & 1) == 0) ++uses0;
+          if (w.nt == 2 || (oc & 1) == 1) ++uses1;
+          oc += w.nt;
+          w.next(p);
+          j = w.j0;
+        }
+      };
+      Cursor a;  // next S
+      a.w = it;
+      a.j = it.j0;
+      a.qt = a.x = a.kt = a.oc = a.uses0 = a.uses1 = a.steps0 = a.steps1 = 0;
+      Cursor b = a;  // next P V
+      uint32_t idle = 0;
+      bool ok = true;
+      while (b.w.valid()) {
+        bool went = false;
+        if (a.w.valid() && a.x <= b.x + 1) {
+          const int slot = a.slot();
+          if (test_wait(&st->bars[kKFull + (a.kt & 1)], uint32_t(a.kt >> 1) & 1u) &&
+              (a.j > a.w.j0 || test_wait(&st->bars[kQFull + slot], uint32_t(a.uses()) & 1u))) {
+            tc::fence_after();
+            const uint32_t kaddr = sbase + C::kK + (a.kt & 1) * C::kOpBytes;
+            const uint32_t qaddr = sbase + C::kQ + slot * C::kOpBytes;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * C::kHalfBytes + (kk & 3) * 32;
+              tc::mma_ss(tmem + C::kS + (a.x & 1) * kBN, tc::desc_sw128(qaddr + off, 16, 1024),
+                         tc::desc_sw128(kaddr + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
+            }
+            tc::commit(&st->bars[kSFull + 2 * slot + (a.step() & 1)]);
+            if (a.qt == a.w.nt - 1) tc::commit(&st->bars[kKEmpty + (a.kt & 1)]);
+            if (a.j == a.w.j1 - 1) tc::commit(&st->bars[kQEmpty + slot]);
+            a.advance(p);
+            went = true;
+          }
+        }
+        if (b.x < a.x) {
+          const int slot = b.slot(), u = b.uses();
+          const bool first = b.j == b.w.j0;
+          if (test_wait(&st->bars[kPFull + (b.x & 1)], uint32_t(b.x >> 1) & 1u) &&
+              test_wait(&st->bars[kVFull + (b.kt & 1)], uint32_t(b.kt >> 1) & 1u) &&
+              (!first || u == 0 || test_wait(&st->bars[kOFree + slot], uint32_t(u - 1) & 1u))) {
+            tc::fence_after();
+            const uint32_t vaddr = sbase + C::kV + (b.kt & 1) * C::kOpBytes;
+#pragma unroll
+            for (int kk = 0; kk < kBN / 16; ++kk)
+              tc::mma_ts(tmem + C::kO + slot * D, tmem + C::kS + (b.x & 1) * kBN + 8 * kk,
+                         tc::desc_sw128(vaddr + kk * 16 * 128, C::kHalfBytes, 1024), idO,
+                         (!first || kk > 0) ? 1u : 0u);
+            tc::commit(&st->bars[kODone + slot]);
+            if (b.qt == b.w.nt - 1) tc::commit(&st->bars[kVEmpty + (b.kt & 1)]);
+            b.advance(p);
+            went = true;
+          }
+        }
+        if (went) {
+          idle = 0;
+        } else if ((++idle & 255u) == 0 && (st->abort || idle > (kWaitPolls << 4))) {
+          ok = false;
+          break;
+        }
+      }
+      // every MMA issued has completed before the tensor memory is freed
+      tc::commit(&st->bars[kDrain]);
+      (void)mbar_wait_bounded(&st->bars[kDrain], 0);
+      if (!ok) {
+        st->abort = 1;
+        raise_device_error(p.err, kErrTimeout);
+      }
+    }
+  } else if (warp >= 4) {
+    // ---- softmax warpgroup `wg` (slot wg): row r of its row tiles, r = tensor-memory lane --
+    const int wg = (warp >> 2) - 1, q = warp & 3;
+    const int r = 32 * q + lane;
+    const uint32_t lane_off = uint32_t(32 * q) << 16;
+    const uint32_t tO = tmem + C::kO + wg * D + lane_off;
+    const float sl = p.qk_scale_log2;
+    int x0 = 0, kt0 = 0, oc = 0, item = 0, steps = 0;  // `steps`: of this slot so far
+    bool ok = true;
+    for (; ok && it.valid(); x0 += (it.j1 - it.j0) * it.nt, kt0 += it.j1 - it.j0, oc += it.nt, ++item, it.next(p)) {
+      const int qt = (oc & 1) == wg ? 0 : 1;
+      if (qt >= it.nt) continue;
+      const tree::Extent& e = it.q.e;
+      const int node = (2 * it.pair + qt) * TQ + r / g;
+      const bool row_ok = r < TQ * g && node < e.n;
+      const bool warp_ok = __any_sync(0xffffffffu, row_ok);
+      const int64_t trow = e.q0 + node;
+      const int64_t* mask = p.tree_mask && row_ok ? p.tree_mask + trow * p.mask_stride : nullptr;
+      const int n_hidden = p.tree_mask ? e.n : 0;
+      uint32_t* bad_rows = st->bad_rows[item & 3];
+      const int jt = (e.P - it.q.base) / kBN;  // first tile with drafted nodes
+      float m_ref = -INFINITY, l_run = 0.f;
+      for (int j = it.j0; j < it.j1; ++j, ++steps) {
+        const int x = x0 + (j - it.j0) * it.nt + qt;
+        const int pos = it.q.base + j * kBN;
+        const uint32_t tS = tmem + C::kS + (x & 1) * kBN + lane_off;
+        if (!(ok = wait_warp(st, kSFull + 2 * wg + (steps & 1), uint32_t(steps >> 1) & 1u, warp_ok))) break;
+        tc::fence_after();
+        const bool cut = pos + kBN > e.P || pos + kBN > e.L || pos < e.lo;  // some position may be hidden
+        // V rows that are no position of the row's range are zeroed in shared memory (they
+        // may hold anything), and infinities and NaN of drafted nodes taken out of it (rows
+        // that do not see the node must not meet them): once per tile, by the first row
+        // tile's warpgroup
+        if (qt == 0 && cut) {
+          const int kt = kt0 + (j - it.j0);
+          if (!(ok = wait_warp(st, kVFull + (kt & 1), uint32_t(kt >> 1) & 1u))) break;
+          unsigned char* vt = smem + C::kV + (kt & 1) * C::kOpBytes;
+          const bool scan = n_hidden > 0 && pos + kBN > e.P;
+          uint32_t bad = 0u;  // of the warp's 32 rows
+          for (int i = lane; i < 32 * 8 * C::kHalves; i += 32) {
+            const int row = 32 * q + ((i >> 3) & 31), at = pos + row;
+            uint4* cell = reinterpret_cast<uint4*>(vt + (i >> 8) * C::kHalfBytes + row * 128 + (i & 7) * 16);
+            if (at < e.lo || at >= e.L) {
+              *cell = make_uint4(0u, 0u, 0u, 0u);
+            } else if (scan && at >= e.P) {
+              const uint4 v = *cell;
+              uint32_t w[4] = {v.x, v.y, v.z, v.w};
+              bool any = false;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if ((w[k] & 0x7f80u) == 0x7f80u) { w[k] &= 0xffff0000u; any = true; }
+                if ((w[k] & 0x7f800000u) == 0x7f800000u) { w[k] &= 0xffffu; any = true; }
+              }
+              if (any) {
+                *cell = make_uint4(w[0], w[1], w[2], w[3]);
+                bad |= 1u << (row & 31);
+              }
+            }
+          }
+          if (scan) {
+            bad = __reduce_or_sync(0xffffffffu, bad);
+            if (lane == 0) bad_rows[4 * (j - jt) + q] = bad;
+          }
+          fence_proxy_async_smem();
+        }
+        if (warp_ok) {
+          uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
+          if (cut) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int at = pos + 32 * w;
+              keep[w] = n_hidden ? mask_bits(mask, at - e.P, n_hidden)
+                                 : at + 32 <= e.L ? ~0u : at >= e.L ? 0u : (1u << (e.L - at)) - 1u;
+              if (at < e.lo) keep[w] &= at + 32 <= e.lo ? 0u : ~0u << (e.lo - at);
+            }
+          }
+          // the row's maximum
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t w0[32], w1[32];
+            tc::ld32(tS + 64 * c, w0);
+            tc::ld32(tS + 64 * c + 32, w1);
+            tc::wait_ld();
+            float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (cut) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                if (keep[2 * c] >> i & 1u) t4[i & 1] = fmaxf(t4[i & 1], __uint_as_float(w0[i]));
+                if (keep[2 * c + 1] >> i & 1u) t4[2 + (i & 1)] = fmaxf(t4[2 + (i & 1)], __uint_as_float(w1[i]));
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                t4[i & 1] = fmaxf(t4[i & 1], __uint_as_float(w0[i]));
+                t4[2 + (i & 1)] = fmaxf(t4[2 + (i & 1)], __uint_as_float(w1[i]));
+              }
+            }
+            mx = fmaxf(mx, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
+          }
+          mx *= sl;
+          const bool first = m_ref == -INFINITY;
+          const bool move = row_ok && mx != -INFINITY && (first || mx > m_ref + kGap);
+          if (__any_sync(0xffffffffu, move && !first)) {
+            // some row's O is rescaled: its product of the step before has to be in it
+            if (!(ok = wait_warp(st, kODone + wg, uint32_t(steps - 1) & 1u, true))) break;
+            tc::fence_after();
+            const float alpha = move && !first ? fast_exp2(m_ref - mx) : 1.f;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t w[32];
+              tc::ld32(tO + 32 * c, w);
+              tc::wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+              tc::st32(tO + 32 * c, w);
+            }
+            tc::wait_st();
+            l_run *= alpha;
+          }
+          if (move) m_ref = mx;
+          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+          float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[32], pk[16];
+            tc::ld32(tS + 32 * c, w);
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float a = fast_exp2(fmaf(__uint_as_float(w[2 * i]), sl, -mu));
+              float b = fast_exp2(fmaf(__uint_as_float(w[2 * i + 1]), sl, -mu));
+              if (cut) {
+                if (!(keep[c] >> (2 * i) & 1u)) a = 0.f;
+                if (!(keep[c] >> (2 * i + 1) & 1u)) b = 0.f;
+              }
+              ps[i & 3] += a + b;
+              const __nv_bfloat162 pr = __floats2bfloat162_rn(a, b);
+              pk[i] = *reinterpret_cast<const uint32_t*>(&pr);
+            }
+            tc::st16(tS + 16 * c, pk);  // (over scores that have been read)
+          }
+          l_run += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+          tc::wait_st();
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st->bars[kPFull + (x & 1)]);
+      }
+      if (!ok) break;
+      // ---- the part's output ---------------------------------------------------------------
+      if (!(ok = wait_warp(st, kODone + wg, uint32_t(steps - 1) & 1u))) break;
+      tc::fence_after();
+      if (warp_ok) {
+        const bool whole = it.begins() && it.ends();
+        const float inv = whole ? (l_run != 0.f ? 1.f / l_run : 0.f) : 1.f;
+        const int64_t prow = int64_t(2 * blockIdx.x + (it.begins() ? 1 : 0)) * sp.rows + qt * kBM + r;
+        if (row_ok && !whole) sp.ml[prow] = make_float2(m_ref, l_run);
+        // (the words of this part's tiles; the others are not this item's)
+        const int bw0 = 4 * (max(it.j0, jt) - jt), bw1 = 4 * (it.j1 - jt);
+        bool any_bad = false;
+        if (n_hidden > 0 && row_ok)
+          for (int w = bw0; w < bw1; ++w) any_bad |= bad_rows[w] != 0u;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t w[32];
+          tc::ld32(tO + 32 * c, w);
+          tc::wait_ld();
+          if (any_bad) {
+            // add what was taken out of V to the rows that see it
+            for (int k = 32 * bw0; k < 32 * bw1; ++k) {
+              const int at = it.q.base + jt * kBN + k;
+              if (!(bad_rows[k >> 5] >> (k & 31) & 1u) || !tree::sees_node(mask, at - e.P)) continue;
+              const int blk = __ldg(p.block_tables + int64_t(it.s) * p.bt_stride + at / p.block_size);
+              if (blk < 0 || int64_t(blk) >= p.num_blocks) continue;
+              const uint16_t* v = static_cast<const uint16_t*>(p.value_cache) + int64_t(blk) * p.cs_block +
+                                  int64_t(it.kvh) * p.cs_head + int64_t(at % p.block_size) * D + 32 * c;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if ((v[i] & 0x7f80u) == 0x7f80u) w[i] = __float_as_uint(__uint_as_float(w[i]) + bf16_lo_to_f32(v[i]));
+            }
+          }
+          if (!row_ok) continue;
+          if (whole) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + trow * p.out_stride_t +
+                                 int64_t(it.kvh * g + r % g) * p.out_stride_h + 32 * c;
+            uint32_t o16[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const __nv_bfloat162 pr = __floats2bfloat162_rn(__uint_as_float(w[2 * i]) * inv,
+                                                              __uint_as_float(w[2 * i + 1]) * inv);
+              o16[i] = *reinterpret_cast<const uint32_t*>(&pr);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(out + 8 * i) =
+                  make_uint4(o16[4 * i], o16[4 * i + 1], o16[4 * i + 2], o16[4 * i + 3]);
+          } else {
+            uint4* o = reinterpret_cast<uint4*>(sp.o + prow * D + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          }
+        }
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&st->bars[kOFree + wg]);
+    }
+    if (!ok && lane == 0) {
+      st->abort = 1;
+      raise_device_error(p.err, kErrTimeout);
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 0) tc::dealloc(tmem, kTmemCols);
+}
+
+// Folds the items cut by range borders.  Block (c, y): the item that begins in range c and
+// goes on behind it, rows 32 y .. 32 y + 31 of its row tiles; a warp takes a row, its lanes
+// D / 32 columns each.  The parts are taken in order.
+constexpr int kMergeWarps = 8, kMergeRows = 32;
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ TreeParams p, const TreeSplit sp) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  constexpr int kCols = D / 32;
+  const int c = int(blockIdx.x);
+  const TreeSplit::Tail t = sp.tails[c];
+  const int g = p.group, TQ = kBM / g;
+  const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+  for (int i = warp; i < kMergeRows; i += kMergeWarps) {
+    const int row = int(blockIdx.y) * kMergeRows + i, qt = row / kBM, r = row % kBM;
+    const int node = qt * TQ + r / g;
+    if (r >= TQ * g || node >= t.nodes) continue;
+    float M = -INFINITY, den = 0.f, o[kCols];
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) o[k] = 0.f;
+    constexpr int kInFlight = 4;
+    for (int b0 = c; b0 <= t.last; b0 += kInFlight) {
+      float2 ml[kInFlight];
+      float v[kInFlight][kCols];
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        ml[u] = make_float2(-INFINITY, 0.f);
+        if (b0 + u <= t.last) {
+          const int64_t pr = int64_t(2 * (b0 + u) + (b0 + u == c ? 1 : 0)) * sp.rows + row;
+          ml[u] = sp.ml[pr];
+          const float* src = sp.o + pr * D + lane * kCols;
+          if constexpr (kCols == 4) {
+            const float4 f = *reinterpret_cast<const float4*>(src);
+            v[u][0] = f.x; v[u][1] = f.y; v[u][2] = f.z; v[u][3] = f.w;
+          } else {
+            const float2 f = *reinterpret_cast<const float2*>(src);
+            v[u][0] = f.x; v[u][1] = f.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kInFlight; ++u) {
+        if (b0 + u > t.last) break;
+        // (a part whose positions the row does not see, or whose scores are all NaN, has no
+        // maximum: it counts as it stands)
+        const float m2 = fmaxf(M, ml[u].x), ref = m2 == -INFINITY ? 0.f : m2;
+        const float a = M == -INFINITY ? 1.f : fast_exp2(M - ref);
+        const float b = ml[u].x == -INFINITY ? 1.f : fast_exp2(ml[u].x - ref);
+        den = den * a + ml[u].y * b;
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) o[k] = o[k] * a + v[u][k] * b;
+        M = m2;
+      }
+    }
+    const float inv = den != 0.f ? 1.f / den : 0.f;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(t.row0 + node) * p.out_stride_t +
+                         int64_t(t.kvh * g + r % g) * p.out_stride_h + lane * kCols;
+#pragma unroll
+    for (int k = 0; k < kCols; k += 2) {
+      const __nv_bfloat162 pr = __floats2bfloat162_rn(o[k] * inv, o[k + 1] * inv);
+      *reinterpret_cast<uint32_t*>(out + k) = *reinterpret_cast<const uint32_t*>(&pr);
+    }
+  }
+}
+
+}  // namespace tree_tc
+
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 tree_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// 3-D map over the queries [T, Hq, D]: box = 64 columns x the group's heads x `nodes` rows,
+// 128-byte swizzle.
+cudaError_t make_tree_query_map(CUtensorMap* map, const TreeParams& p, int nodes) {
+  auto fn = tree_map_encoder();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {cuuint64_t(p.head_dim), cuuint64_t(p.num_heads), cuuint64_t(p.num_tokens)};
+  // (the stride of a dimension of one may be anything)
+  const int64_t sh = p.num_heads > 1 ? p.q_stride_h : p.head_dim;
+  const int64_t st = p.num_tokens > 1 ? p.q_stride_t : sh * p.num_heads;
+  const cuuint64_t strides[2] = {cuuint64_t(sh) * 2, cuuint64_t(st) * 2};
+  const cuuint32_t box[3] = {64, cuuint32_t(p.group), cuuint32_t(nodes)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.query), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_dependent(void (*kern)(TreeParams, TreeSplit), dim3 grid, int threads, const TreeParams& p,
+                             const TreeSplit& sp, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, sp);
+  note_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_tree_tc_tpl(const TreeParams& p, TreeSplit sp, cudaStream_t stream) {
+  using C = tree_tc::Cfg<D>;
+  CUtensorMap mq, mk, mv;
+  // the tile's rows that can hold nodes: no more than the batch has
+  sp.q_nodes = int(std::min<int64_t>(tree_tc::kBM / p.group, p.query_start_loc ? p.num_tokens : 1));
+  cudaError_t e = make_tree_query_map(&mq, p, sp.q_nodes);
+  if (e != cudaSuccess) return e;
+  DecodeParams dp{};  // (what the cache maps are made from)
+  dp.kv_dtype = p.kv_dtype;
+  dp.head_dim = p.head_dim;
+  dp.block_size = p.block_size;
+  dp.num_kv_heads = p.num_kv_heads;
+  dp.num_blocks = p.num_blocks;
+  dp.cs_head = p.num_kv_heads > 1 ? p.cs_head : int64_t(p.block_size) * p.head_dim;
+  dp.cs_block = p.num_blocks > 1 ? p.cs_block : dp.cs_head * p.num_kv_heads;
+  const int box = std::min(p.block_size, 16);
+  if ((e = cached_cache_map(&mk, p.key_cache, dp, box)) != cudaSuccess) return e;
+  if ((e = cached_cache_map(&mv, p.value_cache, dp, box)) != cudaSuccess) return e;
+  auto kern = tree_tc::tree_tc_kernel<D>;
+  static std::once_flag once[kMapCacheDevices];
+  static cudaError_t set[kMapCacheDevices];
+  int dev = 0;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMapCacheDevices) return cudaErrorInvalidDevice;
+  std::call_once(once[dev], [&] {
+    set[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
+  });
+  if (set[dev] != cudaSuccess) return set[dev];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(sp.grid));
+  cfg.blockDim = dim3(tree_tc::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, p, sp);
+  note_launch();
+  if (e != cudaSuccess) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const dim3 grid(unsigned(sp.grid), unsigned((sp.rows + tree_tc::kMergeRows - 1) / tree_tc::kMergeRows));
+  return launch_dependent(tree_tc::tree_merge_kernel<D>, grid, tree_tc::kMergeWarps * 32, p, sp, stream);
+}
+
+}  // namespace
+
+bool tree_tc_supported(const TreeParams& p) {
+  if (p.q_dtype != kBF16 || p.kv_dtype != kBF16) return false;
+  if (!(p.block_size == 8 || p.block_size == 16 || p.block_size == 32)) return false;
+  if (p.group > tree_tc::kBM) return false;
+  if (!(p.qk_scale_log2 > 0.f)) return false;  // (the maximum is taken before the scale)
+  // tensor maps take no stride of 0 (expanded views)
+  if ((p.num_heads > 1 && p.q_stride_h == 0) || (p.num_tokens > 1 && p.q_stride_t == 0)) return false;
+  if ((p.num_kv_heads > 1 && p.cs_head == 0) || (p.num_blocks > 1 && p.cs_block == 0)) return false;
+  if ((reinterpret_cast<uintptr_t>(p.query) & 15) || (p.q_stride_t & 7) || (p.q_stride_h & 7)) return false;
+  if ((reinterpret_cast<uintptr_t>(p.out) & 15) || (p.out_stride_t & 7) || (p.out_stride_h & 7)) return false;
+  return tree_map_encoder() != nullptr;
+}
+
+// Rows of a partial slot: one row tile's worth where the whole batch fits it, else two.
+int tree_tc_rows(int64_t num_tokens, int group, bool decode) {
+  const int tq = tree_tc::kBM / group;
+  if (decode) return group;
+  return num_tokens <= tq ? int(num_tokens) * group : 2 * tree_tc::kBM;
+}
+
+size_t tree_tc_workspace(int grid, int rows, int head_dim) {
+  return TreeSplit::kHeader + size_t(grid) * 2 * rows * (size_t(head_dim) + 2) * 4;
+}
+
+cudaError_t launch_tree_tc(const TreeParams& p, int grid, int rows, void* ws, cudaStream_t stream) {
+  TreeSplit sp{};
+  sp.grid = grid;
+  sp.rows = rows;
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  // (the first words of the workspace are the decode kernel's counters, zero between calls)
+  sp.tails = reinterpret_cast<TreeSplit::Tail*>(w + kWorkspaceHeader);
+  sp.o = reinterpret_cast<float*>(w + TreeSplit::kHeader);
+  sp.ml = reinterpret_cast<float2*>(sp.o + size_t(grid) * 2 * rows * p.head_dim);
+  return p.head_dim == 128 ? launch_tree_tc_tpl<128>(p, sp, stream) : launch_tree_tc_tpl<64>(p, sp, stream);
+}
+
+}  // namespace pkv
