@@ -98,11 +98,10 @@ __device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity) {
       : "=r"(done) : "r"(smem_addr(bar)), "r"(parity) : "memory");
   return done != 0;
 }
-// Bounded wait that gives up when another role has; `spin`: without suspending the thread.
-__device__ __forceinline__ bool wait(State* st, int bar, uint32_t parity, bool spin = false) {
-  const uint32_t polls = spin ? kWaitPolls << 4 : kWaitPolls;
-  for (uint32_t i = 0; i < polls; ++i) {
-    if (spin ? test_wait(&st->bars[bar], parity) : mbar_try_wait(&st->bars[bar], parity)) return true;
+// Bounded wait that gives up when another role has.
+__device__ __forceinline__ bool wait(State* st, int bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kWaitPolls; ++i) {
+    if (mbar_try_wait(&st->bars[bar], parity)) return true;
     if ((i & 255u) == 255u && st->abort) return false;
   }
   st->abort = 1;
@@ -110,8 +109,8 @@ __device__ __forceinline__ bool wait(State* st, int bar, uint32_t parity, bool s
 }
 
 // The same by a whole warp: all its lanes see one answer.
-__device__ __forceinline__ bool wait_warp(State* st, int bar, uint32_t parity, bool spin = false) {
-  return __all_sync(0xffffffffu, wait(st, bar, parity, spin));
+__device__ __forceinline__ bool wait_warp(State* st, int bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait(st, bar, parity));
 }
 
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
@@ -211,6 +210,47 @@ __device__ __forceinline__ uint32_t mask_bits(const int64_t* mask, int c0, int n
   uint32_t bits = uint32_t(b);
   if (valid < 32) bits &= (1u << valid) - 1u;
   return past | (bits << sh);
+}
+
+__device__ __forceinline__ uint32_t keep_word(const uint32_t (&k)[4], int c) {
+  return c < 2 ? (c == 0 ? k[0] : k[1]) : (c == 2 ? k[2] : k[3]);
+}
+
+// Largest of a row's 32 scores at tensor-memory column `ts`, those kept alone if kCut.
+template <bool kCut>
+__device__ __forceinline__ float row_max(uint32_t ts, uint32_t keep) {
+  uint32_t w[32];
+  tc::ld32(ts, w);
+  tc::wait_ld();
+  float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (!kCut || (keep >> i & 1u)) t[i & 3] = fmaxf(t[i & 3], __uint_as_float(w[i]));
+  return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+}
+
+// Weights 2^(score * sl - mu) of a row's 32 scores at column `ts`, written as bf16 pairs to
+// column `tp` (whose scores have been read); returns their sum.
+template <bool kCut>
+__device__ __forceinline__ float weights(uint32_t ts, uint32_t tp, uint32_t keep, float sl, float mu) {
+  uint32_t w[32], pk[16];
+  tc::ld32(ts, w);
+  tc::wait_ld();
+  float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float a = fast_exp2(fmaf(__uint_as_float(w[2 * i]), sl, -mu));
+    float b = fast_exp2(fmaf(__uint_as_float(w[2 * i + 1]), sl, -mu));
+    if (kCut) {
+      if (!(keep >> (2 * i) & 1u)) a = 0.f;
+      if (!(keep >> (2 * i + 1) & 1u)) b = 0.f;
+    }
+    ps[i & 3] += a + b;
+    const __nv_bfloat162 pr = __floats2bfloat162_rn(a, b);
+    pk[i] = *reinterpret_cast<const uint32_t*>(&pr);
+  }
+  tc::st16(tp, pk);
+  return (ps[0] + ps[1]) + (ps[2] + ps[3]);
 }
 
 template <int D>
@@ -367,84 +407,86 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       if (uses1) (void)mbar_wait_bounded(&st->bars[kQFull + 1], uint32_t(uses1 - 1) & 1u);
     }
   } else if (warp == 1) {
-    // ---- MMAs (one thread): two cursors over the steps, S ahead of P V; whichever can go
-    // next goes ---------------------------------------------------------------------------
+    // ---- MMAs (one thread): S runs up to two steps ahead of P V; whichever can go next
+    // goes, so that neither a late key tile nor a late softmax holds up the other ----------
     if (lane == 0) {
       constexpr uint32_t idS = tc::idesc_bf16(kBM, kBN, 0, 0);
       constexpr uint32_t idO = tc::idesc_bf16(kBM, D, 0, 1);
-      struct Cursor {
-        Walk w;
-        int j, qt, x, kt, oc, uses0, uses1, steps0, steps1;
-        __device__ __forceinline__ int slot() const { return (oc + qt) & 1; }
-        __device__ __forceinline__ int step() const { return slot() ? steps1 : steps0; }
-        __device__ __forceinline__ int uses() const { return slot() ? uses1 : uses0; }  // of the slot before
-        __device__ __forceinline__ void advance(const TreeParams& p) {
-          ++x;
-          if (slot()) ++steps1; else ++steps0;
-          if (++qt < w.nt) return;
-          qt = 0;
-          ++kt;
-          if (++j < w.j1) return;
-          if (w.nt == 2 || (oc & 1) == 0) ++uses0;
-          if (w.nt == 2 || (oc & 1) == 1) ++uses1;
-          oc += w.nt;
-          w.next(p);
-          j = w.j0;
-        }
+      constexpr uint64_t kOp = C::kOpBytes >> 4;  // (descriptors hold addresses / 16)
+      const uint64_t qdesc = tc::desc_sw128(sbase + C::kQ, 16, 1024), kdesc = tc::desc_sw128(sbase + C::kK, 16, 1024);
+      const uint64_t vdesc = tc::desc_sw128(sbase + C::kV, C::kHalfBytes, 1024);
+      // a step between its S and its P V: what the P V needs to know
+      struct Pending {
+        bool slot, kt, kt_phase, x, x_phase, first, last_tile, wait_o, o_phase;
       };
-      Cursor a;  // next S
-      a.w = it;
-      a.j = it.j0;
-      a.qt = a.x = a.kt = a.oc = a.uses0 = a.uses1 = a.steps0 = a.steps1 = 0;
-      Cursor b = a;  // next P V
+      Pending pend[2];  // [step & 1] (constant indices below: registers)
+      int xs = 0, xp = 0;   // next step of either kind
+      int j = it.j0, qt = 0, kt = 0, oc = 0, uses0 = 0, uses1 = 0, steps0 = 0, steps1 = 0;
       uint32_t idle = 0;
       bool ok = true;
-      while (b.w.valid()) {
+      while (it.valid() || xp < xs) {
         bool went = false;
-        if (a.w.valid() && a.x <= b.x + 1) {
-          const int slot = a.slot();
-          if (test_wait(&st->bars[kKFull + (a.kt & 1)], uint32_t(a.kt >> 1) & 1u) &&
-              (a.j > a.w.j0 || test_wait(&st->bars[kQFull + slot], uint32_t(a.uses()) & 1u))) {
+        if (it.valid() && xs <= xp + 1 && test_wait(&st->bars[kKFull + (kt & 1)], uint32_t(kt >> 1) & 1u)) {
+          const int slot = (oc + qt) & 1, u = slot ? uses1 : uses0, n = slot ? steps1 : steps0;
+          if (j > it.j0 || test_wait(&st->bars[kQFull + slot], uint32_t(u) & 1u)) {
             tc::fence_after();
-            const uint32_t kaddr = sbase + C::kK + (a.kt & 1) * C::kOpBytes;
-            const uint32_t qaddr = sbase + C::kQ + slot * C::kOpBytes;
+            const uint64_t qd = qdesc + slot * kOp, kd = kdesc + (kt & 1) * kOp;
+            const uint32_t ts = tmem + C::kS + (xs & 1) * kBN;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * C::kHalfBytes + (kk & 3) * 32;
-              tc::mma_ss(tmem + C::kS + (a.x & 1) * kBN, tc::desc_sw128(qaddr + off, 16, 1024),
-                         tc::desc_sw128(kaddr + off, 16, 1024), idS, kk > 0 ? 1u : 0u);
+              constexpr uint64_t kHalf = C::kHalfBytes >> 4;
+              const uint64_t off = (kk >> 2) * kHalf + (kk & 3) * 2;
+              tc::mma_ss(ts, qd + off, kd + off, idS, kk > 0 ? 1u : 0u);
             }
-            tc::commit(&st->bars[kSFull + 2 * slot + (a.step() & 1)]);
-            if (a.qt == a.w.nt - 1) tc::commit(&st->bars[kKEmpty + (a.kt & 1)]);
-            if (a.j == a.w.j1 - 1) tc::commit(&st->bars[kQEmpty + slot]);
-            a.advance(p);
+            tc::commit(&st->bars[kSFull + 2 * slot + (n & 1)]);
+            const bool last_row_tile = qt == it.nt - 1;
+            if (last_row_tile) tc::commit(&st->bars[kKEmpty + (kt & 1)]);
+            if (j == it.j1 - 1) tc::commit(&st->bars[kQEmpty + slot]);
+            const Pending pd = {slot != 0, (kt & 1) != 0, ((kt >> 1) & 1) != 0, (xs & 1) != 0, ((xs >> 1) & 1) != 0,
+                                j == it.j0, last_row_tile, j == it.j0 && u > 0, ((u - 1) & 1) != 0};
+            if (xs & 1) pend[1] = pd; else pend[0] = pd;
+            ++xs;
+            if (slot) ++steps1; else ++steps0;
+            if (!last_row_tile) {
+              ++qt;
+            } else {
+              qt = 0;
+              ++kt;
+              if (++j == it.j1) {
+                if (it.nt == 2 || (oc & 1) == 0) ++uses0;
+                if (it.nt == 2 || (oc & 1) == 1) ++uses1;
+                oc += it.nt;
+                it.next(p);
+                j = it.j0;
+              }
+            }
             went = true;
           }
         }
-        if (b.x < a.x) {
-          const int slot = b.slot(), u = b.uses();
-          const bool first = b.j == b.w.j0;
-          if (test_wait(&st->bars[kPFull + (b.x & 1)], uint32_t(b.x >> 1) & 1u) &&
-              test_wait(&st->bars[kVFull + (b.kt & 1)], uint32_t(b.kt >> 1) & 1u) &&
-              (!first || u == 0 || test_wait(&st->bars[kOFree + slot], uint32_t(u - 1) & 1u))) {
+        if (xp < xs) {
+          const Pending pd = (xp & 1) ? pend[1] : pend[0];
+          if (test_wait(&st->bars[kPFull + pd.x], pd.x_phase) && test_wait(&st->bars[kVFull + pd.kt], pd.kt_phase) &&
+              (!pd.wait_o || test_wait(&st->bars[kOFree + pd.slot], pd.o_phase))) {
             tc::fence_after();
-            const uint32_t vaddr = sbase + C::kV + (b.kt & 1) * C::kOpBytes;
+            const uint64_t vd = vdesc + pd.kt * kOp;
+            const uint32_t ts = tmem + C::kS + pd.x * kBN, to = tmem + C::kO + pd.slot * D;
 #pragma unroll
             for (int kk = 0; kk < kBN / 16; ++kk)
-              tc::mma_ts(tmem + C::kO + slot * D, tmem + C::kS + (b.x & 1) * kBN + 8 * kk,
-                         tc::desc_sw128(vaddr + kk * 16 * 128, C::kHalfBytes, 1024), idO,
-                         (!first || kk > 0) ? 1u : 0u);
-            tc::commit(&st->bars[kODone + slot]);
-            if (b.qt == b.w.nt - 1) tc::commit(&st->bars[kVEmpty + (b.kt & 1)]);
-            b.advance(p);
+              tc::mma_ts(to, ts + 8 * kk, vd + kk * (16 * 128 >> 4), idO, (!pd.first || kk > 0) ? 1u : 0u);
+            tc::commit(&st->bars[kODone + pd.slot]);
+            if (pd.last_tile) tc::commit(&st->bars[kVEmpty + pd.kt]);
+            ++xp;
             went = true;
           }
         }
         if (went) {
           idle = 0;
-        } else if ((++idle & 255u) == 0 && (st->abort || idle > (kWaitPolls << 4))) {
-          ok = false;
-          break;
+        } else {
+          __nanosleep(20);  // (a spinning thread takes issue slots from the softmax beside it)
+          if ((++idle & 255u) == 0 && (st->abort || idle > kWaitPolls)) {
+            ok = false;
+            break;
+          }
         }
       }
       // every MMA issued has completed before the tensor memory is freed
@@ -481,9 +523,62 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         const int x = x0 + (j - it.j0) * it.nt + qt;
         const int pos = it.q.base + j * kBN;
         const uint32_t tS = tmem + C::kS + (x & 1) * kBN + lane_off;
-        if (!(ok = wait_warp(st, kSFull + 2 * wg + (steps & 1), uint32_t(steps >> 1) & 1u, warp_ok))) break;
+        if (!(ok = wait_warp(st, kSFull + 2 * wg + (steps & 1), uint32_t(steps >> 1) & 1u))) break;
         tc::fence_after();
         const bool cut = pos + kBN > e.P || pos + kBN > e.L || pos < e.lo;  // some position may be hidden
+        if (warp_ok) {
+          uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
+          if (cut) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int at = pos + 32 * w;
+              keep[w] = n_hidden ? mask_bits(mask, at - e.P, n_hidden)
+                                 : at + 32 <= e.L ? ~0u : at >= e.L ? 0u : (1u << (e.L - at)) - 1u;
+              if (at < e.lo) keep[w] &= at + 32 <= e.lo ? 0u : ~0u << (e.lo - at);
+            }
+          }
+          // the row's maximum
+          float mx = -INFINITY;
+          if (cut) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) mx = fmaxf(mx, row_max<true>(tS + 32 * c, keep_word(keep, c)));
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) mx = fmaxf(mx, row_max<false>(tS + 32 * c, ~0u));
+          }
+          mx *= sl;
+          const bool first = m_ref == -INFINITY;
+          const bool move = row_ok && mx != -INFINITY && (first || mx > m_ref + kGap);
+          if (__any_sync(0xffffffffu, move && !first)) {
+            // some row's O is rescaled: its product of the step before has to be in it
+            if (!(ok = wait_warp(st, kODone + wg, uint32_t(steps - 1) & 1u))) break;
+            tc::fence_after();
+            const float alpha = move && !first ? fast_exp2(m_ref - mx) : 1.f;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t w[32];
+              tc::ld32(tO + 32 * c, w);
+              tc::wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+              tc::st32(tO + 32 * c, w);
+            }
+            tc::wait_st();
+            l_run *= alpha;
+          }
+          if (move) m_ref = mx;
+          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+          float sum = 0.f;
+          if (cut) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) sum += weights<true>(tS + 32 * c, tS + 16 * c, keep_word(keep, c), sl, mu);
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) sum += weights<false>(tS + 32 * c, tS + 16 * c, ~0u, sl, mu);
+          }
+          l_run += sum;
+          tc::wait_st();
+        }
         // V rows that are no position of the row's range are zeroed in shared memory (they
         // may hold anything), and infinities and NaN of drafted nodes taken out of it (rows
         // that do not see the node must not meet them): once per tile, by the first row
@@ -519,86 +614,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
             if (lane == 0) bad_rows[4 * (j - jt) + q] = bad;
           }
           fence_proxy_async_smem();
-        }
-        if (warp_ok) {
-          uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-          if (cut) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int at = pos + 32 * w;
-              keep[w] = n_hidden ? mask_bits(mask, at - e.P, n_hidden)
-                                 : at + 32 <= e.L ? ~0u : at >= e.L ? 0u : (1u << (e.L - at)) - 1u;
-              if (at < e.lo) keep[w] &= at + 32 <= e.lo ? 0u : ~0u << (e.lo - at);
-            }
-          }
-          // the row's maximum
-          float mx = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t w0[32], w1[32];
-            tc::ld32(tS + 64 * c, w0);
-            tc::ld32(tS + 64 * c + 32, w1);
-            tc::wait_ld();
-            float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            if (cut) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                if (keep[2 * c] >> i & 1u) t4[i & 1] = fmaxf(t4[i & 1], __uint_as_float(w0[i]));
-                if (keep[2 * c + 1] >> i & 1u) t4[2 + (i & 1)] = fmaxf(t4[2 + (i & 1)], __uint_as_float(w1[i]));
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                t4[i & 1] = fmaxf(t4[i & 1], __uint_as_float(w0[i]));
-                t4[2 + (i & 1)] = fmaxf(t4[2 + (i & 1)], __uint_as_float(w1[i]));
-              }
-            }
-            mx = fmaxf(mx, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
-          }
-          mx *= sl;
-          const bool first = m_ref == -INFINITY;
-          const bool move = row_ok && mx != -INFINITY && (first || mx > m_ref + kGap);
-          if (__any_sync(0xffffffffu, move && !first)) {
-            // some row's O is rescaled: its product of the step before has to be in it
-            if (!(ok = wait_warp(st, kODone + wg, uint32_t(steps - 1) & 1u, true))) break;
-            tc::fence_after();
-            const float alpha = move && !first ? fast_exp2(m_ref - mx) : 1.f;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t w[32];
-              tc::ld32(tO + 32 * c, w);
-              tc::wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
-              tc::st32(tO + 32 * c, w);
-            }
-            tc::wait_st();
-            l_run *= alpha;
-          }
-          if (move) m_ref = mx;
-          const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-          float ps[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t w[32], pk[16];
-            tc::ld32(tS + 32 * c, w);
-            tc::wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float a = fast_exp2(fmaf(__uint_as_float(w[2 * i]), sl, -mu));
-              float b = fast_exp2(fmaf(__uint_as_float(w[2 * i + 1]), sl, -mu));
-              if (cut) {
-                if (!(keep[c] >> (2 * i) & 1u)) a = 0.f;
-                if (!(keep[c] >> (2 * i + 1) & 1u)) b = 0.f;
-              }
-              ps[i & 3] += a + b;
-              const __nv_bfloat162 pr = __floats2bfloat162_rn(a, b);
-              pk[i] = *reinterpret_cast<const uint32_t*>(&pr);
-            }
-            tc::st16(tS + 16 * c, pk);  // (over scores that have been read)
-          }
-          l_run += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-          tc::wait_st();
         }
         tc::fence_before();
         __syncwarp();
