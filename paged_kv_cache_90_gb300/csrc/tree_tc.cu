@@ -31,8 +31,9 @@
 // reference maximum moves only when a row's maximum grows by more than 2^8, as in the
 // decode kernel.
 //
-// Warps: 0 streams K tiles, 2 V tiles (TMA, two-deep rings), 3 the queries; 1 issues the
-// MMAs; 4-7 and 8-11 are the softmax warpgroups.  Every wait is bounded; when one runs
+// Warps: 0 streams K tiles, 2 V tiles (TMA, rings of two and three), 3 the queries; 1 issues the
+// MMAs; 4-7 and 8-11 are the softmax warpgroups; 12 cleans the V tiles at the ends of the
+// contexts.  Every wait is bounded; when one runs
 // out the block sets an error bit and a flag that makes every role stop, lets its copies
 // and MMAs land and frees the tensor memory.
 #include <cudaTypedefs.h>
@@ -49,7 +50,8 @@ namespace tree_tc {
 
 constexpr int kBM = 128;  // rows per row tile
 constexpr int kBN = 128;  // positions per key tile
-constexpr int kThreads = 384;
+constexpr int kThreads = 416;
+constexpr int kVRing = 3;  // V tiles in flight (a V tile is held until its P V, so longer than a K tile)
 constexpr uint32_t kTmemCols = 512;
 constexpr float kGap = 8.f;  // growth of a row's maximum (log2) that moves its reference
 
@@ -58,11 +60,11 @@ struct Cfg {
   static constexpr int kHalves = D / 64;             // 64-column halves of an operand (128-byte rows)
   static constexpr uint32_t kHalfBytes = kBM * 128;  // 16 KB
   static constexpr uint32_t kOpBytes = kHalves * kHalfBytes;
-  // from the 1024-aligned base: Q[2] | K[2] | V[2] | barriers and small state
+  // from the 1024-aligned base: Q[2] | K[2] | V[3] | barriers and small state
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kK = 2 * kOpBytes;
   static constexpr uint32_t kV = kK + 2 * kOpBytes;
-  static constexpr uint32_t kState = kV + 2 * kOpBytes;
+  static constexpr uint32_t kState = kV + kVRing * kOpBytes;
   static constexpr uint32_t kStateBytes = 2048;
   static constexpr size_t kSmem = kState + kStateBytes + 1024;  // (+ alignment)
   // tensor memory: S of even and odd steps (128 columns each), then O of the two slots
@@ -73,8 +75,34 @@ struct Cfg {
 // away: those that a softmax warpgroup waits for count its own slot's steps (S: two per
 // slot, by the parity of the slot's step), since a warpgroup may wait for a step while the
 // other one is still several steps behind it.
-enum Bar { kQFull = 0, kQEmpty = 2, kKFull = 4, kKEmpty = 6, kVFull = 8, kVEmpty = 10, kSFull = 12, kPFull = 16,
-           kODone = 18, kOFree = 20, kDrain = 22, kNumBars = 23 };
+enum Bar { kQFull = 0, kQEmpty = 2, kKFull = 4, kKEmpty = 6, kVFull = 8, kVEmpty = 11, kVClean = 14, kSFull = 17,
+           kPFull = 21, kODone = 23, kOFree = 25, kDrain = 27, kNumBars = 28 };
+
+// A sequence's work in tiles: key tiles x row-tile pairs x KV heads.
+struct SeqWork {
+  tree::Extent e;
+  int base;    // first position of its first tile: the block that holds e.lo
+  int tiles;   // key tiles of an item (at least one where there are rows)
+  int pairs;   // row-tile pairs
+  __device__ __forceinline__ void load(const TreeParams& p, int s, bool* bad) {
+    e = tree::extent(p, s, bad);
+    base = e.lo - e.lo % p.block_size;
+    tiles = max(1, (e.L - base + kBN - 1) / kBN);
+    const int tq = kBM / p.group, rt = (e.n + tq - 1) / tq;
+    pairs = (rt + 1) >> 1;
+  }
+  // row tiles of pair `pair`
+  __device__ __forceinline__ int row_tiles(const TreeParams& p, int pair) const {
+    return e.n - 2 * pair * (kBM / p.group) > kBM / p.group ? 2 : 1;
+  }
+  __device__ __forceinline__ int64_t total(const TreeParams& p) const {
+    return int64_t(tiles) * pairs * p.num_kv_heads;  // (no rows: no pairs)
+  }
+};
+
+constexpr int kSeqs = 16;     // sequences of the range whose work is kept in shared memory
+constexpr int kBadItems = 6;  // items whose bad rows are kept: the cleaning warp is up to four
+                              // items ahead of a warpgroup that writes its output
 
 // Small shared state behind the operands.
 struct State {
@@ -86,8 +114,10 @@ struct State {
   int64_t total;             // all tiles
   int64_t warp_sum[kThreads / 32];
   // drafted positions with an infinity or a NaN in V, 32 to a word from the first tile
-  // that holds drafted nodes on (1024 nodes touch at most 9 tiles), per item (index mod 4)
-  uint32_t bad_rows[4][36];
+  // that holds drafted nodes on (1024 nodes touch at most 9 tiles), per item (index mod
+  // kBadItems)
+  uint32_t bad_rows[kBadItems][36];
+  SeqWork seqs[kSeqs];        // first_seq, first_seq + 1, ...
 };
 static_assert(sizeof(State) <= 2048, "state");
 
@@ -127,24 +157,6 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
       : "memory");
 }
 
-// A sequence's work in tiles: key tiles x row-tile pairs x KV heads.
-struct SeqWork {
-  tree::Extent e;
-  int base;    // first position of its first tile: the block that holds e.lo
-  int tiles;   // key tiles of an item (at least one where there are rows)
-  int pairs;   // row-tile pairs
-  __device__ __forceinline__ void load(const TreeParams& p, int s, bool* bad) {
-    e = tree::extent(p, s, bad);
-    base = e.lo - e.lo % p.block_size;
-    tiles = max(1, (e.L - base + kBN - 1) / kBN);
-    const int tq = kBM / p.group, rt = (e.n + tq - 1) / tq;
-    pairs = (rt + 1) >> 1;
-  }
-  __device__ __forceinline__ int64_t total(const TreeParams& p) const {
-    return int64_t(tiles) * pairs * p.num_kv_heads;  // (no rows: no pairs)
-  }
-};
-
 // Walks the item parts of a block's range; every role walks the same sequence.
 struct Walk {
   SeqWork q;
@@ -155,24 +167,32 @@ struct Walk {
   __device__ __forceinline__ bool valid() const { return left > 0; }
   __device__ __forceinline__ bool begins() const { return j0 == 0; }
   __device__ __forceinline__ bool ends() const { return j1 == q.tiles; }
+  // whether some position of tile j may be hidden from some row
+  __device__ __forceinline__ bool cut(int j) const {
+    const int pos = q.base + j * kBN;
+    return pos + kBN > q.e.P || pos < q.e.lo;  // (P <= L)
+  }
   __device__ __forceinline__ void part(const TreeParams& p) {
     j1 = int(min(int64_t(q.tiles), j0 + left));
-    const int tq = kBM / p.group, rt = (q.e.n + tq - 1) / tq;
-    nt = min(2, rt - 2 * pair);
+    nt = q.row_tiles(p, pair);
   }
-  __device__ __forceinline__ void start(const TreeParams& p, int seq, int64_t off, int64_t count) {
+  __device__ __forceinline__ void load(const TreeParams& p, const State* st) {
+    const int i = s - st->first_seq;
+    bool bad;
+    if (i < kSeqs) q = st->seqs[i]; else q.load(p, s, &bad);
+  }
+  __device__ __forceinline__ void start(const TreeParams& p, const State* st, int64_t count) {
     left = count;
     if (count <= 0) return;
-    bool bad;
-    s = seq;
-    q.load(p, s, &bad);
-    const int item = int(off / q.tiles);
-    j0 = int(off - int64_t(item) * q.tiles);
+    s = st->first_seq;
+    load(p, st);
+    const int item = int(st->first_off / q.tiles);
+    j0 = int(st->first_off - int64_t(item) * q.tiles);
     kvh = item / q.pairs;
     pair = item - kvh * q.pairs;
     part(p);
   }
-  __device__ __forceinline__ void next(const TreeParams& p) {
+  __device__ __forceinline__ void next(const TreeParams& p, const State* st) {
     left -= j1 - j0;
     if (left <= 0) return;
     j0 = 0;
@@ -180,9 +200,9 @@ struct Walk {
       pair = 0;
       if (++kvh == p.num_kv_heads) {
         kvh = 0;
-        bool bad;
         do {
-          q.load(p, ++s, &bad);  // (tiles are left, so a later sequence has some)
+          ++s;
+          load(p, st);  // (tiles are left, so a later sequence has some)
         } while (q.pairs == 0 && s + 1 < p.num_seqs);
       }
     }
@@ -190,9 +210,9 @@ struct Walk {
   }
 };
 
-// Bits c0 .. c0 + 31 of a row's mask: 1 for positions before the drafted nodes (c < 0), 0
+// Bits c0 .. c0 + 31 of a row's mask (its first word loaded beforehand): 1 for positions before the drafted nodes (c < 0), 0
 // behind them (c >= n).
-__device__ __forceinline__ uint32_t mask_bits(const int64_t* mask, int c0, int n) {
+__device__ __forceinline__ uint32_t mask_bits(const int64_t* mask, uint64_t word0, int c0, int n) {
   if (c0 >= n) return 0u;
   uint32_t past = 0u;
   int sh = 0;
@@ -204,16 +224,12 @@ __device__ __forceinline__ uint32_t mask_bits(const int64_t* mask, int c0, int n
   }
   if (!mask) return past;  // (no mask: every position is before the nodes, n = 0 of them)
   const int w = c0 >> 6, o = c0 & 63;
-  uint64_t b = uint64_t(__ldg(mask + w)) >> o;
+  uint64_t b = (w == 0 ? word0 : uint64_t(__ldg(mask + w))) >> o;
   if (o > 32 && 64 * (w + 1) < n) b |= uint64_t(__ldg(mask + w + 1)) << (64 - o);
   const int valid = n - c0;
   uint32_t bits = uint32_t(b);
   if (valid < 32) bits &= (1u << valid) - 1u;
   return past | (bits << sh);
-}
-
-__device__ __forceinline__ uint32_t keep_word(const uint32_t (&k)[4], int c) {
-  return c < 2 ? (c == 0 ? k[0] : k[1]) : (c == 2 ? k[2] : k[3]);
 }
 
 // Largest of a row's 32 scores at tensor-memory column `ts`, those kept alone if kCut.
@@ -330,8 +346,15 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
   const int64_t share = (total + gridDim.x - 1) / gridDim.x;
   const int64_t from = share * blockIdx.x;
   const int64_t count = max(int64_t(0), min(share, total - from));
+  if (warp == 12 && lane < kSeqs && count > 0 && st->first_seq + lane < p.num_seqs) {
+    SeqWork w;
+    bool bad;
+    w.load(p, st->first_seq + lane, &bad);
+    st->seqs[lane] = w;
+  }
+  __syncthreads();
   Walk it;
-  it.start(p, st->first_seq, st->first_off, count);
+  it.start(p, st, count);
 
   if (warp == 0 || warp == 2) {
     // ---- K (warp 0) and V (warp 2) tiles: lane i issues copy i of a tile (one box of
@@ -342,38 +365,56 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
     const uint32_t region = sbase + (isv ? C::kV : C::kK);
     const CUtensorMap* map = isv ? &tmv : &tmk;
     const int bx = lane / C::kHalves, half = lane % C::kHalves;
-    int kt = 0;
-    bool ok = true;
-    for (; ok && it.valid(); it.next(p)) {
-      const int32_t* row = p.block_tables + int64_t(it.s) * p.bt_stride;
-      // (positions before e.lo share its block; the tile's other boxes end at L)
-      auto entry = [&](int j) -> int {
-        const int key = it.q.base + j * kBN + bx * box;
-        if (bx * box >= kBN || key >= it.q.e.L) return 0;
-        const int e = __ldg(row + key / bs);
-        if (e >= 0 && int64_t(e) < p.num_blocks) return e;
-        raise_device_error(p.err, kErrTableEntry);
-        return 0;
-      };
-      int e = entry(it.j0);
-      for (int j = it.j0; j < it.j1; ++j, ++kt) {
-        const int e_next = j + 1 < it.j1 ? entry(j + 1) : 0;
-        const int slot = kt & 1, pos = it.q.base + j * kBN;
-        const int nbox = max(0, min(kBN, it.q.e.L - pos) + box - 1) / box;
-        if (lane == 0 && kt >= 2) ok = wait(st, eb + slot, uint32_t((kt - 2) >> 1) & 1u);
-        ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&st->bars[fb + slot], uint32_t(nbox * box) * 128u * C::kHalves);
+    const int ring = isv ? kVRing : 2;
+    int kt = 0, slot = 0;    // tile, its slot
+    uint32_t phase = 0;      // and the parity of the slot's use
+    // tile j of `it` is looked up (its entry loaded) one tile before its copy is issued, over
+    // the borders of items too
+    int j = it.valid() ? it.j0 : 0, pos = 0, kvh = 0, nbox = 0, e = 0;
+    bool have = false;
+    while (true) {
+      const int pos0 = pos, kvh0 = kvh, nbox0 = nbox, e0 = e;
+      const bool copy = have;
+      have = it.valid();
+      if (have) {
+        pos = it.q.base + j * kBN;
+        kvh = it.kvh;
+        nbox = max(0, min(kBN, it.q.e.L - pos) + box - 1) / box;  // (the tile's boxes end at L)
+        e = 0;
+        if (bx < nbox) e = __ldg(p.block_tables + int64_t(it.s) * p.bt_stride + (pos + bx * box) / bs);
+        if (++j == it.j1) {
+          it.next(p, st);
+          j = it.j0;
+        }
+      }
+      if (copy) {
+        bool ok = true;
+        if (lane == 0 && kt >= ring) ok = wait(st, eb + slot, phase ^ 1u);
+        if (!__shfl_sync(0xffffffffu, int(ok), 0)) break;
+        if (lane == 0) mbar_arrive_expect_tx(&st->bars[fb + slot], uint32_t(nbox0 * box) * 128u * C::kHalves);
         __syncwarp();
-        if (bx < nbox)
+        if (bx < nbox0) {
+          int blk = e0;
+          if (blk < 0 || int64_t(blk) >= p.num_blocks) {
+            raise_device_error(p.err, kErrTableEntry);
+            blk = 0;
+          }
           tma_4d(region + slot * C::kOpBytes + half * C::kHalfBytes + uint32_t(bx * box * 128), map, 64 * half,
-                 (pos + bx * box) & (bs - 1), it.kvh, e, &st->bars[fb + slot]);
-        e = e_next;
+                 (pos0 + bx * box) & (bs - 1), kvh0, blk, &st->bars[fb + slot]);
+        }
+        ++kt;
+        if (++slot == ring) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      } else if (!have) {
+        break;
       }
     }
     // the copies in flight land before the block may exit
     if (lane == 0)
-      for (int k = max(0, kt - 2); k < kt; ++k) (void)mbar_wait_bounded(&st->bars[fb + (k & 1)], uint32_t(k >> 1) & 1u);
+      for (int k = max(0, kt - ring); k < kt; ++k)
+        (void)mbar_wait_bounded(&st->bars[fb + k % ring], uint32_t(k / ring) & 1u);
   } else if (warp == 3) {
     // ---- queries: the row tiles of each item, alternating between the two slots; and what
     // the fold needs of an item that goes on in the next block's range --------------------
@@ -382,7 +423,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       bool ok = true;
       int64_t at = from;
       TreeSplit::Tail tail = {0, 0, 0, 0};
-      for (; ok && it.valid(); it.next(p)) {
+      for (; ok && it.valid(); it.next(p, st)) {
         for (int qt = 0; ok && qt < it.nt; ++qt, ++oc) {
           const int slot = oc & 1, n = slot ? uses1 : uses0;
           if (n > 0) ok = wait(st, kQEmpty + slot, uint32_t(n - 1) & 1u);
@@ -417,11 +458,15 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       const uint64_t vdesc = tc::desc_sw128(sbase + C::kV, C::kHalfBytes, 1024);
       // a step between its S and its P V: what the P V needs to know
       struct Pending {
-        bool slot, kt, kt_phase, x, x_phase, first, last_tile, wait_o, o_phase;
+        bool slot, x, x_phase, first, last_tile, wait_o, o_phase, v_phase;
+        uint8_t v, v_bar;  // V slot, and the barrier that says that it is there (and clean)
       };
       Pending pend[2];  // [step & 1] (constant indices below: registers)
       int xs = 0, xp = 0;   // next step of either kind
       int j = it.j0, qt = 0, kt = 0, oc = 0, uses0 = 0, uses1 = 0, steps0 = 0, steps1 = 0;
+      int vs = 0;               // V slot of tile kt
+      uint32_t clean = 0;       // parities of the slots' cleaned tiles
+      bool vp = false;          // and the parity of the slot's use
       uint32_t idle = 0;
       bool ok = true;
       while (it.valid() || xp < xs) {
@@ -442,8 +487,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
             const bool last_row_tile = qt == it.nt - 1;
             if (last_row_tile) tc::commit(&st->bars[kKEmpty + (kt & 1)]);
             if (j == it.j1 - 1) tc::commit(&st->bars[kQEmpty + slot]);
-            const Pending pd = {slot != 0, (kt & 1) != 0, ((kt >> 1) & 1) != 0, (xs & 1) != 0, ((xs >> 1) & 1) != 0,
-                                j == it.j0, last_row_tile, j == it.j0 && u > 0, ((u - 1) & 1) != 0};
+            const bool cut = it.cut(j);
+            const Pending pd = {slot != 0, (xs & 1) != 0, ((xs >> 1) & 1) != 0, j == it.j0, last_row_tile,
+                                j == it.j0 && u > 0, ((u - 1) & 1) != 0, cut ? ((clean >> vs) & 1u) != 0 : vp,
+                                uint8_t(vs), uint8_t((cut ? kVClean : kVFull) + vs)};
             if (xs & 1) pend[1] = pd; else pend[0] = pd;
             ++xs;
             if (slot) ++steps1; else ++steps0;
@@ -452,11 +499,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
             } else {
               qt = 0;
               ++kt;
+              clean ^= uint32_t(cut) << vs;
+              if (++vs == kVRing) {
+                vs = 0;
+                vp = !vp;
+              }
               if (++j == it.j1) {
                 if (it.nt == 2 || (oc & 1) == 0) ++uses0;
                 if (it.nt == 2 || (oc & 1) == 1) ++uses1;
                 oc += it.nt;
-                it.next(p);
+                it.next(p, st);
                 j = it.j0;
               }
             }
@@ -465,16 +517,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         }
         if (xp < xs) {
           const Pending pd = (xp & 1) ? pend[1] : pend[0];
-          if (test_wait(&st->bars[kPFull + pd.x], pd.x_phase) && test_wait(&st->bars[kVFull + pd.kt], pd.kt_phase) &&
+          if (test_wait(&st->bars[kPFull + pd.x], pd.x_phase) && test_wait(&st->bars[pd.v_bar], pd.v_phase) &&
               (!pd.wait_o || test_wait(&st->bars[kOFree + pd.slot], pd.o_phase))) {
             tc::fence_after();
-            const uint64_t vd = vdesc + pd.kt * kOp;
+            const uint64_t vd = vdesc + pd.v * kOp;
             const uint32_t ts = tmem + C::kS + pd.x * kBN, to = tmem + C::kO + pd.slot * D;
 #pragma unroll
             for (int kk = 0; kk < kBN / 16; ++kk)
               tc::mma_ts(to, ts + 8 * kk, vd + kk * (16 * 128 >> 4), idO, (!pd.first || kk > 0) ? 1u : 0u);
             tc::commit(&st->bars[kODone + pd.slot]);
-            if (pd.last_tile) tc::commit(&st->bars[kVEmpty + pd.kt]);
+            if (pd.last_tile) tc::commit(&st->bars[kVEmpty + pd.v]);
             ++xp;
             went = true;
           }
@@ -497,6 +549,62 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         raise_device_error(p.err, kErrTimeout);
       }
     }
+  } else if (warp == 12) {
+    // ---- tiles with positions that are hidden from some row: V rows that are no position
+    // of the sequence's range are zeroed in shared memory (they may hold anything), and
+    // infinities and NaN of drafted nodes taken out of it (0 x infinity would reach the rows
+    // that do not see the node; those that do get them back with the output) -------------------
+    int kt = 0, item = 0;
+    bool ok = true;
+    for (; ok && it.valid(); it.next(p, st), ++item) {
+      const tree::Extent& e = it.q.e;
+      const int jt = (e.P - it.q.base) / kBN;  // first tile with drafted nodes
+      for (int j = it.j0; j < it.j1; ++j, ++kt) {
+        // (every tile is waited for, the others too: a phase further away has no name)
+        const int slot = kt % kVRing, pos = it.q.base + j * kBN;
+        if (!(ok = wait_warp(st, kVFull + slot, uint32_t(kt / kVRing) & 1u))) break;
+        if (!it.cut(j)) continue;
+        unsigned char* vt = smem + C::kV + slot * C::kOpBytes;
+        const bool scan = p.tree_mask && pos + kBN > e.P;
+        for (int q = 0; q < 4; ++q) {
+          const int r0 = pos + 32 * q;  // 32 positions
+          uint32_t bad = 0u;
+          if (r0 < e.lo || r0 + 32 > (p.tree_mask ? e.P : e.L)) {
+            for (int i = lane; i < 32 * 8 * C::kHalves; i += 32) {
+              const int row = 32 * q + ((i >> 3) & 31), at = pos + row;
+              uint4* cell = reinterpret_cast<uint4*>(vt + (i >> 8) * C::kHalfBytes + row * 128 + (i & 7) * 16);
+              if (at < e.lo || at >= e.L) {
+                *cell = make_uint4(0u, 0u, 0u, 0u);
+              } else if (scan && at >= e.P) {
+                const uint4 v = *cell;
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                bool any = false;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if ((w[k] & 0x7f80u) == 0x7f80u) { w[k] &= 0xffff0000u; any = true; }
+                  if ((w[k] & 0x7f800000u) == 0x7f800000u) { w[k] &= 0xffffu; any = true; }
+                }
+                if (any) {
+                  *cell = make_uint4(w[0], w[1], w[2], w[3]);
+                  bad |= 1u << (row & 31);
+                }
+              }
+            }
+          }
+          if (scan) {
+            bad = __reduce_or_sync(0xffffffffu, bad);
+            if (lane == 0) st->bad_rows[item % kBadItems][4 * (j - jt) + q] = bad;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st->bars[kVClean + slot]);
+      }
+    }
+    if (!ok && lane == 0) {
+      st->abort = 1;
+      raise_device_error(p.err, kErrTimeout);
+    }
   } else if (warp >= 4) {
     // ---- softmax warpgroup `wg` (slot wg): row r of its row tiles, r = tensor-memory lane --
     const int wg = (warp >> 2) - 1, q = warp & 3;
@@ -504,9 +612,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
     const uint32_t lane_off = uint32_t(32 * q) << 16;
     const uint32_t tO = tmem + C::kO + wg * D + lane_off;
     const float sl = p.qk_scale_log2;
-    int x0 = 0, kt0 = 0, oc = 0, item = 0, steps = 0;  // `steps`: of this slot so far
+    int x0 = 0, oc = 0, item = 0, steps = 0;  // `steps`: of this slot so far
     bool ok = true;
-    for (; ok && it.valid(); x0 += (it.j1 - it.j0) * it.nt, kt0 += it.j1 - it.j0, oc += it.nt, ++item, it.next(p)) {
+    for (; ok && it.valid(); x0 += (it.j1 - it.j0) * it.nt, oc += it.nt, ++item, it.next(p, st)) {
       const int qt = (oc & 1) == wg ? 0 : 1;
       if (qt >= it.nt) continue;
       const tree::Extent& e = it.q.e;
@@ -516,7 +624,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       const int64_t trow = e.q0 + node;
       const int64_t* mask = p.tree_mask && row_ok ? p.tree_mask + trow * p.mask_stride : nullptr;
       const int n_hidden = p.tree_mask ? e.n : 0;
-      uint32_t* bad_rows = st->bad_rows[item & 3];
+      const uint64_t word0 = mask ? uint64_t(__ldg(mask)) : 0u;
+      const uint32_t* bad_rows = st->bad_rows[item % kBadItems];
       const int jt = (e.P - it.q.base) / kBN;  // first tile with drafted nodes
       float m_ref = -INFINITY, l_run = 0.f;
       for (int j = it.j0; j < it.j1; ++j, ++steps) {
@@ -525,23 +634,21 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         const uint32_t tS = tmem + C::kS + (x & 1) * kBN + lane_off;
         if (!(ok = wait_warp(st, kSFull + 2 * wg + (steps & 1), uint32_t(steps >> 1) & 1u))) break;
         tc::fence_after();
-        const bool cut = pos + kBN > e.P || pos + kBN > e.L || pos < e.lo;  // some position may be hidden
+        const bool cut = it.cut(j);
         if (warp_ok) {
-          uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-          if (cut) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int at = pos + 32 * w;
-              keep[w] = n_hidden ? mask_bits(mask, at - e.P, n_hidden)
-                                 : at + 32 <= e.L ? ~0u : at >= e.L ? 0u : (1u << (e.L - at)) - 1u;
-              if (at < e.lo) keep[w] &= at + 32 <= e.lo ? 0u : ~0u << (e.lo - at);
-            }
-          }
+          // the row's positions pos + 32 c .. + 31: a bit for each that it sees
+          auto keep = [&](int c) -> uint32_t {
+            const int at = pos + 32 * c;
+            uint32_t k = n_hidden ? mask_bits(mask, word0, at - e.P, n_hidden)
+                                  : at + 32 <= e.L ? ~0u : at >= e.L ? 0u : (1u << (e.L - at)) - 1u;
+            if (at < e.lo) k &= at + 32 <= e.lo ? 0u : ~0u << (e.lo - at);
+            return k;
+          };
           // the row's maximum
           float mx = -INFINITY;
           if (cut) {
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) mx = fmaxf(mx, row_max<true>(tS + 32 * c, keep_word(keep, c)));
+            for (int c = 0; c < 4; ++c) mx = fmaxf(mx, row_max<true>(tS + 32 * c, keep(c)));
           } else {
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) mx = fmaxf(mx, row_max<false>(tS + 32 * c, ~0u));
@@ -571,49 +678,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
           float sum = 0.f;
           if (cut) {
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) sum += weights<true>(tS + 32 * c, tS + 16 * c, keep_word(keep, c), sl, mu);
+            for (int c = 0; c < 4; ++c) sum += weights<true>(tS + 32 * c, tS + 16 * c, keep(c), sl, mu);
           } else {
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) sum += weights<false>(tS + 32 * c, tS + 16 * c, ~0u, sl, mu);
           }
           l_run += sum;
           tc::wait_st();
-        }
-        // V rows that are no position of the row's range are zeroed in shared memory (they
-        // may hold anything), and infinities and NaN of drafted nodes taken out of it (rows
-        // that do not see the node must not meet them): once per tile, by the first row
-        // tile's warpgroup
-        if (qt == 0 && cut) {
-          const int kt = kt0 + (j - it.j0);
-          if (!(ok = wait_warp(st, kVFull + (kt & 1), uint32_t(kt >> 1) & 1u))) break;
-          unsigned char* vt = smem + C::kV + (kt & 1) * C::kOpBytes;
-          const bool scan = n_hidden > 0 && pos + kBN > e.P;
-          uint32_t bad = 0u;  // of the warp's 32 rows
-          for (int i = lane; i < 32 * 8 * C::kHalves; i += 32) {
-            const int row = 32 * q + ((i >> 3) & 31), at = pos + row;
-            uint4* cell = reinterpret_cast<uint4*>(vt + (i >> 8) * C::kHalfBytes + row * 128 + (i & 7) * 16);
-            if (at < e.lo || at >= e.L) {
-              *cell = make_uint4(0u, 0u, 0u, 0u);
-            } else if (scan && at >= e.P) {
-              const uint4 v = *cell;
-              uint32_t w[4] = {v.x, v.y, v.z, v.w};
-              bool any = false;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if ((w[k] & 0x7f80u) == 0x7f80u) { w[k] &= 0xffff0000u; any = true; }
-                if ((w[k] & 0x7f800000u) == 0x7f800000u) { w[k] &= 0xffffu; any = true; }
-              }
-              if (any) {
-                *cell = make_uint4(w[0], w[1], w[2], w[3]);
-                bad |= 1u << (row & 31);
-              }
-            }
-          }
-          if (scan) {
-            bad = __reduce_or_sync(0xffffffffu, bad);
-            if (lane == 0) bad_rows[4 * (j - jt) + q] = bad;
-          }
-          fence_proxy_async_smem();
         }
         tc::fence_before();
         __syncwarp();

@@ -560,3 +560,17 @@ def test_tree_workspace_bytes():
     f = binding.tree_workspace_bytes
     assert f(0, 1, 8, 2, 128) == 0 and f(1, 0, 8, 2, 128) == 0 and f(1, 1, 7, 2, 128) == 0
     assert f(4, 64, 8, 2, 128) >= f(4, 4, 8, 2, 128) >= 0
+
+
+@gpu
+@pytest.mark.parametrize("cache", ["bf16", "int8"])
+def test_batch_of_several_tiles_an_item(cache):
+    """More items than SMs, each of several key tiles, one and two row tiles mixed; then the
+    same batch of single-tile contexts."""
+    g = torch.Generator().manual_seed(40)
+    lens = torch.randint(200, 900, (44,), generator=g).tolist()
+    nodes = torch.randint(1, 40, (44,), generator=g).tolist()
+    Case(41, lens, nodes, 4, 4, 64, 16, cache=cache).check()
+    lens = torch.randint(40, 128, (130,), generator=g).tolist()
+    nodes = torch.randint(1, 9, (130,), generator=g).tolist()
+    Case(42, lens, nodes, 4, 4, 64, 16, cache=cache).check()
