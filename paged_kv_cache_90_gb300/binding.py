@@ -142,12 +142,21 @@ def describe(t: torch.Tensor, scale: float = 1.0, head_scales: Optional[torch.Te
 # Descriptors the call wrappers pass, by everything a descriptor holds (address, dtype,
 # shape, strides, scale, per-head scales): a serving loop passes the same tensors every
 # step, and building a descriptor costs several microseconds of Python.  The cached
-# objects never leave this module, so nothing mutates them.
+# objects never leave this module, so nothing mutates them.  A key of four parts is that of
+# a tensor without scales, which most are (looking at less halves the cost).
 _DESC_CACHE: dict = {}
 _DESC_CACHE_MAX = 4096
 
 
 def _ref(t: torch.Tensor, scale: float = 1.0, head_scales: Optional[torch.Tensor] = None):
+    if scale == 1.0 and head_scales is None:
+        key = (t.data_ptr(), t.dtype, t.shape, t.stride())
+        r = _DESC_CACHE.get(key)
+        if r is None:
+            if len(_DESC_CACHE) >= _DESC_CACHE_MAX:
+                _DESC_CACHE.clear()
+            r = _DESC_CACHE[key] = ctypes.byref(describe(t))
+        return r
     hs = None if head_scales is None else (head_scales.data_ptr(), head_scales.dtype, head_scales.device,
                                              head_scales.stride())
     key = (t.data_ptr(), t.dtype, t.device, t.shape, t.stride(), float(scale), hs)
@@ -159,10 +168,16 @@ def _ref(t: torch.Tensor, scale: float = 1.0, head_scales: Optional[torch.Tensor
     return r
 
 
+_have_cuda = False  # (asked until the answer is yes: the question costs microseconds)
+
+
 def _stream(stream) -> ctypes.c_void_p:
+    global _have_cuda
     if stream is None:
-        if not torch.cuda.is_available():
-            return ctypes.c_void_p(0)
+        if not _have_cuda:
+            _have_cuda = torch.cuda.is_available()
+            if not _have_cuda:
+                return ctypes.c_void_p(0)
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)

@@ -72,7 +72,9 @@ struct TreeSplit {
   static constexpr size_t kHeader = kWorkspaceHeader + kMaxGrid * sizeof(Tail);  // (a multiple of 256)
   int grid;
   int rows;     // rows of a part's slot
+  int tq;       // nodes of a row tile: 128 / group
   int q_nodes;  // nodes of one query copy
+  int bs_shift; // log2 of the block size
   Tail* tails;  // [grid]
   float* o;     // [2 grid, rows, D]: block b's part of an item begun before it, then of its own
   float2* ml;   // [2 grid, rows] maximum (base 2) and sum

@@ -78,22 +78,25 @@ struct Cfg {
 enum Bar { kQFull = 0, kQEmpty = 2, kKFull = 4, kKEmpty = 6, kVFull = 8, kVEmpty = 11, kVClean = 14, kSFull = 17,
            kPFull = 21, kODone = 23, kOFree = 25, kDrain = 27, kNumBars = 28 };
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // A sequence's work in tiles: key tiles x row-tile pairs x KV heads.
 struct SeqWork {
   tree::Extent e;
   int base;    // first position of its first tile: the block that holds e.lo
   int tiles;   // key tiles of an item (at least one where there are rows)
   int pairs;   // row-tile pairs
-  __device__ __forceinline__ void load(const TreeParams& p, int s, bool* bad) {
+  __device__ __forceinline__ void load(const TreeParams& p, const TreeSplit& sp, int s, bool* bad) {
     e = tree::extent(p, s, bad);
-    base = e.lo - e.lo % p.block_size;
+    base = e.lo & ~(p.block_size - 1);
     tiles = max(1, (e.L - base + kBN - 1) / kBN);
-    const int tq = kBM / p.group, rt = (e.n + tq - 1) / tq;
-    pairs = (rt + 1) >> 1;
+    const uint32_t tq2 = 2 * sp.tq;
+    pairs = e.n <= int(tq2) ? (e.n > 0) : int((uint32_t(e.n) + tq2 - 1) / tq2);
   }
-  // row tiles of pair `pair`
-  __device__ __forceinline__ int row_tiles(const TreeParams& p, int pair) const {
-    return e.n - 2 * pair * (kBM / p.group) > kBM / p.group ? 2 : 1;
+  __device__ __forceinline__ int row_tiles(const TreeSplit& sp, int pair) const {  // of pair `pair`
+    return e.n - 2 * pair * sp.tq > sp.tq ? 2 : 1;
   }
   __device__ __forceinline__ int64_t total(const TreeParams& p) const {
     return int64_t(tiles) * pairs * p.num_kv_heads;  // (no rows: no pairs)
@@ -111,7 +114,7 @@ struct State {
   uint32_t tmem;
   int first_seq;             // the range's first sequence
   int64_t first_off;         // and its offset in that sequence's work
-  int64_t total;             // all tiles
+  int64_t total, share;      // all tiles, and those of a block's range
   int64_t warp_sum[kThreads / 32];
   // drafted positions with an infinity or a NaN in V, 32 to a word from the first tile
   // that holds drafted nodes on (1024 nodes touch at most 9 tiles), per item (index mod
@@ -172,27 +175,28 @@ struct Walk {
     const int pos = q.base + j * kBN;
     return pos + kBN > q.e.P || pos < q.e.lo;  // (P <= L)
   }
-  __device__ __forceinline__ void part(const TreeParams& p) {
+  __device__ __forceinline__ void part(const TreeSplit& sp) {
     j1 = int(min(int64_t(q.tiles), j0 + left));
-    nt = q.row_tiles(p, pair);
+    nt = q.row_tiles(sp, pair);
   }
-  __device__ __forceinline__ void load(const TreeParams& p, const State* st) {
+  __device__ __forceinline__ void load(const TreeParams& p, const TreeSplit& sp, const State* st) {
     const int i = s - st->first_seq;
     bool bad;
-    if (i < kSeqs) q = st->seqs[i]; else q.load(p, s, &bad);
+    if (i < kSeqs) q = st->seqs[i]; else q.load(p, sp, s, &bad);
   }
-  __device__ __forceinline__ void start(const TreeParams& p, const State* st, int64_t count) {
+  __device__ __forceinline__ void start(const TreeParams& p, const TreeSplit& sp, const State* st, int64_t count) {
     left = count;
     if (count <= 0) return;
     s = st->first_seq;
-    load(p, st);
-    const int item = int(st->first_off / q.tiles);
-    j0 = int(st->first_off - int64_t(item) * q.tiles);
-    kvh = item / q.pairs;
+    load(p, sp, st);
+    const int64_t off = st->first_off;
+    const int item = off < q.tiles ? 0 : off <= 0xffffffff ? int(uint32_t(off) / uint32_t(q.tiles)) : int(off / q.tiles);
+    j0 = int(off - int64_t(item) * q.tiles);
+    kvh = q.pairs == 1 ? item : item / q.pairs;
     pair = item - kvh * q.pairs;
-    part(p);
+    part(sp);
   }
-  __device__ __forceinline__ void next(const TreeParams& p, const State* st) {
+  __device__ __forceinline__ void next(const TreeParams& p, const TreeSplit& sp, const State* st) {
     left -= j1 - j0;
     if (left <= 0) return;
     j0 = 0;
@@ -202,11 +206,11 @@ struct Walk {
         kvh = 0;
         do {
           ++s;
-          load(p, st);  // (tiles are left, so a later sequence has some)
+          load(p, sp, st);  // (tiles are left, so a later sequence has some)
         } while (q.pairs == 0 && s + 1 < p.num_seqs);
       }
     }
-    part(p);
+    part(sp);
   }
 };
 
@@ -278,7 +282,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
   unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   State* st = reinterpret_cast<State*>(smem + C::kState);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = p.group, TQ = kBM / g;
+  const int g = p.group, TQ = sp.tq;
   const uint32_t sbase = smem_addr(smem);
 
   if (tid == 0) {
@@ -290,21 +294,26 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
     fence_barrier_init();
   }
   if (warp == 0) tc::alloc(&st->tmem, kTmemCols);
+  if (tid == 32) {  // the first copies find their maps near
+    prefetch_map(&tmq);
+    prefetch_map(&tmk);
+    prefetch_map(&tmv);
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing of the caller's is read before
   asm volatile("griddepcontrol.launch_dependents;");
 
   // ---- the block's range of the flattened tiles: every thread adds up a run of sequences,
   // then the one whose run holds the range's start finds the sequence -------------------
+  const int per = p.num_seqs <= kThreads ? 1 : (p.num_seqs + kThreads - 1) / kThreads;
+  const int s0 = min(p.num_seqs, tid * per), s1 = min(p.num_seqs, s0 + per);
+  SeqWork mine;  // the last one of the run (the only one where there are no more than threads)
   {
-    const int per = (p.num_seqs + kThreads - 1) / kThreads;
-    const int s0 = min(p.num_seqs, tid * per), s1 = min(p.num_seqs, s0 + per);
     int64_t sum = 0;
     for (int s = s0; s < s1; ++s) {
-      SeqWork w;
       bool bad;
-      w.load(p, s, &bad);
+      mine.load(p, sp, s, &bad);
       if (bad && blockIdx.x == 0) raise_device_error(p.err, kErrContextLen);
-      sum += w.total(p);
+      sum += mine.total(p);
     }
     int64_t incl = sum;
 #pragma unroll
@@ -315,18 +324,21 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
     if (lane == 31) st->warp_sum[warp] = incl;
     __syncthreads();
     int64_t before = 0, total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += st->warp_sum[w];
-      total += st->warp_sum[w];
+    const int warps = (p.num_seqs + 32 * per - 1) / (32 * per);  // that hold sequences
+    for (int w = 0; w < warps; ++w) {
+      const int64_t x = st->warp_sum[w];
+      if (w < warp) before += x;
+      total += x;
     }
-    const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t share = total <= 0x7fffffff ? int64_t((uint32_t(total) + gridDim.x - 1) / gridDim.x)
+                                              : (total + gridDim.x - 1) / gridDim.x;
     const int64_t from = share * blockIdx.x;
     int64_t at = before + incl - sum;  // where this thread's run starts
     if (from >= at && from < at + sum) {
       for (int s = s0; s < s1; ++s) {
-        SeqWork w;
+        SeqWork w = mine;
         bool bad;
-        w.load(p, s, &bad);
+        if (per > 1) w.load(p, sp, s, &bad);
         const int64_t n = w.total(p);
         if (from < at + n) {
           st->first_seq = s;
@@ -336,25 +348,32 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         at += n;
       }
     }
-    if (tid == 0) st->total = total;
+    if (tid == 0) {
+      st->total = total;
+      st->share = share;
+    }
   }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = st->tmem;
-  const int64_t total = st->total;
-  const int64_t share = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t total = st->total, share = st->share;
   const int64_t from = share * blockIdx.x;
   const int64_t count = max(int64_t(0), min(share, total - from));
-  if (warp == 12 && lane < kSeqs && count > 0 && st->first_seq + lane < p.num_seqs) {
-    SeqWork w;
-    bool bad;
-    w.load(p, st->first_seq + lane, &bad);
-    st->seqs[lane] = w;
+  if (count > 0) {
+    const int first = st->first_seq;
+    if (per == 1) {
+      if (s0 < s1 && s0 >= first && s0 < first + kSeqs) st->seqs[s0 - first] = mine;
+    } else if (tid < kSeqs && first + tid < p.num_seqs) {
+      SeqWork w;
+      bool bad;
+      w.load(p, sp, first + tid, &bad);
+      st->seqs[tid] = w;
+    }
   }
   __syncthreads();
   Walk it;
-  it.start(p, st, count);
+  it.start(p, sp, st, count);
 
   if (warp == 0 || warp == 2) {
     // ---- K (warp 0) and V (warp 2) tiles: lane i issues copy i of a tile (one box of
@@ -381,9 +400,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         kvh = it.kvh;
         nbox = max(0, min(kBN, it.q.e.L - pos) + box - 1) / box;  // (the tile's boxes end at L)
         e = 0;
-        if (bx < nbox) e = __ldg(p.block_tables + int64_t(it.s) * p.bt_stride + (pos + bx * box) / bs);
+        if (bx < nbox) e = __ldg(p.block_tables + int64_t(it.s) * p.bt_stride + ((pos + bx * box) >> sp.bs_shift));
         if (++j == it.j1) {
-          it.next(p, st);
+          it.next(p, sp, st);
           j = it.j0;
         }
       }
@@ -423,7 +442,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       bool ok = true;
       int64_t at = from;
       TreeSplit::Tail tail = {0, 0, 0, 0};
-      for (; ok && it.valid(); it.next(p, st)) {
+      for (; ok && it.valid(); it.next(p, sp, st)) {
         for (int qt = 0; ok && qt < it.nt; ++qt, ++oc) {
           const int slot = oc & 1, n = slot ? uses1 : uses0;
           if (n > 0) ok = wait(st, kQEmpty + slot, uint32_t(n - 1) & 1u);
@@ -508,7 +527,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
                 if (it.nt == 2 || (oc & 1) == 0) ++uses0;
                 if (it.nt == 2 || (oc & 1) == 1) ++uses1;
                 oc += it.nt;
-                it.next(p, st);
+                it.next(p, sp, st);
                 j = it.j0;
               }
             }
@@ -556,7 +575,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
     // that do not see the node; those that do get them back with the output) -------------------
     int kt = 0, item = 0;
     bool ok = true;
-    for (; ok && it.valid(); it.next(p, st), ++item) {
+    for (; ok && it.valid(); it.next(p, sp, st), ++item) {
       const tree::Extent& e = it.q.e;
       const int jt = (e.P - it.q.base) / kBN;  // first tile with drafted nodes
       for (int j = it.j0; j < it.j1; ++j, ++kt) {
@@ -608,17 +627,17 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
   } else if (warp >= 4) {
     // ---- softmax warpgroup `wg` (slot wg): row r of its row tiles, r = tensor-memory lane --
     const int wg = (warp >> 2) - 1, q = warp & 3;
-    const int r = 32 * q + lane;
+    const int r = 32 * q + lane, r_node = r / g, r_head = r - r_node * g;
     const uint32_t lane_off = uint32_t(32 * q) << 16;
     const uint32_t tO = tmem + C::kO + wg * D + lane_off;
     const float sl = p.qk_scale_log2;
     int x0 = 0, oc = 0, item = 0, steps = 0;  // `steps`: of this slot so far
     bool ok = true;
-    for (; ok && it.valid(); x0 += (it.j1 - it.j0) * it.nt, oc += it.nt, ++item, it.next(p, st)) {
+    for (; ok && it.valid(); x0 += (it.j1 - it.j0) * it.nt, oc += it.nt, ++item, it.next(p, sp, st)) {
       const int qt = (oc & 1) == wg ? 0 : 1;
       if (qt >= it.nt) continue;
       const tree::Extent& e = it.q.e;
-      const int node = (2 * it.pair + qt) * TQ + r / g;
+      const int node = (2 * it.pair + qt) * TQ + r_node;
       const bool row_ok = r < TQ * g && node < e.n;
       const bool warp_ok = __any_sync(0xffffffffu, row_ok);
       const int64_t trow = e.q0 + node;
@@ -714,10 +733,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
             for (int k = 32 * bw0; k < 32 * bw1; ++k) {
               const int at = it.q.base + jt * kBN + k;
               if (!(bad_rows[k >> 5] >> (k & 31) & 1u) || !tree::sees_node(mask, at - e.P)) continue;
-              const int blk = __ldg(p.block_tables + int64_t(it.s) * p.bt_stride + at / p.block_size);
+              const int blk = __ldg(p.block_tables + int64_t(it.s) * p.bt_stride + (at >> sp.bs_shift));
               if (blk < 0 || int64_t(blk) >= p.num_blocks) continue;
               const uint16_t* v = static_cast<const uint16_t*>(p.value_cache) + int64_t(blk) * p.cs_block +
-                                  int64_t(it.kvh) * p.cs_head + int64_t(at % p.block_size) * D + 32 * c;
+                                  int64_t(it.kvh) * p.cs_head + int64_t(at & (p.block_size - 1)) * D + 32 * c;
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if ((v[i] & 0x7f80u) == 0x7f80u) w[i] = __float_as_uint(__uint_as_float(w[i]) + bf16_lo_to_f32(v[i]));
@@ -726,7 +745,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
           if (!row_ok) continue;
           if (whole) {
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + trow * p.out_stride_t +
-                                 int64_t(it.kvh * g + r % g) * p.out_stride_h + 32 * c;
+                                 int64_t(it.kvh * g + r_head) * p.out_stride_h + 32 * c;
             uint32_t o16[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -761,65 +780,85 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
 }
 
 // Folds the items cut by range borders.  Block (c, y): the item that begins in range c and
-// goes on behind it, rows 32 y .. 32 y + 31 of its row tiles; a warp takes a row, its lanes
-// D / 32 columns each.  The parts are taken in order.
+// goes on behind it, rows 32 y .. 32 y + 31 of its row tiles; a warp takes four of them at
+// once (their loads overlap), its lanes D / 32 columns each.  The parts are taken in order.
 constexpr int kMergeWarps = 8, kMergeRows = 32;
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ TreeParams p, const TreeSplit sp) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  constexpr int kCols = D / 32;
+  constexpr int kCols = D / 32, kRows = kMergeRows / kMergeWarps;
   const int c = int(blockIdx.x);
   const TreeSplit::Tail t = sp.tails[c];
-  const int g = p.group, TQ = kBM / g;
+  const int g = p.group, TQ = sp.tq;
   const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
-  for (int i = warp; i < kMergeRows; i += kMergeWarps) {
-    const int row = int(blockIdx.y) * kMergeRows + i, qt = row / kBM, r = row % kBM;
-    const int node = qt * TQ + r / g;
-    if (r >= TQ * g || node >= t.nodes) continue;
-    float M = -INFINITY, den = 0.f, o[kCols];
+  int row[kRows], node[kRows];
+  bool live[kRows], any = false;
 #pragma unroll
-    for (int k = 0; k < kCols; ++k) o[k] = 0.f;
-    constexpr int kInFlight = 4;
-    for (int b0 = c; b0 <= t.last; b0 += kInFlight) {
-      float2 ml[kInFlight];
-      float v[kInFlight][kCols];
+  for (int i = 0; i < kRows; ++i) {
+    row[i] = int(blockIdx.y) * kMergeRows + i * kMergeWarps + warp;
+    const int qt = row[i] / kBM, r = row[i] % kBM;
+    node[i] = qt * TQ + r / g;
+    live[i] = r < TQ * g && node[i] < t.nodes;
+    any |= live[i];
+  }
+  if (!any) return;
+  float M[kRows], den[kRows], o[kRows][kCols];
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
-        ml[u] = make_float2(-INFINITY, 0.f);
-        if (b0 + u <= t.last) {
-          const int64_t pr = int64_t(2 * (b0 + u) + (b0 + u == c ? 1 : 0)) * sp.rows + row;
-          ml[u] = sp.ml[pr];
+  for (int i = 0; i < kRows; ++i) {
+    M[i] = -INFINITY;
+    den[i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) o[i][k] = 0.f;
+  }
+  constexpr int kInFlight = 2;
+  for (int b0 = c; b0 <= t.last; b0 += kInFlight) {
+    float2 ml[kInFlight][kRows];
+    float v[kInFlight][kRows][kCols];
+#pragma unroll
+    for (int u = 0; u < kInFlight; ++u)
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        ml[u][i] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) v[u][i][k] = 0.f;
+        if (b0 + u <= t.last && live[i]) {
+          const int64_t pr = int64_t(2 * (b0 + u) + (b0 + u == c ? 1 : 0)) * sp.rows + row[i];
+          ml[u][i] = sp.ml[pr];
           const float* src = sp.o + pr * D + lane * kCols;
           if constexpr (kCols == 4) {
             const float4 f = *reinterpret_cast<const float4*>(src);
-            v[u][0] = f.x; v[u][1] = f.y; v[u][2] = f.z; v[u][3] = f.w;
+            v[u][i][0] = f.x; v[u][i][1] = f.y; v[u][i][2] = f.z; v[u][i][3] = f.w;
           } else {
             const float2 f = *reinterpret_cast<const float2*>(src);
-            v[u][0] = f.x; v[u][1] = f.y;
+            v[u][i][0] = f.x; v[u][i][1] = f.y;
           }
         }
       }
 #pragma unroll
-      for (int u = 0; u < kInFlight; ++u) {
-        if (b0 + u > t.last) break;
+    for (int u = 0; u < kInFlight; ++u)
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
         // (a part whose positions the row does not see, or whose scores are all NaN, has no
         // maximum: it counts as it stands)
-        const float m2 = fmaxf(M, ml[u].x), ref = m2 == -INFINITY ? 0.f : m2;
-        const float a = M == -INFINITY ? 1.f : fast_exp2(M - ref);
-        const float b = ml[u].x == -INFINITY ? 1.f : fast_exp2(ml[u].x - ref);
-        den = den * a + ml[u].y * b;
+        const float m2 = fmaxf(M[i], ml[u][i].x), ref = m2 == -INFINITY ? 0.f : m2;
+        const float a = M[i] == -INFINITY ? 1.f : fast_exp2(M[i] - ref);
+        const float b = ml[u][i].x == -INFINITY ? 1.f : fast_exp2(ml[u][i].x - ref);
+        den[i] = den[i] * a + ml[u][i].y * b;
 #pragma unroll
-        for (int k = 0; k < kCols; ++k) o[k] = o[k] * a + v[u][k] * b;
-        M = m2;
+        for (int k = 0; k < kCols; ++k) o[i][k] = o[i][k] * a + v[u][i][k] * b;
+        M[i] = m2;
       }
-    }
-    const float inv = den != 0.f ? 1.f / den : 0.f;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(t.row0 + node) * p.out_stride_t +
-                         int64_t(t.kvh * g + r % g) * p.out_stride_h + lane * kCols;
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (!live[i]) continue;
+    const float inv = den[i] != 0.f ? 1.f / den[i] : 0.f;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(t.row0 + node[i]) * p.out_stride_t +
+                         int64_t(t.kvh * g + (row[i] % kBM) % g) * p.out_stride_h + lane * kCols;
 #pragma unroll
     for (int k = 0; k < kCols; k += 2) {
-      const __nv_bfloat162 pr = __floats2bfloat162_rn(o[k] * inv, o[k + 1] * inv);
+      const __nv_bfloat162 pr = __floats2bfloat162_rn(o[i][k] * inv, o[i][k + 1] * inv);
       *reinterpret_cast<uint32_t*>(out + k) = *reinterpret_cast<const uint32_t*>(&pr);
     }
   }
@@ -881,6 +920,8 @@ cudaError_t launch_tree_tc_tpl(const TreeParams& p, TreeSplit sp, cudaStream_t s
   using C = tree_tc::Cfg<D>;
   CUtensorMap mq, mk, mv;
   // the tile's rows that can hold nodes: no more than the batch has
+  sp.tq = tree_tc::kBM / p.group;
+  sp.bs_shift = p.block_size == 8 ? 3 : p.block_size == 16 ? 4 : 5;
   sp.q_nodes = int(std::min<int64_t>(tree_tc::kBM / p.group, p.query_start_loc ? p.num_tokens : 1));
   cudaError_t e = make_tree_query_map(&mq, p, sp.q_nodes);
   if (e != cudaSuccess) return e;
