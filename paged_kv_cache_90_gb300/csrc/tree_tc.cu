@@ -31,7 +31,7 @@
 // reference maximum moves only when a row's maximum grows by more than 2^8, as in the
 // decode kernel.
 //
-// Warps: 0 streams K tiles, 2 V tiles (TMA, rings of two and three), 3 the queries; 1 issues the
+// Warps: 0 streams K tiles, 2 V tiles (TMA), 3 the queries; 1 issues the
 // MMAs; 4-7 and 8-11 are the softmax warpgroups; 12 cleans the V tiles at the ends of the
 // contexts.  Every wait is bounded; when one runs
 // out the block sets an error bit and a flag that makes every role stop, lets its copies
@@ -51,20 +51,21 @@ namespace tree_tc {
 constexpr int kBM = 128;  // rows per row tile
 constexpr int kBN = 128;  // positions per key tile
 constexpr int kThreads = 416;
-constexpr int kVRing = 3;  // V tiles in flight (a V tile is held until its P V, so longer than a K tile)
 constexpr uint32_t kTmemCols = 512;
 constexpr float kGap = 8.f;  // growth of a row's maximum (log2) that moves its reference
 
+// Shared memory: slots of one operand tile (128 rows), for the queries, then a ring of K
+// tiles and one of V tiles.  In-flight copies are what the HBM rate hangs on, so the second
+// query slot goes to the K ring where no sequence has a second row tile.
 template <int D>
 struct Cfg {
   static constexpr int kHalves = D / 64;             // 64-column halves of an operand (128-byte rows)
   static constexpr uint32_t kHalfBytes = kBM * 128;  // 16 KB
   static constexpr uint32_t kOpBytes = kHalves * kHalfBytes;
-  // from the 1024-aligned base: Q[2] | K[2] | V[3] | barriers and small state
-  static constexpr uint32_t kQ = 0;
-  static constexpr uint32_t kK = 2 * kOpBytes;
-  static constexpr uint32_t kV = kK + 2 * kOpBytes;
-  static constexpr uint32_t kState = kV + kVRing * kOpBytes;
+  static constexpr int kSlots = D == 128 ? 7 : 13;
+  __host__ __device__ static constexpr int k_ring(int q_slots) { return (kSlots - q_slots) / 2; }
+  __host__ __device__ static constexpr int v_ring(int q_slots) { return kSlots - q_slots - k_ring(q_slots); }
+  static constexpr uint32_t kState = kSlots * kOpBytes;
   static constexpr uint32_t kStateBytes = 2048;
   static constexpr size_t kSmem = kState + kStateBytes + 1024;  // (+ alignment)
   // tensor memory: S of even and odd steps (128 columns each), then O of the two slots
@@ -75,8 +76,10 @@ struct Cfg {
 // away: those that a softmax warpgroup waits for count its own slot's steps (S: two per
 // slot, by the parity of the slot's step), since a warpgroup may wait for a step while the
 // other one is still several steps behind it.
-enum Bar { kQFull = 0, kQEmpty = 2, kKFull = 4, kKEmpty = 6, kVFull = 8, kVEmpty = 11, kVClean = 14, kSFull = 17,
-           kPFull = 21, kODone = 23, kOFree = 25, kDrain = 27, kNumBars = 28 };
+constexpr int kMaxRing = 6;
+enum Bar { kQFull = 0, kQEmpty = 2, kKFull = 4, kKEmpty = kKFull + kMaxRing, kVFull = kKEmpty + kMaxRing,
+           kVEmpty = kVFull + kMaxRing, kVRaw = kVEmpty + kMaxRing, kSFull = kVRaw + kMaxRing, kPFull = kSFull + 4,
+           kODone = kPFull + 2, kOFree = kODone + 2, kDrain = kOFree + 2, kNumBars = kDrain + 1 };
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
@@ -103,9 +106,9 @@ struct SeqWork {
   }
 };
 
-constexpr int kSeqs = 16;     // sequences of the range whose work is kept in shared memory
-constexpr int kBadItems = 6;  // items whose bad rows are kept: the cleaning warp is up to four
-                              // items ahead of a warpgroup that writes its output
+constexpr int kSeqs = 8;      // sequences of the range whose work is kept in shared memory
+constexpr int kBadItems = 8;  // items whose bad rows are kept: the cleaning warp is up to a ring of
+                              // V tiles and one item ahead of a warpgroup that writes its output
 
 // Small shared state behind the operands.
 struct State {
@@ -236,35 +239,60 @@ __device__ __forceinline__ uint32_t mask_bits(const int64_t* mask, uint64_t word
   return past | (bits << sh);
 }
 
-// Largest of a row's 32 scores at tensor-memory column `ts`, those kept alone if kCut.
+// The positions pos .. pos + 127 of a tile that a row sees, 64 to a word; `mask` null: no
+// drafted nodes.
+__device__ __forceinline__ void tile_bits(const tree::Extent& e, int pos, const int64_t* mask, uint64_t word0,
+                                          int n_hidden, uint64_t (&k)[2]) {
+  auto ones = [](int n) -> uint64_t { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; };
+  if (n_hidden <= 64) {
+    // bits below sh are positions before the nodes, then come the nodes' bits
+    const int sh = e.P - pos;
+    const uint64_t m = word0 & ones(n_hidden);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const int s = sh - 64 * w;
+      k[w] = ones(s) | (s >= 64 || s <= -64 ? 0ull : s >= 0 ? m << s : m >> -s);
+    }
+  } else {
+#pragma unroll 1
+    for (int w = 0; w < 4; ++w) {
+      const uint64_t b = mask_bits(mask, word0, pos + 32 * w - e.P, n_hidden);
+      if (w & 1) k[w >> 1] |= b << 32; else k[w >> 1] = b;
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < 2; ++w) k[w] &= ~ones(e.lo - pos - 64 * w);
+}
+
+// Largest of a row's 32 scores at tensor-memory column `ts`; with kCut those not kept
+// become -infinity there.
 template <bool kCut>
 __device__ __forceinline__ float row_max(uint32_t ts, uint32_t keep) {
   uint32_t w[32];
   tc::ld32(ts, w);
   tc::wait_ld();
+  if (kCut) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) w[i] = keep >> i & 1u ? w[i] : 0xff800000u;
+    tc::st32(ts, w);
+  }
   float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    if (!kCut || (keep >> i & 1u)) t[i & 3] = fmaxf(t[i & 3], __uint_as_float(w[i]));
+  for (int i = 0; i < 32; ++i) t[i & 3] = fmaxf(t[i & 3], __uint_as_float(w[i]));
   return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
 }
 
 // Weights 2^(score * sl - mu) of a row's 32 scores at column `ts`, written as bf16 pairs to
 // column `tp` (whose scores have been read); returns their sum.
-template <bool kCut>
-__device__ __forceinline__ float weights(uint32_t ts, uint32_t tp, uint32_t keep, float sl, float mu) {
+__device__ __forceinline__ float weights(uint32_t ts, uint32_t tp, float sl, float mu) {
   uint32_t w[32], pk[16];
   tc::ld32(ts, w);
   tc::wait_ld();
   float ps[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    float a = fast_exp2(fmaf(__uint_as_float(w[2 * i]), sl, -mu));
-    float b = fast_exp2(fmaf(__uint_as_float(w[2 * i + 1]), sl, -mu));
-    if (kCut) {
-      if (!(keep >> (2 * i) & 1u)) a = 0.f;
-      if (!(keep >> (2 * i + 1) & 1u)) b = 0.f;
-    }
+    const float a = fast_exp2(fmaf(__uint_as_float(w[2 * i]), sl, -mu));
+    const float b = fast_exp2(fmaf(__uint_as_float(w[2 * i + 1]), sl, -mu));
     ps[i & 3] += a + b;
     const __nv_bfloat162 pr = __floats2bfloat162_rn(a, b);
     pk[i] = *reinterpret_cast<const uint32_t*>(&pr);
@@ -306,12 +334,15 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
   // then the one whose run holds the range's start finds the sequence -------------------
   const int per = p.num_seqs <= kThreads ? 1 : (p.num_seqs + kThreads - 1) / kThreads;
   const int s0 = min(p.num_seqs, tid * per), s1 = min(p.num_seqs, s0 + per);
+  int nq;        // query slots: two where some sequence of the batch has a second row tile
   SeqWork mine;  // the last one of the run (the only one where there are no more than threads)
   {
     int64_t sum = 0;
+    bool second = false;
     for (int s = s0; s < s1; ++s) {
       bool bad;
       mine.load(p, sp, s, &bad);
+      second |= mine.e.n > sp.tq;
       if (bad && blockIdx.x == 0) raise_device_error(p.err, kErrContextLen);
       sum += mine.total(p);
     }
@@ -322,7 +353,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       if (lane >= o) incl += v;
     }
     if (lane == 31) st->warp_sum[warp] = incl;
-    __syncthreads();
+    nq = __syncthreads_or(second) ? 2 : 1;
     int64_t before = 0, total = 0;
     const int warps = (p.num_seqs + 32 * per - 1) / (32 * per);  // that hold sequences
     for (int w = 0; w < warps; ++w) {
@@ -374,6 +405,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
   __syncthreads();
   Walk it;
   it.start(p, sp, st, count);
+  const int kr = C::k_ring(nq), vr = C::v_ring(nq);
+  const uint32_t sq = sbase, sk = sq + nq * C::kOpBytes, sv = sk + kr * C::kOpBytes;  // the slots
 
   if (warp == 0 || warp == 2) {
     // ---- K (warp 0) and V (warp 2) tiles: lane i issues copy i of a tile (one box of
@@ -381,24 +414,27 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
     const bool isv = warp == 2;
     const int bs = p.block_size, box = min(bs, 16);
     const int eb = isv ? kVEmpty : kKEmpty, fb = isv ? kVFull : kKFull;
-    const uint32_t region = sbase + (isv ? C::kV : C::kK);
+    const uint32_t region = isv ? sv : sk;
     const CUtensorMap* map = isv ? &tmv : &tmk;
     const int bx = lane / C::kHalves, half = lane % C::kHalves;
-    const int ring = isv ? kVRing : 2;
+    const int ring = isv ? vr : kr;
     int kt = 0, slot = 0;    // tile, its slot
     uint32_t phase = 0;      // and the parity of the slot's use
     // tile j of `it` is looked up (its entry loaded) one tile before its copy is issued, over
     // the borders of items too
-    int j = it.valid() ? it.j0 : 0, pos = 0, kvh = 0, nbox = 0, e = 0;
+    int j = it.valid() ? it.j0 : 0, pos = 0, kvh = 0, nbox = 0, e = 0, bar = fb;
+    uint32_t raw = 0;        // the slots whose last copy went to the cleaning warp,
+    uint32_t raw_phase = 0;  // and the parities of their uses by it
     bool have = false;
     while (true) {
-      const int pos0 = pos, kvh0 = kvh, nbox0 = nbox, e0 = e;
+      const int pos0 = pos, kvh0 = kvh, nbox0 = nbox, e0 = e, bar0 = bar;
       const bool copy = have;
       have = it.valid();
       if (have) {
         pos = it.q.base + j * kBN;
         kvh = it.kvh;
         nbox = max(0, min(kBN, it.q.e.L - pos) + box - 1) / box;  // (the tile's boxes end at L)
+        bar = isv && it.cut(j) ? kVRaw : fb;
         e = 0;
         if (bx < nbox) e = __ldg(p.block_tables + int64_t(it.s) * p.bt_stride + ((pos + bx * box) >> sp.bs_shift));
         if (++j == it.j1) {
@@ -410,8 +446,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         bool ok = true;
         if (lane == 0 && kt >= ring) ok = wait(st, eb + slot, phase ^ 1u);
         if (!__shfl_sync(0xffffffffu, int(ok), 0)) break;
-        if (lane == 0) mbar_arrive_expect_tx(&st->bars[fb + slot], uint32_t(nbox0 * box) * 128u * C::kHalves);
+        if (lane == 0) mbar_arrive_expect_tx(&st->bars[bar0 + slot], uint32_t(nbox0 * box) * 128u * C::kHalves);
         __syncwarp();
+        raw = bar0 == kVRaw ? raw | 1u << slot : raw & ~(1u << slot);
+        if (bar0 == kVRaw) raw_phase ^= 1u << slot;
         if (bx < nbox0) {
           int blk = e0;
           if (blk < 0 || int64_t(blk) >= p.num_blocks) {
@@ -419,9 +457,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
             blk = 0;
           }
           tma_4d(region + slot * C::kOpBytes + half * C::kHalfBytes + uint32_t(bx * box * 128), map, 64 * half,
-                 (pos0 + bx * box) & (bs - 1), kvh0, blk, &st->bars[fb + slot]);
+                 (pos0 + bx * box) & (bs - 1), kvh0, blk, &st->bars[bar0 + slot]);
         }
         ++kt;
+
         if (++slot == ring) {
           slot = 0;
           phase ^= 1u;
@@ -432,8 +471,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
     }
     // the copies in flight land before the block may exit
     if (lane == 0)
-      for (int k = max(0, kt - ring); k < kt; ++k)
-        (void)mbar_wait_bounded(&st->bars[fb + k % ring], uint32_t(k / ring) & 1u);
+      for (int k = max(0, kt - ring); k < kt; ++k) {
+        const int s = k % ring;
+        if (raw >> s & 1u) (void)mbar_wait_bounded(&st->bars[kVRaw + s], (raw_phase >> s & 1u) ^ 1u);
+        else (void)mbar_wait_bounded(&st->bars[fb + s], uint32_t(k / ring) & 1u);
+      }
   } else if (warp == 3) {
     // ---- queries: the row tiles of each item, alternating between the two slots; and what
     // the fold needs of an item that goes on in the next block's range --------------------
@@ -444,13 +486,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       TreeSplit::Tail tail = {0, 0, 0, 0};
       for (; ok && it.valid(); it.next(p, sp, st)) {
         for (int qt = 0; ok && qt < it.nt; ++qt, ++oc) {
-          const int slot = oc & 1, n = slot ? uses1 : uses0;
+          const int slot = oc & (nq - 1), n = slot ? uses1 : uses0;
           if (n > 0) ok = wait(st, kQEmpty + slot, uint32_t(n - 1) & 1u);
           if (!ok) break;
           if (slot) ++uses1; else ++uses0;
           mbar_arrive_expect_tx(&st->bars[kQFull + slot], uint32_t(g * sp.q_nodes) * 128u * C::kHalves);
           for (int h = 0; h < C::kHalves; ++h)
-            tma_3d(sbase + C::kQ + slot * C::kOpBytes + h * C::kHalfBytes, &tmq, 64 * h, it.kvh * g,
+            tma_3d(sq + slot * C::kOpBytes + h * C::kHalfBytes, &tmq, 64 * h, it.kvh * g,
                    it.q.e.q0 + (2 * it.pair + qt) * TQ, &st->bars[kQFull + slot]);
         }
         if (it.begins() && !it.ends()) {
@@ -473,28 +515,29 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       constexpr uint32_t idS = tc::idesc_bf16(kBM, kBN, 0, 0);
       constexpr uint32_t idO = tc::idesc_bf16(kBM, D, 0, 1);
       constexpr uint64_t kOp = C::kOpBytes >> 4;  // (descriptors hold addresses / 16)
-      const uint64_t qdesc = tc::desc_sw128(sbase + C::kQ, 16, 1024), kdesc = tc::desc_sw128(sbase + C::kK, 16, 1024);
-      const uint64_t vdesc = tc::desc_sw128(sbase + C::kV, C::kHalfBytes, 1024);
+      const uint64_t qdesc = tc::desc_sw128(sq, 16, 1024), kdesc = tc::desc_sw128(sk, 16, 1024);
+      const uint64_t vdesc = tc::desc_sw128(sv, C::kHalfBytes, 1024);
       // a step between its S and its P V: what the P V needs to know
       struct Pending {
         bool slot, x, x_phase, first, last_tile, wait_o, o_phase, v_phase;
-        uint8_t v, v_bar;  // V slot, and the barrier that says that it is there (and clean)
+        uint8_t v;  // V slot
       };
       Pending pend[2];  // [step & 1] (constant indices below: registers)
       int xs = 0, xp = 0;   // next step of either kind
-      int j = it.j0, qt = 0, kt = 0, oc = 0, uses0 = 0, uses1 = 0, steps0 = 0, steps1 = 0;
-      int vs = 0;               // V slot of tile kt
-      uint32_t clean = 0;       // parities of the slots' cleaned tiles
-      bool vp = false;          // and the parity of the slot's use
+      int j = it.j0, qt = 0, oc = 0, uses0 = 0, uses1 = 0, steps0 = 0, steps1 = 0;
+      int ks = 0, vs = 0;             // K and V slot of the tile
+      uint32_t kp = 0;                // and the parities of the slots' uses
+      bool vp = false;
       uint32_t idle = 0;
       bool ok = true;
       while (it.valid() || xp < xs) {
         bool went = false;
-        if (it.valid() && xs <= xp + 1 && test_wait(&st->bars[kKFull + (kt & 1)], uint32_t(kt >> 1) & 1u)) {
+        if (it.valid() && xs <= xp + 1 && test_wait(&st->bars[kKFull + ks], kp)) {
           const int slot = (oc + qt) & 1, u = slot ? uses1 : uses0, n = slot ? steps1 : steps0;
-          if (j > it.j0 || test_wait(&st->bars[kQFull + slot], uint32_t(u) & 1u)) {
+          const int qs = slot & (nq - 1);  // (with one query slot its uses are those of both O slots)
+          if (j > it.j0 || test_wait(&st->bars[kQFull + qs], uint32_t(nq == 2 ? u : uses0 + uses1) & 1u)) {
             tc::fence_after();
-            const uint64_t qd = qdesc + slot * kOp, kd = kdesc + (kt & 1) * kOp;
+            const uint64_t qd = qdesc + qs * kOp, kd = kdesc + ks * kOp;
             const uint32_t ts = tmem + C::kS + (xs & 1) * kBN;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -504,12 +547,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
             }
             tc::commit(&st->bars[kSFull + 2 * slot + (n & 1)]);
             const bool last_row_tile = qt == it.nt - 1;
-            if (last_row_tile) tc::commit(&st->bars[kKEmpty + (kt & 1)]);
-            if (j == it.j1 - 1) tc::commit(&st->bars[kQEmpty + slot]);
-            const bool cut = it.cut(j);
+            if (last_row_tile) tc::commit(&st->bars[kKEmpty + ks]);
+            if (j == it.j1 - 1) tc::commit(&st->bars[kQEmpty + qs]);
             const Pending pd = {slot != 0, (xs & 1) != 0, ((xs >> 1) & 1) != 0, j == it.j0, last_row_tile,
-                                j == it.j0 && u > 0, ((u - 1) & 1) != 0, cut ? ((clean >> vs) & 1u) != 0 : vp,
-                                uint8_t(vs), uint8_t((cut ? kVClean : kVFull) + vs)};
+                                j == it.j0 && u > 0, ((u - 1) & 1) != 0, vp, uint8_t(vs)};
             if (xs & 1) pend[1] = pd; else pend[0] = pd;
             ++xs;
             if (slot) ++steps1; else ++steps0;
@@ -517,9 +558,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
               ++qt;
             } else {
               qt = 0;
-              ++kt;
-              clean ^= uint32_t(cut) << vs;
-              if (++vs == kVRing) {
+              if (++ks == kr) {
+                ks = 0;
+                kp ^= 1u;
+              }
+              if (++vs == vr) {
                 vs = 0;
                 vp = !vp;
               }
@@ -536,7 +579,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         }
         if (xp < xs) {
           const Pending pd = (xp & 1) ? pend[1] : pend[0];
-          if (test_wait(&st->bars[kPFull + pd.x], pd.x_phase) && test_wait(&st->bars[pd.v_bar], pd.v_phase) &&
+          if (test_wait(&st->bars[kPFull + pd.x], pd.x_phase) && test_wait(&st->bars[kVFull + pd.v], pd.v_phase) &&
               (!pd.wait_o || test_wait(&st->bars[kOFree + pd.slot], pd.o_phase))) {
             tc::fence_after();
             const uint64_t vd = vdesc + pd.v * kOp;
@@ -573,17 +616,20 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
     // of the sequence's range are zeroed in shared memory (they may hold anything), and
     // infinities and NaN of drafted nodes taken out of it (0 x infinity would reach the rows
     // that do not see the node; those that do get them back with the output) -------------------
-    int kt = 0, item = 0;
+    int slot = 0, item = 0;
+    uint32_t phase = 0;  // parities of the slots' uses by this warp
     bool ok = true;
     for (; ok && it.valid(); it.next(p, sp, st), ++item) {
       const tree::Extent& e = it.q.e;
       const int jt = (e.P - it.q.base) / kBN;  // first tile with drafted nodes
-      for (int j = it.j0; j < it.j1; ++j, ++kt) {
-        // (every tile is waited for, the others too: a phase further away has no name)
-        const int slot = kt % kVRing, pos = it.q.base + j * kBN;
-        if (!(ok = wait_warp(st, kVFull + slot, uint32_t(kt / kVRing) & 1u))) break;
+      for (int j = it.j0; j < it.j1; ++j, slot = slot + 1 == vr ? 0 : slot + 1) {
         if (!it.cut(j)) continue;
-        unsigned char* vt = smem + C::kV + slot * C::kOpBytes;
+        // (such a tile's copies complete on a barrier of its own; the MMA thread sees the
+        // tile when this warp passes it on)
+        const int pos = it.q.base + j * kBN;
+        if (!(ok = wait_warp(st, kVRaw + slot, phase >> slot & 1u))) break;
+        phase ^= 1u << slot;
+        unsigned char* vt = smem + (sv - sbase) + slot * C::kOpBytes;
         const bool scan = p.tree_mask && pos + kBN > e.P;
         for (int q = 0; q < 4; ++q) {
           const int r0 = pos + 32 * q;  // 32 positions
@@ -617,7 +663,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&st->bars[kVClean + slot]);
+        if (lane == 0) mbar_arrive(&st->bars[kVFull + slot]);
       }
     }
     if (!ok && lane == 0) {
@@ -643,7 +689,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       const int64_t trow = e.q0 + node;
       const int64_t* mask = p.tree_mask && row_ok ? p.tree_mask + trow * p.mask_stride : nullptr;
       const int n_hidden = p.tree_mask ? e.n : 0;
-      const uint64_t word0 = mask ? uint64_t(__ldg(mask)) : 0u;
+      const uint64_t word0 = mask ? uint64_t(__ldg(mask)) : 0u;  // (n_hidden = 0: P = L ends the context)
       const uint32_t* bad_rows = st->bad_rows[item % kBadItems];
       const int jt = (e.P - it.q.base) / kBN;  // first tile with drafted nodes
       float m_ref = -INFINITY, l_run = 0.f;
@@ -655,22 +701,20 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         tc::fence_after();
         const bool cut = it.cut(j);
         if (warp_ok) {
-          // the row's positions pos + 32 c .. + 31: a bit for each that it sees
-          auto keep = [&](int c) -> uint32_t {
-            const int at = pos + 32 * c;
-            uint32_t k = n_hidden ? mask_bits(mask, word0, at - e.P, n_hidden)
-                                  : at + 32 <= e.L ? ~0u : at >= e.L ? 0u : (1u << (e.L - at)) - 1u;
-            if (at < e.lo) k &= at + 32 <= e.lo ? 0u : ~0u << (e.lo - at);
-            return k;
-          };
-          // the row's maximum
           float mx = -INFINITY;
           if (cut) {
+            uint64_t k[2];
+            tile_bits(e, pos, mask, word0, n_hidden, k);
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) mx = fmaxf(mx, row_max<true>(tS + 32 * c, keep(c)));
+            for (int c = 0; c < 4; ++c) {
+              mx = fmaxf(mx, row_max<true>(tS + 32 * c, uint32_t(k[0])));
+              k[0] = k[0] >> 32 | k[1] << 32;
+              k[1] >>= 32;
+            }
+            tc::wait_st();
           } else {
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) mx = fmaxf(mx, row_max<false>(tS + 32 * c, ~0u));
+            for (int c = 0; c < 4; ++c) mx = fmaxf(mx, row_max<false>(tS + 32 * c, 0u));
           }
           mx *= sl;
           const bool first = m_ref == -INFINITY;
@@ -695,13 +739,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
           if (move) m_ref = mx;
           const float mu = m_ref == -INFINITY ? 0.f : m_ref;
           float sum = 0.f;
-          if (cut) {
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) sum += weights<true>(tS + 32 * c, tS + 16 * c, keep(c), sl, mu);
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) sum += weights<false>(tS + 32 * c, tS + 16 * c, ~0u, sl, mu);
-          }
+          for (int c = 0; c < 4; ++c) sum += weights(tS + 32 * c, tS + 16 * c, sl, mu);
           l_run += sum;
           tc::wait_st();
         }
@@ -785,8 +824,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
 constexpr int kMergeWarps = 8, kMergeRows = 32;
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ TreeParams p, const TreeSplit sp) {
+  // (no early launch of the next kernel: one block of the next call's main kernel on an SM
+  // keeps this kernel's blocks off it, 72 -> 106 us per call on ragged trees back to back)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
   constexpr int kCols = D / 32, kRows = kMergeRows / kMergeWarps;
   const int c = int(blockIdx.x);
   const TreeSplit::Tail t = sp.tails[c];
