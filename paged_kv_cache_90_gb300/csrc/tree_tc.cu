@@ -101,8 +101,8 @@ struct SeqWork {
   __device__ __forceinline__ int row_tiles(const TreeSplit& sp, int pair) const {  // of pair `pair`
     return e.n - 2 * pair * sp.tq > sp.tq ? 2 : 1;
   }
-  __device__ __forceinline__ int64_t total(const TreeParams& p) const {
-    return int64_t(tiles) * pairs * p.num_kv_heads;  // (no rows: no pairs)
+  __device__ __forceinline__ int64_t items(const TreeParams& p) const {
+    return int64_t(pairs) * p.num_kv_heads;  // (no rows: no pairs)
   }
 };
 
@@ -117,8 +117,9 @@ struct State {
   uint32_t tmem;
   int first_seq;             // the range's first sequence
   int64_t first_off;         // and its offset in that sequence's work
-  int64_t total, share;      // all tiles, and those of a block's range
-  int64_t warp_sum[kThreads / 32];
+  int64_t total, share;      // all units of work, and those of a block's range
+  int item_cost;             // units of an item beside its tiles
+  longlong2 warp_sum[kThreads / 32];
   // drafted positions with an infinity or a NaN in V, 32 to a word from the first tile
   // that holds drafted nodes on (1024 nodes touch at most 9 tiles), per item (index mod
   // kBadItems)
@@ -163,13 +164,15 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
       : "memory");
 }
 
-// Walks the item parts of a block's range; every role walks the same sequence.
+// Walks the item parts of a block's range; every role walks the same sequence.  The range
+// is in units of work: an item is `cost` units for its start and end, then its tiles.
 struct Walk {
   SeqWork q;
   int s, kvh, pair;
-  int j0, j1;      // the part's key tiles
+  int u0, u1;      // the part's units of the item
+  int j0, j1;      // and its key tiles
   int nt;          // row tiles of the pair (1 or 2)
-  int64_t left;    // tiles left in the range, this part's included
+  int64_t left;    // units left in the range, this part's included
   __device__ __forceinline__ bool valid() const { return left > 0; }
   __device__ __forceinline__ bool begins() const { return j0 == 0; }
   __device__ __forceinline__ bool ends() const { return j1 == q.tiles; }
@@ -178,8 +181,11 @@ struct Walk {
     const int pos = q.base + j * kBN;
     return pos + kBN > q.e.P || pos < q.e.lo;  // (P <= L)
   }
-  __device__ __forceinline__ void part(const TreeSplit& sp) {
-    j1 = int(min(int64_t(q.tiles), j0 + left));
+  __device__ __forceinline__ void part(const TreeSplit& sp, int cost) {
+    u1 = int(min(int64_t(q.tiles + cost), u0 + left));
+    j0 = max(0, u0 - cost);
+    j1 = u1 - cost;
+    if (j1 <= j0) left = 0;  // (the range ends before the item's first tile)
     nt = q.row_tiles(sp, pair);
   }
   __device__ __forceinline__ void load(const TreeParams& p, const TreeSplit& sp, const State* st) {
@@ -193,27 +199,28 @@ struct Walk {
     s = st->first_seq;
     load(p, sp, st);
     const int64_t off = st->first_off;
-    const int item = off < q.tiles ? 0 : off <= 0xffffffff ? int(uint32_t(off) / uint32_t(q.tiles)) : int(off / q.tiles);
-    j0 = int(off - int64_t(item) * q.tiles);
+    const uint32_t units = uint32_t(q.tiles + st->item_cost);
+    const int item = off < units ? 0 : off <= 0xffffffff ? int(uint32_t(off) / units) : int(off / units);
+    u0 = int(off - int64_t(item) * units);
     kvh = q.pairs == 1 ? item : item / q.pairs;
     pair = item - kvh * q.pairs;
-    part(sp);
+    part(sp, st->item_cost);
   }
   __device__ __forceinline__ void next(const TreeParams& p, const TreeSplit& sp, const State* st) {
-    left -= j1 - j0;
+    left -= u1 - u0;
     if (left <= 0) return;
-    j0 = 0;
+    u0 = 0;
     if (++pair == q.pairs) {
       pair = 0;
       if (++kvh == p.num_kv_heads) {
         kvh = 0;
         do {
           ++s;
-          load(p, sp, st);  // (tiles are left, so a later sequence has some)
+          load(p, sp, st);  // (units are left, so a later sequence has some)
         } while (q.pairs == 0 && s + 1 < p.num_seqs);
       }
     }
-    part(sp);
+    part(sp, st->item_cost);
   }
 };
 
@@ -337,40 +344,52 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
   int nq;        // query slots: two where some sequence of the batch has a second row tile
   SeqWork mine;  // the last one of the run (the only one where there are no more than threads)
   {
-    int64_t sum = 0;
+    longlong2 sum = make_longlong2(0, 0);  // (tiles, items)
     bool second = false;
     for (int s = s0; s < s1; ++s) {
       bool bad;
       mine.load(p, sp, s, &bad);
       second |= mine.e.n > sp.tq;
       if (bad && blockIdx.x == 0) raise_device_error(p.err, kErrContextLen);
-      sum += mine.total(p);
+      sum.x += mine.tiles * mine.items(p);
+      sum.y += mine.items(p);
     }
-    int64_t incl = sum;
+    longlong2 incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+      if (lane >= o) {
+        incl.x += x;
+        incl.y += y;
+      }
     }
     if (lane == 31) st->warp_sum[warp] = incl;
     nq = __syncthreads_or(second) ? 2 : 1;
-    int64_t before = 0, total = 0;
+    longlong2 before = make_longlong2(incl.x - sum.x, incl.y - sum.y), all = make_longlong2(0, 0);
     const int warps = (p.num_seqs + 32 * per - 1) / (32 * per);  // that hold sequences
     for (int w = 0; w < warps; ++w) {
-      const int64_t x = st->warp_sum[w];
-      if (w < warp) before += x;
-      total += x;
+      const longlong2 x = st->warp_sum[w];
+      if (w < warp) {
+        before.x += x.x;
+        before.y += x.y;
+      }
+      all.x += x.x;
+      all.y += x.y;
     }
+    // an item's start and end take about as long as a tile; where a block has few tiles the
+    // SMs matter more
+    const int cost = all.x >= 4 * int64_t(gridDim.x) ? 1 : 0;
+    const int64_t total = all.x + cost * all.y;
     const int64_t share = total <= 0x7fffffff ? int64_t((uint32_t(total) + gridDim.x - 1) / gridDim.x)
                                               : (total + gridDim.x - 1) / gridDim.x;
     const int64_t from = share * blockIdx.x;
-    int64_t at = before + incl - sum;  // where this thread's run starts
-    if (from >= at && from < at + sum) {
+    int64_t at = before.x + cost * before.y;  // where this thread's run starts
+    if (from >= at && from < at + sum.x + cost * sum.y) {
       for (int s = s0; s < s1; ++s) {
         SeqWork w = mine;
         bool bad;
         if (per > 1) w.load(p, sp, s, &bad);
-        const int64_t n = w.total(p);
+        const int64_t n = (w.tiles + cost) * w.items(p);
         if (from < at + n) {
           st->first_seq = s;
           st->first_off = from - at;
@@ -382,6 +401,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
     if (tid == 0) {
       st->total = total;
       st->share = share;
+      st->item_cost = cost;
     }
   }
   tc::fence_before();
@@ -500,9 +520,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
           tail.row0 = it.q.e.q0 + node0;
           tail.nodes = min(2 * TQ, it.q.e.n - node0);
           tail.kvh = it.kvh;
-          tail.last = int((at + it.q.tiles - 1) / share);
+          tail.last = int((at - it.u0 + it.q.tiles + st->item_cost - 1) / share);
         }
-        at += it.j1 - it.j0;
+        at += it.u1 - it.u0;
       }
       sp.tails[blockIdx.x] = tail;
       if (uses0) (void)mbar_wait_bounded(&st->bars[kQFull], uint32_t(uses0 - 1) & 1u);
