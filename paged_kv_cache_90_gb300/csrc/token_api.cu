@@ -209,12 +209,12 @@ pkv_status tree_launch(TreeParams& p, cudaStream_t stream, const char* what) {
   pkv_status st = device_state(&s);
   if (st) return st;
   p.err = s->err;
-  if (!tree_tc_supported(p)) return finish_call(s, launch_tree_core(p, stream), stream, what);
+  if (!tree_tensor_supported(p)) return finish_call(s, launch_tree_core(p, stream), stream, what);
   const int grid = tree_grid(s->num_sms);
-  const int rows = tree_tc_rows(p.num_tokens, p.group, !p.query_start_loc);
+  const int rows = tree_part_rows(p.num_tokens, p.group, !p.query_start_loc, p.kv_dtype == kI8);
   std::unique_lock<std::mutex> use(s->ws_use);
-  if ((st = ensure_workspace(s, tree_tc_workspace(grid, rows, p.head_dim), stream))) return st;
-  return finish_call(s, launch_tree_tc(p, grid, rows, s->ws, stream), stream, what);
+  if ((st = ensure_workspace(s, tree_workspace(grid, rows, p.head_dim), stream))) return st;
+  return finish_call(s, launch_tree_tensor(p, grid, rows, s->ws, stream), stream, what);
 }
 
 }  // namespace
@@ -394,7 +394,7 @@ int64_t pkv_tree_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t n
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     num_sms = int(TreeSplit::kMaxGrid);
-  return int64_t(tree_tc_workspace(tree_grid(num_sms), tree_tc_rows(num_tokens, group, false), head_dim));
+  return int64_t(tree_workspace(tree_grid(num_sms), tree_part_rows(num_tokens, group, false, false), head_dim));
 }
 
 }  // extern "C"

@@ -73,15 +73,20 @@ struct TreeSplit {
   int grid;
   int rows;     // rows of a part's slot
   int tq;       // nodes of a row tile: 128 / group
+  int item_nodes;  // nodes of an item
   int q_nodes;  // nodes of one query copy
   int bs_shift; // log2 of the block size
   Tail* tails;  // [grid]
   float* o;     // [2 grid, rows, D]: block b's part of an item begun before it, then of its own
   float2* ml;   // [2 grid, rows] maximum (base 2) and sum
 };
-bool tree_tc_supported(const TreeParams& p);
-int tree_tc_rows(int64_t num_tokens, int group, bool decode);
-size_t tree_tc_workspace(int grid, int rows, int head_dim);
-cudaError_t launch_tree_tc(const TreeParams& p, int grid, int rows, void* ws, cudaStream_t stream);
+bool tree_tc_supported(const TreeParams& p);  // bf16 caches (tree_tc.cu)
+bool tree_i8_supported(const TreeParams& p);  // token-scaled caches (tree_i8.cu)
+bool tree_tensor_supported(const TreeParams& p);
+int tree_part_rows(int64_t num_tokens, int group, bool decode, bool one_tile);
+size_t tree_workspace(int grid, int rows, int head_dim);
+cudaError_t launch_tree_tensor(const TreeParams& p, int grid, int rows, void* ws, cudaStream_t stream);
+cudaError_t launch_tree_i8(const TreeParams& p, TreeSplit sp, cudaStream_t stream);
+cudaError_t launch_tree_merge(const TreeParams& p, const TreeSplit& sp, cudaStream_t stream);
 
 }  // namespace pkv

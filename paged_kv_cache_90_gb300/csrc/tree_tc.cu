@@ -43,16 +43,15 @@
 
 #include "decode_mma_launch.cuh"
 #include "tcgen05.cuh"
-#include "tree_common.cuh"
+#include "tree_split.cuh"
 
 namespace pkv {
 namespace tree_tc {
 
-constexpr int kBM = 128;  // rows per row tile
-constexpr int kBN = 128;  // positions per key tile
+using namespace tree;
+
 constexpr int kThreads = 416;
 constexpr uint32_t kTmemCols = 512;
-constexpr float kGap = 8.f;  // growth of a row's maximum (log2) that moves its reference
 
 // Shared memory: slots of one operand tile (128 rows), for the queries, then a ring of K
 // tiles and one of V tiles.  In-flight copies are what the HBM rate hangs on, so the second
@@ -81,32 +80,6 @@ enum Bar { kQFull = 0, kQEmpty = 2, kKFull = 4, kKEmpty = kKFull + kMaxRing, kVF
            kVEmpty = kVFull + kMaxRing, kVRaw = kVEmpty + kMaxRing, kSFull = kVRaw + kMaxRing, kPFull = kSFull + 4,
            kODone = kPFull + 2, kOFree = kODone + 2, kDrain = kOFree + 2, kNumBars = kDrain + 1 };
 
-__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-}
-
-// A sequence's work in tiles: key tiles x row-tile pairs x KV heads.
-struct SeqWork {
-  tree::Extent e;
-  int base;    // first position of its first tile: the block that holds e.lo
-  int tiles;   // key tiles of an item (at least one where there are rows)
-  int pairs;   // row-tile pairs
-  __device__ __forceinline__ void load(const TreeParams& p, const TreeSplit& sp, int s, bool* bad) {
-    e = tree::extent(p, s, bad);
-    base = e.lo & ~(p.block_size - 1);
-    tiles = max(1, (e.L - base + kBN - 1) / kBN);
-    const uint32_t tq2 = 2 * sp.tq;
-    pairs = e.n <= int(tq2) ? (e.n > 0) : int((uint32_t(e.n) + tq2 - 1) / tq2);
-  }
-  __device__ __forceinline__ int row_tiles(const TreeSplit& sp, int pair) const {  // of pair `pair`
-    return e.n - 2 * pair * sp.tq > sp.tq ? 2 : 1;
-  }
-  __device__ __forceinline__ int64_t items(const TreeParams& p) const {
-    return int64_t(pairs) * p.num_kv_heads;  // (no rows: no pairs)
-  }
-};
-
-constexpr int kSeqs = 8;      // sequences of the range whose work is kept in shared memory
 constexpr int kBadItems = 8;  // items whose bad rows are kept: the cleaning warp is up to a ring of
                               // V tiles and one item ahead of a warpgroup that writes its output
 
@@ -115,117 +88,24 @@ struct State {
   uint64_t bars[kNumBars + 1];
   volatile int abort;
   uint32_t tmem;
-  int first_seq;             // the range's first sequence
-  int64_t first_off;         // and its offset in that sequence's work
-  int64_t total, share;      // all units of work, and those of a block's range
-  int item_cost;             // units of an item beside its tiles
-  longlong2 warp_sum[kThreads / 32];
+  Range range;
   // drafted positions with an infinity or a NaN in V, 32 to a word from the first tile
   // that holds drafted nodes on (1024 nodes touch at most 9 tiles), per item (index mod
   // kBadItems)
   uint32_t bad_rows[kBadItems][36];
-  SeqWork seqs[kSeqs];        // first_seq, first_seq + 1, ...
 };
 static_assert(sizeof(State) <= 2048, "state");
 
-__device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done) : "r"(smem_addr(bar)), "r"(parity) : "memory");
-  return done != 0;
-}
-// Bounded wait that gives up when another role has.
+// Waits for barrier `bar`; by a whole warp: all its lanes see one answer.
 __device__ __forceinline__ bool wait(State* st, int bar, uint32_t parity) {
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    if (mbar_try_wait(&st->bars[bar], parity)) return true;
-    if ((i & 255u) == 255u && st->abort) return false;
-  }
-  st->abort = 1;
-  return false;
+  return tree::wait(&st->bars[bar], parity, &st->abort);
 }
-
-// The same by a whole warp: all its lanes see one answer.
 __device__ __forceinline__ bool wait_warp(State* st, int bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait(st, bar, parity));
 }
 
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5}], [%6];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
-      : "memory");
-}
-
-// Walks the item parts of a block's range; every role walks the same sequence.  The range
-// is in units of work: an item is `cost` units for its start and end, then its tiles.
-struct Walk {
-  SeqWork q;
-  int s, kvh, pair;
-  int u0, u1;      // the part's units of the item
-  int j0, j1;      // and its key tiles
-  int nt;          // row tiles of the pair (1 or 2)
-  int64_t left;    // units left in the range, this part's included
-  __device__ __forceinline__ bool valid() const { return left > 0; }
-  __device__ __forceinline__ bool begins() const { return j0 == 0; }
-  __device__ __forceinline__ bool ends() const { return j1 == q.tiles; }
-  // whether some position of tile j may be hidden from some row
-  __device__ __forceinline__ bool cut(int j) const {
-    const int pos = q.base + j * kBN;
-    return pos + kBN > q.e.P || pos < q.e.lo;  // (P <= L)
-  }
-  __device__ __forceinline__ void part(const TreeSplit& sp, int cost) {
-    u1 = int(min(int64_t(q.tiles + cost), u0 + left));
-    j0 = max(0, u0 - cost);
-    j1 = u1 - cost;
-    if (j1 <= j0) left = 0;  // (the range ends before the item's first tile)
-    nt = q.row_tiles(sp, pair);
-  }
-  __device__ __forceinline__ void load(const TreeParams& p, const TreeSplit& sp, const State* st) {
-    const int i = s - st->first_seq;
-    bool bad;
-    if (i < kSeqs) q = st->seqs[i]; else q.load(p, sp, s, &bad);
-  }
-  __device__ __forceinline__ void start(const TreeParams& p, const TreeSplit& sp, const State* st, int64_t count) {
-    left = count;
-    if (count <= 0) return;
-    s = st->first_seq;
-    load(p, sp, st);
-    const int64_t off = st->first_off;
-    const uint32_t units = uint32_t(q.tiles + st->item_cost);
-    const int item = off < units ? 0 : off <= 0xffffffff ? int(uint32_t(off) / units) : int(off / units);
-    u0 = int(off - int64_t(item) * units);
-    kvh = q.pairs == 1 ? item : item / q.pairs;
-    pair = item - kvh * q.pairs;
-    part(sp, st->item_cost);
-  }
-  __device__ __forceinline__ void next(const TreeParams& p, const TreeSplit& sp, const State* st) {
-    left -= u1 - u0;
-    if (left <= 0) return;
-    u0 = 0;
-    if (++pair == q.pairs) {
-      pair = 0;
-      if (++kvh == p.num_kv_heads) {
-        kvh = 0;
-        do {
-          ++s;
-          load(p, sp, st);  // (units are left, so a later sequence has some)
-        } while (q.pairs == 0 && s + 1 < p.num_seqs);
-      }
-    }
-    part(sp, st->item_cost);
-  }
-};
-
-// Bits c0 .. c0 + 31 of a row's mask (its first word loaded beforehand): 1 for positions before the drafted nodes (c < 0), 0
-// behind them (c >= n).
+// Bits c0 .. c0 + 31 of a row's mask (its first word loaded beforehand): 1 for positions
+// before the drafted nodes (c < 0), 0 behind them (c >= n).
 __device__ __forceinline__ uint32_t mask_bits(const int64_t* mask, uint64_t word0, int c0, int n) {
   if (c0 >= n) return 0u;
   uint32_t past = 0u;
@@ -337,94 +217,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
   asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing of the caller's is read before
   asm volatile("griddepcontrol.launch_dependents;");
 
-  // ---- the block's range of the flattened tiles: every thread adds up a run of sequences,
-  // then the one whose run holds the range's start finds the sequence -------------------
-  const int per = p.num_seqs <= kThreads ? 1 : (p.num_seqs + kThreads - 1) / kThreads;
-  const int s0 = min(p.num_seqs, tid * per), s1 = min(p.num_seqs, s0 + per);
-  int nq;        // query slots: two where some sequence of the batch has a second row tile
-  SeqWork mine;  // the last one of the run (the only one where there are no more than threads)
-  {
-    longlong2 sum = make_longlong2(0, 0);  // (tiles, items)
-    bool second = false;
-    for (int s = s0; s < s1; ++s) {
-      bool bad;
-      mine.load(p, sp, s, &bad);
-      second |= mine.e.n > sp.tq;
-      if (bad && blockIdx.x == 0) raise_device_error(p.err, kErrContextLen);
-      sum.x += mine.tiles * mine.items(p);
-      sum.y += mine.items(p);
-    }
-    longlong2 incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
-      if (lane >= o) {
-        incl.x += x;
-        incl.y += y;
-      }
-    }
-    if (lane == 31) st->warp_sum[warp] = incl;
-    nq = __syncthreads_or(second) ? 2 : 1;
-    longlong2 before = make_longlong2(incl.x - sum.x, incl.y - sum.y), all = make_longlong2(0, 0);
-    const int warps = (p.num_seqs + 32 * per - 1) / (32 * per);  // that hold sequences
-    for (int w = 0; w < warps; ++w) {
-      const longlong2 x = st->warp_sum[w];
-      if (w < warp) {
-        before.x += x.x;
-        before.y += x.y;
-      }
-      all.x += x.x;
-      all.y += x.y;
-    }
-    // an item's start and end take about as long as a tile; where a block has few tiles the
-    // SMs matter more
-    const int cost = all.x >= 4 * int64_t(gridDim.x) ? 1 : 0;
-    const int64_t total = all.x + cost * all.y;
-    const int64_t share = total <= 0x7fffffff ? int64_t((uint32_t(total) + gridDim.x - 1) / gridDim.x)
-                                              : (total + gridDim.x - 1) / gridDim.x;
-    const int64_t from = share * blockIdx.x;
-    int64_t at = before.x + cost * before.y;  // where this thread's run starts
-    if (from >= at && from < at + sum.x + cost * sum.y) {
-      for (int s = s0; s < s1; ++s) {
-        SeqWork w = mine;
-        bool bad;
-        if (per > 1) w.load(p, sp, s, &bad);
-        const int64_t n = (w.tiles + cost) * w.items(p);
-        if (from < at + n) {
-          st->first_seq = s;
-          st->first_off = from - at;
-          break;
-        }
-        at += n;
-      }
-    }
-    if (tid == 0) {
-      st->total = total;
-      st->share = share;
-      st->item_cost = cost;
-    }
-  }
+  // (nq: query slots, two where some sequence of the batch has a second row tile)
+  const int nq = find_range<kThreads>(p, sp, &st->range, sp.tq) ? 2 : 1;
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = st->tmem;
-  const int64_t total = st->total, share = st->share;
-  const int64_t from = share * blockIdx.x;
-  const int64_t count = max(int64_t(0), min(share, total - from));
-  if (count > 0) {
-    const int first = st->first_seq;
-    if (per == 1) {
-      if (s0 < s1 && s0 >= first && s0 < first + kSeqs) st->seqs[s0 - first] = mine;
-    } else if (tid < kSeqs && first + tid < p.num_seqs) {
-      SeqWork w;
-      bool bad;
-      w.load(p, sp, first + tid, &bad);
-      st->seqs[tid] = w;
-    }
-  }
-  __syncthreads();
+  const Range* rg = &st->range;
+  const int64_t from = rg->from;
   Walk it;
-  it.start(p, sp, st, count);
+  it.start(p, sp, rg);
   const int kr = C::k_ring(nq), vr = C::v_ring(nq);
   const uint32_t sq = sbase, sk = sq + nq * C::kOpBytes, sv = sk + kr * C::kOpBytes;  // the slots
 
@@ -458,7 +260,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         e = 0;
         if (bx < nbox) e = __ldg(p.block_tables + int64_t(it.s) * p.bt_stride + ((pos + bx * box) >> sp.bs_shift));
         if (++j == it.j1) {
-          it.next(p, sp, st);
+          it.next(p, sp, rg);
           j = it.j0;
         }
       }
@@ -504,7 +306,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       bool ok = true;
       int64_t at = from;
       TreeSplit::Tail tail = {0, 0, 0, 0};
-      for (; ok && it.valid(); it.next(p, sp, st)) {
+      for (; ok && it.valid(); it.next(p, sp, rg)) {
         for (int qt = 0; ok && qt < it.nt; ++qt, ++oc) {
           const int slot = oc & (nq - 1), n = slot ? uses1 : uses0;
           if (n > 0) ok = wait(st, kQEmpty + slot, uint32_t(n - 1) & 1u);
@@ -520,7 +322,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
           tail.row0 = it.q.e.q0 + node0;
           tail.nodes = min(2 * TQ, it.q.e.n - node0);
           tail.kvh = it.kvh;
-          tail.last = int((at - it.u0 + it.q.tiles + st->item_cost - 1) / share);
+          tail.last = int((at - it.u0 + it.q.tiles + rg->cost - 1) / rg->share);
         }
         at += it.u1 - it.u0;
       }
@@ -590,7 +392,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
                 if (it.nt == 2 || (oc & 1) == 0) ++uses0;
                 if (it.nt == 2 || (oc & 1) == 1) ++uses1;
                 oc += it.nt;
-                it.next(p, sp, st);
+                it.next(p, sp, rg);
                 j = it.j0;
               }
             }
@@ -639,7 +441,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
     int slot = 0, item = 0;
     uint32_t phase = 0;  // parities of the slots' uses by this warp
     bool ok = true;
-    for (; ok && it.valid(); it.next(p, sp, st), ++item) {
+    for (; ok && it.valid(); it.next(p, sp, rg), ++item) {
       const tree::Extent& e = it.q.e;
       const int jt = (e.P - it.q.base) / kBN;  // first tile with drafted nodes
       for (int j = it.j0; j < it.j1; ++j, slot = slot + 1 == vr ? 0 : slot + 1) {
@@ -699,7 +501,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
     const float sl = p.qk_scale_log2;
     int x0 = 0, oc = 0, item = 0, steps = 0;  // `steps`: of this slot so far
     bool ok = true;
-    for (; ok && it.valid(); x0 += (it.j1 - it.j0) * it.nt, oc += it.nt, ++item, it.next(p, sp, st)) {
+    for (; ok && it.valid(); x0 += (it.j1 - it.j0) * it.nt, oc += it.nt, ++item, it.next(p, sp, rg)) {
       const int qt = (oc & 1) == wg ? 0 : 1;
       if (qt >= it.nt) continue;
       const tree::Extent& e = it.q.e;
@@ -838,92 +640,6 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
   if (warp == 0) tc::dealloc(tmem, kTmemCols);
 }
 
-// Folds the items cut by range borders.  Block (c, y): the item that begins in range c and
-// goes on behind it, rows 32 y .. 32 y + 31 of its row tiles; a warp takes four of them at
-// once (their loads overlap), its lanes D / 32 columns each.  The parts are taken in order.
-constexpr int kMergeWarps = 8, kMergeRows = 32;
-template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ TreeParams p, const TreeSplit sp) {
-  // (no early launch of the next kernel: one block of the next call's main kernel on an SM
-  // keeps this kernel's blocks off it, 72 -> 106 us per call on ragged trees back to back)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int kCols = D / 32, kRows = kMergeRows / kMergeWarps;
-  const int c = int(blockIdx.x);
-  const TreeSplit::Tail t = sp.tails[c];
-  const int g = p.group, TQ = sp.tq;
-  const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
-  int row[kRows], node[kRows];
-  bool live[kRows], any = false;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    row[i] = int(blockIdx.y) * kMergeRows + i * kMergeWarps + warp;
-    const int qt = row[i] / kBM, r = row[i] % kBM;
-    node[i] = qt * TQ + r / g;
-    live[i] = r < TQ * g && node[i] < t.nodes;
-    any |= live[i];
-  }
-  if (!any) return;
-  float M[kRows], den[kRows], o[kRows][kCols];
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    M[i] = -INFINITY;
-    den[i] = 0.f;
-#pragma unroll
-    for (int k = 0; k < kCols; ++k) o[i][k] = 0.f;
-  }
-  constexpr int kInFlight = 2;
-  for (int b0 = c; b0 <= t.last; b0 += kInFlight) {
-    float2 ml[kInFlight][kRows];
-    float v[kInFlight][kRows][kCols];
-#pragma unroll
-    for (int u = 0; u < kInFlight; ++u)
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        ml[u][i] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) v[u][i][k] = 0.f;
-        if (b0 + u <= t.last && live[i]) {
-          const int64_t pr = int64_t(2 * (b0 + u) + (b0 + u == c ? 1 : 0)) * sp.rows + row[i];
-          ml[u][i] = sp.ml[pr];
-          const float* src = sp.o + pr * D + lane * kCols;
-          if constexpr (kCols == 4) {
-            const float4 f = *reinterpret_cast<const float4*>(src);
-            v[u][i][0] = f.x; v[u][i][1] = f.y; v[u][i][2] = f.z; v[u][i][3] = f.w;
-          } else {
-            const float2 f = *reinterpret_cast<const float2*>(src);
-            v[u][i][0] = f.x; v[u][i][1] = f.y;
-          }
-        }
-      }
-#pragma unroll
-    for (int u = 0; u < kInFlight; ++u)
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        // (a part whose positions the row does not see, or whose scores are all NaN, has no
-        // maximum: it counts as it stands)
-        const float m2 = fmaxf(M[i], ml[u][i].x), ref = m2 == -INFINITY ? 0.f : m2;
-        const float a = M[i] == -INFINITY ? 1.f : fast_exp2(M[i] - ref);
-        const float b = ml[u][i].x == -INFINITY ? 1.f : fast_exp2(ml[u][i].x - ref);
-        den[i] = den[i] * a + ml[u][i].y * b;
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) o[i][k] = o[i][k] * a + v[u][i][k] * b;
-        M[i] = m2;
-      }
-  }
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    if (!live[i]) continue;
-    const float inv = den[i] != 0.f ? 1.f / den[i] : 0.f;
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(t.row0 + node[i]) * p.out_stride_t +
-                         int64_t(t.kvh * g + (row[i] % kBM) % g) * p.out_stride_h + lane * kCols;
-#pragma unroll
-    for (int k = 0; k < kCols; k += 2) {
-      const __nv_bfloat162 pr = __floats2bfloat162_rn(o[i][k] * inv, o[i][k + 1] * inv);
-      *reinterpret_cast<uint32_t*>(out + k) = *reinterpret_cast<const uint32_t*>(&pr);
-    }
-  }
-}
-
 }  // namespace tree_tc
 
 namespace {
@@ -959,30 +675,13 @@ cudaError_t make_tree_query_map(CUtensorMap* map, const TreeParams& p, int nodes
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t launch_dependent(void (*kern)(TreeParams, TreeSplit), dim3 grid, int threads, const TreeParams& p,
-                             const TreeSplit& sp, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(unsigned(threads));
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p, sp);
-  note_launch();
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 template <int D>
 cudaError_t launch_tree_tc_tpl(const TreeParams& p, TreeSplit sp, cudaStream_t stream) {
   using C = tree_tc::Cfg<D>;
   CUtensorMap mq, mk, mv;
+  sp.item_nodes = 2 * sp.tq;
   // the tile's rows that can hold nodes: no more than the batch has
-  sp.tq = tree_tc::kBM / p.group;
-  sp.bs_shift = p.block_size == 8 ? 3 : p.block_size == 16 ? 4 : 5;
-  sp.q_nodes = int(std::min<int64_t>(tree_tc::kBM / p.group, p.query_start_loc ? p.num_tokens : 1));
+  sp.q_nodes = int(std::min<int64_t>(tree::kBM / p.group, p.query_start_loc ? p.num_tokens : 1));
   cudaError_t e = make_tree_query_map(&mq, p, sp.q_nodes);
   if (e != cudaSuccess) return e;
   DecodeParams dp{};  // (what the cache maps are made from)
@@ -1020,8 +719,7 @@ cudaError_t launch_tree_tc_tpl(const TreeParams& p, TreeSplit sp, cudaStream_t s
   note_launch();
   if (e != cudaSuccess) return e;
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const dim3 grid(unsigned(sp.grid), unsigned((sp.rows + tree_tc::kMergeRows - 1) / tree_tc::kMergeRows));
-  return launch_dependent(tree_tc::tree_merge_kernel<D>, grid, tree_tc::kMergeWarps * 32, p, sp, stream);
+  return launch_tree_merge(p, sp, stream);
 }
 
 }  // namespace
@@ -1029,7 +727,7 @@ cudaError_t launch_tree_tc_tpl(const TreeParams& p, TreeSplit sp, cudaStream_t s
 bool tree_tc_supported(const TreeParams& p) {
   if (p.q_dtype != kBF16 || p.kv_dtype != kBF16) return false;
   if (!(p.block_size == 8 || p.block_size == 16 || p.block_size == 32)) return false;
-  if (p.group > tree_tc::kBM) return false;
+  if (p.group > tree::kBM) return false;
   if (!(p.qk_scale_log2 > 0.f)) return false;  // (the maximum is taken before the scale)
   // tensor maps take no stride of 0 (expanded views)
   if ((p.num_heads > 1 && p.q_stride_h == 0) || (p.num_tokens > 1 && p.q_stride_t == 0)) return false;
@@ -1039,26 +737,48 @@ bool tree_tc_supported(const TreeParams& p) {
   return tree_map_encoder() != nullptr;
 }
 
-// Rows of a partial slot: one row tile's worth where the whole batch fits it, else two.
-int tree_tc_rows(int64_t num_tokens, int group, bool decode) {
-  const int tq = tree_tc::kBM / group;
-  if (decode) return group;
-  return num_tokens <= tq ? int(num_tokens) * group : 2 * tree_tc::kBM;
+cudaError_t launch_tree_merge(const TreeParams& p, const TreeSplit& sp, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(sp.grid), unsigned((sp.rows + tree::kMergeRows - 1) / tree::kMergeRows));
+  cfg.blockDim = dim3(tree::kMergeWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = p.head_dim == 128 ? cudaLaunchKernelEx(&cfg, tree::tree_merge_kernel<128>, p, sp)
+                                          : cudaLaunchKernelEx(&cfg, tree::tree_merge_kernel<64>, p, sp);
+  note_launch();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-size_t tree_tc_workspace(int grid, int rows, int head_dim) {
+bool tree_tensor_supported(const TreeParams& p) { return tree_tc_supported(p) || tree_i8_supported(p); }
+
+// Rows of a part's slot: the batch's, or at most one row tile of 128 (int8 cache) or two.
+int tree_part_rows(int64_t num_tokens, int group, bool decode, bool one_tile) {
+  const int tq = tree::kBM / group;
+  if (decode) return group;
+  return num_tokens <= tq ? int(num_tokens) * group : (one_tile ? 1 : 2) * tree::kBM;
+}
+
+size_t tree_workspace(int grid, int rows, int head_dim) {
   return TreeSplit::kHeader + size_t(grid) * 2 * rows * (size_t(head_dim) + 2) * 4;
 }
 
-cudaError_t launch_tree_tc(const TreeParams& p, int grid, int rows, void* ws, cudaStream_t stream) {
+cudaError_t launch_tree_tensor(const TreeParams& p, int grid, int rows, void* ws, cudaStream_t stream) {
   TreeSplit sp{};
   sp.grid = grid;
   sp.rows = rows;
+  sp.tq = tree::kBM / p.group;
+  sp.bs_shift = 0;
+  while ((1 << sp.bs_shift) < p.block_size) ++sp.bs_shift;
   unsigned char* w = static_cast<unsigned char*>(ws);
   // (the first words of the workspace are the decode kernel's counters, zero between calls)
   sp.tails = reinterpret_cast<TreeSplit::Tail*>(w + kWorkspaceHeader);
   sp.o = reinterpret_cast<float*>(w + TreeSplit::kHeader);
   sp.ml = reinterpret_cast<float2*>(sp.o + size_t(grid) * 2 * rows * p.head_dim);
+  if (p.kv_dtype == kI8) return launch_tree_i8(p, sp, stream);
   return p.head_dim == 128 ? launch_tree_tc_tpl<128>(p, sp, stream) : launch_tree_tc_tpl<64>(p, sp, stream);
 }
 

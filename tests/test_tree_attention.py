@@ -9,7 +9,13 @@ sum_j p_j |V_j|; bf16 for a bf16 cache, f16 for an int8 one, none where they sta
 and what binary32 sums leave: a score is off by at most (D + 8) 2^-24 of sum_d |q_d k_d| scale
 (products and their sum, the scaling, the exponent's 2^-22 relative), a weight by that times
 itself twice (numerator and denominator), and a sum over L positions by L 2^-24 at most; all
-of them times sum_j p_j |V_j|."""
+of them times sum_j p_j |V_j|.
+
+With an int8 cache a weight times its value scale is an f16 number relative to the row's
+largest weight so far and to a power of two at most twice the largest value scale: below
+2^-14 of them it is subnormal and rounded by up to 2^-25 of them, whatever its own size.  The
+row's weights sum to at least 1 in those units, so L positions are off by at most
+L 2^-25 * 2 max scale * 127 = L 2^-24 max |V| together."""
 import math
 
 import pytest
@@ -144,6 +150,7 @@ class Case:
     def reference(self):
         """(outputs, sum_j p_j |V_j|, score error bound per unit roundoff), 64 bits."""
         out = torch.zeros(self.T, self.hk * self.group, self.d, dtype=torch.float64)
+        self.floor = torch.zeros(self.T, self.hk * self.group, 1, dtype=torch.float64)
         wabs, dz = torch.zeros_like(out), torch.zeros(self.T, self.hk * self.group, 1, dtype=torch.float64)
         for s, L in enumerate(self.lens):
             n, a = self.nodes[s], int(self.starts[s])
@@ -169,6 +176,9 @@ class Case:
                     o[:, h, :, c] += torch.where(keep[:, 0, :, l], p[:, h, :, l] * V[l, h, c], 0.0)
                 return o
             out[a:a + n] = pv(V).reshape(n, -1, self.d)
+            if self.cache == "int8" and self.q.dtype == torch.bfloat16:
+                top = torch.where(torch.isfinite(V), V.abs(), 0.0).amax((0, 2))              # [hk]
+                self.floor[a:a + n] = (L * 2.0 ** -24 * top).repeat_interleave(self.group)[None, :, None]
             wabs[a:a + n] = pv(V.abs()).reshape(n, -1, self.d)
             za = torch.einsum("nhgd,lhd->nhgl", q.abs(), K.abs()).masked_fill(~keep, 0.0).amax(-1) * self.scale
             dz[a:a + n] = za.reshape(n, -1, 1)
@@ -181,7 +191,8 @@ class Case:
         L = max(self.lens + [1])
         rel = p16 + 2 * ((self.d + 8) * u * dz + 2.0 ** -22) + L * u
         step = torch.finfo(self.q.dtype).eps / 2
-        return step * (ref.abs() + rel * wabs) + rel * wabs + 1e-30
+        fp = rel * wabs + self.floor
+        return step * (ref.abs() + fp) + fp + 1e-30
 
     def device(self):
         def mv(t):
