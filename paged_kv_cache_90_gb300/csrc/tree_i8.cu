@@ -28,7 +28,7 @@
 // 32 KB tile at D = 128) is close behind.
 //
 // Warps: 0 streams codes, K and V tiles in turn (bulk copies of one (block, head) run each); 1
-// issues the MMAs; 3 the queries; 4-7 and 8-11 are the softmax warpgroups; 12-15 widen.  Every
+// issues the MMAs; 3 the queries; 4-7 and 8-11 are the softmax warpgroups; 12-15 widen K, 16-19 V.  Every
 // wait is bounded; when one runs out the block sets an error bit and a flag, every role runs
 // through its loops without waiting, lets its copies and MMAs land and frees the tensor memory.
 #include <cuda_fp16.h>
@@ -44,7 +44,11 @@ namespace tree_i8 {
 
 using namespace tree;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
+// registers of a thread, by warpgroup: launched with 96 each (5 x 96 = 480), then split anew
+// into control, two softmax and two widening warpgroups (80 + 2 x 144 + 2 x 56 = 480)
+constexpr int kRegsControl = 80, kRegsSoftmax = 144, kRegsWiden = 56;
+static_assert(kRegsControl + 2 * kRegsSoftmax + 2 * kRegsWiden <= 5 * 96, "registers");
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxSlots = 16;  // of the ring of code tiles
 constexpr int kFewRows = 16;   // rows that one warpgroup takes alone
@@ -74,7 +78,7 @@ enum Bar { kQFull = 0, kQEmpty, kCodeFull, kCodeEmpty = kCodeFull + kMaxSlots, k
 // What a warpgroup keeps of its rows.
 struct Rows {
   float m[kHalfRows];        // reference maximum (base 2), -infinity before the first score
-  float limit[kHalfRows];    // a score above this moves it
+  float limit[kHalfRows];    // a score before its row's factor above this moves it
   float shift[kHalfRows];    // m, or 0 where it is -infinity
   float alpha_l[kHalfRows];  // the last move's factors on the sums and on the output
   float alpha_o[kHalfRows];
@@ -87,14 +91,17 @@ struct State {
   volatile int abort;
   uint32_t tmem;
   Range range;
+  longlong2 warp_sum[kThreads / 32];
   float qf[4][2][kHalfRows];  // a row's score factor, per item (index mod 4: a warpgroup may be
                               // two items behind the queries)
   Rows rows[2];
 };
 
+// A wait that runs out tells the others and is not one for the loops to stop at: a role
+// whose waits fail runs through its loops, so that barriers among warps always meet.
 __device__ __forceinline__ bool wait(State* st, int bar, uint32_t parity) {
-  if (st->abort) return false;
-  return tree::wait(&st->bars[bar], parity, &st->abort);
+  if (mbar_try_wait(&st->bars[bar], parity)) return true;
+  return !st->abort && tree::wait(&st->bars[bar], parity, &st->abort);
 }
 
 // The rows of a Walk's item: rows, row halves' size (a multiple of 16) and halves in use.
@@ -123,24 +130,28 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
 }
 
 // A tile of codes [128][D] -> f16 operand tile (128-byte rows of 64 columns, swizzled), by
-// the 128 threads of the widening warpgroup.
+// the 128 threads of a widening warpgroup.  `src` and `dst` are the thread's first chunk of 16
+// codes and its row: the next one is 2048 / D rows, a multiple of 8, further (so the swizzle
+// stays).
 template <int D>
-__device__ __forceinline__ void widen_tile(const unsigned char* codes, unsigned char* dst, int t) {
-  constexpr int kPer = D / 16;  // 16-code chunks of a row
-#pragma unroll 4
-  for (int i = t; i < kBN * kPer; i += 128) {
-    const int row = i / kPer, k = i % kPer;
-    const uint4 c = *reinterpret_cast<const uint4*>(codes + i * 16);
+__device__ __forceinline__ void widen_tile(const unsigned char* src, unsigned char* dst, uint32_t at0, uint32_t at1,
+                                           bool swap) {
+  constexpr int kChunks = kBN * D / 16 / 128, kRows = 128 * 16 / D;
+#pragma unroll 2
+  for (int i = 0; i < kChunks; ++i) {
+    const uint4 c = *reinterpret_cast<const uint4*>(src + i * 2048);
     const uint2 a = widen4(c.x), b = widen4(c.y), e = widen4(c.z), f = widen4(c.w);
-    unsigned char* out = dst + (k >> 2) * Cfg<D>::kHalfBytes + row * 128;
-    const int c0 = 2 * (k & 3), sw = row & 7;
     const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(e.x, e.y, f.x, f.y);
-    // (the second half's chunks in the other order: no two lanes on one bank)
-    const bool second = (k >> 2) != 0;
-    *reinterpret_cast<uint4*>(out + (((c0 + (second ? 1 : 0)) ^ sw) << 4)) = second ? hi : lo;
-    *reinterpret_cast<uint4*>(out + (((c0 + (second ? 0 : 1)) ^ sw) << 4)) = second ? lo : hi;
+    // (the upper half's chunks go in the other order: no two lanes on one bank)
+    *reinterpret_cast<uint4*>(dst + i * kRows * 128 + at0) = swap ? hi : lo;
+    *reinterpret_cast<uint4*>(dst + i * kRows * 128 + at1) = swap ? lo : hi;
   }
 }
+
+template <int N>
+__device__ __forceinline__ void less_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
 __device__ __forceinline__ bool group_any(int id, bool x) {  // over a warpgroup, with a barrier
   uint32_t r;
@@ -186,36 +197,76 @@ struct Token {
   uint64_t keep;
 };
 
-// One key tile for the NC x 16 rows of a warpgroup.  `vref`: the power of two that value
+// The sums of a thread's rows, 16 to an array so that loops over the rows need no unrolling
+// (unrolled code misses the instruction cache at every tile): a register array takes constant
+// indices only.
+struct Sums {
+  float a[4][16];
+  template <typename F>
+  __device__ __forceinline__ void chunk(int c, F f) {
+    if (c == 0) f(a[0]);
+    else if (c == 1) f(a[1]);
+    else if (c == 2) f(a[2]);
+    else f(a[3]);
+  }
+};
+
+// Weights of the 16 rows at tensor-memory column `ts`: added to their sums, and times the
+// token's value scale `vn` written as f16 to `row` (the token's row of P, swizzled by `sw`).
+template <bool kCut>
+__device__ __forceinline__ void weights(uint32_t ts, const float* qf, const float* shift, float ks, float vn,
+                                        uint32_t keep, float (&pw)[16], uint4* row, int c, int sw) {
+  uint32_t w[16], h[8];
+  float f[16], sh[16];
+  ld16(ts, w);
+  lds16(qf, f);
+  lds16(shift, sh);
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) {
+    pw[i] = fast_exp2(fmaf(__uint_as_float(w[i]) * ks, f[i], -sh[i]));
+    pw[i + 1] = fast_exp2(fmaf(__uint_as_float(w[i + 1]) * ks, f[i + 1], -sh[i + 1]));
+    float a = pw[i] * vn, b = pw[i + 1] * vn;
+    if (kCut) {  // (a position that is not seen has weight 0 whatever its scales are)
+      if (!(keep >> i & 1u)) pw[i] = a = 0.f;
+      if (!(keep >> (i + 1) & 1u)) pw[i + 1] = b = 0.f;
+    }
+    const __half2 pr = __floats2half2_rn(a, b);
+    h[i / 2] = *reinterpret_cast<const uint32_t*>(&pr);
+  }
+  row[(2 * c) ^ sw] = make_uint4(h[0], h[1], h[2], h[3]);
+  row[(2 * c + 1) ^ sw] = make_uint4(h[4], h[5], h[6], h[7]);
+}
+
+// One key tile for the nc x 16 rows of a warpgroup.  `vref`: the power of two that value
 // scales are taken relative to (0 at first).
-template <int NC>
-__device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* qf, const Token& tk, uint32_t tS,
+__device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* qf, const Token& tk, int nc, uint32_t tS,
                                              uint32_t tO, unsigned char* ptile, int done_bar, int step, bool first,
-                                             float& vref, float (&l)[kHalfRows]) {
+                                             float& vref, Sums& l) {
   const int t = 32 * tk.warp + tk.lane;
   // does a score, or the value scale, exceed its reference?
   const float av = fabsf(tk.vs);
   bool move = tk.valid && av > 16.f * vref && av < INFINITY;
 #pragma unroll 1
-  for (int c = 0; c < NC; ++c) {
+  for (int c = 0; c < nc; ++c) {
     uint32_t w[16];
-    float f[16], lim[16];
+    float lim[16];
     ld16(tS + 16 * c, w);
-    lds16(qf + 16 * c, f);
     lds16(rw.limit + 16 * c, lim);
-    const uint32_t kp = tk.cut ? uint32_t(tk.keep >> (16 * c)) & 0xffffu : 0xffffu;
+    uint32_t over = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) move |= (kp >> i & 1u) && __uint_as_float(w[i]) * tk.ks * f[i] > lim[i];
+    for (int i = 0; i < 16; ++i) over |= __uint_as_float(w[i]) * tk.ks > lim[i] ? 1u << i : 0u;
+    if (tk.cut) over &= uint32_t(tk.keep >> (16 * c));
+    move |= (over & 0xffffu) != 0u;
   }
   if (group_any(tk.id, move)) {
     // the tile's maxima, row by row, and the new references
 #pragma unroll 1
-    for (int c = 0; c < NC; ++c) {
+    for (int c = 0; c < nc; ++c) {
       uint32_t w[16];
       float f[16];
       ld16(tS + 16 * c, w);
       lds16(qf + 16 * c, f);
-      const uint32_t kp = tk.cut ? uint32_t(tk.keep >> (16 * c)) & 0xffffu : 0xffffu;
+      const uint32_t kp = uint32_t(tk.keep >> (16 * c));
       float mine = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -237,34 +288,32 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
       valpha = vref / ref;  // (both powers of two, or 0)
       vref = ref;
     }
-    if (t < 16 * NC) {
+    if (t < 16 * nc) {
       const float mx = fmaxf(fmaxf(rw.part[0][t], rw.part[1][t]), fmaxf(rw.part[2][t], rw.part[3][t]));
       const float m = rw.m[t];
       const bool go = mx > m + kGap || (m == -INFINITY && mx > -INFINITY);
       const float m2 = go ? mx : m;
       const float a = go ? fast_exp2(m - m2) : 1.f;  // (0 from -infinity)
       rw.m[t] = m2;
-      rw.limit[t] = m2 + kGap;
+      rw.limit[t] = (m2 + kGap) / qf[t];  // (a row's factor is above zero)
       rw.shift[t] = m2 == -INFINITY ? 0.f : m2;
       rw.alpha_l[t] = a;
       rw.alpha_o[t] = a * valpha;
     }
     group_sync(tk.id);
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      float a[16];
-      lds16(rw.alpha_l + 16 * c, a);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) l[16 * c + i] *= a[i];
-    }
     if (!first) {
       // O^T holds the tiles before this one
       (void)__all_sync(0xffffffffu, wait(st, done_bar, uint32_t(step - 1) & 1u));
       tc::fence_after();
 #pragma unroll 1
-      for (int c = 0; c < NC; ++c) {
+      for (int c = 0; c < nc; ++c) {
         uint32_t w[16];
         float a[16];
+        lds16(rw.alpha_l + 16 * c, a);
+        l.chunk(c, [&](float (&x)[16]) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] *= a[i];
+        });
         ld16(tO + 16 * c, w);
         lds16(rw.alpha_o + 16 * c, a);
 #pragma unroll
@@ -277,76 +326,72 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
   // the weights (P's last product has to be done before its tile is written again)
   if (step > 0) (void)__all_sync(0xffffffffu, wait(st, done_bar, uint32_t(step - 1) & 1u));
   const float vn = tk.valid ? tk.vs * (vref > 0.f ? 1.f / vref : 0.f) : 0.f;
+  uint4* row = reinterpret_cast<uint4*>(ptile + t * 128);
+#pragma unroll 1
+  for (int c = 0; c < nc; ++c) {
+    float pw[16];
+    if (tk.cut)
+      weights<true>(tS + 16 * c, qf + 16 * c, rw.shift + 16 * c, tk.ks, vn, uint32_t(tk.keep >> (16 * c)), pw, row, c, t & 7);
+    else
+      weights<false>(tS + 16 * c, qf + 16 * c, rw.shift + 16 * c, tk.ks, vn, 0u, pw, row, c, t & 7);
+    l.chunk(c, [&](float (&x)[16]) {
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    uint32_t w[16];
-    float f[16], sh[16];
-    ld16(tS + 16 * c, w);
-    lds16(qf + 16 * c, f);
-    lds16(rw.shift + 16 * c, sh);
-    uint32_t h[8];
-    const uint32_t kp = tk.cut ? uint32_t(tk.keep >> (16 * c)) & 0xffffu : 0xffffu;
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      float a = fast_exp2(fmaf(__uint_as_float(w[i]) * tk.ks, f[i], -sh[i]));
-      float b = fast_exp2(fmaf(__uint_as_float(w[i + 1]) * tk.ks, f[i + 1], -sh[i + 1]));
-      if (!(kp >> i & 1u)) a = 0.f;
-      if (!(kp >> (i + 1) & 1u)) b = 0.f;
-      l[16 * c + i] += a;
-      l[16 * c + i + 1] += b;
-      // (a position that is not seen has weight 0 whatever its scale is)
-      const __half2 pr = __floats2half2_rn(kp >> i & 1u ? a * vn : 0.f, kp >> (i + 1) & 1u ? b * vn : 0.f);
-      h[i / 2] = *reinterpret_cast<const uint32_t*>(&pr);
-    }
-    uint4* row = reinterpret_cast<uint4*>(ptile + t * 128);
-    row[(2 * c) ^ (t & 7)] = make_uint4(h[0], h[1], h[2], h[3]);
-    row[(2 * c + 1) ^ (t & 7)] = make_uint4(h[4], h[5], h[6], h[7]);
+      for (int i = 0; i < 16; ++i) x[i] += pw[i];
+    });
   }
 }
 
 // Writes the rows' output, or the part of it, from O^T.
-template <int NC, int D>
+template <int D>
 __device__ __forceinline__ void write_rows(const TreeParams& p, const TreeSplit& sp, const Walk& it, const ItemRows& ir,
-                                           Rows& rw, int id, int wg, int warp, int lane, uint32_t tO, float vref,
-                                           const float (&l)[kHalfRows]) {
+                                           Rows& rw, int id, int wg, int warp, int lane, int nc, uint32_t tO, float vref,
+                                           Sums& l) {
+  const int row0 = wg * ir.half, t = 32 * warp + lane;
+#pragma unroll 1
+  for (int c = 0; c < nc; ++c) {
+    float x[16];
+    l.chunk(c, [&](float (&y)[16]) {
 #pragma unroll
-  for (int i = 0; i < 16 * NC; ++i) {
-    float s = l[i];
+      for (int i = 0; i < 16; ++i) x[i] = y[i];
+    });
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) rw.part[warp][i] = s;
+    for (int i = 0; i < 16; ++i) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
+      if (lane == 0) rw.part[warp][16 * c + i] = x[i];
+    }
   }
   group_sync(id);
-  const int row0 = wg * ir.half, t = 32 * warp + lane;
   const bool whole = it.begins() && it.ends();
   const int64_t prow = int64_t(2 * blockIdx.x + (it.begins() ? 1 : 0)) * sp.rows + row0;
-  if (t < 16 * NC) {
+  if (t < 16 * nc) {
     const float sum = (rw.part[0][t] + rw.part[1][t]) + (rw.part[2][t] + rw.part[3][t]);
     rw.alpha_o[t] = whole ? (sum != 0.f ? vref / sum : 0.f) : vref;
     if (!whole && row0 + t < ir.rows) sp.ml[prow + t] = make_float2(rw.m[t], sum);
   }
   group_sync(id);
-  const int d = 32 * warp + lane;
   const int64_t tok0 = it.q.e.q0 + it.pair * sp.item_nodes;
 #pragma unroll 1
-  for (int c = 0; c < NC; ++c) {
+  for (int c = 0; c < nc; ++c) {
     uint32_t w[16];
+    float a[16];
     ld16(tO + 16 * c, w);
-    if (d < D) {  // (64 columns: the upper lanes repeat them)
-#pragma unroll 1
-      for (int i = 0; i < 16; ++i) {
-        const int r = row0 + 16 * c + i;
-        if (r >= ir.rows) break;
-        float v = 0.f;  // w[i], i not a constant
+    if (t >= D) continue;  // (64 columns: the upper lanes repeat them)
+    lds16(rw.alpha_o + 16 * c, a);
+    const int r0 = row0 + 16 * c, n = min(16, ir.rows - r0);
+    int node = r0 / p.group, h = r0 - node * p.group;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v = k == i ? __uint_as_float(w[k]) : v;
-        v *= rw.alpha_o[16 * c + i];
-        if (whole) {
-          const int node = r / p.group, h = r - node * p.group;
+    for (int i = 0; i < 16; ++i) {
+      if (i < n) {
+        const float v = __uint_as_float(w[i]) * a[i];
+        if (whole)
           static_cast<__nv_bfloat16*>(p.out)[(tok0 + node) * p.out_stride_t +
-                                             int64_t(it.kvh * p.group + h) * p.out_stride_h + d] = __float2bfloat16_rn(v);
-        } else {
-          sp.o[(prow + 16 * c + i) * D + d] = v;
+                                             int64_t(it.kvh * p.group + h) * p.out_stride_h + t] = __float2bfloat16_rn(v);
+        else
+          sp.o[(prow + 16 * c + i) * D + t] = v;
+        if (++h == p.group) {
+          h = 0;
+          ++node;
         }
       }
     }
@@ -376,7 +421,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
   if (warp == 0) tc::alloc(&st->tmem, kTmemCols);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing of the caller's is read before
   asm volatile("griddepcontrol.launch_dependents;");
-  const bool many = find_range<kThreads>(p, sp, &st->range, kFewRows / g);
+  const bool many = find_range<kThreads>(p, sp, &st->range, st->warp_sum, kFewRows / g);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -388,9 +433,11 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
   const int q_rows = many ? kHalfRows : kFewRows, groups = many ? 2 : 1;  // of Q, per warpgroup
   const uint32_t q_half = uint32_t(q_rows) * 128, q_group = q_half * C::kHalves;
   const uint32_t oP = C::kQ + groups * q_group, oCodes = oP + groups * C::kPBytes;
-  const int slots = min(kMaxSlots, int((C::kState - oCodes) / C::kCodeBytes));
+  const int slots = min(kMaxSlots, int((C::kState - oCodes) / C::kCodeBytes));  // (K and V in turn, odd or even)
 
+  // (each role takes its registers itself: the compiler counts them by branch)
   if (warp == 0) {
+    less_registers<kRegsControl>();
     // ---- codes: K then V of every tile, one bulk copy per block of the cache ----------------
     const int bs = p.block_size;
     const uint32_t bytes = uint32_t(bs) * D;
@@ -446,6 +493,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
       for (int k = max(0, n - slots); k < n; ++k)
         (void)mbar_wait_bounded(&st->bars[kCodeFull + k % slots], uint32_t(k / slots) & 1u);
   } else if (warp == 1) {
+    less_registers<kRegsControl>();
     // ---- MMAs (one thread): scores run up to two tiles ahead of the products ----------------
     if (lane == 0) {
       const uint32_t base = smem_addr(smem);
@@ -550,7 +598,10 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
         raise_device_error(p.err, kErrTimeout);
       }
     }
+  } else if (warp == 2) {
+    less_registers<kRegsControl>();
   } else if (warp == 3) {
+    less_registers<kRegsControl>();
     // ---- queries: an item's rows to f16, each scaled by a power of two of its own; and what
     // the fold needs of an item that goes on in the next block's range ------------------------
     constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a pass
@@ -617,31 +668,37 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
     }
     if (lane == 0) sp.tails[blockIdx.x] = tail;
   } else if (warp >= 12) {
-    // ---- widening ---------------------------------------------------------------------------
-    const int t = tid - 384;
-    int slot = 0, n = 0;
+    less_registers<kRegsWiden>();
+    // ---- widening: K by one warpgroup, V by the other, every second tile of the ring each -----
+    const int v = warp >= 16, t = (tid - 384) & 127;
+    constexpr int kPer = D / 16;  // chunks of 16 codes in a row
+    const int row = t / kPer, k = t % kPer, sw = row & 7, c0 = 2 * (k & 3);
+    const bool swap = k >= 4;
+    const uint32_t at0 = uint32_t((c0 + (swap ? 1 : 0)) ^ sw) << 4, at1 = uint32_t((c0 + (swap ? 0 : 1)) ^ sw) << 4;
+    unsigned char* dst = smem + (v ? C::kV : C::kK) + (k >> 2) * C::kHalfBytes + row * 128;
+    const int empty = v ? kVEmpty : kKEmpty, full = v ? kVFull : kKFull;
+    int slot = v, n = 0;
     uint32_t phase = 0;
     for (; it.valid(); it.next(p, sp, rg)) {
       for (int j = it.j0; j < it.j1; ++j, ++n) {
-#pragma unroll 1
-        for (int v = 0; v < 2; ++v) {
-          (void)__all_sync(0xffffffffu, wait(st, kCodeFull + slot, phase));
-          if (n > 0) (void)__all_sync(0xffffffffu, wait(st, v ? kVEmpty : kKEmpty, uint32_t(n - 1) & 1u));
-          widen_tile<D>(smem + oCodes + slot * C::kCodeBytes, smem + (v ? C::kV : C::kK), t);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&st->bars[kCodeEmpty + slot]);
-            mbar_arrive(&st->bars[v ? kVFull : kKFull]);
-          }
-          if (++slot == slots) {
-            slot = 0;
-            phase ^= 1u;
-          }
+        (void)__all_sync(0xffffffffu, wait(st, kCodeFull + slot, phase));
+        if (n > 0) (void)__all_sync(0xffffffffu, wait(st, empty, uint32_t(n - 1) & 1u));
+        widen_tile<D>(smem + oCodes + slot * C::kCodeBytes + t * 16, dst, at0, at1, swap);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&st->bars[kCodeEmpty + slot]);
+          mbar_arrive(&st->bars[full]);
+        }
+        slot += 2;
+        if (slot >= slots) {
+          slot -= slots;
+          phase ^= 1u;
         }
       }
     }
-  } else if (warp >= 4) {
+  } else {
+    more_registers<kRegsSoftmax>();
     // ---- softmax warpgroup `wg`: thread = token of the tile ---------------------------------
     const int wg = (warp >> 2) - 1, q = warp & 3, t = 32 * q + lane;
     const uint32_t lane_off = uint32_t(32 * q) << 16;
@@ -675,17 +732,16 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
     }
     while (it.valid()) {
       const ItemRows ir(p, sp, it);
-      Walk nx = it;
-      nx.next(p, sp, rg);
       if (wg < ir.groups) {
         const Extent& e = it.q.e;
         const int nc = ir.half >> 4, ob = use & 1;
         const uint32_t tO = tmem + C::kO + ob * 128 + wg * 64 + lane_off;
         const float* qf = st->qf[item & 3][wg];
         unsigned char* ptile = smem + oP + wg * C::kPBytes;
-        float vref = 0.f, l[kHalfRows];
+        float vref = 0.f;
+        Sums l;
 #pragma unroll
-        for (int i = 0; i < kHalfRows; ++i) l[i] = 0.f;
+        for (int i = 0; i < kHalfRows; ++i) l.a[i >> 4][i & 15] = 0.f;
         if (t < kHalfRows) {
           rw.m[t] = rw.limit[t] = -INFINITY;
           rw.shift[t] = 0.f;
@@ -727,10 +783,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
           tc::fence_after();
           const uint32_t tS = tmem + C::kS + wg * 128 + (step & 1) * 64 + lane_off;
           const bool first = j == it.j0;
-          if (nc == 1) softmax_step<1>(st, rw, qf, tk, tS, tO, ptile, kODone + wg, step, first, vref, l);
-          else if (nc == 2) softmax_step<2>(st, rw, qf, tk, tS, tO, ptile, kODone + wg, step, first, vref, l);
-          else if (nc == 3) softmax_step<3>(st, rw, qf, tk, tS, tO, ptile, kODone + wg, step, first, vref, l);
-          else softmax_step<4>(st, rw, qf, tk, tS, tO, ptile, kODone + wg, step, first, vref, l);
+          softmax_step(st, rw, qf, tk, nc, tS, tO, ptile, kODone + wg, step, first, vref, l);
           fence_proxy_async_smem();
           tc::fence_before();
           __syncwarp();
@@ -739,25 +792,27 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
           vs = vs1;
         }
         // the next item's first scales are on their way while this one's output is written
+        Walk nx = it;
+        nx.next(p, sp, rg);
         const int e0 = nx.valid() ? entry(nx, nx.j0) : -1;
         if (nx.valid()) e1 = entry(nx, nx.j0 + 1);
         (void)__all_sync(0xffffffffu, wait(st, kODone + wg, uint32_t(step - 1) & 1u));
         tc::fence_after();
         if (nx.valid()) scales(nx, nx.j0, e0, ks, vs);
-        if (nc == 1) write_rows<1, D>(p, sp, it, ir, rw, tk.id, wg, q, lane, tO, vref, l);
-        else if (nc == 2) write_rows<2, D>(p, sp, it, ir, rw, tk.id, wg, q, lane, tO, vref, l);
-        else if (nc == 3) write_rows<3, D>(p, sp, it, ir, rw, tk.id, wg, q, lane, tO, vref, l);
-        else write_rows<4, D>(p, sp, it, ir, rw, tk.id, wg, q, lane, tO, vref, l);
+        write_rows<D>(p, sp, it, ir, rw, tk.id, wg, q, lane, nc, tO, vref, l);
         tc::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&st->bars[kOFree + 2 * wg + ob]);
         group_sync(tk.id);  // (the rows' state is this item's until all have written)
         ++use;
-      } else if (nx.valid()) {
-        scales(nx, nx.j0, entry(nx, nx.j0), ks, vs);
-        e1 = entry(nx, nx.j0 + 1);
+        it = nx;
+      } else {
+        it.next(p, sp, rg);
+        if (it.valid()) {
+          scales(it, it.j0, entry(it, it.j0), ks, vs);
+          e1 = entry(it, it.j0 + 1);
+        }
       }
-      it = nx;
       ++item;
     }
     if (lane == 0 && st->abort) raise_device_error(p.err, kErrTimeout);
@@ -811,6 +866,7 @@ cudaError_t launch_tree_i8_tpl(const TreeParams& p, const TreeSplit& sp, cudaStr
 bool tree_i8_supported(const TreeParams& p) {
   if (p.q_dtype != kBF16 || p.kv_dtype != kI8) return false;
   if (p.group > tree::kBM) return false;
+  if (!(p.qk_scale_log2 > 0.f)) return false;  // (limits are divided by the row's factor)
   if ((reinterpret_cast<uintptr_t>(p.query) & 15) || (p.q_stride_t & 7) || (p.q_stride_h & 7)) return false;
   return true;
 }

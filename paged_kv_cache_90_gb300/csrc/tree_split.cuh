@@ -81,7 +81,6 @@ struct Range {
   int cost;                  // units of an item beside its tiles
   int64_t first_off;         // the range's start in that sequence's work
   int64_t share, from, count;  // units of a block's range, where this one starts, what it holds
-  longlong2 warp_sum[16];
   SeqWork seqs[kSeqs];       // first_seq, first_seq + 1, ...
 };
 
@@ -146,9 +145,11 @@ struct Walk {
 };
 
 // Finds the block's range; all threads call it, and it ends with a barrier.  Returns whether
-// some sequence of the batch has more than `few` nodes.
+// some sequence of the batch has more than `few` nodes.  `warp_sum`: shared scratch, one entry
+// per warp.
 template <int kThreads>
-__device__ __forceinline__ bool find_range(const TreeParams& p, const TreeSplit& sp, Range* rg, int few) {
+__device__ __forceinline__ bool find_range(const TreeParams& p, const TreeSplit& sp, Range* rg, longlong2* warp_sum,
+                                           int few) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // every thread adds up a run of sequences, then the one whose run holds the range's start
   // finds the sequence
@@ -174,12 +175,12 @@ __device__ __forceinline__ bool find_range(const TreeParams& p, const TreeSplit&
       incl.y += y;
     }
   }
-  if (lane == 31) rg->warp_sum[warp] = incl;
+  if (lane == 31) warp_sum[warp] = incl;
   many = __syncthreads_or(many);
   longlong2 before = make_longlong2(incl.x - sum.x, incl.y - sum.y), all = make_longlong2(0, 0);
   const int warps = (p.num_seqs + 32 * per - 1) / (32 * per);  // that hold sequences
   for (int w = 0; w < warps; ++w) {
-    const longlong2 x = rg->warp_sum[w];
+    const longlong2 x = warp_sum[w];
     if (w < warp) {
       before.x += x.x;
       before.y += x.y;

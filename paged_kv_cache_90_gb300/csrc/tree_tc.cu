@@ -89,6 +89,7 @@ struct State {
   volatile int abort;
   uint32_t tmem;
   Range range;
+  longlong2 warp_sum[kThreads / 32];
   // drafted positions with an infinity or a NaN in V, 32 to a word from the first tile
   // that holds drafted nodes on (1024 nodes touch at most 9 tiles), per item (index mod
   // kBadItems)
@@ -218,7 +219,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
   asm volatile("griddepcontrol.launch_dependents;");
 
   // (nq: query slots, two where some sequence of the batch has a second row tile)
-  const int nq = find_range<kThreads>(p, sp, &st->range, sp.tq) ? 2 : 1;
+  const int nq = find_range<kThreads>(p, sp, &st->range, st->warp_sum, sp.tq) ? 2 : 1;
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
