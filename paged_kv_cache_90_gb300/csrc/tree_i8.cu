@@ -27,8 +27,8 @@
 // in flight; shared memory (codes in and out, operands in, and read by two MMAs: 176 KB per
 // 32 KB tile at D = 128) is close behind.
 //
-// Warps: 0 streams codes, K and V tiles in turn (bulk copies of one (block, head) run each); 1
-// issues the MMAs; 3 the queries; 4-7 and 8-11 are the softmax warpgroups; 12-15 widen K, 16-19 V.  Every
+// Warps: 0 streams codes, K and V tiles in turn (bulk copies of one (block, head) run each), and
+// scales; 1 issues the score MMAs, 2 the products'; 3 the queries; 4-7 and 8-11 are the softmax warpgroups; 12-15 widen K, 16-19 V.  Every
 // wait is bounded; when one runs out the block sets an error bit and a flag, every role runs
 // through its loops without waiting, lets its copies and MMAs land and frees the tensor memory.
 #include <cuda_fp16.h>
@@ -56,24 +56,32 @@ constexpr int kHalfRows = 64;  // rows of a warpgroup at most
 
 template <int D>
 struct Cfg {
-  static constexpr int kHalves = D / 64;
-  static constexpr uint32_t kHalfBytes = kBN * 128;  // one 64-column half of an operand tile
-  static constexpr uint32_t kOpBytes = kHalves * kHalfBytes;
+  // Widened operands go in units of 16 KB, two buffers for K and two for V, so that one is
+  // filled while the MMAs read the other.  At D = 128 a tile is two units: of K, 64 columns of
+  // the 128 tokens (half of the MMA's K); of V, 64 tokens with both halves of their columns.
+  // At D = 64 it is one.
+  static constexpr int kUnits = D / 64;
+  static constexpr uint32_t kUnitBytes = kBN * 128;
+  static constexpr int kVTokens = kBN / kUnits;             // of a unit of V
+  static constexpr uint32_t kVHalf = kVTokens * 128;        // pitch of its 64-column halves
   static constexpr uint32_t kCodeBytes = kBN * D;
   static constexpr uint32_t kPBytes = kBN * 128;
-  // from the 1024-aligned base: widened K | widened V | Q | P | ring of code tiles | state.  A
+  // from the 1024-aligned base: K units | V units | Q | P | ring of code tiles | state.  A
   // batch of few rows needs one P and 16 rows of Q, and the ring has the rest.
-  static constexpr uint32_t kK = 0, kV = kOpBytes, kQ = 2 * kOpBytes;
+  static constexpr uint32_t kK = 0, kV = 2 * kUnitBytes, kQ = 4 * kUnitBytes;
   static constexpr uint32_t kState = 212 * 1024;
-  static constexpr uint32_t kStateBytes = 10 * 1024;
+  static constexpr uint32_t kStateBytes = 14 * 1024;
   static constexpr size_t kSmem = kState + kStateBytes + 1024;  // (+ alignment)
   // tensor memory: S^T [warpgroup][2], then O^T [2][warpgroup], 64 columns each
   static constexpr uint32_t kS = 0, kO = 256;
 };
 
-enum Bar { kQFull = 0, kQEmpty, kCodeFull, kCodeEmpty = kCodeFull + kMaxSlots, kKFull = kCodeEmpty + kMaxSlots, kKEmpty,
-           kVFull, kVEmpty, kSFull, kPFull = kSFull + 4, kODone = kPFull + 2, kOFree = kODone + 2, kDrain = kOFree + 4,
-           kNumBars };
+constexpr int kScaleSlots = 8;  // tiles whose scales are in shared memory
+
+enum Bar { kQFull = 0, kQEmpty, kCodeFull, kCodeEmpty = kCodeFull + kMaxSlots, kKFull = kCodeEmpty + kMaxSlots,
+           kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kScaleFull = kVEmpty + 2,
+           kScaleEmpty = kScaleFull + kScaleSlots, kSFull = kScaleEmpty + kScaleSlots, kSFree = kSFull + 4,
+           kPFull = kSFree + 4, kODone = kPFull + 2, kOFree = kODone + 2, kDrain = kOFree + 4, kNumBars = kDrain + 2 };
 
 // What a warpgroup keeps of its rows.
 struct Rows {
@@ -82,7 +90,6 @@ struct Rows {
   float shift[kHalfRows];    // m, or 0 where it is -infinity
   float alpha_l[kHalfRows];  // the last move's factors on the sums and on the output
   float alpha_o[kHalfRows];
-  float part[4][kHalfRows];  // per warp: maxima on the way, sums at the end
   float vpart[4];
 };
 
@@ -95,6 +102,7 @@ struct State {
   float qf[4][2][kHalfRows];  // a row's score factor, per item (index mod 4: a warpgroup may be
                               // two items behind the queries)
   Rows rows[2];
+  float scales[kScaleSlots][2][kBN];  // of K and of V
 };
 
 // A wait that runs out tells the others and is not one for the loops to stop at: a role
@@ -129,23 +137,27 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
 }
 
-// A tile of codes [128][D] -> f16 operand tile (128-byte rows of 64 columns, swizzled), by
-// the 128 threads of a widening warpgroup.  `src` and `dst` are the thread's first chunk of 16
-// codes and its row: the next one is 2048 / D rows, a multiple of 8, further (so the swizzle
-// stays).
-template <int D>
-__device__ __forceinline__ void widen_tile(const unsigned char* src, unsigned char* dst, uint32_t at0, uint32_t at1,
+// 512 chunks of 16 codes -> one unit of an operand (128-byte rows of 64 columns, swizzled), four
+// to each thread of a widening warpgroup: `src` and `dst` are those of its first chunk, the next
+// ones follow at the given pitches (`dst`'s is a multiple of 8 rows, so the swizzle stays).
+template <uint32_t kSrcPitch, uint32_t kDstPitch>
+__device__ __forceinline__ void widen_unit(const unsigned char* src, unsigned char* dst, uint32_t at0, uint32_t at1,
                                            bool swap) {
-  constexpr int kChunks = kBN * D / 16 / 128, kRows = 128 * 16 / D;
-#pragma unroll 2
-  for (int i = 0; i < kChunks; ++i) {
-    const uint4 c = *reinterpret_cast<const uint4*>(src + i * 2048);
-    const uint2 a = widen4(c.x), b = widen4(c.y), e = widen4(c.z), f = widen4(c.w);
+  uint4 c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const uint4*>(src + i * kSrcPitch);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint2 a = widen4(c[i].x), b = widen4(c[i].y), e = widen4(c[i].z), f = widen4(c[i].w);
     const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(e.x, e.y, f.x, f.y);
-    // (the upper half's chunks go in the other order: no two lanes on one bank)
-    *reinterpret_cast<uint4*>(dst + i * kRows * 128 + at0) = swap ? hi : lo;
-    *reinterpret_cast<uint4*>(dst + i * kRows * 128 + at1) = swap ? lo : hi;
+    *reinterpret_cast<uint4*>(dst + i * kDstPitch + at0) = swap ? hi : lo;
+    *reinterpret_cast<uint4*>(dst + i * kDstPitch + at1) = swap ? lo : hi;
   }
+}
+
+// Asynchronous copy of one float, or of a zero.
+__device__ __forceinline__ void copy4(float* dst, const float* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 4 : 0) : "memory");
 }
 
 template <int N>
@@ -237,6 +249,27 @@ __device__ __forceinline__ void weights(uint32_t ts, const float* qf, const floa
   row[(2 * c + 1) ^ sw] = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
+// Reduces 16 rows of 128 tokens through shared memory: every thread has its token's 16
+// values `x`, thread t returns the result of row t / 8 (eight threads share it).  `buf` is
+// 8 KB, free when the warpgroup calls; two calls in a row take different ones.
+template <bool kMax>
+__device__ __forceinline__ float reduce_rows(int id, int t, const float (&x)[16], float* buf) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) buf[i * kBN + t] = x[i];
+  group_sync(id);
+  float y[16];
+  lds16(buf + 16 * t, y);
+  float r = y[0];
+#pragma unroll
+  for (int i = 1; i < 16; ++i) r = kMax ? fmaxf(r, y[i]) : r + y[i];
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    const float z = __shfl_xor_sync(0xffffffffu, r, o);
+    r = kMax ? fmaxf(r, z) : r + z;
+  }
+  return r;
+}
+
 // One key tile for the nc x 16 rows of a warpgroup.  `vref`: the power of two that value
 // scales are taken relative to (0 at first).
 __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* qf, const Token& tk, int nc, uint32_t tS,
@@ -252,58 +285,63 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
     float lim[16];
     ld16(tS + 16 * c, w);
     lds16(rw.limit + 16 * c, lim);
-    uint32_t over = 0;
+    const uint32_t kp = uint32_t(tk.keep >> (16 * c));
+    float over = -INFINITY;  // (fmaxf passes a NaN by)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) over |= __uint_as_float(w[i]) * tk.ks > lim[i] ? 1u << i : 0u;
-    if (tk.cut) over &= uint32_t(tk.keep >> (16 * c));
-    move |= (over & 0xffffu) != 0u;
-  }
-  if (group_any(tk.id, move)) {
-    // the tile's maxima, row by row, and the new references
-#pragma unroll 1
-    for (int c = 0; c < nc; ++c) {
-      uint32_t w[16];
-      float f[16];
-      ld16(tS + 16 * c, w);
-      lds16(qf + 16 * c, f);
-      const uint32_t kp = uint32_t(tk.keep >> (16 * c));
-      float mine = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float z = warp_max(kp >> i & 1u ? __uint_as_float(w[i]) * tk.ks * f[i] : -INFINITY);
-        if (tk.lane == i) mine = z;
-      }
-      if (tk.lane < 16) rw.part[tk.warp][16 * c + tk.lane] = mine;
+    for (int i = 0; i < 16; ++i) {
+      float x = fmaf(__uint_as_float(w[i]), tk.ks, -lim[i]);
+      if (tk.cut && !(kp >> i & 1u)) x = -INFINITY;
+      over = fmaxf(over, x);
     }
+    move |= over > 0.f;
+  }
+  const bool any = group_any(tk.id, move);
+  // (P's last product has to be done before its tile is written again, and O^T with it)
+  if (step > 0) (void)__all_sync(0xffffffffu, wait(st, done_bar, uint32_t(step - 1) & 1u));
+  if (any) {
+    // the tile's maxima, row by row, and the new references
     const float wv = warp_max(tk.valid && av < INFINITY ? av : 0.f);
     if (tk.lane == 0) rw.vpart[tk.warp] = wv;
-    group_sync(tk.id);
-    const float top = fmaxf(fmaxf(rw.vpart[0], rw.vpart[1]), fmaxf(rw.vpart[2], rw.vpart[3]));
     float valpha = 1.f;
-    if (top > 16.f * vref) {
-      // the power of two at or above it (subnormal ones: the smallest normal)
-      const uint32_t b = __float_as_uint(fmaxf(top, 0x1p-126f));
-      const float up = __uint_as_float((b & 0x7f800000u) + ((b & 0x7fffffu) ? 0x800000u : 0u));
-      const float ref = fminf(up, 0x1p127f);
-      valpha = vref / ref;  // (both powers of two, or 0)
-      vref = ref;
-    }
-    if (t < 16 * nc) {
-      const float mx = fmaxf(fmaxf(rw.part[0][t], rw.part[1][t]), fmaxf(rw.part[2][t], rw.part[3][t]));
-      const float m = rw.m[t];
-      const bool go = mx > m + kGap || (m == -INFINITY && mx > -INFINITY);
-      const float m2 = go ? mx : m;
-      const float a = go ? fast_exp2(m - m2) : 1.f;  // (0 from -infinity)
-      rw.m[t] = m2;
-      rw.limit[t] = (m2 + kGap) / qf[t];  // (a row's factor is above zero)
-      rw.shift[t] = m2 == -INFINITY ? 0.f : m2;
-      rw.alpha_l[t] = a;
-      rw.alpha_o[t] = a * valpha;
+#pragma unroll 1
+    for (int c = 0; c < nc; ++c) {
+      float x[16];
+      {
+        uint32_t w[16];
+        float f[16];
+        ld16(tS + 16 * c, w);
+        lds16(qf + 16 * c, f);
+        const uint32_t kp = uint32_t(tk.keep >> (16 * c));
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = kp >> i & 1u ? __uint_as_float(w[i]) * tk.ks * f[i] : -INFINITY;
+      }
+      const float mx = reduce_rows<true>(tk.id, t, x, reinterpret_cast<float*>(ptile) + (c & 1) * 16 * kBN);
+      if (c == 0) {  // (vpart is complete behind the barrier in there)
+        const float top = fmaxf(fmaxf(rw.vpart[0], rw.vpart[1]), fmaxf(rw.vpart[2], rw.vpart[3]));
+        if (top > 16.f * vref) {
+          // the power of two at or above it (subnormal ones: the smallest normal)
+          const uint32_t b = __float_as_uint(fmaxf(top, 0x1p-126f));
+          const float up = __uint_as_float((b & 0x7f800000u) + ((b & 0x7fffffu) ? 0x800000u : 0u));
+          const float ref = fminf(up, 0x1p127f);
+          valpha = vref / ref;  // (both powers of two, or 0)
+          vref = ref;
+        }
+      }
+      if ((t & 7) == 0) {
+        const int r = 16 * c + (t >> 3);
+        const float m = rw.m[r];
+        const bool go = mx > m + kGap || (m == -INFINITY && mx > -INFINITY);
+        const float m2 = go ? mx : m;
+        const float a = go ? fast_exp2(m - m2) : 1.f;  // (0 from -infinity)
+        rw.m[r] = m2;
+        rw.limit[r] = (m2 + kGap) / qf[r];  // (a row's factor is above zero)
+        rw.shift[r] = m2 == -INFINITY ? 0.f : m2;
+        rw.alpha_l[r] = a;
+        rw.alpha_o[r] = a * valpha;
+      }
     }
     group_sync(tk.id);
     if (!first) {
-      // O^T holds the tiles before this one
-      (void)__all_sync(0xffffffffu, wait(st, done_bar, uint32_t(step - 1) & 1u));
       tc::fence_after();
 #pragma unroll 1
       for (int c = 0; c < nc; ++c) {
@@ -323,8 +361,7 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
       tc::wait_st();
     }
   }
-  // the weights (P's last product has to be done before its tile is written again)
-  if (step > 0) (void)__all_sync(0xffffffffu, wait(st, done_bar, uint32_t(step - 1) & 1u));
+  // the weights
   const float vn = tk.valid ? tk.vs * (vref > 0.f ? 1.f / vref : 0.f) : 0.f;
   uint4* row = reinterpret_cast<uint4*>(ptile + t * 128);
 #pragma unroll 1
@@ -341,12 +378,18 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
   }
 }
 
-// Writes the rows' output, or the part of it, from O^T.
+// Writes the rows' output, or the part of it, from O^T (lane = column of the head): through
+// shared memory, so that a warp writes whole rows.  `ptile` is free.
 template <int D>
 __device__ __forceinline__ void write_rows(const TreeParams& p, const TreeSplit& sp, const Walk& it, const ItemRows& ir,
                                            Rows& rw, int id, int wg, int warp, int lane, int nc, uint32_t tO, float vref,
-                                           Sums& l) {
+                                           unsigned char* ptile, Sums& l) {
   const int row0 = wg * ir.half, t = 32 * warp + lane;
+  const bool whole = it.begins() && it.ends();
+  const int64_t prow = int64_t(2 * blockIdx.x + (it.begins() ? 1 : 0)) * sp.rows + row0;
+  const int64_t tok0 = it.q.e.q0 + it.pair * sp.item_nodes;
+  float* sums = reinterpret_cast<float*>(ptile);
+  float* vals = sums + 16 * kBN;
 #pragma unroll 1
   for (int c = 0; c < nc; ++c) {
     float x[16];
@@ -354,47 +397,45 @@ __device__ __forceinline__ void write_rows(const TreeParams& p, const TreeSplit&
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] = y[i];
     });
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) x[i] += __shfl_xor_sync(0xffffffffu, x[i], o);
-      if (lane == 0) rw.part[warp][16 * c + i] = x[i];
-    }
-  }
-  group_sync(id);
-  const bool whole = it.begins() && it.ends();
-  const int64_t prow = int64_t(2 * blockIdx.x + (it.begins() ? 1 : 0)) * sp.rows + row0;
-  if (t < 16 * nc) {
-    const float sum = (rw.part[0][t] + rw.part[1][t]) + (rw.part[2][t] + rw.part[3][t]);
-    rw.alpha_o[t] = whole ? (sum != 0.f ? vref / sum : 0.f) : vref;
-    if (!whole && row0 + t < ir.rows) sp.ml[prow + t] = make_float2(rw.m[t], sum);
-  }
-  group_sync(id);
-  const int64_t tok0 = it.q.e.q0 + it.pair * sp.item_nodes;
-#pragma unroll 1
-  for (int c = 0; c < nc; ++c) {
     uint32_t w[16];
-    float a[16];
     ld16(tO + 16 * c, w);
-    if (t >= D) continue;  // (64 columns: the upper lanes repeat them)
-    lds16(rw.alpha_o + 16 * c, a);
-    const int r0 = row0 + 16 * c, n = min(16, ir.rows - r0);
-    int node = r0 / p.group, h = r0 - node * p.group;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if (i < n) {
-        const float v = __uint_as_float(w[i]) * a[i];
-        if (whole)
-          static_cast<__nv_bfloat16*>(p.out)[(tok0 + node) * p.out_stride_t +
-                                             int64_t(it.kvh * p.group + h) * p.out_stride_h + t] = __float2bfloat16_rn(v);
-        else
-          sp.o[(prow + 16 * c + i) * D + t] = v;
-        if (++h == p.group) {
-          h = 0;
-          ++node;
+    for (int i = 0; i < 16; ++i) vals[i * kBN + t] = __uint_as_float(w[i]);
+    const float sum = reduce_rows<false>(id, t, x, sums);
+    if ((t & 7) == 0) {
+      const int r = 16 * c + (t >> 3);
+      rw.alpha_o[r] = whole ? (sum != 0.f ? vref / sum : 0.f) : vref;
+      if (!whole && row0 + r < ir.rows) sp.ml[prow + r] = make_float2(rw.m[r], sum);
+    }
+    group_sync(id);
+    const int n = min(16, ir.rows - row0 - 16 * c);
+    if (D == 128 || lane < 16) {  // (64 columns: the upper lanes of the accumulator repeat them)
+#pragma unroll 1
+      for (int i = warp; i < n; i += 4) {
+        const int r = row0 + 16 * c + i;
+        const float a = rw.alpha_o[16 * c + i];
+        float4 v = reinterpret_cast<const float4*>(vals + i * kBN)[lane];
+        v = make_float4(v.x * a, v.y * a, v.z * a, v.w * a);
+        if (whole) {
+          const int node = r / p.group, h = r - node * p.group;
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (tok0 + node) * p.out_stride_t +
+                               int64_t(it.kvh * p.group + h) * p.out_stride_h + 4 * lane;
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+          if (sp.out_vec) {
+            *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                        *reinterpret_cast<const uint32_t*>(&hi));
+          } else {
+            out[0] = lo.x;
+            out[1] = lo.y;
+            out[2] = hi.x;
+            out[3] = hi.y;
+          }
+        } else {
+          *reinterpret_cast<float4*>(sp.o + (prow + 16 * c + i) * D + 4 * lane) = v;
         }
       }
     }
+    group_sync(id);
   }
 }
 
@@ -411,9 +452,11 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       // one arrival per warp where a warpgroup arrives
-      const bool warps4 = (i >= kCodeEmpty && i < kCodeEmpty + kMaxSlots) || i == kKFull || i == kVFull ||
-                          (i >= kPFull && i < kPFull + 2) || (i >= kOFree && i < kOFree + 4);
-      mbar_init(&st->bars[i], warps4 ? 4 : 1);
+      const bool warps4 = (i >= kCodeEmpty && i < kCodeEmpty + kMaxSlots) || (i >= kKFull && i < kKFull + 2) ||
+                          (i >= kVFull && i < kVFull + 2) || (i >= kPFull && i < kPFull + 2) ||
+                          (i >= kOFree && i < kOFree + 4) || (i >= kSFree && i < kSFree + 4);
+      const bool lanes = i >= kScaleFull && i < kScaleFull + kScaleSlots;  // (each lane's copies)
+      mbar_init(&st->bars[i], lanes ? 32 : warps4 ? 4 : 1);
     }
     st->abort = 0;
     fence_barrier_init();
@@ -431,7 +474,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
   it.start(p, sp, rg);
   // the layout behind the widened tiles
   const int q_rows = many ? kHalfRows : kFewRows, groups = many ? 2 : 1;  // of Q, per warpgroup
-  const uint32_t q_half = uint32_t(q_rows) * 128, q_group = q_half * C::kHalves;
+  const uint32_t q_half = uint32_t(q_rows) * 128, q_group = q_half * C::kUnits;
   const uint32_t oP = C::kQ + groups * q_group, oCodes = oP + groups * C::kPBytes;
   const int slots = min(kMaxSlots, int((C::kState - oCodes) / C::kCodeBytes));  // (K and V in turn, odd or even)
 
@@ -443,163 +486,192 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
     const uint32_t bytes = uint32_t(bs) * D;
     int slot = 0, n = 0;
     uint32_t phase = 0;
-    for (; it.valid(); it.next(p, sp, rg)) {
-      const int32_t* row = p.block_tables + int64_t(it.s) * p.bt_stride;
-      for (int j = it.j0; j < it.j1; ++j) {
+    // tile j of `it` is looked up one tile before its copies are issued, over items too (up to
+    // 64 blocks of two tokens: two to a lane)
+    int j = it.valid() ? it.j0 : 0, kvh = 0, left = 0, nblk = 0, e0 = 0, e1 = 0;
+    int tiles = 0, sslot = 0;  // of the scales' ring
+    uint32_t sphase = 0;
+    bool have = false;
+    while (true) {
+      const int kvh_now = kvh, left_now = left, nblk_now = nblk;
+      int now[2] = {e0, e1};
+      const bool copy = have;
+      have = it.valid();
+      if (have) {
         const int pos = it.q.base + j * kBN;
-        const int nblk = (max(0, min(kBN, it.q.e.L - pos)) + bs - 1) >> sp.bs_shift;
-        // (up to 64 blocks of two tokens: two to a lane)
-        int e[2];
+        kvh = it.kvh;
+        left = max(0, min(kBN, it.q.e.L - pos));
+        nblk = (left + bs - 1) >> sp.bs_shift;
+        const int32_t* row = p.block_tables + int64_t(it.s) * p.bt_stride + (pos >> sp.bs_shift);
+        e0 = lane < nblk ? __ldg(row + lane) : 0;
+        e1 = lane + 32 < nblk ? __ldg(row + lane + 32) : 0;
+        if (++j == it.j1) {
+          it.next(p, sp, rg);
+          j = it.j0;
+        }
+      }
+      if (!copy) {
+        if (!have) break;
+        continue;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        if (now[u] < 0 || int64_t(now[u]) >= p.num_blocks) {
+          raise_device_error(p.err, kErrTableEntry);
+          now[u] = 0;
+        }
+      // the tokens' scales: asynchronous 4-byte copies, four tokens to a lane (their block's
+      // entry is in lane token / bs, the upper 32 blocks of two tokens in the second register)
+      {
+        if (tiles >= kScaleSlots) (void)__all_sync(0xffffffffu, wait(st, kScaleEmpty + sslot, sphase ^ 1u));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int b = (4 * lane + i) >> sp.bs_shift;
+          const int ea = __shfl_sync(0xffffffffu, now[0], b & 31), eb = __shfl_sync(0xffffffffu, now[1], b & 31);
+          const bool there = 4 * lane + i < left_now;
+          const int64_t at = there ? int64_t(b < 32 ? ea : eb) * p.ts_block + int64_t(kvh_now) * p.ts_head +
+                                         ((4 * lane + i) & (bs - 1))
+                                   : 0;
+          copy4(&st->scales[sslot][0][4 * lane + i], p.k_token_scales + at, there);
+          copy4(&st->scales[sslot][1][4 * lane + i], p.v_token_scales + at, there);
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_addr(&st->bars[kScaleFull + sslot]))
+                     : "memory");
+        ++tiles;
+        if (++sslot == kScaleSlots) {
+          sslot = 0;
+          sphase ^= 1u;
+        }
+      }
+#pragma unroll 1
+      for (int v = 0; v < 2; ++v) {
+        bool ok = true;
+        if (lane == 0 && n >= slots) ok = wait(st, kCodeEmpty + slot, phase ^ 1u);
+        ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+        if (!ok) continue;
+        if (lane == 0) mbar_arrive_expect_tx(&st->bars[kCodeFull + slot], uint32_t(nblk_now) * bytes);
+        __syncwarp();
+        const unsigned char* src = static_cast<const unsigned char*>(v ? p.value_cache : p.key_cache);
+        unsigned char* dst = smem + oCodes + slot * C::kCodeBytes;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int b = lane + 32 * u;
-          e[u] = 0;
-          if (b < nblk) {
-            e[u] = __ldg(row + (pos >> sp.bs_shift) + b);
-            if (e[u] < 0 || int64_t(e[u]) >= p.num_blocks) {
-              raise_device_error(p.err, kErrTableEntry);
-              e[u] = 0;
-            }
-          }
+          if (b < nblk_now)
+            bulk_copy_g2s(dst + b * bytes, src + int64_t(now[u]) * p.cs_block + int64_t(kvh_now) * p.cs_head, bytes,
+                          &st->bars[kCodeFull + slot]);
         }
-#pragma unroll 1
-        for (int v = 0; v < 2; ++v) {
-          bool ok = true;
-          if (lane == 0 && n >= slots) ok = wait(st, kCodeEmpty + slot, phase ^ 1u);
-          ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
-          if (ok) {
-            if (lane == 0) mbar_arrive_expect_tx(&st->bars[kCodeFull + slot], uint32_t(nblk) * bytes);
-            __syncwarp();
-            const unsigned char* src = static_cast<const unsigned char*>(v ? p.value_cache : p.key_cache);
-            unsigned char* dst = smem + oCodes + slot * C::kCodeBytes;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int b = lane + 32 * u;
-              if (b < nblk)
-                bulk_copy_g2s(dst + b * bytes, src + int64_t(e[u]) * p.cs_block + int64_t(it.kvh) * p.cs_head, bytes,
-                              &st->bars[kCodeFull + slot]);
-            }
-            ++n;
-            if (++slot == slots) {
-              slot = 0;
-              phase ^= 1u;
-            }
-          }
+        ++n;
+        if (++slot == slots) {
+          slot = 0;
+          phase ^= 1u;
         }
       }
     }
     // the copies in flight land before the block may exit
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (lane == 0)
       for (int k = max(0, n - slots); k < n; ++k)
         (void)mbar_wait_bounded(&st->bars[kCodeFull + k % slots], uint32_t(k / slots) & 1u);
   } else if (warp == 1) {
     less_registers<kRegsControl>();
-    // ---- MMAs (one thread): scores run up to two tiles ahead of the products ----------------
+    // ---- score MMAs (one thread; the products' are another's: each waits only for its own) ----
     if (lane == 0) {
       const uint32_t base = smem_addr(smem);
-      const uint64_t kdesc = tc::desc_sw128(base + C::kK, 16, 1024);
-      // (a head of 64 columns has one chunk of them: the second 64 rows of the MMA repeat it)
-      const uint64_t vdesc = tc::desc_sw128(base + C::kV, D == 128 ? C::kHalfBytes : 0, 1024);
-      const uint64_t qdesc = tc::desc_sw128(base + C::kQ, 16, 1024), pdesc = tc::desc_sw128(base + oP, 16, 1024);
-      struct Pending {
-        int half;
-        bool two, first;
-        uint8_t ob, of;  // O^T buffers of the two groups (bits), and whether they are waited for and the phases
-        uint8_t wait;
-      };
-      Pending pend[2];
-      int ts = 0, tp = 0;            // tiles whose scores, and products, have been issued
-      int done = 0;                  // groups of tile tp whose product has been issued
-      int j = it.j0, item = 0;
-      int use[2] = {0, 0};           // items of the warpgroups so far (constant indices: registers)
-      int sn0 = 0, sn1 = 0, pn0 = 0, pn1 = 0;  // their steps
-      uint32_t idle = 0;
+      constexpr uint64_t kUnit = C::kUnitBytes >> 4;  // (descriptors hold addresses / 16)
+      const uint64_t kdesc = tc::desc_sw128(base + C::kK, 16, 1024), qdesc = tc::desc_sw128(base + C::kQ, 16, 1024);
+      int kn = 0, item = 0, n0 = 0, n1 = 0;  // units of K, items, steps of the warpgroups
       bool ok = true;
-      while (it.valid() || tp < ts) {
-        bool went = false;
-        if (it.valid() && ts <= tp + 1 && test_wait(&st->bars[kKFull], uint32_t(ts) & 1u) &&
-            (j > it.j0 || test_wait(&st->bars[kQFull], uint32_t(item) & 1u))) {
-          tc::fence_after();
-          const ItemRows ir(p, sp, it);
-          const uint32_t id = idesc_f16(kBN, ir.half, 0, 0);
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (w < ir.groups) {
-              const int n = w ? sn1 : sn0;
-              const uint32_t ts_col = tmem + C::kS + w * 128 + (n & 1) * 64;
-              const uint64_t qd = qdesc + (w * q_group >> 4);
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk)
-                tc::mma_ss(ts_col, kdesc + ((kk >> 2) * C::kHalfBytes >> 4) + (kk & 3) * 2,
-                           qd + ((kk >> 2) * q_half >> 4) + (kk & 3) * 2, id, kk > 0 ? 1u : 0u);
-              tc::commit(&st->bars[kSFull + 2 * w + (n & 1)]);
-            }
-          }
-          tc::commit(&st->bars[kKEmpty]);
-          if (j == it.j1 - 1) tc::commit(&st->bars[kQEmpty]);
-          Pending pd;
-          pd.half = ir.half;
-          pd.two = ir.groups == 2;
-          pd.first = j == it.j0;
-          pd.ob = uint8_t((use[0] & 1) | (use[1] & 1) << 1);
-          pd.wait = uint8_t((use[0] >= 2 ? 1 : 0) | (use[1] >= 2 ? 2 : 0));
-          pd.of = uint8_t((((use[0] - 2) >> 1) & 1) | (((use[1] - 2) >> 1) & 1) << 1);
-          if (ts & 1) pend[1] = pd; else pend[0] = pd;
-          ++ts;
-          ++sn0;
-          if (pd.two) ++sn1;
-          if (++j == it.j1) {
-            ++use[0];
-            if (pd.two) ++use[1];
-            ++item;
-            it.next(p, sp, rg);
-            j = it.j0;
-          }
-          went = true;
-        }
-        if (tp < ts) {
-          const Pending pd = (tp & 1) ? pend[1] : pend[0];
-          const int w = done, n = w ? pn1 : pn0, ob = (pd.ob >> w) & 1;
-          if (test_wait(&st->bars[kPFull + w], uint32_t(n) & 1u) && test_wait(&st->bars[kVFull], uint32_t(tp) & 1u) &&
-              (!pd.first || !((pd.wait >> w) & 1) || test_wait(&st->bars[kOFree + 2 * w + ob], (pd.of >> w) & 1u))) {
+      for (; ok && it.valid(); it.next(p, sp, rg), ++item) {
+        const ItemRows ir(p, sp, it);
+        const uint32_t id = idesc_f16(kBN, ir.half, 0, 0);
+        for (int j = it.j0; ok && j < it.j1; ++j) {
+          if (j == it.j0) ok = wait(st, kQFull, uint32_t(item) & 1u);
+          if (n0 >= 2) ok = ok && wait(st, kSFree + (n0 & 1), uint32_t((n0 >> 1) - 1) & 1u);
+          if (ir.groups == 2 && n1 >= 2) ok = ok && wait(st, kSFree + 2 + (n1 & 1), uint32_t((n1 >> 1) - 1) & 1u);
+          const uint32_t t0 = tmem + C::kS + (n0 & 1) * 64, t1 = tmem + C::kS + 128 + (n1 & 1) * 64;
+#pragma unroll 1
+          for (int u = 0; ok && u < C::kUnits; ++u, ++kn) {
+            if (!(ok = wait(st, kKFull + (kn & 1), uint32_t(kn >> 1) & 1u))) break;
             tc::fence_after();
-            const uint32_t id = idesc_f16(128, pd.half, 1, 1);
-            const uint32_t to = tmem + C::kO + ob * 128 + w * 64;
-            const uint64_t pdsc = pdesc + (w * C::kPBytes >> 4);
+            const uint64_t kd = kdesc + (kn & 1) * kUnit, qd = qdesc + ((u * q_half) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kBN / 16; ++kk)
-              tc::mma_ss(to, vdesc + kk * (16 * 128 >> 4), pdsc + kk * (16 * 128 >> 4), id,
-                         (!pd.first || kk > 0) ? 1u : 0u);
-            tc::commit(&st->bars[kODone + w]);
-            if (w) ++pn1; else ++pn0;
-            if (++done == (pd.two ? 2 : 1)) {
-              tc::commit(&st->bars[kVEmpty]);
-              done = 0;
-              ++tp;
+            for (int kk = 0; kk < 4; ++kk) tc::mma_ss(t0, kd + kk * 2, qd + kk * 2, id, (u > 0 || kk > 0) ? 1u : 0u);
+            if (ir.groups == 2) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                tc::mma_ss(t1, kd + kk * 2, qd + (q_group >> 4) + kk * 2, id, (u > 0 || kk > 0) ? 1u : 0u);
             }
-            went = true;
+            tc::commit(&st->bars[kKEmpty + (kn & 1)]);
+          }
+          if (!ok) break;
+          tc::commit(&st->bars[kSFull + (n0 & 1)]);
+          ++n0;
+          if (ir.groups == 2) {
+            tc::commit(&st->bars[kSFull + 2 + (n1 & 1)]);
+            ++n1;
           }
         }
-        if (went) {
-          idle = 0;
-        } else {
-          __nanosleep(20);
-          if ((++idle & 255u) == 0 && (st->abort || idle > kWaitPolls)) {
-            ok = false;
-            break;
-          }
-        }
+        if (ok) tc::commit(&st->bars[kQEmpty]);
       }
       // every MMA issued has completed before the tensor memory is freed
       tc::commit(&st->bars[kDrain]);
       (void)mbar_wait_bounded(&st->bars[kDrain], 0);
-      if (!ok) {
-        st->abort = 1;
-        raise_device_error(p.err, kErrTimeout);
-      }
+      if (!ok) raise_device_error(p.err, kErrTimeout);
     }
   } else if (warp == 2) {
     less_registers<kRegsControl>();
+    // ---- product MMAs (one thread) -------------------------------------------------------------
+    if (lane == 0) {
+      const uint32_t base = smem_addr(smem);
+      constexpr uint64_t kUnit = C::kUnitBytes >> 4;
+      // (a head of 64 columns has one chunk of them: the second 64 rows of the MMA repeat it)
+      const uint64_t vdesc = tc::desc_sw128(base + C::kV, D == 128 ? C::kVHalf : 0, 1024);
+      const uint64_t pdesc = tc::desc_sw128(base + oP, 16, 1024);
+      int vn = 0, tile = 0, n[2] = {0, 0}, use[2] = {0, 0};  // units of V, tiles, the warpgroups' steps and items
+      bool ok = true;
+      for (; ok && it.valid(); it.next(p, sp, rg)) {
+        const ItemRows ir(p, sp, it);
+        const uint32_t id = idesc_f16(128, ir.half, 1, 1);
+        for (int j = it.j0; ok && j < it.j1; ++j, ++tile) {
+          const bool first = j == it.j0;
+#pragma unroll 1
+          for (int u = 0; u < C::kUnits; ++u, ++vn) {
+            const uint64_t vd = vdesc + (vn & 1) * kUnit;
+            const bool last = u == C::kUnits - 1;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              if (w < ir.groups) {
+                const int ob = use[w] & 1;
+                if (u == 0) {
+                  if (first && use[w] >= 2) ok = ok && wait(st, kOFree + 2 * w + ob, uint32_t((use[w] >> 1) - 1) & 1u);
+                  ok = ok && wait(st, kPFull + w, uint32_t(n[w]) & 1u);
+                }
+                if (w == 0) ok = ok && wait(st, kVFull + (vn & 1), uint32_t(vn >> 1) & 1u);
+                if (ok) {
+                  tc::fence_after();
+                  const uint32_t to = tmem + C::kO + ob * 128 + w * 64;
+                  const uint64_t pb = pdesc + ((w * C::kPBytes + u * C::kVTokens * 128) >> 4);
+#pragma unroll
+                  for (int kk = 0; kk < C::kVTokens / 16; ++kk)
+                    tc::mma_ss(to, vd + kk * (16 * 128 >> 4), pb + kk * (16 * 128 >> 4), id,
+                               (!first || u > 0 || kk > 0) ? 1u : 0u);
+                  if (last) tc::commit(&st->bars[kODone + w]);
+                }
+                if (last) ++n[w];
+              }
+            }
+            if (!ok) break;
+            tc::commit(&st->bars[kVEmpty + (vn & 1)]);
+            if (last) tc::commit(&st->bars[kScaleEmpty + tile % kScaleSlots]);  // (P, so the scales, have been used)
+          }
+        }
+        ++use[0];
+        if (ir.groups == 2) ++use[1];
+      }
+      tc::commit(&st->bars[kDrain + 1]);
+      (void)mbar_wait_bounded(&st->bars[kDrain + 1], 0);
+      if (!ok) raise_device_error(p.err, kErrTimeout);
+    }
   } else if (warp == 3) {
     less_registers<kRegsControl>();
     // ---- queries: an item's rows to f16, each scaled by a power of two of its own; and what
@@ -671,24 +743,32 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
     less_registers<kRegsWiden>();
     // ---- widening: K by one warpgroup, V by the other, every second tile of the ring each -----
     const int v = warp >= 16, t = (tid - 384) & 127;
-    constexpr int kPer = D / 16;  // chunks of 16 codes in a row
-    const int row = t / kPer, k = t % kPer, sw = row & 7, c0 = 2 * (k & 3);
-    const bool swap = k >= 4;
+    // the thread's first chunk of 16 codes of a unit: row and column chunk (of K, a row of a unit
+    // is 4 chunks; of V, all of the token's), and where its two halves go in the operand's row
+    const int per = v ? D / 16 : 4, row = t / per, k = t % per, sw = row & 7, c0 = 2 * (k & 3);
+    const bool swap = k >= 4;  // (V's upper columns in the other order: no two lanes on one bank)
     const uint32_t at0 = uint32_t((c0 + (swap ? 1 : 0)) ^ sw) << 4, at1 = uint32_t((c0 + (swap ? 0 : 1)) ^ sw) << 4;
-    unsigned char* dst = smem + (v ? C::kV : C::kK) + (k >> 2) * C::kHalfBytes + row * 128;
+    unsigned char* dst = smem + (v ? C::kV + (k >> 2) * C::kVHalf : C::kK) + row * 128;
+    const unsigned char* src = smem + oCodes + row * D + k * 16;
     const int empty = v ? kVEmpty : kKEmpty, full = v ? kVFull : kKFull;
-    int slot = v, n = 0;
+    int slot = v, n = 0;  // n: units
     uint32_t phase = 0;
     for (; it.valid(); it.next(p, sp, rg)) {
-      for (int j = it.j0; j < it.j1; ++j, ++n) {
+      for (int j = it.j0; j < it.j1; ++j) {
         (void)__all_sync(0xffffffffu, wait(st, kCodeFull + slot, phase));
-        if (n > 0) (void)__all_sync(0xffffffffu, wait(st, empty, uint32_t(n - 1) & 1u));
-        widen_tile<D>(smem + oCodes + slot * C::kCodeBytes + t * 16, dst, at0, at1, swap);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&st->bars[kCodeEmpty + slot]);
-          mbar_arrive(&st->bars[full]);
+        const unsigned char* tile = src + slot * C::kCodeBytes;
+#pragma unroll 1
+        for (int u = 0; u < C::kUnits; ++u, ++n) {
+          if (n > 1) (void)__all_sync(0xffffffffu, wait(st, empty + (n & 1), uint32_t((n >> 1) - 1) & 1u));
+          unsigned char* to = dst + (n & 1) * C::kUnitBytes;
+          if (v) widen_unit<2048, 128 * (2048 / D)>(tile + u * C::kVTokens * D, to, at0, at1, swap);
+          else widen_unit<32 * D, 32 * 128>(tile + u * 64, to, at0, at1, false);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (u == C::kUnits - 1) mbar_arrive(&st->bars[kCodeEmpty + slot]);
+            mbar_arrive(&st->bars[full + (n & 1)]);
+          }
         }
         slot += 2;
         if (slot >= slots) {
@@ -707,29 +787,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
     tk.id = 1 + wg;
     tk.warp = q;
     tk.lane = lane;
-    const int bs = p.block_size;
-    // the token's table entry in tile j of `w` (-1: no position of the sequence), and its scales
-    auto entry = [&](const Walk& w, int j) -> int {
-      const int pos = w.q.base + j * kBN + t;
-      return j < w.j1 && pos < w.q.e.L ? __ldg(p.block_tables + int64_t(w.s) * p.bt_stride + (pos >> sp.bs_shift)) : -1;
-    };
-    auto scales = [&](const Walk& w, int j, int e, float& ks, float& vs) {
-      const int pos = w.q.base + j * kBN + t;
-      ks = vs = 0.f;
-      if (j < w.j1 && pos < w.q.e.L) {
-        const int blk = e < 0 || int64_t(e) >= p.num_blocks ? 0 : e;  // (reported with the copies)
-        const int64_t i = int64_t(blk) * p.ts_block + int64_t(w.kvh) * p.ts_head + (pos & (bs - 1));
-        ks = __ldg(p.k_token_scales + i);
-        vs = __ldg(p.v_token_scales + i);
-      }
-    };
-    int item = 0, use = 0, step = 0;
-    float ks = 0.f, vs = 0.f;
-    int e1 = -1;
-    if (it.valid()) {
-      scales(it, it.j0, entry(it, it.j0), ks, vs);
-      e1 = entry(it, it.j0 + 1);
-    }
+    int item = 0, use = 0, step = 0, tile = 0;  // `step`: tiles of this warpgroup's; `tile`: all
     while (it.valid()) {
       const ItemRows ir(p, sp, it);
       if (wg < ir.groups) {
@@ -748,13 +806,8 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
         }
         group_sync(tk.id);
 #pragma unroll 1
-        for (int j = it.j0; j < it.j1; ++j, ++step) {
-          float ks1, vs1;
-          scales(it, j + 1, e1, ks1, vs1);
-          e1 = entry(it, j + 2);
+        for (int j = it.j0; j < it.j1; ++j, ++step, ++tile) {
           const int pos = it.q.base + j * kBN + t;
-          tk.ks = ks;
-          tk.vs = vs;
           tk.valid = pos >= e.lo && pos < e.L;
           tk.cut = it.cut(j);
           tk.keep = ~0ull;
@@ -781,38 +834,33 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
           }
           (void)__all_sync(0xffffffffu, wait(st, kSFull + 2 * wg + (step & 1), uint32_t(step >> 1) & 1u));
           tc::fence_after();
+          // (this tile's scores are there, so its scales are at most one use of their slot away)
+          const int sl = tile % kScaleSlots;
+          (void)__all_sync(0xffffffffu, wait(st, kScaleFull + sl, uint32_t(tile / kScaleSlots) & 1u));
+          tk.ks = st->scales[sl][0][t];
+          tk.vs = st->scales[sl][1][t];
           const uint32_t tS = tmem + C::kS + wg * 128 + (step & 1) * 64 + lane_off;
           const bool first = j == it.j0;
           softmax_step(st, rw, qf, tk, nc, tS, tO, ptile, kODone + wg, step, first, vref, l);
           fence_proxy_async_smem();
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&st->bars[kPFull + wg]);
-          ks = ks1;
-          vs = vs1;
+          if (lane == 0) {
+            mbar_arrive(&st->bars[kPFull + wg]);
+            mbar_arrive(&st->bars[kSFree + 2 * wg + (step & 1)]);
+          }
         }
-        // the next item's first scales are on their way while this one's output is written
-        Walk nx = it;
-        nx.next(p, sp, rg);
-        const int e0 = nx.valid() ? entry(nx, nx.j0) : -1;
-        if (nx.valid()) e1 = entry(nx, nx.j0 + 1);
         (void)__all_sync(0xffffffffu, wait(st, kODone + wg, uint32_t(step - 1) & 1u));
         tc::fence_after();
-        if (nx.valid()) scales(nx, nx.j0, e0, ks, vs);
-        write_rows<D>(p, sp, it, ir, rw, tk.id, wg, q, lane, nc, tO, vref, l);
+        write_rows<D>(p, sp, it, ir, rw, tk.id, wg, q, lane, nc, tO, vref, ptile, l);
         tc::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&st->bars[kOFree + 2 * wg + ob]);
-        group_sync(tk.id);  // (the rows' state is this item's until all have written)
         ++use;
-        it = nx;
       } else {
-        it.next(p, sp, rg);
-        if (it.valid()) {
-          scales(it, it.j0, entry(it, it.j0), ks, vs);
-          e1 = entry(it, it.j0 + 1);
-        }
+        tile += it.j1 - it.j0;
       }
+      it.next(p, sp, rg);
       ++item;
     }
     if (lane == 0 && st->abort) raise_device_error(p.err, kErrTimeout);
@@ -873,6 +921,7 @@ bool tree_i8_supported(const TreeParams& p) {
 
 cudaError_t launch_tree_i8(const TreeParams& p, TreeSplit sp, cudaStream_t stream) {
   sp.item_nodes = sp.tq;
+  sp.out_vec = (reinterpret_cast<uintptr_t>(p.out) & 7) == 0 && (p.out_stride_t & 3) == 0 && (p.out_stride_h & 3) == 0;
   return p.head_dim == 128 ? launch_tree_i8_tpl<128>(p, sp, stream) : launch_tree_i8_tpl<64>(p, sp, stream);
 }
 
