@@ -66,8 +66,9 @@ struct Cfg {
   static constexpr uint32_t kVHalf = kVTokens * 128;        // pitch of its 64-column halves
   static constexpr uint32_t kCodeBytes = kBN * D;
   static constexpr uint32_t kPBytes = kBN * 128;
-  // from the 1024-aligned base: K units | V units | Q | P | ring of code tiles | state.  A
-  // batch of few rows needs one P and 16 rows of Q, and the ring has the rest.
+  // from the 1024-aligned base: K units | V units | Q | P (two for each warpgroup) | ring of code
+  // tiles | state.  A batch of few rows needs one warpgroup's P and 16 rows of Q, and the ring
+  // has the rest.
   static constexpr uint32_t kK = 0, kV = 2 * kUnitBytes, kQ = 4 * kUnitBytes;
   static constexpr uint32_t kState = 212 * 1024;
   static constexpr uint32_t kStateBytes = 14 * 1024;
@@ -81,7 +82,7 @@ constexpr int kScaleSlots = 8;  // tiles whose scales are in shared memory
 enum Bar { kQFull = 0, kQEmpty, kCodeFull, kCodeEmpty = kCodeFull + kMaxSlots, kKFull = kCodeEmpty + kMaxSlots,
            kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kScaleFull = kVEmpty + 2,
            kScaleEmpty = kScaleFull + kScaleSlots, kSFull = kScaleEmpty + kScaleSlots, kSFree = kSFull + 4,
-           kPFull = kSFree + 4, kODone = kPFull + 2, kOFree = kODone + 2, kDrain = kOFree + 4, kNumBars = kDrain + 2 };
+           kPFull = kSFree + 4, kODone = kPFull + 4, kOFree = kODone + 4, kDrain = kOFree + 4, kNumBars = kDrain + 2 };
 
 // What a warpgroup keeps of its rows.
 struct Rows {
@@ -108,8 +109,7 @@ struct State {
 // A wait that runs out tells the others and is not one for the loops to stop at: a role
 // whose waits fail runs through its loops, so that barriers among warps always meet.
 __device__ __forceinline__ bool wait(State* st, int bar, uint32_t parity) {
-  if (mbar_try_wait(&st->bars[bar], parity)) return true;
-  return !st->abort && tree::wait(&st->bars[bar], parity, &st->abort);
+  return tree::wait(&st->bars[bar], parity, &st->abort);
 }
 
 // The rows of a Walk's item: rows, row halves' size (a multiple of 16) and halves in use.
@@ -140,18 +140,20 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
 // 512 chunks of 16 codes -> one unit of an operand (128-byte rows of 64 columns, swizzled), four
 // to each thread of a widening warpgroup: `src` and `dst` are those of its first chunk, the next
 // ones follow at the given pitches (`dst`'s is a multiple of 8 rows, so the swizzle stays).
-template <uint32_t kSrcPitch, uint32_t kDstPitch>
-__device__ __forceinline__ void widen_unit(const unsigned char* src, unsigned char* dst, uint32_t at0, uint32_t at1,
-                                           bool swap) {
-  uint4 c[4];
+__device__ __forceinline__ void widen_unit(const unsigned char* src, uint32_t src_pitch, unsigned char* dst,
+                                           uint32_t dst_pitch, uint32_t at0, uint32_t at1, bool swap) {
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h, src += 2 * src_pitch, dst += 2 * dst_pitch) {
+    uint4 c[2];
+    c[0] = *reinterpret_cast<const uint4*>(src);
+    c[1] = *reinterpret_cast<const uint4*>(src + src_pitch);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = *reinterpret_cast<const uint4*>(src + i * kSrcPitch);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint2 a = widen4(c[i].x), b = widen4(c[i].y), e = widen4(c[i].z), f = widen4(c[i].w);
-    const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(e.x, e.y, f.x, f.y);
-    *reinterpret_cast<uint4*>(dst + i * kDstPitch + at0) = swap ? hi : lo;
-    *reinterpret_cast<uint4*>(dst + i * kDstPitch + at1) = swap ? lo : hi;
+    for (int i = 0; i < 2; ++i) {
+      const uint2 a = widen4(c[i].x), b = widen4(c[i].y), e = widen4(c[i].z), f = widen4(c[i].w);
+      const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(e.x, e.y, f.x, f.y);
+      *reinterpret_cast<uint4*>(dst + i * dst_pitch + at0) = swap ? hi : lo;
+      *reinterpret_cast<uint4*>(dst + i * dst_pitch + at1) = swap ? lo : hi;
+    }
   }
 }
 
@@ -205,7 +207,7 @@ struct Token {
   int warp, lane;  // of the warpgroup
   float ks, vs;    // the token's scales
   bool valid;      // the token is a position of the row's range
-  bool cut;        // some row may not see it: `keep` says which do
+  bool cut;        // a tile where some row may not see some token: `keep` has this one's rows
   uint64_t keep;
 };
 
@@ -223,9 +225,10 @@ struct Sums {
   }
 };
 
-// Weights of the 16 rows at tensor-memory column `ts`: added to their sums, and times the
-// token's value scale `vn` written as f16 to `row` (the token's row of P, swizzled by `sw`).
-template <bool kCut>
+// Weights of the 16 rows at tensor-memory column `ts`: returned in `pw`, and times the token's
+// value scale `vn` written as f16 to `row` (the token's row of P, swizzled by `sw`).  With
+// kKeep a row that does not see the token has a product of 0 whatever `vn` is.
+template <bool kKeep>
 __device__ __forceinline__ void weights(uint32_t ts, const float* qf, const float* shift, float ks, float vn,
                                         uint32_t keep, float (&pw)[16], uint4* row, int c, int sw) {
   uint32_t w[16], h[8];
@@ -238,15 +241,29 @@ __device__ __forceinline__ void weights(uint32_t ts, const float* qf, const floa
     pw[i] = fast_exp2(fmaf(__uint_as_float(w[i]) * ks, f[i], -sh[i]));
     pw[i + 1] = fast_exp2(fmaf(__uint_as_float(w[i + 1]) * ks, f[i + 1], -sh[i + 1]));
     float a = pw[i] * vn, b = pw[i + 1] * vn;
-    if (kCut) {  // (a position that is not seen has weight 0 whatever its scales are)
-      if (!(keep >> i & 1u)) pw[i] = a = 0.f;
-      if (!(keep >> (i + 1) & 1u)) pw[i + 1] = b = 0.f;
+    if (kKeep) {
+      if (!(keep >> i & 1u)) a = 0.f;
+      if (!(keep >> (i + 1) & 1u)) b = 0.f;
     }
     const __half2 pr = __floats2half2_rn(a, b);
     h[i / 2] = *reinterpret_cast<const uint32_t*>(&pr);
   }
   row[(2 * c) ^ sw] = make_uint4(h[0], h[1], h[2], h[3]);
   row[(2 * c + 1) ^ sw] = make_uint4(h[4], h[5], h[6], h[7]);
+}
+
+// A tile that some row may not see all of: scores times the key scale, -infinity for hidden
+// ones, back to tensor memory (the caller goes on with a key scale of 1).
+__device__ __forceinline__ void hide(uint32_t tS, int nc, float ks, uint64_t keep) {
+#pragma unroll 1
+  for (int c = 0; c < nc; ++c, keep >>= 16) {
+    uint32_t w[16];
+    ld16(tS + 16 * c, w);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = uint32_t(keep) >> i & 1u ? __float_as_uint(__uint_as_float(w[i]) * ks) : 0xff800000u;
+    tc::st16(tS + 16 * c, w);
+  }
+  tc::wait_st();
 }
 
 // Reduces 16 rows of 128 tokens through shared memory: every thread has its token's 16
@@ -275,6 +292,7 @@ __device__ __forceinline__ float reduce_rows(int id, int t, const float (&x)[16]
 __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* qf, const Token& tk, int nc, uint32_t tS,
                                              uint32_t tO, unsigned char* ptile, int done_bar, int step, bool first,
                                              float& vref, Sums& l) {
+  // (`done_bar`: products done, by the step's parity; `ptile`: this step's of the two)
   const int t = 32 * tk.warp + tk.lane;
   // does a score, or the value scale, exceed its reference?
   const float av = fabsf(tk.vs);
@@ -285,19 +303,14 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
     float lim[16];
     ld16(tS + 16 * c, w);
     lds16(rw.limit + 16 * c, lim);
-    const uint32_t kp = uint32_t(tk.keep >> (16 * c));
     float over = -INFINITY;  // (fmaxf passes a NaN by)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float x = fmaf(__uint_as_float(w[i]), tk.ks, -lim[i]);
-      if (tk.cut && !(kp >> i & 1u)) x = -INFINITY;
-      over = fmaxf(over, x);
-    }
+    for (int i = 0; i < 16; ++i) over = fmaxf(over, fmaf(__uint_as_float(w[i]), tk.ks, -lim[i]));
     move |= over > 0.f;
   }
   const bool any = group_any(tk.id, move);
-  // (P's last product has to be done before its tile is written again, and O^T with it)
-  if (step > 0) (void)__all_sync(0xffffffffu, wait(st, done_bar, uint32_t(step - 1) & 1u));
+  // (the product of the step before last has to be done before its P is written again)
+  if (step > 1) (void)__all_sync(0xffffffffu, wait(st, done_bar + (step & 1), uint32_t((step >> 1) - 1) & 1u));
   if (any) {
     // the tile's maxima, row by row, and the new references
     const float wv = warp_max(tk.valid && av < INFINITY ? av : 0.f);
@@ -311,9 +324,8 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
         float f[16];
         ld16(tS + 16 * c, w);
         lds16(qf + 16 * c, f);
-        const uint32_t kp = uint32_t(tk.keep >> (16 * c));
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = kp >> i & 1u ? __uint_as_float(w[i]) * tk.ks * f[i] : -INFINITY;
+        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(w[i]) * tk.ks * f[i];
       }
       const float mx = reduce_rows<true>(tk.id, t, x, reinterpret_cast<float*>(ptile) + (c & 1) * 16 * kBN);
       if (c == 0) {  // (vpart is complete behind the barrier in there)
@@ -342,6 +354,8 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
     }
     group_sync(tk.id);
     if (!first) {
+      // O^T has to hold the tiles before this one
+      (void)__all_sync(0xffffffffu, wait(st, done_bar + ((step - 1) & 1), uint32_t((step - 1) >> 1) & 1u));
       tc::fence_after();
 #pragma unroll 1
       for (int c = 0; c < nc; ++c) {
@@ -363,11 +377,13 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
   }
   // the weights
   const float vn = tk.valid ? tk.vs * (vref > 0.f ? 1.f / vref : 0.f) : 0.f;
+  // (a value scale that is no number, and rows that must not meet it)
+  const bool odd = tk.cut && __any_sync(0xffffffffu, !(fabsf(vn) <= 3.4e38f));
   uint4* row = reinterpret_cast<uint4*>(ptile + t * 128);
 #pragma unroll 1
   for (int c = 0; c < nc; ++c) {
     float pw[16];
-    if (tk.cut)
+    if (odd)
       weights<true>(tS + 16 * c, qf + 16 * c, rw.shift + 16 * c, tk.ks, vn, uint32_t(tk.keep >> (16 * c)), pw, row, c, t & 7);
     else
       weights<false>(tS + 16 * c, qf + 16 * c, rw.shift + 16 * c, tk.ks, vn, 0u, pw, row, c, t & 7);
@@ -453,7 +469,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
     for (int i = 0; i < kNumBars; ++i) {
       // one arrival per warp where a warpgroup arrives
       const bool warps4 = (i >= kCodeEmpty && i < kCodeEmpty + kMaxSlots) || (i >= kKFull && i < kKFull + 2) ||
-                          (i >= kVFull && i < kVFull + 2) || (i >= kPFull && i < kPFull + 2) ||
+                          (i >= kVFull && i < kVFull + 2) || (i >= kPFull && i < kPFull + 4) ||
                           (i >= kOFree && i < kOFree + 4) || (i >= kSFree && i < kSFree + 4);
       const bool lanes = i >= kScaleFull && i < kScaleFull + kScaleSlots;  // (each lane's copies)
       mbar_init(&st->bars[i], lanes ? 32 : warps4 ? 4 : 1);
@@ -475,7 +491,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
   // the layout behind the widened tiles
   const int q_rows = many ? kHalfRows : kFewRows, groups = many ? 2 : 1;  // of Q, per warpgroup
   const uint32_t q_half = uint32_t(q_rows) * 128, q_group = q_half * C::kUnits;
-  const uint32_t oP = C::kQ + groups * q_group, oCodes = oP + groups * C::kPBytes;
+  const uint32_t oP = C::kQ + groups * q_group, oCodes = oP + 2 * groups * C::kPBytes;
   const int slots = min(kMaxSlots, int((C::kState - oCodes) / C::kCodeBytes));  // (K and V in turn, odd or even)
 
   // (each role takes its registers itself: the compiler counts them by branch)
@@ -524,7 +540,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
       // entry is in lane token / bs, the upper 32 blocks of two tokens in the second register)
       {
         if (tiles >= kScaleSlots) (void)__all_sync(0xffffffffu, wait(st, kScaleEmpty + sslot, sphase ^ 1u));
-#pragma unroll
+#pragma unroll 1
         for (int i = 0; i < 4; ++i) {
           const int b = (4 * lane + i) >> sp.bs_shift;
           const int ea = __shfl_sync(0xffffffffu, now[0], b & 31), eb = __shfl_sync(0xffffffffu, now[1], b & 31);
@@ -627,46 +643,45 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
       // (a head of 64 columns has one chunk of them: the second 64 rows of the MMA repeat it)
       const uint64_t vdesc = tc::desc_sw128(base + C::kV, D == 128 ? C::kVHalf : 0, 1024);
       const uint64_t pdesc = tc::desc_sw128(base + oP, 16, 1024);
-      int vn = 0, tile = 0, n[2] = {0, 0}, use[2] = {0, 0};  // units of V, tiles, the warpgroups' steps and items
+      int vn = 0, sslot = 0;  // units of V, the tile's slot of scales
+      int n0 = 0, n1 = 0, use0 = 0, use1 = 0;  // the warpgroups' steps and items
       bool ok = true;
       for (; ok && it.valid(); it.next(p, sp, rg)) {
         const ItemRows ir(p, sp, it);
         const uint32_t id = idesc_f16(128, ir.half, 1, 1);
-        for (int j = it.j0; ok && j < it.j1; ++j, ++tile) {
-          const bool first = j == it.j0;
+        // (an O^T buffer is written again when the item before last has been written out)
+        if (use0 >= 2) ok = wait(st, kOFree + (use0 & 1), uint32_t((use0 >> 1) - 1) & 1u);
+        if (ir.groups == 2 && use1 >= 2) ok = ok && wait(st, kOFree + 2 + (use1 & 1), uint32_t((use1 >> 1) - 1) & 1u);
+        for (int j = it.j0; ok && j < it.j1; ++j) {
 #pragma unroll 1
           for (int u = 0; u < C::kUnits; ++u, ++vn) {
             const uint64_t vd = vdesc + (vn & 1) * kUnit;
-            const bool last = u == C::kUnits - 1;
+            const uint32_t acc = j > it.j0 || u > 0;
+            ok = wait(st, kVFull + (vn & 1), uint32_t(vn >> 1) & 1u);
+#pragma unroll 1
+            for (int w = 0; w < ir.groups; ++w) {
+              const int n = w ? n1 : n0;
+              if (u == 0) ok = ok && wait(st, kPFull + 2 * w + (n & 1), uint32_t(n >> 1) & 1u);
+              if (!ok) break;
+              tc::fence_after();
+              const uint32_t to = tmem + C::kO + ((w ? use1 : use0) & 1) * 128 + w * 64;
+              const uint64_t pb = pdesc + (((2 * w + (n & 1)) * C::kPBytes + u * C::kVTokens * 128) >> 4);
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              if (w < ir.groups) {
-                const int ob = use[w] & 1;
-                if (u == 0) {
-                  if (first && use[w] >= 2) ok = ok && wait(st, kOFree + 2 * w + ob, uint32_t((use[w] >> 1) - 1) & 1u);
-                  ok = ok && wait(st, kPFull + w, uint32_t(n[w]) & 1u);
-                }
-                if (w == 0) ok = ok && wait(st, kVFull + (vn & 1), uint32_t(vn >> 1) & 1u);
-                if (ok) {
-                  tc::fence_after();
-                  const uint32_t to = tmem + C::kO + ob * 128 + w * 64;
-                  const uint64_t pb = pdesc + ((w * C::kPBytes + u * C::kVTokens * 128) >> 4);
-#pragma unroll
-                  for (int kk = 0; kk < C::kVTokens / 16; ++kk)
-                    tc::mma_ss(to, vd + kk * (16 * 128 >> 4), pb + kk * (16 * 128 >> 4), id,
-                               (!first || u > 0 || kk > 0) ? 1u : 0u);
-                  if (last) tc::commit(&st->bars[kODone + w]);
-                }
-                if (last) ++n[w];
-              }
+              for (int kk = 0; kk < C::kVTokens / 16; ++kk)
+                tc::mma_ss(to, vd + kk * (16 * 128 >> 4), pb + kk * (16 * 128 >> 4), id, acc | (kk > 0));
+              if (u == C::kUnits - 1) tc::commit(&st->bars[kODone + 2 * w + (n & 1)]);
             }
             if (!ok) break;
             tc::commit(&st->bars[kVEmpty + (vn & 1)]);
-            if (last) tc::commit(&st->bars[kScaleEmpty + tile % kScaleSlots]);  // (P, so the scales, have been used)
           }
+          if (!ok) break;
+          tc::commit(&st->bars[kScaleEmpty + sslot]);  // (P, so the scales, have been used)
+          if (++sslot == kScaleSlots) sslot = 0;
+          ++n0;
+          if (ir.groups == 2) ++n1;
         }
-        ++use[0];
-        if (ir.groups == 2) ++use[1];
+        ++use0;
+        if (ir.groups == 2) ++use1;
       }
       tc::commit(&st->bars[kDrain + 1]);
       (void)mbar_wait_bounded(&st->bars[kDrain + 1], 0);
@@ -747,22 +762,30 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
     // is 4 chunks; of V, all of the token's), and where its two halves go in the operand's row
     const int per = v ? D / 16 : 4, row = t / per, k = t % per, sw = row & 7, c0 = 2 * (k & 3);
     const bool swap = k >= 4;  // (V's upper columns in the other order: no two lanes on one bank)
+    const uint32_t unit_pitch = v ? C::kVTokens * D : 64;  // in the codes
+    const uint32_t src_pitch = v ? 2048 : 32 * D, dst_pitch = v ? 128 * (2048 / D) : 32 * 128;
     const uint32_t at0 = uint32_t((c0 + (swap ? 1 : 0)) ^ sw) << 4, at1 = uint32_t((c0 + (swap ? 0 : 1)) ^ sw) << 4;
     unsigned char* dst = smem + (v ? C::kV + (k >> 2) * C::kVHalf : C::kK) + row * 128;
     const unsigned char* src = smem + oCodes + row * D + k * 16;
     const int empty = v ? kVEmpty : kKEmpty, full = v ? kVFull : kKFull;
-    int slot = v, n = 0;  // n: units
-    uint32_t phase = 0;
+    int slot = v, sslot = 0, n = 0;  // n: units
+    uint32_t phase = 0, sphase = 0;
     for (; it.valid(); it.next(p, sp, rg)) {
       for (int j = it.j0; j < it.j1; ++j) {
         (void)__all_sync(0xffffffffu, wait(st, kCodeFull + slot, phase));
+        if (!v) {
+          (void)__all_sync(0xffffffffu, wait(st, kScaleFull + sslot, sphase));
+          if (++sslot == kScaleSlots) {
+            sslot = 0;
+            sphase ^= 1u;
+          }
+        }
         const unsigned char* tile = src + slot * C::kCodeBytes;
 #pragma unroll 1
         for (int u = 0; u < C::kUnits; ++u, ++n) {
           if (n > 1) (void)__all_sync(0xffffffffu, wait(st, empty + (n & 1), uint32_t((n >> 1) - 1) & 1u));
           unsigned char* to = dst + (n & 1) * C::kUnitBytes;
-          if (v) widen_unit<2048, 128 * (2048 / D)>(tile + u * C::kVTokens * D, to, at0, at1, swap);
-          else widen_unit<32 * D, 32 * 128>(tile + u * 64, to, at0, at1, false);
+          widen_unit(tile + u * unit_pitch, src_pitch, to, dst_pitch, at0, at1, swap);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -795,7 +818,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
         const int nc = ir.half >> 4, ob = use & 1;
         const uint32_t tO = tmem + C::kO + ob * 128 + wg * 64 + lane_off;
         const float* qf = st->qf[item & 3][wg];
-        unsigned char* ptile = smem + oP + wg * C::kPBytes;
+        unsigned char* pbuf = smem + oP + 2 * wg * C::kPBytes;
         float vref = 0.f;
         Sums l;
 #pragma unroll
@@ -834,25 +857,27 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
           }
           (void)__all_sync(0xffffffffu, wait(st, kSFull + 2 * wg + (step & 1), uint32_t(step >> 1) & 1u));
           tc::fence_after();
-          // (this tile's scores are there, so its scales are at most one use of their slot away)
-          const int sl = tile % kScaleSlots;
-          (void)__all_sync(0xffffffffu, wait(st, kScaleFull + sl, uint32_t(tile / kScaleSlots) & 1u));
+          const int sl = tile % kScaleSlots;  // (the tile's scales are there: its K waited for them)
           tk.ks = st->scales[sl][0][t];
           tk.vs = st->scales[sl][1][t];
           const uint32_t tS = tmem + C::kS + wg * 128 + (step & 1) * 64 + lane_off;
+          if (tk.cut) {
+            hide(tS, nc, tk.ks, tk.keep);
+            tk.ks = 1.f;
+          }
           const bool first = j == it.j0;
-          softmax_step(st, rw, qf, tk, nc, tS, tO, ptile, kODone + wg, step, first, vref, l);
+          softmax_step(st, rw, qf, tk, nc, tS, tO, pbuf + (step & 1) * C::kPBytes, kODone + 2 * wg, step, first, vref, l);
           fence_proxy_async_smem();
           tc::fence_before();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&st->bars[kPFull + wg]);
+            mbar_arrive(&st->bars[kPFull + 2 * wg + (step & 1)]);
             mbar_arrive(&st->bars[kSFree + 2 * wg + (step & 1)]);
           }
         }
-        (void)__all_sync(0xffffffffu, wait(st, kODone + wg, uint32_t(step - 1) & 1u));
+        (void)__all_sync(0xffffffffu, wait(st, kODone + 2 * wg + ((step - 1) & 1), uint32_t((step - 1) >> 1) & 1u));
         tc::fence_after();
-        write_rows<D>(p, sp, it, ir, rw, tk.id, wg, q, lane, nc, tO, vref, ptile, l);
+        write_rows<D>(p, sp, it, ir, rw, tk.id, wg, q, lane, nc, tO, vref, pbuf, l);
         tc::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&st->bars[kOFree + 2 * wg + ob]);

@@ -42,14 +42,16 @@ __device__ __forceinline__ bool test_wait(uint64_t* bar, uint32_t parity) {
       : "=r"(done) : "r"(smem_addr(bar)), "r"(parity) : "memory");
   return done != 0;
 }
-// Bounded wait that gives up when another role of the block has (and tells them).
+// Bounded wait that gives up when another role of the block has (and tells them).  (Short: it
+// is inlined wherever a role waits, and the roles' loops share the instruction caches.)
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  for (uint32_t i = 0; i < kWaitPolls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 255u) == 255u && *abort) return false;
-  }
-  *abort = 1;
-  return false;
+  uint32_t polls = 0;
+  bool ok;
+  do {
+    ok = mbar_try_wait(bar, parity);
+  } while (!ok && ++polls < kWaitPolls && !*abort);
+  if (!ok) *abort = 1;
+  return ok;
 }
 
 // A sequence's work in tiles: key tiles x groups of nodes x KV heads.
