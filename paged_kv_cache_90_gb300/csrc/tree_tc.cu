@@ -44,6 +44,7 @@
 #include "decode_mma_launch.cuh"
 #include "tcgen05.cuh"
 #include "tree_split.cuh"
+#include "umma.cuh"
 
 namespace pkv {
 namespace tree_tc {
@@ -103,6 +104,10 @@ __device__ __forceinline__ bool wait(State* st, int bar, uint32_t parity) {
 }
 __device__ __forceinline__ bool wait_warp(State* st, int bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait(st, bar, parity));
+}
+
+__device__ __forceinline__ bool ready(uint64_t* bar, uint32_t parity) {  // one answer for a warp
+  return __all_sync(0xffffffffu, test_wait(bar, parity));
 }
 
 // Bits c0 .. c0 + 31 of a row's mask (its first word loaded beforehand): 1 for positions
@@ -332,9 +337,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       if (uses1) (void)mbar_wait_bounded(&st->bars[kQFull + 1], uint32_t(uses1 - 1) & 1u);
     }
   } else if (warp == 1) {
-    // ---- MMAs (one thread): S runs up to two steps ahead of P V; whichever can go next
+    // ---- MMAs (a warp, see umma.cuh): S runs up to two steps ahead of P V; whichever can go next
     // goes, so that neither a late key tile nor a late softmax holds up the other ----------
-    if (lane == 0) {
+    {
       constexpr uint32_t idS = tc::idesc_bf16(kBM, kBN, 0, 0);
       constexpr uint32_t idO = tc::idesc_bf16(kBM, D, 0, 1);
       constexpr uint64_t kOp = C::kOpBytes >> 4;  // (descriptors hold addresses / 16)
@@ -355,10 +360,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       bool ok = true;
       while (it.valid() || xp < xs) {
         bool went = false;
-        if (it.valid() && xs <= xp + 1 && test_wait(&st->bars[kKFull + ks], kp)) {
+        if (it.valid() && xs <= xp + 1 && ready(&st->bars[kKFull + ks], kp)) {
           const int slot = (oc + qt) & 1, u = slot ? uses1 : uses0, n = slot ? steps1 : steps0;
           const int qs = slot & (nq - 1);  // (with one query slot its uses are those of both O slots)
-          if (j > it.j0 || test_wait(&st->bars[kQFull + qs], uint32_t(nq == 2 ? u : uses0 + uses1) & 1u)) {
+          if (j > it.j0 || ready(&st->bars[kQFull + qs], uint32_t(nq == 2 ? u : uses0 + uses1) & 1u)) {
             tc::fence_after();
             const uint64_t qd = qdesc + qs * kOp, kd = kdesc + ks * kOp;
             const uint32_t ts = tmem + C::kS + (xs & 1) * kBN;
@@ -366,12 +371,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
             for (int kk = 0; kk < D / 16; ++kk) {
               constexpr uint64_t kHalf = C::kHalfBytes >> 4;
               const uint64_t off = (kk >> 2) * kHalf + (kk & 3) * 2;
-              tc::mma_ss(ts, qd + off, kd + off, idS, kk > 0 ? 1u : 0u);
+              umma::mma_ss(ts, qd + off, kd + off, idS, kk > 0 ? 1u : 0u);
             }
-            tc::commit(&st->bars[kSFull + 2 * slot + (n & 1)]);
+            umma::commit(&st->bars[kSFull + 2 * slot + (n & 1)]);
             const bool last_row_tile = qt == it.nt - 1;
-            if (last_row_tile) tc::commit(&st->bars[kKEmpty + ks]);
-            if (j == it.j1 - 1) tc::commit(&st->bars[kQEmpty + qs]);
+            if (last_row_tile) umma::commit(&st->bars[kKEmpty + ks]);
+            if (j == it.j1 - 1) umma::commit(&st->bars[kQEmpty + qs]);
             const Pending pd = {slot != 0, (xs & 1) != 0, ((xs >> 1) & 1) != 0, j == it.j0, last_row_tile,
                                 j == it.j0 && u > 0, ((u - 1) & 1) != 0, vp, uint8_t(vs)};
             if (xs & 1) pend[1] = pd; else pend[0] = pd;
@@ -402,16 +407,16 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         }
         if (xp < xs) {
           const Pending pd = (xp & 1) ? pend[1] : pend[0];
-          if (test_wait(&st->bars[kPFull + pd.x], pd.x_phase) && test_wait(&st->bars[kVFull + pd.v], pd.v_phase) &&
-              (!pd.wait_o || test_wait(&st->bars[kOFree + pd.slot], pd.o_phase))) {
+          if (ready(&st->bars[kPFull + pd.x], pd.x_phase) && ready(&st->bars[kVFull + pd.v], pd.v_phase) &&
+              (!pd.wait_o || ready(&st->bars[kOFree + pd.slot], pd.o_phase))) {
             tc::fence_after();
             const uint64_t vd = vdesc + pd.v * kOp;
             const uint32_t ts = tmem + C::kS + pd.x * kBN, to = tmem + C::kO + pd.slot * D;
 #pragma unroll
             for (int kk = 0; kk < kBN / 16; ++kk)
-              tc::mma_ts(to, ts + 8 * kk, vd + kk * (16 * 128 >> 4), idO, (!pd.first || kk > 0) ? 1u : 0u);
-            tc::commit(&st->bars[kODone + pd.slot]);
-            if (pd.last_tile) tc::commit(&st->bars[kVEmpty + pd.v]);
+              umma::mma_ts(to, ts + 8 * kk, vd + kk * (16 * 128 >> 4), idO, (!pd.first || kk > 0) ? 1u : 0u);
+            umma::commit(&st->bars[kODone + pd.slot]);
+            if (pd.last_tile) umma::commit(&st->bars[kVEmpty + pd.v]);
             ++xp;
             went = true;
           }
@@ -427,11 +432,11 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         }
       }
       // every MMA issued has completed before the tensor memory is freed
-      tc::commit(&st->bars[kDrain]);
+      umma::commit(&st->bars[kDrain]);
       (void)mbar_wait_bounded(&st->bars[kDrain], 0);
       if (!ok) {
         st->abort = 1;
-        raise_device_error(p.err, kErrTimeout);
+        if (lane == 0) raise_device_error(p.err, kErrTimeout);
       }
     }
   } else if (warp == 12) {
