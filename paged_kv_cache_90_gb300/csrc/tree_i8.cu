@@ -38,6 +38,7 @@
 
 #include "tcgen05.cuh"
 #include "tree_split.cuh"
+#include "umma.cuh"
 
 namespace pkv {
 namespace tree_i8 {
@@ -110,6 +111,11 @@ struct State {
 // whose waits fail runs through its loops, so that barriers among warps always meet.
 __device__ __forceinline__ bool wait(State* st, int bar, uint32_t parity) {
   return tree::wait(&st->bars[bar], parity, &st->abort);
+}
+
+// By a whole warp: one answer.
+__device__ __forceinline__ bool wait_warp(State* st, int bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait(st, bar, parity));
 }
 
 // The rows of a Walk's item: rows, row halves' size (a multiple of 16) and halves in use.
@@ -291,7 +297,7 @@ __device__ __forceinline__ float reduce_rows(int id, int t, const float (&x)[16]
 // scales are taken relative to (0 at first).
 __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* qf, const Token& tk, int nc, uint32_t tS,
                                              uint32_t tO, unsigned char* ptile, int done_bar, int step, bool first,
-                                             float& vref, Sums& l) {
+                                             float& vref, float& vinv, Sums& l) {
   // (`done_bar`: products done, by the step's parity; `ptile`: this step's of the two)
   const int t = 32 * tk.warp + tk.lane;
   // does a score, or the value scale, exceed its reference?
@@ -310,7 +316,7 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
   }
   const bool any = group_any(tk.id, move);
   // (the product of the step before last has to be done before its P is written again)
-  if (step > 1) (void)__all_sync(0xffffffffu, wait(st, done_bar + (step & 1), uint32_t((step >> 1) - 1) & 1u));
+  if (step > 1) (void)wait_warp(st, done_bar + (step & 1), uint32_t((step >> 1) - 1) & 1u);
   if (any) {
     // the tile's maxima, row by row, and the new references
     const float wv = warp_max(tk.valid && av < INFINITY ? av : 0.f);
@@ -337,6 +343,7 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
           const float ref = fminf(up, 0x1p127f);
           valpha = vref / ref;  // (both powers of two, or 0)
           vref = ref;
+          vinv = 1.f / ref;
         }
       }
       if ((t & 7) == 0) {
@@ -355,7 +362,7 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
     group_sync(tk.id);
     if (!first) {
       // O^T has to hold the tiles before this one
-      (void)__all_sync(0xffffffffu, wait(st, done_bar + ((step - 1) & 1), uint32_t((step - 1) >> 1) & 1u));
+      (void)wait_warp(st, done_bar + ((step - 1) & 1), uint32_t((step - 1) >> 1) & 1u);
       tc::fence_after();
 #pragma unroll 1
       for (int c = 0; c < nc; ++c) {
@@ -376,7 +383,7 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
     }
   }
   // the weights
-  const float vn = tk.valid ? tk.vs * (vref > 0.f ? 1.f / vref : 0.f) : 0.f;
+  const float vn = tk.valid ? tk.vs * vinv : 0.f;
   // (a value scale that is no number, and rows that must not meet it)
   const bool odd = tk.cut && __any_sync(0xffffffffu, !(fabsf(vn) <= 3.4e38f));
   uint4* row = reinterpret_cast<uint4*>(ptile + t * 128);
@@ -539,7 +546,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
       // the tokens' scales: asynchronous 4-byte copies, four tokens to a lane (their block's
       // entry is in lane token / bs, the upper 32 blocks of two tokens in the second register)
       {
-        if (tiles >= kScaleSlots) (void)__all_sync(0xffffffffu, wait(st, kScaleEmpty + sslot, sphase ^ 1u));
+        if (tiles >= kScaleSlots) (void)wait_warp(st, kScaleEmpty + sslot, sphase ^ 1u);
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
           const int b = (4 * lane + i) >> sp.bs_shift;
@@ -590,8 +597,8 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
         (void)mbar_wait_bounded(&st->bars[kCodeFull + k % slots], uint32_t(k / slots) & 1u);
   } else if (warp == 1) {
     less_registers<kRegsControl>();
-    // ---- score MMAs (one thread; the products' are another's: each waits only for its own) ----
-    if (lane == 0) {
+    // ---- score MMAs (a warp, see umma.cuh; the products' are another's: each waits only for its own) ----
+    {
       const uint32_t base = smem_addr(smem);
       constexpr uint64_t kUnit = C::kUnitBytes >> 4;  // (descriptors hold addresses / 16)
       const uint64_t kdesc = tc::desc_sw128(base + C::kK, 16, 1024), qdesc = tc::desc_sw128(base + C::kQ, 16, 1024);
@@ -601,43 +608,43 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
         const ItemRows ir(p, sp, it);
         const uint32_t id = idesc_f16(kBN, ir.half, 0, 0);
         for (int j = it.j0; ok && j < it.j1; ++j) {
-          if (j == it.j0) ok = wait(st, kQFull, uint32_t(item) & 1u);
-          if (n0 >= 2) ok = ok && wait(st, kSFree + (n0 & 1), uint32_t((n0 >> 1) - 1) & 1u);
-          if (ir.groups == 2 && n1 >= 2) ok = ok && wait(st, kSFree + 2 + (n1 & 1), uint32_t((n1 >> 1) - 1) & 1u);
+          if (j == it.j0) ok = wait_warp(st, kQFull, uint32_t(item) & 1u);
+          if (n0 >= 2) ok = ok && wait_warp(st, kSFree + (n0 & 1), uint32_t((n0 >> 1) - 1) & 1u);
+          if (ir.groups == 2 && n1 >= 2) ok = ok && wait_warp(st, kSFree + 2 + (n1 & 1), uint32_t((n1 >> 1) - 1) & 1u);
           const uint32_t t0 = tmem + C::kS + (n0 & 1) * 64, t1 = tmem + C::kS + 128 + (n1 & 1) * 64;
 #pragma unroll 1
           for (int u = 0; ok && u < C::kUnits; ++u, ++kn) {
-            if (!(ok = wait(st, kKFull + (kn & 1), uint32_t(kn >> 1) & 1u))) break;
+            if (!(ok = wait_warp(st, kKFull + (kn & 1), uint32_t(kn >> 1) & 1u))) break;
             tc::fence_after();
             const uint64_t kd = kdesc + (kn & 1) * kUnit, qd = qdesc + ((u * q_half) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) tc::mma_ss(t0, kd + kk * 2, qd + kk * 2, id, (u > 0 || kk > 0) ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk) umma::mma_ss(t0, kd + kk * 2, qd + kk * 2, id, (u > 0 || kk > 0) ? 1u : 0u);
             if (ir.groups == 2) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                tc::mma_ss(t1, kd + kk * 2, qd + (q_group >> 4) + kk * 2, id, (u > 0 || kk > 0) ? 1u : 0u);
+                umma::mma_ss(t1, kd + kk * 2, qd + (q_group >> 4) + kk * 2, id, (u > 0 || kk > 0) ? 1u : 0u);
             }
-            tc::commit(&st->bars[kKEmpty + (kn & 1)]);
+            umma::commit(&st->bars[kKEmpty + (kn & 1)]);
           }
           if (!ok) break;
-          tc::commit(&st->bars[kSFull + (n0 & 1)]);
+          umma::commit(&st->bars[kSFull + (n0 & 1)]);
           ++n0;
           if (ir.groups == 2) {
-            tc::commit(&st->bars[kSFull + 2 + (n1 & 1)]);
+            umma::commit(&st->bars[kSFull + 2 + (n1 & 1)]);
             ++n1;
           }
         }
-        if (ok) tc::commit(&st->bars[kQEmpty]);
+        if (ok) umma::commit(&st->bars[kQEmpty]);
       }
       // every MMA issued has completed before the tensor memory is freed
-      tc::commit(&st->bars[kDrain]);
+      umma::commit(&st->bars[kDrain]);
       (void)mbar_wait_bounded(&st->bars[kDrain], 0);
-      if (!ok) raise_device_error(p.err, kErrTimeout);
+      if (!ok && lane == 0) raise_device_error(p.err, kErrTimeout);
     }
   } else if (warp == 2) {
     less_registers<kRegsControl>();
-    // ---- product MMAs (one thread) -------------------------------------------------------------
-    if (lane == 0) {
+    // ---- product MMAs (a warp) -------------------------------------------------------------
+    {
       const uint32_t base = smem_addr(smem);
       constexpr uint64_t kUnit = C::kUnitBytes >> 4;
       // (a head of 64 columns has one chunk of them: the second 64 rows of the MMA repeat it)
@@ -650,32 +657,32 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
         const ItemRows ir(p, sp, it);
         const uint32_t id = idesc_f16(128, ir.half, 1, 1);
         // (an O^T buffer is written again when the item before last has been written out)
-        if (use0 >= 2) ok = wait(st, kOFree + (use0 & 1), uint32_t((use0 >> 1) - 1) & 1u);
-        if (ir.groups == 2 && use1 >= 2) ok = ok && wait(st, kOFree + 2 + (use1 & 1), uint32_t((use1 >> 1) - 1) & 1u);
+        if (use0 >= 2) ok = wait_warp(st, kOFree + (use0 & 1), uint32_t((use0 >> 1) - 1) & 1u);
+        if (ir.groups == 2 && use1 >= 2) ok = ok && wait_warp(st, kOFree + 2 + (use1 & 1), uint32_t((use1 >> 1) - 1) & 1u);
         for (int j = it.j0; ok && j < it.j1; ++j) {
 #pragma unroll 1
           for (int u = 0; u < C::kUnits; ++u, ++vn) {
             const uint64_t vd = vdesc + (vn & 1) * kUnit;
             const uint32_t acc = j > it.j0 || u > 0;
-            ok = wait(st, kVFull + (vn & 1), uint32_t(vn >> 1) & 1u);
+            ok = wait_warp(st, kVFull + (vn & 1), uint32_t(vn >> 1) & 1u);
 #pragma unroll 1
             for (int w = 0; w < ir.groups; ++w) {
               const int n = w ? n1 : n0;
-              if (u == 0) ok = ok && wait(st, kPFull + 2 * w + (n & 1), uint32_t(n >> 1) & 1u);
+              if (u == 0) ok = ok && wait_warp(st, kPFull + 2 * w + (n & 1), uint32_t(n >> 1) & 1u);
               if (!ok) break;
               tc::fence_after();
               const uint32_t to = tmem + C::kO + ((w ? use1 : use0) & 1) * 128 + w * 64;
               const uint64_t pb = pdesc + (((2 * w + (n & 1)) * C::kPBytes + u * C::kVTokens * 128) >> 4);
 #pragma unroll
               for (int kk = 0; kk < C::kVTokens / 16; ++kk)
-                tc::mma_ss(to, vd + kk * (16 * 128 >> 4), pb + kk * (16 * 128 >> 4), id, acc | (kk > 0));
-              if (u == C::kUnits - 1) tc::commit(&st->bars[kODone + 2 * w + (n & 1)]);
+                umma::mma_ss(to, vd + kk * (16 * 128 >> 4), pb + kk * (16 * 128 >> 4), id, acc | (kk > 0));
+              if (u == C::kUnits - 1) umma::commit(&st->bars[kODone + 2 * w + (n & 1)]);
             }
             if (!ok) break;
-            tc::commit(&st->bars[kVEmpty + (vn & 1)]);
+            umma::commit(&st->bars[kVEmpty + (vn & 1)]);
           }
           if (!ok) break;
-          tc::commit(&st->bars[kScaleEmpty + sslot]);  // (P, so the scales, have been used)
+          umma::commit(&st->bars[kScaleEmpty + sslot]);  // (P, so the scales, have been used)
           if (++sslot == kScaleSlots) sslot = 0;
           ++n0;
           if (ir.groups == 2) ++n1;
@@ -683,9 +690,9 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
         ++use0;
         if (ir.groups == 2) ++use1;
       }
-      tc::commit(&st->bars[kDrain + 1]);
+      umma::commit(&st->bars[kDrain + 1]);
       (void)mbar_wait_bounded(&st->bars[kDrain + 1], 0);
-      if (!ok) raise_device_error(p.err, kErrTimeout);
+      if (!ok && lane == 0) raise_device_error(p.err, kErrTimeout);
     }
   } else if (warp == 3) {
     less_registers<kRegsControl>();
@@ -700,7 +707,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
       const ItemRows ir(p, sp, it);
       const int node0 = it.pair * sp.item_nodes;
       const int64_t tok0 = it.q.e.q0 + node0;
-      if (item > 0) (void)__all_sync(0xffffffffu, wait(st, kQEmpty, uint32_t(item - 1) & 1u));
+      if (item > 0) (void)wait_warp(st, kQEmpty, uint32_t(item - 1) & 1u);
       constexpr int kBatch = 8;
       for (int r0 = 0; r0 < ir.groups * ir.half; r0 += kBatch * kPer) {
         uint4 x[kBatch];
@@ -772,9 +779,9 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
     uint32_t phase = 0, sphase = 0;
     for (; it.valid(); it.next(p, sp, rg)) {
       for (int j = it.j0; j < it.j1; ++j) {
-        (void)__all_sync(0xffffffffu, wait(st, kCodeFull + slot, phase));
+        (void)wait_warp(st, kCodeFull + slot, phase);
         if (!v) {
-          (void)__all_sync(0xffffffffu, wait(st, kScaleFull + sslot, sphase));
+          (void)wait_warp(st, kScaleFull + sslot, sphase);
           if (++sslot == kScaleSlots) {
             sslot = 0;
             sphase ^= 1u;
@@ -783,7 +790,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
         const unsigned char* tile = src + slot * C::kCodeBytes;
 #pragma unroll 1
         for (int u = 0; u < C::kUnits; ++u, ++n) {
-          if (n > 1) (void)__all_sync(0xffffffffu, wait(st, empty + (n & 1), uint32_t((n >> 1) - 1) & 1u));
+          if (n > 1) (void)wait_warp(st, empty + (n & 1), uint32_t((n >> 1) - 1) & 1u);
           unsigned char* to = dst + (n & 1) * C::kUnitBytes;
           widen_unit(tile + u * unit_pitch, src_pitch, to, dst_pitch, at0, at1, swap);
           fence_proxy_async_smem();
@@ -819,7 +826,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
         const uint32_t tO = tmem + C::kO + ob * 128 + wg * 64 + lane_off;
         const float* qf = st->qf[item & 3][wg];
         unsigned char* pbuf = smem + oP + 2 * wg * C::kPBytes;
-        float vref = 0.f;
+        float vref = 0.f, vinv = 0.f;  // (and its inverse)
         Sums l;
 #pragma unroll
         for (int i = 0; i < kHalfRows; ++i) l.a[i >> 4][i & 15] = 0.f;
@@ -855,7 +862,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
               }
             }
           }
-          (void)__all_sync(0xffffffffu, wait(st, kSFull + 2 * wg + (step & 1), uint32_t(step >> 1) & 1u));
+          (void)wait_warp(st, kSFull + 2 * wg + (step & 1), uint32_t(step >> 1) & 1u);
           tc::fence_after();
           const int sl = tile % kScaleSlots;  // (the tile's scales are there: its K waited for them)
           tk.ks = st->scales[sl][0][t];
@@ -866,7 +873,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
             tk.ks = 1.f;
           }
           const bool first = j == it.j0;
-          softmax_step(st, rw, qf, tk, nc, tS, tO, pbuf + (step & 1) * C::kPBytes, kODone + 2 * wg, step, first, vref, l);
+          softmax_step(st, rw, qf, tk, nc, tS, tO, pbuf + (step & 1) * C::kPBytes, kODone + 2 * wg, step, first, vref, vinv, l);
           fence_proxy_async_smem();
           tc::fence_before();
           __syncwarp();
@@ -875,7 +882,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
             mbar_arrive(&st->bars[kSFree + 2 * wg + (step & 1)]);
           }
         }
-        (void)__all_sync(0xffffffffu, wait(st, kODone + 2 * wg + ((step - 1) & 1), uint32_t((step - 1) >> 1) & 1u));
+        (void)wait_warp(st, kODone + 2 * wg + ((step - 1) & 1), uint32_t((step - 1) >> 1) & 1u);
         tc::fence_after();
         write_rows<D>(p, sp, it, ir, rw, tk.id, wg, q, lane, nc, tO, vref, pbuf, l);
         tc::fence_before();
