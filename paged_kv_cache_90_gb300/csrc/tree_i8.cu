@@ -86,10 +86,10 @@ enum Bar { kQFull = 0, kQEmpty, kCodeFull, kCodeEmpty = kCodeFull + kMaxSlots, k
            kPFull = kSFree + 4, kODone = kPFull + 4, kOFree = kODone + 4, kDrain = kOFree + 4, kNumBars = kDrain + 2 };
 
 // What a warpgroup keeps of its rows.
-struct Rows {
+struct alignas(16) Rows {
   float m[kHalfRows];        // reference maximum (base 2), -infinity before the first score
-  float limit[kHalfRows];    // a score before its row's factor above this moves it
-  float shift[kHalfRows];    // m, or 0 where it is -infinity
+  float drop[kHalfRows];     // a score before its row's factor, plus this, above 0 moves it
+  float lift[kHalfRows];     // -m, or 0 where it is -infinity
   float alpha_l[kHalfRows];  // the last move's factors on the sums and on the output
   float alpha_o[kHalfRows];
   float vpart[4];
@@ -101,10 +101,10 @@ struct State {
   uint32_t tmem;
   Range range;
   longlong2 warp_sum[kThreads / 32];
-  float qf[4][2][kHalfRows];  // a row's score factor, per item (index mod 4: a warpgroup may be
+  alignas(16) float qf[4][2][kHalfRows];  // a row's score factor, per item (index mod 4: a warpgroup may be
                               // two items behind the queries)
   Rows rows[2];
-  float scales[kScaleSlots][2][kBN];  // of K and of V
+  alignas(16) float scales[kScaleSlots][2][kBN];  // of K and of V
 };
 
 // A wait that runs out tells the others and is not one for the loops to stop at: a role
@@ -144,23 +144,46 @@ __device__ __forceinline__ uint2 widen4(uint32_t w) {
 }
 
 // 512 chunks of 16 codes -> one unit of an operand (128-byte rows of 64 columns, swizzled), four
-// to each thread of a widening warpgroup: `src` and `dst` are those of its first chunk, the next
-// ones follow at the given pitches (`dst`'s is a multiple of 8 rows, so the swizzle stays).
-__device__ __forceinline__ void widen_unit(const unsigned char* src, uint32_t src_pitch, unsigned char* dst,
-                                           uint32_t dst_pitch, uint32_t at0, uint32_t at1, bool swap) {
-#pragma unroll 1
-  for (int h = 0; h < 2; ++h, src += 2 * src_pitch, dst += 2 * dst_pitch) {
-    uint4 c[2];
-    c[0] = *reinterpret_cast<const uint4*>(src);
-    c[1] = *reinterpret_cast<const uint4*>(src + src_pitch);
+// to each thread of a widening warpgroup: the first from `src` to bytes `lo` and `hi` of shared
+// memory, the others a, b and a + b further (`da`, `db`: multiples of 8 rows, so the swizzle
+// stays).
+__device__ __forceinline__ void widen_unit(const unsigned char* src, uint32_t a, uint32_t b, unsigned char* lo,
+                                           unsigned char* hi, uint32_t da, uint32_t db) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint2 a = widen4(c[i].x), b = widen4(c[i].y), e = widen4(c[i].z), f = widen4(c[i].w);
-      const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(e.x, e.y, f.x, f.y);
-      *reinterpret_cast<uint4*>(dst + i * dst_pitch + at0) = swap ? hi : lo;
-      *reinterpret_cast<uint4*>(dst + i * dst_pitch + at1) = swap ? lo : hi;
-    }
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t so = (i & 1 ? a : 0) + (i & 2 ? b : 0), to = (i & 1 ? da : 0) + (i & 2 ? db : 0);
+    const uint4 c = *reinterpret_cast<const uint4*>(src + so);
+    const uint2 x = widen4(c.x), y = widen4(c.y), z = widen4(c.z), w = widen4(c.w);
+    *reinterpret_cast<uint4*>(lo + to) = make_uint4(x.x, x.y, y.x, y.y);
+    *reinterpret_cast<uint4*>(hi + to) = make_uint4(z.x, z.y, w.x, w.y);
   }
+}
+
+// Two binary32 numbers in one register pair, and the operations that take both at once.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
 // Asynchronous copy of one float, or of a zero.
@@ -221,7 +244,7 @@ struct Token {
 // (unrolled code misses the instruction cache at every tile): a register array takes constant
 // indices only.
 struct Sums {
-  float a[4][16];
+  uint64_t a[4][8];
   template <typename F>
   __device__ __forceinline__ void chunk(int c, F f) {
     if (c == 0) f(a[0]);
@@ -231,28 +254,35 @@ struct Sums {
   }
 };
 
-// Weights of the 16 rows at tensor-memory column `ts`: returned in `pw`, and times the token's
-// value scale `vn` written as f16 to `row` (the token's row of P, swizzled by `sw`).  With
-// kKeep a row that does not see the token has a product of 0 whatever `vn` is.
+// Weights of the 16 rows at tensor-memory column `ts`, in pairs: returned in `pw`, and times
+// the token's value scale `vn` written as f16 to `row` (the token's row of P, swizzled by `sw`).
+// `lift` holds the references' negatives.  With kKeep a row that does not see the token has a
+// product of 0 whatever `vn` is.
 template <bool kKeep>
-__device__ __forceinline__ void weights(uint32_t ts, const float* qf, const float* shift, float ks, float vn,
-                                        uint32_t keep, float (&pw)[16], uint4* row, int c, int sw) {
+__device__ __forceinline__ void weights(uint32_t ts, const float* qf, const float* lift, float ks, float vn,
+                                        uint32_t keep, uint64_t (&pw)[8], uint4* row, int c, int sw) {
   uint32_t w[16], h[8];
-  float f[16], sh[16];
   ld16(ts, w);
-  lds16(qf, f);
-  lds16(shift, sh);
+  const uint64_t ks2 = pack2(ks, ks), vn2 = pack2(vn, vn);
 #pragma unroll
-  for (int i = 0; i < 16; i += 2) {
-    pw[i] = fast_exp2(fmaf(__uint_as_float(w[i]) * ks, f[i], -sh[i]));
-    pw[i + 1] = fast_exp2(fmaf(__uint_as_float(w[i + 1]) * ks, f[i + 1], -sh[i + 1]));
-    float a = pw[i] * vn, b = pw[i + 1] * vn;
-    if (kKeep) {
-      if (!(keep >> i & 1u)) a = 0.f;
-      if (!(keep >> (i + 1) & 1u)) b = 0.f;
+  for (int i = 0; i < 4; ++i) {
+    const ulonglong2 f = reinterpret_cast<const ulonglong2*>(qf)[i], m = reinterpret_cast<const ulonglong2*>(lift)[i];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int e = 4 * i + 2 * j;
+      const uint64_t z = fma2(mul2(pack2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])), ks2), j ? f.y : f.x,
+                              j ? m.y : m.x);
+      const float2 zz = unpack2(z);
+      const uint64_t p = pack2(fast_exp2(zz.x), fast_exp2(zz.y));
+      pw[2 * i + j] = p;
+      float2 x = unpack2(mul2(p, vn2));
+      if (kKeep) {
+        if (!(keep >> e & 1u)) x.x = 0.f;
+        if (!(keep >> (e + 1) & 1u)) x.y = 0.f;
+      }
+      const __half2 pr = __floats2half2_rn(x.x, x.y);
+      h[2 * i + j] = *reinterpret_cast<const uint32_t*>(&pr);
     }
-    const __half2 pr = __floats2half2_rn(a, b);
-    h[i / 2] = *reinterpret_cast<const uint32_t*>(&pr);
   }
   row[(2 * c) ^ sw] = make_uint4(h[0], h[1], h[2], h[3]);
   row[(2 * c + 1) ^ sw] = make_uint4(h[4], h[5], h[6], h[7]);
@@ -306,12 +336,16 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
 #pragma unroll 1
   for (int c = 0; c < nc; ++c) {
     uint32_t w[16];
-    float lim[16];
     ld16(tS + 16 * c, w);
-    lds16(rw.limit + 16 * c, lim);
+    const uint64_t ks2 = pack2(tk.ks, tk.ks);
     float over = -INFINITY;  // (fmaxf passes a NaN by)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) over = fmaxf(over, fmaf(__uint_as_float(w[i]), tk.ks, -lim[i]));
+    for (int i = 0; i < 4; ++i) {
+      const ulonglong2 d = reinterpret_cast<const ulonglong2*>(rw.drop + 16 * c)[i];
+      const float2 x = unpack2(fma2(pack2(__uint_as_float(w[4 * i]), __uint_as_float(w[4 * i + 1])), ks2, d.x));
+      const float2 y = unpack2(fma2(pack2(__uint_as_float(w[4 * i + 2]), __uint_as_float(w[4 * i + 3])), ks2, d.y));
+      over = fmaxf(over, fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y)));
+    }
     move |= over > 0.f;
   }
   const bool any = group_any(tk.id, move);
@@ -353,8 +387,8 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
         const float m2 = go ? mx : m;
         const float a = go ? fast_exp2(m - m2) : 1.f;  // (0 from -infinity)
         rw.m[r] = m2;
-        rw.limit[r] = (m2 + kGap) / qf[r];  // (a row's factor is above zero)
-        rw.shift[r] = m2 == -INFINITY ? 0.f : m2;
+        rw.drop[r] = -(m2 + kGap) / qf[r];  // (a row's factor is above zero)
+        rw.lift[r] = m2 == -INFINITY ? 0.f : -m2;
         rw.alpha_l[r] = a;
         rw.alpha_o[r] = a * valpha;
       }
@@ -369,9 +403,9 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
         uint32_t w[16];
         float a[16];
         lds16(rw.alpha_l + 16 * c, a);
-        l.chunk(c, [&](float (&x)[16]) {
+        l.chunk(c, [&](uint64_t (&x)[8]) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] *= a[i];
+          for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], pack2(a[2 * i], a[2 * i + 1]));
         });
         ld16(tO + 16 * c, w);
         lds16(rw.alpha_o + 16 * c, a);
@@ -389,14 +423,14 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
   uint4* row = reinterpret_cast<uint4*>(ptile + t * 128);
 #pragma unroll 1
   for (int c = 0; c < nc; ++c) {
-    float pw[16];
+    uint64_t pw[8];
     if (odd)
-      weights<true>(tS + 16 * c, qf + 16 * c, rw.shift + 16 * c, tk.ks, vn, uint32_t(tk.keep >> (16 * c)), pw, row, c, t & 7);
+      weights<true>(tS + 16 * c, qf + 16 * c, rw.lift + 16 * c, tk.ks, vn, uint32_t(tk.keep >> (16 * c)), pw, row, c, t & 7);
     else
-      weights<false>(tS + 16 * c, qf + 16 * c, rw.shift + 16 * c, tk.ks, vn, 0u, pw, row, c, t & 7);
-    l.chunk(c, [&](float (&x)[16]) {
+      weights<false>(tS + 16 * c, qf + 16 * c, rw.lift + 16 * c, tk.ks, vn, 0u, pw, row, c, t & 7);
+    l.chunk(c, [&](uint64_t (&x)[8]) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] += pw[i];
+      for (int i = 0; i < 8; ++i) x[i] = add2(x[i], pw[i]);
     });
   }
 }
@@ -416,9 +450,13 @@ __device__ __forceinline__ void write_rows(const TreeParams& p, const TreeSplit&
 #pragma unroll 1
   for (int c = 0; c < nc; ++c) {
     float x[16];
-    l.chunk(c, [&](float (&y)[16]) {
+    l.chunk(c, [&](uint64_t (&y)[8]) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = y[i];
+      for (int i = 0; i < 8; ++i) {
+        const float2 v = unpack2(y[i]);
+        x[2 * i] = v.x;
+        x[2 * i + 1] = v.y;
+      }
     });
     uint32_t w[16];
     ld16(tO + 16 * c, w);
@@ -543,10 +581,12 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
           raise_device_error(p.err, kErrTableEntry);
           now[u] = 0;
         }
-      // the tokens' scales: asynchronous 4-byte copies, four tokens to a lane (their block's
-      // entry is in lane token / bs, the upper 32 blocks of two tokens in the second register)
-      {
-        if (tiles >= kScaleSlots) (void)wait_warp(st, kScaleEmpty + sslot, sphase ^ 1u);
+      // the tokens' scales: a bulk copy per block with the K codes, where they are aligned for
+      // it; else asynchronous 4-byte copies, four tokens to a lane (their block's entry is in lane
+      // token / bs, the upper 32 blocks of two tokens in the second register)
+      if (tiles >= kScaleSlots) (void)wait_warp(st, kScaleEmpty + sslot, sphase ^ 1u);
+      const int sslot_now = sslot;
+      if (!sp.bulk_scales) {
 #pragma unroll 1
         for (int i = 0; i < 4; ++i) {
           const int b = (4 * lane + i) >> sp.bs_shift;
@@ -560,11 +600,11 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_addr(&st->bars[kScaleFull + sslot]))
                      : "memory");
-        ++tiles;
-        if (++sslot == kScaleSlots) {
-          sslot = 0;
-          sphase ^= 1u;
-        }
+      }
+      ++tiles;
+      if (++sslot == kScaleSlots) {
+        sslot = 0;
+        sphase ^= 1u;
       }
 #pragma unroll 1
       for (int v = 0; v < 2; ++v) {
@@ -572,8 +612,15 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
         if (lane == 0 && n >= slots) ok = wait(st, kCodeEmpty + slot, phase ^ 1u);
         ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
         if (!ok) continue;
-        if (lane == 0) mbar_arrive_expect_tx(&st->bars[kCodeFull + slot], uint32_t(nblk_now) * bytes);
+        const bool with_scales = v == 0 && sp.bulk_scales;
+        if (lane == 0)
+          mbar_arrive_expect_tx(&st->bars[kCodeFull + slot], uint32_t(nblk_now) * (bytes + (with_scales ? 8 * bs : 0)));
         __syncwarp();
+        if (with_scales && lane < nblk_now) {  // (at most 32 blocks, of four tokens and more)
+          const int64_t at = int64_t(now[0]) * p.ts_block + int64_t(kvh_now) * p.ts_head;
+          bulk_copy_g2s(&st->scales[sslot_now][0][lane * bs], p.k_token_scales + at, 4 * bs, &st->bars[kCodeFull + slot]);
+          bulk_copy_g2s(&st->scales[sslot_now][1][lane * bs], p.v_token_scales + at, 4 * bs, &st->bars[kCodeFull + slot]);
+        }
         const unsigned char* src = static_cast<const unsigned char*>(v ? p.value_cache : p.key_cache);
         unsigned char* dst = smem + oCodes + slot * C::kCodeBytes;
 #pragma unroll
@@ -765,22 +812,22 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
     less_registers<kRegsWiden>();
     // ---- widening: K by one warpgroup, V by the other, every second tile of the ring each -----
     const int v = warp >= 16, t = (tid - 384) & 127;
-    // the thread's first chunk of 16 codes of a unit: row and column chunk (of K, a row of a unit
-    // is 4 chunks; of V, all of the token's), and where its two halves go in the operand's row
-    const int per = v ? D / 16 : 4, row = t / per, k = t % per, sw = row & 7, c0 = 2 * (k & 3);
-    const bool swap = k >= 4;  // (V's upper columns in the other order: no two lanes on one bank)
-    const uint32_t unit_pitch = v ? C::kVTokens * D : 64;  // in the codes
-    const uint32_t src_pitch = v ? 2048 : 32 * D, dst_pitch = v ? 128 * (2048 / D) : 32 * 128;
-    const uint32_t at0 = uint32_t((c0 + (swap ? 1 : 0)) ^ sw) << 4, at1 = uint32_t((c0 + (swap ? 0 : 1)) ^ sw) << 4;
-    unsigned char* dst = smem + (v ? C::kV + (k >> 2) * C::kVHalf : C::kK) + row * 128;
+    // the thread's chunks of 16 codes of a unit: columns 16 (t % 4) .. of 64, rows t / 4 and 32
+    // further ones (of a unit of V at D = 128: 32 further, then the other 64 columns)
+    const int row = t >> 2, k = t & 3, sw = row & 7;
+    const bool halves = v && D == 128;
+    const uint32_t a = 32 * D, b = halves ? 64 : 64 * D, da = 32 * 128, db = halves ? C::kVHalf : 64 * 128;
     const unsigned char* src = smem + oCodes + row * D + k * 16;
+    unsigned char* lo = smem + (v ? C::kV : C::kK) + row * 128 + ((2 * k ^ sw) << 4);
+    unsigned char* hi = smem + (v ? C::kV : C::kK) + row * 128 + (((2 * k + 1) ^ sw) << 4);
     const int empty = v ? kVEmpty : kKEmpty, full = v ? kVFull : kKFull;
+    const uint32_t unit_pitch = v ? C::kVTokens * D : 64;  // in the codes
     int slot = v, sslot = 0, n = 0;  // n: units
     uint32_t phase = 0, sphase = 0;
     for (; it.valid(); it.next(p, sp, rg)) {
       for (int j = it.j0; j < it.j1; ++j) {
         (void)wait_warp(st, kCodeFull + slot, phase);
-        if (!v) {
+        if (!v && !sp.bulk_scales) {
           (void)wait_warp(st, kScaleFull + sslot, sphase);
           if (++sslot == kScaleSlots) {
             sslot = 0;
@@ -791,8 +838,8 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
 #pragma unroll 1
         for (int u = 0; u < C::kUnits; ++u, ++n) {
           if (n > 1) (void)wait_warp(st, empty + (n & 1), uint32_t((n >> 1) - 1) & 1u);
-          unsigned char* to = dst + (n & 1) * C::kUnitBytes;
-          widen_unit(tile + u * unit_pitch, src_pitch, to, dst_pitch, at0, at1, swap);
+          const uint32_t buf = (n & 1) * C::kUnitBytes;
+          widen_unit(tile + u * unit_pitch, a, b, lo + buf, hi + buf, da, db);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -829,10 +876,11 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
         float vref = 0.f, vinv = 0.f;  // (and its inverse)
         Sums l;
 #pragma unroll
-        for (int i = 0; i < kHalfRows; ++i) l.a[i >> 4][i & 15] = 0.f;
+        for (int i = 0; i < kHalfRows / 2; ++i) l.a[i >> 3][i & 7] = 0ull;
         if (t < kHalfRows) {
-          rw.m[t] = rw.limit[t] = -INFINITY;
-          rw.shift[t] = 0.f;
+          rw.m[t] = -INFINITY;
+          rw.drop[t] = INFINITY;
+          rw.lift[t] = 0.f;
         }
         group_sync(tk.id);
 #pragma unroll 1
@@ -953,6 +1001,9 @@ bool tree_i8_supported(const TreeParams& p) {
 
 cudaError_t launch_tree_i8(const TreeParams& p, TreeSplit sp, cudaStream_t stream) {
   sp.item_nodes = sp.tq;
+  sp.bulk_scales = p.block_size >= 4 && !((reinterpret_cast<uintptr_t>(p.k_token_scales) |
+                                           reinterpret_cast<uintptr_t>(p.v_token_scales)) & 15) &&
+                   !(p.ts_block & 3) && !(p.ts_head & 3);
   sp.out_vec = (reinterpret_cast<uintptr_t>(p.out) & 7) == 0 && (p.out_stride_t & 3) == 0 && (p.out_stride_h & 3) == 0;
   return p.head_dim == 128 ? launch_tree_i8_tpl<128>(p, sp, stream) : launch_tree_i8_tpl<64>(p, sp, stream);
 }
