@@ -200,8 +200,10 @@ pkv_status tree_prepare(const pkv_tensor* out, const pkv_tensor* query, const pk
   return PKV_OK;
 }
 
-// Blocks of the tensor-core kernel: one per SM.
-int tree_grid(int num_sms) { return num_sms < int(TreeSplit::kMaxGrid) ? num_sms : int(TreeSplit::kMaxGrid); }
+// Blocks of a tensor-core kernel.
+int tree_grid(int num_sms, int per_sm) {
+  return per_sm * (num_sms < int(TreeSplit::kMaxSms) ? num_sms : int(TreeSplit::kMaxSms));
+}
 
 pkv_status tree_launch(TreeParams& p, cudaStream_t stream, const char* what) {
   if (dry_run() || p.num_seqs == 0 || p.num_tokens == 0 || p.num_heads == 0) return PKV_OK;
@@ -210,7 +212,7 @@ pkv_status tree_launch(TreeParams& p, cudaStream_t stream, const char* what) {
   if (st) return st;
   p.err = s->err;
   if (!tree_tensor_supported(p)) return finish_call(s, launch_tree_core(p, stream), stream, what);
-  const int grid = tree_grid(s->num_sms);
+  const int grid = tree_grid(s->num_sms, decode_i8_supported(p) ? decode_i8_blocks_per_sm(p.group) : 1);
   const int rows = tree_part_rows(p.num_tokens, p.group, !p.query_start_loc, p.kv_dtype == kI8);
   std::unique_lock<std::mutex> use(s->ws_use);
   if ((st = ensure_workspace(s, tree_workspace(grid, rows, p.head_dim), stream))) return st;
@@ -393,8 +395,11 @@ int64_t pkv_tree_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t n
   int num_sms = 0, dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    num_sms = int(TreeSplit::kMaxGrid);
-  return int64_t(tree_workspace(tree_grid(num_sms), tree_part_rows(num_tokens, group, false, false), head_dim));
+    num_sms = int(TreeSplit::kMaxSms);
+  const size_t tree = tree_workspace(tree_grid(num_sms, 1), tree_part_rows(num_tokens, group, false, false), head_dim);
+  const size_t decode = tree_workspace(tree_grid(num_sms, decode_i8_blocks_per_sm(group)),
+                                       tree_part_rows(num_tokens, group, true, false), head_dim);
+  return int64_t(tree > decode || group > 16 ? tree : decode);
 }
 
 }  // extern "C"

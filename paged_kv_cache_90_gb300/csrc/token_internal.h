@@ -68,7 +68,8 @@ struct TreeSplit {
   struct Tail {
     int nodes, row0, kvh, last;
   };
-  static constexpr size_t kMaxGrid = 240;                             // blocks: one per SM
+  static constexpr size_t kMaxSms = 240;
+  static constexpr size_t kMaxGrid = 3 * kMaxSms;                     // blocks
   static constexpr size_t kHeader = kWorkspaceHeader + kMaxGrid * sizeof(Tail);  // (a multiple of 256)
   int grid;
   int rows;     // rows of a part's slot
@@ -85,10 +86,13 @@ struct TreeSplit {
 bool tree_tc_supported(const TreeParams& p);  // bf16 caches (tree_tc.cu)
 bool tree_i8_supported(const TreeParams& p);  // token-scaled caches (tree_i8.cu)
 bool tree_tensor_supported(const TreeParams& p);
+bool decode_i8_supported(const TreeParams& p);  // one row a sequence, few heads (decode_i8.cu)
+int decode_i8_blocks_per_sm(int group);
 int tree_part_rows(int64_t num_tokens, int group, bool decode, bool one_tile);
 size_t tree_workspace(int grid, int rows, int head_dim);
 cudaError_t launch_tree_tensor(const TreeParams& p, int grid, int rows, void* ws, cudaStream_t stream);
 cudaError_t launch_tree_i8(const TreeParams& p, TreeSplit sp, cudaStream_t stream);
+cudaError_t launch_decode_i8(const TreeParams& p, TreeSplit sp, cudaStream_t stream);
 cudaError_t launch_tree_merge(const TreeParams& p, const TreeSplit& sp, cudaStream_t stream);
 
 }  // namespace pkv

@@ -1,5 +1,5 @@
-// tree_i8.cu — decode attention and attention of drafted trees over a token-scaled int8
-// cache on the fifth-generation tensor cores.
+// tree_i8.cu — attention of drafted trees (and decode of more than 16 heads a KV head) over a
+// token-scaled int8 cache on the fifth-generation tensor cores.
 //
 // A cached token is head_dim codes and one scale.  With the MMA's 128 rows on the tokens of a
 // key tile and its columns on the query rows (drafted nodes x the group's heads, up to 128),
@@ -23,19 +23,22 @@
 //
 // A tile is 2 x 128 x (D + 4) bytes from HBM, and 2 x 128 x D codes to widen: about 27 warp
 // instructions for 512 codes (an exclusive-or, two byte permutes and two subtractions for four
-// codes), one warpgroup's whole work.  HBM bounds the long calls as long as enough copies are
-// in flight; shared memory (codes in and out, operands in, and read by two MMAs: 176 KB per
-// 32 KB tile at D = 128) is close behind.
+// codes), one warpgroup's whole work.  The chain of a tile bounds it, not a unit: scores, weights
+// and products of a warpgroup follow one another, about 1500 clocks a tile of 16 rows and twice
+// that of 64 rows, with two S^T buffers so that the MMAs are not part of it.  32 trees of 8 to
+// 32 nodes, 4 x 8 heads of 128, over 1000 to 8192 positions: 249 us, 191 TFLOP/s.  (Copying the
+// codes in the widening warps, which takes most of the loader's work, left that at 246 us.)
 //
 // Warps: 0 streams codes, K and V tiles in turn (bulk copies of one (block, head) run each), and
-// scales; 1 issues the score MMAs, 2 the products'; 3 the queries; 4-7 and 8-11 are the softmax warpgroups; 12-15 widen K, 16-19 V.  Every
-// wait is bounded; when one runs out the block sets an error bit and a flag, every role runs
-// through its loops without waiting, lets its copies and MMAs land and frees the tensor memory.
-#include <cuda_fp16.h>
+// scales; 1 issues the score MMAs, 2 the products'; 3 the queries; 4-7 and 8-11 are the softmax
+// warpgroups; 12-15 widen K, 16-19 V.  Every wait is bounded; when one runs out the block sets an
+// error bit and a flag, every role runs through its loops without waiting, lets its copies and
+// MMAs land and frees the tensor memory.
 
 #include <algorithm>
 #include <mutex>
 
+#include "i8_codes.cuh"
 #include "tcgen05.cuh"
 #include "tree_split.cuh"
 #include "umma.cuh"
@@ -133,16 +136,6 @@ __device__ __forceinline__ uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) 
   return (1u << 4) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
 
-// Four int8 codes -> four f16 values, exact: code + 128 in the low byte of 0x64.. is 1152 +
-// code in f16.
-__device__ __forceinline__ uint2 widen4(uint32_t w) {
-  const uint32_t u = w ^ 0x80808080u;
-  const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
-  uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-  const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), off), y = __hsub2(*reinterpret_cast<__half2*>(&b), off);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-}
-
 // 512 chunks of 16 codes -> one unit of an operand (128-byte rows of 64 columns, swizzled), four
 // to each thread of a widening warpgroup: the first from `src` to bytes `lo` and `hi` of shared
 // memory, the others a, b and a + b further (`da`, `db`: multiples of 8 rows, so the swizzle
@@ -153,7 +146,7 @@ __device__ __forceinline__ void widen_unit(const unsigned char* src, uint32_t a,
   for (int i = 0; i < 4; ++i) {
     const uint32_t so = (i & 1 ? a : 0) + (i & 2 ? b : 0), to = (i & 1 ? da : 0) + (i & 2 ? db : 0);
     const uint4 c = *reinterpret_cast<const uint4*>(src + so);
-    const uint2 x = widen4(c.x), y = widen4(c.y), z = widen4(c.z), w = widen4(c.w);
+    const uint2 x = i8::widen4(c.x), y = i8::widen4(c.y), z = i8::widen4(c.z), w = i8::widen4(c.w);
     *reinterpret_cast<uint4*>(lo + to) = make_uint4(x.x, x.y, y.x, y.y);
     *reinterpret_cast<uint4*>(hi + to) = make_uint4(z.x, z.y, w.x, w.y);
   }
@@ -203,13 +196,6 @@ __device__ __forceinline__ bool group_any(int id, bool x) {  // over a warpgroup
   return r != 0;
 }
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-
-// Largest of a warp's values, NaN aside (an order-preserving map to integers).
-__device__ __forceinline__ float warp_max(float x) {
-  const int i = __float_as_int(x == x ? x : -INFINITY);
-  const int o = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7fffffff));
-  return __int_as_float(o ^ ((o >> 31) & 0x7fffffff));
-}
 
 __device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -353,7 +339,7 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
   if (step > 1) (void)wait_warp(st, done_bar + (step & 1), uint32_t((step >> 1) - 1) & 1u);
   if (any) {
     // the tile's maxima, row by row, and the new references
-    const float wv = warp_max(tk.valid && av < INFINITY ? av : 0.f);
+    const float wv = i8::warp_max(tk.valid && av < INFINITY ? av : 0.f);
     if (tk.lane == 0) rw.vpart[tk.warp] = wv;
     float valpha = 1.f;
 #pragma unroll 1
@@ -371,10 +357,7 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
       if (c == 0) {  // (vpart is complete behind the barrier in there)
         const float top = fmaxf(fmaxf(rw.vpart[0], rw.vpart[1]), fmaxf(rw.vpart[2], rw.vpart[3]));
         if (top > 16.f * vref) {
-          // the power of two at or above it (subnormal ones: the smallest normal)
-          const uint32_t b = __float_as_uint(fmaxf(top, 0x1p-126f));
-          const float up = __uint_as_float((b & 0x7f800000u) + ((b & 0x7fffffu) ? 0x800000u : 0u));
-          const float ref = fminf(up, 0x1p127f);
+          const float ref = i8::power_above(top);
           valpha = vref / ref;  // (both powers of two, or 0)
           vref = ref;
           vinv = 1.f / ref;
@@ -778,10 +761,8 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
           for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
 #pragma unroll
           for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          // 2^(14 - exponent of the largest), kept within 2^-100 .. 2^100
-          const int ex = int(__float_as_uint(top) >> 23) - 127;
-          const int sh = top > 0.f && top < INFINITY ? max(-100, min(100, 14 - ex)) : 0;
-          const float s = __uint_as_float(uint32_t(127 + sh) << 23), inv = __uint_as_float(uint32_t(127 - sh) << 23);
+          const int sh = i8::query_shift(top);
+          const float s = i8::power(sh), inv = i8::power(-sh);
           if (r < ir.groups * ir.half) {
             uint32_t h[4];
 #pragma unroll

@@ -759,7 +759,10 @@ cudaError_t launch_tree_merge(const TreeParams& p, const TreeSplit& sp, cudaStre
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-bool tree_tensor_supported(const TreeParams& p) { return tree_tc_supported(p) || tree_i8_supported(p); }
+bool tree_tensor_supported(const TreeParams& p) {
+  // (an entry that is out of range is read as block 0, which has to be there)
+  return p.num_blocks > 0 && (tree_tc_supported(p) || tree_i8_supported(p));
+}
 
 // Rows of a part's slot: the batch's, or at most one row tile of 128 (int8 cache) or two.
 int tree_part_rows(int64_t num_tokens, int group, bool decode, bool one_tile) {
@@ -784,6 +787,7 @@ cudaError_t launch_tree_tensor(const TreeParams& p, int grid, int rows, void* ws
   sp.tails = reinterpret_cast<TreeSplit::Tail*>(w + kWorkspaceHeader);
   sp.o = reinterpret_cast<float*>(w + TreeSplit::kHeader);
   sp.ml = reinterpret_cast<float2*>(sp.o + size_t(grid) * 2 * rows * p.head_dim);
+  if (decode_i8_supported(p)) return launch_decode_i8(p, sp, stream);
   if (p.kv_dtype == kI8) return launch_tree_i8(p, sp, stream);
   return p.head_dim == 128 ? launch_tree_tc_tpl<128>(p, sp, stream) : launch_tree_tc_tpl<64>(p, sp, stream);
 }
