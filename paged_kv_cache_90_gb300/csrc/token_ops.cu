@@ -14,21 +14,49 @@ namespace pkv {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 4;     // of a block: a warp takes a slice of one token's rows
+constexpr int kBatch = 4;     // passes whose loads a warp issues together
+constexpr int kFewRows = 24;  // rows of a slice at most (see slices())
 
+// How a row's columns go to its lanes, two groups of four each: side by side as pairs of
+// columns turn (none, or 2 i with 2 i + 1), or one of each half of the rotated columns (i with
+// half + i, half a multiple of 4); kOdd is the latter for any other half.
+enum Layout { kPairs, kHalves, kOdd };
+
+// A lane's eight columns as they are stored, so that a batch of loads takes few registers.
 template <typename T>
-__device__ __forceinline__ void load_row8(const void* base, int64_t elt, float* f);
+struct Raw;
 template <>
-__device__ __forceinline__ void load_row8<BF16>(const void* base, int64_t elt, float* f) {
-  Chunk<BF16>::expand(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + elt), f);
-}
+struct Raw<BF16> {
+  uint2 a, b;
+  __device__ __forceinline__ void load(const void* base, int64_t elt, int c0, int c1, bool joined) {
+    const uint16_t* s = static_cast<const uint16_t*>(base) + elt;
+    if (joined) {
+      const uint4 v = *reinterpret_cast<const uint4*>(s + c0);
+      a = make_uint2(v.x, v.y);
+      b = make_uint2(v.z, v.w);
+    } else {
+      a = *reinterpret_cast<const uint2*>(s + c0);
+      b = *reinterpret_cast<const uint2*>(s + c1);
+    }
+  }
+  __device__ __forceinline__ void expand(float* f) const { Chunk<BF16>::expand(make_uint4(a.x, a.y, b.x, b.y), f); }
+  __device__ __forceinline__ void clear() { a = b = make_uint2(0u, 0u); }
+};
 template <>
-__device__ __forceinline__ void load_row8<F32>(const void* base, int64_t elt, float* f) {
-  const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + elt);
-  const uint4 a = s[0], b = s[1];
-  Chunk<F32>::expand(a, f);
-  Chunk<F32>::expand(b, f + 4);
-}
+struct Raw<F32> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const void* base, int64_t elt, int c0, int c1, bool) {
+    const float* s = static_cast<const float*>(base) + elt;
+    a = *reinterpret_cast<const uint4*>(s + c0);
+    b = *reinterpret_cast<const uint4*>(s + c1);
+  }
+  __device__ __forceinline__ void expand(float* f) const {
+    Chunk<F32>::expand(a, f);
+    Chunk<F32>::expand(b, f + 4);
+  }
+  __device__ __forceinline__ void clear() { a = b = make_uint4(0u, 0u, 0u, 0u); }
+};
 
 template <typename T>
 __device__ __forceinline__ float load_one(const void* base, int64_t elt);
@@ -42,226 +70,339 @@ __device__ __forceinline__ float load_one<F32>(const void* base, int64_t elt) {
 }
 
 template <typename T>
-__device__ __forceinline__ void store_row8(void* base, int64_t elt, const float* f);
+__device__ __forceinline__ void store_row(void* base, int64_t elt, int c0, int c1, bool joined, const float* f);
 template <>
-__device__ __forceinline__ void store_row8<BF16>(void* base, int64_t elt, const float* f) {
+__device__ __forceinline__ void store_row<BF16>(void* base, int64_t elt, int c0, int c1, bool joined, const float* f) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + elt) = make_uint4(w[0], w[1], w[2], w[3]);
+  uint16_t* d = static_cast<uint16_t*>(base) + elt;
+  if (joined) {
+    *reinterpret_cast<uint4*>(d + c0) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    *reinterpret_cast<uint2*>(d + c0) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(d + c1) = make_uint2(w[2], w[3]);
+  }
 }
 template <>
-__device__ __forceinline__ void store_row8<F32>(void* base, int64_t elt, const float* f) {
-  float4* d = reinterpret_cast<float4*>(static_cast<float*>(base) + elt);
-  d[0] = make_float4(f[0], f[1], f[2], f[3]);
-  d[1] = make_float4(f[4], f[5], f[6], f[7]);
+__device__ __forceinline__ void store_row<F32>(void* base, int64_t elt, int c0, int c1, bool, const float* f) {
+  float* d = static_cast<float*>(base) + elt;
+  *reinterpret_cast<float4*>(d + c0) = make_float4(f[0], f[1], f[2], f[3]);
+  *reinterpret_cast<float4*>(d + c1) = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// Eight values -> eight codes clamp(rint(x / s), +-127), s = amax / 127 (see pkv.h).
-__device__ __forceinline__ uint2 quantize8(const float* x, float s) {
-  uint32_t w[2] = {0u, 0u};
-  if (s > 0.f) {  // (0: all zeros; NaN: zeros, the scale tells)
-    const DivRn div(s);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      int c = __float2int_rn(div(x[i]));
-      c = min(127, max(-127, c));
-      w[i >> 2] |= uint32_t(c & 0xff) << (8 * (i & 3));
-    }
+// Eight codes (words of columns c0 .. and c1 ..) to a row of an 8-bit cache.
+__device__ __forceinline__ void store_codes(void* base, int64_t elt, int c0, int c1, bool joined, uint2 w) {
+  unsigned char* d = static_cast<unsigned char*>(base) + elt;
+  if (joined) {
+    *reinterpret_cast<uint2*>(d + c0) = w;
+  } else {
+    *reinterpret_cast<uint32_t*>(d + c0) = w.x;
+    *reinterpret_cast<uint32_t*>(d + c1) = w.y;
   }
-  return make_uint2(w[0], w[1]);
 }
 
-// The scale of a row with largest magnitude `top`; `bad`: it holds an infinity or a NaN.
-__device__ __forceinline__ float token_scale(float top, bool bad) {
-  const float s = __fdiv_rn(top, 127.f);
-  return bad ? __uint_as_float(0x7fc00000u) : s >= 0x1p-126f ? s : 0.f;
+__device__ __forceinline__ float approx_inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// One thread block per token (and, when few tokens leave SMs idle, per slice of its
-// rows): query rows, then key rows, then value rows.
+// Eight values -> eight codes rint(x / s), s = amax / 127 correctly rounded, or 0 (all codes 0)
+// or NaN (zeros too).  |x / s| is at most 127 (1 + 2^-23), so none needs clamping.
+//
+// The division is made for few of them.  q = x y, y = 1 / s within 2^-23, differs from x / s by
+// less than 127 * 1.5 * 2^-23 < 3e-5, and binary32's x / s by 127 * 2^-24 < 1e-5: where q is
+// further than 1e-4 from the middle of two whole numbers all three round alike.
+__device__ __forceinline__ uint2 quantize8(const float* x, float s) {
+  const bool zero = !(s > 0.f);
+  const float y = zero ? 0.f : approx_inverse(s);
+  uint32_t c[8];
+  float far = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // (1.5 * 2^23 + q rounds q to a whole number, in the low bits)
+    const float q = x[i] * y, r = q + 12582912.f;
+    c[i] = __float_as_uint(r);
+    far = fmaxf(far, fabsf(q - (r - 12582912.f)));
+  }
+  if (far > 0.4999f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = uint32_t(__float2int_rn(__fdiv_rn(x[i], s)));
+  }
+  const uint32_t a = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+  const uint32_t b = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
+  return zero ? make_uint2(0u, 0u) : make_uint2(a, b);
+}
+
+// The scale of a row whose largest magnitude has the bits `top` (an infinity's or a NaN's are
+// above every number's).
+__device__ __forceinline__ float token_scale(uint32_t top) {
+  const DivRn div(127.f);
+  const float s = div(__uint_as_float(top));
+  return top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : s >= 0x1p-126f ? s : 0.f;
+}
+
+// One warp per slice of a token's rows: query rows, then key rows, then value rows.  Block
+// (x, y): slice y of kWarps tokens.
 //
 // The angle of pair i is position * turns[i] mod 2^64 in units of 2^-64 turn: a 64-bit
 // product that wraps at whole turns, exact but for the 2^-53 relative error of the
 // frequency, at any position.  Its top 32 bits, a signed fraction of a turn, go to
 // sincospif: the cosines are within 3e-7 whatever the position, where a binary32 angle
-// in radians would lose all its bits past 2^24.
-template <typename Src, int D>
-__global__ void __launch_bounds__(kThreads) token_write_kernel(const __grid_constant__ TokenParams p) {
+// in radians would lose all its bits past 2^24.  A lane has the same four pairs in every row,
+// so their cosines and sines are in its registers.
+template <typename Src, int D, Layout kLayout>
+__global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_constant__ TokenParams p) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows of a pass
+  constexpr int kN = kLayout == kOdd ? 1 : kBatch;
+  constexpr bool kJoined = kLayout != kHalves && (Src::bytes == 2 || kLayout == kOdd);  // 8 columns side by side
+  __shared__ uint64_t turns[64];
+  const int lane = threadIdx.x & 31, sub = lane / kLanes, l = lane % kLanes;
+  const int half = p.rotary_dim / 2;
+  if (int(threadIdx.x) < half) turns[threadIdx.x] = p.turns[threadIdx.x];
+  __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");  // as in the other cache writes
   asm volatile("griddepcontrol.launch_dependents;");
-  constexpr int kLanes = D / 8;                // lanes per row
-  constexpr int kRows = kThreads / kLanes;     // rows per pass
-  __shared__ float2 cs[D / 2];                 // (cos, sin) of the token's pairs, times the magnitude
-  const int64_t t = blockIdx.x;
-  const int half = p.rotary_dim / 2;
-  if (half) {
-    if (threadIdx.x < half) {
-      const int64_t pos = p.positions64 ? static_cast<const int64_t*>(p.positions)[t]
-                                        : static_cast<const int32_t*>(p.positions)[t];
-      const uint64_t turn = uint64_t(pos) * p.turns[threadIdx.x];
-      const int32_t frac = int32_t(uint32_t(turn >> 32));  // 2^-32 turn, in [-1/2, 1/2)
-      float s, c;
-      sincospif(float(frac) * 0x1p-31f, &s, &c);
-      cs[threadIdx.x] = make_float2(c * p.magnitude, s * p.magnitude);
-    }
-    __syncthreads();
-  }
+  const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (t >= p.w.num_tokens) return;
   const int64_t slot = p.w.slot_mapping[t];
+  int c0 = 8 * l, c1 = 8 * l + 4, pair0 = 0, pair1 = 0, turning = 0;  // (pairs of the first and last four columns)
+  if (kLayout == kHalves) {
+    if (4 * l < half) {
+      c0 = 4 * l;
+      c1 = half + c0;
+      pair0 = c0;
+      pair1 = c0 + 2;
+      turning = 4;
+    } else {
+      c0 = p.rotary_dim + 8 * (l - half / 4);
+      c1 = c0 + 4;
+    }
+  } else if (kLayout == kPairs) {
+    if (!kJoined) {  // (so that a warp's 16-byte accesses lie side by side)
+      c0 = 4 * l;
+      c1 = D / 2 + 4 * l;
+    }
+    pair0 = c0 / 2;
+    pair1 = c1 / 2;
+  }
+  float cs[4], sn[4];
+  bool turn[4];
+  if (half && kLayout != kOdd) {
+    const int64_t pos = p.positions64 ? static_cast<const int64_t*>(p.positions)[t]
+                                      : static_cast<const int32_t*>(p.positions)[t];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k = (i < 2 ? pair0 : pair1 - 2) + i;
+      turn[i] = kLayout == kHalves ? turning != 0 : k < half;
+      const uint64_t angle = turn[i] ? uint64_t(pos) * turns[k] : 0;
+      sincospif(float(int32_t(uint32_t(angle >> 32))) * 0x1p-31f, &sn[i], &cs[i]);  // 2^-32 turn, in [-1/2, 1/2)
+      cs[i] *= p.magnitude;
+      sn[i] *= p.magnitude;
+    }
+  }
   const bool in_cache = slot >= 0 && slot < p.w.num_blocks * p.w.block_size;
-  if (slot >= 0 && !in_cache && threadIdx.x == 0 && blockIdx.y == 0) raise_device_error(p.w.err, kErrSlot);
-  const int64_t blk = in_cache ? slot / p.w.block_size : 0;
-  const int off = in_cache ? int(slot - blk * p.w.block_size) : 0;
+  if (slot >= 0 && !in_cache && lane == 0 && blockIdx.y == 0) raise_device_error(p.w.err, kErrSlot);
+  const int64_t blk = in_cache ? slot >> (31 - __clz(p.w.block_size)) : 0;  // (a power of two)
+  const int off = in_cache ? int(slot) & (p.w.block_size - 1) : 0;
   const int hq = p.num_heads, hk = p.w.num_kv_heads;
   const int rows = hq + (in_cache ? 2 * hk : 0);
-  const int col = int(threadIdx.x % kLanes) * 8;
-  // (a warp's lanes hold whole rows and take the same number of passes, for the shuffles)
-  for (int base = int(blockIdx.y) * kRows; base < rows; base += int(gridDim.y) * kRows) {
-    const int r = base + int(threadIdx.x) / kLanes;
-    const bool live = r < rows;
-    const bool is_q = r < hq, is_v = r >= hq + hk;
-    const int h = is_q ? r : is_v ? r - hq - hk : r - hq;
-    const void* src = is_q ? p.query : is_v ? p.w.value : p.w.key;
-    const int64_t row = is_q ? t * p.q_stride_t + h * p.q_stride_h : t * p.w.src_stride_t + h * p.w.src_stride_h;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (live) load_row8<Src>(src, row + col, x);
-    if (live && !is_v && col < p.rotary_dim) {
-      if (p.interleaved) {
+  const int passes = (hq + 2 * hk + kRows - 1) / kRows, per = (passes + int(gridDim.y) - 1) / int(gridDim.y);
+  const int first = int(blockIdx.y) * per, last = min(first + per, (rows + kRows - 1) / kRows);
+  // (all of a warp's lanes take the same passes, for the shuffles)
+  for (int p0 = first; p0 < last; p0 += kN) {
+    Raw<Src> raw[kN];
+    float y[8];  // (kOdd) the other columns of the pairs
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          if (col + i < p.rotary_dim) {
-            const float2 a = cs[(col + i) >> 1];
-            const float lo = x[i], hi = x[i + 1];
-            x[i] = lo * a.x - hi * a.y;
-            x[i + 1] = hi * a.x + lo * a.y;
-          }
-        }
-      } else {
-        // the other column of each pair: half a rotary_dim away, 16-byte aligned when
-        // half of it is a multiple of 8
-        float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if ((half & 7) == 0) {
-          load_row8<Src>(src, row + (col < half ? col + half : col - half), y);
-        } else {
+    for (int u = 0; u < kN; ++u) {
+      const int r = (p0 + u) * kRows + sub;
+      raw[u].clear();
+      if (p0 + u < last && r < rows) {
+        const bool is_q = r < hq, is_v = r >= hq + hk;
+        const void* src = is_q ? p.query : is_v ? p.w.value : p.w.key;
+        const int64_t row = is_q ? t * p.q_stride_t + r * p.q_stride_h
+                                 : t * p.w.src_stride_t + (is_v ? r - hq - hk : r - hq) * p.w.src_stride_h;
+        raw[u].load(src, row, c0, c1, kJoined);
+        if (kLayout == kOdd && !is_v) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const int c = col + i;
+            const int c = c0 + i;
             if (c < p.rotary_dim) y[i] = load_one<Src>(src, row + (c < half ? c + half : c - half));
           }
         }
+      }
+    }
+    if (kLayout == kOdd) __syncwarp();  // every lane has read its row before one is written (query_out may be query)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int c = col + i;
-          if (c < p.rotary_dim) {
-            const float2 a = cs[c < half ? c : c - half];
-            x[i] = x[i] * a.x + (c < half ? -y[i] : y[i]) * a.y;
+    for (int u = 0; u < kN; ++u) {
+      if (p0 + u >= last) break;
+      const int r = (p0 + u) * kRows + sub;
+      const bool live = r < rows, is_q = r < hq, is_v = r >= hq + hk;
+      const int h = is_q ? r : is_v ? r - hq - hk : r - hq;
+      float x[8];
+      raw[u].expand(x);
+      if (half && !is_v) {
+        if (kLayout == kOdd) {
+          if (live) {
+            const int64_t pos = p.positions64 ? static_cast<const int64_t*>(p.positions)[t]
+                                              : static_cast<const int32_t*>(p.positions)[t];
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+              const int c = c0 + i;
+              if (c >= p.rotary_dim) break;
+              const uint64_t angle = uint64_t(pos) * turns[c < half ? c : c - half];
+              float s, k;
+              sincospif(float(int32_t(uint32_t(angle >> 32))) * 0x1p-31f, &s, &k);
+              s *= p.magnitude;
+              k *= p.magnitude;
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (e == i) x[e] = x[e] * k + (c < half ? -y[e] : y[e]) * s;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float& a = x[kLayout == kHalves ? i : 2 * i];
+            float& b = x[kLayout == kHalves ? 4 + i : 2 * i + 1];
+            const float lo = a, hi = b;
+            if (turn[i]) {
+              a = lo * cs[i] - hi * sn[i];
+              b = hi * cs[i] + lo * sn[i];
+            }
           }
         }
       }
-    }
-    __syncwarp();  // every lane has read its row before one is written (query_out may be query)
-    if (is_q) {
-      if (live) store_row8<Src>(p.query_out, t * p.qo_stride_t + h * p.qo_stride_h + col, x);
-    }
-    if (p.w.cache_dtype == kI8) {
-      float top = 0.f;
-      bool bad = false;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        top = fmaxf(top, fabsf(x[i]));
-        bad |= !(fabsf(x[i]) <= 3.402823466e38f);
+      if (is_q) {
+        if (live) store_row<Src>(p.query_out, t * p.qo_stride_t + h * p.qo_stride_h, c0, c1, kJoined, x);
       }
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) {
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        bad |= __shfl_xor_sync(0xffffffffu, int(bad), o) != 0;
-      }
-      if (live && !is_q) {
-        const float s = token_scale(top, bad);
-        unsigned char* dst = static_cast<unsigned char*>(is_v ? p.w.value_cache : p.w.key_cache);
-        *reinterpret_cast<uint2*>(dst + blk * p.w.cs_block + h * p.w.cs_head + off * D + col) = quantize8(x, s);
-        if (col == 0) (is_v ? p.v_token_scales : p.k_token_scales)[blk * p.ts_block + h * p.ts_head + off] = s;
-      }
-    } else if (live && !is_q) {
+      const int64_t at = blk * p.w.cs_block + h * p.w.cs_head + int64_t(off) * D;
       void* dst = is_v ? p.w.value_cache : p.w.key_cache;
-      const int64_t at = blk * p.w.cs_block + h * p.w.cs_head + int64_t(off) * D + col;
-      if (p.w.cache_dtype == kE4M3) {
-        const float* hs = is_v ? p.w.v_head_scales : p.w.k_head_scales;
-        const float s = hs ? __ldg(hs + h) : is_v ? p.w.v_scale : p.w.k_scale;
-        *reinterpret_cast<uint2*>(static_cast<unsigned char*>(dst) + at) = e4m3_quantize8(x, DivRn(s));
-      } else {
-        store_row8<Src>(dst, at, x);
+      if (p.w.cache_dtype == kI8) {
+        uint32_t top = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (live && !is_q) {
+          const float s = token_scale(top);
+          store_codes(dst, at, c0, c1, kJoined, quantize8(x, s));
+          if (l == 0) (is_v ? p.v_token_scales : p.k_token_scales)[blk * p.ts_block + h * p.ts_head + off] = s;
+        }
+      } else if (live && !is_q) {
+        if (p.w.cache_dtype == kE4M3) {
+          const float* hs = is_v ? p.w.v_head_scales : p.w.k_head_scales;
+          const float s = hs ? __ldg(hs + h) : is_v ? p.w.v_scale : p.w.k_scale;
+          store_codes(dst, at, c0, c1, kJoined, e4m3_quantize8(x, DivRn(s)));
+        } else {
+          store_row<Src>(dst, at, c0, c1, kJoined, x);
+        }
       }
     }
   }
 }
 
-// One thread per eight columns of a (token, tensor, KV head) row.
+// The read back: a warp per slice of a token's key rows, then value rows.
 template <typename Dst, int D>
-__global__ void __launch_bounds__(kThreads) token_read_kernel(const __grid_constant__ TokenParams p) {
+__global__ void __launch_bounds__(32 * kWarps) token_read_kernel(const __grid_constant__ TokenParams p) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  constexpr bool kJoined = Dst::bytes == 2;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  constexpr int kLanes = D / 8;
-  const int64_t t = blockIdx.x;
+  const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (t >= p.w.num_tokens) return;
+  const int lane = threadIdx.x & 31, sub = lane / kLanes, l = lane % kLanes;
   const int64_t slot = p.w.slot_mapping[t];
   if (slot < 0) return;
   if (slot >= p.w.num_blocks * p.w.block_size) {
-    if (threadIdx.x == 0 && blockIdx.y == 0) raise_device_error(p.w.err, kErrSlot);
+    if (lane == 0 && blockIdx.y == 0) raise_device_error(p.w.err, kErrSlot);
     return;
   }
-  const int64_t blk = slot / p.w.block_size;
-  const int off = int(slot - blk * p.w.block_size);
+  const int64_t blk = slot >> (31 - __clz(p.w.block_size));
+  const int off = int(slot) & (p.w.block_size - 1);
   const int hk = p.w.num_kv_heads;
-  const int col = int(threadIdx.x % kLanes) * 8;
-  constexpr int kRows = kThreads / kLanes;
-  for (int r = int(blockIdx.y) * kRows + int(threadIdx.x) / kLanes; r < 2 * hk; r += int(gridDim.y) * kRows) {
-    const bool is_v = r >= hk;
-    const int h = is_v ? r - hk : r;
-    const void* src = is_v ? p.w.value_cache : p.w.key_cache;
-    const int64_t at = blk * p.w.cs_block + h * p.w.cs_head + int64_t(off) * D + col;
-    float x[8];
-    if (p.w.cache_dtype == kF32) {
-      load_row8<F32>(src, at, x);
-    } else if (p.w.cache_dtype == kBF16) {
-      load_row8<BF16>(src, at, x);
-    } else {
-      const uint2 c = *reinterpret_cast<const uint2*>(static_cast<const unsigned char*>(src) + at);
-      float s;
-      if (p.w.cache_dtype == kE4M3) {
-        e4m3x4_to_f32x4(c.x, x);
-        e4m3x4_to_f32x4(c.y, x + 4);
-        const float* hs = is_v ? p.w.v_head_scales : p.w.k_head_scales;
-        s = hs ? __ldg(hs + h) : is_v ? p.w.v_scale : p.w.k_scale;
+  const int c0 = kJoined ? 8 * l : 4 * l, c1 = kJoined ? c0 + 4 : c0 + D / 2;
+  const int passes = (2 * hk + kRows - 1) / kRows, per = (passes + int(gridDim.y) - 1) / int(gridDim.y);
+  const int first = int(blockIdx.y) * per, last = min(first + per, passes);
+  const int type = p.w.cache_dtype;
+  for (int p0 = first; p0 < last; p0 += kBatch) {
+    uint4 a[kBatch], b[kBatch];  // columns c0 .. and c1 .., as they are stored
+    float s[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int r = (p0 + u) * kRows + sub;
+      if (p0 + u >= last || r >= 2 * hk) continue;
+      const bool is_v = r >= hk;
+      const int h = is_v ? r - hk : r;
+      const int elt = type == kF32 ? 4 : type == kBF16 ? 2 : 1;
+      const unsigned char* src = static_cast<const unsigned char*>(is_v ? p.w.value_cache : p.w.key_cache) +
+                                 (blk * p.w.cs_block + h * p.w.cs_head + int64_t(off) * D) * elt;
+      if (type == kF32) {
+        a[u] = *reinterpret_cast<const uint4*>(src + 4 * c0);
+        b[u] = *reinterpret_cast<const uint4*>(src + 4 * c1);
+      } else if (type == kBF16) {
+        const uint2 x = *reinterpret_cast<const uint2*>(src + 2 * c0), y = *reinterpret_cast<const uint2*>(src + 2 * c1);
+        a[u].x = x.x; a[u].y = x.y;
+        b[u].x = y.x; b[u].y = y.y;
       } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = float(int(int8_t((i < 4 ? c.x : c.y) >> (8 * (i & 3)))));
-        s = (is_v ? p.v_token_scales : p.k_token_scales)[blk * p.ts_block + h * p.ts_head + off];
+        a[u].x = *reinterpret_cast<const uint32_t*>(src + c0);
+        b[u].x = *reinterpret_cast<const uint32_t*>(src + c1);
+        const float* hs = is_v ? p.w.v_head_scales : p.w.k_head_scales;
+        s[u] = type == kI8 ? (is_v ? p.v_token_scales : p.k_token_scales)[blk * p.ts_block + h * p.ts_head + off]
+               : hs        ? __ldg(hs + h)
+               : is_v      ? p.w.v_scale
+                           : p.w.k_scale;
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] *= s;
     }
-    void* dst = const_cast<void*>(is_v ? p.w.value : p.w.key);
-    store_row8<Dst>(dst, t * p.w.src_stride_t + h * p.w.src_stride_h + col, x);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int r = (p0 + u) * kRows + sub;
+      if (p0 + u >= last || r >= 2 * hk) continue;
+      const bool is_v = r >= hk;
+      const int h = is_v ? r - hk : r;
+      float x[8];
+      if (type == kF32) {
+        Chunk<F32>::expand(a[u], x);
+        Chunk<F32>::expand(b[u], x + 4);
+      } else if (type == kBF16) {
+        Chunk<BF16>::expand(make_uint4(a[u].x, a[u].y, b[u].x, b[u].y), x);
+      } else {
+        if (type == kE4M3) {
+          e4m3x4_to_f32x4(a[u].x, x);
+          e4m3x4_to_f32x4(b[u].x, x + 4);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[i] = float(int(int8_t((i < 4 ? a[u].x : b[u].x) >> (8 * (i & 3)))));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] *= s[u];
+      }
+      store_row<Dst>(const_cast<void*>(is_v ? p.w.value : p.w.key), t * p.w.src_stride_t + h * p.w.src_stride_h, c0, c1,
+                     kJoined, x);
+    }
   }
 }
 
-// grid.y slices of a token's rows: one block per token once that fills the GPU
-unsigned row_slices(int64_t tokens, int rows, int head_dim) {
-  const int per_pass = kThreads / (head_dim / 8);
-  const int passes = (rows + per_pass - 1) / per_pass;
-  int64_t y = 1;
-  while (y < passes && tokens * y < 608) ++y;  // 608 = 152 SMs x 4 blocks
-  return unsigned(y);
+// Slices of a token's rows: as many as make a warp for each of the GPU's places (152 SMs x 16),
+// down to one pass each; and no slice of more than kFewRows rows, so that the last blocks of a
+// large call end together.
+unsigned slices(int64_t tokens, int rows, int head_dim) {
+  const int per_pass = 256 / head_dim, passes = (rows + per_pass - 1) / per_pass;
+  int64_t y = (rows + kFewRows - 1) / kFewRows;
+  if (tokens * y < 2432) y = (2432 + tokens - 1) / tokens;
+  y = y < passes ? y : passes;
+  return unsigned(y < 65535 ? y : 65535);
 }
 
 template <typename K>
 cudaError_t launch(K kern, const TokenParams& p, int rows, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.w.num_tokens), row_slices(p.w.num_tokens, rows, p.w.head_dim));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(unsigned((p.w.num_tokens + kWarps - 1) / kWarps), slices(p.w.num_tokens, rows, p.w.head_dim));
+  cfg.blockDim = dim3(32 * kWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -273,15 +414,20 @@ cudaError_t launch(K kern, const TokenParams& p, int rows, cudaStream_t stream) 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <typename Src, int D>
+cudaError_t launch_write(const TokenParams& p, cudaStream_t stream) {
+  const int rows = p.num_heads + 2 * p.w.num_kv_heads;
+  if (p.rotary_dim == 0 || p.interleaved) return launch(token_write_kernel<Src, D, kPairs>, p, rows, stream);
+  return p.rotary_dim % 8 == 0 ? launch(token_write_kernel<Src, D, kHalves>, p, rows, stream)
+                               : launch(token_write_kernel<Src, D, kOdd>, p, rows, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_token_write(const TokenParams& p, cudaStream_t stream) {
-  const int rows = p.num_heads + 2 * p.w.num_kv_heads;
   if (p.w.src_dtype == kBF16)
-    return p.w.head_dim == 128 ? launch(token_write_kernel<BF16, 128>, p, rows, stream)
-                               : launch(token_write_kernel<BF16, 64>, p, rows, stream);
-  return p.w.head_dim == 128 ? launch(token_write_kernel<F32, 128>, p, rows, stream)
-                             : launch(token_write_kernel<F32, 64>, p, rows, stream);
+    return p.w.head_dim == 128 ? launch_write<BF16, 128>(p, stream) : launch_write<BF16, 64>(p, stream);
+  return p.w.head_dim == 128 ? launch_write<F32, 128>(p, stream) : launch_write<F32, 64>(p, stream);
 }
 
 cudaError_t launch_token_read(const TokenParams& p, cudaStream_t stream) {
