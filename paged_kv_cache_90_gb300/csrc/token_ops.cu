@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kWarps = 4;     // of a block: a warp takes a slice of one token's rows
 constexpr int kBatch = 4;     // passes whose loads a warp issues together
-constexpr int kFewRows = 24;  // rows of a slice at most (see slices())
+constexpr int kFewRows = 48;  // rows of a slice at most (see slices())
 
 // How a row's columns go to its lanes, two groups of four each: side by side as pairs of
 // columns turn (none, or 2 i with 2 i + 1), or one of each half of the rotated columns (i with
@@ -170,14 +170,17 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
   const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   if (t >= p.w.num_tokens) return;
   const int64_t slot = p.w.slot_mapping[t];
-  int c0 = 8 * l, c1 = 8 * l + 4, pair0 = 0, pair1 = 0, turning = 0;  // (pairs of the first and last four columns)
+  int64_t pos = 0;
+  if (half) pos = p.positions64 ? static_cast<const int64_t*>(p.positions)[t] : static_cast<const int32_t*>(p.positions)[t];
+  int c0 = 8 * l, c1 = 8 * l + 4, pair0 = 0, pair1 = 0;  // (pairs of the first and last four columns)
+  bool turning = false;
   if (kLayout == kHalves) {
     if (4 * l < half) {
       c0 = 4 * l;
       c1 = half + c0;
       pair0 = c0;
       pair1 = c0 + 2;
-      turning = 4;
+      turning = true;
     } else {
       c0 = p.rotary_dim + 8 * (l - half / 4);
       c1 = c0 + 4;
@@ -192,27 +195,10 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
   }
   float cs[4], sn[4];
   bool turn[4];
-  if (half && kLayout != kOdd) {
-    const int64_t pos = p.positions64 ? static_cast<const int64_t*>(p.positions)[t]
-                                      : static_cast<const int32_t*>(p.positions)[t];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = (i < 2 ? pair0 : pair1 - 2) + i;
-      turn[i] = kLayout == kHalves ? turning != 0 : k < half;
-      const uint64_t angle = turn[i] ? uint64_t(pos) * turns[k] : 0;
-      sincospif(float(int32_t(uint32_t(angle >> 32))) * 0x1p-31f, &sn[i], &cs[i]);  // 2^-32 turn, in [-1/2, 1/2)
-      cs[i] *= p.magnitude;
-      sn[i] *= p.magnitude;
-    }
-  }
-  const bool in_cache = slot >= 0 && slot < p.w.num_blocks * p.w.block_size;
-  if (slot >= 0 && !in_cache && lane == 0 && blockIdx.y == 0) raise_device_error(p.w.err, kErrSlot);
-  const int64_t blk = in_cache ? slot >> (31 - __clz(p.w.block_size)) : 0;  // (a power of two)
-  const int off = in_cache ? int(slot) & (p.w.block_size - 1) : 0;
   const int hq = p.num_heads, hk = p.w.num_kv_heads;
-  const int rows = hq + (in_cache ? 2 * hk : 0);
-  const int passes = (hq + 2 * hk + kRows - 1) / kRows, per = (passes + int(gridDim.y) - 1) / int(gridDim.y);
-  const int first = int(blockIdx.y) * per, last = min(first + per, (rows + kRows - 1) / kRows);
+  const int rows = hq + 2 * hk;
+  const int passes = (rows + kRows - 1) / kRows, per = (passes + int(gridDim.y) - 1) / int(gridDim.y);
+  const int first = int(blockIdx.y) * per, last = min(first + per, passes);
   // (all of a warp's lanes take the same passes, for the shuffles)
   for (int p0 = first; p0 < last; p0 += kN) {
     Raw<Src> raw[kN];
@@ -236,6 +222,20 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
         }
       }
     }
+    if (p0 == first && half && kLayout != kOdd) {  // (behind the first loads, as is all that needs the slot)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = (i < 2 ? pair0 : pair1 - 2) + i;
+        turn[i] = kLayout == kHalves ? turning : k < half;
+        const uint64_t angle = turn[i] ? uint64_t(pos) * turns[k] : 0;
+        sincospif(float(int32_t(uint32_t(angle >> 32))) * 0x1p-31f, &sn[i], &cs[i]);  // 2^-32 turn, in [-1/2, 1/2)
+        cs[i] *= p.magnitude;
+        sn[i] *= p.magnitude;
+      }
+    }
+    const bool in_cache = slot >= 0 && slot < p.w.num_blocks * p.w.block_size;
+    const int64_t blk = in_cache ? slot >> (31 - __clz(p.w.block_size)) : 0;  // (a power of two)
+    const int off = in_cache ? int(slot) & (p.w.block_size - 1) : 0;
     if (kLayout == kOdd) __syncwarp();  // every lane has read its row before one is written (query_out may be query)
 #pragma unroll
     for (int u = 0; u < kN; ++u) {
@@ -248,8 +248,6 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
       if (half && !is_v) {
         if (kLayout == kOdd) {
           if (live) {
-            const int64_t pos = p.positions64 ? static_cast<const int64_t*>(p.positions)[t]
-                                              : static_cast<const int32_t*>(p.positions)[t];
 #pragma unroll 1
             for (int i = 0; i < 8; ++i) {
               const int c = c0 + i;
@@ -288,12 +286,12 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
         for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (live && !is_q) {
+        if (live && !is_q && in_cache) {
           const float s = token_scale(top);
           store_codes(dst, at, c0, c1, kJoined, quantize8(x, s));
           if (l == 0) (is_v ? p.v_token_scales : p.k_token_scales)[blk * p.ts_block + h * p.ts_head + off] = s;
         }
-      } else if (live && !is_q) {
+      } else if (live && !is_q && in_cache) {
         if (p.w.cache_dtype == kE4M3) {
           const float* hs = is_v ? p.w.v_head_scales : p.w.k_head_scales;
           const float s = hs ? __ldg(hs + h) : is_v ? p.w.v_scale : p.w.k_scale;
@@ -304,10 +302,65 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
       }
     }
   }
+  if (slot >= p.w.num_blocks * p.w.block_size && lane == 0 && blockIdx.y == 0) raise_device_error(p.w.err, kErrSlot);
+}
+
+// The same for the write into a token-scaled cache alone: key rows, then value rows.
+template <typename Src, int D>
+__global__ void __launch_bounds__(32 * kWarps) token_quantize_kernel(const __grid_constant__ TokenParams p) {
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;
+  constexpr bool kJoined = Src::bytes == 2;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  if (t >= p.w.num_tokens) return;
+  const int lane = threadIdx.x & 31, sub = lane / kLanes, l = lane % kLanes;
+  const int64_t slot = p.w.slot_mapping[t];
+  const int c0 = kJoined ? 8 * l : 4 * l, c1 = kJoined ? c0 + 4 : c0 + D / 2;
+  const int hk = p.w.num_kv_heads, rows = 2 * hk;
+  const int passes = (rows + kRows - 1) / kRows, per = (passes + int(gridDim.y) - 1) / int(gridDim.y);
+  const int first = int(blockIdx.y) * per, last = min(first + per, passes);
+  for (int p0 = first; p0 < last; p0 += kBatch) {
+    Raw<Src> raw[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int r = (p0 + u) * kRows + sub;
+      raw[u].clear();
+      if (p0 + u < last && r < rows)
+        raw[u].load(r >= hk ? p.w.value : p.w.key, t * p.w.src_stride_t + (r >= hk ? r - hk : r) * p.w.src_stride_h, c0, c1,
+                    kJoined);
+    }
+    if (slot < 0) return;  // padding
+    if (slot >= p.w.num_blocks * p.w.block_size) {
+      if (lane == 0 && blockIdx.y == 0) raise_device_error(p.w.err, kErrSlot);
+      return;
+    }
+    const int64_t blk = slot >> (31 - __clz(p.w.block_size));
+    const int off = int(slot) & (p.w.block_size - 1);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int r = (p0 + u) * kRows + sub;
+      if (p0 + u >= last) break;
+      const bool is_v = r >= hk;
+      const int h = is_v ? r - hk : r;
+      float x[8];
+      raw[u].expand(x);
+      uint32_t top = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (r >= rows) continue;
+      const float s = token_scale(top);
+      store_codes(is_v ? p.w.value_cache : p.w.key_cache, blk * p.w.cs_block + h * p.w.cs_head + int64_t(off) * D, c0, c1,
+                  kJoined, quantize8(x, s));
+      if (l == 0) (is_v ? p.v_token_scales : p.k_token_scales)[blk * p.ts_block + h * p.ts_head + off] = s;
+    }
+  }
 }
 
 // The read back: a warp per slice of a token's key rows, then value rows.
-template <typename Dst, int D>
+template <typename Dst, int D, int type>
 __global__ void __launch_bounds__(32 * kWarps) token_read_kernel(const __grid_constant__ TokenParams p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
   constexpr bool kJoined = Dst::bytes == 2;
@@ -328,7 +381,6 @@ __global__ void __launch_bounds__(32 * kWarps) token_read_kernel(const __grid_co
   const int c0 = kJoined ? 8 * l : 4 * l, c1 = kJoined ? c0 + 4 : c0 + D / 2;
   const int passes = (2 * hk + kRows - 1) / kRows, per = (passes + int(gridDim.y) - 1) / int(gridDim.y);
   const int first = int(blockIdx.y) * per, last = min(first + per, passes);
-  const int type = p.w.cache_dtype;
   for (int p0 = first; p0 < last; p0 += kBatch) {
     uint4 a[kBatch], b[kBatch];  // columns c0 .. and c1 .., as they are stored
     float s[kBatch];
@@ -417,9 +469,22 @@ cudaError_t launch(K kern, const TokenParams& p, int rows, cudaStream_t stream) 
 template <typename Src, int D>
 cudaError_t launch_write(const TokenParams& p, cudaStream_t stream) {
   const int rows = p.num_heads + 2 * p.w.num_kv_heads;
+  if (p.num_heads == 0 && p.rotary_dim == 0 && p.w.cache_dtype == kI8)
+    return launch(token_quantize_kernel<Src, D>, p, rows, stream);
   if (p.rotary_dim == 0 || p.interleaved) return launch(token_write_kernel<Src, D, kPairs>, p, rows, stream);
   return p.rotary_dim % 8 == 0 ? launch(token_write_kernel<Src, D, kHalves>, p, rows, stream)
                                : launch(token_write_kernel<Src, D, kOdd>, p, rows, stream);
+}
+
+template <typename Dst, int D>
+cudaError_t launch_read(const TokenParams& p, cudaStream_t stream) {
+  const int rows = 2 * p.w.num_kv_heads;
+  switch (p.w.cache_dtype) {
+    case kF32: return launch(token_read_kernel<Dst, D, kF32>, p, rows, stream);
+    case kBF16: return launch(token_read_kernel<Dst, D, kBF16>, p, rows, stream);
+    case kE4M3: return launch(token_read_kernel<Dst, D, kE4M3>, p, rows, stream);
+    default: return launch(token_read_kernel<Dst, D, kI8>, p, rows, stream);
+  }
 }
 
 }  // namespace
@@ -431,12 +496,9 @@ cudaError_t launch_token_write(const TokenParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_token_read(const TokenParams& p, cudaStream_t stream) {
-  const int rows = 2 * p.w.num_kv_heads;
   if (p.w.src_dtype == kBF16)
-    return p.w.head_dim == 128 ? launch(token_read_kernel<BF16, 128>, p, rows, stream)
-                               : launch(token_read_kernel<BF16, 64>, p, rows, stream);
-  return p.w.head_dim == 128 ? launch(token_read_kernel<F32, 128>, p, rows, stream)
-                             : launch(token_read_kernel<F32, 64>, p, rows, stream);
+    return p.w.head_dim == 128 ? launch_read<BF16, 128>(p, stream) : launch_read<BF16, 64>(p, stream);
+  return p.w.head_dim == 128 ? launch_read<F32, 128>(p, stream) : launch_read<F32, 64>(p, stream);
 }
 
 }  // namespace pkv
