@@ -78,7 +78,7 @@ struct TreeSplit {
   int q_nodes;  // nodes of one query copy
   int bs_shift; // log2 of the block size
   bool out_vec;      // output rows are 8-byte aligned
-  bool bulk_scales;  // a block's scales are a 16-byte aligned run
+  bool vec_scales;   // four tokens' scales are 16 aligned bytes
   Tail* tails;  // [grid]
   float* o;     // [2 grid, rows, D]: block b's part of an item begun before it, then of its own
   float2* ml;   // [2 grid, rows] maximum (base 2) and sum

@@ -10,8 +10,8 @@
 //   P^T = 2^(S ks c - m) vs   by one thread per token, written to shared memory as f16
 //   O^T += V^T P^T      M = D, N = rows, K = 128 tokens: V codes widened to f16, O^T in
 //                       tensor memory, lane = column of the head
-// The rows go in two halves to two softmax warpgroups (one, if there are at most 16), each with
-// its own P, S^T buffers and O^T; every key tile is widened once for all of them.
+// The rows are shared by two softmax warpgroups (one, if there are at most 16); every key tile is
+// widened once for all of them, and one MMA has all their rows.
 //
 // The codes are whole numbers, so f16 holds them exactly; a query row is scaled by a power of
 // two that brings its largest element to 2^14, so its bf16 values are exact down to 2^-29 of
@@ -23,17 +23,19 @@
 //
 // A tile is 2 x 128 x (D + 4) bytes from HBM, and 2 x 128 x D codes to widen: about 27 warp
 // instructions for 512 codes (an exclusive-or, two byte permutes and two subtractions for four
-// codes), one warpgroup's whole work.  The chain of a tile bounds it, not a unit: scores, weights
-// and products of a warpgroup follow one another, about 1500 clocks a tile of 16 rows and twice
-// that of 64 rows, with two S^T buffers so that the MMAs are not part of it.  32 trees of 8 to
-// 32 nodes, 4 x 8 heads of 128, over 1000 to 8192 positions: 249 us, 191 TFLOP/s.  (Copying the
-// codes in the widening warps, which takes most of the loader's work, left that at 246 us.)
+// codes), one warpgroup's whole work.  The chain of a tile bounds it, not a unit: of 64 rows a
+// warp's weights take 2600 clocks, what is between two tiles' weights (a signal, a wait, the
+// scales) another 1500, with two S^T buffers so that the score MMAs are not part of it.  32 trees
+// of 8 to 32 nodes, 4 x 8 heads of 128, over 1000 to 8192 positions: 195 us, 245 TFLOP/s.  It was
+// 249 us with a pass over the scores before the weights, with products of each half of the rows
+// (their A operand was read twice), and with the queries converted by one warp (33000 clocks
+// between two items).
 //
-// Warps: 0 streams codes, K and V tiles in turn (bulk copies of one (block, head) run each), and
-// scales; 1 issues the score MMAs, 2 the products'; 3 the queries; 4-7 and 8-11 are the softmax
-// warpgroups; 12-15 widen K, 16-19 V.  Every wait is bounded; when one runs out the block sets an
-// error bit and a flag, every role runs through its loops without waiting, lets its copies and
-// MMAs land and frees the tensor memory.
+// Warps: 0 streams K codes and the scales, 3 V codes (bulk copies of one (block, head) run each);
+// 1 issues the score MMAs, 2 the products'; 4-7 and 8-11 are the softmax warpgroups, which also
+// bring the queries in; 12-15 widen K, 16-19 V.  Every wait is bounded; when one runs out the
+// block sets an error bit and a flag, every role runs through its loops without waiting, lets its
+// copies and MMAs land and frees the tensor memory.
 
 #include <algorithm>
 #include <mutex>
@@ -70,33 +72,36 @@ struct Cfg {
   static constexpr uint32_t kVHalf = kVTokens * 128;        // pitch of its 64-column halves
   static constexpr uint32_t kCodeBytes = kBN * D;
   static constexpr uint32_t kPBytes = kBN * 128;
-  // from the 1024-aligned base: K units | V units | Q | P (two for each warpgroup) | ring of code
-  // tiles | state.  A batch of few rows needs one warpgroup's P and 16 rows of Q, and the ring
-  // has the rest.
+  // from the 1024-aligned base: K units | V units | Q | P | ring of code tiles | state.  A batch
+  // of few rows needs 16 rows of Q and of two P; else there is one P of two times 64 rows.
   static constexpr uint32_t kK = 0, kV = 2 * kUnitBytes, kQ = 4 * kUnitBytes;
-  static constexpr uint32_t kState = 212 * 1024;
-  static constexpr uint32_t kStateBytes = 14 * 1024;
+  static constexpr uint32_t kState = 211 * 1024;
+  static constexpr uint32_t kStateBytes = 15 * 1024;
   static constexpr size_t kSmem = kState + kStateBytes + 1024;  // (+ alignment)
-  // tensor memory: S^T [warpgroup][2], then O^T [2][warpgroup], 64 columns each
+  // tensor memory: S^T [2], then O^T [2], 128 columns each
   static constexpr uint32_t kS = 0, kO = 256;
 };
 
 constexpr int kScaleSlots = 8;  // tiles whose scales are in shared memory
 
-enum Bar { kQFull = 0, kQEmpty, kCodeFull, kCodeEmpty = kCodeFull + kMaxSlots, kKFull = kCodeEmpty + kMaxSlots,
+enum Bar { kQFull = 0, kCodeFull, kCodeEmpty = kCodeFull + kMaxSlots, kKFull = kCodeEmpty + kMaxSlots,
            kKEmpty = kKFull + 2, kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kScaleFull = kVEmpty + 2,
-           kScaleEmpty = kScaleFull + kScaleSlots, kSFull = kScaleEmpty + kScaleSlots, kSFree = kSFull + 4,
-           kPFull = kSFree + 4, kODone = kPFull + 4, kOFree = kODone + 4, kDrain = kOFree + 4, kNumBars = kDrain + 2 };
+           kScaleEmpty = kScaleFull + kScaleSlots, kSFull = kScaleEmpty + kScaleSlots, kPFull = kSFull + 2,
+           kODone = kPFull + 2, kOFree = kODone + 2, kDrain = kOFree + 2, kNumBars = kDrain + 2 };
 
 // What a warpgroup keeps of its rows.
 struct alignas(16) Rows {
   float m[kHalfRows];        // reference maximum (base 2), -infinity before the first score
-  float drop[kHalfRows];     // a score before its row's factor, plus this, above 0 moves it
-  float lift[kHalfRows];     // -m, or 0 where it is -infinity
+  float lift[kHalfRows];     // -m; where that is infinite kNoLift, with which every score moves it
+  float old[kHalfRows];      // the last move's lift before it
   float alpha_l[kHalfRows];  // the last move's factors on the sums and on the output
   float alpha_o[kHalfRows];
+  float part[4][16];          // of a reduction over the tokens: each warp's
   float vpart[4];
 };
+
+constexpr float kNoLift = 3.402823466e38f;
+constexpr float kTop = 100.f;  // a weight's exponent at most, so that it can be taken back
 
 struct State {
   uint64_t bars[kNumBars + 1];
@@ -104,8 +109,7 @@ struct State {
   uint32_t tmem;
   Range range;
   longlong2 warp_sum[kThreads / 32];
-  alignas(16) float qf[4][2][kHalfRows];  // a row's score factor, per item (index mod 4: a warpgroup may be
-                              // two items behind the queries)
+  alignas(16) float qf[2][2][kHalfRows];  // a row's score factor, per item (index mod 2)
   Rows rows[2];
   alignas(16) float scales[kScaleSlots][2][kBN];  // of K and of V
 };
@@ -179,9 +183,13 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// Asynchronous copy of one float, or of a zero.
+// Asynchronous copies of one float and of four, or of zeros.
 __device__ __forceinline__ void copy4(float* dst, const float* src, bool there) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 4 : 0) : "memory");
+}
+
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
 template <int N>
@@ -216,7 +224,7 @@ __device__ __forceinline__ void lds16(const float* s, float (&f)[16]) {
   }
 }
 
-// A softmax warpgroup's thread: token `t` of the tile, its rows' sums in registers.
+// A softmax warpgroup's thread: token 32 warp + lane of the tile.
 struct Token {
   int id;          // the warpgroup's barrier
   int warp, lane;  // of the warpgroup
@@ -240,35 +248,48 @@ struct Sums {
   }
 };
 
-// Weights of the 16 rows at tensor-memory column `ts`, in pairs: returned in `pw`, and times
-// the token's value scale `vn` written as f16 to `row` (the token's row of P, swizzled by `sw`).
-// `lift` holds the references' negatives.  With kKeep a row that does not see the token has a
-// product of 0 whatever `vn` is.
-template <bool kKeep>
-__device__ __forceinline__ void weights(uint32_t ts, const float* qf, const float* lift, float ks, float vn,
-                                        uint32_t keep, uint64_t (&pw)[8], uint4* row, int c, int sw) {
-  uint32_t w[16], h[8];
-  ld16(ts, w);
-  const uint64_t ks2 = pack2(ks, ks), vn2 = pack2(vn, vn);
+__device__ __forceinline__ float min_nan(float x, float y) {  // (a NaN stays one)
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+
+// Weights of 16 rows from their scores `w`, in pairs: returned in `pw`.  `lift` holds the
+// references' negatives; returns the largest exponent, NaN aside.
+__device__ __forceinline__ float exponentials(const uint32_t (&w)[16], const float* qf, const float* lift, float ks,
+                                              uint64_t (&pw)[8]) {
+  const uint64_t ks2 = pack2(ks, ks);
+  float over = -INFINITY;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const ulonglong2 f = reinterpret_cast<const ulonglong2*>(qf)[i], m = reinterpret_cast<const ulonglong2*>(lift)[i];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int e = 4 * i + 2 * j;
-      const uint64_t z = fma2(mul2(pack2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])), ks2), j ? f.y : f.x,
-                              j ? m.y : m.x);
-      const float2 zz = unpack2(z);
-      const uint64_t p = pack2(fast_exp2(zz.x), fast_exp2(zz.y));
-      pw[2 * i + j] = p;
-      float2 x = unpack2(mul2(p, vn2));
-      if (kKeep) {
-        if (!(keep >> e & 1u)) x.x = 0.f;
-        if (!(keep >> (e + 1) & 1u)) x.y = 0.f;
-      }
-      const __half2 pr = __floats2half2_rn(x.x, x.y);
-      h[2 * i + j] = *reinterpret_cast<const uint32_t*>(&pr);
+      const float2 z = unpack2(fma2(mul2(pack2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])), ks2), j ? f.y : f.x,
+                                    j ? m.y : m.x));
+      over = fmaxf(over, fmaxf(z.x, z.y));
+      pw[2 * i + j] = pack2(fast_exp2(min_nan(z.x, kTop)), fast_exp2(min_nan(z.y, kTop)));
     }
+  }
+  return over;
+}
+
+// Weights times the token's value scale `vn`, as f16, to `row` (the token's row of P, swizzled
+// by `sw`).  With kKeep a row that does not see the token has a product of 0 whatever `vn` is.
+template <bool kKeep>
+__device__ __forceinline__ void store_weights(const uint64_t (&pw)[8], float vn, uint32_t keep, uint4* row, int c, int sw) {
+  const uint64_t vn2 = pack2(vn, vn);
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float2 x = unpack2(mul2(pw[i], vn2));
+    if (kKeep) {
+      if (!(keep >> (2 * i) & 1u)) x.x = 0.f;
+      if (!(keep >> (2 * i + 1) & 1u)) x.y = 0.f;
+    }
+    const __half2 pr = __floats2half2_rn(x.x, x.y);
+    h[i] = *reinterpret_cast<const uint32_t*>(&pr);
   }
   row[(2 * c) ^ sw] = make_uint4(h[0], h[1], h[2], h[3]);
   row[(2 * c + 1) ^ sw] = make_uint4(h[4], h[5], h[6], h[7]);
@@ -288,148 +309,200 @@ __device__ __forceinline__ void hide(uint32_t tS, int nc, float ks, uint64_t kee
   tc::wait_st();
 }
 
-// Reduces 16 rows of 128 tokens through shared memory: every thread has its token's 16
-// values `x`, thread t returns the result of row t / 8 (eight threads share it).  `buf` is
-// 8 KB, free when the warpgroup calls; two calls in a row take different ones.
+// Reduces 16 rows over the warpgroup's 128 tokens: every thread has its token's 16 values `x`;
+// lane 2 r + (0 or 1) of each warp returns the result of row r.  (A warp's rows are halved as its
+// lanes are: 16 shuffles for 16 rows.)  `part` is free when the warpgroup calls.
 template <bool kMax>
-__device__ __forceinline__ float reduce_rows(int id, int t, const float (&x)[16], float* buf) {
+__device__ __forceinline__ float reduce_rows(int id, int warp, int lane, float (&x)[16], float (*part)[16]) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) buf[i * kBN + t] = x[i];
+  for (int n = 8, o = 16; n > 0; n >>= 1, o >>= 1)
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      // (the upper lanes take the upper rows)
+      const bool up = lane & o;
+      const float mine = up ? x[n + i] : x[i], z = __shfl_xor_sync(0xffffffffu, up ? x[i] : x[n + i], o);
+      x[i] = kMax ? fmaxf(mine, z) : mine + z;
+    }
+  const float z = __shfl_xor_sync(0xffffffffu, x[0], 1);
+  const float y = kMax ? fmaxf(x[0], z) : x[0] + z;
+  if (!(lane & 1)) part[warp][lane >> 1] = y;
   group_sync(id);
-  float y[16];
-  lds16(buf + 16 * t, y);
-  float r = y[0];
-#pragma unroll
-  for (int i = 1; i < 16; ++i) r = kMax ? fmaxf(r, y[i]) : r + y[i];
-#pragma unroll
-  for (int o = 4; o > 0; o >>= 1) {
-    const float z = __shfl_xor_sync(0xffffffffu, r, o);
-    r = kMax ? fmaxf(r, z) : r + z;
-  }
-  return r;
+  const float* a = &part[0][lane >> 1];
+  return kMax ? fmaxf(fmaxf(a[0], a[16]), fmaxf(a[32], a[48])) : (a[0] + a[16]) + (a[32] + a[48]);
 }
 
 // One key tile for the nc x 16 rows of a warpgroup.  `vref`: the power of two that value
-// scales are taken relative to (0 at first).
+// scales are taken relative to (0 at first), `vinv` its inverse.
+//
+// The weights are taken relative to the references as they are.  If one then turns out to
+// exceed its reference by kGap the maxima are looked for, the references moved, and the tile's
+// weights taken back and computed anew (a weight cut off at 2^kTop loses nothing: relative to the
+// new reference the sum it was added to is below 2^-kTop).  An item's first tile starts there.
 __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* qf, const Token& tk, int nc, uint32_t tS,
-                                             uint32_t tO, unsigned char* ptile, int done_bar, int step, bool first,
+                                             uint32_t tO, unsigned char* ptile, bool one_p, int c0, int step, bool first,
                                              float& vref, float& vinv, Sums& l) {
-  // (`done_bar`: products done, by the step's parity; `ptile`: this step's of the two)
+  // (`ptile`: this step's P, 64 rows of 128 tokens after another, the only one with `one_p`; `c0`:
+  // the warpgroup's first chunk of 16 rows in it)
   const int t = 32 * tk.warp + tk.lane;
-  // does a score, or the value scale, exceed its reference?
+  auto row = [&](int c) { return reinterpret_cast<uint4*>(ptile + ((c0 + c) >> 2) * (kBN * 128) + t * 128); };
+  if (one_p && step > 0) (void)wait_warp(st, kODone + ((step - 1) & 1), uint32_t((step - 1) >> 1) & 1u);
   const float av = fabsf(tk.vs);
-  bool move = tk.valid && av > 16.f * vref && av < INFINITY;
+  float vn = tk.valid ? tk.vs * vinv : 0.f;
+  if (!first) {
+    float over = -INFINITY;
+    // (a value scale that is no number, and rows that must not meet it: the other way)
+    bool move = (tk.valid && av > 16.f * vref && av < INFINITY) || (tk.cut && !(fabsf(vn) <= 3.4e38f));
+#pragma unroll 1
+    for (int c = 0; c < nc; ++c) {
+      uint32_t w[16];
+      uint64_t pw[8];
+      ld16(tS + 16 * c, w);
+      over = fmaxf(over, exponentials(w, qf + 16 * c, rw.lift + 16 * c, tk.ks, pw));
+      store_weights<false>(pw, vn, 0u, row(c), (c0 + c) & 3, t & 7);
+      l.chunk(c, [&](uint64_t (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = add2(x[i], pw[i]);
+      });
+    }
+    if (!group_any(tk.id, move || over > kGap)) return;
+  }
+  // the tile's maxima, row by row, and the new references
+  const float wv = i8::warp_max(tk.valid && av < INFINITY ? av : 0.f);
+  if (tk.lane == 0) rw.vpart[tk.warp] = wv;
+  float valpha = 1.f;
+#pragma unroll 1
+  for (int c = 0; c < nc; ++c) {
+    float x[16];
+    {
+      uint32_t w[16];
+      float f[16];
+      ld16(tS + 16 * c, w);
+      lds16(qf + 16 * c, f);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(w[i]) * tk.ks * f[i];
+    }
+    const float mx = reduce_rows<true>(tk.id, tk.warp, tk.lane, x, rw.part);
+    if (c == 0) {  // (vpart is complete behind the barrier in there)
+      const float top = fmaxf(fmaxf(rw.vpart[0], rw.vpart[1]), fmaxf(rw.vpart[2], rw.vpart[3]));
+      if (top > 16.f * vref) {
+        const float ref = i8::power_above(top);
+        valpha = vref / ref;  // (both powers of two, or 0)
+        vref = ref;
+        vinv = 1.f / ref;
+        vn = tk.valid ? tk.vs * vinv : 0.f;
+      }
+    }
+    if (tk.warp == 0 && !(tk.lane & 1)) {
+      const int r = 16 * c + (tk.lane >> 1);
+      const float m = rw.m[r];
+      const bool go = mx > m + kGap || (m == -INFINITY && mx > -INFINITY);
+      const float m2 = go ? mx : m;
+      const float a = go ? fast_exp2(m - m2) : 1.f;  // (0 from -infinity)
+      rw.m[r] = m2;
+      rw.old[r] = first ? -INFINITY : rw.lift[r];
+      rw.lift[r] = m2 == -INFINITY ? kNoLift : -m2;
+      rw.alpha_l[r] = a;
+      rw.alpha_o[r] = a * valpha;
+    }
+    group_sync(tk.id);
+  }
+  if (!first) {
+    // O^T has to hold the tiles before this one
+    (void)wait_warp(st, kODone + ((step - 1) & 1), uint32_t((step - 1) >> 1) & 1u);
+    tc::fence_after();
+  }
 #pragma unroll 1
   for (int c = 0; c < nc; ++c) {
     uint32_t w[16];
-    ld16(tS + 16 * c, w);
-    const uint64_t ks2 = pack2(tk.ks, tk.ks);
-    float over = -INFINITY;  // (fmaxf passes a NaN by)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const ulonglong2 d = reinterpret_cast<const ulonglong2*>(rw.drop + 16 * c)[i];
-      const float2 x = unpack2(fma2(pack2(__uint_as_float(w[4 * i]), __uint_as_float(w[4 * i + 1])), ks2, d.x));
-      const float2 y = unpack2(fma2(pack2(__uint_as_float(w[4 * i + 2]), __uint_as_float(w[4 * i + 3])), ks2, d.y));
-      over = fmaxf(over, fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y)));
-    }
-    move |= over > 0.f;
-  }
-  const bool any = group_any(tk.id, move);
-  // (the product of the step before last has to be done before its P is written again)
-  if (step > 1) (void)wait_warp(st, done_bar + (step & 1), uint32_t((step >> 1) - 1) & 1u);
-  if (any) {
-    // the tile's maxima, row by row, and the new references
-    const float wv = i8::warp_max(tk.valid && av < INFINITY ? av : 0.f);
-    if (tk.lane == 0) rw.vpart[tk.warp] = wv;
-    float valpha = 1.f;
-#pragma unroll 1
-    for (int c = 0; c < nc; ++c) {
-      float x[16];
-      {
-        uint32_t w[16];
-        float f[16];
-        ld16(tS + 16 * c, w);
-        lds16(qf + 16 * c, f);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(w[i]) * tk.ks * f[i];
-      }
-      const float mx = reduce_rows<true>(tk.id, t, x, reinterpret_cast<float*>(ptile) + (c & 1) * 16 * kBN);
-      if (c == 0) {  // (vpart is complete behind the barrier in there)
-        const float top = fmaxf(fmaxf(rw.vpart[0], rw.vpart[1]), fmaxf(rw.vpart[2], rw.vpart[3]));
-        if (top > 16.f * vref) {
-          const float ref = i8::power_above(top);
-          valpha = vref / ref;  // (both powers of two, or 0)
-          vref = ref;
-          vinv = 1.f / ref;
-        }
-      }
-      if ((t & 7) == 0) {
-        const int r = 16 * c + (t >> 3);
-        const float m = rw.m[r];
-        const bool go = mx > m + kGap || (m == -INFINITY && mx > -INFINITY);
-        const float m2 = go ? mx : m;
-        const float a = go ? fast_exp2(m - m2) : 1.f;  // (0 from -infinity)
-        rw.m[r] = m2;
-        rw.drop[r] = -(m2 + kGap) / qf[r];  // (a row's factor is above zero)
-        rw.lift[r] = m2 == -INFINITY ? 0.f : -m2;
-        rw.alpha_l[r] = a;
-        rw.alpha_o[r] = a * valpha;
-      }
-    }
-    group_sync(tk.id);
-    if (!first) {
-      // O^T has to hold the tiles before this one
-      (void)wait_warp(st, done_bar + ((step - 1) & 1), uint32_t((step - 1) >> 1) & 1u);
-      tc::fence_after();
-#pragma unroll 1
-      for (int c = 0; c < nc; ++c) {
-        uint32_t w[16];
-        float a[16];
-        lds16(rw.alpha_l + 16 * c, a);
-        l.chunk(c, [&](uint64_t (&x)[8]) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = mul2(x[i], pack2(a[2 * i], a[2 * i + 1]));
-        });
-        ld16(tO + 16 * c, w);
-        lds16(rw.alpha_o + 16 * c, a);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * a[i]);
-        tc::st16(tO + 16 * c, w);
-      }
-      tc::wait_st();
-    }
-  }
-  // the weights
-  const float vn = tk.valid ? tk.vs * vinv : 0.f;
-  // (a value scale that is no number, and rows that must not meet it)
-  const bool odd = tk.cut && __any_sync(0xffffffffu, !(fabsf(vn) <= 3.4e38f));
-  uint4* row = reinterpret_cast<uint4*>(ptile + t * 128);
-#pragma unroll 1
-  for (int c = 0; c < nc; ++c) {
     uint64_t pw[8];
-    if (odd)
-      weights<true>(tS + 16 * c, qf + 16 * c, rw.lift + 16 * c, tk.ks, vn, uint32_t(tk.keep >> (16 * c)), pw, row, c, t & 7);
-    else
-      weights<false>(tS + 16 * c, qf + 16 * c, rw.lift + 16 * c, tk.ks, vn, 0u, pw, row, c, t & 7);
+    ld16(tS + 16 * c, w);
+    (void)exponentials(w, qf + 16 * c, rw.old + 16 * c, tk.ks, pw);
+    const uint64_t minus = pack2(-1.f, -1.f);
     l.chunk(c, [&](uint64_t (&x)[8]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = add2(x[i], pw[i]);
+      for (int i = 0; i < 8; ++i) x[i] = fma2(pw[i], minus, x[i]);
     });
+    ld16(tS + 16 * c, w);
+    (void)exponentials(w, qf + 16 * c, rw.lift + 16 * c, tk.ks, pw);
+    l.chunk(c, [&](uint64_t (&x)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = fma2(x[i], reinterpret_cast<const uint64_t*>(rw.alpha_l + 16 * c)[i], pw[i]);
+    });
+    if (tk.cut)
+      store_weights<true>(pw, vn, uint32_t(tk.keep >> (16 * c)), row(c), (c0 + c) & 3, t & 7);
+    else
+      store_weights<false>(pw, vn, 0u, row(c), (c0 + c) & 3, t & 7);
+    if (first) continue;
+    ld16(tO + 16 * c, w);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * rw.alpha_o[16 * c + i]);
+    tc::st16(tO + 16 * c, w);
+  }
+  tc::wait_st();
+}
+
+// A warpgroup's query rows of an item (row0 .. row0 + half - 1) to f16, each scaled by a power
+// of two of its own, and their score factors to `qf`.  `div`: 2^16 / group, rounded up.
+template <int D>
+__device__ __forceinline__ void load_queries(const TreeParams& p, const TreeSplit& sp, const Walk& it, const ItemRows& ir,
+                                             int row0, unsigned char* q, uint32_t q_unit, float* qf, int warp, int lane,
+                                             int div) {
+  constexpr int kLanes = D / 8, kPer = 32 / kLanes, kBatch = 4;  // lanes of a row, rows of a pass, passes
+  const int sub = lane / kLanes, col = (lane % kLanes) * 8, g = p.group;
+  const int64_t tok0 = it.q.e.q0 + it.pair * sp.item_nodes;
+#pragma unroll 1
+  for (int i0 = warp * kBatch * kPer; i0 < ir.half; i0 += 4 * kBatch * kPer) {
+    uint4 x[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int r = row0 + i0 + u * kPer + sub;
+      x[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < ir.rows) {
+        const int node = (r * div) >> 16, h = r - node * g;  // (r < 256: exact)
+        x[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.query) + (tok0 + node) * p.q_stride_t +
+                                               int64_t(it.kvh * g + h) * p.q_stride_h + col);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * kPer + sub, r = row0 + i;
+      float f[8];
+      Chunk<BF16>::expand(x[u], f);
+      float top = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+#pragma unroll
+      for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int sh = i8::query_shift(top);
+      const float s = i8::power(sh), inv = i8::power(-sh);
+      if (i < ir.half) {
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half2 v = __floats2half2_rn(f[2 * e] * s, f[2 * e + 1] * s);
+          h[e] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        *reinterpret_cast<uint4*>(q + (col >> 6) * q_unit + r * 128 + (((col >> 3) & 7) ^ (r & 7)) * 16) =
+            make_uint4(h[0], h[1], h[2], h[3]);
+        if (col == 0) qf[i] = p.qk_scale_log2 * inv;
+      }
+    }
   }
 }
 
-// Writes the rows' output, or the part of it, from O^T (lane = column of the head): through
-// shared memory, so that a warp writes whole rows.  `ptile` is free.
+// What write_rows needs of an item's part.
+struct Part {
+  int rows, tok0, kvh;  // query rows, their first node's, KV head
+  bool whole, begins;
+};
+
+// Writes the rows' output, or the part of it, from O^T (lane = column of the head): a warp writes
+// 32 columns of a row at a time.
 template <int D>
-__device__ __forceinline__ void write_rows(const TreeParams& p, const TreeSplit& sp, const Walk& it, const ItemRows& ir,
-                                           Rows& rw, int id, int wg, int warp, int lane, int nc, uint32_t tO, float vref,
-                                           unsigned char* ptile, Sums& l) {
-  const int row0 = wg * ir.half, t = 32 * warp + lane;
-  const bool whole = it.begins() && it.ends();
-  const int64_t prow = int64_t(2 * blockIdx.x + (it.begins() ? 1 : 0)) * sp.rows + row0;
-  const int64_t tok0 = it.q.e.q0 + it.pair * sp.item_nodes;
-  float* sums = reinterpret_cast<float*>(ptile);
-  float* vals = sums + 16 * kBN;
+__device__ __forceinline__ void write_rows(const TreeParams& p, const TreeSplit& sp, const Part& pt, Rows& rw, int id,
+                                           int row0, int warp, int lane, int nc, uint32_t tO, float vref, int div, Sums& l) {
+  const int64_t prow = int64_t(2 * blockIdx.x + (pt.begins ? 1 : 0)) * sp.rows;
+  const int col = 32 * warp + lane;
 #pragma unroll 1
   for (int c = 0; c < nc; ++c) {
     float x[16];
@@ -441,45 +514,29 @@ __device__ __forceinline__ void write_rows(const TreeParams& p, const TreeSplit&
         x[2 * i + 1] = v.y;
       }
     });
+    const float sum = reduce_rows<false>(id, warp, lane, x, rw.part);
+    if (warp == 0 && !(lane & 1)) {
+      const int i = 16 * c + (lane >> 1), r = row0 + i;
+      rw.alpha_o[i] = pt.whole ? (sum != 0.f ? vref / sum : 0.f) : vref;
+      if (!pt.whole && r < pt.rows) sp.ml[prow + r] = make_float2(rw.m[i], sum);
+    }
+    group_sync(id);
     uint32_t w[16];
     ld16(tO + 16 * c, w);
+    if (col >= D) continue;  // (64 columns: the upper lanes of the accumulator repeat them)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) vals[i * kBN + t] = __uint_as_float(w[i]);
-    const float sum = reduce_rows<false>(id, t, x, sums);
-    if ((t & 7) == 0) {
-      const int r = 16 * c + (t >> 3);
-      rw.alpha_o[r] = whole ? (sum != 0.f ? vref / sum : 0.f) : vref;
-      if (!whole && row0 + r < ir.rows) sp.ml[prow + r] = make_float2(rw.m[r], sum);
-    }
-    group_sync(id);
-    const int n = min(16, ir.rows - row0 - 16 * c);
-    if (D == 128 || lane < 16) {  // (64 columns: the upper lanes of the accumulator repeat them)
-#pragma unroll 1
-      for (int i = warp; i < n; i += 4) {
-        const int r = row0 + 16 * c + i;
-        const float a = rw.alpha_o[16 * c + i];
-        float4 v = reinterpret_cast<const float4*>(vals + i * kBN)[lane];
-        v = make_float4(v.x * a, v.y * a, v.z * a, v.w * a);
-        if (whole) {
-          const int node = r / p.group, h = r - node * p.group;
-          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (tok0 + node) * p.out_stride_t +
-                               int64_t(it.kvh * p.group + h) * p.out_stride_h + 4 * lane;
-          const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
-          if (sp.out_vec) {
-            *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                                        *reinterpret_cast<const uint32_t*>(&hi));
-          } else {
-            out[0] = lo.x;
-            out[1] = lo.y;
-            out[2] = hi.x;
-            out[3] = hi.y;
-          }
-        } else {
-          *reinterpret_cast<float4*>(sp.o + (prow + 16 * c + i) * D + 4 * lane) = v;
-        }
+    for (int i = 0; i < 16; ++i) {
+      const int r = row0 + 16 * c + i;
+      if (r >= pt.rows) break;
+      const float v = __uint_as_float(w[i]) * rw.alpha_o[16 * c + i];
+      if (pt.whole) {
+        const int node = (r * div) >> 16, h = r - node * p.group;
+        static_cast<__nv_bfloat16*>(p.out)[int64_t(pt.tok0 + node) * p.out_stride_t +
+                                           int64_t(pt.kvh * p.group + h) * p.out_stride_h + col] = __float2bfloat16_rn(v);
+      } else {
+        sp.o[(prow + r) * D + col] = v;
       }
     }
-    group_sync(id);
   }
 }
 
@@ -497,10 +554,10 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
     for (int i = 0; i < kNumBars; ++i) {
       // one arrival per warp where a warpgroup arrives
       const bool warps4 = (i >= kCodeEmpty && i < kCodeEmpty + kMaxSlots) || (i >= kKFull && i < kKFull + 2) ||
-                          (i >= kVFull && i < kVFull + 2) || (i >= kPFull && i < kPFull + 4) ||
-                          (i >= kOFree && i < kOFree + 4) || (i >= kSFree && i < kSFree + 4);
+                          (i >= kVFull && i < kVFull + 2);
+      const bool warps8 = i == kQFull || (i >= kPFull && i < kPFull + 2) || (i >= kOFree && i < kOFree + 2);
       const bool lanes = i >= kScaleFull && i < kScaleFull + kScaleSlots;  // (each lane's copies)
-      mbar_init(&st->bars[i], lanes ? 32 : warps4 ? 4 : 1);
+      mbar_init(&st->bars[i], lanes ? 32 : warps8 ? 8 : warps4 ? 4 : 1);
     }
     st->abort = 0;
     fence_barrier_init();
@@ -517,18 +574,24 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
   Walk it;
   it.start(p, sp, rg);
   // the layout behind the widened tiles
-  const int q_rows = many ? kHalfRows : kFewRows, groups = many ? 2 : 1;  // of Q, per warpgroup
-  const uint32_t q_half = uint32_t(q_rows) * 128, q_group = q_half * C::kUnits;
-  const uint32_t oP = C::kQ + groups * q_group, oCodes = oP + 2 * groups * C::kPBytes;
-  const int slots = min(kMaxSlots, int((C::kState - oCodes) / C::kCodeBytes));  // (K and V in turn, odd or even)
+  const int q_rows = many ? 2 * kHalfRows : kFewRows, groups = many ? 2 : 1;  // rows of Q, warpgroups in use
+  const uint32_t q_unit = uint32_t(q_rows) * 128, p_step = groups * C::kPBytes;
+  const uint32_t oP = C::kQ + C::kUnits * q_unit, oCodes = oP + (many ? 1 : 2) * p_step;
+  const int p_odd = many ? 0 : 1;  // (few rows: two P tiles)
+  // (an even number: a loader and the widening warps it feeds have slots of their own, and see
+  // every phase of their barriers)
+  const int slots = min(kMaxSlots, int((C::kState - oCodes) / C::kCodeBytes)) & ~1;
 
   // (each role takes its registers itself: the compiler counts them by branch)
-  if (warp == 0) {
+  if (warp == 0 || warp == 3) {
     less_registers<kRegsControl>();
-    // ---- codes: K then V of every tile, one bulk copy per block of the cache ----------------
-    const int bs = p.block_size;
+    // ---- codes, K by one warp and V by another, every second tile of the ring each: one bulk copy
+    // per block of the cache (copies issued side by side from one warp go one by one, about 100
+    // clocks each).  The first also copies the tokens' scales, four tokens to a lane ------------
+    const int v = warp == 3, bs = p.block_size;
+    const unsigned char* cache = static_cast<const unsigned char*>(v ? p.value_cache : p.key_cache);
     const uint32_t bytes = uint32_t(bs) * D;
-    int slot = 0, n = 0;
+    int slot = v, n = v;  // of the ring: tile and tile copies before this one
     uint32_t phase = 0;
     // tile j of `it` is looked up one tile before its copies are issued, over items too (up to
     // 64 blocks of two tokens: two to a lane)
@@ -564,67 +627,64 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
           raise_device_error(p.err, kErrTableEntry);
           now[u] = 0;
         }
-      // the tokens' scales: a bulk copy per block with the K codes, where they are aligned for
-      // it; else asynchronous 4-byte copies, four tokens to a lane (their block's entry is in lane
-      // token / bs, the upper 32 blocks of two tokens in the second register)
-      if (tiles >= kScaleSlots) (void)wait_warp(st, kScaleEmpty + sslot, sphase ^ 1u);
-      const int sslot_now = sslot;
-      if (!sp.bulk_scales) {
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          const int b = (4 * lane + i) >> sp.bs_shift;
-          const int ea = __shfl_sync(0xffffffffu, now[0], b & 31), eb = __shfl_sync(0xffffffffu, now[1], b & 31);
-          const bool there = 4 * lane + i < left_now;
-          const int64_t at = there ? int64_t(b < 32 ? ea : eb) * p.ts_block + int64_t(kvh_now) * p.ts_head +
-                                         ((4 * lane + i) & (bs - 1))
-                                   : 0;
-          copy4(&st->scales[sslot][0][4 * lane + i], p.k_token_scales + at, there);
-          copy4(&st->scales[sslot][1][4 * lane + i], p.v_token_scales + at, there);
-        }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_addr(&st->bars[kScaleFull + sslot]))
-                     : "memory");
-      }
-      ++tiles;
-      if (++sslot == kScaleSlots) {
-        sslot = 0;
-        sphase ^= 1u;
-      }
-#pragma unroll 1
-      for (int v = 0; v < 2; ++v) {
-        bool ok = true;
-        if (lane == 0 && n >= slots) ok = wait(st, kCodeEmpty + slot, phase ^ 1u);
-        ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
-        if (!ok) continue;
-        const bool with_scales = v == 0 && sp.bulk_scales;
-        if (lane == 0)
-          mbar_arrive_expect_tx(&st->bars[kCodeFull + slot], uint32_t(nblk_now) * (bytes + (with_scales ? 8 * bs : 0)));
+      bool ok = true;
+      if (n >= slots) ok = wait_warp(st, kCodeEmpty + slot, phase ^ 1u);
+      if (ok) {
+        if (lane == 0) mbar_arrive_expect_tx(&st->bars[kCodeFull + slot], uint32_t(nblk_now) * bytes);
         __syncwarp();
-        if (with_scales && lane < nblk_now) {  // (at most 32 blocks, of four tokens and more)
-          const int64_t at = int64_t(now[0]) * p.ts_block + int64_t(kvh_now) * p.ts_head;
-          bulk_copy_g2s(&st->scales[sslot_now][0][lane * bs], p.k_token_scales + at, 4 * bs, &st->bars[kCodeFull + slot]);
-          bulk_copy_g2s(&st->scales[sslot_now][1][lane * bs], p.v_token_scales + at, 4 * bs, &st->bars[kCodeFull + slot]);
-        }
-        const unsigned char* src = static_cast<const unsigned char*>(v ? p.value_cache : p.key_cache);
         unsigned char* dst = smem + oCodes + slot * C::kCodeBytes;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int b = lane + 32 * u;
           if (b < nblk_now)
-            bulk_copy_g2s(dst + b * bytes, src + int64_t(now[u]) * p.cs_block + int64_t(kvh_now) * p.cs_head, bytes,
+            bulk_copy_g2s(dst + b * bytes, cache + int64_t(now[u]) * p.cs_block + int64_t(kvh_now) * p.cs_head, bytes,
                           &st->bars[kCodeFull + slot]);
         }
-        ++n;
-        if (++slot == slots) {
-          slot = 0;
-          phase ^= 1u;
+      }
+      n += 2;
+      slot += 2;
+      if (slot >= slots) {
+        slot -= slots;
+        phase ^= 1u;
+      }
+      if (v) continue;
+      // the tokens' scales: asynchronous copies of four tokens' 16 bytes where they are aligned
+      // (their block's entry is in lane token / bs), else of each (the upper 32 blocks of two
+      // tokens in the second register)
+      if (tiles >= kScaleSlots) (void)wait_warp(st, kScaleEmpty + sslot, sphase ^ 1u);
+      float* kd = &st->scales[sslot][0][4 * lane];
+      float* vd = &st->scales[sslot][1][4 * lane];
+      const int64_t head = int64_t(kvh_now) * p.ts_head;
+      if (sp.vec_scales) {
+        const int e = __shfl_sync(0xffffffffu, now[0], (4 * lane) >> sp.bs_shift);
+        const bool there = 4 * lane < left_now;
+        const int64_t at = there ? int64_t(e) * p.ts_block + head + ((4 * lane) & (bs - 1)) : 0;
+        copy16(kd, p.k_token_scales + at, there);
+        copy16(vd, p.v_token_scales + at, there);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+          const int b = (4 * lane + i) >> sp.bs_shift;
+          const int ea = __shfl_sync(0xffffffffu, now[0], b & 31), eb = __shfl_sync(0xffffffffu, now[1], b & 31);
+          const bool there = 4 * lane + i < left_now;
+          const int64_t at = there ? int64_t(b < 32 ? ea : eb) * p.ts_block + head + ((4 * lane + i) & (bs - 1)) : 0;
+          copy4(kd + i, p.k_token_scales + at, there);
+          copy4(vd + i, p.v_token_scales + at, there);
         }
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_addr(&st->bars[kScaleFull + sslot]))
+                   : "memory");
+      ++tiles;
+      if (++sslot == kScaleSlots) {
+        sslot = 0;
+        sphase ^= 1u;
       }
     }
     // the copies in flight land before the block may exit
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (lane == 0)
       for (int k = max(0, n - slots); k < n; ++k)
-        (void)mbar_wait_bounded(&st->bars[kCodeFull + k % slots], uint32_t(k / slots) & 1u);
+        if ((k & 1) == v) (void)mbar_wait_bounded(&st->bars[kCodeFull + k % slots], uint32_t(k / slots) & 1u);
   } else if (warp == 1) {
     less_registers<kRegsControl>();
     // ---- score MMAs (a warp, see umma.cuh; the products' are another's: each waits only for its own) ----
@@ -632,39 +692,28 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
       const uint32_t base = smem_addr(smem);
       constexpr uint64_t kUnit = C::kUnitBytes >> 4;  // (descriptors hold addresses / 16)
       const uint64_t kdesc = tc::desc_sw128(base + C::kK, 16, 1024), qdesc = tc::desc_sw128(base + C::kQ, 16, 1024);
-      int kn = 0, item = 0, n0 = 0, n1 = 0;  // units of K, items, steps of the warpgroups
+      int kn = 0, item = 0, n = 0;  // units of K, items, steps
       bool ok = true;
       for (; ok && it.valid(); it.next(p, sp, rg), ++item) {
         const ItemRows ir(p, sp, it);
-        const uint32_t id = idesc_f16(kBN, ir.half, 0, 0);
-        for (int j = it.j0; ok && j < it.j1; ++j) {
+        const uint32_t id = idesc_f16(kBN, ir.groups * ir.half, 0, 0);
+        for (int j = it.j0; ok && j < it.j1; ++j, ++n) {
           if (j == it.j0) ok = wait_warp(st, kQFull, uint32_t(item) & 1u);
-          if (n0 >= 2) ok = ok && wait_warp(st, kSFree + (n0 & 1), uint32_t((n0 >> 1) - 1) & 1u);
-          if (ir.groups == 2 && n1 >= 2) ok = ok && wait_warp(st, kSFree + 2 + (n1 & 1), uint32_t((n1 >> 1) - 1) & 1u);
-          const uint32_t t0 = tmem + C::kS + (n0 & 1) * 64, t1 = tmem + C::kS + 128 + (n1 & 1) * 64;
+          // S^T and P of the step before last are free when its product is done (so the softmax
+          // warps need not wait for that)
+          if (n >= 2) ok = ok && wait_warp(st, kODone + (n & 1), uint32_t((n >> 1) - 1) & 1u);
+          const uint32_t to = tmem + C::kS + (n & 1) * 128;
 #pragma unroll 1
           for (int u = 0; ok && u < C::kUnits; ++u, ++kn) {
             if (!(ok = wait_warp(st, kKFull + (kn & 1), uint32_t(kn >> 1) & 1u))) break;
             tc::fence_after();
-            const uint64_t kd = kdesc + (kn & 1) * kUnit, qd = qdesc + ((u * q_half) >> 4);
+            const uint64_t kd = kdesc + (kn & 1) * kUnit, qd = qdesc + ((u * q_unit) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) umma::mma_ss(t0, kd + kk * 2, qd + kk * 2, id, (u > 0 || kk > 0) ? 1u : 0u);
-            if (ir.groups == 2) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                umma::mma_ss(t1, kd + kk * 2, qd + (q_group >> 4) + kk * 2, id, (u > 0 || kk > 0) ? 1u : 0u);
-            }
+            for (int kk = 0; kk < 4; ++kk) umma::mma_ss(to, kd + kk * 2, qd + kk * 2, id, (u > 0 || kk > 0) ? 1u : 0u);
             umma::commit(&st->bars[kKEmpty + (kn & 1)]);
           }
-          if (!ok) break;
-          umma::commit(&st->bars[kSFull + (n0 & 1)]);
-          ++n0;
-          if (ir.groups == 2) {
-            umma::commit(&st->bars[kSFull + 2 + (n1 & 1)]);
-            ++n1;
-          }
+          if (ok) umma::commit(&st->bars[kSFull + (n & 1)]);
         }
-        if (ok) umma::commit(&st->bars[kQEmpty]);
       }
       // every MMA issued has completed before the tensor memory is freed
       umma::commit(&st->bars[kDrain]);
@@ -679,116 +728,50 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
       constexpr uint64_t kUnit = C::kUnitBytes >> 4;
       // (a head of 64 columns has one chunk of them: the second 64 rows of the MMA repeat it)
       const uint64_t vdesc = tc::desc_sw128(base + C::kV, D == 128 ? C::kVHalf : 0, 1024);
-      const uint64_t pdesc = tc::desc_sw128(base + oP, 16, 1024);
+      const uint64_t pdesc = tc::desc_sw128(base + oP, C::kPBytes, 1024);
       int vn = 0, sslot = 0;  // units of V, the tile's slot of scales
-      int n0 = 0, n1 = 0, use0 = 0, use1 = 0;  // the warpgroups' steps and items
+      int n = 0, item = 0;  // steps, items
+      int64_t at = rg->from;
+      TreeSplit::Tail tail = {0, 0, 0, 0};  // what the fold needs of an item that goes on in the next range
       bool ok = true;
-      for (; ok && it.valid(); it.next(p, sp, rg)) {
+      for (; ok && it.valid(); it.next(p, sp, rg), ++item) {
+        if (it.begins() && !it.ends()) {
+          const int node0 = it.pair * sp.item_nodes;
+          tail.row0 = it.q.e.q0 + node0;
+          tail.nodes = min(sp.item_nodes, it.q.e.n - node0);
+          tail.kvh = it.kvh;
+          tail.last = int((at - it.u0 + it.q.tiles + rg->cost - 1) / rg->share);
+        }
+        at += it.u1 - it.u0;
         const ItemRows ir(p, sp, it);
-        const uint32_t id = idesc_f16(128, ir.half, 1, 1);
+        const uint32_t id = idesc_f16(128, ir.groups * ir.half, 1, 1);
         // (an O^T buffer is written again when the item before last has been written out)
-        if (use0 >= 2) ok = wait_warp(st, kOFree + (use0 & 1), uint32_t((use0 >> 1) - 1) & 1u);
-        if (ir.groups == 2 && use1 >= 2) ok = ok && wait_warp(st, kOFree + 2 + (use1 & 1), uint32_t((use1 >> 1) - 1) & 1u);
-        for (int j = it.j0; ok && j < it.j1; ++j) {
+        if (item >= 2) ok = wait_warp(st, kOFree + (item & 1), uint32_t((item >> 1) - 1) & 1u);
+        const uint32_t to = tmem + C::kO + (item & 1) * 128;
+        for (int j = it.j0; ok && j < it.j1; ++j, ++n) {
+          ok = wait_warp(st, kPFull + (n & 1), uint32_t(n >> 1) & 1u);
 #pragma unroll 1
-          for (int u = 0; u < C::kUnits; ++u, ++vn) {
-            const uint64_t vd = vdesc + (vn & 1) * kUnit;
+          for (int u = 0; ok && u < C::kUnits; ++u, ++vn) {
+            if (!(ok = wait_warp(st, kVFull + (vn & 1), uint32_t(vn >> 1) & 1u))) break;
+            tc::fence_after();
+            const uint64_t vd = vdesc + (vn & 1) * kUnit, pb = pdesc + (((n & p_odd) * p_step + u * C::kVTokens * 128) >> 4);
             const uint32_t acc = j > it.j0 || u > 0;
-            ok = wait_warp(st, kVFull + (vn & 1), uint32_t(vn >> 1) & 1u);
-#pragma unroll 1
-            for (int w = 0; w < ir.groups; ++w) {
-              const int n = w ? n1 : n0;
-              if (u == 0) ok = ok && wait_warp(st, kPFull + 2 * w + (n & 1), uint32_t(n >> 1) & 1u);
-              if (!ok) break;
-              tc::fence_after();
-              const uint32_t to = tmem + C::kO + ((w ? use1 : use0) & 1) * 128 + w * 64;
-              const uint64_t pb = pdesc + (((2 * w + (n & 1)) * C::kPBytes + u * C::kVTokens * 128) >> 4);
 #pragma unroll
-              for (int kk = 0; kk < C::kVTokens / 16; ++kk)
-                umma::mma_ss(to, vd + kk * (16 * 128 >> 4), pb + kk * (16 * 128 >> 4), id, acc | (kk > 0));
-              if (u == C::kUnits - 1) umma::commit(&st->bars[kODone + 2 * w + (n & 1)]);
-            }
-            if (!ok) break;
+            for (int kk = 0; kk < C::kVTokens / 16; ++kk)
+              umma::mma_ss(to, vd + kk * (16 * 128 >> 4), pb + kk * (16 * 128 >> 4), id, acc | (kk > 0));
             umma::commit(&st->bars[kVEmpty + (vn & 1)]);
           }
           if (!ok) break;
+          umma::commit(&st->bars[kODone + (n & 1)]);
           umma::commit(&st->bars[kScaleEmpty + sslot]);  // (P, so the scales, have been used)
           if (++sslot == kScaleSlots) sslot = 0;
-          ++n0;
-          if (ir.groups == 2) ++n1;
         }
-        ++use0;
-        if (ir.groups == 2) ++use1;
       }
+      if (lane == 0) sp.tails[blockIdx.x] = tail;
       umma::commit(&st->bars[kDrain + 1]);
       (void)mbar_wait_bounded(&st->bars[kDrain + 1], 0);
       if (!ok && lane == 0) raise_device_error(p.err, kErrTimeout);
     }
-  } else if (warp == 3) {
-    less_registers<kRegsControl>();
-    // ---- queries: an item's rows to f16, each scaled by a power of two of its own; and what
-    // the fold needs of an item that goes on in the next block's range ------------------------
-    constexpr int kLanes = D / 8, kPer = 32 / kLanes;  // lanes of a row, rows of a pass
-    const int sub = lane / kLanes, col = (lane % kLanes) * 8;
-    int item = 0;
-    int64_t at = rg->from;
-    TreeSplit::Tail tail = {0, 0, 0, 0};
-    for (; it.valid(); it.next(p, sp, rg), ++item) {
-      const ItemRows ir(p, sp, it);
-      const int node0 = it.pair * sp.item_nodes;
-      const int64_t tok0 = it.q.e.q0 + node0;
-      if (item > 0) (void)wait_warp(st, kQEmpty, uint32_t(item - 1) & 1u);
-      constexpr int kBatch = 8;
-      for (int r0 = 0; r0 < ir.groups * ir.half; r0 += kBatch * kPer) {
-        uint4 x[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int r = r0 + u * kPer + sub;
-          x[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < ir.rows) {
-            const int node = r / g, h = r - node * g;
-            x[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.query) + (tok0 + node) * p.q_stride_t +
-                                                   int64_t(it.kvh * g + h) * p.q_stride_h + col);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-          const int r = r0 + u * kPer + sub;
-          float f[8];
-          Chunk<BF16>::expand(x[u], f);
-          float top = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const int sh = i8::query_shift(top);
-          const float s = i8::power(sh), inv = i8::power(-sh);
-          if (r < ir.groups * ir.half) {
-            uint32_t h[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const __half2 v = __floats2half2_rn(f[2 * i] * s, f[2 * i + 1] * s);
-              h[i] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            const int w = r >= ir.half, n = r - w * ir.half;
-            unsigned char* q = smem + C::kQ + w * q_group + (col >> 6) * q_half + n * 128;
-            *reinterpret_cast<uint4*>(q + (((col >> 3) & 7) ^ (n & 7)) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
-            if (col == 0) st->qf[item & 3][w][n] = p.qk_scale_log2 * inv;
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&st->bars[kQFull]);
-      if (it.begins() && !it.ends()) {
-        tail.row0 = int(tok0);
-        tail.nodes = min(sp.item_nodes, it.q.e.n - node0);
-        tail.kvh = it.kvh;
-        tail.last = int((at - it.u0 + it.q.tiles + rg->cost - 1) / rg->share);
-      }
-      at += it.u1 - it.u0;
-    }
-    if (lane == 0) sp.tails[blockIdx.x] = tail;
   } else if (warp >= 12) {
     less_registers<kRegsWiden>();
     // ---- widening: K by one warpgroup, V by the other, every second tile of the ring each -----
@@ -808,7 +791,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
     for (; it.valid(); it.next(p, sp, rg)) {
       for (int j = it.j0; j < it.j1; ++j) {
         (void)wait_warp(st, kCodeFull + slot, phase);
-        if (!v && !sp.bulk_scales) {
+        if (!v) {
           (void)wait_warp(st, kScaleFull + sslot, sphase);
           if (++sslot == kScaleSlots) {
             sslot = 0;
@@ -845,27 +828,35 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
     tk.id = 1 + wg;
     tk.warp = q;
     tk.lane = lane;
-    int item = 0, use = 0, step = 0, tile = 0;  // `step`: tiles of this warpgroup's; `tile`: all
+    const int div = (65535 + g) / g;
+    int item = 0, step = 0;
+    // (Q is free once the scores of the item's last tile are there)
+    auto queries = [&](const ItemRows& ir) {
+      if (wg < ir.groups)
+        load_queries<D>(p, sp, it, ir, wg * ir.half, smem + C::kQ, q_unit, st->qf[item & 1][wg], q, lane, div);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&st->bars[kQFull]);
+    };
+    if (it.valid()) queries(ItemRows(p, sp, it));
     while (it.valid()) {
       const ItemRows ir(p, sp, it);
-      if (wg < ir.groups) {
+      const int row0 = wg * ir.half, nc = wg < ir.groups ? ir.half >> 4 : 0, ob = item & 1;
+      {
         const Extent& e = it.q.e;
-        const int nc = ir.half >> 4, ob = use & 1;
-        const uint32_t tO = tmem + C::kO + ob * 128 + wg * 64 + lane_off;
-        const float* qf = st->qf[item & 3][wg];
-        unsigned char* pbuf = smem + oP + 2 * wg * C::kPBytes;
+        const uint32_t tO = tmem + C::kO + ob * 128 + row0 + lane_off;
+        const float* qf = st->qf[item & 1][wg];
         float vref = 0.f, vinv = 0.f;  // (and its inverse)
         Sums l;
 #pragma unroll
         for (int i = 0; i < kHalfRows / 2; ++i) l.a[i >> 3][i & 7] = 0ull;
         if (t < kHalfRows) {
           rw.m[t] = -INFINITY;
-          rw.drop[t] = INFINITY;
-          rw.lift[t] = 0.f;
+          rw.lift[t] = kNoLift;
         }
         group_sync(tk.id);
 #pragma unroll 1
-        for (int j = it.j0; j < it.j1; ++j, ++step, ++tile) {
+        for (int j = it.j0; j < it.j1; ++j, ++step) {
           const int pos = it.q.base + j * kBN + t;
           tk.valid = pos >= e.lo && pos < e.L;
           tk.cut = it.cut(j);
@@ -875,7 +866,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
               tk.keep = 0;
             } else if (p.tree_mask && pos >= e.P) {
               // the rows (node by node, g each) that see this node
-              const int c = pos - e.P, r0 = wg * ir.half;
+              const int c = pos - e.P, r0 = row0;
               tk.keep = 0;
               int node = r0 / g, h = r0 - node * g;
               const int64_t* mask = p.tree_mask + (e.q0 + it.pair * sp.item_nodes + node) * p.mask_stride;
@@ -891,38 +882,35 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
               }
             }
           }
-          (void)wait_warp(st, kSFull + 2 * wg + (step & 1), uint32_t(step >> 1) & 1u);
+          (void)wait_warp(st, kSFull + (step & 1), uint32_t(step >> 1) & 1u);
           tc::fence_after();
-          const int sl = tile % kScaleSlots;  // (the tile's scales are there: its K waited for them)
+          const int sl = step % kScaleSlots;  // (the tile's scales are there: its K waited for them)
           tk.ks = st->scales[sl][0][t];
           tk.vs = st->scales[sl][1][t];
-          const uint32_t tS = tmem + C::kS + wg * 128 + (step & 1) * 64 + lane_off;
+          const uint32_t tS = tmem + C::kS + (step & 1) * 128 + row0 + lane_off;
           if (tk.cut) {
             hide(tS, nc, tk.ks, tk.keep);
             tk.ks = 1.f;
           }
           const bool first = j == it.j0;
-          softmax_step(st, rw, qf, tk, nc, tS, tO, pbuf + (step & 1) * C::kPBytes, kODone + 2 * wg, step, first, vref, vinv, l);
+          if (nc > 0)
+            softmax_step(st, rw, qf, tk, nc, tS, tO, smem + oP + (step & p_odd) * p_step, p_odd == 0, row0 >> 4, step, first, vref, vinv, l);
           fence_proxy_async_smem();
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&st->bars[kPFull + 2 * wg + (step & 1)]);
-            mbar_arrive(&st->bars[kSFree + 2 * wg + (step & 1)]);
-          }
+          if (lane == 0) mbar_arrive(&st->bars[kPFull + (step & 1)]);
         }
-        (void)wait_warp(st, kODone + 2 * wg + ((step - 1) & 1), uint32_t((step - 1) >> 1) & 1u);
+        const Part pt = {ir.rows, e.q0 + it.pair * sp.item_nodes, it.kvh, it.begins() && it.ends(), it.begins()};
+        it.next(p, sp, rg);
+        ++item;
+        if (it.valid()) queries(ItemRows(p, sp, it));  // (the next item's scores, while this one is written)
+        (void)wait_warp(st, kODone + ((step - 1) & 1), uint32_t((step - 1) >> 1) & 1u);
         tc::fence_after();
-        write_rows<D>(p, sp, it, ir, rw, tk.id, wg, q, lane, nc, tO, vref, pbuf, l);
+        write_rows<D>(p, sp, pt, rw, tk.id, row0, q, lane, nc, tO, vref, div, l);
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&st->bars[kOFree + 2 * wg + ob]);
-        ++use;
-      } else {
-        tile += it.j1 - it.j0;
+        if (lane == 0) mbar_arrive(&st->bars[kOFree + ob]);
       }
-      it.next(p, sp, rg);
-      ++item;
     }
     if (lane == 0 && st->abort) raise_device_error(p.err, kErrTimeout);
   }
@@ -982,10 +970,9 @@ bool tree_i8_supported(const TreeParams& p) {
 
 cudaError_t launch_tree_i8(const TreeParams& p, TreeSplit sp, cudaStream_t stream) {
   sp.item_nodes = sp.tq;
-  sp.bulk_scales = p.block_size >= 4 && !((reinterpret_cast<uintptr_t>(p.k_token_scales) |
-                                           reinterpret_cast<uintptr_t>(p.v_token_scales)) & 15) &&
-                   !(p.ts_block & 3) && !(p.ts_head & 3);
-  sp.out_vec = (reinterpret_cast<uintptr_t>(p.out) & 7) == 0 && (p.out_stride_t & 3) == 0 && (p.out_stride_h & 3) == 0;
+  sp.vec_scales = p.block_size >= 4 && !((reinterpret_cast<uintptr_t>(p.k_token_scales) |
+                                          reinterpret_cast<uintptr_t>(p.v_token_scales)) & 15) &&
+                  !(p.ts_block & 3) && !(p.ts_head & 3);
   return p.head_dim == 128 ? launch_tree_i8_tpl<128>(p, sp, stream) : launch_tree_i8_tpl<64>(p, sp, stream);
 }
 
