@@ -73,13 +73,14 @@ struct Cfg {
 };
 
 // Barriers.  A wait names a phase by its parity, so its barrier may be at most one phase
-// away: those that a softmax warpgroup waits for count its own slot's steps (S: two per
-// slot, by the parity of the slot's step), since a warpgroup may wait for a step while the
-// other one is still several steps behind it.
+// away: those that a softmax warpgroup waits for (S, and the products' completion) count its
+// own slot's steps, two barriers a slot by the parity of the slot's step.  A warpgroup may wait
+// for a step while the other one is several steps behind it, and for the last product of an
+// item while the one before it is still held up by its V tile.
 constexpr int kMaxRing = 6;
 enum Bar { kQFull = 0, kQEmpty = 2, kKFull = 4, kKEmpty = kKFull + kMaxRing, kVFull = kKEmpty + kMaxRing,
            kVEmpty = kVFull + kMaxRing, kVRaw = kVEmpty + kMaxRing, kSFull = kVRaw + kMaxRing, kPFull = kSFull + 4,
-           kODone = kPFull + 2, kOFree = kODone + 2, kDrain = kOFree + 2, kNumBars = kDrain + 1 };
+           kODone = kPFull + 2, kOFree = kODone + 4, kDrain = kOFree + 2, kNumBars = kDrain + 1 };
 
 constexpr int kBadItems = 8;  // items whose bad rows are kept: the cleaning warp is up to a ring of
                               // V tiles and one item ahead of a warpgroup that writes its output
@@ -347,7 +348,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       const uint64_t vdesc = tc::desc_sw128(sv, C::kHalfBytes, 1024);
       // a step between its S and its P V: what the P V needs to know
       struct Pending {
-        bool slot, x, x_phase, first, last_tile, wait_o, o_phase, v_phase;
+        bool slot, odd, x, x_phase, first, last_tile, wait_o, o_phase, v_phase;
         uint8_t v;  // V slot
       };
       Pending pend[2];  // [step & 1] (constant indices below: registers)
@@ -377,7 +378,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
             const bool last_row_tile = qt == it.nt - 1;
             if (last_row_tile) umma::commit(&st->bars[kKEmpty + ks]);
             if (j == it.j1 - 1) umma::commit(&st->bars[kQEmpty + qs]);
-            const Pending pd = {slot != 0, (xs & 1) != 0, ((xs >> 1) & 1) != 0, j == it.j0, last_row_tile,
+            const Pending pd = {slot != 0, (n & 1) != 0, (xs & 1) != 0, ((xs >> 1) & 1) != 0, j == it.j0, last_row_tile,
                                 j == it.j0 && u > 0, ((u - 1) & 1) != 0, vp, uint8_t(vs)};
             if (xs & 1) pend[1] = pd; else pend[0] = pd;
             ++xs;
@@ -415,7 +416,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
 #pragma unroll
             for (int kk = 0; kk < kBN / 16; ++kk)
               umma::mma_ts(to, ts + 8 * kk, vd + kk * (16 * 128 >> 4), idO, (!pd.first || kk > 0) ? 1u : 0u);
-            umma::commit(&st->bars[kODone + pd.slot]);
+            umma::commit(&st->bars[kODone + 2 * pd.slot + pd.odd]);
             if (pd.last_tile) umma::commit(&st->bars[kVEmpty + pd.v]);
             ++xp;
             went = true;
@@ -549,7 +550,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
           const bool move = row_ok && mx != -INFINITY && (first || mx > m_ref + kGap);
           if (__any_sync(0xffffffffu, move && !first)) {
             // some row's O is rescaled: its product of the step before has to be in it
-            if (!(ok = wait_warp(st, kODone + wg, uint32_t(steps - 1) & 1u))) break;
+            if (!(ok = wait_warp(st, kODone + 2 * wg + ((steps - 1) & 1), uint32_t((steps - 1) >> 1) & 1u))) break;
             tc::fence_after();
             const float alpha = move && !first ? fast_exp2(m_ref - mx) : 1.f;
 #pragma unroll 1
@@ -578,7 +579,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       }
       if (!ok) break;
       // ---- the part's output ---------------------------------------------------------------
-      if (!(ok = wait_warp(st, kODone + wg, uint32_t(steps - 1) & 1u))) break;
+      if (!(ok = wait_warp(st, kODone + 2 * wg + ((steps - 1) & 1), uint32_t((steps - 1) >> 1) & 1u))) break;
       tc::fence_after();
       if (warp_ok) {
         const bool whole = it.begins() && it.ends();

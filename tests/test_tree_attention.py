@@ -585,3 +585,25 @@ def test_batch_of_several_tiles_an_item(cache):
     lens = torch.randint(40, 128, (130,), generator=g).tolist()
     nodes = torch.randint(1, 9, (130,), generator=g).tolist()
     Case(42, lens, nodes, 4, 4, 64, 16, cache=cache).check()
+
+
+@gpu
+@pytest.mark.parametrize("cache", ["bf16", "int8"])
+def test_ragged_batch_from_cold_memory(cache):
+    """Many items to a block whose tiles come late: with nothing of the cache in L2 a product
+    may wait for its V tile long after its weights are there, and the item's output must wait
+    for the last one.  Against 64 bits, and the same bits in every run."""
+    g = torch.Generator().manual_seed(43)
+    lens = torch.randint(160, 2049, (64,), generator=g).tolist()
+    nodes = torch.randint(5, 25, (64,), generator=g).tolist()
+    case = Case(44, lens, nodes, 8, 4, 128, 16, cache=cache)
+    x = case.device()
+    flush = torch.empty(256 << 20, dtype=torch.uint8, device="cuda")
+    outs = []
+    for i in range(8):
+        flush.fill_(i)
+        outs.append(case.call(x).clone())
+    torch.cuda.synchronize()
+    assert binding.read_device_errors() == 0
+    case.check(outs[0])
+    assert all(torch.equal(o, outs[0]) for o in outs)
