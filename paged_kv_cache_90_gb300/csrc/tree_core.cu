@@ -1,6 +1,7 @@
 // tree_core.cu — attention of drafted trees and decode over a token-scaled cache on the
-// CUDA cores: the path for what the tensor-core kernel does not take (f32 queries, f32
-// and e4m3 caches, block sizes 2 and 4, groups of more than 128 query heads).
+// CUDA cores: the path for what the tensor-core kernels do not take (f32 queries, f32 and
+// e4m3 caches, bf16 caches of block sizes 2 and 4, groups of more than 128 query heads, a
+// scale that is not above zero, rows not aligned to 16 bytes, an empty cache).
 //
 // One thread block per (query row, query head).  Its four warps take 32 keys at a time in
 // turn: a lane computes one key's score from 16-byte loads of the key's row, then every
@@ -8,7 +9,8 @@
 // keeps a running base-2 maximum, sum and output in binary32; the four are folded at the
 // end.  Keys that the row does not attend to are not read.  Bound by the load latency of
 // one key row per lane and by re-reading the keys for every head of a group; it is a
-// path for rare types, not a fast one.
+// path for rare types, not a fast one: 64 trees of 5 to 24 nodes over 160 to 2048 positions
+// take 3.4 ms here (bf16), 67 us on the tensor cores.
 #include "tree_common.cuh"
 
 namespace pkv {

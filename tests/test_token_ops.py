@@ -231,6 +231,62 @@ def test_quantize_and_read_back(T, hk, d, bs, dt):
 
 
 @gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_codes_next_to_the_borders(d):
+    """Quotients at the middle of two codes and one binary32 number beside it, at scales that
+    are and are not powers of two, huge and tiny: the codes of the binary32 quotient, ties to
+    even, bit for bit."""
+    tops = [127.0, 1.0, 3.7e-3, 3.402823466e38, 1.3e38, 2.0e-36, 1.6e-36, 127.0 * 2.0 ** -60, 5.5]
+    rows = []
+    for top in tops:
+        s = torch.tensor(top) / torch.tensor(127.0)
+        h = (torch.arange(-127, 127).double() + 0.5) * s.double()
+        mid = h.float()
+        near = torch.cat([mid, torch.nextafter(mid, torch.tensor(math.inf)), torch.nextafter(mid, torch.tensor(-math.inf))])
+        near = near[near.abs() < top]
+        near = torch.cat([near, near[: -near.numel() % (d - 1)]]).view(-1, d - 1)
+        rows.append(torch.cat([torch.full((near.shape[0], 1), top), near], 1))
+    x = torch.cat(rows)
+    T, bs = x.shape[0], 16
+    nb = -(-T // bs)
+    k, v = x[:, None].clone(), -x[:, None].flip(0)
+    kc = torch.zeros(nb, 1, bs, d, dtype=torch.int8).cuda()
+    vc, ks, vs = kc.clone(), torch.zeros(nb, 1, bs).cuda(), torch.zeros(nb, 1, bs).cuda()
+    slots = torch.arange(T)
+    binding.quantize_and_cache(k.cuda(), v.cuda(), kc, vc, ks, vs, slots.cuda())
+    for y, c, sc in ((k, kc, ks), (v, vc, vs)):
+        code, scale = quantise(y)
+        assert torch.equal(sc.cpu()[slots // bs, :, slots % bs], scale)
+        assert torch.equal(c.cpu()[slots // bs, :, slots % bs], code)
+    assert binding.read_device_errors() == 0
+
+
+@gpu
+@pytest.mark.parametrize("kw", [dict(rotary_dim=64), dict(rotary_dim=24), dict(rotary_dim=20), dict(rotary_dim=6),
+                                dict(rotary_dim=20, interleaved=True), dict(rotary_dim=64, interleaved=True)])
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+def test_rotary_of_one_projection(kw, dt):
+    """Query, key and value as views of one tensor, as a joint projection gives them, more
+    heads than a warp's slice holds, rotated in place."""
+    T, hq, hk, d, bs = 21, 71, 1, 64, 4
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(T, hq + 2 * hk, d, generator=g).to(dt)
+    rot = binding.rotary(**kw)
+    pos = torch.randint(-50, 5000, (T,), generator=g).int()
+    slots = torch.randperm(40, generator=g)[:T]
+    kc = torch.zeros(10, hk, bs, d, dtype=dt).cuda()
+    vc = kc.clone()
+    y = x.cuda()
+    q, k, v = y[:, :hq], y[:, hq:hq + hk], y[:, hq + hk:]
+    binding.rotary_and_cache(q, q, k, v, pos.cuda(), kc, vc, slots.cuda(), rot)
+    check_near(y.cpu()[:, :hq], *rotate64(x[:, :hq], pos, rot), dt)
+    check_near(kc.cpu()[slots // bs, :, slots % bs], *rotate64(x[:, hq:hq + hk], pos, rot), dt)
+    assert torch.equal(vc.cpu()[slots // bs, :, slots % bs], x[:, hq + hk:])
+    assert torch.equal(y.cpu()[:, hq:], x[:, hq:])
+    assert binding.read_device_errors() == 0
+
+
+@gpu
 @pytest.mark.parametrize("cache", [torch.float32, torch.bfloat16, torch.float8_e4m3fn])
 def test_read_cache_of_the_other_types(cache):
     T, hk, d, bs, nb = 50, 2, 128, 16, 6
