@@ -9,10 +9,10 @@
 // four passes' loads at a time, and waits for nothing else before them (not for the slot).
 //
 // What it measured: rotary write of 16384 tokens of 32 + 2 x 8 heads of 128 in bf16 (403 MB)
-// 75 us, 5.4 TB/s (a block per token with the cosines in shared memory: 175 us); quantising
-// write of 16384 tokens of 2 x 8 heads 35 us, read back into f32 33 us (168 MB, 5.1 TB/s).
-// The write is held back by its instructions: about 150 for 8 columns of two rows, a third of
-// them the codes.
+// 70 us, 5.8 TB/s (a block per token with the cosines in shared memory: 175 us); quantising
+// write of 16384 tokens of 2 x 8 heads 31 us, read back into f32 26 us (168 MB, 6.4 TB/s).  The
+// write is held back by its instructions, 190 for 8 columns of two rows, issued in four of five
+// cycles.
 #include "device_common.cuh"
 #include "token_internal.h"
 
@@ -25,10 +25,31 @@ constexpr int kBatch = 4;     // passes whose loads a warp issues together (rota
                               // step with 2, 4 and 8: 81, 75, 78 us; quantising 57, 57, 66 us)
 constexpr int kFewRows = 48;  // rows of a slice at most (16, 24, 48: 83, 77, 73 us; see slices())
 
+// A value that is the same in all lanes, so that the compiler knows it (and computes what
+// follows from it once for the warp).
+template <typename T>
+__device__ __forceinline__ T one_answer(T x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // How a row's columns go to its lanes, two groups of four each: side by side as pairs of
 // columns turn (none, or 2 i with 2 i + 1), or one of each half of the rotated columns (i with
 // half + i, half a multiple of 4); kOdd is the latter for any other half.
 enum Layout { kPairs, kHalves, kOdd };
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+template <int kLanes>
+__device__ __forceinline__ uint32_t row_top_bits(const float (&x)[8]) {
+  uint32_t top = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+  return top;
+}
 
 // A lane's eight columns as they are stored, so that a batch of loads takes few registers.
 template <typename T>
@@ -36,6 +57,14 @@ struct Raw;
 template <>
 struct Raw<BF16> {
   uint2 a, b;
+  // The bits of a row's largest magnitude, as a binary32 number's (all lanes of the row call).
+  template <int kLanes>
+  __device__ __forceinline__ uint32_t row_top() const {
+    uint32_t m = max_u16x2(max_u16x2(a.x & 0x7fff7fffu, a.y & 0x7fff7fffu), max_u16x2(b.x & 0x7fff7fffu, b.y & 0x7fff7fffu));
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) m = max_u16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    return max(m & 0xffff0000u, m << 16);
+  }
   __device__ __forceinline__ void load(const void* base, int64_t elt, int c0, int c1, bool joined) {
     const uint16_t* s = static_cast<const uint16_t*>(base) + elt;
     if (joined) {
@@ -53,6 +82,12 @@ struct Raw<BF16> {
 template <>
 struct Raw<F32> {
   uint4 a, b;
+  template <int kLanes>
+  __device__ __forceinline__ uint32_t row_top() const {
+    float f[8];
+    expand(f);
+    return row_top_bits<kLanes>(f);
+  }
   __device__ __forceinline__ void load(const void* base, int64_t elt, int c0, int c1, bool) {
     const float* s = static_cast<const float*>(base) + elt;
     a = *reinterpret_cast<const uint4*>(s + c0);
@@ -112,37 +147,33 @@ __device__ __forceinline__ void store_codes(void* base, int64_t elt, int c0, int
   }
 }
 
-__device__ __forceinline__ float approx_inverse(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // Eight values -> eight codes rint(x / s), s = amax / 127 correctly rounded, or 0 (all codes 0)
 // or NaN (zeros too).  |x / s| is at most 127 (1 + 2^-23), so none needs clamping.
 //
-// The division is made for few of them.  q = x y, y = 1 / s within 2^-23, differs from x / s by
-// less than 127 * 1.5 * 2^-23 < 3e-5, and binary32's x / s by 127 * 2^-24 < 1e-5: where q is
-// further than 1e-4 from the middle of two whole numbers all three round alike.
+// The quotient is the correctly rounded one: the product with the correctly rounded 1 / s, and
+// twice the remainder's share added (as DivRn; what underflows on the way belongs to quotients
+// far below 1/2).  16-bit activations have many quotients in the middle of two codes: a cheaper
+// quotient, with a division for those near it, divided in every second pass and was no faster.
 __device__ __forceinline__ uint2 quantize8(const float* x, float s) {
-  const bool zero = !(s > 0.f);
-  const float y = zero ? 0.f : approx_inverse(s);
   uint32_t c[8];
-  float far = 0.f;
+  if (s >= 0x1p-90f) {
+    const float y = __frcp_rn(s);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    // (1.5 * 2^23 + q rounds q to a whole number, in the low bits)
-    const float q = x[i] * y, r = q + 12582912.f;
-    c[i] = __float_as_uint(r);
-    far = fmaxf(far, fabsf(q - (r - 12582912.f)));
-  }
-  if (far > 0.4999f) {
+    for (int i = 0; i < 8; ++i) {
+      float q = __fmul_rn(x[i], y);
+      q = __fmaf_rn(__fmaf_rn(-s, q, x[i]), y, q);
+      q = __fmaf_rn(__fmaf_rn(-s, q, x[i]), y, q);
+      c[i] = __float_as_uint(__fadd_rn(q, 12582912.f));  // (1.5 * 2^23: rounded, in the low bits)
+    }
+  } else if (s > 0.f) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] = uint32_t(__float2int_rn(__fdiv_rn(x[i], s)));
+  } else {
+    return make_uint2(0u, 0u);
   }
   const uint32_t a = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
   const uint32_t b = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
-  return zero ? make_uint2(0u, 0u) : make_uint2(a, b);
+  return make_uint2(a, b);
 }
 
 // The scale of a row whose largest magnitude has the bits `top` (an infinity's or a NaN's are
@@ -174,9 +205,9 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
   __syncthreads();
   asm volatile("griddepcontrol.wait;" ::: "memory");  // as in the other cache writes
   asm volatile("griddepcontrol.launch_dependents;");
-  const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t t = int64_t(blockIdx.x) * kWarps + one_answer(int(threadIdx.x) >> 5);
   if (t >= p.w.num_tokens) return;
-  const int64_t slot = p.w.slot_mapping[t];
+  const int64_t slot = one_answer(p.w.slot_mapping[t]);
   int64_t pos = 0;
   if (half) pos = p.positions64 ? static_cast<const int64_t*>(p.positions)[t] : static_cast<const int32_t*>(p.positions)[t];
   int c0 = 8 * l, c1 = 8 * l + 4, pair0 = 0, pair1 = 0;  // (pairs of the first and last four columns)
@@ -288,11 +319,7 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
       const int64_t at = blk * p.w.cs_block + h * p.w.cs_head + int64_t(off) * D;
       void* dst = is_v ? p.w.value_cache : p.w.key_cache;
       if (p.w.cache_dtype == kI8) {
-        uint32_t top = 0u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const uint32_t top = row_top_bits<kLanes>(x);
         if (live && !is_q && in_cache) {
           const float s = token_scale(top);
           store_codes(dst, at, c0, c1, kJoined, quantize8(x, s));
@@ -319,23 +346,25 @@ __global__ void __launch_bounds__(32 * kWarps) token_quantize_kernel(const __gri
   constexpr bool kJoined = Src::bytes == 2;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t t = int64_t(blockIdx.x) * kWarps + one_answer(int(threadIdx.x) >> 5);
   if (t >= p.w.num_tokens) return;
   const int lane = threadIdx.x & 31, sub = lane / kLanes, l = lane % kLanes;
-  const int64_t slot = p.w.slot_mapping[t];
+  const int64_t slot = one_answer(p.w.slot_mapping[t]);
   const int c0 = kJoined ? 8 * l : 4 * l, c1 = kJoined ? c0 + 4 : c0 + D / 2;
-  const int hk = p.w.num_kv_heads, rows = 2 * hk;
-  const int passes = (rows + kRows - 1) / kRows, per = (passes + int(gridDim.y) - 1) / int(gridDim.y);
+  const int hk = p.w.num_kv_heads;
+  // (a pass is of one tensor: the choice is the warp's, not a lane's)
+  const int tensor = (hk + kRows - 1) / kRows, passes = 2 * tensor;
+  const int per = (passes + int(gridDim.y) - 1) / int(gridDim.y);
   const int first = int(blockIdx.y) * per, last = min(first + per, passes);
+  const int64_t from = t * p.w.src_stride_t;
   for (int p0 = first; p0 < last; p0 += kBatch) {
     Raw<Src> raw[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int r = (p0 + u) * kRows + sub;
+      const bool is_v = p0 + u >= tensor;
+      const int h = (p0 + u - (is_v ? tensor : 0)) * kRows + sub;
       raw[u].clear();
-      if (p0 + u < last && r < rows)
-        raw[u].load(r >= hk ? p.w.value : p.w.key, t * p.w.src_stride_t + (r >= hk ? r - hk : r) * p.w.src_stride_h, c0, c1,
-                    kJoined);
+      if (p0 + u < last && h < hk) raw[u].load(is_v ? p.w.value : p.w.key, from + h * p.w.src_stride_h, c0, c1, kJoined);
     }
     if (slot < 0) return;  // padding
     if (slot >= p.w.num_blocks * p.w.block_size) {
@@ -344,24 +373,19 @@ __global__ void __launch_bounds__(32 * kWarps) token_quantize_kernel(const __gri
     }
     const int64_t blk = slot >> (31 - __clz(p.w.block_size));
     const int off = int(slot) & (p.w.block_size - 1);
+    const int64_t to = blk * p.w.cs_block + int64_t(off) * D, scale_to = blk * p.ts_block + off;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int r = (p0 + u) * kRows + sub;
       if (p0 + u >= last) break;
-      const bool is_v = r >= hk;
-      const int h = is_v ? r - hk : r;
+      const bool is_v = p0 + u >= tensor;
+      const int h = (p0 + u - (is_v ? tensor : 0)) * kRows + sub;
+      const uint32_t top = raw[u].template row_top<kLanes>();
+      if (h >= hk) continue;
       float x[8];
       raw[u].expand(x);
-      uint32_t top = 0u;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-#pragma unroll
-      for (int o = kLanes / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (r >= rows) continue;
       const float s = token_scale(top);
-      store_codes(is_v ? p.w.value_cache : p.w.key_cache, blk * p.w.cs_block + h * p.w.cs_head + int64_t(off) * D, c0, c1,
-                  kJoined, quantize8(x, s));
-      if (l == 0) (is_v ? p.v_token_scales : p.k_token_scales)[blk * p.ts_block + h * p.ts_head + off] = s;
+      store_codes(is_v ? p.w.value_cache : p.w.key_cache, to + h * p.w.cs_head, c0, c1, kJoined, quantize8(x, s));
+      if (l == 0) (is_v ? p.v_token_scales : p.k_token_scales)[scale_to + h * p.ts_head] = s;
     }
   }
 }
@@ -373,10 +397,10 @@ __global__ void __launch_bounds__(32 * kWarps) token_read_kernel(const __grid_co
   constexpr bool kJoined = Dst::bytes == 2;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t t = int64_t(blockIdx.x) * kWarps + one_answer(int(threadIdx.x) >> 5);
   if (t >= p.w.num_tokens) return;
   const int lane = threadIdx.x & 31, sub = lane / kLanes, l = lane % kLanes;
-  const int64_t slot = p.w.slot_mapping[t];
+  const int64_t slot = one_answer(p.w.slot_mapping[t]);
   if (slot < 0) return;
   if (slot >= p.w.num_blocks * p.w.block_size) {
     if (lane == 0 && blockIdx.y == 0) raise_device_error(p.w.err, kErrSlot);
@@ -386,17 +410,17 @@ __global__ void __launch_bounds__(32 * kWarps) token_read_kernel(const __grid_co
   const int off = int(slot) & (p.w.block_size - 1);
   const int hk = p.w.num_kv_heads;
   const int c0 = kJoined ? 8 * l : 4 * l, c1 = kJoined ? c0 + 4 : c0 + D / 2;
-  const int passes = (2 * hk + kRows - 1) / kRows, per = (passes + int(gridDim.y) - 1) / int(gridDim.y);
+  const int tensor = (hk + kRows - 1) / kRows, passes = 2 * tensor;  // (a pass is of one tensor)
+  const int per = (passes + int(gridDim.y) - 1) / int(gridDim.y);
   const int first = int(blockIdx.y) * per, last = min(first + per, passes);
   for (int p0 = first; p0 < last; p0 += kBatch) {
     uint4 a[kBatch], b[kBatch];  // columns c0 .. and c1 .., as they are stored
     float s[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int r = (p0 + u) * kRows + sub;
-      if (p0 + u >= last || r >= 2 * hk) continue;
-      const bool is_v = r >= hk;
-      const int h = is_v ? r - hk : r;
+      const bool is_v = p0 + u >= tensor;
+      const int h = (p0 + u - (is_v ? tensor : 0)) * kRows + sub;
+      if (p0 + u >= last || h >= hk) continue;
       const int elt = type == kF32 ? 4 : type == kBF16 ? 2 : 1;
       const unsigned char* src = static_cast<const unsigned char*>(is_v ? p.w.value_cache : p.w.key_cache) +
                                  (blk * p.w.cs_block + h * p.w.cs_head + int64_t(off) * D) * elt;
@@ -419,10 +443,9 @@ __global__ void __launch_bounds__(32 * kWarps) token_read_kernel(const __grid_co
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int r = (p0 + u) * kRows + sub;
-      if (p0 + u >= last || r >= 2 * hk) continue;
-      const bool is_v = r >= hk;
-      const int h = is_v ? r - hk : r;
+      const bool is_v = p0 + u >= tensor;
+      const int h = (p0 + u - (is_v ? tensor : 0)) * kRows + sub;
+      if (p0 + u >= last || h >= hk) continue;
       float x[8];
       if (type == kF32) {
         Chunk<F32>::expand(a[u], x);
@@ -435,7 +458,9 @@ __global__ void __launch_bounds__(32 * kWarps) token_read_kernel(const __grid_co
           e4m3x4_to_f32x4(b[u].x, x + 4);
         } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = float(int(int8_t((i < 4 ? a[u].x : b[u].x) >> (8 * (i & 3)))));
+          for (int i = 0; i < 8; ++i)  // (2^23 + code + 128 in the low byte, exact)
+            x[i] = __uint_as_float(__byte_perm((i < 4 ? a[u].x : b[u].x) ^ 0x80808080u, 0x4b000000u, 0x7650 + (i & 3))) -
+                   8388736.f;
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] *= s[u];
