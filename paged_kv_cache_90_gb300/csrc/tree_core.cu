@@ -10,7 +10,7 @@
 // end.  Keys that the row does not attend to are not read.  Bound by the load latency of
 // one key row per lane and by re-reading the keys for every head of a group; it is a
 // path for rare types, not a fast one: 64 trees of 5 to 24 nodes over 160 to 2048 positions
-// take 3.4 ms here (bf16), 67 us on the tensor cores.
+// take 3.4 ms here (bf16), 62 us on the tensor cores.
 #include "tree_common.cuh"
 
 namespace pkv {

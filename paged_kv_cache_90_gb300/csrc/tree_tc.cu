@@ -27,11 +27,13 @@
 // so that one item's output is written while the next one's softmax runs.
 //
 // What it measured, 32 query heads to 8 KV heads of 128: 64 trees of 5 to 24 nodes over 160 to
-// 2048 positions 67 us, 4.6 TB/s, bound by the copies in flight (a step is a tile of 64 KB, three
-// and three in the rings) and by each block's start and end; 8 trees of 64 nodes over 32000
-// positions 253 us, 1.05 PFLOP/s, bound by the softmax of a step (a row of 128 scores a thread).
+// 2048 positions 62 us, 5.0 TB/s, bound by the copies in flight (a tile is 64 KB, the rings hold
+// three and three) and by each block's start and end; 8 trees of 64 nodes over 32000 positions 250
+// us, 1.05 PFLOP/s at the power limit: a tile's two steps take 3500 to 3900 clocks (a warpgroup's
+// softmax 3000 beside the other's, and the MMA warp between them), an item's end and the next
+// one's start 16000 more, so blocks with such a border end a tenth after the others.
 //
-// P is rounded to bf16 for the product (half a step, 2^-9 of a weight on average; the
+// P is rounded to bf16 for the product (at most half a step, 2^-8 of a weight; the
 // other operand is bf16); scores, maximum, sum and output stay in binary32.  The
 // reference maximum moves only when a row's maximum grows by more than 2^8, as in the
 // decode kernel.
@@ -465,35 +467,39 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         phase ^= 1u << slot;
         unsigned char* vt = smem + (sv - sbase) + slot * C::kOpBytes;
         const bool scan = p.tree_mask && pos + kBN > e.P;
-        for (int q = 0; q < 4; ++q) {
-          const int r0 = pos + 32 * q;  // 32 positions
+        constexpr int kCells = 8 * C::kHalves;  // 16-byte cells of a row
+        auto cell = [&](int i) {  // (row i / kCells)
+          return reinterpret_cast<uint4*>(vt + ((i >> 3) % C::kHalves) * C::kHalfBytes + (i / kCells) * 128 + (i & 7) * 16);
+        };
+        const int hi = max(0, min(kBN, e.L - pos));
+        for (int i = lane; i < (e.lo - pos) * kCells; i += 32) *cell(i) = make_uint4(0u, 0u, 0u, 0u);
+        for (int i = hi * kCells + lane; i < kBN * kCells; i += 32) *cell(i) = make_uint4(0u, 0u, 0u, 0u);
+        for (int q = 0; scan && q < 4; ++q) {  // the drafted nodes, 32 positions to a word
+          const int end = min(hi, 32 * q + 32) * kCells;
           uint32_t bad = 0u;
-          if (r0 < e.lo || r0 + 32 > (p.tree_mask ? e.P : e.L)) {
-            for (int i = lane; i < 32 * 8 * C::kHalves; i += 32) {
-              const int row = 32 * q + ((i >> 3) & 31), at = pos + row;
-              uint4* cell = reinterpret_cast<uint4*>(vt + (i >> 8) * C::kHalfBytes + row * 128 + (i & 7) * 16);
-              if (at < e.lo || at >= e.L) {
-                *cell = make_uint4(0u, 0u, 0u, 0u);
-              } else if (scan && at >= e.P) {
-                const uint4 v = *cell;
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                bool any = false;
+          // (four loads together: one after the other they take longer than the tile's products)
+#pragma unroll 1
+          for (int i0 = max(e.P - pos, 32 * q) * kCells + lane; i0 < end; i0 += 128) {
+            uint4 x[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if ((w[k] & 0x7f80u) == 0x7f80u) { w[k] &= 0xffff0000u; any = true; }
-                  if ((w[k] & 0x7f800000u) == 0x7f800000u) { w[k] &= 0xffffu; any = true; }
-                }
-                if (any) {
-                  *cell = make_uint4(w[0], w[1], w[2], w[3]);
-                  bad |= 1u << (row & 31);
-                }
+            for (int u = 0; u < 4; ++u) x[u] = i0 + 32 * u < end ? *cell(i0 + 32 * u) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+              bool any = false;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                if ((w[k] & 0x7f80u) == 0x7f80u) { w[k] &= 0xffff0000u; any = true; }
+                if ((w[k] & 0x7f800000u) == 0x7f800000u) { w[k] &= 0xffffu; any = true; }
+              }
+              if (any) {
+                *cell(i0 + 32 * u) = make_uint4(w[0], w[1], w[2], w[3]);
+                bad |= 1u << (((i0 + 32 * u) / kCells) & 31);
               }
             }
           }
-          if (scan) {
-            bad = __reduce_or_sync(0xffffffffu, bad);
-            if (lane == 0) st->bad_rows[item % kBadItems][4 * (j - jt) + q] = bad;
-          }
+          bad = __reduce_or_sync(0xffffffffu, bad);
+          if (lane == 0) st->bad_rows[item % kBadItems][4 * (j - jt) + q] = bad;
         }
         fence_proxy_async_smem();
         __syncwarp();
