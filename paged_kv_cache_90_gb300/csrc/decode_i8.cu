@@ -432,7 +432,6 @@ int decode_i8_blocks_per_sm(int group) { return group <= 8 ? 3 : 2; }
 
 cudaError_t launch_decode_i8(const TreeParams& p, TreeSplit sp, cudaStream_t stream) {
   sp.item_nodes = sp.tq = 1;
-  sp.out_vec = (reinterpret_cast<uintptr_t>(p.out) & 7) == 0 && (p.out_stride_t & 3) == 0 && (p.out_stride_h & 3) == 0;
   if (p.head_dim == 128)
     return p.group <= 8 ? launch_decode_i8_tpl<128, 1>(p, sp, stream) : launch_decode_i8_tpl<128, 2>(p, sp, stream);
   return p.group <= 8 ? launch_decode_i8_tpl<64, 1>(p, sp, stream) : launch_decode_i8_tpl<64, 2>(p, sp, stream);

@@ -1,7 +1,7 @@
 // tree_core.cu — attention of drafted trees and decode over a token-scaled cache on the
 // CUDA cores: the path for what the tensor-core kernels do not take (f32 queries, f32 and
 // e4m3 caches, bf16 caches of block sizes 2 and 4, groups of more than 128 query heads, a
-// scale that is not above zero, rows not aligned to 16 bytes, an empty cache).
+// scale that is not above zero, rows not aligned to 16 bytes).
 //
 // One thread block per (query row, query head).  Its four warps take 32 keys at a time in
 // turn: a lane computes one key's score from 16-byte loads of the key's row, then every

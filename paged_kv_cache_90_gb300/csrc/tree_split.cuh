@@ -316,7 +316,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __gr
 #pragma unroll
     for (int k = 0; k < kCols; k += 2) {
       const __nv_bfloat162 pr = __floats2bfloat162_rn(o[i][k] * inv, o[i][k + 1] * inv);
-      *reinterpret_cast<uint32_t*>(out + k) = *reinterpret_cast<const uint32_t*>(&pr);
+      if (sp.out_vec) {
+        *reinterpret_cast<uint32_t*>(out + k) = *reinterpret_cast<const uint32_t*>(&pr);
+      } else {  // (rows at any address)
+        out[k] = pr.x;
+        out[k + 1] = pr.y;
+      }
     }
   }
 }

@@ -771,10 +771,8 @@ cudaError_t launch_tree_merge(const TreeParams& p, const TreeSplit& sp, cudaStre
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-bool tree_tensor_supported(const TreeParams& p) {
-  // (an entry that is out of range is read as block 0, which has to be there)
-  return p.num_blocks > 0 && (tree_tc_supported(p) || tree_i8_supported(p));
-}
+// (an entry that is out of range is read as block 0: the host refuses a cache without blocks)
+bool tree_tensor_supported(const TreeParams& p) { return tree_tc_supported(p) || tree_i8_supported(p); }
 
 // Rows of a part's slot: the batch's, or at most one row tile of 128 (int8 cache) or two.
 int tree_part_rows(int64_t num_tokens, int group, bool decode, bool one_tile) {
@@ -794,6 +792,7 @@ cudaError_t launch_tree_tensor(const TreeParams& p, int grid, int rows, void* ws
   sp.tq = tree::kBM / p.group;
   sp.bs_shift = 0;
   while ((1 << sp.bs_shift) < p.block_size) ++sp.bs_shift;
+  sp.out_vec = (reinterpret_cast<uintptr_t>(p.out) & 7) == 0 && (p.out_stride_t & 3) == 0 && (p.out_stride_h & 3) == 0;
   unsigned char* w = static_cast<unsigned char*>(ws);
   // (the first words of the workspace are the decode kernel's counters, zero between calls)
   sp.tails = reinterpret_cast<TreeSplit::Tail*>(w + kWorkspaceHeader);

@@ -607,3 +607,59 @@ def test_ragged_batch_from_cold_memory(cache):
     assert binding.read_device_errors() == 0
     case.check(outs[0])
     assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+@gpu
+@pytest.mark.parametrize("hk,group,d", [(2, 4, 128), (1, 12, 64), (1, 16, 128), (1, 40, 128)])
+@pytest.mark.parametrize("shift", [1, 2, 4])
+def test_decode_quantized_output_rows_of_any_alignment(hk, group, d, shift):
+    """Output rows off 16 and 8 bytes, in a wider tensor whose other columns stay."""
+    c = Case(45, [3, 700, 130, 1], None, hk, group, d, 16, cache="int8", decode=True)
+    x = c.device()
+    wide = torch.full((c.T, hk * group, d + 9), 7.0, dtype=torch.bfloat16, device="cuda")
+    x["out"] = wide[:, :, shift:shift + d]
+    c.call(x)
+    torch.cuda.synchronize()
+    c.check(x["out"])
+    assert (wide[:, :, :shift] == 7).all() and (wide[:, :, shift + d:] == 7).all()
+
+
+@gpu
+@pytest.mark.parametrize("hk,group", [(8, 4), (1, 16), (1, 30)])
+def test_decode_quantized_from_a_graph(hk, group):
+    """Captured once, replayed as the contexts grow and change: each time the eager call's
+    bits; scales of 0 and of a type's largest and smallest numbers among them."""
+    lens = [900, 33, 0, 4000, 128, 1]
+    c = Case(46, lens, None, hk, group, 128, 16, cache="int8", decode=True)
+    c.k_scales[0, :, 3] = 0.0
+    c.v_scales[1, :, 2] = 3e38
+    c.v_scales[2, :, 2] = 1e-38
+    x = c.device()
+    eager = c.call(x).clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.call(x)
+    for k in range(4):
+        x["lens"][0] = 900 - 37 * k
+        x["lens"][3] = 4000 - 1001 * k
+        x["q"].mul_(0.75)
+        x["out"].fill_(7.0)
+        g.replay()
+        got = x["out"].clone()
+        assert torch.equal(got.view(torch.int16), c.call(x).view(torch.int16))
+        assert not torch.equal(got, eager)
+    assert binding.read_device_errors() == 0
+
+
+@gpu
+def test_decode_quantized_scales_with_strides_of_their_own():
+    """Scales as a slice of a wider tensor, off 16 bytes; blocks of two tokens."""
+    for bs in (2, 16):
+        c = Case(47, [250, 31], None, 2, 4, 64, bs, cache="int8", decode=True)
+        x = c.device()
+        nb = x["ks"].shape[0]
+        wide = torch.zeros(2, nb, 3, bs + 3, device="cuda")
+        wide[0, :, 1:, 1:bs + 1], wide[1, :, 1:, 1:bs + 1] = x["ks"], x["vs"]
+        x["ks"], x["vs"] = wide[0, :, 1:, 1:bs + 1], wide[1, :, 1:, 1:bs + 1]
+        c.check(c.call(x))
+        assert binding.read_device_errors() == 0
