@@ -26,10 +26,10 @@
 // codes), one warpgroup's whole work.  The chain of a tile bounds it, not a unit: of 64 rows a
 // warp's weights take 2600 clocks, what is between two tiles' weights (a signal, a wait, the
 // scales) another 1500, with two S^T buffers so that the score MMAs are not part of it.  32 trees
-// of 8 to 32 nodes, 4 x 8 heads of 128, over 1000 to 8192 positions: 195 us, 245 TFLOP/s.  It was
+// of 8 to 32 nodes, 4 x 8 heads of 128, over 1000 to 8192 positions: 179 us, 268 TFLOP/s.  It was
 // 249 us with a pass over the scores before the weights, with products of each half of the rows
 // (their A operand was read twice), and with the queries converted by one warp (33000 clocks
-// between two items).
+// between two items); and 195 with each thread working out its output rows' addresses.
 //
 // Warps: 0 streams K codes and the scales, 3 V codes (bulk copies of one (block, head) run each);
 // 1 issues the score MMAs, 2 the products'; 4-7 and 8-11 are the softmax warpgroups, which also
@@ -52,8 +52,8 @@ using namespace tree;
 
 constexpr int kThreads = 640;
 // registers of a thread, by warpgroup: launched with 96 each (5 x 96 = 480), then split anew
-// into control, two softmax and two widening warpgroups (80 + 2 x 144 + 2 x 56 = 480)
-constexpr int kRegsControl = 80, kRegsSoftmax = 144, kRegsWiden = 56;
+// into control, two softmax and two widening warpgroups (64 + 2 x 152 + 2 x 56 = 480)
+constexpr int kRegsControl = 64, kRegsSoftmax = 152, kRegsWiden = 56;
 static_assert(kRegsControl + 2 * kRegsSoftmax + 2 * kRegsWiden <= 5 * 96, "registers");
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxSlots = 16;  // of the ring of code tiles
@@ -524,18 +524,26 @@ __device__ __forceinline__ void write_rows(const TreeParams& p, const TreeSplit&
     uint32_t w[16];
     ld16(tO + 16 * c, w);
     if (col >= D) continue;  // (64 columns: the upper lanes of the accumulator repeat them)
+    const int r0 = row0 + 16 * c, n = pt.rows - r0;
+    if (pt.whole) {
+      const int node = (r0 * div) >> 16;
+      int h = r0 - node * p.group;
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(pt.tok0 + node) * p.out_stride_t +
+                           int64_t(pt.kvh * p.group + h) * p.out_stride_h + col;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int r = row0 + 16 * c + i;
-      if (r >= pt.rows) break;
-      const float v = __uint_as_float(w[i]) * rw.alpha_o[16 * c + i];
-      if (pt.whole) {
-        const int node = (r * div) >> 16, h = r - node * p.group;
-        static_cast<__nv_bfloat16*>(p.out)[int64_t(pt.tok0 + node) * p.out_stride_t +
-                                           int64_t(pt.kvh * p.group + h) * p.out_stride_h + col] = __float2bfloat16_rn(v);
-      } else {
-        sp.o[(prow + r) * D + col] = v;
+      for (int i = 0; i < 16; ++i) {
+        if (i < n) *out = __float2bfloat16_rn(__uint_as_float(w[i]) * rw.alpha_o[16 * c + i]);
+        out += p.out_stride_h;
+        if (++h == p.group) {
+          h = 0;
+          out += p.out_stride_t - p.group * p.out_stride_h;
+        }
       }
+    } else {
+      float* o = sp.o + (prow + r0) * D + col;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < n) o[i * D] = __uint_as_float(w[i]) * rw.alpha_o[16 * c + i];
     }
   }
 }
@@ -547,7 +555,9 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   State* st = reinterpret_cast<State*>(smem + C::kState);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the warp's number from one lane: the compiler then knows that it is the same in all, and what
+  // follows from it, a role's loops and addresses, is computed once for the warp)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int g = p.group;
 
   if (tid == 0) {

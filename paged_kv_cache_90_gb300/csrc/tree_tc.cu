@@ -28,8 +28,8 @@
 //
 // What it measured, 32 query heads to 8 KV heads of 128: 64 trees of 5 to 24 nodes over 160 to
 // 2048 positions 62 us, 5.0 TB/s, bound by the copies in flight (a tile is 64 KB, the rings hold
-// three and three) and by each block's start and end; 8 trees of 64 nodes over 32000 positions 250
-// us, 1.05 PFLOP/s at the power limit: a tile's two steps take 3500 to 3900 clocks (a warpgroup's
+// three and three) and by each block's start and end; 8 trees of 64 nodes over 32000 positions 241
+// us, 1.09 PFLOP/s at the power limit: a tile's two steps take 3500 to 3900 clocks (a warpgroup's
 // softmax 3000 beside the other's, and the MMA warp between them), an item's end and the next
 // one's start 16000 more, so blocks with such a border end a tenth after the others.
 //
@@ -210,7 +210,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   State* st = reinterpret_cast<State*>(smem + C::kState);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the warp's number from one lane: the compiler then knows that it is the same in all, and what
+  // follows from it, a role's loops and addresses, is computed once for the warp)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int g = p.group, TQ = sp.tq;
   const uint32_t sbase = smem_addr(smem);
 
