@@ -12,7 +12,8 @@
 // queries share), or V^T from pairs of tokens' bytes, and O^T stays in 32 accumulators a lane.
 // The fifth-generation MMAs take operands from shared memory only: there the same codes are
 // copied, widened, written back and waited for by four roles, 33 M warp instructions a launch
-// for 64 sequences of 1100 positions and 83 us; here 38 us (4.0 TB/s).
+// for 64 sequences of 1100 positions and 83 us at best; here 38 us (4.0 TB/s), and 97 us (5.7 TB/s)
+// for 8 of 32768.
 //
 // A warp takes 32 positions of a tile of 128, its loads of K a step ahead and of V during the
 // scores; 12 warps on an SM keep about 90 KB on the way.  A warp has its own maximum (moved when
@@ -424,10 +425,16 @@ cudaError_t launch_decode_i8_tpl(const TreeParams& p, const TreeSplit& sp, cudaS
 
 }  // namespace
 
+// Up to two tiles of 8 heads: a third would not leave registers for a step's codes.  64 sequences
+// of 129 to 2048 positions with this kernel and with tree_i8.cu's: 8 KV heads of 4 heads of 128 36
+// and 102 us, 4 KV heads of 16 29 and 53, 8 KV heads of 16 heads of 64 33 and 90.
 bool decode_i8_supported(const TreeParams& p) {
   return !p.query_start_loc && p.group <= 16 && tree_i8_supported(p);
 }
 
+// What the registers allow (168 a thread; 255 with two tiles).  Batch and long contexts with two
+// blocks of one tile 44 and 115 us, with three 38 and 97, with four (128 registers, spills) 49 and
+// 132.
 int decode_i8_blocks_per_sm(int group) { return group <= 8 ? 3 : 2; }
 
 cudaError_t launch_decode_i8(const TreeParams& p, TreeSplit sp, cudaStream_t stream) {
