@@ -26,10 +26,10 @@
 // codes), one warpgroup's whole work.  The chain of a tile bounds it, not a unit: of 64 rows a
 // warp's weights take 2600 clocks, what is between two tiles' weights (a signal, a wait, the
 // scales) another 1500, with two S^T buffers so that the score MMAs are not part of it.  32 trees
-// of 8 to 32 nodes, 4 x 8 heads of 128, over 1000 to 8192 positions: 179 us, 268 TFLOP/s.  It was
+// of 8 to 32 nodes, 4 x 8 heads of 128, over 1000 to 8192 positions: 172 us, 277 TFLOP/s.  It was
 // 249 us with a pass over the scores before the weights, with products of each half of the rows
 // (their A operand was read twice), and with the queries converted by one warp (33000 clocks
-// between two items); and 195 with each thread working out its output rows' addresses.
+// between two items), and 195 with each thread working out its output rows' addresses.
 //
 // Warps: 0 streams K codes and the scales, 3 V codes (bulk copies of one (block, head) run each);
 // 1 issues the score MMAs, 2 the products'; 4-7 and 8-11 are the softmax warpgroups, which also
@@ -72,11 +72,15 @@ struct Cfg {
   static constexpr uint32_t kVHalf = kVTokens * 128;        // pitch of its 64-column halves
   static constexpr uint32_t kCodeBytes = kBN * D;
   static constexpr uint32_t kPBytes = kBN * 128;
-  // from the 1024-aligned base: K units | V units | Q | P | ring of code tiles | state.  A batch
-  // of few rows needs 16 rows of Q and of two P; else there is one P of two times 64 rows.
-  static constexpr uint32_t kK = 0, kV = 2 * kUnitBytes, kQ = 4 * kUnitBytes;
+  // from the 1024-aligned base: K units | V units | Q | P (two times 64 rows) | ring of code tiles |
+  // state
+  static constexpr uint32_t kK = 0, kV = 2 * kUnitBytes, kQ = 4 * kUnitBytes, kQUnit = kBN * 128;
+  static constexpr uint32_t kP = kQ + kUnits * kQUnit, kCodes = kP + 2 * kPBytes;
   static constexpr uint32_t kState = 211 * 1024;
   static constexpr uint32_t kStateBytes = 15 * 1024;
+  // slots of the ring, K and V in turn: an even number, so that a loader and the widening warps it
+  // feeds have slots of their own and see every phase of their barriers
+  static constexpr int kSlots = int((kState - kCodes) / kCodeBytes) & ~1;
   static constexpr size_t kSmem = kState + kStateBytes + 1024;  // (+ alignment)
   // tensor memory: S^T [2], then O^T [2], 128 columns each
   static constexpr uint32_t kS = 0, kO = 256;
@@ -339,13 +343,13 @@ __device__ __forceinline__ float reduce_rows(int id, int warp, int lane, float (
 // weights taken back and computed anew (a weight cut off at 2^kTop loses nothing: relative to the
 // new reference the sum it was added to is below 2^-kTop).  An item's first tile starts there.
 __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* qf, const Token& tk, int nc, uint32_t tS,
-                                             uint32_t tO, unsigned char* ptile, bool one_p, int c0, int step, bool first,
+                                             uint32_t tO, unsigned char* ptile, int c0, int step, bool first,
                                              float& vref, float& vinv, Sums& l) {
-  // (`ptile`: this step's P, 64 rows of 128 tokens after another, the only one with `one_p`; `c0`:
-  // the warpgroup's first chunk of 16 rows in it)
+  // (`ptile`: P, 64 rows of 128 tokens after another; `c0`: the warpgroup's first chunk of 16 rows)
   const int t = 32 * tk.warp + tk.lane;
   auto row = [&](int c) { return reinterpret_cast<uint4*>(ptile + ((c0 + c) >> 2) * (kBN * 128) + t * 128); };
-  if (one_p && step > 0) (void)wait_warp(st, kODone + ((step - 1) & 1), uint32_t((step - 1) >> 1) & 1u);
+  // (the product of the step before has read P)
+  if (step > 0) (void)wait_warp(st, kODone + ((step - 1) & 1), uint32_t((step - 1) >> 1) & 1u);
   const float av = fabsf(tk.vs);
   float vn = tk.valid ? tk.vs * vinv : 0.f;
   if (!first) {
@@ -406,11 +410,7 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
     }
     group_sync(tk.id);
   }
-  if (!first) {
-    // O^T has to hold the tiles before this one
-    (void)wait_warp(st, kODone + ((step - 1) & 1), uint32_t((step - 1) >> 1) & 1u);
-    tc::fence_after();
-  }
+  tc::fence_after();  // (O^T holds the tiles before this one)
 #pragma unroll 1
   for (int c = 0; c < nc; ++c) {
     uint32_t w[16];
@@ -445,7 +445,7 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
 // of two of its own, and their score factors to `qf`.  `div`: 2^16 / group, rounded up.
 template <int D>
 __device__ __forceinline__ void load_queries(const TreeParams& p, const TreeSplit& sp, const Walk& it, const ItemRows& ir,
-                                             int row0, unsigned char* q, uint32_t q_unit, float* qf, int warp, int lane,
+                                             int row0, unsigned char* q, float* qf, int warp, int lane,
                                              int div) {
   constexpr int kLanes = D / 8, kPer = 32 / kLanes, kBatch = 4;  // lanes of a row, rows of a pass, passes
   const int sub = lane / kLanes, col = (lane % kLanes) * 8, g = p.group;
@@ -482,7 +482,7 @@ __device__ __forceinline__ void load_queries(const TreeParams& p, const TreeSpli
           const __half2 v = __floats2half2_rn(f[2 * e] * s, f[2 * e + 1] * s);
           h[e] = *reinterpret_cast<const uint32_t*>(&v);
         }
-        *reinterpret_cast<uint4*>(q + (col >> 6) * q_unit + r * 128 + (((col >> 3) & 7) ^ (r & 7)) * 16) =
+        *reinterpret_cast<uint4*>(q + (col >> 6) * Cfg<D>::kQUnit + r * 128 + (((col >> 3) & 7) ^ (r & 7)) * 16) =
             make_uint4(h[0], h[1], h[2], h[3]);
         if (col == 0) qf[i] = p.qk_scale_log2 * inv;
       }
@@ -575,7 +575,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
   if (warp == 0) tc::alloc(&st->tmem, kTmemCols);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing of the caller's is read before
   asm volatile("griddepcontrol.launch_dependents;");
-  const bool many = find_range<kThreads>(p, sp, &st->range, st->warp_sum, kFewRows / g);
+  (void)find_range<kThreads>(p, sp, &st->range, st->warp_sum, 0);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
@@ -583,14 +583,6 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
   const Range* rg = &st->range;
   Walk it;
   it.start(p, sp, rg);
-  // the layout behind the widened tiles
-  const int q_rows = many ? 2 * kHalfRows : kFewRows, groups = many ? 2 : 1;  // rows of Q, warpgroups in use
-  const uint32_t q_unit = uint32_t(q_rows) * 128, p_step = groups * C::kPBytes;
-  const uint32_t oP = C::kQ + C::kUnits * q_unit, oCodes = oP + (many ? 1 : 2) * p_step;
-  const int p_odd = many ? 0 : 1;  // (few rows: two P tiles)
-  // (an even number: a loader and the widening warps it feeds have slots of their own, and see
-  // every phase of their barriers)
-  const int slots = min(kMaxSlots, int((C::kState - oCodes) / C::kCodeBytes)) & ~1;
 
   // (each role takes its registers itself: the compiler counts them by branch)
   if (warp == 0 || warp == 3) {
@@ -638,11 +630,11 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
           now[u] = 0;
         }
       bool ok = true;
-      if (n >= slots) ok = wait_warp(st, kCodeEmpty + slot, phase ^ 1u);
+      if (n >= C::kSlots) ok = wait_warp(st, kCodeEmpty + slot, phase ^ 1u);
       if (ok) {
         if (lane == 0) mbar_arrive_expect_tx(&st->bars[kCodeFull + slot], uint32_t(nblk_now) * bytes);
         __syncwarp();
-        unsigned char* dst = smem + oCodes + slot * C::kCodeBytes;
+        unsigned char* dst = smem + C::kCodes + slot * C::kCodeBytes;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int b = lane + 32 * u;
@@ -653,8 +645,8 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
       }
       n += 2;
       slot += 2;
-      if (slot >= slots) {
-        slot -= slots;
+      if (slot >= C::kSlots) {
+        slot -= C::kSlots;
         phase ^= 1u;
       }
       if (v) continue;
@@ -693,8 +685,8 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
     // the copies in flight land before the block may exit
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (lane == 0)
-      for (int k = max(0, n - slots); k < n; ++k)
-        if ((k & 1) == v) (void)mbar_wait_bounded(&st->bars[kCodeFull + k % slots], uint32_t(k / slots) & 1u);
+      for (int k = max(0, n - C::kSlots); k < n; ++k)
+        if ((k & 1) == v) (void)mbar_wait_bounded(&st->bars[kCodeFull + k % C::kSlots], uint32_t(k / C::kSlots) & 1u);
   } else if (warp == 1) {
     less_registers<kRegsControl>();
     // ---- score MMAs (a warp, see umma.cuh; the products' are another's: each waits only for its own) ----
@@ -717,7 +709,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
           for (int u = 0; ok && u < C::kUnits; ++u, ++kn) {
             if (!(ok = wait_warp(st, kKFull + (kn & 1), uint32_t(kn >> 1) & 1u))) break;
             tc::fence_after();
-            const uint64_t kd = kdesc + (kn & 1) * kUnit, qd = qdesc + ((u * q_unit) >> 4);
+            const uint64_t kd = kdesc + (kn & 1) * kUnit, qd = qdesc + ((u * C::kQUnit) >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) umma::mma_ss(to, kd + kk * 2, qd + kk * 2, id, (u > 0 || kk > 0) ? 1u : 0u);
             umma::commit(&st->bars[kKEmpty + (kn & 1)]);
@@ -738,7 +730,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
       constexpr uint64_t kUnit = C::kUnitBytes >> 4;
       // (a head of 64 columns has one chunk of them: the second 64 rows of the MMA repeat it)
       const uint64_t vdesc = tc::desc_sw128(base + C::kV, D == 128 ? C::kVHalf : 0, 1024);
-      const uint64_t pdesc = tc::desc_sw128(base + oP, C::kPBytes, 1024);
+      const uint64_t pdesc = tc::desc_sw128(base + C::kP, C::kPBytes, 1024);
       int vn = 0, sslot = 0;  // units of V, the tile's slot of scales
       int n = 0, item = 0;  // steps, items
       int64_t at = rg->from;
@@ -764,7 +756,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
           for (int u = 0; ok && u < C::kUnits; ++u, ++vn) {
             if (!(ok = wait_warp(st, kVFull + (vn & 1), uint32_t(vn >> 1) & 1u))) break;
             tc::fence_after();
-            const uint64_t vd = vdesc + (vn & 1) * kUnit, pb = pdesc + (((n & p_odd) * p_step + u * C::kVTokens * 128) >> 4);
+            const uint64_t vd = vdesc + (vn & 1) * kUnit, pb = pdesc + ((u * C::kVTokens * 128) >> 4);
             const uint32_t acc = j > it.j0 || u > 0;
 #pragma unroll
             for (int kk = 0; kk < C::kVTokens / 16; ++kk)
@@ -791,7 +783,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
     const int row = t >> 2, k = t & 3, sw = row & 7;
     const bool halves = v && D == 128;
     const uint32_t a = 32 * D, b = halves ? 64 : 64 * D, da = 32 * 128, db = halves ? C::kVHalf : 64 * 128;
-    const unsigned char* src = smem + oCodes + row * D + k * 16;
+    const unsigned char* src = smem + C::kCodes + row * D + k * 16;
     unsigned char* lo = smem + (v ? C::kV : C::kK) + row * 128 + ((2 * k ^ sw) << 4);
     unsigned char* hi = smem + (v ? C::kV : C::kK) + row * 128 + (((2 * k + 1) ^ sw) << 4);
     const int empty = v ? kVEmpty : kKEmpty, full = v ? kVFull : kKFull;
@@ -822,8 +814,8 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
           }
         }
         slot += 2;
-        if (slot >= slots) {
-          slot -= slots;
+        if (slot >= C::kSlots) {
+          slot -= C::kSlots;
           phase ^= 1u;
         }
       }
@@ -843,7 +835,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
     // (Q is free once the scores of the item's last tile are there)
     auto queries = [&](const ItemRows& ir) {
       if (wg < ir.groups)
-        load_queries<D>(p, sp, it, ir, wg * ir.half, smem + C::kQ, q_unit, st->qf[item & 1][wg], q, lane, div);
+        load_queries<D>(p, sp, it, ir, wg * ir.half, smem + C::kQ, st->qf[item & 1][wg], q, lane, div);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&st->bars[kQFull]);
@@ -904,7 +896,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
           }
           const bool first = j == it.j0;
           if (nc > 0)
-            softmax_step(st, rw, qf, tk, nc, tS, tO, smem + oP + (step & p_odd) * p_step, p_odd == 0, row0 >> 4, step, first, vref, vinv, l);
+            softmax_step(st, rw, qf, tk, nc, tS, tO, smem + C::kP, row0 >> 4, step, first, vref, vinv, l);
           fence_proxy_async_smem();
           tc::fence_before();
           __syncwarp();
@@ -939,6 +931,7 @@ cudaError_t launch_tree_i8_tpl(const TreeParams& p, const TreeSplit& sp, cudaStr
   using C = tree_i8::Cfg<D>;
   static_assert(sizeof(tree_i8::State) <= C::kStateBytes, "state");
   static_assert(C::kSmem <= 227 * 1024, "shared memory");
+  static_assert(C::kSlots >= 2 && C::kSlots <= tree_i8::kMaxSlots, "ring");
   constexpr int kDevices = 64;
   auto kern = tree_i8::tree_i8_kernel<D>;
   static std::once_flag once[kDevices];
