@@ -456,6 +456,10 @@ pkv_status pkv_read_cache(const pkv_tensor* key, const pkv_tensor* value, const 
  * the full context).  A context length out of range sets PKV_DEVERR_CONTEXT_LEN and leaves
  * the sequence's row as it was.  Workspace: the decode workspace, as described for
  * pkv_paged_attention_decode, its need given by pkv_tree_workspace_bytes (num_tokens = num_seqs).
+ * With bf16 queries a softmax weight times its value scale is rounded once to 16 bits: by at
+ * most 2^-11 of itself, or, if it is small, by 2^-31 of the largest such product in its row
+ * (value scales below 2^-80 count as 2^-80 there; above 2^90 sums lose bits).  With f32 queries
+ * it stays in binary32.
  */
 pkv_status pkv_paged_attention_decode_quantized(const pkv_tensor* out, const pkv_tensor* query,
                                                 const pkv_tensor* key_cache, const pkv_tensor* value_cache,

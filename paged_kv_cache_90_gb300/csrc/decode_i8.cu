@@ -2,7 +2,9 @@
 // token-scaled int8 cache.
 //
 // For a sequence's row h, position j and the caches' codes ck, cv with scales sk, sv:
-//   z_j = sk_j (q . ck_j) scale log2 e,  p_j = 2^(z_j - m),  out = sum_j (p_j sv_j) cv_j / sum_j p_j.
+//   z_j = sk_j (q . ck_j) scale log2 e,  p_j = 2^(z_j - m),  out = sum_j (p_j sv_j) cv_j / sum_j p_j
+// with any m; here the largest z_j + log2 sv_j (i8::scale_exponent), which puts the row's largest
+// product p_j sv_j near the top of f16.
 //
 // What bounds it is HBM: 2 (D + 4) bytes a position and KV head, for 8 heads of 128 about 31
 // operations a byte.  What it must not do is spend instructions: a code is widened once, in
@@ -16,10 +18,10 @@
 // for 8 of 32768.
 //
 // A warp takes 32 positions of a tile of 128, its loads of K a step ahead and of V during the
-// scores; 12 warps on an SM keep about 90 KB on the way.  A warp has its own maximum (moved when
-// a score exceeds it by 2^8), its own power of two for the value scales, and its own sums; the
-// four are folded at an item's end, in order.  Weights are f16 relative to that power of two (at
-// most half a step off, 2^-11, as the widening is exact), everything else is binary32.
+// scores; 12 warps on an SM keep about 90 KB on the way.  A warp has its own reference m of a row
+// (moved when a token exceeds it by 2^8) and its own sums; the four are folded at an item's end,
+// in order.  The products p_j sv_j are rounded to f16: half a step, 2^-11, down to 2^-20 of the
+// row's largest, 2^-31 of that below.  Everything else is exact (the widening) or binary32.
 #include "i8_codes.cuh"
 #include "tree_split.cuh"
 
@@ -72,7 +74,7 @@ template <int D, int NT>
 struct Shared {
   Range range;
   longlong2 warp_sum[kWarps];
-  float m[kWarps][8 * NT], l[kWarps][8 * NT], vref[kWarps];
+  float m[kWarps][8 * NT], l[kWarps][8 * NT];
   alignas(16) float o[kWarps][8 * NT][D + 4];
 };
 
@@ -175,8 +177,8 @@ decode_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
       qf[n][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
     }
 
-    float m[NT][2], l[NT][2], vref = 0.f, vinv = 0.f;  // of rows 2t, 2t + 1 (l: this lane's tokens)
-    float o[NT][2 * kW][4];                            // O^T: see the products
+    float m[NT][2], l[NT][2];  // of rows 2t, 2t + 1 (l: this lane's tokens)
+    float o[NT][2 * kW][4];    // O^T: see the products
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       m[n][0] = m[n][1] = -INFINITY;
@@ -218,17 +220,16 @@ decode_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
           }
         }
       }
-      // the scales of the lane's tokens 16 u + 8 h + g
-      float tk[2][2], tv[2][2];
-      const float av = fabsf(vs);
-      bool move = av < INFINITY && av > 16.f * vref && pos >= lo;  // (0 beyond the end)
-      const float wv = av < INFINITY && pos >= lo ? av : 0.f;
+      // the scales of the lane's tokens 16 u + 8 h + g, and the value scales' exponents
+      float tk[2][2], tv[2][2], ex[2][2];
+      const float vex = i8::scale_exponent(vs);
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           tk[u][h] = __shfl_sync(0xffffffffu, ks, 16 * u + 8 * h + g);
           tv[u][h] = __shfl_sync(0xffffffffu, vs, 16 * u + 8 * h + g);
+          ex[u][h] = __shfl_sync(0xffffffffu, vex, 16 * u + 8 * h + g);
         }
       const bool cut = pos0 + 32 > L || pos0 < lo;  // some token is not attended to
       // the next step's codes and scales, and the entries of the one after it
@@ -238,6 +239,7 @@ decode_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
         e_next = j + 2 < steps ? entry(pos + kBN) : 0;
       }
       pos -= kBN;
+      bool move = false;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -251,31 +253,23 @@ decode_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
             for (int r = 0; r < 2; ++r) {
               float& z = s[u][n][2 * h + r];
               z = hidden ? -INFINITY : z * tk[u][h] * qf[n][r];
-              move |= z > m[n][r] + kGap;
+              move |= z + ex[u][h] > m[n][r] + kGap;
             }
         }
       if (__any_sync(0xffffffffu, move)) {
-        float valpha = 1.f;
-        const float top = i8::warp_max(wv);
-        if (top > 16.f * vref) {
-          const float ref = i8::power_above(top);
-          valpha = vref / ref;  // (both powers of two, or 0)
-          vref = ref;
-          vinv = 1.f / ref;
-        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float a[2];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            float mx = fmaxf(fmaxf(s[0][n][r], s[0][n][2 + r]), fmaxf(s[1][n][r], s[1][n][2 + r]));
+            float mx = fmaxf(fmaxf(s[0][n][r] + ex[0][0], s[0][n][2 + r] + ex[0][1]),
+                             fmaxf(s[1][n][r] + ex[1][0], s[1][n][2 + r] + ex[1][1]));
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
             const bool go = mx > m[n][r] + kGap || (m[n][r] == -INFINITY && mx > -INFINITY);
             a[r] = go ? fast_exp2(m[n][r] - mx) : 1.f;  // (0 from -infinity)
             if (go) m[n][r] = mx;
             l[n][r] *= a[r];
-            a[r] *= valpha;
           }
 #pragma unroll
           for (int i = 0; i < 2 * kW; ++i) {
@@ -290,7 +284,8 @@ decode_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
       uint32_t pb[2][NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0], r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+        const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - i8::kTopWeight;
+        const float r1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - i8::kTopWeight;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -298,8 +293,7 @@ decode_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
             const float x = fast_exp2(s[u][n][2 * h] - r0), y = fast_exp2(s[u][n][2 * h + 1] - r1);
             l[n][0] += x;
             l[n][1] += y;
-            const float f = tv[u][h] * vinv;
-            pb[u][n][h] = transpose8x8(half2_bits(x * f, y * f));
+            pb[u][n][h] = transpose8x8(half2_bits(x * tv[u][h], y * tv[u][h]));
           }
       }
       // O^T: two products for each of the lane's words of V, whose first 8 rows are the lanes'
@@ -343,7 +337,6 @@ decode_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
               make_float4(o[n][2 * w][r], o[n][2 * w][2 + r], o[n][2 * w + 1][r], o[n][2 * w + 1][2 + r]);
       }
     }
-    if (lane == 0) sh.vref[warp] = vref;
     __syncthreads();
     constexpr int kPer = kThreads / kRows;  // threads of a row
     const int r = tid / kPer, c0 = tid % kPer;
@@ -357,7 +350,6 @@ decode_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
         // (a warp whose scores are all NaN has no maximum: it counts as it stands)
         f[w] = sh.m[w][r] == -INFINITY ? 1.f : fast_exp2(sh.m[w][r] - ref);
         den += sh.l[w][r] * f[w];
-        f[w] *= sh.vref[w];
       }
       const bool whole = it.begins() && it.ends();
       const float inv = !whole ? 1.f : den != 0.f ? 1.f / den : 0.f;

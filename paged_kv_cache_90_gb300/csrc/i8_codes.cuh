@@ -23,17 +23,20 @@ __device__ __forceinline__ uint2 widen4_flipped(uint32_t u) {
 __device__ __forceinline__ uint32_t flip4(uint32_t w) { return w ^ 0x80808080u; }
 __device__ __forceinline__ uint2 widen4(uint32_t w) { return widen4_flipped(flip4(w)); }
 
-// Largest of a warp's values, NaN aside (an order-preserving map to integers).
-__device__ __forceinline__ float warp_max(float x) {
-  const int i = __float_as_int(x == x ? x : -INFINITY);
-  const int o = __reduce_max_sync(0xffffffffu, i ^ ((i >> 31) & 0x7fffffff));
-  return __int_as_float(o ^ ((o >> 31) & 0x7fffffff));
-}
+// A weight times its token's value scale is an f16 operand.  A row's weights are 2^(z - m +
+// kTopWeight) with m the largest z + scale_exponent of the tokens that it sees: the products
+// then reach 2^kTopWeight and, with a reference that lags by 2^8 and a scale's fraction below 2,
+// stay under 2^15.  The weights themselves and their sum are binary32; a product smaller than
+// 2^-20 of the row's largest is a subnormal f16 number, off by at most 2^-31 of that.
+constexpr float kTopWeight = 6.f;
 
-// The power of two at or above x > 0 (subnormal ones: the smallest normal; at most 2^127).
-__device__ __forceinline__ float power_above(float x) {
-  const uint32_t b = __float_as_uint(fmaxf(x, 0x1p-126f));
-  return fminf(__uint_as_float((b & 0x7f800000u) + ((b & 0x7fffffu) ? 0x800000u : 0u)), 0x1p127f);
+// floor(log2 |s|) of a value scale; that of 2^-80 for smaller ones, 0 among them, so that a weight
+// is below 2^(14 + 80) and a sum of 2^30 of them a binary32 number.  (Scales below 2^-100 lose
+// bits, as do sums beside scales above 2^90: 2^-126 is the smallest weight.)  What is no number
+// moves no reference.
+__device__ __forceinline__ float scale_exponent(float s) {
+  const float a = fabsf(s), b = a < INFINITY ? fmaxf(a, 0x1p-80f) : 0x1p-80f;
+  return float(int(__float_as_uint(b) >> 23) - 127);
 }
 
 // The power of two that a query row with largest magnitude `top` is multiplied by before it

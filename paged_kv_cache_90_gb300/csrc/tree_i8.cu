@@ -7,7 +7,7 @@
 // there are, and few rows cost little:
 //   S^T = K Q^T         M = 128 tokens, N = rows, K = D: K codes widened to f16 and Q (f16) in
 //                       shared memory, S^T in tensor memory, lane = token
-//   P^T = 2^(S ks c - m) vs   by one thread per token, written to shared memory as f16
+//   P^T = 2^(S ks c - m) vs   by one thread per token, written to shared memory as f16 (m: see below)
 //   O^T += V^T P^T      M = D, N = rows, K = 128 tokens: V codes widened to f16, O^T in
 //                       tensor memory, lane = column of the head
 // The rows are shared by two softmax warpgroups (one, if there are at most 16); every key tile is
@@ -15,11 +15,13 @@
 //
 // The codes are whole numbers, so f16 holds them exactly; a query row is scaled by a power of
 // two that brings its largest element to 2^14, so its bf16 values are exact down to 2^-29 of
-// that.  A weight times its value scale is rounded to f16 (half a step, 2^-11), relative to the
-// running largest value scale, a power of two; maximum, sum, scores and output stay in binary32.
-// A row's reference maximum moves when a score exceeds it by 2^8, the value scales' when one
-// exceeds it by 2^4: whether any thread of the warpgroup saw one is one barrier per tile, and
-// only then are the maxima looked for.
+// that.  A weight times its value scale is rounded to f16, relative to a row's reference m: the
+// largest of score + log2 of the value scale (i8::scale_exponent) among the tokens that the row
+// sees, so neither a token of little weight nor a hidden one takes bits from the rest, whatever
+// its scale.  Half a step, 2^-11, down to 2^-20 of the row's largest product, 2^-31 of that below.
+// Sum, scores and output stay in binary32.  A reference moves when a row's largest exceeds it by
+// 2^8: whether any thread of the warpgroup saw that is one barrier per tile (a thread adds its
+// token's exponent once, to the largest of its rows), and only then are the maxima looked for.
 //
 // A tile is 2 x 128 x (D + 4) bytes from HBM, and 2 x 128 x D codes to widen: about 27 warp
 // instructions for 512 codes (an exclusive-or, two byte permutes and two subtractions for four
@@ -95,13 +97,11 @@ enum Bar { kQFull = 0, kCodeFull, kCodeEmpty = kCodeFull + kMaxSlots, kKFull = k
 
 // What a warpgroup keeps of its rows.
 struct alignas(16) Rows {
-  float m[kHalfRows];        // reference maximum (base 2), -infinity before the first score
-  float lift[kHalfRows];     // -m; where that is infinite kNoLift, with which every score moves it
-  float old[kHalfRows];      // the last move's lift before it
-  float alpha_l[kHalfRows];  // the last move's factors on the sums and on the output
-  float alpha_o[kHalfRows];
-  float part[4][16];          // of a reduction over the tokens: each warp's
-  float vpart[4];
+  float m[kHalfRows];      // reference (base 2), -infinity before the first score
+  float lift[kHalfRows];   // kTopWeight - m; where m is infinite kNoLift, with which every score moves it
+  float old[kHalfRows];    // the last move's lift before it
+  float alpha[kHalfRows];  // the last move's factor on the sum and the output
+  float part[4][16];       // of a reduction over the tokens: each warp's
 };
 
 constexpr float kNoLift = 3.402823466e38f;
@@ -233,6 +233,7 @@ struct Token {
   int id;          // the warpgroup's barrier
   int warp, lane;  // of the warpgroup
   float ks, vs;    // the token's scales
+  float ex;        // the value scale's exponent
   bool valid;      // the token is a position of the row's range
   bool cut;        // a tile where some row may not see some token: `keep` has this one's rows
   uint64_t keep;
@@ -279,15 +280,15 @@ __device__ __forceinline__ float exponentials(const uint32_t (&w)[16], const flo
   return over;
 }
 
-// Weights times the token's value scale `vn`, as f16, to `row` (the token's row of P, swizzled
-// by `sw`).  With kKeep a row that does not see the token has a product of 0 whatever `vn` is.
+// Weights times the token's value scale `vs`, as f16, to `row` (the token's row of P, swizzled
+// by `sw`).  With kKeep a row that does not see the token has a product of 0 whatever `vs` is.
 template <bool kKeep>
-__device__ __forceinline__ void store_weights(const uint64_t (&pw)[8], float vn, uint32_t keep, uint4* row, int c, int sw) {
-  const uint64_t vn2 = pack2(vn, vn);
+__device__ __forceinline__ void store_weights(const uint64_t (&pw)[8], float vs, uint32_t keep, uint4* row, int c, int sw) {
+  const uint64_t vs2 = pack2(vs, vs);
   uint32_t h[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float2 x = unpack2(mul2(pw[i], vn2));
+    float2 x = unpack2(mul2(pw[i], vs2));
     if (kKeep) {
       if (!(keep >> (2 * i) & 1u)) x.x = 0.f;
       if (!(keep >> (2 * i + 1) & 1u)) x.y = 0.f;
@@ -335,45 +336,38 @@ __device__ __forceinline__ float reduce_rows(int id, int warp, int lane, float (
   return kMax ? fmaxf(fmaxf(a[0], a[16]), fmaxf(a[32], a[48])) : (a[0] + a[16]) + (a[32] + a[48]);
 }
 
-// One key tile for the nc x 16 rows of a warpgroup.  `vref`: the power of two that value
-// scales are taken relative to (0 at first), `vinv` its inverse.
+// One key tile for the nc x 16 rows of a warpgroup.
 //
 // The weights are taken relative to the references as they are.  If one then turns out to
 // exceed its reference by kGap the maxima are looked for, the references moved, and the tile's
 // weights taken back and computed anew (a weight cut off at 2^kTop loses nothing: relative to the
 // new reference the sum it was added to is below 2^-kTop).  An item's first tile starts there.
 __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* qf, const Token& tk, int nc, uint32_t tS,
-                                             uint32_t tO, unsigned char* ptile, int c0, int step, bool first,
-                                             float& vref, float& vinv, Sums& l) {
+                                             uint32_t tO, unsigned char* ptile, int c0, int step, bool first, Sums& l) {
   // (`ptile`: P, 64 rows of 128 tokens after another; `c0`: the warpgroup's first chunk of 16 rows)
   const int t = 32 * tk.warp + tk.lane;
   auto row = [&](int c) { return reinterpret_cast<uint4*>(ptile + ((c0 + c) >> 2) * (kBN * 128) + t * 128); };
   // (the product of the step before has read P)
   if (step > 0) (void)wait_warp(st, kODone + ((step - 1) & 1), uint32_t((step - 1) >> 1) & 1u);
-  const float av = fabsf(tk.vs);
-  float vn = tk.valid ? tk.vs * vinv : 0.f;
+  const float vs = tk.valid ? tk.vs : 0.f;
   if (!first) {
     float over = -INFINITY;
-    // (a value scale that is no number, and rows that must not meet it: the other way)
-    bool move = (tk.valid && av > 16.f * vref && av < INFINITY) || (tk.cut && !(fabsf(vn) <= 3.4e38f));
 #pragma unroll 1
     for (int c = 0; c < nc; ++c) {
       uint32_t w[16];
       uint64_t pw[8];
       ld16(tS + 16 * c, w);
       over = fmaxf(over, exponentials(w, qf + 16 * c, rw.lift + 16 * c, tk.ks, pw));
-      store_weights<false>(pw, vn, 0u, row(c), (c0 + c) & 3, t & 7);
+      store_weights<false>(pw, vs, 0u, row(c), (c0 + c) & 3, t & 7);
       l.chunk(c, [&](uint64_t (&x)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = add2(x[i], pw[i]);
       });
     }
-    if (!group_any(tk.id, move || over > kGap)) return;
+    // (a value scale that is no number, and rows that must not meet it: the other way)
+    if (!group_any(tk.id, over + tk.ex > kGap + i8::kTopWeight || (tk.cut && !(fabsf(vs) < INFINITY)))) return;
   }
   // the tile's maxima, row by row, and the new references
-  const float wv = i8::warp_max(tk.valid && av < INFINITY ? av : 0.f);
-  if (tk.lane == 0) rw.vpart[tk.warp] = wv;
-  float valpha = 1.f;
 #pragma unroll 1
   for (int c = 0; c < nc; ++c) {
     float x[16];
@@ -383,30 +377,18 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
       ld16(tS + 16 * c, w);
       lds16(qf + 16 * c, f);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(w[i]) * tk.ks * f[i];
+      for (int i = 0; i < 16; ++i) x[i] = fmaf(__uint_as_float(w[i]) * tk.ks, f[i], tk.ex);
     }
     const float mx = reduce_rows<true>(tk.id, tk.warp, tk.lane, x, rw.part);
-    if (c == 0) {  // (vpart is complete behind the barrier in there)
-      const float top = fmaxf(fmaxf(rw.vpart[0], rw.vpart[1]), fmaxf(rw.vpart[2], rw.vpart[3]));
-      if (top > 16.f * vref) {
-        const float ref = i8::power_above(top);
-        valpha = vref / ref;  // (both powers of two, or 0)
-        vref = ref;
-        vinv = 1.f / ref;
-        vn = tk.valid ? tk.vs * vinv : 0.f;
-      }
-    }
     if (tk.warp == 0 && !(tk.lane & 1)) {
       const int r = 16 * c + (tk.lane >> 1);
       const float m = rw.m[r];
       const bool go = mx > m + kGap || (m == -INFINITY && mx > -INFINITY);
       const float m2 = go ? mx : m;
-      const float a = go ? fast_exp2(m - m2) : 1.f;  // (0 from -infinity)
       rw.m[r] = m2;
       rw.old[r] = first ? -INFINITY : rw.lift[r];
-      rw.lift[r] = m2 == -INFINITY ? kNoLift : -m2;
-      rw.alpha_l[r] = a;
-      rw.alpha_o[r] = a * valpha;
+      rw.lift[r] = m2 == -INFINITY ? kNoLift : i8::kTopWeight - m2;
+      rw.alpha[r] = go ? fast_exp2(m - m2) : 1.f;  // (0 from -infinity)
     }
     group_sync(tk.id);
   }
@@ -426,16 +408,16 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
     (void)exponentials(w, qf + 16 * c, rw.lift + 16 * c, tk.ks, pw);
     l.chunk(c, [&](uint64_t (&x)[8]) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = fma2(x[i], reinterpret_cast<const uint64_t*>(rw.alpha_l + 16 * c)[i], pw[i]);
+      for (int i = 0; i < 8; ++i) x[i] = fma2(x[i], reinterpret_cast<const uint64_t*>(rw.alpha + 16 * c)[i], pw[i]);
     });
     if (tk.cut)
-      store_weights<true>(pw, vn, uint32_t(tk.keep >> (16 * c)), row(c), (c0 + c) & 3, t & 7);
+      store_weights<true>(pw, vs, uint32_t(tk.keep >> (16 * c)), row(c), (c0 + c) & 3, t & 7);
     else
-      store_weights<false>(pw, vn, 0u, row(c), (c0 + c) & 3, t & 7);
+      store_weights<false>(pw, vs, 0u, row(c), (c0 + c) & 3, t & 7);
     if (first) continue;
     ld16(tO + 16 * c, w);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * rw.alpha_o[16 * c + i]);
+    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * rw.alpha[16 * c + i]);
     tc::st16(tO + 16 * c, w);
   }
   tc::wait_st();
@@ -500,7 +482,7 @@ struct Part {
 // 32 columns of a row at a time.
 template <int D>
 __device__ __forceinline__ void write_rows(const TreeParams& p, const TreeSplit& sp, const Part& pt, Rows& rw, int id,
-                                           int row0, int warp, int lane, int nc, uint32_t tO, float vref, int div, Sums& l) {
+                                           int row0, int warp, int lane, int nc, uint32_t tO, int div, Sums& l) {
   const int64_t prow = int64_t(2 * blockIdx.x + (pt.begins ? 1 : 0)) * sp.rows;
   const int col = 32 * warp + lane;
 #pragma unroll 1
@@ -517,7 +499,7 @@ __device__ __forceinline__ void write_rows(const TreeParams& p, const TreeSplit&
     const float sum = reduce_rows<false>(id, warp, lane, x, rw.part);
     if (warp == 0 && !(lane & 1)) {
       const int i = 16 * c + (lane >> 1), r = row0 + i;
-      rw.alpha_o[i] = pt.whole ? (sum != 0.f ? vref / sum : 0.f) : vref;
+      rw.alpha[i] = !pt.whole ? 1.f : sum != 0.f ? 1.f / sum : 0.f;
       if (!pt.whole && r < pt.rows) sp.ml[prow + r] = make_float2(rw.m[i], sum);
     }
     group_sync(id);
@@ -532,7 +514,7 @@ __device__ __forceinline__ void write_rows(const TreeParams& p, const TreeSplit&
                            int64_t(pt.kvh * p.group + h) * p.out_stride_h + col;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        if (i < n) *out = __float2bfloat16_rn(__uint_as_float(w[i]) * rw.alpha_o[16 * c + i]);
+        if (i < n) *out = __float2bfloat16_rn(__uint_as_float(w[i]) * rw.alpha[16 * c + i]);
         out += p.out_stride_h;
         if (++h == p.group) {
           h = 0;
@@ -543,7 +525,7 @@ __device__ __forceinline__ void write_rows(const TreeParams& p, const TreeSplit&
       float* o = sp.o + (prow + r0) * D + col;
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if (i < n) o[i * D] = __uint_as_float(w[i]) * rw.alpha_o[16 * c + i];
+        if (i < n) o[i * D] = __uint_as_float(w[i]) * rw.alpha[16 * c + i];
     }
   }
 }
@@ -848,7 +830,6 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
         const Extent& e = it.q.e;
         const uint32_t tO = tmem + C::kO + ob * 128 + row0 + lane_off;
         const float* qf = st->qf[item & 1][wg];
-        float vref = 0.f, vinv = 0.f;  // (and its inverse)
         Sums l;
 #pragma unroll
         for (int i = 0; i < kHalfRows / 2; ++i) l.a[i >> 3][i & 7] = 0ull;
@@ -889,6 +870,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
           const int sl = step % kScaleSlots;  // (the tile's scales are there: its K waited for them)
           tk.ks = st->scales[sl][0][t];
           tk.vs = st->scales[sl][1][t];
+          tk.ex = i8::scale_exponent(tk.vs);
           const uint32_t tS = tmem + C::kS + (step & 1) * 128 + row0 + lane_off;
           if (tk.cut) {
             hide(tS, nc, tk.ks, tk.keep);
@@ -896,7 +878,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
           }
           const bool first = j == it.j0;
           if (nc > 0)
-            softmax_step(st, rw, qf, tk, nc, tS, tO, smem + C::kP, row0 >> 4, step, first, vref, vinv, l);
+            softmax_step(st, rw, qf, tk, nc, tS, tO, smem + C::kP, row0 >> 4, step, first, l);
           fence_proxy_async_smem();
           tc::fence_before();
           __syncwarp();
@@ -908,7 +890,7 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
         if (it.valid()) queries(ItemRows(p, sp, it));  // (the next item's scores, while this one is written)
         (void)wait_warp(st, kODone + ((step - 1) & 1), uint32_t((step - 1) >> 1) & 1u);
         tc::fence_after();
-        write_rows<D>(p, sp, pt, rw, tk.id, row0, q, lane, nc, tO, vref, div, l);
+        write_rows<D>(p, sp, pt, rw, tk.id, row0, q, lane, nc, tO, div, l);
         tc::fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&st->bars[kOFree + ob]);
