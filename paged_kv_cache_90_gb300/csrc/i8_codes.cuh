@@ -40,10 +40,11 @@ __device__ __forceinline__ float scale_exponent(float s) {
 }
 
 // The power of two that a query row with largest magnitude `top` is multiplied by before it
-// becomes f16: 2^(14 - exponent of the largest), kept within 2^-100 .. 2^100.
+// becomes f16: 2^(14 - exponent of the largest), which is at least 2^-113, and at most 2^126, whose
+// inverse is a normal number (the smallest bf16 number, 2^-133, then becomes 2^-7).
 __device__ __forceinline__ int query_shift(float top) {
   const int ex = int(__float_as_uint(top) >> 23) - 127;
-  return top > 0.f && top < INFINITY ? max(-100, min(100, 14 - ex)) : 0;
+  return top > 0.f && top < INFINITY ? min(126, 14 - ex) : 0;
 }
 __device__ __forceinline__ float power(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
 
