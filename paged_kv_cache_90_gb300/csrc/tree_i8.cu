@@ -466,7 +466,8 @@ __device__ __forceinline__ void load_queries(const TreeParams& p, const TreeSpli
         }
         *reinterpret_cast<uint4*>(q + (col >> 6) * Cfg<D>::kQUnit + r * 128 + (((col >> 3) & 7) ^ (r & 7)) * 16) =
             make_uint4(h[0], h[1], h[2], h[3]);
-        if (col == 0) qf[i] = p.qk_scale_log2 * inv;
+        // (never 0, with which a hidden score of -infinity would be NaN)
+        if (col == 0) qf[i] = fmaxf(p.qk_scale_log2 * inv, 0x1p-149f);
       }
     }
   }
