@@ -338,14 +338,14 @@ pkv_status pkv_reshape_and_cache_amax(const pkv_tensor* key, const pkv_tensor* v
  * Pair i (i < rotary_dim / 2) of a head at position p is turned by the angle
  * a = p * frequency[i]:  (x, y) -> magnitude * (x cos a - y sin a, y cos a + x sin a).
  * The pair is columns (i, i + rotary_dim / 2), or (2i, 2i + 1) if interleaved; columns
- * from rotary_dim on are copied.  The angle is reduced in 64-bit fixed point (a whole
- * turn = 2^64), so far positions lose nothing.
+ * from rotary_dim on are copied.  The angle is reduced in fixed point, with the frequency's
+ * turn per position to 2^-97, so that cosine and sine are as good at any position.
  */
 typedef struct pkv_rotary {
   int32_t rotary_dim;   /* even, 0 (no rotation) to head_dim */
   int32_t interleaved;  /* 0 or 1 */
   double magnitude;     /* factor on cosine and sine; 1 unless the scaling asks for another */
-  double frequency[64]; /* radians per position, for each pair */
+  double frequency[64]; /* radians per position, for each pair; at most 2^64 in magnitude */
 } pkv_rotary;
 
 /* How the frequencies f_i = base^(-2 i / rotary_dim) are changed for contexts longer than
@@ -392,7 +392,7 @@ pkv_status pkv_rotary_init(pkv_rotary* rotary, int32_t rotary_dim, int32_t inter
  * value_cache      as for pkv_reshape_and_cache: the key's dtype or e4m3; or PKV_I8 with
  *                  k_scales and v_scales as for pkv_quantize_and_cache (NULL otherwise).
  * slot_mapping     [num_tokens] int64, contiguous, distinct slots.
- * rotary           host pointer; rotary_dim <= head_dim; finite frequencies and magnitude.
+ * rotary           host pointer; rotary_dim <= head_dim; frequencies as above, finite magnitude.
  * Base pointers and strides of query, query_out, key and value: multiples of 16 bytes.
  */
 pkv_status pkv_rotary_and_cache(const pkv_tensor* query_out, const pkv_tensor* query, const pkv_tensor* key,

@@ -200,6 +200,40 @@ pkv_status tree_prepare(const pkv_tensor* out, const pkv_tensor* query, const pk
   return PKV_OK;
 }
 
+// f radians as a part of a turn in units of 2^-96, rounded to nearest: *high 2^32 + *low.  f is
+// taken as the number that it is, m 2^e, and the turn from a product of whole numbers, so that
+// nothing is lost but the last bit: at position p the angle is off by at most p 2^-97 turns.
+// |f| <= 2^64, so that the 256 bits of 1 / 2 pi below are enough.
+void radians_to_turn(double f, uint64_t* high, uint32_t* low) {
+  static const uint64_t kInverse[4] = {0x7f9458eaf7aef158ull, 0x36d8a5664f10e410ull, 0x7f09d5f47d4d3770ull,
+                                       0x28be60db9391054aull};  // floor(2^256 / 2 pi), lowest first
+  int e;
+  const uint64_t m = uint64_t(std::ldexp(std::frexp(std::fabs(f), &e), 53));  // (exact)
+  uint64_t x[7] = {0, 0, 0, 0, 0, 0, 0}, carry = 0;  // m / 2 pi, in units of 2^-256
+  for (int i = 0; i < 4; ++i) {
+    const unsigned __int128 y = static_cast<unsigned __int128>(m) * kInverse[i] + carry;
+    x[i] = uint64_t(y);
+    carry = uint64_t(y >> 64);
+  }
+  x[4] = carry;
+  const int shift = 160 - (e - 53);  // of units of 2^-256 to those of 2^-96, for m 2^(e - 53)
+  if (shift > 320) {  // (less than half a unit)
+    *high = 0;
+    *low = 0;
+    return;
+  }
+  auto bits = [&](int at) {  // 64 of them from bit `at` on
+    const int w = at >> 6, o = at & 63;
+    return o ? x[w] >> o | x[w + 1] << (64 - o) : x[w];
+  };
+  unsigned __int128 n = static_cast<unsigned __int128>(bits(shift)) |
+                        static_cast<unsigned __int128>(shift + 64 < 384 ? bits(shift + 64) : 0) << 64;
+  n += bits(shift - 1) & 1;
+  if (f < 0) n = -n;
+  *high = uint64_t(n >> 32);
+  *low = uint32_t(n);
+}
+
 // Blocks of a tensor-core kernel.
 int tree_grid(int num_sms, int per_sm) {
   return per_sm * (num_sms < int(TreeSplit::kMaxSms) ? num_sms : int(TreeSplit::kMaxSms));
@@ -312,9 +346,9 @@ pkv_status pkv_rotary_and_cache(const pkv_tensor* query_out, const pkv_tensor* q
   p.magnitude = float(rotary->magnitude);
   for (int i = 0; i < rotary->rotary_dim / 2; ++i) {
     const double f = rotary->frequency[i];
-    if (!std::isfinite(f)) return fail(PKV_ERR_INVALID_ARG, "rotary frequency %d is not finite", i);
-    const double turn = f / kTwoPi, part = turn - std::floor(turn);  // whole turns per position change nothing
-    p.turns[i] = part >= 1.0 ? 0 : uint64_t(part * 0x1p64);
+    if (!(std::fabs(f) <= 0x1p64))
+      return fail(PKV_ERR_INVALID_ARG, "rotary frequency %d is not a number of at most 2^64 in magnitude", i);
+    radians_to_turn(f, &p.turns[i], &p.turns_low[i]);
   }
   if (dry_run() || T == 0 || (p.num_heads == 0 && p.w.num_kv_heads == 0)) return PKV_OK;
   DeviceState* s;

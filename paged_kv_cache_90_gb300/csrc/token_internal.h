@@ -24,7 +24,9 @@ struct TokenParams {
   int rotary_dim;              // 0: no rotation
   bool interleaved;
   float magnitude;
-  uint64_t turns[64];          // pair i turns by turns[i] / 2^64 of a circle per position
+  // pair i turns by turns[i] / 2^64 + turns_low[i] / 2^96 of a circle per position
+  uint64_t turns[64];
+  uint32_t turns_low[64];
 };
 cudaError_t launch_token_write(const TokenParams& p, cudaStream_t stream);
 cudaError_t launch_token_read(const TokenParams& p, cudaStream_t stream);

@@ -9,7 +9,7 @@
 // four passes' loads at a time, and waits for nothing else before them (not for the slot).
 //
 // What it measured: rotary write of 16384 tokens of 32 + 2 x 8 heads of 128 in bf16 (403 MB)
-// 70 us, 5.8 TB/s (a block per token with the cosines in shared memory: 175 us); quantising
+// 71 us, 5.7 TB/s (a block per token with the cosines in shared memory: 175 us); quantising
 // write of 16384 tokens of 2 x 8 heads 31 us, read back into f32 26 us (168 MB, 6.4 TB/s).  The
 // write is held back by its instructions, 190 for 8 columns of two rows, issued in four of five
 // cycles.
@@ -184,15 +184,23 @@ __device__ __forceinline__ float token_scale(uint32_t top) {
   return top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : s >= 0x1p-126f ? s : 0.f;
 }
 
+__device__ __forceinline__ uint64_t angle_at(int64_t pos, uint64_t turn, const uint32_t* low) {
+  uint64_t angle = uint64_t(pos) * turn;
+  if (pos != int32_t(pos)) angle += uint64_t((pos >> 32) * int64_t(*low)) + (uint64_t(uint32_t(pos)) * *low >> 32);
+  return angle;
+}
+
 // One warp per slice of a token's rows: query rows, then key rows, then value rows.  Block
 // (x, y): slice y of kWarps tokens.
 //
-// The angle of pair i is position * turns[i] mod 2^64 in units of 2^-64 turn: a 64-bit
-// product that wraps at whole turns, exact but for the 2^-53 relative error of the
-// frequency, at any position.  Its top 32 bits, a signed fraction of a turn, go to
-// sincospif: the cosines are within 3e-7 whatever the position, where a binary32 angle
-// in radians would lose all its bits past 2^24.  A lane has the same four pairs in every row,
-// so their cosines and sines are in its registers.
+// The angle of pair i is position * (turns[i] + turns_low[i] 2^-32) mod 2^64 in units of 2^-64
+// turn: products of whole numbers that wrap at whole turns, off by 2^-34 turn at the farthest
+// position (the low part is less than 2^-33 turn at those of 32 bits, and left out there: 70.9
+// us in place of 71.3 for a prefill step's write, 70.0 without any).  Its top 32 bits, a signed
+// fraction of a turn, go to sincospif as a binary32 number (24 of them, 1e-7 of a radian): the
+// cosines are within 3e-7 whatever the position, where a binary32 angle in radians would lose
+// all its bits past 2^24.  A lane has the same four pairs in every row, so their cosines and
+// sines are in its registers.
 template <typename Src, int D, Layout kLayout>
 __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_constant__ TokenParams p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows of a pass
@@ -265,7 +273,7 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
       for (int i = 0; i < 4; ++i) {
         const int k = (i < 2 ? pair0 : pair1 - 2) + i;
         turn[i] = kLayout == kHalves ? turning : k < half;
-        const uint64_t angle = turn[i] ? uint64_t(pos) * turns[k] : 0;
+        const uint64_t angle = turn[i] ? angle_at(pos, turns[k], p.turns_low + k) : 0;
         sincospif(float(int32_t(uint32_t(angle >> 32))) * 0x1p-31f, &sn[i], &cs[i]);  // 2^-32 turn, in [-1/2, 1/2)
         cs[i] *= p.magnitude;
         sn[i] *= p.magnitude;
@@ -290,7 +298,8 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
             for (int i = 0; i < 8; ++i) {
               const int c = c0 + i;
               if (c >= p.rotary_dim) break;
-              const uint64_t angle = uint64_t(pos) * turns[c < half ? c : c - half];
+              const int pair = c < half ? c : c - half;
+              const uint64_t angle = angle_at(pos, turns[pair], p.turns_low + pair);
               float s, k;
               sincospif(float(int32_t(uint32_t(angle >> 32))) * 0x1p-31f, &s, &k);
               s *= p.magnitude;
