@@ -58,6 +58,12 @@ __global__ void __launch_bounds__(kWarps * 32) tree_core_kernel(const __grid_con
   __shared__ float2 ml_sh[kWarps];
   const int t = int(blockIdx.x), h = int(blockIdx.y);
   const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+  bool bad;
+  if (h == 0 && threadIdx.x == 0)  // every sequence is checked, those whose rows are none of the batch's too
+    for (int c = t; c < p.num_seqs; c += int(gridDim.x)) {
+      (void)tree::extent(p, c, &bad);
+      if (bad) raise_device_error(p.err, kErrContextLen);
+    }
   // the row's sequence: the last one that starts at or before it
   int s = t;
   if (p.query_start_loc) {
@@ -69,9 +75,7 @@ __global__ void __launch_bounds__(kWarps * 32) tree_core_kernel(const __grid_con
     }
     s = a;
   }
-  bool bad;
   const tree::Extent e = tree::extent(p, s, &bad);
-  if (bad && threadIdx.x == 0 && h == 0) raise_device_error(p.err, kErrContextLen);
   const int node = t - e.q0;
   if (node < 0 || node >= e.n) return;
   const int64_t* mask = p.tree_mask ? p.tree_mask + int64_t(t) * p.mask_stride : nullptr;
