@@ -338,7 +338,7 @@ pkv_status pkv_reshape_and_cache_amax(const pkv_tensor* key, const pkv_tensor* v
  * Pair i (i < rotary_dim / 2) of a head at position p is turned by the angle
  * a = p * frequency[i]:  (x, y) -> magnitude * (x cos a - y sin a, y cos a + x sin a).
  * The pair is columns (i, i + rotary_dim / 2), or (2i, 2i + 1) if interleaved; columns
- * from rotary_dim on are copied.  The angle is reduced in fixed point, with the frequency's
+ * from rotary_dim on are copied (a NaN as some NaN).  The angle is reduced in fixed point, with the frequency's
  * turn per position to 2^-97, so that cosine and sine are as good at any position.
  */
 typedef struct pkv_rotary {

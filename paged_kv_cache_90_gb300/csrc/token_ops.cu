@@ -455,6 +455,12 @@ __global__ void __launch_bounds__(32 * kWarps) token_read_kernel(const __grid_co
       const bool is_v = p0 + u >= tensor;
       const int h = (p0 + u - (is_v ? tensor : 0)) * kRows + sub;
       if (p0 + u >= last || h >= hk) continue;
+      void* dst = const_cast<void*>(is_v ? p.w.value : p.w.key);
+      const int64_t to = t * p.w.src_stride_t + h * p.w.src_stride_h;
+      if (type == kBF16 && kJoined) {  // as they are: a conversion would change a NaN's bits
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + to + c0) = make_uint4(a[u].x, a[u].y, b[u].x, b[u].y);
+        continue;
+      }
       float x[8];
       if (type == kF32) {
         Chunk<F32>::expand(a[u], x);
@@ -474,8 +480,7 @@ __global__ void __launch_bounds__(32 * kWarps) token_read_kernel(const __grid_co
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] *= s[u];
       }
-      store_row<Dst>(const_cast<void*>(is_v ? p.w.value : p.w.key), t * p.w.src_stride_t + h * p.w.src_stride_h, c0, c1,
-                     kJoined, x);
+      store_row<Dst>(dst, to, c0, c1, kJoined, x);
     }
   }
 }
