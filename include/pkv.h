@@ -392,7 +392,7 @@ pkv_status pkv_rotary_init(pkv_rotary* rotary, int32_t rotary_dim, int32_t inter
  * value_cache      as for pkv_reshape_and_cache: the key's dtype or e4m3; or PKV_I8 with
  *                  k_scales and v_scales as for pkv_quantize_and_cache (NULL otherwise).
  * slot_mapping     [num_tokens] int64, contiguous, distinct slots.
- * rotary           host pointer; rotary_dim <= head_dim; frequencies as above, finite magnitude.
+ * rotary           host pointer; rotary_dim <= head_dim; frequencies as above; magnitude finite in f32.
  * Base pointers and strides of query, query_out, key and value: multiples of 16 bytes.
  */
 pkv_status pkv_rotary_and_cache(const pkv_tensor* query_out, const pkv_tensor* query, const pkv_tensor* key,

@@ -330,7 +330,8 @@ pkv_status pkv_rotary_and_cache(const pkv_tensor* query_out, const pkv_tensor* q
   if (rotary->rotary_dim < 0 || rotary->rotary_dim % 2 || rotary->rotary_dim > D)
     return fail(PKV_ERR_INVALID_ARG, "rotary_dim (%d) must be even, 0 to head_dim (%lld)", rotary->rotary_dim, (long long)D);
   if (rotary->interleaved != 0 && rotary->interleaved != 1) return fail(PKV_ERR_INVALID_ARG, "interleaved is 0 or 1");
-  if (!std::isfinite(rotary->magnitude)) return fail(PKV_ERR_INVALID_ARG, "the rotary magnitude must be finite");
+  if (!std::isfinite(float(rotary->magnitude)))
+    return fail(PKV_ERR_INVALID_ARG, "the rotary magnitude must be finite in binary32");
   if (query->shape[1] > 65535) return fail(PKV_ERR_UNSUPPORTED, "too many heads");
   p.query = query->data;
   p.query_out = query_out->data;

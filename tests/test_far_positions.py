@@ -87,6 +87,23 @@ def test_frequencies_past_the_range_are_refused():
         binding.set_option("dry_run", 0)
 
 
+def test_magnitudes_past_binary32_are_refused():
+    """The factor is used in binary32, where a larger double would be infinite."""
+    z = torch.zeros
+    binding.set_option("dry_run", 1)
+    try:
+        for m, fine in ((3.4e38, True), (-3.4e38, True), (0.0, True), (3.5e38, False), (-1e300, False), (math.inf, False)):
+            try:
+                binding.rotary_and_cache(z(1, 1, 64), z(1, 1, 64), z(1, 1, 64), z(1, 1, 64), z(1, dtype=torch.int64),
+                                         z(1, 1, 16, 64), z(1, 1, 16, 64), z(1, dtype=torch.int64),
+                                         binding.rotary(64, magnitude=m))
+                assert fine, m
+            except binding.PkvError as e:
+                assert e.status == 1 and not fine, m
+    finally:
+        binding.set_option("dry_run", 0)
+
+
 def test_two_pi():
     assert float(two_pi()) == 2 * math.pi
     assert str(two_pi().numerator * 10 ** 60 // two_pi().denominator) == \
