@@ -44,7 +44,7 @@
  *   FP8 cache halves the memory of a 16-bit one); other dtypes ignore `scale`.
  *   Token-scaled caches: PKV_I8 codes with one fp32 scale per (slot, KV head) in two
  *   arrays beside the caches (code * scale = value); only the calls that take those
- *   arrays (k_scales, v_scales) accept them.
+ *   arrays (k_scales, v_scales) accept them, and pkv_copy_blocks.
  *   Queries and outputs: PKV_F32 or PKV_BF16, the output in the query's dtype.
  *   Supported head_dim: 64 and 128.  Supported block_size: 2, 4, 8, 16, 32.
  * Streams.  `stream` is a cudaStream_t (NULL = the legacy default stream) of the
@@ -518,9 +518,12 @@ int64_t pkv_tree_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t n
  * block that another sequence still references, the engine copies that block.
  *
  * For each row (src, dst) of src_dst_pairs: cache[dst, :, :, :] = cache[src, :, :, :]
- * (all KV heads, byte copy).  Call once for the key cache and once for the value cache.
+ * (all KV heads, byte copy).  Call once for the key cache and once for the value cache, and
+ * for a token-scaled cache once for each of its scale arrays.
  *
- * cache          [num_blocks, num_kv_heads, block_size, head_dim], layout rules above.
+ * cache          [num_blocks, num_kv_heads, block_size, head_dim], layout rules above (any
+ *                cache dtype, PKV_I8 too); or a scale array [num_blocks, num_kv_heads,
+ *                block_size] f32, last dim contiguous.
  * src_dst_pairs  [num_pairs, 2] int64, contiguous; num_pairs may be 0.
  * Pairs are copied in parallel: destinations must be distinct and no destination may
  * also be a source (breaking this gives an unspecified mix of old and new bytes, never

@@ -327,7 +327,8 @@ def reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, k_scale:
 
 
 def copy_blocks(cache, src_dst_pairs, stream=None) -> None:
-    """cache[dst] = cache[src] for every (src, dst) row of ``src_dst_pairs``."""
+    """cache[dst] = cache[src] for every (src, dst) row of ``src_dst_pairs``; ``cache`` may be
+    the scale array [num_blocks, Hk, block_size] of an int8 cache, which is copied like it."""
     lib = load_library()
     pairs = src_dst_pairs
     if pairs.numel() == 0:

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kWriteThreads) cache_write_e4m3_kernel(const C
   }
 }
 
-// One thread block per (pair, KV head): copy the contiguous bs x D tile.
+// One thread block per (pair, KV head): copy the contiguous bs x D tile, or bs token scales.
 __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const CopyBlocksParams p) {
   const int64_t pair = blockIdx.x;
   const int h = blockIdx.y;
@@ -154,10 +154,19 @@ __global__ void __launch_bounds__(kCopyThreads) copy_blocks_kernel(const CopyBlo
     if (threadIdx.x == 0 && h == 0) raise_device_error(p.err, kErrCopyPair);
     return;
   }
-  const uint4* s = reinterpret_cast<const uint4*>(p.cache + src * p.block_stride_bytes + h * p.head_stride_bytes);
-  uint4* d = reinterpret_cast<uint4*>(p.cache + dst * p.block_stride_bytes + h * p.head_stride_bytes);
-  const int64_t nvec = p.chunk_bytes / 16;
-  for (int64_t i = threadIdx.x; i < nvec; i += kCopyThreads) d[i] = s[i];
+  const unsigned char* from = p.cache + src * p.block_stride_bytes + h * p.head_stride_bytes;
+  unsigned char* to = p.cache + dst * p.block_stride_bytes + h * p.head_stride_bytes;
+  if (p.vec16) {
+    const uint4* s = reinterpret_cast<const uint4*>(from);
+    uint4* d = reinterpret_cast<uint4*>(to);
+    const int64_t nvec = p.chunk_bytes / 16;
+    for (int64_t i = threadIdx.x; i < nvec; i += kCopyThreads) d[i] = s[i];
+  } else {  // scales: a word each
+    const uint32_t* s = reinterpret_cast<const uint32_t*>(from);
+    uint32_t* d = reinterpret_cast<uint32_t*>(to);
+    const int64_t words = p.chunk_bytes / 4;
+    for (int64_t i = threadIdx.x; i < words; i += kCopyThreads) d[i] = s[i];
+  }
 }
 
 // Precondition of a parallel copy: destinations distinct and never a source.  Thread i

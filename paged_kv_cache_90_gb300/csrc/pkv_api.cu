@@ -201,6 +201,14 @@ pkv_status check_cache(const pkv_tensor* c, const char* name, bool i8) {
   return PKV_OK;
 }
 
+pkv_status check_scales(const pkv_tensor* t, const char* name) {
+  pkv_status st = check_basic(t, name, 3);
+  if (st) return st;
+  if ((st = check_dtype(t, name, PKV_F32))) return st;
+  if (reinterpret_cast<uintptr_t>(t->data) & 3) return fail(PKV_ERR_INVALID_ARG, "%s must be 4-byte aligned", name);
+  return PKV_OK;
+}
+
 bool same_layout(const pkv_tensor* a, const pkv_tensor* b) {
   if (a->dtype != b->dtype || a->ndim != b->ndim) return false;
   for (int i = 0; i < a->ndim; ++i)
@@ -798,11 +806,14 @@ pkv_status pkv_decode_append(const pkv_tensor* out, const pkv_tensor* query, con
 
 pkv_status pkv_copy_blocks(const pkv_tensor* cache, const pkv_tensor* src_dst_pairs, pkv_stream stream) {
   pkv_status st;
-  if ((st = check_cache(cache, "cache")) || (st = check_basic(src_dst_pairs, "src_dst_pairs", 2))) return st;
+  const bool scales = cache && cache->ndim == 3;  // of a token-scaled cache
+  if ((st = scales ? check_scales(cache, "scales") : check_cache(cache, "cache", true)) ||
+      (st = check_basic(src_dst_pairs, "src_dst_pairs", 2)))
+    return st;
   if ((st = check_dtype(src_dst_pairs, "src_dst_pairs", PKV_I64))) return st;
   if (src_dst_pairs->shape[1] != 2 || (src_dst_pairs->shape[0] > 1 && src_dst_pairs->stride[0] != 2))
     return fail(PKV_ERR_INVALID_ARG, "src_dst_pairs must be a contiguous [num_pairs, 2] array");
-  if (!supported_head_dim(cache->shape[3]))
+  if (!scales && !supported_head_dim(cache->shape[3]))
     return fail(PKV_ERR_UNSUPPORTED, "head_dim %lld (supported: 64, 128)", (long long)cache->shape[3]);
   if (!supported_block_size(cache->shape[2]))
     return fail(PKV_ERR_UNSUPPORTED, "block_size %lld (supported: 2, 4, 8, 16, 32)", (long long)cache->shape[2]);
@@ -817,7 +828,8 @@ pkv_status pkv_copy_blocks(const pkv_tensor* cache, const pkv_tensor* src_dst_pa
   p.cache = static_cast<unsigned char*>(cache->data);
   p.block_stride_bytes = cache->stride[0] * eb;
   p.head_stride_bytes = cache->stride[1] * eb;
-  p.chunk_bytes = cache->shape[2] * cache->shape[3] * eb;
+  p.chunk_bytes = cache->shape[2] * (scales ? 1 : cache->shape[3]) * eb;
+  p.vec16 = aligned16(cache->data) && (p.block_stride_bytes | p.head_stride_bytes | p.chunk_bytes) % 16 == 0;
   p.num_kv_heads = int(cache->shape[1]);
   p.pairs = static_cast<const int64_t*>(src_dst_pairs->data);
   p.num_pairs = n;

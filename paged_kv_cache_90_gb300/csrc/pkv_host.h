@@ -40,6 +40,8 @@ pkv_status check_basic(const pkv_tensor* t, const char* name, int ndim);
 pkv_status check_dtype(const pkv_tensor* t, const char* name, int a, int b = -1, int c = -1);
 // A cache descriptor; `i8`: token-scaled PKV_I8 caches are taken too.
 pkv_status check_cache(const pkv_tensor* c, const char* name, bool i8 = false);
+// Scales of a token-scaled cache, [num_blocks, num_kv_heads, block_size] f32.
+pkv_status check_scales(const pkv_tensor* t, const char* name);
 bool same_layout(const pkv_tensor* a, const pkv_tensor* b);
 
 }  // namespace pkv

@@ -47,7 +47,8 @@ struct CopyBlocksParams {
   unsigned char* cache;      // base of block 0
   int64_t block_stride_bytes;
   int64_t head_stride_bytes;
-  int64_t chunk_bytes;       // bs * D * elt: one (block, head) tile, contiguous
+  int64_t chunk_bytes;       // bs * D * elt: one (block, head) tile, contiguous (of scales, bs * 4)
+  bool vec16;                // tiles are 16-byte aligned and a multiple of that (else of 4 bytes)
   int num_kv_heads;
   const int64_t* pairs;      // [n, 2]
   int64_t num_pairs;

@@ -12,14 +12,12 @@ namespace {
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
 
-pkv_status check_scales(const pkv_tensor* t, const char* name, const pkv_tensor* cache) {
-  pkv_status st = check_basic(t, name, 3);
+pkv_status check_scales_of(const pkv_tensor* t, const char* name, const pkv_tensor* cache) {
+  const pkv_status st = check_scales(t, name);
   if (st) return st;
-  if ((st = check_dtype(t, name, PKV_F32))) return st;
   for (int i = 0; i < 3; ++i)
     if (t->shape[i] != cache->shape[i])
       return fail(PKV_ERR_INVALID_ARG, "%s must be [num_blocks, num_kv_heads, block_size]", name);
-  if (reinterpret_cast<uintptr_t>(t->data) & 3) return fail(PKV_ERR_INVALID_ARG, "%s must be 4-byte aligned", name);
   return PKV_OK;
 }
 
@@ -38,7 +36,7 @@ pkv_status check_caches(const pkv_tensor* kc, const pkv_tensor* vc, const pkv_te
     return PKV_OK;
   }
   if (!ks || !vs) return fail(PKV_ERR_INVALID_ARG, "an i8 cache needs k_scales and v_scales");
-  if ((st = check_scales(ks, "k_scales", kc)) || (st = check_scales(vs, "v_scales", vc))) return st;
+  if ((st = check_scales_of(ks, "k_scales", kc)) || (st = check_scales_of(vs, "v_scales", vc))) return st;
   if (!same_layout(ks, vs)) return fail(PKV_ERR_INVALID_ARG, "k_scales and v_scales must share their strides");
   return PKV_OK;
 }
