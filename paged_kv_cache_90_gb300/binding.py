@@ -171,6 +171,9 @@ def _ref(t: torch.Tensor, scale: float = 1.0, head_scales: Optional[torch.Tensor
 
 
 _have_cuda = False  # (asked until the answer is yes: the question costs microseconds)
+# The current stream's handle alone (a Stream object takes 3 us to make, a fifth of a small
+# call).  Not a public name of torch's: where it is missing the Stream object is asked.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream) -> ctypes.c_void_p:
@@ -180,8 +183,8 @@ def _stream(stream) -> ctypes.c_void_p:
             _have_cuda = torch.cuda.is_available()
             if not _have_cuda:
                 return ctypes.c_void_p(0)
-        # (the handle alone: a Stream object takes 3 us to make, a fifth of a small call)
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        device = torch.cuda.current_device()
+        return ctypes.c_void_p(_raw_stream(device) if _raw_stream else torch.cuda.current_stream(device).cuda_stream)
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
