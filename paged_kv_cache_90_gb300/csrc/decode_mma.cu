@@ -1,7 +1,5 @@
 // decode_mma.cu — host side of the tensor-core decode kernel: which calls it takes,
 // the TMA tensor maps over the K and V pools, and the launch.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <mutex>
 
@@ -12,9 +10,7 @@
 
 namespace pkv {
 
-namespace {
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -28,10 +24,12 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+namespace {
+
 // 4-D map over a cache [NB, Hk, bs, D]: innermost x = head_dim, y = slot in block,
 // z = KV head, w = block.  One box = `box_rows` slots x 128 bytes, 128-byte swizzle.
 cudaError_t make_cache_map(CUtensorMap* map, const void* base, const DecodeParams& p, int box_rows) {
-  auto fn = encode_fn();
+  auto fn = tensor_map_encoder();
   if (!fn) return cudaErrorNotSupported;
   const bool fp8 = p.kv_dtype == kE4M3;
   const int elt = fp8 ? 1 : 2;
@@ -206,7 +204,7 @@ bool prefill_supported(const DecodeParams& p) {
   if (!(p.head_dim == 64 || p.head_dim == 128)) return false;
   if (!(p.block_size == 8 || p.block_size == 16 || p.block_size == 32)) return false;
   if (p.max_blocks_per_seq > kPrefillMaxTableEntries) return false;
-  if (!encode_fn()) return false;
+  if (!tensor_map_encoder()) return false;
   if ((reinterpret_cast<uintptr_t>(p.query) & 15) || (p.q_stride_s & 7) || (p.q_stride_h & 7)) return false;
   if ((reinterpret_cast<uintptr_t>(p.out) & 15) || (p.out_stride_s & 7) || (p.out_stride_h & 7)) return false;
   return true;
@@ -276,7 +274,7 @@ bool mma_decode_supported(const DecodeParams& p) {
   if (G == 0 || p.q_dtype != kBF16 || p.out_dtype != kBF16) return false;
   if (!(p.block_size == 8 || p.block_size == 16 || p.block_size == 32)) return false;
   if (p.num_seqs < 1) return false;
-  if (!encode_fn()) return false;
+  if (!tensor_map_encoder()) return false;
   // 8-byte query loads and 4-byte output stores
   if ((reinterpret_cast<uintptr_t>(p.query) & 15) || (p.q_stride_s & 7) || (p.q_stride_h & 7)) return false;
   if ((reinterpret_cast<uintptr_t>(p.out) & 15) || (p.out_stride_s & 7) || (p.out_stride_h & 7)) return false;

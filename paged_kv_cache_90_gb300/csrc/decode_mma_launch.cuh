@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include "decode_mma.cuh"
 #include "pkv_internal.h"
@@ -11,6 +12,9 @@
 namespace pkv {
 
 constexpr int kMapCacheDevices = 64;
+
+// The driver's encoder of tensor maps (null if there is none).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 // TMA tensor map over a cache pool [NB, Hk, bs, D] (boxes of `box_rows` slots x 128
 // bytes, 128-byte swizzle), from a per-device cache of the most recent pools.

@@ -177,7 +177,6 @@ pkv_status tree_prepare(const pkv_tensor* out, const pkv_tensor* query, const pk
   p.block_tables = static_cast<const int32_t*>(tables->data);
   p.bt_stride = tables->stride[0];
   p.context_lens = static_cast<const int32_t*>(lens->data);
-  p.cl_stride = 1;
   if (qsl) {
     p.query_start_loc = static_cast<const int32_t*>(qsl->data);
     p.tree_mask = static_cast<const int64_t*>(mask->data);

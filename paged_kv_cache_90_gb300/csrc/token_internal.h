@@ -49,7 +49,6 @@ struct TreeParams {
   const int32_t* block_tables;
   int64_t bt_stride;
   const int32_t* context_lens;
-  int64_t cl_stride;
   const int32_t* query_start_loc;  // null: one row per sequence
   const int64_t* tree_mask;        // null: rows see the whole context (with the window)
   int64_t mask_stride;

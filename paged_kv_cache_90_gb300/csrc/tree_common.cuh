@@ -17,7 +17,7 @@ struct Extent {
 // Sequence s's extent; n = 0 if it has no rows or is out of range (*bad tells which).
 __device__ __forceinline__ Extent extent(const TreeParams& p, int s, bool* bad) {
   Extent e;
-  e.L = __ldg(p.context_lens + s * p.cl_stride);
+  e.L = __ldg(p.context_lens + s);
   e.lo = 0;
   if (p.query_start_loc) {
     e.q0 = __ldg(p.query_start_loc + s);

@@ -43,8 +43,6 @@
 // contexts.  Every wait is bounded; when one runs
 // out the block sets an error bit and a flag that makes every role stop, lets its copies
 // and MMAs land and frees the tensor memory.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <mutex>
 
@@ -130,7 +128,6 @@ __device__ __forceinline__ uint32_t mask_bits(const int64_t* mask, uint64_t word
     past = (1u << sh) - 1u;
     c0 = 0;
   }
-  if (!mask) return past;  // (no mask: every position is before the nodes, n = 0 of them)
   const int w = c0 >> 6, o = c0 & 63;
   uint64_t b = (w == 0 ? word0 : uint64_t(__ldg(mask + w))) >> o;
   if (o > 32 && 64 * (w + 1) < n) b |= uint64_t(__ldg(mask + w + 1)) << (64 - o);
@@ -140,15 +137,14 @@ __device__ __forceinline__ uint32_t mask_bits(const int64_t* mask, uint64_t word
   return past | (bits << sh);
 }
 
-// The positions pos .. pos + 127 of a tile that a row sees, 64 to a word; `mask` null: no
-// drafted nodes.
+// The positions pos .. pos + 127 of a tile that a row sees, 64 to a word.
 __device__ __forceinline__ void tile_bits(const tree::Extent& e, int pos, const int64_t* mask, uint64_t word0,
-                                          int n_hidden, uint64_t (&k)[2]) {
+                                          uint64_t (&k)[2]) {
   auto ones = [](int n) -> uint64_t { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; };
-  if (n_hidden <= 64) {
+  if (e.n <= 64) {
     // bits below sh are positions before the nodes, then come the nodes' bits
     const int sh = e.P - pos;
-    const uint64_t m = word0 & ones(n_hidden);
+    const uint64_t m = word0 & ones(e.n);
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       const int s = sh - 64 * w;
@@ -157,12 +153,10 @@ __device__ __forceinline__ void tile_bits(const tree::Extent& e, int pos, const 
   } else {
 #pragma unroll 1
     for (int w = 0; w < 4; ++w) {
-      const uint64_t b = mask_bits(mask, word0, pos + 32 * w - e.P, n_hidden);
+      const uint64_t b = mask_bits(mask, word0, pos + 32 * w - e.P, e.n);
       if (w & 1) k[w >> 1] |= b << 32; else k[w >> 1] = b;
     }
   }
-#pragma unroll
-  for (int w = 0; w < 2; ++w) k[w] &= ~ones(e.lo - pos - 64 * w);
 }
 
 // Largest of a row's 32 scores at tensor-memory column `ts`; with kCut those not kept
@@ -450,10 +444,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       }
     }
   } else if (warp == 12) {
-    // ---- tiles with positions that are hidden from some row: V rows that are no position
-    // of the sequence's range are zeroed in shared memory (they may hold anything), and
-    // infinities and NaN of drafted nodes taken out of it (0 x infinity would reach the rows
-    // that do not see the node; those that do get them back with the output) -------------------
+    // ---- tiles with positions that are hidden from some row: V rows past the sequence's end
+    // are zeroed in shared memory (they may hold anything), and infinities and NaN of drafted
+    // nodes taken out of it (0 x infinity would reach the rows that do not see the node; those
+    // that do get them back with the output) -------------------------------------------------
     int slot = 0, item = 0;
     uint32_t phase = 0;  // parities of the slots' uses by this warp
     bool ok = true;
@@ -468,15 +462,13 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         if (!(ok = wait_warp(st, kVRaw + slot, phase >> slot & 1u))) break;
         phase ^= 1u << slot;
         unsigned char* vt = smem + (sv - sbase) + slot * C::kOpBytes;
-        const bool scan = p.tree_mask && pos + kBN > e.P;
         constexpr int kCells = 8 * C::kHalves;  // 16-byte cells of a row
         auto cell = [&](int i) {  // (row i / kCells)
           return reinterpret_cast<uint4*>(vt + ((i >> 3) % C::kHalves) * C::kHalfBytes + (i / kCells) * 128 + (i & 7) * 16);
         };
         const int hi = max(0, min(kBN, e.L - pos));
-        for (int i = lane; i < (e.lo - pos) * kCells; i += 32) *cell(i) = make_uint4(0u, 0u, 0u, 0u);
         for (int i = hi * kCells + lane; i < kBN * kCells; i += 32) *cell(i) = make_uint4(0u, 0u, 0u, 0u);
-        for (int q = 0; scan && q < 4; ++q) {  // the drafted nodes, 32 positions to a word
+        for (int q = 0; q < 4; ++q) {  // the drafted nodes, 32 positions to a word
           const int end = min(hi, 32 * q + 32) * kCells;
           uint32_t bad = 0u;
           // (four loads together: one after the other they take longer than the tile's products)
@@ -529,9 +521,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
       const bool row_ok = r < TQ * g && node < e.n;
       const bool warp_ok = __any_sync(0xffffffffu, row_ok);
       const int64_t trow = e.q0 + node;
-      const int64_t* mask = p.tree_mask && row_ok ? p.tree_mask + trow * p.mask_stride : nullptr;
-      const int n_hidden = p.tree_mask ? e.n : 0;
-      const uint64_t word0 = mask ? uint64_t(__ldg(mask)) : 0u;  // (n_hidden = 0: P = L ends the context)
+      const int64_t* mask = p.tree_mask + (row_ok ? trow : int64_t(e.q0)) * p.mask_stride;  // (idle rows: any)
+      const uint64_t word0 = uint64_t(__ldg(mask));
       const uint32_t* bad_rows = st->bad_rows[item % kBadItems];
       const int jt = (e.P - it.q.base) / kBN;  // first tile with drafted nodes
       float m_ref = -INFINITY, l_run = 0.f;
@@ -546,7 +537,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
           float mx = -INFINITY;
           if (cut) {
             uint64_t k[2];
-            tile_bits(e, pos, mask, word0, n_hidden, k);
+            tile_bits(e, pos, mask, word0, k);
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               mx = fmaxf(mx, row_max<true>(tS + 32 * c, uint32_t(k[0])));
@@ -602,7 +593,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
         // (the words of this part's tiles; the others are not this item's)
         const int bw0 = 4 * (max(it.j0, jt) - jt), bw1 = 4 * (it.j1 - jt);
         bool any_bad = false;
-        if (n_hidden > 0 && row_ok)
+        if (row_ok)
           for (int w = bw0; w < bw1; ++w) any_bad |= bad_rows[w] != 0u;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
@@ -664,23 +655,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ 
 
 namespace {
 
-PFN_cuTensorMapEncodeTiled_v12000 tree_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
-
 // 3-D map over the queries [T, Hq, D]: box = 64 columns x the group's heads x `nodes` rows,
 // 128-byte swizzle.
 cudaError_t make_tree_query_map(CUtensorMap* map, const TreeParams& p, int nodes) {
-  auto fn = tree_map_encoder();
+  auto fn = tensor_map_encoder();
   if (!fn) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {cuuint64_t(p.head_dim), cuuint64_t(p.num_heads), cuuint64_t(p.num_tokens)};
   // (the stride of a dimension of one may be anything)
@@ -701,7 +679,7 @@ cudaError_t launch_tree_tc_tpl(const TreeParams& p, TreeSplit sp, cudaStream_t s
   CUtensorMap mq, mk, mv;
   sp.item_nodes = 2 * sp.tq;
   // the tile's rows that can hold nodes: no more than the batch has
-  sp.q_nodes = int(std::min<int64_t>(tree::kBM / p.group, p.query_start_loc ? p.num_tokens : 1));
+  sp.q_nodes = int(std::min<int64_t>(tree::kBM / p.group, p.num_tokens));
   cudaError_t e = make_tree_query_map(&mq, p, sp.q_nodes);
   if (e != cudaSuccess) return e;
   DecodeParams dp{};  // (what the cache maps are made from)
@@ -744,6 +722,7 @@ cudaError_t launch_tree_tc_tpl(const TreeParams& p, TreeSplit sp, cudaStream_t s
 
 }  // namespace
 
+// (a bf16 cache comes with the tree call: there is always a mask and never a window)
 bool tree_tc_supported(const TreeParams& p) {
   if (p.q_dtype != kBF16 || p.kv_dtype != kBF16) return false;
   if (!(p.block_size == 8 || p.block_size == 16 || p.block_size == 32)) return false;
@@ -754,7 +733,7 @@ bool tree_tc_supported(const TreeParams& p) {
   if ((p.num_kv_heads > 1 && p.cs_head == 0) || (p.num_blocks > 1 && p.cs_block == 0)) return false;
   if ((reinterpret_cast<uintptr_t>(p.query) & 15) || (p.q_stride_t & 7) || (p.q_stride_h & 7)) return false;
   if ((reinterpret_cast<uintptr_t>(p.out) & 15) || (p.out_stride_t & 7) || (p.out_stride_h & 7)) return false;
-  return tree_map_encoder() != nullptr;
+  return tensor_map_encoder() != nullptr;
 }
 
 cudaError_t launch_tree_merge(const TreeParams& p, const TreeSplit& sp, cudaStream_t stream) {
