@@ -252,7 +252,7 @@ decode_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
               float& z = s[u][n][2 * h + r];
-              z = hidden ? -INFINITY : z * tk[u][h] * qf[n][r];
+              z = hidden ? -INFINITY : z * (tk[u][h] * qf[n][r]);  // (no factor alone takes it out of range)
               move |= z + ex[u][h] > m[n][r] + kGap;
             }
         }

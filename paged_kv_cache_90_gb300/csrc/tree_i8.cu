@@ -271,7 +271,8 @@ __device__ __forceinline__ float exponentials(const uint32_t (&w)[16], const flo
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int e = 4 * i + 2 * j;
-      const float2 z = unpack2(fma2(mul2(pack2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])), ks2), j ? f.y : f.x,
+      // (the factors first: their product with the sum is the score, so none is out of range before it)
+      const float2 z = unpack2(fma2(pack2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])), mul2(j ? f.y : f.x, ks2),
                                     j ? m.y : m.x));
       over = fmaxf(over, fmaxf(z.x, z.y));
       pw[2 * i + j] = pack2(fast_exp2(min_nan(z.x, kTop)), fast_exp2(min_nan(z.y, kTop)));
@@ -300,8 +301,9 @@ __device__ __forceinline__ void store_weights(const uint64_t (&pw)[8], float vs,
   row[(2 * c + 1) ^ sw] = make_uint4(h[4], h[5], h[6], h[7]);
 }
 
-// A tile that some row may not see all of: scores times the key scale, -infinity for hidden
-// ones, back to tensor memory (the caller goes on with a key scale of 1).
+// A tile that some row may not see all of: scores times the key scale's fraction, -infinity for
+// hidden ones, back to tensor memory (the caller goes on with the rest of the scale, which is a
+// number above zero whatever the token's scale is).
 __device__ __forceinline__ void hide(uint32_t tS, int nc, float ks, uint64_t keep) {
 #pragma unroll 1
   for (int c = 0; c < nc; ++c, keep >>= 16) {
@@ -377,7 +379,7 @@ __device__ __forceinline__ void softmax_step(State* st, Rows& rw, const float* q
       ld16(tS + 16 * c, w);
       lds16(qf + 16 * c, f);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = fmaf(__uint_as_float(w[i]) * tk.ks, f[i], tk.ex);
+      for (int i = 0; i < 16; ++i) x[i] = fmaf(__uint_as_float(w[i]), f[i] * tk.ks, tk.ex);
     }
     const float mx = reduce_rows<true>(tk.id, tk.warp, tk.lane, x, rw.part);
     if (tk.warp == 0 && !(tk.lane & 1)) {
@@ -874,8 +876,10 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
           tk.ex = i8::scale_exponent(tk.vs);
           const uint32_t tS = tmem + C::kS + (step & 1) * 128 + row0 + lane_off;
           if (tk.cut) {
-            hide(tS, nc, tk.ks, tk.keep);
-            tk.ks = 1.f;
+            // (a power of two of it is left for later: a sum times all of it may be out of range)
+            const int ke = max(0, min(126, int(__float_as_uint(fabsf(tk.ks)) >> 23) - 127));
+            hide(tS, nc, tk.ks * i8::power(-ke), tk.keep);
+            tk.ks = i8::power(ke);
           }
           const bool first = j == it.j0;
           if (nc > 0)
