@@ -494,6 +494,9 @@ pkv_status pkv_paged_attention_decode_quantized(const pkv_tensor* out, const pkv
  * tree_mask      [num_tokens, mask_words] int64, last dim contiguous, 1 to 16 words; bits
  *                from n on are ignored.
  * Shares the decode workspace and its rules (growth, capture, overlapping calls).
+ * With bf16 queries the softmax weights are rounded once to 16 bits before they meet the
+ * values: over a bf16 cache to bf16, by at most 2^-8 of each; over a token-scaled one as for
+ * pkv_paged_attention_decode_quantized.  Scores, sums and outputs are binary32.
  * Results do not depend on timing: a call's outputs are the same bits every time.
  */
 pkv_status pkv_paged_attention_tree(const pkv_tensor* out, const pkv_tensor* query, const pkv_tensor* key_cache,

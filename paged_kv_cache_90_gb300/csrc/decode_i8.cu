@@ -425,8 +425,8 @@ bool decode_i8_supported(const TreeParams& p) {
 }
 
 // What the registers allow (168 a thread; 255 with two tiles).  Batch and long contexts with two
-// blocks of one tile 44 and 115 us, with three 38 and 97, with four (128 registers, spills) 49 and
-// 132.
+// blocks of one tile 44 and 115 us, with three 38 and 97 (64 bytes a thread are spilled for heads
+// of 128), with four (128 registers, many more spilled) 49 and 132.
 int decode_i8_blocks_per_sm(int group) { return group <= 8 ? 3 : 2; }
 
 cudaError_t launch_decode_i8(const TreeParams& p, TreeSplit sp, cudaStream_t stream) {

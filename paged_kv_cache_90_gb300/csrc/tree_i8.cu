@@ -28,7 +28,7 @@
 // codes), one warpgroup's whole work.  The chain of a tile bounds it, not a unit: of 64 rows a
 // warp's weights take 2600 clocks, what is between two tiles' weights (a signal, a wait, the
 // scales) another 1500, with two S^T buffers so that the score MMAs are not part of it.  32 trees
-// of 8 to 32 nodes, 4 x 8 heads of 128, over 1000 to 8192 positions: 172 us, 277 TFLOP/s.  It was
+// of 8 to 32 nodes, 4 x 8 heads of 128, over 1000 to 8192 positions: 169 us, 282 TFLOP/s.  It was
 // 249 us with a pass over the scores before the weights, with products of each half of the rows
 // (their A operand was read twice), and with the queries converted by one warp (33000 clocks
 // between two items), and 195 with each thread working out its output rows' addresses.

@@ -28,8 +28,8 @@
 //
 // What it measured, 32 query heads to 8 KV heads of 128: 64 trees of 5 to 24 nodes over 160 to
 // 2048 positions 62 us, 5.0 TB/s, bound by the copies in flight (a tile is 64 KB, the rings hold
-// three and three) and by each block's start and end; 8 trees of 64 nodes over 32000 positions 241
-// us, 1.09 PFLOP/s at the power limit: a tile's two steps take 3500 to 3900 clocks (a warpgroup's
+// three and three) and by each block's start and end; 8 trees of 64 nodes over 32000 positions 240
+// us, 1.10 PFLOP/s at the power limit: a tile's two steps take 3500 to 3900 clocks (a warpgroup's
 // softmax 3000 beside the other's, and the MMA warp between them), an item's end and the next
 // one's start 16000 more, so blocks with such a border end a tenth after the others.
 //
