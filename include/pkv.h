@@ -23,7 +23,12 @@
  *                                (one scale per token and KV head, found on the way);
  *   pkv_read_cache               cached tokens read back as values;
  *   pkv_paged_attention_decode_quantized  decode over a token-scaled cache;
- *   pkv_paged_attention_tree     attention of drafted token trees over the cache.
+ *   pkv_paged_attention_tree     attention of drafted token trees over the cache;
+ *   pkv_rotary_axes_and_cache    pkv_rotary_and_cache with several position axes (images
+ *                                and video);
+ *   pkv_copy_cache_blocks        copy blocks of many caches (those of all layers) at once;
+ *   pkv_keep_tokens              move the drafted tokens that were accepted to the places
+ *                                that follow the context, in many caches at once.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -44,7 +49,15 @@
  *   FP8 cache halves the memory of a 16-bit one); other dtypes ignore `scale`.
  *   Token-scaled caches: PKV_I8 codes with one fp32 scale per (slot, KV head) in two
  *   arrays beside the caches (code * scale = value); only the calls that take those
- *   arrays (k_scales, v_scales) accept them, and pkv_copy_blocks.
+ *   arrays (k_scales, v_scales) accept them, pkv_copy_blocks and the calls over many caches.
+ *   4-bit caches: PKV_E2M1X2 bytes of two e2m1 codes (sign, two exponent bits of bias 1, one
+ *   mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6), column 2i in the low half of byte i, so that the
+ *   cache is [num_blocks, num_kv_heads, block_size, head_dim / 2]; beside each cache a
+ *   PKV_FP8_E4M3 array [num_blocks, num_kv_heads, block_size, head_dim / 16] with a scale for
+ *   every 16 columns (the last two dimensions contiguous, base pointer and strides multiples of
+ *   head_dim / 16 bytes), given where token scales are (k_scales, v_scales).  code * group scale *
+ *   (the cache descriptor's `scale` or head_scales, as for an e4m3 cache) = value.  The same calls
+ *   take them as token-scaled caches.
  *   Queries and outputs: PKV_F32 or PKV_BF16, the output in the query's dtype.
  *   Supported head_dim: 64 and 128.  Supported block_size: 2, 4, 8, 16, 32.
  * Streams.  `stream` is a cudaStream_t (NULL = the legacy default stream) of the
@@ -80,7 +93,8 @@ typedef enum pkv_dtype {
   PKV_FP8_E4M3 = 2,
   PKV_I32 = 3,
   PKV_I64 = 4,
-  PKV_I8 = 5
+  PKV_I8 = 5,
+  PKV_E2M1X2 = 6 /* two 4-bit codes a byte */
 } pkv_dtype;
 
 typedef enum pkv_status {
@@ -100,6 +114,7 @@ typedef enum pkv_status {
 #define PKV_DEVERR_TIMEOUT 0x10u     /* a bounded wait for an async copy ran out */
 #define PKV_DEVERR_COPY_OVERLAP 0x20u /* copy pairs: a destination repeated or also a source
                                         (checked only with PKV_OPT_DEBUG_SYNC on) */
+#define PKV_DEVERR_KEEP 0x40u        /* kept nodes out of order or range, or more than there are */
 
 typedef struct pkv_tensor {
   void* data;         /* device pointer */
@@ -107,8 +122,8 @@ typedef struct pkv_tensor {
   int32_t ndim;       /* 1..4 */
   int64_t shape[4];
   int64_t stride[4];  /* in elements */
-  float scale;        /* e4m3 caches: dequantisation scale; ignored otherwise */
-  /* e4m3 caches only, or NULL: DEVICE pointer to num_kv_heads fp32 scales, one per KV
+  float scale;        /* e4m3 and 4-bit caches: dequantisation scale; ignored otherwise */
+  /* e4m3 and 4-bit caches only, or NULL: DEVICE pointer to num_kv_heads fp32 scales, one per KV
    * head, used instead of `scale` (stored code * head_scales[h] = value of head h);
    * must be NULL for other dtypes.  Read by the kernels on the device, so it may be
    * updated there (e.g. from an amax report) between calls on the stream. */
@@ -389,8 +404,8 @@ pkv_status pkv_rotary_init(pkv_rotary* rotary, int32_t rotary_dim, int32_t inter
  * key, value       [num_tokens, num_kv_heads, head_dim], the query's dtype, same strides.
  * positions        [num_tokens] int32 or int64, contiguous; any value, negative ones too.
  * key_cache,
- * value_cache      as for pkv_reshape_and_cache: the key's dtype or e4m3; or PKV_I8 with
- *                  k_scales and v_scales as for pkv_quantize_and_cache (NULL otherwise).
+ * value_cache      as for pkv_reshape_and_cache: the key's dtype or e4m3; or PKV_I8 or PKV_E2M1X2
+ *                  with k_scales and v_scales as for pkv_quantize_and_cache (NULL otherwise).
  * slot_mapping     [num_tokens] int64, contiguous, distinct slots.
  * rotary           host pointer; rotary_dim <= head_dim; frequencies as above; magnitude finite in f32.
  * Base pointers and strides of query, query_out, key and value: multiples of 16 bytes.
@@ -403,7 +418,30 @@ pkv_status pkv_rotary_and_cache(const pkv_tensor* query_out, const pkv_tensor* q
                                 pkv_stream stream);
 
 /*
- * pkv_quantize_and_cache — write new tokens' K and V into a token-scaled 8-bit cache.
+ * Rotary positions with several axes: which of a token's positions turns each pair.  An image
+ * or video token has a time, a height and a width; a text token has the same number in all of
+ * them, and is then turned as pkv_rotary_and_cache turns it, bit for bit.
+ */
+typedef struct pkv_rotary_axes {
+  int32_t num_axes;  /* 1 to 4 */
+  int32_t axis[64];  /* for each of the rotary_dim / 2 pairs, 0 to num_axes - 1 */
+} pkv_rotary_axes;
+
+/*
+ * pkv_rotary_axes_and_cache — pkv_rotary_and_cache with positions [num_axes or more, num_tokens]
+ * (last dim contiguous): pair i of token t turns by positions[axes->axis[i], t] * frequency[i].
+ * `axes` is a host pointer, read during the call only.  Everything else as there.
+ */
+pkv_status pkv_rotary_axes_and_cache(const pkv_tensor* query_out, const pkv_tensor* query, const pkv_tensor* key,
+                                     const pkv_tensor* value, const pkv_tensor* positions,
+                                     const pkv_tensor* key_cache, const pkv_tensor* value_cache,
+                                     const pkv_tensor* k_scales, const pkv_tensor* v_scales,
+                                     const pkv_tensor* slot_mapping, const pkv_rotary* rotary,
+                                     const pkv_rotary_axes* axes, pkv_stream stream);
+
+/*
+ * pkv_quantize_and_cache — write new tokens' K and V into a token-scaled 8-bit cache or a 4-bit
+ * one.
  *
  * For token t with slot = slot_mapping[t] >= 0, block b = slot / bs, offset o = slot % bs,
  * KV head h and x = key[t, h, :] (V alike):
@@ -415,11 +453,20 @@ pkv_status pkv_rotary_and_cache(const pkv_tensor* query_out, const pkv_tensor* q
  * (max |x| < 1.5e-36, a row of zeros among them) is stored as zeros with s = 0; a row
  * holding an infinity or a NaN as zeros with s = NaN, so that what reads it shows it.
  *
+ * A 4-bit cache instead takes, for every 16 columns with largest magnitude a and for the cache's
+ * factor f (its descriptor's `scale`, or head_scales[h]), all in IEEE binary32:
+ *   G = a / (6 f), at most 448, rounded to e4m3          (the group's scale)
+ *   code = x * (1 / (G f)), at most 6 in magnitude, rounded to e2m1
+ * both to nearest, ties to even.  An element is off by at most a / 5.  Values beyond 2688 f are
+ * cut off there and groups below 0.0058 f vanish (G = 0), so f is set where values are far from 1.  A G f below
+ * 2^-126 or above 2^126 is stored as G = 0 with codes of 0, a group holding an infinity or a
+ * NaN as G = NaN with codes of 0.
+ *
  * key, value           as for pkv_reshape_and_cache, f32 or bf16.
  * key_cache,
- * value_cache          PKV_I8, the cache layout above.
- * k_scales, v_scales   [num_blocks, num_kv_heads, block_size] f32, last dim contiguous,
- *                      same strides.
+ * value_cache          PKV_I8 or PKV_E2M1X2, the cache layout above.
+ * k_scales, v_scales   [num_blocks, num_kv_heads, block_size] f32, last dim contiguous, same
+ *                      strides; for a 4-bit cache the group scales described above, same strides.
  * slot_mapping         [num_tokens] int64, contiguous, distinct slots.
  */
 pkv_status pkv_quantize_and_cache(const pkv_tensor* key, const pkv_tensor* value, const pkv_tensor* key_cache,
@@ -431,8 +478,8 @@ pkv_status pkv_quantize_and_cache(const pkv_tensor* key, const pkv_tensor* value
  * pkv_read_cache — read cached tokens back: the inverse of the cache writes.
  *
  * For token t with slot = slot_mapping[t] >= 0: key[t, h, :] = the values that the cache
- * holds at the slot (code * scale in binary32 for an 8-bit cache), rounded once to key's
- * dtype; V alike.  slot < 0 leaves the token's rows as they were.  Reading a token and
+ * holds at the slot (code * scale in binary32 for an 8-bit cache, code * (G * f) for a 4-bit
+ * one), rounded once to key's dtype; V alike.  slot < 0 leaves the token's rows as they were.  Reading a token and
  * writing it elsewhere moves it: bit for bit between caches of one 16- or 32-bit type
  * read in that type; for a token-scaled cache read in f32 the codes are the same and the
  * scale within one unit in its last place.  Slots may repeat.
@@ -440,7 +487,8 @@ pkv_status pkv_quantize_and_cache(const pkv_tensor* key, const pkv_tensor* value
  * key, value           [num_tokens, num_kv_heads, head_dim] f32 or bf16 (written), same
  *                      dtype, shape and strides, last dim contiguous, 16-byte aligned.
  * key_cache,
- * value_cache          any cache dtype; PKV_I8 with k_scales and v_scales (NULL otherwise).
+ * value_cache          any cache dtype; PKV_I8 and PKV_E2M1X2 with k_scales and v_scales (NULL
+ *                      otherwise).
  * slot_mapping         [num_tokens] int64, contiguous.
  */
 pkv_status pkv_read_cache(const pkv_tensor* key, const pkv_tensor* value, const pkv_tensor* key_cache,
@@ -449,14 +497,18 @@ pkv_status pkv_read_cache(const pkv_tensor* key, const pkv_tensor* value, const 
 
 /*
  * pkv_paged_attention_decode_quantized — pkv_paged_attention_decode_window over a
- * token-scaled cache: K_s[j] = codes * k_scales of position j's slot, V_s[j] alike.
+ * token-scaled or a 4-bit cache: K_s[j] = codes * k_scales of position j's slot (* its group's
+ * and the cache's factor), V_s[j] alike.
  *
- * key_cache and value_cache are PKV_I8, k_scales and v_scales as for
+ * key_cache and value_cache are PKV_I8 or PKV_E2M1X2, k_scales and v_scales as for
  * pkv_quantize_and_cache; the other arguments as for the window decode (sliding_window 0:
  * the full context).  A context length out of range sets PKV_DEVERR_CONTEXT_LEN and leaves
  * the sequence's row as it was.  Workspace: the decode workspace, as described for
  * pkv_paged_attention_decode, its need given by pkv_tree_workspace_bytes (num_tokens = num_seqs).
- * With bf16 queries a softmax weight times its value scale is rounded once to 16 bits: by at
+ * Over a 4-bit cache keys and values are taken exactly, and with bf16 queries a softmax weight is
+ * rounded once to 16 bits: by at most 2^-11 of itself, or, if it is small, by 2^-31 of the largest
+ * in its row.
+ * Over an int8 cache, with bf16 queries a softmax weight times its value scale is rounded once to 16 bits: by at
  * most 2^-11 of itself, or, if it is small, by 2^-31 of the largest such product in its row
  * (value scales below 2^-80 count as 2^-80 there; above 2^90 sums lose bits).  With f32 queries
  * it stays in binary32.
@@ -488,14 +540,14 @@ pkv_status pkv_paged_attention_decode_quantized(const pkv_tensor* out, const pkv
  * out, query     [num_tokens, num_heads, head_dim] f32 or bf16, last dim contiguous; rows
  *                of each sequence packed in order.
  * key_cache,
- * value_cache    any cache dtype; PKV_I8 with k_scales and v_scales (NULL otherwise).
+ * value_cache    any cache dtype; PKV_I8 and PKV_E2M1X2 with k_scales and v_scales (NULL otherwise).
  * block_tables   [num_seqs, max_blocks_per_seq] int32; context_lens [num_seqs] int32;
  * query_start_loc [num_seqs + 1] int32, contiguous, non-decreasing, starting at 0.
  * tree_mask      [num_tokens, mask_words] int64, last dim contiguous, 1 to 16 words; bits
  *                from n on are ignored.
  * Shares the decode workspace and its rules (growth, capture, overlapping calls).
  * With bf16 queries the softmax weights are rounded once to 16 bits before they meet the
- * values: over a bf16 cache to bf16, by at most 2^-8 of each; over a token-scaled one as for
+ * values: over a bf16 cache to bf16, by at most 2^-8 of each; over a token-scaled or 4-bit one as for
  * pkv_paged_attention_decode_quantized.  Scores, sums and outputs are binary32.
  * Results do not depend on timing: a call's outputs are the same bits every time.
  */
@@ -522,11 +574,12 @@ int64_t pkv_tree_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t n
  *
  * For each row (src, dst) of src_dst_pairs: cache[dst, :, :, :] = cache[src, :, :, :]
  * (all KV heads, byte copy).  Call once for the key cache and once for the value cache, and
- * for a token-scaled cache once for each of its scale arrays.
+ * for a token-scaled or 4-bit cache once for each of its scale arrays.
  *
  * cache          [num_blocks, num_kv_heads, block_size, head_dim], layout rules above (any
- *                cache dtype, PKV_I8 too); or a scale array [num_blocks, num_kv_heads,
- *                block_size] f32, last dim contiguous.
+ *                cache dtype, PKV_I8 and PKV_E2M1X2 too); or a scale array: [num_blocks,
+ *                num_kv_heads, block_size] f32, last dim contiguous, or a 4-bit cache's group
+ *                scales (e4m3 with 4 or 8 a token).
  * src_dst_pairs  [num_pairs, 2] int64, contiguous; num_pairs may be 0.
  * Pairs are copied in parallel: destinations must be distinct and no destination may
  * also be a source (breaking this gives an unspecified mix of old and new bytes, never
@@ -538,6 +591,48 @@ int64_t pkv_tree_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t n
  */
 pkv_status pkv_copy_blocks(const pkv_tensor* cache, const pkv_tensor* src_dst_pairs,
                            pkv_stream stream);
+
+/*
+ * pkv_copy_cache_blocks — pkv_copy_blocks for many caches at once: the keys, values and scales of
+ * all layers, which share one set of block tables.  One launch for up to 96 of them.
+ *
+ * For each row (src, dst) of src_dst_pairs and each cache c: c[dst] = c[src].  It serves a fork
+ * or a copy-on-write (a child's own copy of a partial block) and the packing of a fragmented pool.
+ *
+ * caches         num_caches (1 to 1024) descriptors of caches or scale arrays, as pkv_copy_blocks
+ *                takes them, of any dtypes; all with the same num_blocks and block_size.
+ * src_dst_pairs  as for pkv_copy_blocks, with the same rules.
+ */
+pkv_status pkv_copy_cache_blocks(const pkv_tensor* const* caches, int32_t num_caches,
+                                 const pkv_tensor* src_dst_pairs, pkv_stream stream);
+
+/*
+ * pkv_keep_tokens — keep the drafted tokens that were accepted: what follows
+ * pkv_paged_attention_tree, in the caches of all layers at once.
+ *
+ * Sequence s has L = context_lens[s] tokens in the cache, the last n = qsl[s+1] - qsl[s] of them
+ * drafted nodes, qsl = query_start_loc.  k = keep_counts[s] of them stay: nodes a_0 < a_1 < ... <
+ * a_(k-1), with a_i = keep[qsl[s] + i].  Afterwards position L - n + i holds, in every cache, what
+ * position L - n + a_i held before, for i < k, and new_lens[s] = L - n + k.  Positions from there
+ * on are not written.  Values move byte for byte.  (A node's ancestors come before it, so an
+ * accepted path is ascending.)
+ *
+ * Checked on the device, and a sequence that fails is left as it is, its new_lens too: nodes that
+ * are out of order or range and k < 0 or k > n set PKV_DEVERR_KEEP; n > L, L past the table or rows
+ * outside `keep` PKV_DEVERR_CONTEXT_LEN; table entries out of range (of tokens that move)
+ * PKV_DEVERR_TABLE_ENTRY.
+ *
+ * caches         as for pkv_copy_cache_blocks, none of them twice.  The blocks of drafted
+ *                positions belong to their sequence alone (no other table has them).
+ * block_tables   [num_seqs, max_blocks_per_seq] int32; context_lens [num_seqs] int32;
+ * query_start_loc [num_seqs + 1] int32, contiguous, non-decreasing.
+ * keep           [num_tokens] int32, contiguous; keep_counts [num_seqs] int32, contiguous.
+ * new_lens       [num_seqs] int32, contiguous, not context_lens itself; or NULL.
+ */
+pkv_status pkv_keep_tokens(const pkv_tensor* const* caches, int32_t num_caches, const pkv_tensor* block_tables,
+                           const pkv_tensor* context_lens, const pkv_tensor* query_start_loc,
+                           const pkv_tensor* keep, const pkv_tensor* keep_counts, const pkv_tensor* new_lens,
+                           int32_t block_size, int32_t max_blocks_per_seq, pkv_stream stream);
 
 /*
  * pkv_paged_attention_decode_noalloc — the same decode as pkv_paged_attention_decode,

@@ -22,12 +22,14 @@ PKV_OK = 0
 STATUS_NAMES = {0: "PKV_OK", 1: "PKV_ERR_INVALID_ARG", 2: "PKV_ERR_UNSUPPORTED", 3: "PKV_ERR_CUDA",
                 4: "PKV_ERR_DEVICE_CHECK"}
 DEVERR = {"table_entry": 0x1, "slot": 0x2, "copy_pair": 0x4, "context_len": 0x8, "timeout": 0x10,
-          "copy_overlap": 0x20}
+          "copy_overlap": 0x20, "keep": 0x40}
 OPTIONS = {"partition_tokens": 0, "debug_sync": 1, "dry_run": 2, "decode_kernel": 3,
            "dynamic_share": 4, "dynamic_chunk": 5, "fused_append": 6,
            "prefill_kernel": 7}
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float8_e4m3fn: 2, torch.int32: 3, torch.int64: 4,
-           torch.int8: 5}
+           torch.int8: 5, torch.uint8: 6}
+if hasattr(torch, "float4_e2m1fn_x2"):
+    _DTYPES[torch.float4_e2m1fn_x2] = 6  # a 4-bit cache's bytes, as torch.uint8
 ROTARY_SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3, "ramp": 4}
 
 
@@ -46,8 +48,14 @@ class PkvTensor(ctypes.Structure):
 
 class PkvRotary(ctypes.Structure):
     """pkv_rotary: how rotary_and_cache turns queries and keys (see :func:`rotary`)."""
+    axes: "Optional[PkvRotaryAxes]" = None  # with several position axes
     _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_double),
                 ("frequency", ctypes.c_double * 64)]
+
+
+class PkvRotaryAxes(ctypes.Structure):
+    """pkv_rotary_axes: which position axis turns each pair."""
+    _fields_ = [("num_axes", ctypes.c_int32), ("axis", ctypes.c_int32 * 64)]
 
 
 _lock = threading.Lock()
@@ -81,6 +89,10 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         lib.pkv_rotary_init.argtypes = [ctypes.POINTER(PkvRotary), i32, i32, ctypes.c_double, i32, ctypes.c_double,
                                         i64]
         lib.pkv_rotary_and_cache.argtypes = [d] * 10 + [ctypes.POINTER(PkvRotary), vp]
+        lib.pkv_rotary_axes_and_cache.argtypes = [d] * 10 + [ctypes.POINTER(PkvRotary),
+                                                             ctypes.POINTER(PkvRotaryAxes), vp]
+        lib.pkv_copy_cache_blocks.argtypes = [ctypes.POINTER(d), i32, d, vp]
+        lib.pkv_keep_tokens.argtypes = [ctypes.POINTER(d), i32] + [d] * 6 + [i32, i32, vp]
         lib.pkv_quantize_and_cache.argtypes = [d] * 7 + [vp]
         lib.pkv_read_cache.argtypes = [d] * 7 + [vp]
         lib.pkv_paged_attention_decode_quantized.argtypes = [d] * 8 + [i32, f32, i32, i32, i32, vp]
@@ -95,6 +107,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                    "pkv_paged_attention_prefill", "pkv_decode_append", "pkv_rotary_init",
                    "pkv_rotary_and_cache", "pkv_quantize_and_cache", "pkv_read_cache",
                    "pkv_paged_attention_decode_quantized", "pkv_paged_attention_tree",
+                   "pkv_rotary_axes_and_cache", "pkv_copy_cache_blocks", "pkv_keep_tokens",
                    "pkv_set_option", "pkv_reserve_workspace", "pkv_read_device_errors"):
             getattr(lib, fn).restype = ctypes.c_int
         lib.pkv_last_error.restype = ctypes.c_char_p
@@ -120,8 +133,8 @@ def _check(status: int) -> None:
 
 
 def describe(t: torch.Tensor, scale: float = 1.0, head_scales: Optional[torch.Tensor] = None) -> PkvTensor:
-    """pkv_tensor descriptor of a tensor (pointer, dtype code, shape, strides); an 8-bit
-    cache may carry one scale per KV head (a float32 tensor on the cache's device)."""
+    """pkv_tensor descriptor of a tensor (pointer, dtype code, shape, strides); an 8-bit or
+    4-bit cache may carry one scale per KV head (a float32 tensor on the cache's device)."""
     if t.dim() > 4 or t.dim() < 1:
         raise ValueError("descriptors cover 1 to 4 dimensions")
     if t.dtype not in _DTYPES:
@@ -331,7 +344,8 @@ def reshape_and_cache(key, value, key_cache, value_cache, slot_mapping, k_scale:
 
 def copy_blocks(cache, src_dst_pairs, stream=None) -> None:
     """cache[dst] = cache[src] for every (src, dst) row of ``src_dst_pairs``; ``cache`` may be
-    the scale array [num_blocks, Hk, block_size] of an int8 cache, which is copied like it."""
+    the scale array of an int8 cache or the group scales of a 4-bit one, which are copied like it.
+    copy_cache_blocks takes the caches of all layers at once."""
     lib = load_library()
     pairs = src_dst_pairs
     if pairs.numel() == 0:
@@ -340,15 +354,70 @@ def copy_blocks(cache, src_dst_pairs, stream=None) -> None:
     _check(lib.pkv_copy_blocks(*descs, _stream(stream)))
 
 
+class CacheList:
+    """The caches (and scale arrays) of all layers, marshalled once for the calls that take
+    many: see :func:`cache_list`.  Holds references to them."""
+
+    def __init__(self, caches):
+        self.caches = tuple(caches)
+        if not self.caches:
+            raise ValueError("a cache list holds at least one cache")
+        if len({c.device for c in self.caches}) != 1:
+            raise ValueError("the caches of a list must be on one device")
+        self._descs = [describe(c) for c in self.caches]
+        self._array = (ctypes.POINTER(PkvTensor) * len(self._descs))(*[ctypes.pointer(x) for x in self._descs])
+
+    def __len__(self) -> int:
+        return len(self.caches)
+
+
+def cache_list(caches) -> CacheList:
+    """Made once, passed to every copy_cache_blocks and keep_tokens: caches [num_blocks, Hk,
+    block_size, ...] of any dtypes with one num_blocks and block_size, and their scale arrays.  The
+    tensors must stay on the same storage, shapes and strides while the list is used."""
+    return CacheList(caches)
+
+
+def copy_cache_blocks(caches, src_dst_pairs, stream=None) -> None:
+    """cache[dst] = cache[src] for every (src, dst) row of ``src_dst_pairs`` (int64) in every
+    cache of ``caches`` (a :func:`cache_list`, or the tensors), in one launch: a fork's or a
+    copy-on-write's private blocks, or the moves that pack a fragmented pool
+    (:meth:`block_manager.BlockManager.compact`)."""
+    lib = load_library()
+    if not isinstance(caches, CacheList):
+        caches = CacheList(caches)
+    pairs = src_dst_pairs
+    if pairs.numel() == 0:
+        pairs = pairs.reshape(0, 2)
+    _check(lib.pkv_copy_cache_blocks(caches._array, len(caches), _ref(pairs), _stream(stream)))
+
+
+def keep_tokens(caches, block_tables, context_lens, query_start_loc, keep, keep_counts, block_size: int,
+                max_blocks_per_seq: int, new_lens=None, stream=None):
+    """Keep the drafted tokens that were accepted, in every cache of ``caches`` (a
+    :func:`cache_list`, or the tensors): of sequence s's drafted nodes (the last
+    query_start_loc[s+1] - query_start_loc[s] of its context_lens[s] cached tokens) the first
+    keep_counts[s] entries of ``keep`` from query_start_loc[s] on, in ascending order, move to the
+    positions that follow the context.  ``new_lens`` (int32, returned) receives the lengths."""
+    lib = load_library()
+    if not isinstance(caches, CacheList):
+        caches = CacheList(caches)
+    _check(lib.pkv_keep_tokens(caches._array, len(caches), _ref(block_tables), _ref(context_lens),
+                               _ref(query_start_loc), _ref(keep), _ref(keep_counts), _opt_ref(new_lens),
+                               int(block_size), int(max_blocks_per_seq), _stream(stream)))
+    return new_lens
+
+
 def rotary(rotary_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
            factor: float = 1.0, original_max_position: int = 0, frequencies=None,
-           magnitude: Optional[float] = None) -> PkvRotary:
+           magnitude: Optional[float] = None, axes=None) -> PkvRotary:
     """The rotation that rotary_and_cache applies: made once, passed to every call.  The
     first ``rotary_dim`` columns of a head are rotated, in pairs half of them apart or
     (``interleaved``) next to each other.  ``scaling`` (none, linear, base, bands, ramp)
     stretches the frequencies by ``factor`` past ``original_max_position`` as pkv_rotary_init
     describes; ``frequencies`` (radians per position, one per pair) and ``magnitude`` replace
-    what that gives."""
+    what that gives.  ``axes`` (one number 0..3 per pair, see :func:`rotary_axes`) says which of
+    a token's positions turns each pair: rotary_and_cache then takes positions [axes, tokens]."""
     if scaling not in ROTARY_SCALINGS:
         raise ValueError(f"unknown rotary scaling {scaling!r} (known: {', '.join(ROTARY_SCALINGS)})")
     r = PkvRotary()
@@ -361,7 +430,31 @@ def rotary(rotary_dim: int, base: float = 10000.0, interleaved: bool = False, sc
         r.frequency[:len(freqs)] = freqs
     if magnitude is not None:
         r.magnitude = float(magnitude)
+    if axes is not None:
+        axes = [int(a) for a in axes]
+        if len(axes) != rotary_dim // 2 or any(not 0 <= a <= 3 for a in axes):
+            raise ValueError("axes must hold rotary_dim / 2 numbers from 0 to 3")
+        r.axes = PkvRotaryAxes(max(axes, default=0) + 1)
+        r.axes.axis[:len(axes)] = axes
     return r
+
+
+def rotary_axes(sections, cyclic: bool = False):
+    """The axis of each pair from the number of pairs that each axis has: the first
+    ``sections[0]`` pairs to axis 0 and so on, or (``cyclic``) the axes in turn over the pairs
+    until each has its number."""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 4 or any(n < 0 for n in left):
+        raise ValueError("sections holds one to four numbers, none below zero")
+    if not cyclic:
+        return [a for a, n in enumerate(left) for _ in range(n)]
+    out = []
+    while any(left):
+        for a, n in enumerate(left):
+            if n:
+                out.append(a)
+                left[a] -= 1
+    return out
 
 
 def _opt_ref(t: Optional[torch.Tensor]):
@@ -373,24 +466,32 @@ def rotary_and_cache(query_out, query, key, value, positions, key_cache, value_c
                      k_head_scales=None, v_head_scales=None, k_token_scales=None, v_token_scales=None) -> torch.Tensor:
     """Rotate the new tokens' queries into ``query_out`` (returned; may be ``query``) and
     write the rotated keys and the values into their cache slots, in one pass.
-    ``k_token_scales`` / ``v_token_scales`` [num_blocks, Hk, block_size] go with an int8
-    cache, which is then written as by quantize_and_cache."""
+    ``positions`` is [tokens], or [axes, tokens] for a rotary with ``axes``.
+    ``k_token_scales`` / ``v_token_scales`` go with an int8 cache ([num_blocks, Hk, block_size])
+    or a 4-bit one (its group scales), which is then written as by quantize_and_cache."""
     lib = load_library()
-    _check(lib.pkv_rotary_and_cache(
-        _ref(query_out), _ref(query), _ref(key), _ref(value), _ref(positions), _ref(key_cache, k_scale, k_head_scales),
-        _ref(value_cache, v_scale, v_head_scales), _opt_ref(k_token_scales), _opt_ref(v_token_scales),
-        _ref(slot_mapping), ctypes.byref(rotary), _stream(stream)))
+    args = (_ref(query_out), _ref(query), _ref(key), _ref(value), _ref(positions),
+            _ref(key_cache, k_scale, k_head_scales), _ref(value_cache, v_scale, v_head_scales),
+            _opt_ref(k_token_scales), _opt_ref(v_token_scales), _ref(slot_mapping), ctypes.byref(rotary))
+    if rotary.axes is None:
+        _check(lib.pkv_rotary_and_cache(*args, _stream(stream)))
+    else:
+        _check(lib.pkv_rotary_axes_and_cache(*args, ctypes.byref(rotary.axes), _stream(stream)))
     return query_out
 
 
 def quantize_and_cache(key, value, key_cache, value_cache, k_token_scales, v_token_scales, slot_mapping,
-                       stream=None) -> None:
-    """Write the new tokens' K/V into an int8 cache (in place), each (token, KV head) row
-    with a scale of its own, max |x| / 127, stored beside the codes."""
+                       stream=None, k_scale: float = 1.0, v_scale: float = 1.0, k_head_scales=None,
+                       v_head_scales=None) -> None:
+    """Write the new tokens' K/V (in place) into an int8 cache, each (token, KV head) row with
+    a scale of its own, max |x| / 127, stored beside the codes; or into a 4-bit cache: uint8
+    [num_blocks, Hk, block_size, head_dim / 2], two e2m1 codes a byte, the scales float8_e4m3fn
+    [num_blocks, Hk, block_size, head_dim / 16], one for every 16 columns.  ``k_scale`` /
+    ``v_scale`` or per-head scales are a 4-bit cache's factors, the same in every call on it."""
     lib = load_library()
-    _check(lib.pkv_quantize_and_cache(_ref(key), _ref(value), _ref(key_cache), _ref(value_cache),
-                                      _ref(k_token_scales), _ref(v_token_scales), _ref(slot_mapping),
-                                      _stream(stream)))
+    _check(lib.pkv_quantize_and_cache(_ref(key), _ref(value), _ref(key_cache, k_scale, k_head_scales),
+                                      _ref(value_cache, v_scale, v_head_scales), _ref(k_token_scales),
+                                      _ref(v_token_scales), _ref(slot_mapping), _stream(stream)))
 
 
 def read_cache(key, value, key_cache, value_cache, slot_mapping, k_scale: float = 1.0, v_scale: float = 1.0,
@@ -406,12 +507,16 @@ def read_cache(key, value, key_cache, value_cache, slot_mapping, k_scale: float 
 
 def paged_attention_decode_quantized(out, query, key_cache, value_cache, k_token_scales, v_token_scales, block_tables,
                                      context_lens, num_kv_heads: int, scale: float, block_size: int,
-                                     max_blocks_per_seq: int, sliding_window: int = 0, stream=None) -> torch.Tensor:
-    """Single-token decode attention over an int8 cache with one scale per (slot, KV head),
-    into ``out`` (returned); ``sliding_window`` as for paged_attention_decode."""
+                                     max_blocks_per_seq: int, sliding_window: int = 0, stream=None,
+                                     k_scale: float = 1.0, v_scale: float = 1.0, k_head_scales=None,
+                                     v_head_scales=None) -> torch.Tensor:
+    """Single-token decode attention over an int8 cache with one scale per (slot, KV head), or
+    a 4-bit cache with its group scales (and factors, as for quantize_and_cache), into ``out``
+    (returned); ``sliding_window`` as for paged_attention_decode."""
     lib = load_library()
     _check(lib.pkv_paged_attention_decode_quantized(
-        _ref(out), _ref(query), _ref(key_cache), _ref(value_cache), _ref(k_token_scales), _ref(v_token_scales),
+        _ref(out), _ref(query), _ref(key_cache, k_scale, k_head_scales), _ref(value_cache, v_scale, v_head_scales),
+        _ref(k_token_scales), _ref(v_token_scales),
         _ref(block_tables), _ref(context_lens), int(num_kv_heads), float(scale), int(block_size),
         int(max_blocks_per_seq), int(sliding_window), _stream(stream)))
     return out

@@ -169,6 +169,71 @@ class BlockManager:
         s.released = max(s.released, min(first_kept, len(s.blocks)))
         return out
 
+    def truncate(self, seq_id, length: int) -> List[int]:
+        """Shorten a sequence to its first ``length`` tokens (drafted tokens that were not
+        accepted) and give back the blocks behind them; returns their ids."""
+        s = self.seqs[seq_id]
+        kept = blocks_needed(length, self.bs)
+        if not 0 <= length <= s.length or (s.released and kept <= s.released):
+            raise ValueError(f"sequence {seq_id} of {s.length} tokens cannot shrink to {length}")
+        out = s.blocks[kept:]
+        del s.blocks[kept:]
+        s.length = length
+        for b in out:
+            self.alloc.decref(b)
+        return out
+
+    def fork_copy(self, parent_id, child_id) -> Optional[Tuple[int, int]]:
+        """:meth:`fork`, with a block of the child's own in place of a partial last block that
+        it would share: the returned pair ``(src, dst)`` (or None) must be copied on the device,
+        in the caches of all layers, before either sequence writes a token."""
+        p = self.seqs[parent_id]
+        partial = p.length % self.bs != 0
+        new = self.alloc.allocate() if partial else None  # (first: it may raise)
+        try:
+            self.fork(parent_id, child_id)
+        except Exception:
+            if partial:
+                self.alloc.decref(new)
+            raise
+        if not partial:
+            return None
+        c = self.seqs[child_id]
+        old = c.blocks[-1]
+        self.alloc.decref(old)
+        c.blocks[-1] = new
+        return old, new
+
+    def compact(self, prefix_caches: Iterable["PrefixCache"] = ()) -> List[Tuple[int, int]]:
+        """Pack the pool: the blocks in use move to the lowest ids, so that what is free is one
+        run at the end.  The k-th free id from the front takes the k-th used one from the back.
+        Tables, reference counts, the free list and the blocks that ``prefix_caches`` hold are
+        changed; the returned pairs ``(src, dst)`` must be copied on the device, in the caches of
+        all layers, before the next step.  No destination is a source.  A block that neither a
+        table nor one of ``prefix_caches`` refers to is somebody else's: ValueError."""
+        count = self.alloc.refcount
+        prefix_caches = list(prefix_caches)
+        known = [0] * self.alloc.num_blocks
+        for b in [b for s in self.seqs.values() for b in s.blocks if b != RELEASED] + \
+                [b for cache in prefix_caches for b in cache.held()]:
+            known[b] += 1
+        if known != count:
+            raise ValueError("some blocks are held by neither the tables nor the prefix caches given")
+        used = sum(c > 0 for c in count)
+        holes = [b for b in range(used) if count[b] == 0]
+        moving = [b for b in range(self.alloc.num_blocks - 1, used - 1, -1) if count[b] > 0]
+        moves = list(zip(moving, holes))
+        to = dict(moves)
+        for src, dst in moves:
+            count[dst], count[src] = count[src], 0
+        for s in self.seqs.values():
+            s.blocks = [to.get(b, b) for b in s.blocks]
+        for cache in prefix_caches:
+            for h, b in cache.by_hash.items():
+                cache.by_hash[h] = to.get(b, b)
+        self.alloc._free = deque(range(used, self.alloc.num_blocks))
+        return moves
+
     # -- growth ------------------------------------------------------------
     def append_token(self, seq_id) -> Tuple[int, Optional[Tuple[int, int]]]:
         """Reserve the slot for the next token of ``seq_id``.

@@ -221,12 +221,17 @@ cudaError_t launch_reshape_and_cache(const CacheWriteParams& p, cudaStream_t str
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+cudaError_t launch_copy_pairs_check(const CopyBlocksParams& p, cudaStream_t stream) {
+  copy_pairs_check_kernel<<<unsigned((p.num_pairs + kCheckThreads - 1) / kCheckThreads), kCheckThreads, 0, stream>>>(p);
+  note_launch();
+  return cudaGetLastError();
+}
+
 cudaError_t launch_copy_blocks(const CopyBlocksParams& p, cudaStream_t stream) {
   if (p.num_pairs == 0) return cudaSuccess;
   if (p.check_overlap) {
-    copy_pairs_check_kernel<<<unsigned((p.num_pairs + kCheckThreads - 1) / kCheckThreads), kCheckThreads, 0,
-                              stream>>>(p);
-    note_launch();
+    const cudaError_t e = launch_copy_pairs_check(p, stream);
+    if (e != cudaSuccess) return e;
   }
   const dim3 grid(static_cast<unsigned>(p.num_pairs), static_cast<unsigned>(p.num_kv_heads));
   copy_blocks_kernel<<<grid, kCopyThreads, 0, stream>>>(p);

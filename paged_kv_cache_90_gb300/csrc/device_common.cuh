@@ -22,6 +22,7 @@ constexpr unsigned int kErrCopyPair = 0x4u;
 constexpr unsigned int kErrContextLen = 0x8u;
 constexpr unsigned int kErrTimeout = 0x10u;
 constexpr unsigned int kErrCopyOverlap = 0x20u;
+constexpr unsigned int kErrKeep = 0x40u;
 
 // First attended position of a context of L tokens under a sliding window of W
 // positions (W <= 0: no window).

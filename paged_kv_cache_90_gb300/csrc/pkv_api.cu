@@ -137,6 +137,7 @@ int elt_bytes(int dtype) {
     case PKV_I32: return 4;
     case PKV_I64: return 8;
     case PKV_I8: return 1;
+    case PKV_E2M1X2: return 1;
     default: return 0;
   }
 }
@@ -149,6 +150,7 @@ const char* dtype_name(int dtype) {
     case PKV_I32: return "i32";
     case PKV_I64: return "i64";
     case PKV_I8: return "i8";
+    case PKV_E2M1X2: return "e2m1x2";
     default: return "?";
   }
 }
@@ -180,26 +182,69 @@ pkv_status check_dtype(const pkv_tensor* t, const char* name, int a, int b, int 
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-pkv_status check_cache(const pkv_tensor* c, const char* name, bool i8) {
+pkv_status check_cache(const pkv_tensor* c, const char* name, bool scaled) {
   pkv_status st = check_basic(c, name, 4);
   if (st) return st;
-  if (!(i8 && c->dtype == PKV_I8) && (st = check_dtype(c, name, PKV_F32, PKV_BF16, PKV_FP8_E4M3))) return st;
-  const int64_t D = c->shape[3];
+  if (!(scaled && (c->dtype == PKV_I8 || c->dtype == PKV_E2M1X2)) && (st = check_dtype(c, name, PKV_F32, PKV_BF16, PKV_FP8_E4M3))) return st;
+  const int64_t D = c->shape[3];  // (of a 4-bit cache: its bytes)
   if (c->shape[2] > 1 && c->stride[2] != D)
     return fail(PKV_ERR_INVALID_ARG, "%s: the (block_size, head_dim) tile must be contiguous (stride[2] == head_dim)", name);
   const int eb = elt_bytes(c->dtype);
   if (!aligned16(c->data) || (c->stride[0] * eb) % 16 || (c->stride[1] * eb) % 16)
     return fail(PKV_ERR_INVALID_ARG, "%s: base pointer and block/head strides must be multiples of 16 bytes", name);
+  const bool factor = c->dtype == PKV_FP8_E4M3 || c->dtype == PKV_E2M1X2;
   if (c->head_scales) {
-    if (c->dtype != PKV_FP8_E4M3)
-      return fail(PKV_ERR_INVALID_ARG, "%s: per-head scales are for an e4m3 cache only", name);
+    if (!factor) return fail(PKV_ERR_INVALID_ARG, "%s: per-head scales are for an e4m3 or 4-bit cache only", name);
     if (reinterpret_cast<uintptr_t>(c->head_scales) & 3)
       return fail(PKV_ERR_INVALID_ARG, "%s: head_scales must be 4-byte aligned", name);
-  } else if (c->dtype == PKV_FP8_E4M3 && !(std::isfinite(c->scale) && c->scale > 0.f)) {
-    return fail(PKV_ERR_INVALID_ARG, "%s: an e4m3 cache needs a finite positive scale", name);
+  } else if (factor && !(std::isfinite(c->scale) && c->scale > 0.f)) {
+    return fail(PKV_ERR_INVALID_ARG, "%s: an %s cache needs a finite positive scale", name,
+                c->dtype == PKV_FP8_E4M3 ? "e4m3" : "e2m1x2");
   }
   return PKV_OK;
 }
+
+int64_t cache_head_dim(const pkv_tensor* c) { return c->dtype == PKV_E2M1X2 ? 2 * c->shape[3] : c->shape[3]; }
+
+bool is_group_scales(const pkv_tensor* t) {
+  return t->ndim == 4 && t->dtype == PKV_FP8_E4M3 && (t->shape[3] == 4 || t->shape[3] == 8);
+}
+
+pkv_status check_group_scales(const pkv_tensor* t, const char* name) {
+  pkv_status st = check_basic(t, name, 4);
+  if (st) return st;
+  if ((st = check_dtype(t, name, PKV_FP8_E4M3))) return st;
+  const int64_t n = t->shape[3];
+  if (n != 4 && n != 8) return fail(PKV_ERR_INVALID_ARG, "%s must hold head_dim / 16 scales a token", name);
+  if (t->shape[2] > 1 && t->stride[2] != n)
+    return fail(PKV_ERR_INVALID_ARG, "%s: the (block_size, head_dim / 16) tile must be contiguous", name);
+  if (reinterpret_cast<uintptr_t>(t->data) % n || t->stride[0] % n || t->stride[1] % n)
+    return fail(PKV_ERR_INVALID_ARG, "%s: base pointer and block/head strides must be multiples of %lld bytes", name,
+                (long long)n);
+  return PKV_OK;
+}
+
+// A cache or one of the scale arrays, as the copies take them: bytes of (block, head) tiles.
+pkv_status check_pages(const pkv_tensor* c, const char* name) {
+  pkv_status st;
+  const bool scales = c && c->ndim == 3, groups = c && is_group_scales(c);
+  if ((st = scales ? check_scales(c, name) : groups ? check_group_scales(c, name) : check_cache(c, name, true))) return st;
+  if (!scales && !groups && !supported_head_dim(cache_head_dim(c)))
+    return fail(PKV_ERR_UNSUPPORTED, "head_dim %lld (supported: 64, 128)", (long long)cache_head_dim(c));
+  if (!supported_block_size(c->shape[2]))
+    return fail(PKV_ERR_UNSUPPORTED, "block_size %lld (supported: 2, 4, 8, 16, 32)", (long long)c->shape[2]);
+  return PKV_OK;
+}
+
+pkv_status check_pairs(const pkv_tensor* pairs) {
+  pkv_status st;
+  if ((st = check_basic(pairs, "src_dst_pairs", 2)) || (st = check_dtype(pairs, "src_dst_pairs", PKV_I64))) return st;
+  if (pairs->shape[1] != 2 || (pairs->shape[0] > 1 && pairs->stride[0] != 2))
+    return fail(PKV_ERR_INVALID_ARG, "src_dst_pairs must be a contiguous [num_pairs, 2] array");
+  return PKV_OK;
+}
+
+bool debug_sync() { return g_opt_debug_sync.load() != 0; }
 
 pkv_status check_scales(const pkv_tensor* t, const char* name) {
   pkv_status st = check_basic(t, name, 3);
@@ -806,17 +851,9 @@ pkv_status pkv_decode_append(const pkv_tensor* out, const pkv_tensor* query, con
 
 pkv_status pkv_copy_blocks(const pkv_tensor* cache, const pkv_tensor* src_dst_pairs, pkv_stream stream) {
   pkv_status st;
-  const bool scales = cache && cache->ndim == 3;  // of a token-scaled cache
-  if ((st = scales ? check_scales(cache, "scales") : check_cache(cache, "cache", true)) ||
-      (st = check_basic(src_dst_pairs, "src_dst_pairs", 2)))
+  if ((st = check_pages(cache, cache && cache->ndim == 3 ? "scales" : "cache")) || (st = check_pairs(src_dst_pairs)))
     return st;
-  if ((st = check_dtype(src_dst_pairs, "src_dst_pairs", PKV_I64))) return st;
-  if (src_dst_pairs->shape[1] != 2 || (src_dst_pairs->shape[0] > 1 && src_dst_pairs->stride[0] != 2))
-    return fail(PKV_ERR_INVALID_ARG, "src_dst_pairs must be a contiguous [num_pairs, 2] array");
-  if (!scales && !supported_head_dim(cache->shape[3]))
-    return fail(PKV_ERR_UNSUPPORTED, "head_dim %lld (supported: 64, 128)", (long long)cache->shape[3]);
-  if (!supported_block_size(cache->shape[2]))
-    return fail(PKV_ERR_UNSUPPORTED, "block_size %lld (supported: 2, 4, 8, 16, 32)", (long long)cache->shape[2]);
+  const bool scales = cache->ndim == 3;  // of a token-scaled cache
   const int64_t n = src_dst_pairs->shape[0];
   if (n > 0x7fffffff || cache->shape[1] > 65535) return fail(PKV_ERR_UNSUPPORTED, "too many pairs or heads");
   if (g_opt_dry_run.load() || n == 0 || cache->shape[1] == 0) return PKV_OK;  // (no KV head: no byte to copy)
@@ -835,7 +872,7 @@ pkv_status pkv_copy_blocks(const pkv_tensor* cache, const pkv_tensor* src_dst_pa
   p.num_pairs = n;
   p.num_blocks = cache->shape[0];
   p.err = s->err;
-  p.check_overlap = g_opt_debug_sync.load() != 0;  // O(pairs^2) device check, debug only
+  p.check_overlap = debug_sync();  // O(pairs^2) device check, debug only
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   return finish_call(s, launch_copy_blocks(p, cs), cs, "copy_blocks");
 }

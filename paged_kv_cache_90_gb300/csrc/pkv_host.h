@@ -30,6 +30,8 @@ pkv_status ensure_workspace(DeviceState* s, size_t bytes, cudaStream_t stream);
 pkv_status finish_call(DeviceState* s, cudaError_t launch_err, cudaStream_t stream, const char* what);
 // Whether calls only validate their arguments (PKV_OPT_DRY_RUN).
 bool dry_run();
+// Whether calls synchronise and check the device (PKV_OPT_DEBUG_SYNC).
+bool debug_sync();
 
 int elt_bytes(int dtype);
 const char* dtype_name(int dtype);
@@ -38,10 +40,18 @@ bool supported_head_dim(int64_t d);
 bool supported_block_size(int64_t bs);
 pkv_status check_basic(const pkv_tensor* t, const char* name, int ndim);
 pkv_status check_dtype(const pkv_tensor* t, const char* name, int a, int b = -1, int c = -1);
-// A cache descriptor; `i8`: token-scaled PKV_I8 caches are taken too.
-pkv_status check_cache(const pkv_tensor* c, const char* name, bool i8 = false);
+// A cache descriptor; `scaled`: token-scaled PKV_I8 caches and 4-bit ones are taken too.
+pkv_status check_cache(const pkv_tensor* c, const char* name, bool scaled = false);
+// Columns of a head (a 4-bit cache's descriptor has its bytes).
+int64_t cache_head_dim(const pkv_tensor* c);
 // Scales of a token-scaled cache, [num_blocks, num_kv_heads, block_size] f32.
 pkv_status check_scales(const pkv_tensor* t, const char* name);
+// Group scales of a 4-bit cache, [num_blocks, num_kv_heads, block_size, head_dim / 16] e4m3.
+pkv_status check_group_scales(const pkv_tensor* t, const char* name);
+// Anything that pages are copied of: a cache or a scale array.
+pkv_status check_pages(const pkv_tensor* c, const char* name);
+// (src, dst) block pairs.
+pkv_status check_pairs(const pkv_tensor* pairs);
 bool same_layout(const pkv_tensor* a, const pkv_tensor* b);
 
 }  // namespace pkv

@@ -57,6 +57,8 @@ struct CopyBlocksParams {
   bool check_overlap;        // first check that destinations are distinct and no source
 };
 cudaError_t launch_copy_blocks(const CopyBlocksParams& p, cudaStream_t stream);
+// Compares the pairs with one another (pairs, num_pairs and err alone).
+cudaError_t launch_copy_pairs_check(const CopyBlocksParams& p, cudaStream_t stream);
 
 // ---- paged decode attention ------------------------------------------------------
 struct DecodeParams {

@@ -1,6 +1,6 @@
 // token_api.cu — the C ABI's calls around a step's new tokens (declared in
-// include/pkv.h): rotary positions with the cache write, the token-scaled 8-bit cache
-// (write, read back, decode) and attention of drafted trees.  Argument checks and kernel
+// include/pkv.h): rotary positions with the cache write, the token-scaled 8-bit cache and
+// the 4-bit one (write, read back, decode) and attention of drafted trees.  Argument checks and kernel
 // selection only.
 #include <cmath>
 
@@ -21,22 +21,36 @@ pkv_status check_scales_of(const pkv_tensor* t, const char* name, const pkv_tens
   return PKV_OK;
 }
 
-// The caches with, for PKV_I8 ones, their scale arrays.
+pkv_status check_groups_of(const pkv_tensor* t, const char* name, const pkv_tensor* cache) {
+  const pkv_status st = check_group_scales(t, name);
+  if (st) return st;
+  for (int i = 0; i < 4; ++i)
+    if (t->shape[i] != (i < 3 ? cache->shape[i] : cache->shape[3] / 8))
+      return fail(PKV_ERR_INVALID_ARG, "%s must be [num_blocks, num_kv_heads, block_size, head_dim / 16]", name);
+  return PKV_OK;
+}
+
+// The caches with, for PKV_I8 and PKV_E2M1X2 ones, their scale arrays.
 pkv_status check_caches(const pkv_tensor* kc, const pkv_tensor* vc, const pkv_tensor* ks, const pkv_tensor* vs) {
   pkv_status st;
   if ((st = check_cache(kc, "key_cache", true)) || (st = check_cache(vc, "value_cache", true))) return st;
   if (!same_layout(kc, vc))
     return fail(PKV_ERR_INVALID_ARG, "key_cache and value_cache must share dtype, shape and strides");
-  if (!supported_head_dim(kc->shape[3]))
-    return fail(PKV_ERR_UNSUPPORTED, "head_dim %lld (supported: 64, 128)", (long long)kc->shape[3]);
+  if (!supported_head_dim(cache_head_dim(kc)))
+    return fail(PKV_ERR_UNSUPPORTED, "head_dim %lld (supported: 64, 128)", (long long)cache_head_dim(kc));
   if (!supported_block_size(kc->shape[2]))
     return fail(PKV_ERR_UNSUPPORTED, "block_size %lld (supported: 2, 4, 8, 16, 32)", (long long)kc->shape[2]);
-  if (kc->dtype != PKV_I8) {
-    if (ks || vs) return fail(PKV_ERR_INVALID_ARG, "k_scales and v_scales are for a token-scaled (i8) cache only");
+  if (kc->dtype != PKV_I8 && kc->dtype != PKV_E2M1X2) {
+    if (ks || vs)
+      return fail(PKV_ERR_INVALID_ARG, "k_scales and v_scales are for a token-scaled (i8) or 4-bit (e2m1x2) cache only");
     return PKV_OK;
   }
-  if (!ks || !vs) return fail(PKV_ERR_INVALID_ARG, "an i8 cache needs k_scales and v_scales");
-  if ((st = check_scales_of(ks, "k_scales", kc)) || (st = check_scales_of(vs, "v_scales", vc))) return st;
+  if (!ks || !vs) return fail(PKV_ERR_INVALID_ARG, "an %s cache needs k_scales and v_scales", dtype_name(kc->dtype));
+  if (kc->dtype == PKV_E2M1X2) {
+    if ((st = check_groups_of(ks, "k_scales", kc)) || (st = check_groups_of(vs, "v_scales", vc))) return st;
+  } else if ((st = check_scales_of(ks, "k_scales", kc)) || (st = check_scales_of(vs, "v_scales", vc))) {
+    return st;
+  }
   if (!same_layout(ks, vs)) return fail(PKV_ERR_INVALID_ARG, "k_scales and v_scales must share their strides");
   return PKV_OK;
 }
@@ -64,9 +78,9 @@ pkv_status token_prepare(const pkv_tensor* key, const pkv_tensor* value, const p
     return st;
   if (!same_layout(key, value)) return fail(PKV_ERR_INVALID_ARG, "key and value must share dtype, shape and strides");
   const int64_t T = key->shape[0], Hk = key->shape[1], D = key->shape[2];
-  if (kc->shape[1] != Hk || kc->shape[3] != D)
-    return fail(PKV_ERR_INVALID_ARG, "key [T, %lld, %lld] does not match the cache's [.., %lld, .., %lld]",
-                (long long)Hk, (long long)D, (long long)kc->shape[1], (long long)kc->shape[3]);
+  if (kc->shape[1] != Hk || cache_head_dim(kc) != D)
+    return fail(PKV_ERR_INVALID_ARG, "key [T, %lld, %lld] does not match the cache's %lld heads of %lld columns",
+                (long long)Hk, (long long)D, (long long)kc->shape[1], (long long)cache_head_dim(kc));
   if (slots->shape[0] != T) return fail(PKV_ERR_INVALID_ARG, "slot_mapping must be [num_tokens]");
   if ((st = check_contiguous(slots, "slot_mapping")) || (st = check_rows16(key, "key")) ||
       (st = check_rows16(value, "value")))
@@ -95,8 +109,13 @@ pkv_status token_prepare(const pkv_tensor* key, const pkv_tensor* value, const p
   p.w.block_size = int(kc->shape[2]);
   p.w.num_blocks = kc->shape[0];
   if (ks) {
-    p.k_token_scales = static_cast<float*>(ks->data);
-    p.v_token_scales = static_cast<float*>(vs->data);
+    if (kc->dtype == PKV_E2M1X2) {
+      p.k_group_scales = static_cast<unsigned char*>(ks->data);
+      p.v_group_scales = static_cast<unsigned char*>(vs->data);
+    } else {
+      p.k_token_scales = static_cast<float*>(ks->data);
+      p.v_token_scales = static_cast<float*>(vs->data);
+    }
     p.ts_block = ks->stride[0];
     p.ts_head = ks->stride[1];
   }
@@ -128,7 +147,7 @@ pkv_status tree_prepare(const pkv_tensor* out, const pkv_tensor* query, const pk
   if (Hq % num_kv_heads)
     return fail(PKV_ERR_INVALID_ARG, "num_heads (%lld) must be a multiple of num_kv_heads (%d)", (long long)Hq,
                 num_kv_heads);
-  if (kc->shape[2] != block_size || kc->shape[3] != D)
+  if (kc->shape[2] != block_size || cache_head_dim(kc) != D)
     return fail(PKV_ERR_INVALID_ARG, "block_size / head_dim must match the cache");
   if (tables->shape[1] != max_blocks || max_blocks < 1)
     return fail(PKV_ERR_INVALID_ARG, "block_tables must be [num_seqs, max_blocks_per_seq]");
@@ -166,14 +185,19 @@ pkv_status tree_prepare(const pkv_tensor* out, const pkv_tensor* query, const pk
   p.cs_block = kc->stride[0];
   p.cs_head = kc->stride[1];
   if (ks) {
-    p.k_token_scales = static_cast<const float*>(ks->data);
-    p.v_token_scales = static_cast<const float*>(vs->data);
+    if (kc->dtype == PKV_E2M1X2) {
+      p.k_group_scales = static_cast<const unsigned char*>(ks->data);
+      p.v_group_scales = static_cast<const unsigned char*>(vs->data);
+    } else {
+      p.k_token_scales = static_cast<const float*>(ks->data);
+      p.v_token_scales = static_cast<const float*>(vs->data);
+    }
     p.ts_block = ks->stride[0];
     p.ts_head = ks->stride[1];
   }
-  const bool fp8 = kc->dtype == PKV_FP8_E4M3;
-  p.k_head_scales = fp8 ? kc->head_scales : nullptr;
-  p.v_head_scales = fp8 ? vc->head_scales : nullptr;
+  const bool factor = kc->dtype == PKV_FP8_E4M3 || kc->dtype == PKV_E2M1X2;
+  p.k_head_scales = factor ? kc->head_scales : nullptr;
+  p.v_head_scales = factor ? vc->head_scales : nullptr;
   p.block_tables = static_cast<const int32_t*>(tables->data);
   p.bt_stride = tables->stride[0];
   p.context_lens = static_cast<const int32_t*>(lens->data);
@@ -192,8 +216,8 @@ pkv_status tree_prepare(const pkv_tensor* out, const pkv_tensor* query, const pk
   p.block_size = block_size;
   p.max_blocks_per_seq = max_blocks;
   p.num_blocks = kc->shape[0];
-  p.qk_scale_log2 = float(double(scale) * 1.4426950408889634 * double(fp8 && !p.k_head_scales ? kc->scale : 1.f));
-  p.v_scale = fp8 && !p.v_head_scales ? vc->scale : 1.f;
+  p.qk_scale_log2 = float(double(scale) * 1.4426950408889634 * double(factor && !p.k_head_scales ? kc->scale : 1.f));
+  p.v_scale = factor && !p.v_head_scales ? vc->scale : 1.f;
   return PKV_OK;
 }
 
@@ -230,6 +254,82 @@ void radians_to_turn(double f, uint64_t* high, uint32_t* low) {
   *high = uint64_t(n >> 32);
   *low = uint32_t(n);
 }
+
+// pkv_rotary_and_cache, and with `axes` pkv_rotary_axes_and_cache.
+pkv_status rotary_write(const pkv_tensor* query_out, const pkv_tensor* query, const pkv_tensor* key,
+                        const pkv_tensor* value, const pkv_tensor* positions, const pkv_tensor* key_cache,
+                        const pkv_tensor* value_cache, const pkv_tensor* k_scales, const pkv_tensor* v_scales,
+                        const pkv_tensor* slot_mapping, const pkv_rotary* rotary, const pkv_rotary_axes* axes,
+                        cudaStream_t stream, const char* what) {
+  TokenParams p;
+  pkv_status st = token_prepare(key, value, key_cache, value_cache, k_scales, v_scales, slot_mapping, &p);
+  if (st) return st;
+  if ((st = check_basic(query, "query", 3)) || (st = check_basic(query_out, "query_out", 3)) ||
+      (st = check_basic(positions, "positions", axes ? 2 : 1)) ||
+      (st = check_dtype(positions, "positions", PKV_I32, PKV_I64)))
+    return st;
+  if (!axes && (st = check_contiguous(positions, "positions"))) return st;
+  const int64_t T = key->shape[0], D = key->shape[2];
+  if (query->dtype != key->dtype || query_out->dtype != key->dtype)
+    return fail(PKV_ERR_INVALID_ARG, "query, query_out, key and value must share a dtype");
+  if (query->shape[0] != T || query->shape[2] != D)
+    return fail(PKV_ERR_INVALID_ARG, "query must be [num_tokens=%lld, num_heads, head_dim=%lld]", (long long)T,
+                (long long)D);
+  for (int i = 0; i < 3; ++i)
+    if (query_out->shape[i] != query->shape[i]) return fail(PKV_ERR_INVALID_ARG, "query_out shape must equal query shape");
+  if ((st = check_rows16(query, "query")) || (st = check_rows16(query_out, "query_out"))) return st;
+  if (query_out->data == query->data &&
+      (query_out->stride[0] != query->stride[0] || query_out->stride[1] != query->stride[1]))
+    return fail(PKV_ERR_INVALID_ARG, "query_out in place of query must have its strides");
+  if (positions->shape[axes ? 1 : 0] != T || (axes && positions->shape[0] < axes->num_axes))
+    return fail(PKV_ERR_INVALID_ARG, "positions must be [%snum_tokens]", axes ? "num_axes, " : "");
+  if (reinterpret_cast<uintptr_t>(positions->data) % elt_bytes(positions->dtype))
+    return fail(PKV_ERR_INVALID_ARG, "positions must be aligned to their elements");
+  const int c = key_cache->dtype;
+  if (c != key->dtype && c != PKV_FP8_E4M3 && c != PKV_I8 && c != PKV_E2M1X2)
+    return fail(PKV_ERR_UNSUPPORTED, "writing %s tokens into a %s cache", dtype_name(key->dtype), dtype_name(c));
+  if (!rotary) return fail(PKV_ERR_INVALID_ARG, "null rotary pointer");
+  if (rotary->rotary_dim < 0 || rotary->rotary_dim % 2 || rotary->rotary_dim > D)
+    return fail(PKV_ERR_INVALID_ARG, "rotary_dim (%d) must be even, 0 to head_dim (%lld)", rotary->rotary_dim, (long long)D);
+  if (rotary->interleaved != 0 && rotary->interleaved != 1) return fail(PKV_ERR_INVALID_ARG, "interleaved is 0 or 1");
+  if (!std::isfinite(float(rotary->magnitude)))
+    return fail(PKV_ERR_INVALID_ARG, "the rotary magnitude must be finite in binary32");
+  if (axes) {
+    if (axes->num_axes < 1 || axes->num_axes > 4) return fail(PKV_ERR_INVALID_ARG, "num_axes must be 1 to 4");
+    for (int i = 0; i < rotary->rotary_dim / 2; ++i) {
+      if (axes->axis[i] < 0 || axes->axis[i] >= axes->num_axes)
+        return fail(PKV_ERR_INVALID_ARG, "pair %d: axis %d is not one of the %d", i, axes->axis[i], axes->num_axes);
+      p.axis[i >> 4] |= uint32_t(axes->axis[i]) << (2 * (i & 15));
+    }
+    p.num_axes = axes->num_axes;
+    p.pos_stride = positions->stride[0];
+  }
+  if (query->shape[1] > 65535) return fail(PKV_ERR_UNSUPPORTED, "too many heads");
+  p.query = query->data;
+  p.query_out = query_out->data;
+  p.q_stride_t = query->stride[0];
+  p.q_stride_h = query->stride[1];
+  p.qo_stride_t = query_out->stride[0];
+  p.qo_stride_h = query_out->stride[1];
+  p.num_heads = int(query->shape[1]);
+  p.positions = positions->data;
+  p.positions64 = positions->dtype == PKV_I64;
+  p.rotary_dim = rotary->rotary_dim;
+  p.interleaved = rotary->interleaved != 0;
+  p.magnitude = float(rotary->magnitude);
+  for (int i = 0; i < rotary->rotary_dim / 2; ++i) {
+    const double f = rotary->frequency[i];
+    if (!(std::fabs(f) <= 0x1p64))
+      return fail(PKV_ERR_INVALID_ARG, "rotary frequency %d is not a number of at most 2^64 in magnitude", i);
+    radians_to_turn(f, &p.turns[i], &p.turns_low[i]);
+  }
+  if (dry_run() || T == 0 || (p.num_heads == 0 && p.w.num_kv_heads == 0)) return PKV_OK;
+  DeviceState* s;
+  if ((st = device_state(&s))) return st;
+  p.w.err = s->err;
+  return finish_call(s, launch_token_write(p, stream), stream, what);
+}
+
 
 // Blocks of a tensor-core kernel.
 int tree_grid(int num_sms, int per_sm) {
@@ -300,60 +400,18 @@ pkv_status pkv_rotary_and_cache(const pkv_tensor* query_out, const pkv_tensor* q
                                 const pkv_tensor* value, const pkv_tensor* positions, const pkv_tensor* key_cache,
                                 const pkv_tensor* value_cache, const pkv_tensor* k_scales, const pkv_tensor* v_scales,
                                 const pkv_tensor* slot_mapping, const pkv_rotary* rotary, pkv_stream stream) {
-  TokenParams p;
-  pkv_status st = token_prepare(key, value, key_cache, value_cache, k_scales, v_scales, slot_mapping, &p);
-  if (st) return st;
-  if ((st = check_basic(query, "query", 3)) || (st = check_basic(query_out, "query_out", 3)) ||
-      (st = check_basic(positions, "positions", 1)) ||
-      (st = check_dtype(positions, "positions", PKV_I32, PKV_I64)) || (st = check_contiguous(positions, "positions")))
-    return st;
-  const int64_t T = key->shape[0], D = key->shape[2];
-  if (query->dtype != key->dtype || query_out->dtype != key->dtype)
-    return fail(PKV_ERR_INVALID_ARG, "query, query_out, key and value must share a dtype");
-  if (query->shape[0] != T || query->shape[2] != D)
-    return fail(PKV_ERR_INVALID_ARG, "query must be [num_tokens=%lld, num_heads, head_dim=%lld]", (long long)T,
-                (long long)D);
-  for (int i = 0; i < 3; ++i)
-    if (query_out->shape[i] != query->shape[i]) return fail(PKV_ERR_INVALID_ARG, "query_out shape must equal query shape");
-  if ((st = check_rows16(query, "query")) || (st = check_rows16(query_out, "query_out"))) return st;
-  if (query_out->data == query->data &&
-      (query_out->stride[0] != query->stride[0] || query_out->stride[1] != query->stride[1]))
-    return fail(PKV_ERR_INVALID_ARG, "query_out in place of query must have its strides");
-  if (positions->shape[0] != T) return fail(PKV_ERR_INVALID_ARG, "positions must be [num_tokens]");
-  const int c = key_cache->dtype;
-  if (c != key->dtype && c != PKV_FP8_E4M3 && c != PKV_I8)
-    return fail(PKV_ERR_UNSUPPORTED, "writing %s tokens into a %s cache", dtype_name(key->dtype), dtype_name(c));
-  if (!rotary) return fail(PKV_ERR_INVALID_ARG, "null rotary pointer");
-  if (rotary->rotary_dim < 0 || rotary->rotary_dim % 2 || rotary->rotary_dim > D)
-    return fail(PKV_ERR_INVALID_ARG, "rotary_dim (%d) must be even, 0 to head_dim (%lld)", rotary->rotary_dim, (long long)D);
-  if (rotary->interleaved != 0 && rotary->interleaved != 1) return fail(PKV_ERR_INVALID_ARG, "interleaved is 0 or 1");
-  if (!std::isfinite(float(rotary->magnitude)))
-    return fail(PKV_ERR_INVALID_ARG, "the rotary magnitude must be finite in binary32");
-  if (query->shape[1] > 65535) return fail(PKV_ERR_UNSUPPORTED, "too many heads");
-  p.query = query->data;
-  p.query_out = query_out->data;
-  p.q_stride_t = query->stride[0];
-  p.q_stride_h = query->stride[1];
-  p.qo_stride_t = query_out->stride[0];
-  p.qo_stride_h = query_out->stride[1];
-  p.num_heads = int(query->shape[1]);
-  p.positions = positions->data;
-  p.positions64 = positions->dtype == PKV_I64;
-  p.rotary_dim = rotary->rotary_dim;
-  p.interleaved = rotary->interleaved != 0;
-  p.magnitude = float(rotary->magnitude);
-  for (int i = 0; i < rotary->rotary_dim / 2; ++i) {
-    const double f = rotary->frequency[i];
-    if (!(std::fabs(f) <= 0x1p64))
-      return fail(PKV_ERR_INVALID_ARG, "rotary frequency %d is not a number of at most 2^64 in magnitude", i);
-    radians_to_turn(f, &p.turns[i], &p.turns_low[i]);
-  }
-  if (dry_run() || T == 0 || (p.num_heads == 0 && p.w.num_kv_heads == 0)) return PKV_OK;
-  DeviceState* s;
-  if ((st = device_state(&s))) return st;
-  p.w.err = s->err;
-  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  return finish_call(s, launch_token_write(p, cs), cs, "rotary_and_cache");
+  return rotary_write(query_out, query, key, value, positions, key_cache, value_cache, k_scales, v_scales, slot_mapping,
+                      rotary, nullptr, static_cast<cudaStream_t>(stream), "rotary_and_cache");
+}
+
+pkv_status pkv_rotary_axes_and_cache(const pkv_tensor* query_out, const pkv_tensor* query, const pkv_tensor* key,
+                                     const pkv_tensor* value, const pkv_tensor* positions, const pkv_tensor* key_cache,
+                                     const pkv_tensor* value_cache, const pkv_tensor* k_scales,
+                                     const pkv_tensor* v_scales, const pkv_tensor* slot_mapping,
+                                     const pkv_rotary* rotary, const pkv_rotary_axes* axes, pkv_stream stream) {
+  if (!axes) return fail(PKV_ERR_INVALID_ARG, "null axes pointer");
+  return rotary_write(query_out, query, key, value, positions, key_cache, value_cache, k_scales, v_scales, slot_mapping,
+                      rotary, axes, static_cast<cudaStream_t>(stream), "rotary_axes_and_cache");
 }
 
 pkv_status pkv_quantize_and_cache(const pkv_tensor* key, const pkv_tensor* value, const pkv_tensor* key_cache,
@@ -362,8 +420,8 @@ pkv_status pkv_quantize_and_cache(const pkv_tensor* key, const pkv_tensor* value
   TokenParams p;
   pkv_status st = token_prepare(key, value, key_cache, value_cache, k_scales, v_scales, slot_mapping, &p);
   if (st) return st;
-  if (key_cache->dtype != PKV_I8)
-    return fail(PKV_ERR_UNSUPPORTED, "quantize_and_cache writes i8 caches (got %s)", dtype_name(key_cache->dtype));
+  if (key_cache->dtype != PKV_I8 && key_cache->dtype != PKV_E2M1X2)
+    return fail(PKV_ERR_UNSUPPORTED, "quantize_and_cache writes i8 and e2m1x2 caches (got %s)", dtype_name(key_cache->dtype));
   if (dry_run() || p.w.num_tokens == 0 || p.w.num_kv_heads == 0) return PKV_OK;
   DeviceState* s;
   if ((st = device_state(&s))) return st;
@@ -396,8 +454,8 @@ pkv_status pkv_paged_attention_decode_quantized(const pkv_tensor* out, const pkv
   pkv_status st = tree_prepare(out, query, key_cache, value_cache, k_scales, v_scales, block_tables, context_lens,
                                nullptr, nullptr, num_kv_heads, scale, block_size, max_blocks_per_seq, &p);
   if (st) return st;
-  if (key_cache->dtype != PKV_I8)
-    return fail(PKV_ERR_UNSUPPORTED, "decode_quantized reads i8 caches (got %s)", dtype_name(key_cache->dtype));
+  if (key_cache->dtype != PKV_I8 && key_cache->dtype != PKV_E2M1X2)
+    return fail(PKV_ERR_UNSUPPORTED, "decode_quantized reads i8 and e2m1x2 caches (got %s)", dtype_name(key_cache->dtype));
   if (sliding_window < 0) return fail(PKV_ERR_INVALID_ARG, "sliding_window must be >= 0 (0: no window)");
   p.sliding_window = sliding_window;
   return tree_launch(p, static_cast<cudaStream_t>(stream), "paged_attention_decode_quantized");

@@ -7,20 +7,25 @@
 
 namespace pkv {
 
-constexpr int kI8 = 5;  // PKV_I8, beside DType's codes
+constexpr int kI8 = 5, kE2M1 = 6;  // PKV_I8, PKV_E2M1X2, beside DType's codes
 
 // ---- rotary_and_cache, quantize_and_cache, read_cache ----------------------------------
 struct TokenParams {
   CacheWriteParams w;          // key / value, caches, slots (no amax)
   float* k_token_scales;       // i8 cache: [NB, Hk, bs] scales (or null)
   float* v_token_scales;
-  int64_t ts_block, ts_head;   // their strides, elements
+  unsigned char* k_group_scales;  // 4-bit cache: [NB, Hk, bs, D / 16] e4m3 (or null)
+  unsigned char* v_group_scales;
+  int64_t ts_block, ts_head;   // strides of the scales, elements
   const void* query;           // [T, Hq, D], the key's dtype
   void* query_out;
   int64_t q_stride_t, q_stride_h, qo_stride_t, qo_stride_h;
   int num_heads;               // 0: no query
-  const void* positions;       // [T]
+  const void* positions;       // [T], or [num_axes, T]
   bool positions64;
+  int num_axes;                // 0: one position for all pairs
+  int64_t pos_stride;          // between two axes' positions
+  uint32_t axis[4];            // pair i's axis in bits 2 (i % 16) of word i / 16
   int rotary_dim;              // 0: no rotation
   bool interleaved;
   float magnitude;
@@ -43,8 +48,10 @@ struct TreeParams {
   int64_t cs_block, cs_head;   // elements
   const float* k_token_scales; // i8 cache: [NB, Hk, bs]
   const float* v_token_scales;
+  const unsigned char* k_group_scales;  // 4-bit cache: [NB, Hk, bs, D / 16] e4m3
+  const unsigned char* v_group_scales;
   int64_t ts_block, ts_head;
-  const float* k_head_scales;  // e4m3 cache: [Hk] (or null)
+  const float* k_head_scales;  // e4m3 and 4-bit caches: [Hk] (or null)
   const float* v_head_scales;
   const int32_t* block_tables;
   int64_t bt_stride;

@@ -1,6 +1,6 @@
 // token_ops.cu — per-token passes between the activations and the paged cache: rotary
 // positions with the cache write (rotary_and_cache), the write into a token-scaled
-// 8-bit cache (quantize_and_cache), and the read back (read_cache).
+// 8-bit cache or a 4-bit one (quantize_and_cache), and the read back (read_cache).
 //
 // All are streams: every byte is touched once, so HBM bounds the large calls and the
 // launch the small ones.  A head row (head_dim elements) is held by head_dim / 8
@@ -14,6 +14,7 @@
 // write is held back by its instructions, 190 for 8 columns of two rows, issued in four of five
 // cycles.
 #include "device_common.cuh"
+#include "e2m1_codes.cuh"
 #include "token_internal.h"
 
 namespace pkv {
@@ -190,6 +191,40 @@ __device__ __forceinline__ uint64_t angle_at(int64_t pos, uint64_t turn, const u
   return angle;
 }
 
+// The position that turns pair k of token t.
+__device__ __forceinline__ int64_t axis_position(const TokenParams& p, int64_t t, int k) {
+  const int64_t at = int64_t((p.axis[k >> 4] >> (2 * (k & 15))) & 3u) * p.pos_stride + t;
+  return p.positions64 ? static_cast<const int64_t*>(p.positions)[at] : static_cast<const int32_t*>(p.positions)[at];
+}
+
+// A row's columns 8 l .. 8 l + 7 to a 4-bit cache: `codes` and `scales` are the row's first bytes,
+// `f` the cache's factor.  All lanes of the row call it (`live`: the row is stored); a group is
+// two lanes', and its scales leave as words of four.
+template <int D>
+__device__ __forceinline__ void store_e2m1(const float (&x)[8], uint32_t top, float f, unsigned char* codes,
+                                           unsigned char* scales, int l, bool live) {
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  const e2m1::Group g(top, f, DivRn(__fmul_rn(6.f, f)));
+  uint32_t four = g.byte << (8 * ((l >> 1) & 3));
+  four |= __shfl_xor_sync(0xffffffffu, four, 2);
+  four |= __shfl_xor_sync(0xffffffffu, four, 4);
+  if (!live) return;
+  *reinterpret_cast<uint32_t*>(codes + 4 * l) = e2m1::encode8(x, g);
+  if ((l & 7) == 0) *reinterpret_cast<uint32_t*>(scales + (l >> 1)) = four;
+}
+
+__device__ __forceinline__ uint32_t top_bits8(const float (&x)[8]) {
+  uint32_t top = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  return top;
+}
+
+__device__ __forceinline__ float cache_factor(const CacheWriteParams& w, bool is_v, int h) {
+  const float* hs = is_v ? w.v_head_scales : w.k_head_scales;
+  return hs ? __ldg(hs + h) : is_v ? w.v_scale : w.k_scale;
+}
+
 // One warp per slice of a token's rows: query rows, then key rows, then value rows.  Block
 // (x, y): slice y of kWarps tokens.
 //
@@ -207,6 +242,7 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
   constexpr int kN = kLayout == kOdd ? 1 : kBatch;
   constexpr bool kJoined = kLayout != kHalves && (Src::bytes == 2 || kLayout == kOdd);  // 8 columns side by side
   __shared__ uint64_t turns[64];
+  __shared__ alignas(16) float staged[kWarps][256];  // (a 4-bit cache) a pass's rows, columns in order
   const int lane = threadIdx.x & 31, sub = lane / kLanes, l = lane % kLanes;
   const int half = p.rotary_dim / 2;
   if (int(threadIdx.x) < half) turns[threadIdx.x] = p.turns[threadIdx.x];
@@ -217,7 +253,7 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
   if (t >= p.w.num_tokens) return;
   const int64_t slot = one_answer(p.w.slot_mapping[t]);
   int64_t pos = 0;
-  if (half) pos = p.positions64 ? static_cast<const int64_t*>(p.positions)[t] : static_cast<const int32_t*>(p.positions)[t];
+  if (half && !p.num_axes) pos = p.positions64 ? static_cast<const int64_t*>(p.positions)[t] : static_cast<const int32_t*>(p.positions)[t];
   int c0 = 8 * l, c1 = 8 * l + 4, pair0 = 0, pair1 = 0;  // (pairs of the first and last four columns)
   bool turning = false;
   if (kLayout == kHalves) {
@@ -273,7 +309,8 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
       for (int i = 0; i < 4; ++i) {
         const int k = (i < 2 ? pair0 : pair1 - 2) + i;
         turn[i] = kLayout == kHalves ? turning : k < half;
-        const uint64_t angle = turn[i] ? angle_at(pos, turns[k], p.turns_low + k) : 0;
+        const int64_t at = p.num_axes && turn[i] ? axis_position(p, t, k) : pos;
+        const uint64_t angle = turn[i] ? angle_at(at, turns[k], p.turns_low + k) : 0;
         sincospif(float(int32_t(uint32_t(angle >> 32))) * 0x1p-31f, &sn[i], &cs[i]);  // 2^-32 turn, in [-1/2, 1/2)
         cs[i] *= p.magnitude;
         sn[i] *= p.magnitude;
@@ -299,7 +336,8 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
               const int c = c0 + i;
               if (c >= p.rotary_dim) break;
               const int pair = c < half ? c : c - half;
-              const uint64_t angle = angle_at(pos, turns[pair], p.turns_low + pair);
+              const int64_t at = p.num_axes ? axis_position(p, t, pair) : pos;
+              const uint64_t angle = angle_at(at, turns[pair], p.turns_low + pair);
               float s, k;
               sincospif(float(int32_t(uint32_t(angle >> 32))) * 0x1p-31f, &s, &k);
               s *= p.magnitude;
@@ -325,8 +363,24 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
       if (is_q) {
         if (live) store_row<Src>(p.query_out, t * p.qo_stride_t + h * p.qo_stride_h, c0, c1, kJoined, x);
       }
-      const int64_t at = blk * p.w.cs_block + h * p.w.cs_head + int64_t(off) * D;
       void* dst = is_v ? p.w.value_cache : p.w.key_cache;
+      if (p.w.cache_dtype == kE2M1) {
+        if ((p0 + u + 1) * kRows <= hq) continue;  // (query rows alone)
+        float* row = staged[threadIdx.x >> 5] + sub * D;
+        *reinterpret_cast<float4*>(row + c0) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4*>(row + c1) = make_float4(x[4], x[5], x[6], x[7]);
+        __syncwarp();
+        const float4 a = *reinterpret_cast<const float4*>(row + 8 * l), b = *reinterpret_cast<const float4*>(row + 8 * l + 4);
+        __syncwarp();
+        const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        const bool stored = live && !is_q && in_cache;
+        store_e2m1<D>(y, top_bits8(y), stored ? cache_factor(p.w, is_v, h) : 1.f,
+                      static_cast<unsigned char*>(dst) + blk * p.w.cs_block + h * p.w.cs_head + off * (D / 2),
+                      (is_v ? p.v_group_scales : p.k_group_scales) + blk * p.ts_block + h * p.ts_head + off * (D / 16), l,
+                      stored);
+        continue;
+      }
+      const int64_t at = blk * p.w.cs_block + h * p.w.cs_head + int64_t(off) * D;
       if (p.w.cache_dtype == kI8) {
         const uint32_t top = row_top_bits<kLanes>(x);
         if (live && !is_q && in_cache) {
@@ -348,18 +402,19 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
   if (slot >= p.w.num_blocks * p.w.block_size && lane == 0 && blockIdx.y == 0) raise_device_error(p.w.err, kErrSlot);
 }
 
-// The same for the write into a token-scaled cache alone: key rows, then value rows.
-template <typename Src, int D>
+// The same for the write into a token-scaled or a 4-bit cache alone: key rows, then value rows.
+template <typename Src, int D, int type>
 __global__ void __launch_bounds__(32 * kWarps) token_quantize_kernel(const __grid_constant__ TokenParams p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;
   constexpr bool kJoined = Src::bytes == 2;
+  constexpr bool kInOrder = kJoined || type == kE2M1;  // a lane's columns are side by side
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int64_t t = int64_t(blockIdx.x) * kWarps + one_answer(int(threadIdx.x) >> 5);
   if (t >= p.w.num_tokens) return;
   const int lane = threadIdx.x & 31, sub = lane / kLanes, l = lane % kLanes;
   const int64_t slot = one_answer(p.w.slot_mapping[t]);
-  const int c0 = kJoined ? 8 * l : 4 * l, c1 = kJoined ? c0 + 4 : c0 + D / 2;
+  const int c0 = kInOrder ? 8 * l : 4 * l, c1 = kInOrder ? c0 + 4 : c0 + D / 2;
   const int hk = p.w.num_kv_heads;
   // (a pass is of one tensor: the choice is the warp's, not a lane's)
   const int tensor = (hk + kRows - 1) / kRows, passes = 2 * tensor;
@@ -382,12 +437,21 @@ __global__ void __launch_bounds__(32 * kWarps) token_quantize_kernel(const __gri
     }
     const int64_t blk = slot >> (31 - __clz(p.w.block_size));
     const int off = int(slot) & (p.w.block_size - 1);
-    const int64_t to = blk * p.w.cs_block + int64_t(off) * D, scale_to = blk * p.ts_block + off;
+    const int64_t to = blk * p.w.cs_block + int64_t(off) * (type == kE2M1 ? D / 2 : D);
+    const int64_t scale_to = blk * p.ts_block + off * (type == kE2M1 ? D / 16 : 1);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       if (p0 + u >= last) break;
       const bool is_v = p0 + u >= tensor;
       const int h = (p0 + u - (is_v ? tensor : 0)) * kRows + sub;
+      if constexpr (type == kE2M1) {
+        float x[8];
+        raw[u].expand(x);
+        store_e2m1<D>(x, top_bits8(x), h < hk ? cache_factor(p.w, is_v, h) : 1.f,
+                      static_cast<unsigned char*>(is_v ? p.w.value_cache : p.w.key_cache) + to + h * p.w.cs_head,
+                      (is_v ? p.v_group_scales : p.k_group_scales) + scale_to + h * p.ts_head, l, h < hk);
+        continue;
+      }
       const uint32_t top = raw[u].template row_top<kLanes>();
       if (h >= hk) continue;
       float x[8];
@@ -432,8 +496,15 @@ __global__ void __launch_bounds__(32 * kWarps) token_read_kernel(const __grid_co
       if (p0 + u >= last || h >= hk) continue;
       const int elt = type == kF32 ? 4 : type == kBF16 ? 2 : 1;
       const unsigned char* src = static_cast<const unsigned char*>(is_v ? p.w.value_cache : p.w.key_cache) +
-                                 (blk * p.w.cs_block + h * p.w.cs_head + int64_t(off) * D) * elt;
-      if (type == kF32) {
+                                 (blk * p.w.cs_block + h * p.w.cs_head + int64_t(off) * (type == kE2M1 ? D / 2 : D)) * elt;
+      if (type == kE2M1) {
+        const unsigned char* g = (is_v ? p.v_group_scales : p.k_group_scales) + blk * p.ts_block + h * p.ts_head + off * (D / 16);
+        a[u].x = *reinterpret_cast<const uint16_t*>(src + c0 / 2);
+        b[u].x = *reinterpret_cast<const uint16_t*>(src + c1 / 2);
+        a[u].y = g[c0 >> 4];
+        b[u].y = g[c1 >> 4];
+        s[u] = cache_factor(p.w, is_v, h);
+      } else if (type == kF32) {
         a[u] = *reinterpret_cast<const uint4*>(src + 4 * c0);
         b[u] = *reinterpret_cast<const uint4*>(src + 4 * c1);
       } else if (type == kBF16) {
@@ -462,7 +533,13 @@ __global__ void __launch_bounds__(32 * kWarps) token_read_kernel(const __grid_co
         continue;
       }
       float x[8];
-      if (type == kF32) {
+      if (type == kE2M1) {
+        e2m1::widen4(a[u].x, x);
+        e2m1::widen4(b[u].x, x + 4);
+        const float g = __fmul_rn(e2m1::scale1(a[u].y), s[u]), e = __fmul_rn(e2m1::scale1(b[u].y), s[u]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], i < 4 ? g : e);
+      } else if (type == kF32) {
         Chunk<F32>::expand(a[u], x);
         Chunk<F32>::expand(b[u], x + 4);
       } else if (type == kBF16) {
@@ -516,7 +593,9 @@ template <typename Src, int D>
 cudaError_t launch_write(const TokenParams& p, cudaStream_t stream) {
   const int rows = p.num_heads + 2 * p.w.num_kv_heads;
   if (p.num_heads == 0 && p.rotary_dim == 0 && p.w.cache_dtype == kI8)
-    return launch(token_quantize_kernel<Src, D>, p, rows, stream);
+    return launch(token_quantize_kernel<Src, D, kI8>, p, rows, stream);
+  if (p.num_heads == 0 && p.rotary_dim == 0 && p.w.cache_dtype == kE2M1)
+    return launch(token_quantize_kernel<Src, D, kE2M1>, p, rows, stream);
   if (p.rotary_dim == 0 || p.interleaved) return launch(token_write_kernel<Src, D, kPairs>, p, rows, stream);
   return p.rotary_dim % 8 == 0 ? launch(token_write_kernel<Src, D, kHalves>, p, rows, stream)
                                : launch(token_write_kernel<Src, D, kOdd>, p, rows, stream);
@@ -529,6 +608,7 @@ cudaError_t launch_read(const TokenParams& p, cudaStream_t stream) {
     case kF32: return launch(token_read_kernel<Dst, D, kF32>, p, rows, stream);
     case kBF16: return launch(token_read_kernel<Dst, D, kBF16>, p, rows, stream);
     case kE4M3: return launch(token_read_kernel<Dst, D, kE4M3>, p, rows, stream);
+    case kE2M1: return launch(token_read_kernel<Dst, D, kE2M1>, p, rows, stream);
     default: return launch(token_read_kernel<Dst, D, kI8>, p, rows, stream);
   }
 }

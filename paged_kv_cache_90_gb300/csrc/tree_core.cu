@@ -1,7 +1,8 @@
 // tree_core.cu — attention of drafted trees and decode over a token-scaled cache on the
 // CUDA cores: the path for what the tensor-core kernels do not take (f32 queries, f32 and
-// e4m3 caches, bf16 caches of block sizes 2 and 4, groups of more than 128 query heads, a
-// scale that is not above zero, rows not aligned to 16 bytes).
+// e4m3 caches, bf16 caches of block sizes 2 and 4, 4-bit caches whose blocks' scales are not 16
+// aligned bytes a head, groups of more than 128 query heads, a scale that is not above zero, rows
+// not aligned to 16 bytes).
 //
 // One thread block per (query row, query head).  Its four warps take 32 keys at a time in
 // turn: a lane computes one key's score from 16-byte loads of the key's row, then every
@@ -11,6 +12,9 @@
 // one key row per lane and by re-reading the keys for every head of a group; it is a
 // path for rare types, not a fast one: 64 trees of 5 to 24 nodes over 160 to 2048 positions
 // take 3.4 ms here (bf16), 62 us on the tensor cores.
+#include <type_traits>
+
+#include "e2m1_codes.cuh"
 #include "tree_common.cuh"
 
 namespace pkv {
@@ -19,6 +23,7 @@ namespace {
 constexpr int kWarps = 4;
 
 struct I8 { static constexpr int bytes = 1; };
+struct E2M1 {};  // (two codes a byte)
 
 template <typename KV>
 __device__ __forceinline__ void expand16(const uint4& v, float* f) { Chunk<KV>::expand(v, f); }
@@ -53,6 +58,7 @@ __global__ void __launch_bounds__(kWarps * 32) tree_core_kernel(const __grid_con
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   constexpr int kCols = D / 32;
+  constexpr bool kFour = std::is_same<KV, E2M1>::value;
   __shared__ float q_sh[D];
   __shared__ float o_sh[kWarps][D];
   __shared__ float2 ml_sh[kWarps];
@@ -94,7 +100,7 @@ __global__ void __launch_bounds__(kWarps * 32) tree_core_kernel(const __grid_con
   for (int j0 = e.lo + 32 * warp; j0 < e.L; j0 += 32 * kWarps) {
     const int j = j0 + lane;
     bool on = j < e.L && (j < e.P || tree::sees_node(mask, j - e.P));
-    int64_t at = 0;
+    int64_t at = 0, gat = 0;
     float z = -INFINITY, vs = 1.f;
     if (on) {
       const int lb = j / p.block_size, off = j - lb * p.block_size;
@@ -103,16 +109,34 @@ __global__ void __launch_bounds__(kWarps * 32) tree_core_kernel(const __grid_con
         raise_device_error(p.err, kErrTableEntry);
         blk = 0;
       }
-      at = int64_t(blk) * p.cs_block + int64_t(kvh) * p.cs_head + int64_t(off) * D;
-      const uint4* row = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.key_cache) + at * KV::bytes);
-      constexpr int kPer = 16 / KV::bytes;
       float acc = 0.f;
-#pragma unroll 4
-      for (int c = 0; c < D / kPer; ++c) {
-        float f[kPer];
-        expand16<KV>(row[c], f);
+      if constexpr (kFour) {
+        at = int64_t(blk) * p.cs_block + int64_t(kvh) * p.cs_head + int64_t(off) * (D / 2);
+        gat = int64_t(blk) * p.ts_block + int64_t(kvh) * p.ts_head + int64_t(off) * (D / 16);
+        const uint2* row = reinterpret_cast<const uint2*>(static_cast<const unsigned char*>(p.key_cache) + at);
+#pragma unroll 2
+        for (int c = 0; c < D / 16; ++c) {  // a group
+          const uint2 w = row[c];
+          float f[16], part = 0.f;
+          e2m1::widen4(w.x, f);
+          e2m1::widen4(w.x >> 16, f + 4);
+          e2m1::widen4(w.y, f + 8);
+          e2m1::widen4(w.y >> 16, f + 12);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) acc = fmaf(f[i], q_sh[c * kPer + i], acc);
+          for (int i = 0; i < 16; ++i) part = fmaf(f[i], q_sh[c * 16 + i], part);
+          acc = fmaf(part, e2m1::scale1(p.k_group_scales[gat + c]), acc);
+        }
+      } else {
+        at = int64_t(blk) * p.cs_block + int64_t(kvh) * p.cs_head + int64_t(off) * D;
+        const uint4* row = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.key_cache) + at * KV::bytes);
+        constexpr int kPer = 16 / KV::bytes;
+#pragma unroll 4
+        for (int c = 0; c < D / kPer; ++c) {
+          float f[kPer];
+          expand16<KV>(row[c], f);
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) acc = fmaf(f[i], q_sh[c * kPer + i], acc);
+        }
       }
       if (p.k_token_scales) {
         const int64_t sc = int64_t(blk) * p.ts_block + int64_t(kvh) * p.ts_head + off;
@@ -141,9 +165,21 @@ __global__ void __launch_bounds__(kWarps * 32) tree_core_kernel(const __grid_con
       const int k = __ffs(int(todo)) - 1;
       todo &= todo - 1;
       const float wk = __shfl_sync(0xffffffffu, w * vs, k);
-      const int64_t ak = __shfl_sync(0xffffffffu, at, k) + lane;
+      const int64_t ak = __shfl_sync(0xffffffffu, at, k);
+      if constexpr (kFour) {
+        const int64_t gk = __shfl_sync(0xffffffffu, gat, k);
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) o[c] = fmaf(wk, value_at<KV>(p.value_cache, ak + 32 * c), o[c]);
+        for (int c = 0; c < kCols; ++c) {
+          const int col = lane + 32 * c;
+          const uint32_t code = static_cast<const unsigned char*>(p.value_cache)[ak + (col >> 1)] >> (4 * (col & 1));
+          float f[4];
+          e2m1::widen4(code, f);
+          o[c] = fmaf(wk, f[0] * e2m1::scale1(p.v_group_scales[gk + (col >> 4)]), o[c]);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) o[c] = fmaf(wk, value_at<KV>(p.value_cache, ak + lane + 32 * c), o[c]);
+      }
     }
   }
 #pragma unroll
@@ -193,6 +229,7 @@ cudaError_t launch_tree_core(const TreeParams& p, cudaStream_t stream) {
     case kF32: return launch_kv<F32>(p, stream);
     case kBF16: return launch_kv<BF16>(p, stream);
     case kE4M3: return launch_kv<E4M3>(p, stream);
+    case kE2M1: return launch_kv<E2M1>(p, stream);
     default: return launch_kv<I8>(p, stream);
   }
 }
