@@ -343,7 +343,9 @@ pkv_status tree_launch(TreeParams& p, cudaStream_t stream, const char* what) {
   if (st) return st;
   p.err = s->err;
   if (!tree_tensor_supported(p)) return finish_call(s, launch_tree_core(p, stream), stream, what);
-  const int grid = tree_grid(s->num_sms, decode_i8_supported(p) ? decode_i8_blocks_per_sm(p.group) : 1);
+  const int grid = tree_grid(s->num_sms, decode_i8_supported(p)     ? decode_i8_blocks_per_sm(p.group)
+                                         : decode_e2m1_supported(p) ? decode_e2m1_blocks_per_sm(p.group)
+                                                                    : 1);
   const int rows = tree_part_rows(p.num_tokens, p.group, !p.query_start_loc, p.kv_dtype == kI8);
   std::unique_lock<std::mutex> use(s->ws_use);
   if ((st = ensure_workspace(s, tree_workspace(grid, rows, p.head_dim), stream))) return st;
@@ -487,7 +489,8 @@ int64_t pkv_tree_workspace_bytes(int32_t num_seqs, int32_t num_tokens, int32_t n
       cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     num_sms = int(TreeSplit::kMaxSms);
   const size_t tree = tree_workspace(tree_grid(num_sms, 1), tree_part_rows(num_tokens, group, false, false), head_dim);
-  const size_t decode = tree_workspace(tree_grid(num_sms, decode_i8_blocks_per_sm(group)),
+  const int i8 = decode_i8_blocks_per_sm(group), e2m1 = decode_e2m1_blocks_per_sm(group);
+  const size_t decode = tree_workspace(tree_grid(num_sms, i8 > e2m1 ? i8 : e2m1),
                                        tree_part_rows(num_tokens, group, true, false), head_dim);
   return int64_t(tree > decode || group > 16 ? tree : decode);
 }

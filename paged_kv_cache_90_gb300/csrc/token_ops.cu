@@ -36,6 +36,10 @@ __device__ __forceinline__ T one_answer(T x) { return __shfl_sync(0xffffffffu, x
 // half + i, half a multiple of 4); kOdd is the latter for any other half.
 enum Layout { kPairs, kHalves, kOdd };
 
+// What a rotary write does beside the common case, each kind compiled by itself: with the tests for
+// both in one kernel a prefill step's write took 75 us instead of 71.
+enum Kind { kPlain, kAxes, kFour };  // several position axes; a 4-bit cache (with or without them)
+
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -236,13 +240,14 @@ __device__ __forceinline__ float cache_factor(const CacheWriteParams& w, bool is
 // cosines are within 3e-7 whatever the position, where a binary32 angle in radians would lose
 // all its bits past 2^24.  A lane has the same four pairs in every row, so their cosines and
 // sines are in its registers.
-template <typename Src, int D, Layout kLayout>
+template <typename Src, int D, Layout kLayout, Kind kKind>
 __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_constant__ TokenParams p) {
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row, rows of a pass
   constexpr int kN = kLayout == kOdd ? 1 : kBatch;
   constexpr bool kJoined = kLayout != kHalves && (Src::bytes == 2 || kLayout == kOdd);  // 8 columns side by side
   __shared__ uint64_t turns[64];
-  __shared__ alignas(16) float staged[kWarps][256];  // (a 4-bit cache) a pass's rows, columns in order
+  __shared__ alignas(16) float staged[kKind == kFour ? kWarps : 1][kKind == kFour ? 256 : 4];  // a pass's rows, columns in order
+  const bool axes = kKind == kAxes || (kKind == kFour && p.num_axes);
   const int lane = threadIdx.x & 31, sub = lane / kLanes, l = lane % kLanes;
   const int half = p.rotary_dim / 2;
   if (int(threadIdx.x) < half) turns[threadIdx.x] = p.turns[threadIdx.x];
@@ -253,7 +258,7 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
   if (t >= p.w.num_tokens) return;
   const int64_t slot = one_answer(p.w.slot_mapping[t]);
   int64_t pos = 0;
-  if (half && !p.num_axes) pos = p.positions64 ? static_cast<const int64_t*>(p.positions)[t] : static_cast<const int32_t*>(p.positions)[t];
+  if (half && !axes) pos = p.positions64 ? static_cast<const int64_t*>(p.positions)[t] : static_cast<const int32_t*>(p.positions)[t];
   int c0 = 8 * l, c1 = 8 * l + 4, pair0 = 0, pair1 = 0;  // (pairs of the first and last four columns)
   bool turning = false;
   if (kLayout == kHalves) {
@@ -309,7 +314,7 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
       for (int i = 0; i < 4; ++i) {
         const int k = (i < 2 ? pair0 : pair1 - 2) + i;
         turn[i] = kLayout == kHalves ? turning : k < half;
-        const int64_t at = p.num_axes && turn[i] ? axis_position(p, t, k) : pos;
+        const int64_t at = axes && turn[i] ? axis_position(p, t, k) : pos;
         const uint64_t angle = turn[i] ? angle_at(at, turns[k], p.turns_low + k) : 0;
         sincospif(float(int32_t(uint32_t(angle >> 32))) * 0x1p-31f, &sn[i], &cs[i]);  // 2^-32 turn, in [-1/2, 1/2)
         cs[i] *= p.magnitude;
@@ -336,7 +341,7 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
               const int c = c0 + i;
               if (c >= p.rotary_dim) break;
               const int pair = c < half ? c : c - half;
-              const int64_t at = p.num_axes ? axis_position(p, t, pair) : pos;
+              const int64_t at = axes ? axis_position(p, t, pair) : pos;
               const uint64_t angle = angle_at(at, turns[pair], p.turns_low + pair);
               float s, k;
               sincospif(float(int32_t(uint32_t(angle >> 32))) * 0x1p-31f, &s, &k);
@@ -364,7 +369,7 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
         if (live) store_row<Src>(p.query_out, t * p.qo_stride_t + h * p.qo_stride_h, c0, c1, kJoined, x);
       }
       void* dst = is_v ? p.w.value_cache : p.w.key_cache;
-      if (p.w.cache_dtype == kE2M1) {
+      if constexpr (kKind == kFour) {
         if ((p0 + u + 1) * kRows <= hq) continue;  // (query rows alone)
         float* row = staged[threadIdx.x >> 5] + sub * D;
         *reinterpret_cast<float4*>(row + c0) = make_float4(x[0], x[1], x[2], x[3]);
@@ -378,23 +383,23 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
                       static_cast<unsigned char*>(dst) + blk * p.w.cs_block + h * p.w.cs_head + off * (D / 2),
                       (is_v ? p.v_group_scales : p.k_group_scales) + blk * p.ts_block + h * p.ts_head + off * (D / 16), l,
                       stored);
-        continue;
-      }
-      const int64_t at = blk * p.w.cs_block + h * p.w.cs_head + int64_t(off) * D;
-      if (p.w.cache_dtype == kI8) {
-        const uint32_t top = row_top_bits<kLanes>(x);
-        if (live && !is_q && in_cache) {
-          const float s = token_scale(top);
-          store_codes(dst, at, c0, c1, kJoined, quantize8(x, s));
-          if (l == 0) (is_v ? p.v_token_scales : p.k_token_scales)[blk * p.ts_block + h * p.ts_head + off] = s;
-        }
-      } else if (live && !is_q && in_cache) {
-        if (p.w.cache_dtype == kE4M3) {
-          const float* hs = is_v ? p.w.v_head_scales : p.w.k_head_scales;
-          const float s = hs ? __ldg(hs + h) : is_v ? p.w.v_scale : p.w.k_scale;
-          store_codes(dst, at, c0, c1, kJoined, e4m3_quantize8(x, DivRn(s)));
-        } else {
-          store_row<Src>(dst, at, c0, c1, kJoined, x);
+      } else {
+        const int64_t at = blk * p.w.cs_block + h * p.w.cs_head + int64_t(off) * D;
+        if (p.w.cache_dtype == kI8) {
+          const uint32_t top = row_top_bits<kLanes>(x);
+          if (live && !is_q && in_cache) {
+            const float s = token_scale(top);
+            store_codes(dst, at, c0, c1, kJoined, quantize8(x, s));
+            if (l == 0) (is_v ? p.v_token_scales : p.k_token_scales)[blk * p.ts_block + h * p.ts_head + off] = s;
+          }
+        } else if (live && !is_q && in_cache) {
+          if (p.w.cache_dtype == kE4M3) {
+            const float* hs = is_v ? p.w.v_head_scales : p.w.k_head_scales;
+            const float s = hs ? __ldg(hs + h) : is_v ? p.w.v_scale : p.w.k_scale;
+            store_codes(dst, at, c0, c1, kJoined, e4m3_quantize8(x, DivRn(s)));
+          } else {
+            store_row<Src>(dst, at, c0, c1, kJoined, x);
+          }
         }
       }
     }
@@ -589,6 +594,13 @@ cudaError_t launch(K kern, const TokenParams& p, int rows, cudaStream_t stream) 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <typename Src, int D, Kind kKind>
+cudaError_t launch_rotary(const TokenParams& p, int rows, cudaStream_t stream) {
+  if (p.rotary_dim == 0 || p.interleaved) return launch(token_write_kernel<Src, D, kPairs, kKind>, p, rows, stream);
+  return p.rotary_dim % 8 == 0 ? launch(token_write_kernel<Src, D, kHalves, kKind>, p, rows, stream)
+                               : launch(token_write_kernel<Src, D, kOdd, kKind>, p, rows, stream);
+}
+
 template <typename Src, int D>
 cudaError_t launch_write(const TokenParams& p, cudaStream_t stream) {
   const int rows = p.num_heads + 2 * p.w.num_kv_heads;
@@ -596,9 +608,8 @@ cudaError_t launch_write(const TokenParams& p, cudaStream_t stream) {
     return launch(token_quantize_kernel<Src, D, kI8>, p, rows, stream);
   if (p.num_heads == 0 && p.rotary_dim == 0 && p.w.cache_dtype == kE2M1)
     return launch(token_quantize_kernel<Src, D, kE2M1>, p, rows, stream);
-  if (p.rotary_dim == 0 || p.interleaved) return launch(token_write_kernel<Src, D, kPairs>, p, rows, stream);
-  return p.rotary_dim % 8 == 0 ? launch(token_write_kernel<Src, D, kHalves>, p, rows, stream)
-                               : launch(token_write_kernel<Src, D, kOdd>, p, rows, stream);
+  if (p.w.cache_dtype == kE2M1) return launch_rotary<Src, D, kFour>(p, rows, stream);
+  return p.num_axes ? launch_rotary<Src, D, kAxes>(p, rows, stream) : launch_rotary<Src, D, kPlain>(p, rows, stream);
 }
 
 template <typename Dst, int D>
