@@ -16,11 +16,14 @@
 // shifts and two selections for sixteen codes, and their scales by a transposition of 8 tokens x 8
 // groups (movmatrix).
 //
-// A warp takes 32 positions of a tile of 128, its loads of K a step ahead and of V during the
-// scores.  A warp has its own reference m of a row (moved when a token exceeds it by 2^8) and its
-// own sums; the four are folded at an item's end, in order.  Weights are rounded to f16, half a
-// step, 2^-11, down to 2^-21 of the row's largest, 2^-32 of that below.  Everything else is exact or
-// binary32.
+// A warp takes 32 positions of a tile of 128 and brings them itself, two steps ahead, into a ring
+// of three in shared memory (asynchronous copies of 16 bytes a lane).  A warp has its own reference
+// m of a row (moved when a token exceeds it by 2^8) and its own sums; the four are folded at an
+// item's end, in order.  Weights are rounded to f16, half a step, 2^-11, down to 2^-21 of the row's
+// largest, 2^-32 of that below.  Everything else is exact or binary32.
+#include <algorithm>
+#include <mutex>
+
 #include "decode_few.cuh"
 #include "e2m1_codes.cuh"
 
@@ -33,8 +36,10 @@ using tree::kGap;
 using tree::Range;
 using tree::Walk;
 
-// A row's weights are 2^(z - m + kTop): under 2^15 with a reference that lags by 2^kGap.
+constexpr int kStages = 3;  // of a warp's ring
+// A row's weights are 2^(z - m + kTop): at most 2^15 with a reference that lags by 2^kGap.
 constexpr float kTop = 7.f;
+constexpr float kNoLift = 3.402823466e38f;  // kTop - m before the first score, with which every score moves m
 
 __device__ __forceinline__ uint32_t mul_pair(uint32_t a, __half2 s) {
   const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&a), s);
@@ -42,27 +47,62 @@ __device__ __forceinline__ uint32_t mul_pair(uint32_t a, __half2 s) {
 }
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 
-// 16 bytes of a head of 128 columns' row, 8 of one of 64
-template <int D>
-__device__ __forceinline__ void load_codes(const unsigned char* p, uint32_t (&w)[D / 32]) { load_words(p, w); }
-__device__ __forceinline__ void load_word(const unsigned char* p, uint32_t (&w)[2]) { load_words(p, w); }
-__device__ __forceinline__ void load_word(const unsigned char* p, uint32_t (&w)[1]) {
-  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(w[0]) : "l"(p));
+__device__ __forceinline__ void copy16(uint32_t dst, const unsigned char* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-// The group scales of lane (g, t)'s token: groups 2t, 2t + 1 of 8, or group t of 4.
+__device__ __forceinline__ void copy4(uint32_t dst, const unsigned char* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void end_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void load_shared(uint32_t a, uint32_t (&w)[4]) {
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
+}
+__device__ __forceinline__ void load_shared(uint32_t a, uint32_t (&w)[2]) {
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a));
+}
+__device__ __forceinline__ void load_shared(uint32_t a, uint32_t (&w)[1]) {
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(a));
+}
+// Two group scales (one, at D = 64), as they are stored.
 template <int D>
-__device__ __forceinline__ uint32_t load_scales(const unsigned char* p) {
-  return D == 128 ? uint32_t(*reinterpret_cast<const uint16_t*>(p)) : uint32_t(*p);
+__device__ __forceinline__ uint32_t load_scales(uint32_t a) {
+  uint32_t x;
+  if (D == 128) asm volatile("ld.shared.u16 %0, [%1];" : "=r"(x) : "r"(a));
+  else asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(a));
+  return x;
 }
 
-// NT x 8 rows: the query heads of a KV head.
+// A stage of the ring: 32 positions' rows of K, of V, and the group scales of both.
+//
+// Eight rows lie in 8 kRow bytes.  Lane (g, t) reads 16 (D = 64: 8) bytes of row g of K and 8 (4) of
+// rows 2t and 2t + 1 of V; where a row goes, and its halves, makes neither meet a bank twice.
+template <int D>
+struct Stage {
+  static constexpr int kRow = D / 2, kGroups = D / 16;  // bytes and groups of a row
+  static constexpr uint32_t kV = 32 * kRow, kKScales = 64 * kRow, kVScales = kKScales + 32 * kGroups;
+  static constexpr uint32_t kBytes = kVScales + 32 * kGroups;
+  __device__ static __forceinline__ uint32_t at(int r, int byte) {
+    if (D == 128) return (r ^ ((r >> 1) & 1)) * kRow + (byte ^ ((r & 4) << 3));  // (the upper rows' halves swapped)
+    return ((r & 4) | ((r >> 1) & 1) | (((r ^ (r >> 2)) & 1) << 1)) * kRow + byte;
+  }
+};
 template <int D, int NT>
+constexpr size_t smem_bytes() {
+  return size_t(kWarps) * kStages * Stage<D>::kBytes + sizeof(Shared<D, NT>);
+}
+
+// NT x 8 rows: the query heads of a KV head.  Blocks of 2^kShift tokens, 8 to 32.
+template <int D, int NT, int kShift>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
 decode_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ TreeSplit sp) {
-  constexpr int kRow = D / 2, kGroups = D / 16;  // bytes and groups of a row
-  constexpr int kK = D / 32;                     // words of a K row that a lane holds
-  constexpr int kV = D / 64;                     // and of a V row
-  __shared__ Shared<D, NT> sh;
+  using S = Stage<D>;
+  constexpr int kRow = S::kRow, kGroups = S::kGroups, kMask = (1 << kShift) - 1;
+  constexpr int kK = D / 32, kV = D / 64;  // words of a row of K and of V that a lane holds
+  extern __shared__ __align__(16) unsigned char smem[];
+  Shared<D, NT>& sh = *reinterpret_cast<Shared<D, NT>*>(smem + kWarps * kStages * S::kBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing of the caller's is read before
   asm volatile("griddepcontrol.launch_dependents;");
@@ -70,50 +110,75 @@ decode_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
   const Range* rg = &sh.range;
   Walk it;
   it.start(p, sp, rg);
-  const int bs_mask = p.block_size - 1;
   int64_t at = rg->from;
   TreeSplit::Tail tail = {0, 0, 0, 0};
+  const uint32_t ring = smem_addr(smem) + warp * kStages * S::kBytes;
+  // a copy of codes: of row crow of eight rows, 16 bytes from cbyte on (at D = 64 of 2 x 8 rows)
+  const int crow = D == 128 ? lane >> 2 : (lane >> 1) & 7, cbyte = (D == 128 ? lane & 3 : lane & 1) * 16;
+  const int ceight = D == 128 ? 0 : lane >> 4;
+  const uint32_t cto = ring + S::at(crow, cbyte) + ceight * 8 * kRow;
+  const uint32_t kfrom = ring + S::at(g, 4 * kK * t);
+  const uint32_t vfrom0 = ring + S::kV + S::at(2 * t, 4 * kV * g), vfrom1 = ring + S::kV + S::at(2 * t + 1, 4 * kV * g);
+  const uint32_t gfrom = ring + S::kKScales + g * kGroups + (D / 64) * t;  // of token g, the lane's groups of K
   for (; it.valid(); it.next(p, sp, rg)) {
     const int32_t* table = p.block_tables + int64_t(it.s) * p.bt_stride;
-    const int64_t head = int64_t(it.kvh) * p.cs_head, ghead = int64_t(it.kvh) * p.ts_head;
-    // the lane's part of token g's row of K (of tokens 2t, 2t + 1 of V), and of token g's scales
-    const unsigned char* kc = static_cast<const unsigned char*>(p.key_cache) + head + g * kRow + 4 * kK * t;
-    const unsigned char* vc = static_cast<const unsigned char*>(p.value_cache) + head + 2 * t * kRow + 4 * kV * g;
-    const unsigned char* kg = p.k_group_scales + ghead + g * kGroups + (D / 64) * t;
-    const unsigned char* vg = p.v_group_scales + ghead + g * kGroups + (D / 64) * t;
-    const int L = it.q.e.L, lo = it.q.e.lo, steps = it.j1 - it.j0;
-    int pos = it.q.base + it.j0 * kBN + 32 * warp + lane;
-    auto entry = [&](int at) -> int {
-      if (at >= L) return 0;
-      int e = __ldg(table + (at >> sp.bs_shift));
+    const int64_t head = int64_t(it.kvh) * p.cs_head + crow * kRow + cbyte, ghead = int64_t(it.kvh) * p.ts_head;
+    const unsigned char* kc = static_cast<const unsigned char*>(p.key_cache) + head;
+    const unsigned char* vc = static_cast<const unsigned char*>(p.value_cache) + head;
+    // the warp's steps: its 32 positions of each tile that start inside the context
+    const int L = it.q.e.L, lo = it.q.e.lo, first = it.q.base + it.j0 * kBN + 32 * warp;
+    const int steps = min(it.j1 - it.j0, (L - first + kBN - 1) / kBN);
+    // the table's entry of the lane's position of step j.  (0 where there is none: positions behind
+    // the context are read from block 0, whose numbers have no part: their scores are hidden, their
+    // value scales zero.)
+    auto entry = [&](int j) -> int {
+      const int pos = first + j * kBN + lane;
+      if (j >= steps || pos >= L) return 0;
+      int e = __ldg(table + (pos >> kShift));
       if (e < 0 || int64_t(e) >= p.num_blocks) {
         raise_device_error(p.err, kErrTableEntry);
         e = 0;
       }
       return e;
     };
-    // Eight positions from a multiple of 8 on share a block (of at least 8): its entry comes from the
-    // first one's lane.  (Positions past the context are read from block 0, whose numbers have no
-    // part: their scores are hidden, their value scales zero.)
-    int blk[2][2];
-    uint32_t kreg[2][2][kK];  // K rows g, g + 8 of 16 tokens
-    uint32_t ks[2][2], vs[2][2];  // their group scales, as they are stored
-    auto load_k = [&](int e) {
-      const int first = pos - lane;
+    // A step's first position is a block's first, so eight positions from a multiple of 8 on share a
+    // block and lie at known places in it.
+    auto copy_stage = [&](int e, uint32_t off) {
+      constexpr int kTokens = D == 128 ? 8 : 16;  // of a copy
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          blk[u][h] = __shfl_sync(0xffffffffu, e, 16 * u + 8 * h);
-          const int in = (first + 16 * u + 8 * h) & bs_mask;
-          load_codes<D>(kc + int64_t(blk[u][h]) * p.cs_block + in * kRow, kreg[u][h]);
-          const int64_t sc = int64_t(blk[u][h]) * p.ts_block + in * kGroups;
-          ks[u][h] = load_scales<D>(kg + sc);
-          vs[u][h] = load_scales<D>(vg + sc);
+      for (int c = 0; c < 32; c += kTokens) {
+        const int tok = c + 8 * ceight;
+        const int64_t src = int64_t(__shfl_sync(0xffffffffu, e, tok)) * p.cs_block + (tok & kMask) * kRow;
+        copy16(cto + off + c * kRow, kc + src);
+        copy16(cto + off + c * kRow + S::kV, vc + src);
+      }
+      constexpr int kPer = 16 / kGroups, kLanes = 32 / kPer;  // tokens' scales of 16 bytes, lanes for a tensor's
+      if (sp.vec_scales) {
+        const bool v = lane >= kLanes;
+        const int tok = lane % kLanes * kPer;
+        const int64_t src = ghead + int64_t(__shfl_sync(0xffffffffu, e, tok)) * p.ts_block + (tok & kMask) * kGroups;
+        if (lane < 2 * kLanes)
+          copy16(ring + off + (v ? S::kVScales : S::kKScales) + tok * kGroups,
+                 (v ? p.v_group_scales : p.k_group_scales) + src);
+      } else {  // (words of four, at any multiple of them)
+#pragma unroll 1
+        for (int c = 0; c < kGroups / 2; ++c) {  // 32 kGroups / 4 words a tensor, K's first
+          const bool v = c >= kGroups / 4;
+          const int byte = 4 * (32 * (c - (v ? kGroups / 4 : 0)) + lane), tok = byte / kGroups;
+          const int64_t src = ghead + int64_t(__shfl_sync(0xffffffffu, e, tok)) * p.ts_block + (tok & kMask) * kGroups +
+                              byte % kGroups;
+          copy4(ring + off + (v ? S::kVScales : S::kKScales) + byte, (v ? p.v_group_scales : p.k_group_scales) + src);
         }
+      }
     };
-    load_k(entry(pos));
-    int e_next = steps > 1 ? entry(pos + kBN) : 0;
+    int e_next = entry(0);
+#pragma unroll
+    for (int j = 0; j < kStages - 1; ++j) {
+      const int e = e_next;
+      e_next = entry(j + 1);
+      if (j < steps) copy_stage(e, j * S::kBytes);
+      end_copies();
+    }
 
     // the queries: B of the scores' product, columns permuted as K's are
     uint32_t qb[NT][4 * kK];
@@ -152,45 +217,48 @@ decode_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
       qf[n][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
     }
 
-    float m[NT][2], l[NT][2];  // of rows 2t, 2t + 1 (l: this lane's tokens)
-    float o[NT][4 * kV][4];    // O^T: see the products
+    float m[NT][2], lift[NT][2], l[NT][2];  // of rows 2t, 2t + 1: m, kTop - m, sum over this lane's tokens
+    float o[NT][4 * kV][4];                 // O^T: see the products
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       m[n][0] = m[n][1] = -INFINITY;
+      lift[n][0] = lift[n][1] = kNoLift;
       l[n][0] = l[n][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < 4 * kV; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
     }
 
+    uint32_t off = 0, off_next = (kStages - 1) * S::kBytes;  // this step's stage, and the one that is filled
 #pragma unroll 1
-    for (int j = 0; j < steps; ++j, pos += kBN) {
-      const int pos0 = pos - lane;
-      if (pos0 >= L) break;  // (the last tile: nothing for this warp)
-      // V rows 2t, 2t + 1, 2t + 8, 2t + 9 of 16 tokens, D / 8 codes from D / 8 g on
-      uint32_t v[2][4][kV];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const unsigned char* src =
-              vc + int64_t(blk[u][h]) * p.cs_block + ((pos0 + 16 * u + 8 * h) & bs_mask) * kRow;
-          load_word(src, v[u][2 * h]);
-          load_word(src + kRow, v[u][2 * h + 1]);
-        }
+    for (int j = 0; j < steps; ++j) {
+      const int pos0 = first + j * kBN;
+      wait_copies<kStages - 2>();
+      __syncwarp();  // every lane's copies have landed, and every lane has read the stage before
+      if (j + kStages - 1 < steps) copy_stage(e_next, off_next);
+      end_copies();
+      e_next = entry(j + kStages);
+      off_next = off;
       // S^T: tokens 16 u + g, + 8; rows 2t, 2t + 1
       float s[2][NT][4];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) s[u][n][0] = s[u][n][1] = s[u][n][2] = s[u][n][3] = 0.f;
-        const __half2 ga = as_half2(e2m1::scales2(ks[u][0])), gb = as_half2(e2m1::scales2(ks[u][1]));
+        uint32_t x[2][kK];
+        __half2 gs[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          load_shared(kfrom + off + (2 * u + h) * 8 * kRow, x[h]);
+          gs[h] = as_half2(e2m1::scales2(load_scales<D>(gfrom + off + (2 * u + h) * 8 * kGroups)));
+        }
 #pragma unroll
         for (int c = 0; c < kK; ++c) {
-          // (a word is half a group: of the lane's first or, at D = 128, from word 2 on its second)
-          const __half2 sa = c < 2 ? __low2half2(ga) : __high2half2(ga), sb = c < 2 ? __low2half2(gb) : __high2half2(gb);
+          // (a word is half a group: of the lane's first or, from word 2 on, its second)
+          const __half2 sa = c < 2 ? __low2half2(gs[0]) : __high2half2(gs[0]);
+          const __half2 sb = c < 2 ? __low2half2(gs[1]) : __high2half2(gs[1]);
           uint32_t a[4], b[4];
-          e2m1::widen8(kreg[u][0][c], a);
-          e2m1::widen8(kreg[u][1][c], b);
+          e2m1::widen8(x[0][c], a);
+          e2m1::widen8(x[1][c], b);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             a[i] = mul_pair(a[i], sa);
@@ -203,58 +271,60 @@ decode_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
           }
         }
       }
-      // the value scales of the lane's group for tokens 16 u + 8 h + 2t, + 1
-      __half2 gv[2][2];
+      // the weights' exponents
+      float z[2][NT][4];
       const bool cut = pos0 + 32 > L || pos0 < lo;  // some token is not attended to
+      auto exponents = [&]() {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t two = e2m1::scales2(vs[u][h]);
-          if (D == 64) two = __byte_perm(two, two, 0x1010);  // (each group twice: eight columns a lane)
-          two = transpose8x8(two);
-          if (cut) {
-            const int a = pos0 + 16 * u + 8 * h + 2 * t;
-            if (a >= L || a < lo) two &= 0xffff0000u;
-            if (a + 1 >= L || a + 1 < lo) two &= 0xffffu;
-          }
-          gv[u][h] = as_half2(two);
-        }
-      // the next step's codes and scales, and the entries of the one after it
-      pos += kBN;
-      if (j + 1 < steps) {
-        load_k(e_next);
-        e_next = j + 2 < steps ? entry(pos + kBN) : 0;
-      }
-      pos -= kBN;
-      bool move = false;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int at_tok = pos0 + 16 * u + 8 * h + g;
-          const bool hidden = cut && (at_tok >= L || at_tok < lo);
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              float& z = s[u][n][2 * h + r];
-              z = hidden ? -INFINITY : z * qf[n][r];
-              move |= z > m[n][r] + kGap;
+            for (int i = 0; i < 4; ++i) z[u][n][i] = fmaf(s[u][n][i], qf[n][i & 1], lift[n][i & 1]);
+        if (cut) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int a = pos0 + 16 * u + 8 * h + g;
+              if (a >= L || a < lo) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) z[u][n][2 * h] = z[u][n][2 * h + 1] = -INFINITY;
+              }
             }
         }
-      if (__any_sync(0xffffffffu, move)) {
+      };
+      exponents();
+      float over = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) over = fmaxf(over, z[u][n][i]);
+      if (__any_sync(0xffffffffu, over > kGap + kTop)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float a[2];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            float mx = fmaxf(fmaxf(s[0][n][r], s[0][n][2 + r]), fmaxf(s[1][n][r], s[1][n][2 + r]));
+            float mx = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int tok = pos0 + 16 * u + 8 * h + g;
+                const float x = s[u][n][2 * h + r] * qf[n][r];
+                mx = fmaxf(mx, cut && (tok >= L || tok < lo) ? -INFINITY : x);
+              }
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
             const bool go = mx > m[n][r] + kGap || (m[n][r] == -INFINITY && mx > -INFINITY);
             a[r] = go ? fast_exp2(m[n][r] - mx) : 1.f;  // (0 from -infinity)
-            if (go) m[n][r] = mx;
+            if (go) {
+              m[n][r] = mx;
+              lift[n][r] = kTop - mx;
+            }
             l[n][r] *= a[r];
           }
 #pragma unroll
@@ -265,39 +335,54 @@ decode_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
             o[n][i][3] *= a[1];
           }
         }
+        exponents();
       }
       // the weights, as B of the products
       uint32_t pb[2][NT][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - kTop;
-        const float r1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - kTop;
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float x = fast_exp2(s[u][n][2 * h] - r0), y = fast_exp2(s[u][n][2 * h + 1] - r1);
+            const float x = fast_exp2(z[u][n][2 * h]), y = fast_exp2(z[u][n][2 * h + 1]);
             l[n][0] += x;
             l[n][1] += y;
             pb[u][n][h] = transpose8x8(half2_bits(x, y));
           }
-      }
       // O^T: four products for each of the lane's words of V; the first 8 rows of product i are the
       // lanes' columns 2 i of the word, the others the columns after them
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int u = 0; u < 2; ++u) {
+        uint32_t v[2][2][kV];  // rows 2t, 2t + 1, 8 rows further: D / 8 codes from D / 8 g on
+        __half2 gs[2];         // the lane's group's scales of the two rows
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          load_shared(vfrom0 + off + (2 * u + h) * 8 * kRow, v[h][0]);
+          load_shared(vfrom1 + off + (2 * u + h) * 8 * kRow, v[h][1]);
+          uint32_t two = e2m1::scales2(
+              load_scales<D>(gfrom + off + (S::kVScales - S::kKScales) + (2 * u + h) * 8 * kGroups));
+          if (D == 64) two = __byte_perm(two, two, 0x1010);  // (each group twice: two lanes' columns)
+          two = transpose8x8(two);
+          if (cut) {
+            const int a = pos0 + 16 * u + 8 * h + 2 * t;
+            if (a >= L || a < lo) two &= 0xffff0000u;
+            if (a + 1 >= L || a + 1 < lo) two &= 0xffffu;
+          }
+          gs[h] = as_half2(two);
+        }
 #pragma unroll
         for (int w = 0; w < kV; ++w) {
           uint32_t even[2][4], odd[2][4];  // a column of two tokens, side by side
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t x = v[u][2 * h][w], y = v[u][2 * h + 1][w];
+            const uint32_t x = v[h][0][w], y = v[h][1][w];
             e2m1::widen8((x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u), even[h]);
             e2m1::widen8(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), odd[h]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              even[h][i] = mul_pair(even[h][i], gv[u][h]);
-              odd[h][i] = mul_pair(odd[h][i], gv[u][h]);
+              even[h][i] = mul_pair(even[h][i], gs[h]);
+              odd[h][i] = mul_pair(odd[h][i], gs[h]);
             }
           }
 #pragma unroll
@@ -306,6 +391,8 @@ decode_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
             for (int i = 0; i < 4; ++i)
               mma(o[n][4 * w + i], even[0][i], odd[0][i], even[1][i], odd[1][i], pb[u][n][0], pb[u][n][1]);
         }
+      }
+      off = off + S::kBytes == kStages * S::kBytes ? 0 : off + S::kBytes;
     }
 
     // the warps' results together
@@ -343,22 +430,43 @@ decode_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
 
 namespace {
 
-template <int D, int NT>
-cudaError_t launch_decode_e2m1_tpl(const TreeParams& p, const TreeSplit& sp, cudaStream_t stream) {
+template <int D, int NT, int kShift>
+cudaError_t launch_shift(const TreeParams& p, const TreeSplit& sp, cudaStream_t stream) {
+  constexpr size_t kSmem = decode_e2m1::smem_bytes<D, NT>();
+  static_assert((NT == 1 ? 3 : 2) * (kSmem + 1024) <= 228 * 1024, "shared memory");
+  constexpr int kDevices = 64;
+  auto kern = decode_e2m1::decode_e2m1_kernel<D, NT, kShift>;
+  static std::once_flag once[kDevices];
+  static cudaError_t set[kDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+  std::call_once(once[dev], [&] {
+    set[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+  });
+  if (set[dev] != cudaSuccess) return set[dev];
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(sp.grid));
   cfg.blockDim = dim3(decode_few::kThreads);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, decode_e2m1::decode_e2m1_kernel<D, NT>, p, sp);
+  e = cudaLaunchKernelEx(&cfg, kern, p, sp);
   note_launch();
   if (e != cudaSuccess) return e;
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_tree_merge(p, sp, stream);
+}
+
+template <int D, int NT>
+cudaError_t launch_decode_e2m1_tpl(const TreeParams& p, const TreeSplit& sp, cudaStream_t stream) {
+  if (p.block_size == 8) return launch_shift<D, NT, 3>(p, sp, stream);
+  return p.block_size == 16 ? launch_shift<D, NT, 4>(p, sp, stream) : launch_shift<D, NT, 5>(p, sp, stream);
 }
 
 }  // namespace
@@ -373,6 +481,8 @@ int decode_e2m1_blocks_per_sm(int group) { return group <= 8 ? 3 : 2; }
 
 cudaError_t launch_decode_e2m1(const TreeParams& p, TreeSplit sp, cudaStream_t stream) {
   sp.item_nodes = sp.tq = 1;
+  sp.vec_scales = !((reinterpret_cast<uintptr_t>(p.k_group_scales) | reinterpret_cast<uintptr_t>(p.v_group_scales) |
+                     p.ts_block | p.ts_head) & 15);
   if (p.head_dim == 128)
     return p.group <= 8 ? launch_decode_e2m1_tpl<128, 1>(p, sp, stream) : launch_decode_e2m1_tpl<128, 2>(p, sp, stream);
   return p.group <= 8 ? launch_decode_e2m1_tpl<64, 1>(p, sp, stream) : launch_decode_e2m1_tpl<64, 2>(p, sp, stream);
