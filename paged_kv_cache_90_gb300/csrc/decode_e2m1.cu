@@ -37,6 +37,7 @@ using tree::Range;
 using tree::Walk;
 
 constexpr int kStages = 3;  // of a warp's ring
+constexpr int blocks_per_sm(int nt) { return nt == 1 ? 3 : 2; }
 // A row's weights are 2^(z - m + kTop): at most 2^15 with a reference that lags by 2^kGap.
 constexpr float kTop = 7.f;
 constexpr float kNoLift = 3.402823466e38f;  // kTop - m before the first score, with which every score moves m
@@ -91,18 +92,20 @@ struct Stage {
 };
 template <int D, int NT>
 constexpr size_t smem_bytes() {
-  return size_t(kWarps) * kStages * Stage<D>::kBytes + sizeof(Shared<D, NT>);
+  static_assert(sizeof(Rows<D, NT>) <= kWarps * kStages * Stage<D>::kBytes, "the rows take the rings' place");
+  return size_t(kWarps) * kStages * Stage<D>::kBytes;
 }
 
 // NT x 8 rows: the query heads of a KV head.  Blocks of 2^kShift tokens, 8 to 32.
 template <int D, int NT, int kShift>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(NT))
 decode_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ TreeSplit sp) {
   using S = Stage<D>;
   constexpr int kRow = S::kRow, kGroups = S::kGroups, kMask = (1 << kShift) - 1;
   constexpr int kK = D / 32, kV = D / 64;  // words of a row of K and of V that a lane holds
-  extern __shared__ __align__(16) unsigned char smem[];
-  Shared<D, NT>& sh = *reinterpret_cast<Shared<D, NT>*>(smem + kWarps * kStages * S::kBytes);
+  extern __shared__ __align__(128) unsigned char smem[];  // the rings; at an item's end the warps' O
+  __shared__ Shared<D, NT> sh;
+  Rows<D, NT>& rows = *reinterpret_cast<Rows<D, NT>*>(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing of the caller's is read before
   asm volatile("griddepcontrol.launch_dependents;");
@@ -115,67 +118,76 @@ decode_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
   const uint32_t ring = smem_addr(smem) + warp * kStages * S::kBytes;
   // a copy of codes: of row crow of eight rows, 16 bytes from cbyte on (at D = 64 of 2 x 8 rows)
   const int crow = D == 128 ? lane >> 2 : (lane >> 1) & 7, cbyte = (D == 128 ? lane & 3 : lane & 1) * 16;
-  const int ceight = D == 128 ? 0 : lane >> 4;
-  const uint32_t cto = ring + S::at(crow, cbyte) + ceight * 8 * kRow;
+  const int ceight = D == 128 ? 0 : 8 * (lane >> 4);
+  const uint32_t block_bytes = uint32_t(p.cs_block), block_scales = uint32_t(p.ts_block);
+  const uint32_t cto = ring + S::at(crow, cbyte) + ceight * kRow;
   const uint32_t kfrom = ring + S::at(g, 4 * kK * t);
   const uint32_t vfrom0 = ring + S::kV + S::at(2 * t, 4 * kV * g), vfrom1 = ring + S::kV + S::at(2 * t + 1, 4 * kV * g);
   const uint32_t gfrom = ring + S::kKScales + g * kGroups + (D / 64) * t;  // of token g, the lane's groups of K
   for (; it.valid(); it.next(p, sp, rg)) {
-    const int32_t* table = p.block_tables + int64_t(it.s) * p.bt_stride;
-    const int64_t head = int64_t(it.kvh) * p.cs_head + crow * kRow + cbyte, ghead = int64_t(it.kvh) * p.ts_head;
+    const int64_t head = int64_t(it.kvh) * p.cs_head + (crow + (ceight & kMask)) * kRow + cbyte;
     const unsigned char* kc = static_cast<const unsigned char*>(p.key_cache) + head;
     const unsigned char* vc = static_cast<const unsigned char*>(p.value_cache) + head;
     // the warp's steps: its 32 positions of each tile that start inside the context
     const int L = it.q.e.L, lo = it.q.e.lo, first = it.q.base + it.j0 * kBN + 32 * warp;
     const int steps = min(it.j1 - it.j0, (L - first + kBN - 1) / kBN);
-    // the table's entry of the lane's position of step j.  (0 where there is none: positions behind
-    // the context are read from block 0, whose numbers have no part: their scores are hidden, their
-    // value scales zero.)
-    auto entry = [&](int j) -> int {
-      const int pos = first + j * kBN + lane;
-      if (j >= steps || pos >= L) return 0;
-      int e = __ldg(table + (pos >> kShift));
-      if (e < 0 || int64_t(e) >= p.num_blocks) {
-        raise_device_error(p.err, kErrTableEntry);
-        e = 0;
+    // The table's entries of the lane's positions, a step's each time.  (0 where there is none:
+    // positions behind the context are read from block 0, whose numbers have no part: their scores
+    // are hidden, their value scales zero.)
+    int entry_pos = first + lane;
+    const int32_t* entry_at = p.block_tables + int64_t(it.s) * p.bt_stride + (entry_pos >> kShift);
+    auto entry = [&]() -> uint32_t {
+      uint32_t e = 0;
+      if (entry_pos < L) {
+        e = uint32_t(__ldg(entry_at));
+        if (e >= uint32_t(p.num_blocks)) {
+          raise_device_error(p.err, kErrTableEntry);
+          e = 0;
+        }
       }
+      entry_pos += kBN;
+      entry_at += kBN >> kShift;
       return e;
     };
     // A step's first position is a block's first, so eight positions from a multiple of 8 on share a
     // block and lie at known places in it.
-    auto copy_stage = [&](int e, uint32_t off) {
+    constexpr int kPer = 16 / kGroups, kLanes = 32 / kPer;  // tokens' scales of 16 bytes, lanes for a tensor's
+    const bool of_v = lane >= kLanes;
+    const int stok = lane % kLanes * kPer;
+    const unsigned char* sc = (of_v ? p.v_group_scales : p.k_group_scales) + int64_t(it.kvh) * p.ts_head + (stok & kMask) * kGroups;
+    const uint32_t sto = ring + (of_v ? S::kVScales : S::kKScales) + stok * kGroups;
+    auto copy_stage = [&](uint32_t e, uint32_t off) {
       constexpr int kTokens = D == 128 ? 8 : 16;  // of a copy
+      const unsigned char *k = kc, *v = vc;
 #pragma unroll
       for (int c = 0; c < 32; c += kTokens) {
-        const int tok = c + 8 * ceight;
-        const int64_t src = int64_t(__shfl_sync(0xffffffffu, e, tok)) * p.cs_block + (tok & kMask) * kRow;
-        copy16(cto + off + c * kRow, kc + src);
-        copy16(cto + off + c * kRow + S::kV, vc + src);
+        if ((c & kMask) == 0 || kTokens > kMask) {  // (another block)
+          const uint64_t src = uint64_t(__shfl_sync(0xffffffffu, e, c + (kTokens > kMask ? ceight : 0))) * block_bytes;
+          k = kc + src;
+          v = vc + src;
+        }
+        copy16(cto + off + c * kRow, k + (c & kMask) * kRow);
+        copy16(cto + off + c * kRow + S::kV, v + (c & kMask) * kRow);
       }
-      constexpr int kPer = 16 / kGroups, kLanes = 32 / kPer;  // tokens' scales of 16 bytes, lanes for a tensor's
       if (sp.vec_scales) {
-        const bool v = lane >= kLanes;
-        const int tok = lane % kLanes * kPer;
-        const int64_t src = ghead + int64_t(__shfl_sync(0xffffffffu, e, tok)) * p.ts_block + (tok & kMask) * kGroups;
-        if (lane < 2 * kLanes)
-          copy16(ring + off + (v ? S::kVScales : S::kKScales) + tok * kGroups,
-                 (v ? p.v_group_scales : p.k_group_scales) + src);
+        const uint64_t src = uint64_t(__shfl_sync(0xffffffffu, e, stok)) * block_scales;
+        if (lane < 2 * kLanes) copy16(sto + off, sc + src);
       } else {  // (words of four, at any multiple of them)
 #pragma unroll 1
         for (int c = 0; c < kGroups / 2; ++c) {  // 32 kGroups / 4 words a tensor, K's first
           const bool v = c >= kGroups / 4;
           const int byte = 4 * (32 * (c - (v ? kGroups / 4 : 0)) + lane), tok = byte / kGroups;
-          const int64_t src = ghead + int64_t(__shfl_sync(0xffffffffu, e, tok)) * p.ts_block + (tok & kMask) * kGroups +
-                              byte % kGroups;
+          const int64_t src = int64_t(it.kvh) * p.ts_head + uint64_t(__shfl_sync(0xffffffffu, e, tok)) * block_scales +
+                              (tok & kMask) * kGroups + byte % kGroups;
           copy4(ring + off + (v ? S::kVScales : S::kKScales) + byte, (v ? p.v_group_scales : p.k_group_scales) + src);
         }
       }
     };
-    int e_next = entry(0);
+    uint32_t e_next = entry();
 #pragma unroll
     for (int j = 0; j < kStages - 1; ++j) {
-      const int e = e_next;
-      e_next = entry(j + 1);
+      const uint32_t e = e_next;
+      e_next = entry();
       if (j < steps) copy_stage(e, j * S::kBytes);
       end_copies();
     }
@@ -236,14 +248,12 @@ decode_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
       __syncwarp();  // every lane's copies have landed, and every lane has read the stage before
       if (j + kStages - 1 < steps) copy_stage(e_next, off_next);
       end_copies();
-      e_next = entry(j + kStages);
+      e_next = entry();
       off_next = off;
       // S^T: tokens 16 u + g, + 8; rows 2t, 2t + 1
       float s[2][NT][4];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) s[u][n][0] = s[u][n][1] = s[u][n][2] = s[u][n][3] = 0.f;
         uint32_t x[2][kK];
         __half2 gs[2];
 #pragma unroll
@@ -266,6 +276,7 @@ decode_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
+            if (c == 0) s[u][n][0] = s[u][n][1] = s[u][n][2] = s[u][n][3] = 0.f;
             mma(s[u][n], a[0], b[0], a[1], b[1], qb[n][4 * c], qb[n][4 * c + 1]);
             mma(s[u][n], a[2], b[2], a[3], b[3], qb[n][4 * c + 2], qb[n][4 * c + 3]);
           }
@@ -409,12 +420,13 @@ decode_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__
         }
 #pragma unroll
         for (int w = 0; w < 2 * kV; ++w)
-          *reinterpret_cast<float4*>(&sh.o[warp][8 * n + 2 * t + r][8 * kV * g + 4 * w]) =
+          *reinterpret_cast<float4*>(&rows.o[warp][8 * n + 2 * t + r][8 * kV * g + 4 * w]) =
               make_float4(o[n][2 * w][r], o[n][2 * w][2 + r], o[n][2 * w + 1][r], o[n][2 * w + 1][2 + r]);
       }
     }
     __syncthreads();
-    fold_warps<D, NT>(p, sp, it, sh, p.v_head_scales ? __ldg(p.v_head_scales + it.kvh) : p.v_scale);
+    fold_warps<D, NT>(p, sp, it, sh, rows, p.v_head_scales ? __ldg(p.v_head_scales + it.kvh) : p.v_scale);
+    __syncthreads();  // (the rings are free again)
     if (it.begins() && !it.ends()) {
       tail.row0 = it.q.e.q0;
       tail.nodes = 1;
@@ -433,7 +445,8 @@ namespace {
 template <int D, int NT, int kShift>
 cudaError_t launch_shift(const TreeParams& p, const TreeSplit& sp, cudaStream_t stream) {
   constexpr size_t kSmem = decode_e2m1::smem_bytes<D, NT>();
-  static_assert((NT == 1 ? 3 : 2) * (kSmem + 1024) <= 228 * 1024, "shared memory");
+  static_assert(decode_e2m1::blocks_per_sm(NT) * (kSmem + sizeof(decode_few::Shared<D, NT>) + 1024) <= 228 * 1024,
+                "shared memory");
   constexpr int kDevices = 64;
   auto kern = decode_e2m1::decode_e2m1_kernel<D, NT, kShift>;
   static std::once_flag once[kDevices];
@@ -474,10 +487,11 @@ cudaError_t launch_decode_e2m1_tpl(const TreeParams& p, const TreeSplit& sp, cud
 // Blocks of 2 and 4 tokens do not hold eight positions in a row.
 bool decode_e2m1_supported(const TreeParams& p) {
   if (p.q_dtype != kBF16 || p.kv_dtype != kE2M1 || p.query_start_loc || p.group > 16 || p.block_size < 8) return false;
+  if ((p.cs_block | p.ts_block) >> 32 || p.num_blocks > 0x7fffffff) return false;  // (multiplied in 32 bits)
   return (reinterpret_cast<uintptr_t>(p.query) & 15) == 0 && (p.q_stride_t & 7) == 0 && (p.q_stride_h & 7) == 0;
 }
 
-int decode_e2m1_blocks_per_sm(int group) { return group <= 8 ? 3 : 2; }
+int decode_e2m1_blocks_per_sm(int group) { return decode_e2m1::blocks_per_sm(group <= 8 ? 1 : 2); }
 
 cudaError_t launch_decode_e2m1(const TreeParams& p, TreeSplit sp, cudaStream_t stream) {
   sp.item_nodes = sp.tq = 1;

@@ -54,14 +54,18 @@ struct Shared {
   tree::Range range;
   longlong2 warp_sum[kWarps];
   float m[kWarps][8 * NT], l[kWarps][8 * NT];
-  alignas(16) float o[kWarps][8 * NT][D + 4];
+};
+// The warps' O, row by row, at an item's end.
+template <int D, int NT>
+struct alignas(16) Rows {
+  float o[kWarps][8 * NT][D + 4];
 };
 
-// The warps' results in `sh` together: row r of the item to the output, or to its part.  `factor`:
+// The warps' results in `sh` and `rows` together: row r of the item to the output, or to its part.  `factor`:
 // the cache's on the values.
 template <int D, int NT>
 __device__ __forceinline__ void fold_warps(const TreeParams& p, const TreeSplit& sp, const tree::Walk& it,
-                                           const Shared<D, NT>& sh, float factor) {
+                                           const Shared<D, NT>& sh, const Rows<D, NT>& rows, float factor) {
   const int tid = threadIdx.x;
   constexpr int kPer = kThreads / (8 * NT);  // threads of a row
   const int r = tid / kPer, c0 = tid % kPer;
@@ -87,7 +91,7 @@ __device__ __forceinline__ void fold_warps(const TreeParams& p, const TreeSplit&
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float4 x = *reinterpret_cast<const float4*>(&sh.o[w][r][c]);
+        const float4 x = *reinterpret_cast<const float4*>(&rows.o[w][r][c]);
         y = make_float4(y.x + x.x * f[w], y.y + x.y * f[w], y.z + x.z * f[w], y.w + x.w * f[w]);
       }
       y = make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv);

@@ -41,6 +41,7 @@ decode_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
   constexpr int kW = D / 32;    // words of a V row that a lane holds
   constexpr int kRows = 8 * NT;
   __shared__ Shared<D, NT> sh;
+  __shared__ Rows<D, NT> rows;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing of the caller's is read before
   asm volatile("griddepcontrol.launch_dependents;");
@@ -288,12 +289,12 @@ decode_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
         }
 #pragma unroll
         for (int w = 0; w < kW; ++w)
-          *reinterpret_cast<float4*>(&sh.o[warp][8 * n + 2 * t + r][4 * kW * g + 4 * w]) =
+          *reinterpret_cast<float4*>(&rows.o[warp][8 * n + 2 * t + r][4 * kW * g + 4 * w]) =
               make_float4(o[n][2 * w][r], o[n][2 * w][2 + r], o[n][2 * w + 1][r], o[n][2 * w + 1][2 + r]);
       }
     }
     __syncthreads();
-    fold_warps<D, NT>(p, sp, it, sh, 1.f);
+    fold_warps<D, NT>(p, sp, it, sh, rows, 1.f);
     if (it.begins() && !it.ends()) {
       tail.row0 = it.q.e.q0;
       tail.nodes = 1;
