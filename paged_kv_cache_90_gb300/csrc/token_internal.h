@@ -98,12 +98,14 @@ bool decode_i8_supported(const TreeParams& p);  // one row a sequence, few heads
 int decode_i8_blocks_per_sm(int group);
 bool decode_e2m1_supported(const TreeParams& p);  // the same over a 4-bit cache (decode_e2m1.cu)
 int decode_e2m1_blocks_per_sm(int group);
+bool tree_e2m1_supported(const TreeParams& p);    // 4-bit caches (tree_e2m1.cu)
 int tree_part_rows(int64_t num_tokens, int group, bool decode, bool one_tile);
 size_t tree_workspace(int grid, int rows, int head_dim);
 cudaError_t launch_tree_tensor(const TreeParams& p, int grid, int rows, void* ws, cudaStream_t stream);
 cudaError_t launch_tree_i8(const TreeParams& p, TreeSplit sp, cudaStream_t stream);
 cudaError_t launch_decode_i8(const TreeParams& p, TreeSplit sp, cudaStream_t stream);
 cudaError_t launch_decode_e2m1(const TreeParams& p, TreeSplit sp, cudaStream_t stream);
+cudaError_t launch_tree_e2m1(const TreeParams& p, TreeSplit sp, cudaStream_t stream);
 cudaError_t launch_tree_merge(const TreeParams& p, const TreeSplit& sp, cudaStream_t stream);
 
 }  // namespace pkv

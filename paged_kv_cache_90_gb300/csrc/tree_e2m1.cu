@@ -1,0 +1,802 @@
+// tree_e2m1.cu — attention of drafted trees (and decode of more than 16 heads a KV head, or over
+// blocks of 2 and 4 tokens) over a 4-bit cache on the fifth-generation tensor cores.
+//
+// A row tile is 128 MMA rows: a KV head's g query heads times up to TQ = 128 / g drafted nodes; an
+// item is (sequence, KV head, one or two row tiles) and its work is its key tiles of 128 positions,
+// cut into equal ranges as in tree_split.cuh.  A step is one (key tile, row tile):
+//   S = Q K^T          M 128, N 128, K = D: both f16 in shared memory (128-byte swizzle), S in one
+//                      of two tensor-memory buffers, by the step's parity
+//   P = 2^(S c - m)    written back over S as f16 pairs by a softmax warpgroup, a row per thread
+//   O += P V           M 128, N = D, K = 128 keys: P from tensor memory, V from shared memory
+// The steps of an item go to the two softmax warpgroups in turn, each with a reference m, a sum and
+// an O of its own: two row tiles, one each; or the even and the odd key tiles of one, whose two
+// results are folded when the item ends (each warpgroup then writes half of the columns).  So an
+// item's softmax runs in both at once, whatever its rows.
+//
+// K and V are widened by a warpgroup each: a warp brings 32 positions of a tile (asynchronous
+// copies, one to four tiles ahead, as shared memory allows), and code times group scale is an f16
+// number exactly (e2m1_codes.cuh).  A query row is scaled by the power of two that brings its
+// largest element to 2^14, so its bf16 values are exact down to 2^-29 of that.  A weight is rounded
+// to f16, half a step, 2^-11, down to 2^-21 of the row's largest, 2^-32 of that below.  Scores,
+// maximum, sum and output are binary32.
+//
+// Nothing that a row does not see reaches it: hidden scores become -infinity, V rows outside the
+// context are widened as zeros, and so are groups of drafted nodes whose scale is a NaN: the rows
+// that see such a node get the NaN back with their output.
+//
+// Warps: 1 issues the MMAs; 0, 2 and 3 convert the queries; 4-7 and 8-11 are the softmax
+// warpgroups; 12-15 widen K, 16-19 V.  Every wait is bounded; when one runs out the block sets an
+// error bit and a flag that makes every role stop, lets its copies and MMAs land and frees the
+// tensor memory.
+#include <algorithm>
+#include <mutex>
+
+#include "e2m1_codes.cuh"
+#include "i8_codes.cuh"
+#include "tcgen05.cuh"
+#include "tree_split.cuh"
+#include "umma.cuh"
+
+namespace pkv {
+namespace tree_e2m1 {
+
+using namespace tree;
+
+constexpr int kThreads = 640;
+// registers of a thread, by warpgroup: launched with 96 each (5 x 96 = 480), then split anew
+constexpr int kRegsControl = 56, kRegsSoftmax = 136, kRegsWiden = 72;
+static_assert(kRegsControl + 2 * kRegsSoftmax + 2 * kRegsWiden <= 5 * 96, "registers");
+constexpr uint32_t kTmemCols = 512;
+// A row's weights are 2^(z - m + kTop): at most 2^15 with a reference that lags by 2^kGap.
+constexpr float kTop = 7.f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kHalves = D / 64;             // 64-column halves of an operand (128-byte rows)
+  static constexpr uint32_t kHalfBytes = kBM * 128;  // 16 KB
+  static constexpr uint32_t kOpBytes = kHalves * kHalfBytes;
+  static constexpr int kRow = D / 2, kGroups = D / 16;        // bytes and scales of a cache row
+  static constexpr uint32_t kStage = 32 * (kRow + kGroups);   // a warp's 32 positions
+  // from the 1024-aligned base: one or two query tiles | two K tiles | two V tiles | the stages of
+  // the eight widening warps | state
+  __host__ __device__ static constexpr int stages(int nq) { return D == 128 ? (nq == 1 ? 3 : 1) : 4; }
+  static constexpr uint32_t kState = D == 128 ? 214 * 1024 : 2 * kOpBytes + 4 * kOpBytes + 8 * 4 * kStage;
+  static constexpr uint32_t kStateBytes = 11 * 1024;
+  static constexpr size_t kSmem = kState + kStateBytes + 1024;  // (+ alignment)
+  // tensor memory: S of even and odd steps (128 columns each), then O of the two warpgroups
+  static constexpr uint32_t kS = 0, kO = 2 * kBN;
+};
+
+// Barriers.  A wait names a phase by its parity, so its barrier may be at most one phase away:
+// those that a softmax warpgroup waits for count its own steps, two barriers by their parity.
+enum Bar { kQFull = 0, kQEmpty = 2, kKFull = 4, kKEmpty = 6, kVFull = 8, kVEmpty = 10, kSFull = 12, kPFull = 16,
+           kODone = 18, kOFree = 22, kStat = 23, kDrain = 25, kNumBars = 26 };
+
+constexpr int kQueryWarps = 3;
+constexpr int kQueryTiles = 8;  // row tiles whose score factors are kept: the converting warps are up to
+                                // two of them ahead of the MMAs, and those two steps of the softmax
+constexpr int kBadItems = 8;    // items whose bad rows are kept
+
+struct State {
+  uint64_t bars[kNumBars];
+  volatile int abort;
+  uint32_t tmem;
+  Range range;
+  longlong2 warp_sum[kThreads / 32];
+  float qf[kQueryTiles][kBM];     // a row's score factor
+  float2 stat[2][2][kBM];         // a warpgroup's maximum and sum of a row at an item's end
+  // drafted positions with a NaN scale in V, 8 to a byte from the first tile that holds drafted
+  // nodes on (1024 nodes touch at most 9 tiles)
+  unsigned char bad[kBadItems][144];
+  // What a widening warp of V has to know of a tile, by the tile's number (mod 8: its walk is up to
+  // five tiles ahead): its first position, the context's end, its window's start and its drafted
+  // nodes' (-1: all of the tile is seen by every row), and where the bytes of its bad rows go.
+  struct Tile {
+    int pos, L, lo, P;
+    unsigned char* bad;  // or null
+  } tile[4][8];
+};
+
+__device__ __forceinline__ bool wait(State* st, int bar, uint32_t parity) {
+  return tree::wait(&st->bars[bar], parity, &st->abort);
+}
+__device__ __forceinline__ bool wait_warp(State* st, int bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait(st, bar, parity));
+}
+__device__ __forceinline__ bool ready(uint64_t* bar, uint32_t parity) {  // one answer for a warp
+  return __all_sync(0xffffffffu, test_wait(bar, parity));
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const unsigned char* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const unsigned char* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void end_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void wait_copies(int pending) {  // (at most: 0, 2 or 3)
+  if (pending == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
+  else if (pending == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void less_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// f16 x f16 -> f32, M x N, A and B K-major (0) or MN-major (1)
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
+  return (1u << 4) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
+// The positions pos .. pos + 127 of a tile that a row sees, 64 to a word.
+__device__ __forceinline__ void tile_bits(const Extent& e, int pos, const int64_t* mask, uint64_t word0, uint64_t (&k)[2]) {
+  auto ones = [](int n) -> uint64_t { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; };
+#pragma unroll 1
+  for (int w = 0; w < 2; ++w) {
+    const int p0 = pos + 64 * w;
+    uint64_t b = ones(e.P - p0) & ~ones(e.lo - p0);  // (before the nodes; with no mask P is the end)
+    if (mask) {
+      // bit i is node c + i
+      const int c = p0 - e.P;
+      if (c < e.n && c > -64) {
+        uint64_t m;
+        if (c < 0) {
+          m = word0 << -c;
+        } else {
+          const int i = c >> 6, o = c & 63;
+          m = (i == 0 ? word0 : uint64_t(__ldg(mask + i))) >> o;
+          if (o && 64 * (i + 1) < e.n) m |= uint64_t(__ldg(mask + i + 1)) << (64 - o);
+        }
+        b |= m & ones(e.L - p0) & ~ones(e.P - p0);
+      }
+    }
+    k[w] = b;
+  }
+}
+
+// Largest of a row's 32 scores at tensor-memory column `ts`; with kCut those not kept become
+// -infinity there.
+template <bool kCut>
+__device__ __forceinline__ float row_max(uint32_t ts, uint32_t keep) {
+  uint32_t w[32];
+  tc::ld32(ts, w);
+  tc::wait_ld();
+  if (kCut) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) w[i] = keep >> i & 1u ? w[i] : 0xff800000u;
+    tc::st32(ts, w);
+  }
+  float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < 32; ++i) t[i & 3] = fmaxf(t[i & 3], __uint_as_float(w[i]));
+  return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+}
+
+// Weights 2^(score * sl - mu) of a row's 32 scores at column `ts`, written as f16 pairs to column
+// `tp` (whose scores have been read); returns their sum.
+__device__ __forceinline__ float weights(uint32_t ts, uint32_t tp, float sl, float mu) {
+  uint32_t w[32], pk[16];
+  tc::ld32(ts, w);
+  tc::wait_ld();
+  float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float a = fast_exp2(fmaf(__uint_as_float(w[2 * i]), sl, -mu));
+    const float b = fast_exp2(fmaf(__uint_as_float(w[2 * i + 1]), sl, -mu));
+    ps[i & 3] += a + b;
+    const __half2 pr = __floats2half2_rn(a, b);
+    pk[i] = *reinterpret_cast<const uint32_t*>(&pr);
+  }
+  tc::st16(tp, pk);
+  return (ps[0] + ps[1]) + (ps[2] + ps[3]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ TreeSplit sp) {
+  using C = Cfg<D>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  State* st = reinterpret_cast<State*>(smem + C::kState);
+  // (the warp's number from one lane: the compiler then knows that it is the same in all)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  const int g = p.group, TQ = sp.tq;
+  const uint32_t sbase = smem_addr(smem);
+
+  if (tid == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      // one arrival a warp where warps arrive
+      const bool warps4 = (i >= kKFull && i < kKFull + 2) || (i >= kVFull && i < kVFull + 2) ||
+                          (i >= kPFull && i < kPFull + 2) || (i >= kStat && i < kStat + 2);
+      const bool queries = i >= kQFull && i < kQFull + 2;
+      mbar_init(&st->bars[i], queries ? kQueryWarps : warps4 ? 4 : i == kOFree ? 8 : 1);
+    }
+    st->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) tc::alloc(&st->tmem, kTmemCols);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing of the caller's is read before
+  asm volatile("griddepcontrol.launch_dependents;");
+  // (nq: query tiles in shared memory, two where some sequence of the batch has a second row tile)
+  const int nq = find_range<kThreads>(p, sp, &st->range, st->warp_sum, sp.tq) ? 2 : 1;
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = st->tmem;
+  const Range* rg = &st->range;
+  Walk it;
+  it.start(p, sp, rg);
+  const uint32_t oq = 0, okey = nq * C::kOpBytes, ov = okey + 2 * C::kOpBytes, os = ov + 2 * C::kOpBytes;  // the places
+
+  if (warp == 1) {
+    less_registers<kRegsControl>();
+    // ---- MMAs (a warp, see umma.cuh): S runs up to two steps ahead of P V; whichever can go next goes ----
+    constexpr uint32_t idS = idesc_f16(kBM, kBN, 0, 0), idO = idesc_f16(kBM, D, 0, 1);
+    constexpr uint64_t kOp = C::kOpBytes >> 4;  // (descriptors hold addresses / 16)
+    const uint64_t qdesc = tc::desc_sw128(sbase + oq, 16, 1024), kdesc = tc::desc_sw128(sbase + okey, 16, 1024);
+    const uint64_t vdesc = tc::desc_sw128(sbase + ov, C::kHalfBytes, 1024);
+    // a step between its S and its P V: what the P V needs to know
+    struct Pending {
+      bool slot, odd, x, x_phase, first, last_row_tile, wait_o, o_phase, v, v_phase;
+    };
+    Pending pend[2];      // [step & 1] (constant indices below: registers)
+    int xs = 0, xp = 0;   // next step of either kind
+    int j = it.j0, qt = 0, i = 0, item = 0, qc = 0, tiles = 0, steps0 = 0, steps1 = 0;  // (i: of the item's steps)
+    uint32_t idle = 0;
+    bool ok = true;
+    while (it.valid() || xp < xs) {
+      bool went = false;
+      if (it.valid() && xs <= xp + 1 && ready(&st->bars[kKFull + (tiles & 1)], uint32_t(tiles >> 1) & 1u)) {
+        const int slot = i & 1, n = slot ? steps1 : steps0, q = qc + qt, qs = q & (nq - 1);
+        if (j > it.j0 || ready(&st->bars[kQFull + qs], uint32_t(nq == 2 ? q >> 1 : q) & 1u)) {
+          tc::fence_after();
+          const uint64_t qd = qdesc + qs * kOp, kd = kdesc + (tiles & 1) * kOp;
+          const uint32_t ts = tmem + C::kS + (xs & 1) * kBN;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = (kk >> 2) * (C::kHalfBytes >> 4) + (kk & 3) * 2;
+            umma::mma_ss(ts, qd + off, kd + off, idS, kk > 0 ? 1u : 0u);
+          }
+          umma::commit(&st->bars[kSFull + 2 * slot + (n & 1)]);
+          const bool last_row_tile = qt == it.nt - 1;
+          if (last_row_tile) umma::commit(&st->bars[kKEmpty + (tiles & 1)]);
+          if (j == it.j1 - 1) umma::commit(&st->bars[kQEmpty + qs]);
+          const Pending pd = {slot != 0, (n & 1) != 0, (xs & 1) != 0, ((xs >> 1) & 1) != 0, i < 2, last_row_tile,
+                              i < 2 && item > 0, ((item - 1) & 1) != 0, (tiles & 1) != 0, ((tiles >> 1) & 1) != 0};
+          if (xs & 1) pend[1] = pd; else pend[0] = pd;
+          ++xs;
+          ++i;
+          if (slot) ++steps1; else ++steps0;
+          if (!last_row_tile) {
+            ++qt;
+          } else {
+            qt = 0;
+            ++tiles;
+            if (++j == it.j1) {
+              qc += it.nt;
+              ++item;
+              i = 0;
+              it.next(p, sp, rg);
+              j = it.j0;
+            }
+          }
+          went = true;
+        }
+      }
+      if (xp < xs) {
+        const Pending pd = (xp & 1) ? pend[1] : pend[0];
+        if (ready(&st->bars[kPFull + pd.x], pd.x_phase) && ready(&st->bars[kVFull + pd.v], pd.v_phase) &&
+            (!pd.wait_o || ready(&st->bars[kOFree], pd.o_phase))) {
+          tc::fence_after();
+          const uint64_t vd = vdesc + pd.v * kOp;
+          const uint32_t ts = tmem + C::kS + pd.x * kBN, to = tmem + C::kO + pd.slot * D;
+#pragma unroll
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            umma::mma_ts(to, ts + 8 * kk, vd + kk * (16 * 128 >> 4), idO, (!pd.first || kk > 0) ? 1u : 0u);
+          umma::commit(&st->bars[kODone + 2 * pd.slot + pd.odd]);
+          if (pd.last_row_tile) umma::commit(&st->bars[kVEmpty + pd.v]);
+          ++xp;
+          went = true;
+        }
+      }
+      if (went) {
+        idle = 0;
+      } else {
+        __nanosleep(20);  // (a spinning thread takes issue slots from the softmax beside it)
+        if ((++idle & 255u) == 0 && (st->abort || idle > kWaitPolls)) {
+          ok = false;
+          break;
+        }
+      }
+    }
+    // every MMA issued has completed before the tensor memory is freed
+    umma::commit(&st->bars[kDrain]);
+    (void)mbar_wait_bounded(&st->bars[kDrain], 0);
+    if (!ok) {
+      st->abort = 1;
+      if (lane == 0) raise_device_error(p.err, kErrTimeout);
+    }
+  } else if (warp < 4) {
+    less_registers<kRegsControl>();
+    // ---- queries: the row tiles of each item, converted to f16, every row scaled by a power of two
+    // of its own; and what the fold needs of an item that goes on in the next block's range ---------
+    constexpr int kLanes = D / 8, kPer = 32 / kLanes, kBatch = 4;  // lanes of a row, rows of a pass, passes
+    const int w = warp == 0 ? 0 : warp - 1, sub = lane / kLanes, col = (lane % kLanes) * 8;
+    int q = 0;
+    bool ok = true;
+    int64_t at = rg->from;
+    TreeSplit::Tail tail = {0, 0, 0, 0};
+    for (; ok && it.valid(); it.next(p, sp, rg)) {
+      float f = p.qk_scale_log2 * (p.k_head_scales ? __ldg(p.k_head_scales + it.kvh) : 1.f);
+      for (int qt = 0; ok && qt < it.nt; ++qt, ++q) {
+        const int qs = q & (nq - 1), use = nq == 2 ? q >> 1 : q;
+        const int node0 = (2 * it.pair + qt) * TQ, rows = min(TQ, it.q.e.n - node0) * g;
+        if (use > 0 && !(ok = wait_warp(st, kQEmpty + qs, uint32_t(use - 1) & 1u))) break;
+        unsigned char* to = smem + oq + qs * C::kOpBytes;
+        for (int r0 = w * kBatch * kPer; r0 < rows; r0 += kQueryWarps * kBatch * kPer) {
+          uint4 x[kBatch];
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) {
+            const int r = r0 + u * kPer + sub;
+            x[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows) {
+              const int node = r / g, h = r - node * g;
+              x[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.query) +
+                                                     int64_t(it.q.e.q0 + node0 + node) * p.q_stride_t +
+                                                     int64_t(it.kvh * g + h) * p.q_stride_h + col);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) {
+            const int r = r0 + u * kPer + sub;
+            float y[8], top = 0.f;
+            Chunk<BF16>::expand(x[u], y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(y[e]));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int sh = i8::query_shift(top);
+            const float s = copysignf(i8::power(sh), f);  // (the factor is positive: a row's maximum is that of its sums)
+            if (r < rows) {
+              uint32_t h[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __half2 v = __floats2half2_rn(y[2 * e] * s, y[2 * e + 1] * s);
+                h[e] = *reinterpret_cast<const uint32_t*>(&v);
+              }
+              *reinterpret_cast<uint4*>(to + (col >> 6) * C::kHalfBytes + r * 128 + (((col >> 3) & 7) ^ (r & 7)) * 16) =
+                  make_uint4(h[0], h[1], h[2], h[3]);
+              // (never 0, with which a hidden score of -infinity would be NaN)
+              if (col == 0) st->qf[q % kQueryTiles][r] = fabsf(f) * i8::power(-sh) < 0x1p-149f ? 0x1p-149f : fabsf(f) * i8::power(-sh);
+            }
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st->bars[kQFull + qs]);
+      }
+      if (it.begins() && !it.ends()) {
+        const int node0 = 2 * it.pair * TQ;
+        tail.row0 = it.q.e.q0 + node0;
+        tail.nodes = min(2 * TQ, it.q.e.n - node0);
+        tail.kvh = it.kvh;
+        tail.last = int((at - it.u0 + it.q.tiles + rg->cost - 1) / rg->share);
+      }
+      at += it.u1 - it.u0;
+    }
+    if (warp == 0 && lane == 0) sp.tails[blockIdx.x] = tail;
+    if (!ok && lane == 0) {
+      st->abort = 1;
+      raise_device_error(p.err, kErrTimeout);
+    }
+  } else if (warp >= 12) {
+    less_registers<kRegsWiden>();
+    // ---- widening: K by one warpgroup, V by the other; a warp has 32 positions of every tile --------
+    const bool isv = warp >= 16;
+    const int w4 = warp & 3, gr = lane >> 2, t = lane & 3;  // (D = 128: a lane has 16 bytes of a row)
+    const int nst = C::stages(nq), bs_mask = p.block_size - 1;
+    const unsigned char* cache = static_cast<const unsigned char*>(isv ? p.value_cache : p.key_cache);
+    const unsigned char* scales = isv ? p.v_group_scales : p.k_group_scales;
+    const uint32_t stage0 = sbase + os + (warp - 12) * nst * C::kStage;
+    unsigned char* const tiles = smem + (isv ? ov : okey);
+    constexpr int kLanes = C::kRow / 16, kRows = 32 / kLanes;  // lanes of a row, rows of a copy
+    const int crow = lane / kLanes, cbyte = lane % kLanes * 16;
+    // the walk is that of the table's entries, a tile ahead of the copies
+    int j = it.valid() ? it.j0 : 0, item = 0, next_kvh = 0, found = 0, copied = 0;  // (tiles looked up and copied)
+    uint32_t e_next = 0;
+    auto lookup = [&]() {
+      if (!it.valid()) return;
+      const int pos0 = it.q.base + j * kBN + 32 * w4, pos = pos0 + lane;
+      e_next = 0;
+      next_kvh = it.kvh;
+      if (pos < it.q.e.L)  // (positions behind the context are read from block 0, whose numbers have no part)
+        e_next = uint32_t(__ldg(p.block_tables + int64_t(it.s) * p.bt_stride + (pos >> sp.bs_shift)));
+      if (isv && lane == 0) {
+        const int jt = (it.q.e.P - it.q.base) / kBN;  // first tile with drafted nodes
+        State::Tile& x = st->tile[w4][found & 7];
+        x.pos = pos0;
+        x.L = it.q.e.L;
+        x.lo = it.q.e.lo;
+        x.P = it.cut(j) ? it.q.e.P : -1;
+        x.bad = j >= jt ? st->bad[item % kBadItems] + 16 * (j - jt) + 4 * w4 : nullptr;
+      }
+      ++found;
+      if (++j == it.j1) {
+        it.next(p, sp, rg);
+        ++item;
+        j = it.j0;
+      }
+    };
+    auto copy = [&](uint32_t to) {
+      if (copied < found) {
+        ++copied;
+        uint32_t e = e_next;
+        const int64_t c_head = int64_t(next_kvh) * p.cs_head, s_head = int64_t(next_kvh) * p.ts_head;
+        if (int64_t(e) >= p.num_blocks) {  // (negative ones are large)
+          raise_device_error(p.err, kErrTableEntry);
+          e = 0;
+        }
+        lookup();
+        // (a tile's first position is a block's first)
+#pragma unroll
+        for (int c = 0; c < 32; c += kRows) {
+          const int row = c + crow;
+          copy16(to + row * C::kRow + cbyte, cache + uint64_t(__shfl_sync(0xffffffffu, e, row)) * p.cs_block +
+                                                 c_head + (row & bs_mask) * C::kRow + cbyte);
+        }
+        constexpr int kBytes = 32 * C::kGroups;
+        if (sp.vec_scales) {
+          const int byte = (lane * 16) % kBytes, row = byte / C::kGroups;
+          const unsigned char* src = scales + uint64_t(__shfl_sync(0xffffffffu, e, row)) * p.ts_block +
+                                     s_head + (row & bs_mask) * C::kGroups;
+          if (lane < kBytes / 16) copy16(to + 32 * C::kRow + byte, src);
+        } else {
+#pragma unroll
+          for (int c = 0; c < kBytes; c += 128) {
+            const int byte = c + 4 * lane, row = byte / C::kGroups;
+            copy4(to + 32 * C::kRow + byte, scales + uint64_t(__shfl_sync(0xffffffffu, e, row)) * p.ts_block +
+                                                s_head + (row & bs_mask) * C::kGroups + byte % C::kGroups);
+          }
+        }
+      }
+      end_copies();
+    };
+    lookup();
+    for (int s = 0; s < nst; ++s) copy(stage0 + s * C::kStage);
+    bool ok = true;
+    for (int n = 0, slot = 0; n < copied; ++n, slot = slot + 1 == nst ? 0 : slot + 1) {
+      wait_copies(nst - 1);
+      __syncwarp();
+      // a row's codes of D / 4 columns (one or two groups of 16) and their scales, four or two rows
+      constexpr int kW = D / 32;              // words of a lane
+      constexpr int kN = 32 / 8;              // rows of a lane
+      uint32_t x[kN][kW], sc[kN];
+      const uint32_t from = stage0 + slot * C::kStage;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const uint32_t a = from + (8 * i + gr) * C::kRow + 4 * kW * t, s = from + 32 * C::kRow + (8 * i + gr) * C::kGroups;
+        if constexpr (D == 128) {
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[i][0]), "=r"(x[i][1]), "=r"(x[i][2]), "=r"(x[i][3]) : "r"(a));
+          asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sc[i]) : "r"(s + 2 * t));
+        } else {
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[i][0]), "=r"(x[i][1]) : "r"(a));
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc[i]) : "r"(s + t));
+        }
+      }
+      __syncwarp();  // (every lane has read the stage)
+      copy(from);
+      const State::Tile& tile = st->tile[w4][n & 7];
+      if (isv && tile.P >= 0) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const int pos = tile.pos + 8 * i + gr;
+          bool bad = false;
+          if (pos >= tile.L || pos < tile.lo) {
+            sc[i] = 0;
+          } else if (pos >= tile.P) {
+            if ((sc[i] & 0x7fu) == 0x7fu) { sc[i] &= 0xff00u; bad = true; }
+            if ((sc[i] & 0x7f00u) == 0x7f00u) { sc[i] &= 0xffu; bad = true; }
+          }
+          uint32_t m = __ballot_sync(0xffffffffu, bad), byte = 0;
+          if (m) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) byte |= (m >> (4 * k) & 15u) ? 1u << k : 0u;
+          }
+          if (lane == 0 && tile.bad) tile.bad[i] = static_cast<unsigned char>(byte);
+        }
+      }
+      const int buf = n & 1;
+      if (n > 1 && !(ok = wait_warp(st, (isv ? kVEmpty : kKEmpty) + buf, uint32_t((n >> 1) - 1) & 1u))) break;
+      // The lanes of a row's second half write their cells in another order, so that eight lanes
+      // never meet a bank twice.
+      const bool swap = D == 128 && t >= 2;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const uint32_t two = e2m1::scales2(sc[i]);
+        const __half2 gs = *reinterpret_cast<const __half2*>(&two);
+        const int row = 32 * w4 + 8 * i + gr;
+        unsigned char* to = tiles + buf * C::kOpBytes + (D == 128 ? (t >> 1) * C::kHalfBytes : 0) + row * 128;
+        const int cell0 = D == 128 ? 4 * (t & 1) : 2 * t;
+#pragma unroll
+        for (int c = 0; c < kW; ++c) {
+          const int k = swap ? c ^ 2 : c;  // the word
+          uint32_t word = x[i][c];
+          if (D == 128) word = swap ? x[i][(c ^ 2) % kW] : word;
+          // (a word is half a group: of the lane's first, or, from word 2 on, its second)
+          const __half2 s = D == 128 ? (((c < 2) != swap) ? __low2half2(gs) : __high2half2(gs)) : __low2half2(gs);
+          uint32_t h[4];
+          e2m1::widen8(word, h);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[u]), s);
+            h[u] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          *reinterpret_cast<uint4*>(to + (((cell0 + k) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&st->bars[(isv ? kVFull : kKFull) + buf]);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // the copies in flight land before the block may exit
+    if (!ok && lane == 0) {
+      st->abort = 1;
+      raise_device_error(p.err, kErrTimeout);
+    }
+  } else {
+    more_registers<kRegsSoftmax>();
+    // ---- softmax warpgroup `wg`: row r of its row tiles, r = tensor-memory lane ---------------------
+    const int wg = (warp >> 2) - 1, q = warp & 3;
+    const int r = 32 * q + lane, r_node = r / g, r_head = r - r_node * g;
+    const uint32_t lane_off = uint32_t(32 * q) << 16;
+    const uint32_t tO = tmem + C::kO + wg * D + lane_off;
+    int x0 = 0, qc = 0, item = 0, steps = 0, folds = 0;  // `steps`: of this warpgroup so far; `folds`: items of one row tile
+    bool ok = true;
+    for (; ok && it.valid(); it.next(p, sp, rg), ++item) {
+      const Extent& e = it.q.e;
+      const int total = (it.j1 - it.j0) * it.nt, qt = it.nt == 2 ? wg : 0;
+      const int node = (2 * it.pair + qt) * TQ + r_node;
+      const bool row_ok = r < TQ * g && node < e.n;
+      const bool warp_ok = __any_sync(0xffffffffu, row_ok);
+      const int64_t trow = int64_t(e.q0) + node;
+      const int64_t* mask = p.tree_mask ? p.tree_mask + (row_ok ? trow : int64_t(e.q0)) * p.mask_stride : nullptr;  // (idle rows: any)
+      const uint64_t word0 = mask ? uint64_t(__ldg(mask)) : 0;
+      float m_ref = -INFINITY, l_run = 0.f, sl = 0.f;
+      for (int i = wg; i < total; i += 2, ++steps) {
+        const int j = it.j0 + (it.nt == 2 ? i >> 1 : i), x = x0 + i;
+        const int pos = it.q.base + j * kBN;
+        const uint32_t tS = tmem + C::kS + (x & 1) * kBN + lane_off;
+        if (!(ok = wait_warp(st, kSFull + 2 * wg + (steps & 1), uint32_t(steps >> 1) & 1u))) break;
+        tc::fence_after();
+        if (warp_ok) {
+          if (i == wg) sl = st->qf[(qc + qt) % kQueryTiles][r];
+          float mx = -INFINITY;
+          if (it.cut(j)) {
+            uint64_t k[2];
+            tile_bits(e, pos, mask, word0, k);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              mx = fmaxf(mx, row_max<true>(tS + 32 * c, uint32_t(k[0])));
+              k[0] = k[0] >> 32 | k[1] << 32;
+              k[1] >>= 32;
+            }
+            tc::wait_st();
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) mx = fmaxf(mx, row_max<false>(tS + 32 * c, 0u));
+          }
+          mx *= sl;
+          const bool first = m_ref == -INFINITY;
+          const bool move = row_ok && mx != -INFINITY && (first || mx > m_ref + kGap);
+          if (__any_sync(0xffffffffu, move && !first)) {
+            // some row's O is rescaled: its product of the step before has to be in it
+            if (!(ok = wait_warp(st, kODone + 2 * wg + ((steps - 1) & 1), uint32_t((steps - 1) >> 1) & 1u))) break;
+            tc::fence_after();
+            const float alpha = move && !first ? fast_exp2(m_ref - mx) : 1.f;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t w[32];
+              tc::ld32(tO + 32 * c, w);
+              tc::wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * alpha);
+              tc::st32(tO + 32 * c, w);
+            }
+            tc::wait_st();
+            l_run *= alpha;
+          }
+          if (move) m_ref = mx;
+          const float mu = m_ref == -INFINITY ? 0.f : m_ref - kTop;
+          float sum = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) sum += weights(tS + 32 * c, tS + 16 * c, sl, mu);
+          l_run += sum;
+          tc::wait_st();
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st->bars[kPFull + (x & 1)]);
+      }
+      if (!ok) break;
+      x0 += total;
+      qc += it.nt;
+      // ---- the part's output: this warpgroup's row tile, or half the columns of both results ---------
+      const int own = (total - wg + 1) >> 1;  // steps of this warpgroup in the item
+      if (own > 0 && !(ok = wait_warp(st, kODone + 2 * wg + ((steps - 1) & 1), uint32_t((steps - 1) >> 1) & 1u))) break;
+      // (without a step of its own it might run ahead of the other one by more than a phase)
+      if (item > 0 && !(ok = wait_warp(st, kOFree, uint32_t(item - 1) & 1u))) break;
+      float f0 = 1.f, f1 = 0.f, m = m_ref, l = l_run;  // the factors on this warpgroup's O and on the other's
+      const bool two = it.nt == 1 && total > 1;        // (both have a result)
+      if (it.nt == 1) {
+        st->stat[folds & 1][wg][r] = make_float2(m_ref, l_run);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st->bars[kStat + wg]);
+        if (!(ok = wait_warp(st, kStat + (wg ^ 1), uint32_t(folds) & 1u))) break;
+        const float2 o = st->stat[folds & 1][wg ^ 1][r];
+        ++folds;
+        m = fmaxf(m_ref, o.x);
+        const float ref = m == -INFINITY ? 0.f : m;
+        // (rows whose scores are all NaN have no maximum: they count as they stand)
+        f0 = m_ref == -INFINITY ? 1.f : fast_exp2(m_ref - ref);
+        f1 = o.x == -INFINITY ? 1.f : fast_exp2(o.x - ref);
+        l = wg ? o.y * f1 + l_run * f0 : l_run * f0 + o.y * f1;
+      }
+      tc::fence_after();
+      if (warp_ok) {
+        const bool whole = it.begins() && it.ends();
+        const float fv = p.v_head_scales ? __ldg(p.v_head_scales + it.kvh) : p.v_scale;
+        const float inv = (whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f) * fv;
+        const int64_t prow = int64_t(2 * blockIdx.x + (it.begins() ? 1 : 0)) * sp.rows + qt * kBM + r;
+        if (row_ok && !whole && (it.nt == 2 || wg == 0)) sp.ml[prow] = make_float2(m, l);
+        const int jt = (e.P - it.q.base) / kBN;
+        // (the bytes of this part's tiles; the others are not this item's)
+        const unsigned char* bad = st->bad[item % kBadItems];
+        const int b0 = 16 * (max(it.j0, jt) - jt), b1 = 16 * (it.j1 - jt);
+        bool any_bad = false;
+        if (mask && row_ok)
+          for (int b = b0; b < b1; b += 4) any_bad |= *reinterpret_cast<const uint32_t*>(bad + b) != 0u;
+        const int c_first = it.nt == 2 ? 0 : wg * (D / 64), c_last = it.nt == 2 ? D / 32 : c_first + D / 64;
+        const uint32_t tA = tmem + C::kO + lane_off, tB = tA + D;  // even and odd tiles' results
+#pragma unroll 1
+        for (int c = c_first; c < c_last; ++c) {
+          uint32_t w[32];
+          if (it.nt == 2) {
+            tc::ld32(tO + 32 * c, w);
+            tc::wait_ld();
+          } else {
+            const float fa = wg ? f1 : f0, fb = wg ? f0 : f1;
+            tc::ld32(tA + 32 * c, w);
+            tc::wait_ld();
+            if (two) {
+              uint32_t y[32];
+              tc::ld32(tB + 32 * c, y);
+              tc::wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                w[k] = __float_as_uint(fmaf(__uint_as_float(y[k]), fb, __uint_as_float(w[k]) * fa));
+            } else {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * fa);
+            }
+          }
+          if (any_bad) {  // the NaN that were taken out of V, to the rows that see them
+            for (int k = 8 * b0; k < 8 * b1; ++k) {
+              const int at = it.q.base + jt * kBN + k;
+              if (!(bad[k >> 3] >> (k & 7) & 1) || !tree::sees_node(mask, at - e.P)) continue;
+              const int blk = __ldg(p.block_tables + int64_t(it.s) * p.bt_stride + (at >> sp.bs_shift));
+              if (blk < 0 || int64_t(blk) >= p.num_blocks) continue;
+              const unsigned char* s = p.v_group_scales + int64_t(blk) * p.ts_block + int64_t(it.kvh) * p.ts_head +
+                                       (at & (p.block_size - 1)) * C::kGroups + 2 * c;
+              const bool lo = (s[0] & 0x7f) == 0x7f, hi = (s[1] & 0x7f) == 0x7f;
+#pragma unroll
+              for (int u = 0; u < 32; ++u)
+                if (u < 16 ? lo : hi) w[u] = 0x7fc00000u;
+            }
+          }
+          if (!row_ok) continue;
+          if (whole) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + trow * p.out_stride_t +
+                                 int64_t(it.kvh * g + r_head) * p.out_stride_h + 32 * c;
+            uint32_t o16[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const __nv_bfloat162 pr = __floats2bfloat162_rn(__uint_as_float(w[2 * k]) * inv,
+                                                              __uint_as_float(w[2 * k + 1]) * inv);
+              o16[k] = *reinterpret_cast<const uint32_t*>(&pr);
+            }
+            if (sp.out_vec) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint2*>(out + 4 * k) = make_uint2(o16[2 * k], o16[2 * k + 1]);
+            } else {  // (rows at any address)
+              uint16_t* o = reinterpret_cast<uint16_t*>(out);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                o[2 * k] = uint16_t(o16[k]);
+                o[2 * k + 1] = uint16_t(o16[k] >> 16);
+              }
+            }
+          } else {
+            float4* o = reinterpret_cast<float4*>(sp.o + prow * D + 32 * c);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              o[k] = make_float4(__uint_as_float(w[4 * k]) * inv, __uint_as_float(w[4 * k + 1]) * inv,
+                                 __uint_as_float(w[4 * k + 2]) * inv, __uint_as_float(w[4 * k + 3]) * inv);
+          }
+        }
+      }
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&st->bars[kOFree]);
+    }
+    if (!ok && lane == 0) {
+      st->abort = 1;
+      raise_device_error(p.err, kErrTimeout);
+    }
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  if (warp == 0) tc::dealloc(tmem, kTmemCols);
+}
+
+}  // namespace tree_e2m1
+
+namespace {
+
+template <int D>
+cudaError_t launch_tree_e2m1_tpl(const TreeParams& p, const TreeSplit& sp, cudaStream_t stream) {
+  using C = tree_e2m1::Cfg<D>;
+  static_assert(sizeof(tree_e2m1::State) <= C::kStateBytes, "state");
+  static_assert(C::kSmem <= 227 * 1024, "shared memory");
+  static_assert(5 * C::kOpBytes + 8 * C::stages(1) * C::kStage <= C::kState &&
+                6 * C::kOpBytes + 8 * C::stages(2) * C::kStage <= C::kState, "operands and stages");
+  constexpr int kDevices = 64;
+  auto kern = tree_e2m1::tree_e2m1_kernel<D>;
+  static std::once_flag once[kDevices];
+  static cudaError_t set[kDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+  std::call_once(once[dev], [&] {
+    set[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
+  });
+  if (set[dev] != cudaSuccess) return set[dev];
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(sp.grid));
+  cfg.blockDim = dim3(tree_e2m1::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, p, sp);
+  note_launch();
+  if (e != cudaSuccess) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_tree_merge(p, sp, stream);
+}
+
+}  // namespace
+
+bool tree_e2m1_supported(const TreeParams& p) {
+  if (p.q_dtype != kBF16 || p.kv_dtype != kE2M1) return false;
+  if (p.group > tree::kBM) return false;
+  return (reinterpret_cast<uintptr_t>(p.query) & 15) == 0 && (p.q_stride_t & 7) == 0 && (p.q_stride_h & 7) == 0;
+}
+
+cudaError_t launch_tree_e2m1(const TreeParams& p, TreeSplit sp, cudaStream_t stream) {
+  sp.item_nodes = 2 * sp.tq;
+  // (16 bytes of scales are two or four tokens of a block)
+  sp.vec_scales = p.block_size * (p.head_dim / 16) >= 16 &&
+                  !((reinterpret_cast<uintptr_t>(p.k_group_scales) | reinterpret_cast<uintptr_t>(p.v_group_scales) |
+                     p.ts_block | p.ts_head) & 15);
+  return p.head_dim == 128 ? launch_tree_e2m1_tpl<128>(p, sp, stream) : launch_tree_e2m1_tpl<64>(p, sp, stream);
+}
+
+}  // namespace pkv

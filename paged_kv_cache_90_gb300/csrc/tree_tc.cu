@@ -754,7 +754,7 @@ cudaError_t launch_tree_merge(const TreeParams& p, const TreeSplit& sp, cudaStre
 
 // (an entry that is out of range is read as block 0: the host refuses a cache without blocks)
 bool tree_tensor_supported(const TreeParams& p) {
-  return tree_tc_supported(p) || tree_i8_supported(p) || decode_e2m1_supported(p);
+  return tree_tc_supported(p) || tree_i8_supported(p) || tree_e2m1_supported(p);
 }
 
 // Rows of a part's slot: the batch's, or at most one row tile of 128 (int8 cache) or two.
@@ -783,6 +783,7 @@ cudaError_t launch_tree_tensor(const TreeParams& p, int grid, int rows, void* ws
   sp.ml = reinterpret_cast<float2*>(sp.o + size_t(grid) * 2 * rows * p.head_dim);
   if (decode_i8_supported(p)) return launch_decode_i8(p, sp, stream);
   if (decode_e2m1_supported(p)) return launch_decode_e2m1(p, sp, stream);
+  if (p.kv_dtype == kE2M1) return launch_tree_e2m1(p, sp, stream);
   if (p.kv_dtype == kI8) return launch_tree_i8(p, sp, stream);
   return p.head_dim == 128 ? launch_tree_tc_tpl<128>(p, sp, stream) : launch_tree_tc_tpl<64>(p, sp, stream);
 }
