@@ -44,7 +44,7 @@ using namespace tree;
 
 constexpr int kThreads = 640;
 // registers of a thread, by warpgroup: launched with 96 each (5 x 96 = 480), then split anew
-constexpr int kRegsControl = 56, kRegsSoftmax = 136, kRegsWiden = 72;
+constexpr int kRegsControl = 72, kRegsSoftmax = 128, kRegsWiden = 72;
 static_assert(kRegsControl + 2 * kRegsSoftmax + 2 * kRegsWiden <= 5 * 96, "registers");
 constexpr uint32_t kTmemCols = 512;
 // A row's weights are 2^(z - m + kTop): at most 2^15 with a reference that lags by 2^kGap.
@@ -133,7 +133,7 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_m
 // The positions pos .. pos + 127 of a tile that a row sees, 64 to a word.
 __device__ __forceinline__ void tile_bits(const Extent& e, int pos, const int64_t* mask, uint64_t word0, uint64_t (&k)[2]) {
   auto ones = [](int n) -> uint64_t { return n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1; };
-#pragma unroll 1
+#pragma unroll
   for (int w = 0; w < 2; ++w) {
     const int p0 = pos + 64 * w;
     uint64_t b = ones(e.P - p0) & ~ones(e.lo - p0);  // (before the nodes; with no mask P is the end)
@@ -226,12 +226,12 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
   tc::fence_after();
   const uint32_t tmem = st->tmem;
   const Range* rg = &st->range;
-  Walk it;
-  it.start(p, sp, rg);
   const uint32_t oq = 0, okey = nq * C::kOpBytes, ov = okey + 2 * C::kOpBytes, os = ov + 2 * C::kOpBytes;  // the places
 
   if (warp == 1) {
     less_registers<kRegsControl>();
+    Walk it;
+    it.start(p, sp, rg);
     // ---- MMAs (a warp, see umma.cuh): S runs up to two steps ahead of P V; whichever can go next goes ----
     constexpr uint32_t idS = idesc_f16(kBM, kBN, 0, 0), idO = idesc_f16(kBM, D, 0, 1);
     constexpr uint64_t kOp = C::kOpBytes >> 4;  // (descriptors hold addresses / 16)
@@ -320,6 +320,8 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
     }
   } else if (warp < 4) {
     less_registers<kRegsControl>();
+    Walk it;
+    it.start(p, sp, rg);
     // ---- queries: the row tiles of each item, converted to f16, every row scaled by a power of two
     // of its own; and what the fold needs of an item that goes on in the next block's range ---------
     constexpr int kLanes = D / 8, kPer = 32 / kLanes, kBatch = 4;  // lanes of a row, rows of a pass, passes
@@ -393,6 +395,8 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
     }
   } else if (warp >= 12) {
     less_registers<kRegsWiden>();
+    Walk it;
+    it.start(p, sp, rg);
     // ---- widening: K by one warpgroup, V by the other; a warp has 32 positions of every tile --------
     const bool isv = warp >= 16;
     const int w4 = warp & 3, gr = lane >> 2, t = lane & 3;  // (D = 128: a lane has 16 bytes of a row)
@@ -547,6 +551,8 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
     }
   } else {
     more_registers<kRegsSoftmax>();
+    Walk it;
+    it.start(p, sp, rg);
     // ---- softmax warpgroup `wg`: row r of its row tiles, r = tensor-memory lane ---------------------
     const int wg = (warp >> 2) - 1, q = warp & 3;
     const int r = 32 * q + lane, r_node = r / g, r_head = r - r_node * g;
