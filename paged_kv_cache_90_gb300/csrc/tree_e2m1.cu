@@ -32,6 +32,7 @@
 #include <mutex>
 
 #include "e2m1_codes.cuh"
+#include "f32x2.cuh"
 #include "i8_codes.cuh"
 #include "tcgen05.cuh"
 #include "tree_split.cuh"
@@ -156,6 +157,12 @@ __device__ __forceinline__ void tile_bits(const Extent& e, int pos, const int64_
   }
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
 // Largest of a row's 32 scores at tensor-memory column `ts`; with kCut those not kept become
 // -infinity there.
 template <bool kCut>
@@ -168,10 +175,16 @@ __device__ __forceinline__ float row_max(uint32_t ts, uint32_t keep) {
     for (int i = 0; i < 32; ++i) w[i] = keep >> i & 1u ? w[i] : 0xff800000u;
     tc::st32(ts, w);
   }
-  float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  float t[4];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) t[i & 3] = fmaxf(t[i & 3], __uint_as_float(w[i]));
-  return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+  for (int i = 0; i < 4; ++i) t[i] = max3(__uint_as_float(w[i]), __uint_as_float(w[4 + i]), __uint_as_float(w[8 + i]));
+#pragma unroll
+  for (int i = 12; i < 28; i += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) t[k] = max3(t[k], __uint_as_float(w[i + k]), __uint_as_float(w[i + 4 + k]));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t[i] = fmaxf(t[i], __uint_as_float(w[28 + i]));
+  return max3(fmaxf(t[0], t[1]), t[2], t[3]);
 }
 
 // Weights 2^(score * sl - mu) of a row's 32 scores at column `ts`, written as f16 pairs to column
@@ -180,17 +193,19 @@ __device__ __forceinline__ float weights(uint32_t ts, uint32_t tp, float sl, flo
   uint32_t w[32], pk[16];
   tc::ld32(ts, w);
   tc::wait_ld();
-  float ps[4] = {0.f, 0.f, 0.f, 0.f};
+  const uint64_t sl2 = pack2(sl, sl), mu2 = pack2(-mu, -mu);
+  uint64_t ps[2] = {0ull, 0ull};
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const float a = fast_exp2(fmaf(__uint_as_float(w[2 * i]), sl, -mu));
-    const float b = fast_exp2(fmaf(__uint_as_float(w[2 * i + 1]), sl, -mu));
-    ps[i & 3] += a + b;
+    const float2 z = unpack2(fma2(pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), sl2, mu2));
+    const float a = fast_exp2(z.x), b = fast_exp2(z.y);
+    ps[i & 1] = add2(ps[i & 1], pack2(a, b));
     const __half2 pr = __floats2half2_rn(a, b);
     pk[i] = *reinterpret_cast<const uint32_t*>(&pr);
   }
   tc::st16(tp, pk);
-  return (ps[0] + ps[1]) + (ps[2] + ps[3]);
+  const float2 sum = unpack2(add2(ps[0], ps[1]));
+  return sum.x + sum.y;
 }
 
 template <int D>
@@ -401,12 +416,15 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
     const bool isv = warp >= 16;
     const int w4 = warp & 3, gr = lane >> 2, t = lane & 3;  // (D = 128: a lane has 16 bytes of a row)
     const int nst = C::stages(nq), bs_mask = p.block_size - 1;
+    const uint64_t block_bytes = uint32_t(p.cs_block), block_scales = uint32_t(p.ts_block);  // (32 bits: see the host's check)
     const unsigned char* cache = static_cast<const unsigned char*>(isv ? p.value_cache : p.key_cache);
     const unsigned char* scales = isv ? p.v_group_scales : p.k_group_scales;
     const uint32_t stage0 = sbase + os + (warp - 12) * nst * C::kStage;
     unsigned char* const tiles = smem + (isv ? ov : okey);
     constexpr int kLanes = C::kRow / 16, kRows = 32 / kLanes;  // lanes of a row, rows of a copy
     const int crow = lane / kLanes, cbyte = lane % kLanes * 16;
+    // (a tile's first position is a block's first)
+    const uint32_t in_block = (crow & bs_mask) * C::kRow + cbyte;
     // the walk is that of the table's entries, a tile ahead of the copies
     int j = it.valid() ? it.j0 : 0, item = 0, next_kvh = 0, found = 0, copied = 0;  // (tiles looked up and copied)
     uint32_t e_next = 0;
@@ -443,25 +461,23 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
           e = 0;
         }
         lookup();
-        // (a tile's first position is a block's first)
+        const unsigned char* src = cache + c_head + in_block;
 #pragma unroll
-        for (int c = 0; c < 32; c += kRows) {
-          const int row = c + crow;
-          copy16(to + row * C::kRow + cbyte, cache + uint64_t(__shfl_sync(0xffffffffu, e, row)) * p.cs_block +
-                                                 c_head + (row & bs_mask) * C::kRow + cbyte);
-        }
+        for (int c = 0; c < 32; c += kRows)
+          copy16(to + (c + crow) * C::kRow + cbyte,
+                 src + __shfl_sync(0xffffffffu, e, c + crow) * block_bytes + (kRows <= bs_mask ? (c & bs_mask) * C::kRow : 0));
         constexpr int kBytes = 32 * C::kGroups;
         if (sp.vec_scales) {
           const int byte = (lane * 16) % kBytes, row = byte / C::kGroups;
-          const unsigned char* src = scales + uint64_t(__shfl_sync(0xffffffffu, e, row)) * p.ts_block +
-                                     s_head + (row & bs_mask) * C::kGroups;
+          const unsigned char* src = scales + s_head + __shfl_sync(0xffffffffu, e, row) * block_scales +
+                                     (row & bs_mask) * C::kGroups;
           if (lane < kBytes / 16) copy16(to + 32 * C::kRow + byte, src);
         } else {
 #pragma unroll
           for (int c = 0; c < kBytes; c += 128) {
             const int byte = c + 4 * lane, row = byte / C::kGroups;
-            copy4(to + 32 * C::kRow + byte, scales + uint64_t(__shfl_sync(0xffffffffu, e, row)) * p.ts_block +
-                                                s_head + (row & bs_mask) * C::kGroups + byte % C::kGroups);
+            copy4(to + 32 * C::kRow + byte, scales + s_head + __shfl_sync(0xffffffffu, e, row) * block_scales +
+                                                (row & bs_mask) * C::kGroups + byte % C::kGroups);
           }
         }
       }
@@ -480,9 +496,12 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
       const uint32_t from = stage0 + slot * C::kStage;
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
+        // (the lanes of a row's second half take their words in another order, so that eight lanes never
+        // meet a bank twice when they are written)
         const uint32_t a = from + (8 * i + gr) * C::kRow + 4 * kW * t, s = from + 32 * C::kRow + (8 * i + gr) * C::kGroups;
         if constexpr (D == 128) {
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x[i][0]), "=r"(x[i][1]), "=r"(x[i][2]), "=r"(x[i][3]) : "r"(a));
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[i][0]), "=r"(x[i][1]) : "r"(a + (t & 2) * 4));
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[i][2]), "=r"(x[i][3]) : "r"(a + 8 - (t & 2) * 4));
           asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sc[i]) : "r"(s + 2 * t));
         } else {
           asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[i][0]), "=r"(x[i][1]) : "r"(a));
@@ -513,31 +532,27 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
       }
       const int buf = n & 1;
       if (n > 1 && !(ok = wait_warp(st, (isv ? kVEmpty : kKEmpty) + buf, uint32_t((n >> 1) - 1) & 1u))) break;
-      // The lanes of a row's second half write their cells in another order, so that eight lanes
-      // never meet a bank twice.
       const bool swap = D == 128 && t >= 2;
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const uint32_t two = e2m1::scales2(sc[i]);
-        const __half2 gs = *reinterpret_cast<const __half2*>(&two);
+        // (a word is half a group: two of the lane's first group, then of its second, or the other way round)
+        const uint32_t in_order = swap ? __byte_perm(two, two, 0x1032) : two;
+        const __half2 gs = *reinterpret_cast<const __half2*>(&in_order);
         const int row = 32 * w4 + 8 * i + gr;
         unsigned char* to = tiles + buf * C::kOpBytes + (D == 128 ? (t >> 1) * C::kHalfBytes : 0) + row * 128;
-        const int cell0 = D == 128 ? 4 * (t & 1) : 2 * t;
+        const int cell0 = D == 128 ? (4 * (t & 1)) ^ (t & 2) : 2 * t;  // (with c, the order in which the words come)
 #pragma unroll
         for (int c = 0; c < kW; ++c) {
-          const int k = swap ? c ^ 2 : c;  // the word
-          uint32_t word = x[i][c];
-          if (D == 128) word = swap ? x[i][(c ^ 2) % kW] : word;
-          // (a word is half a group: of the lane's first, or, from word 2 on, its second)
-          const __half2 s = D == 128 ? (((c < 2) != swap) ? __low2half2(gs) : __high2half2(gs)) : __low2half2(gs);
+          const __half2 s = c < 2 ? __low2half2(gs) : __high2half2(gs);
           uint32_t h[4];
-          e2m1::widen8(word, h);
+          e2m1::widen8(x[i][c], h);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[u]), s);
             h[u] = *reinterpret_cast<const uint32_t*>(&v);
           }
-          *reinterpret_cast<uint4*>(to + (((cell0 + k) ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(to + ((cell0 ^ c ^ (row & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
         }
       }
       fence_proxy_async_smem();
@@ -793,6 +808,7 @@ cudaError_t launch_tree_e2m1_tpl(const TreeParams& p, const TreeSplit& sp, cudaS
 bool tree_e2m1_supported(const TreeParams& p) {
   if (p.q_dtype != kBF16 || p.kv_dtype != kE2M1) return false;
   if (p.group > tree::kBM) return false;
+  if ((p.cs_block | p.ts_block) >> 32) return false;  // (multiplied in 32 bits)
   return (reinterpret_cast<uintptr_t>(p.query) & 15) == 0 && (p.q_stride_t & 7) == 0 && (p.q_stride_h & 7) == 0;
 }
 
