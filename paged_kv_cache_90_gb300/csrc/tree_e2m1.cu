@@ -89,13 +89,12 @@ struct State {
   // drafted positions with a NaN scale in V, 8 to a byte from the first tile that holds drafted
   // nodes on (1024 nodes touch at most 9 tiles)
   unsigned char bad[kBadItems][144];
-  // What a widening warp of V has to know of a tile, by the tile's number (mod 8: its walk is up to
-  // five tiles ahead): its first position, the context's end, its window's start and its drafted
-  // nodes' (-1: all of the tile is seen by every row), and where the bytes of its bad rows go.
-  struct Tile {
-    int pos, L, lo, P;
-    unsigned char* bad;  // or null
-  } tile[4][8];
+  // What a widening warp of V has to know of an item's part (mod 8: its walk is up to six tiles, so
+  // items, ahead): tiles, the first one's first position, the context's end, its window's start and
+  // its drafted nodes', and the first tile of these counted from the part's first.
+  struct Item {
+    int tiles, pos, L, lo, P, jt;
+  } item[4][8];
 };
 
 __device__ __forceinline__ bool wait(State* st, int bar, uint32_t parity) {
@@ -417,6 +416,7 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
     const int w4 = warp & 3, gr = lane >> 2, t = lane & 3;  // (D = 128: a lane has 16 bytes of a row)
     const int nst = C::stages(nq), bs_mask = p.block_size - 1;
     const uint64_t block_bytes = uint32_t(p.cs_block), block_scales = uint32_t(p.ts_block);  // (32 bits: see the host's check)
+    const uint64_t head_bytes = uint32_t(p.cs_head), head_scales = uint32_t(p.ts_head);
     const unsigned char* cache = static_cast<const unsigned char*>(isv ? p.value_cache : p.key_cache);
     const unsigned char* scales = isv ? p.v_group_scales : p.k_group_scales;
     const uint32_t stage0 = sbase + os + (warp - 12) * nst * C::kStage;
@@ -425,67 +425,73 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
     const int crow = lane / kLanes, cbyte = lane % kLanes * 16;
     // (a tile's first position is a block's first)
     const uint32_t in_block = (crow & bs_mask) * C::kRow + cbyte;
-    // the walk is that of the table's entries, a tile ahead of the copies
-    int j = it.valid() ? it.j0 : 0, item = 0, next_kvh = 0, found = 0, copied = 0;  // (tiles looked up and copied)
+    // the table's entries are looked up a tile ahead of the copies; the walk is theirs, an item ahead
+    int copied = 0, items = 0, t_left = 0, t_pos = 0, t_end = 0, next_kvh = 0;
+    const int32_t* t_entry = nullptr;
+    bool have_next = false;
     uint32_t e_next = 0;
     auto lookup = [&]() {
-      if (!it.valid()) return;
-      const int pos0 = it.q.base + j * kBN + 32 * w4, pos = pos0 + lane;
-      e_next = 0;
-      next_kvh = it.kvh;
-      if (pos < it.q.e.L)  // (positions behind the context are read from block 0, whose numbers have no part)
-        e_next = uint32_t(__ldg(p.block_tables + int64_t(it.s) * p.bt_stride + (pos >> sp.bs_shift)));
-      if (isv && lane == 0) {
-        const int jt = (it.q.e.P - it.q.base) / kBN;  // first tile with drafted nodes
-        State::Tile& x = st->tile[w4][found & 7];
-        x.pos = pos0;
-        x.L = it.q.e.L;
-        x.lo = it.q.e.lo;
-        x.P = it.cut(j) ? it.q.e.P : -1;
-        x.bad = j >= jt ? st->bad[item % kBadItems] + 16 * (j - jt) + 4 * w4 : nullptr;
-      }
-      ++found;
-      if (++j == it.j1) {
+      if (t_left == 0) {
+        have_next = it.valid();
+        if (!have_next) return;
+        t_left = it.j1 - it.j0;
+        const int pos0 = it.q.base + it.j0 * kBN + 32 * w4;
+        t_pos = pos0 + lane;
+        t_end = it.q.e.L;
+        t_entry = p.block_tables + int64_t(it.s) * p.bt_stride + (t_pos >> sp.bs_shift);
+        next_kvh = it.kvh;
+        if (isv && lane == 0)
+          st->item[w4][items & 7] = {t_left, pos0, it.q.e.L, it.q.e.lo, it.q.e.P, (it.q.e.P - it.q.base) / kBN - it.j0};
+        ++items;
         it.next(p, sp, rg);
-        ++item;
-        j = it.j0;
       }
+      // (positions behind the context are read from block 0, whose numbers have no part)
+      e_next = t_pos < t_end ? uint32_t(__ldg(t_entry)) : 0u;
+      t_pos += kBN;
+      t_entry += kBN >> sp.bs_shift;
+      --t_left;
     };
+    constexpr int kCopies = 32 / kRows, kScaleBytes = 32 * C::kGroups;
+    const int sbyte = (lane * 16) % kScaleBytes, srow = sbyte / C::kGroups;
+    const uint32_t s_in_block = (srow & bs_mask) * C::kGroups;
     auto copy = [&](uint32_t to) {
-      if (copied < found) {
+      if (have_next) {
         ++copied;
         uint32_t e = e_next;
-        const int64_t c_head = int64_t(next_kvh) * p.cs_head, s_head = int64_t(next_kvh) * p.ts_head;
-        if (int64_t(e) >= p.num_blocks) {  // (negative ones are large)
+        if (e >= uint32_t(p.num_blocks)) {  // (negative ones are large)
           raise_device_error(p.err, kErrTableEntry);
           e = 0;
         }
-        lookup();
-        const unsigned char* src = cache + c_head + in_block;
+        // (the blocks of all copies first: one shuffle after the other, not one behind each copy)
+        uint32_t blk[kCopies];
 #pragma unroll
-        for (int c = 0; c < 32; c += kRows)
-          copy16(to + (c + crow) * C::kRow + cbyte,
-                 src + __shfl_sync(0xffffffffu, e, c + crow) * block_bytes + (kRows <= bs_mask ? (c & bs_mask) * C::kRow : 0));
-        constexpr int kBytes = 32 * C::kGroups;
+        for (int c = 0; c < kCopies; ++c) blk[c] = __shfl_sync(0xffffffffu, e, c * kRows + crow);
+        const uint32_t sblk = __shfl_sync(0xffffffffu, e, srow);
+        const unsigned char* src = cache + next_kvh * head_bytes + in_block;
+        const unsigned char* ssrc = scales + next_kvh * head_scales;
+        const uint32_t dst = to + crow * C::kRow + cbyte;
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c)
+          copy16(dst + c * kRows * C::kRow, src + blk[c] * block_bytes + (kRows <= bs_mask ? (c * kRows & bs_mask) * C::kRow : 0));
         if (sp.vec_scales) {
-          const int byte = (lane * 16) % kBytes, row = byte / C::kGroups;
-          const unsigned char* src = scales + s_head + __shfl_sync(0xffffffffu, e, row) * block_scales +
-                                     (row & bs_mask) * C::kGroups;
-          if (lane < kBytes / 16) copy16(to + 32 * C::kRow + byte, src);
+          if (lane < kScaleBytes / 16) copy16(to + 32 * C::kRow + sbyte, ssrc + sblk * block_scales + s_in_block);
         } else {
 #pragma unroll
-          for (int c = 0; c < kBytes; c += 128) {
+          for (int c = 0; c < kScaleBytes; c += 128) {
             const int byte = c + 4 * lane, row = byte / C::kGroups;
-            copy4(to + 32 * C::kRow + byte, scales + s_head + __shfl_sync(0xffffffffu, e, row) * block_scales +
+            copy4(to + 32 * C::kRow + byte, ssrc + __shfl_sync(0xffffffffu, e, row) * block_scales +
                                                 (row & bs_mask) * C::kGroups + byte % C::kGroups);
           }
         }
+        lookup();
       }
       end_copies();
     };
     lookup();
     for (int s = 0; s < nst; ++s) copy(stage0 + s * C::kStage);
     bool ok = true;
+    State::Item part = {};  // the tile's, and how many of its tiles are left
+    int item = 0, k_tile = 0;
     for (int n = 0, slot = 0; n < copied; ++n, slot = slot + 1 == nst ? 0 : slot + 1) {
       wait_copies(nst - 1);
       __syncwarp();
@@ -510,25 +516,34 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
       }
       __syncwarp();  // (every lane has read the stage)
       copy(from);
-      const State::Tile& tile = st->tile[w4][n & 7];
-      if (isv && tile.P >= 0) {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const int pos = tile.pos + 8 * i + gr;
-          bool bad = false;
-          if (pos >= tile.L || pos < tile.lo) {
-            sc[i] = 0;
-          } else if (pos >= tile.P) {
-            if ((sc[i] & 0x7fu) == 0x7fu) { sc[i] &= 0xff00u; bad = true; }
-            if ((sc[i] & 0x7f00u) == 0x7f00u) { sc[i] &= 0xffu; bad = true; }
-          }
-          uint32_t m = __ballot_sync(0xffffffffu, bad), byte = 0;
-          if (m) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) byte |= (m >> (4 * k) & 15u) ? 1u << k : 0u;
-          }
-          if (lane == 0 && tile.bad) tile.bad[i] = static_cast<unsigned char>(byte);
+      if (isv) {
+        if (k_tile == part.tiles) {
+          part = st->item[w4][item & 7];
+          ++item;
+          k_tile = 0;
         }
+        if (part.pos - 32 * w4 + kBN > part.P || part.pos - 32 * w4 < part.lo) {  // (Walk::cut)
+#pragma unroll
+          for (int i = 0; i < kN; ++i) {
+            const int pos = part.pos + 8 * i + gr;
+            bool bad = false;
+            if (pos >= part.L || pos < part.lo) {
+              sc[i] = 0;
+            } else if (pos >= part.P) {
+              if ((sc[i] & 0x7fu) == 0x7fu) { sc[i] &= 0xff00u; bad = true; }
+              if ((sc[i] & 0x7f00u) == 0x7f00u) { sc[i] &= 0xffu; bad = true; }
+            }
+            uint32_t m = __ballot_sync(0xffffffffu, bad), byte = 0;
+            if (m) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) byte |= (m >> (4 * k) & 15u) ? 1u << k : 0u;
+            }
+            if (lane == 0 && k_tile >= part.jt)
+              st->bad[(item - 1) % kBadItems][16 * (k_tile - part.jt) + 4 * w4 + i] = static_cast<unsigned char>(byte);
+          }
+        }
+        part.pos += kBN;
+        ++k_tile;
       }
       const int buf = n & 1;
       if (n > 1 && !(ok = wait_warp(st, (isv ? kVEmpty : kKEmpty) + buf, uint32_t((n >> 1) - 1) & 1u))) break;
@@ -808,7 +823,7 @@ cudaError_t launch_tree_e2m1_tpl(const TreeParams& p, const TreeSplit& sp, cudaS
 bool tree_e2m1_supported(const TreeParams& p) {
   if (p.q_dtype != kBF16 || p.kv_dtype != kE2M1) return false;
   if (p.group > tree::kBM) return false;
-  if ((p.cs_block | p.ts_block) >> 32) return false;  // (multiplied in 32 bits)
+  if ((p.cs_block | p.cs_head | p.ts_block | p.ts_head) >> 32 || p.num_blocks > 0x7fffffff) return false;  // (multiplied in 32 bits)
   return (reinterpret_cast<uintptr_t>(p.query) & 15) == 0 && (p.q_stride_t & 7) == 0 && (p.q_stride_h & 7) == 0;
 }
 
