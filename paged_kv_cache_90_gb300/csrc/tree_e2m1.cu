@@ -103,9 +103,6 @@ __device__ __forceinline__ bool wait(State* st, int bar, uint32_t parity) {
 __device__ __forceinline__ bool wait_warp(State* st, int bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait(st, bar, parity));
 }
-__device__ __forceinline__ bool ready(uint64_t* bar, uint32_t parity) {  // one answer for a warp
-  return __all_sync(0xffffffffu, test_wait(bar, parity));
-}
 
 __device__ __forceinline__ void copy16(uint32_t dst, const unsigned char* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -246,85 +243,71 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
     less_registers<kRegsControl>();
     Walk it;
     it.start(p, sp, rg);
-    // ---- MMAs (a warp, see umma.cuh): S runs up to two steps ahead of P V; whichever can go next goes ----
+    // ---- MMAs (a warp, see umma.cuh): S of a step, then P V of the step before it -------------------
+    // (Counters and descriptors come from values that the compiler knows to be the warp's: a lane's
+    // own would be moved to uniform registers for every MMA.)
     constexpr uint32_t idS = idesc_f16(kBM, kBN, 0, 0), idO = idesc_f16(kBM, D, 0, 1);
-    constexpr uint64_t kOp = C::kOpBytes >> 4;  // (descriptors hold addresses / 16)
-    const uint64_t qdesc = tc::desc_sw128(sbase + oq, 16, 1024), kdesc = tc::desc_sw128(sbase + okey, 16, 1024);
-    const uint64_t vdesc = tc::desc_sw128(sbase + ov, C::kHalfBytes, 1024);
-    // a step between its S and its P V: what the P V needs to know
-    struct Pending {
-      bool slot, odd, x, x_phase, first, last_row_tile, wait_o, o_phase, v, v_phase;
+    constexpr uint64_t kOp = C::kOpBytes >> 4, kHalf = C::kHalfBytes >> 4;  // (descriptors hold addresses / 16)
+    auto one = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    const int nqs = one(nq);
+    const uint32_t base = one(int(sbase)), tm = one(int(tmem));
+    const uint64_t qdesc = tc::desc_sw128(base, 16, 1024), kdesc = tc::desc_sw128(base + nqs * C::kOpBytes, 16, 1024);
+    const uint64_t vdesc = tc::desc_sw128(base + (nqs + 2) * C::kOpBytes, C::kHalfBytes, 1024);
+    int xs = 0, tiles = 0, q = 0, item = 0, steps0 = 0, steps1 = 0;
+    // the step whose P V is next: its warpgroup, that one's step and the tile; whether it is the
+    // warpgroup's first of the item, and the last of its tile
+    int p_slot = 0, p_step = 0, p_tile = 0, p_item = 0;
+    bool p_first = false, p_last = false, p_due = false, ok = true;
+    auto products = [&]() {
+      const int x = xs - 1;
+      ok = wait_warp(st, kVFull + (p_tile & 1), uint32_t(p_tile >> 1) & 1u) &&
+           (!p_first || p_item == 0 || wait_warp(st, kOFree, uint32_t(p_item - 1) & 1u)) &&
+           wait_warp(st, kPFull + (x & 1), uint32_t(x >> 1) & 1u);
+      if (!ok) return;
+      tc::fence_after();
+      const uint64_t vd = vdesc + (p_tile & 1) * kOp;
+      const uint32_t ts = tm + C::kS + (x & 1) * kBN, to = tm + C::kO + p_slot * D;
+#pragma unroll
+      for (int kk = 0; kk < kBN / 16; ++kk)
+        umma::mma_ts(to, ts + 8 * kk, vd + kk * (16 * 128 >> 4), idO, (!p_first || kk > 0) ? 1u : 0u);
+      umma::commit(&st->bars[kODone + 2 * p_slot + (p_step & 1)]);
+      if (p_last) umma::commit(&st->bars[kVEmpty + (p_tile & 1)]);
+      p_due = false;
     };
-    Pending pend[2];      // [step & 1] (constant indices below: registers)
-    int xs = 0, xp = 0;   // next step of either kind
-    int j = it.j0, qt = 0, i = 0, item = 0, qc = 0, tiles = 0, steps0 = 0, steps1 = 0;  // (i: of the item's steps)
-    uint32_t idle = 0;
-    bool ok = true;
-    while (it.valid() || xp < xs) {
-      bool went = false;
-      if (it.valid() && xs <= xp + 1 && ready(&st->bars[kKFull + (tiles & 1)], uint32_t(tiles >> 1) & 1u)) {
-        const int slot = i & 1, n = slot ? steps1 : steps0, q = qc + qt, qs = q & (nq - 1);
-        if (j > it.j0 || ready(&st->bars[kQFull + qs], uint32_t(nq == 2 ? q >> 1 : q) & 1u)) {
-          tc::fence_after();
-          const uint64_t qd = qdesc + qs * kOp, kd = kdesc + (tiles & 1) * kOp;
-          const uint32_t ts = tmem + C::kS + (xs & 1) * kBN;
+    for (; ok && it.valid(); it.next(p, sp, rg), ++item) {
+      const int nt = one(it.nt), count = one(it.j1 - it.j0) * nt;
+      for (int i = 0; ok && i < count; ++i) {
+        const int qt = nt == 2 ? i & 1 : 0, slot = i & 1, qs = (q + qt) & (nqs - 1), use = nqs == 2 ? (q + qt) >> 1 : q + qt;
+        // (an item's queries may be late: the products do not wait for them)
+        if (i == 0 && p_due && !__all_sync(0xffffffffu, test_wait(&st->bars[kQFull + qs], uint32_t(use) & 1u))) products();
+        if (qt == 0) ok = ok && wait_warp(st, kKFull + (tiles & 1), uint32_t(tiles >> 1) & 1u);
+        if (i < nt) ok = ok && wait_warp(st, kQFull + qs, uint32_t(use) & 1u);
+        if (!ok) break;
+        tc::fence_after();
+        const uint64_t qd = qdesc + qs * kOp, kd = kdesc + (tiles & 1) * kOp;
+        const uint32_t ts = tm + C::kS + (xs & 1) * kBN;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t off = (kk >> 2) * (C::kHalfBytes >> 4) + (kk & 3) * 2;
-            umma::mma_ss(ts, qd + off, kd + off, idS, kk > 0 ? 1u : 0u);
-          }
-          umma::commit(&st->bars[kSFull + 2 * slot + (n & 1)]);
-          const bool last_row_tile = qt == it.nt - 1;
-          if (last_row_tile) umma::commit(&st->bars[kKEmpty + (tiles & 1)]);
-          if (j == it.j1 - 1) umma::commit(&st->bars[kQEmpty + qs]);
-          const Pending pd = {slot != 0, (n & 1) != 0, (xs & 1) != 0, ((xs >> 1) & 1) != 0, i < 2, last_row_tile,
-                              i < 2 && item > 0, ((item - 1) & 1) != 0, (tiles & 1) != 0, ((tiles >> 1) & 1) != 0};
-          if (xs & 1) pend[1] = pd; else pend[0] = pd;
-          ++xs;
-          ++i;
-          if (slot) ++steps1; else ++steps0;
-          if (!last_row_tile) {
-            ++qt;
-          } else {
-            qt = 0;
-            ++tiles;
-            if (++j == it.j1) {
-              qc += it.nt;
-              ++item;
-              i = 0;
-              it.next(p, sp, rg);
-              j = it.j0;
-            }
-          }
-          went = true;
-        }
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma::mma_ss(ts, qd + (kk >> 2) * kHalf + (kk & 3) * 2, kd + (kk >> 2) * kHalf + (kk & 3) * 2, idS, kk > 0 ? 1u : 0u);
+        const int step = slot ? steps1 : steps0;
+        umma::commit(&st->bars[kSFull + 2 * slot + (step & 1)]);
+        if (qt == nt - 1) umma::commit(&st->bars[kKEmpty + (tiles & 1)]);
+        if (i >= count - nt) umma::commit(&st->bars[kQEmpty + qs]);
+        if (p_due) products();
+        p_due = true;
+        p_slot = slot;
+        p_step = step;
+        p_tile = tiles;
+        p_item = item;
+        p_first = i < 2;
+        p_last = qt == nt - 1;
+        ++xs;
+        if (slot) ++steps1; else ++steps0;
+        if (qt == nt - 1) ++tiles;
       }
-      if (xp < xs) {
-        const Pending pd = (xp & 1) ? pend[1] : pend[0];
-        if (ready(&st->bars[kPFull + pd.x], pd.x_phase) && ready(&st->bars[kVFull + pd.v], pd.v_phase) &&
-            (!pd.wait_o || ready(&st->bars[kOFree], pd.o_phase))) {
-          tc::fence_after();
-          const uint64_t vd = vdesc + pd.v * kOp;
-          const uint32_t ts = tmem + C::kS + pd.x * kBN, to = tmem + C::kO + pd.slot * D;
-#pragma unroll
-          for (int kk = 0; kk < kBN / 16; ++kk)
-            umma::mma_ts(to, ts + 8 * kk, vd + kk * (16 * 128 >> 4), idO, (!pd.first || kk > 0) ? 1u : 0u);
-          umma::commit(&st->bars[kODone + 2 * pd.slot + pd.odd]);
-          if (pd.last_row_tile) umma::commit(&st->bars[kVEmpty + pd.v]);
-          ++xp;
-          went = true;
-        }
-      }
-      if (went) {
-        idle = 0;
-      } else {
-        __nanosleep(20);  // (a spinning thread takes issue slots from the softmax beside it)
-        if ((++idle & 255u) == 0 && (st->abort || idle > kWaitPolls)) {
-          ok = false;
-          break;
-        }
-      }
+      q += nt;
     }
+    if (ok && p_due) products();
     // every MMA issued has completed before the tensor memory is freed
     umma::commit(&st->bars[kDrain]);
     (void)mbar_wait_bounded(&st->bars[kDrain], 0);
