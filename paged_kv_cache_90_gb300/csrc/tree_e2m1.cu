@@ -24,8 +24,8 @@
 // context are widened as zeros, and so are groups of drafted nodes whose scale is a NaN: the rows
 // that see such a node get the NaN back with their output.
 //
-// Warps: 1 issues the MMAs; 0, 2 and 3 convert the queries; 4-7 and 8-11 are the softmax
-// warpgroups; 12-15 widen K, 16-19 V.  Every wait is bounded; when one runs out the block sets an
+// Warps: 1 issues the MMAs; 4-7 and 8-11 are the softmax warpgroups, which also convert the queries;
+// 12-15 widen K, 16-19 V.  Every wait is bounded; when one runs out the block sets an
 // error bit and a flag that makes every role stop, lets its copies and MMAs land and frees the
 // tensor memory.
 #include <algorithm>
@@ -45,7 +45,7 @@ using namespace tree;
 
 constexpr int kThreads = 640;
 // registers of a thread, by warpgroup: launched with 96 each (5 x 96 = 480), then split anew
-constexpr int kRegsControl = 72, kRegsSoftmax = 128, kRegsWiden = 72;
+constexpr int kRegsControl = 40, kRegsSoftmax = 136, kRegsWiden = 80;
 static_assert(kRegsControl + 2 * kRegsSoftmax + 2 * kRegsWiden <= 5 * 96, "registers");
 constexpr uint32_t kTmemCols = 512;
 // A row's weights are 2^(z - m + kTop): at most 2^15 with a reference that lags by 2^kGap.
@@ -73,9 +73,7 @@ struct Cfg {
 enum Bar { kQFull = 0, kQEmpty = 2, kKFull = 4, kKEmpty = 6, kVFull = 8, kVEmpty = 10, kSFull = 12, kPFull = 16,
            kODone = 18, kOFree = 22, kStat = 23, kDrain = 25, kNumBars = 26 };
 
-constexpr int kQueryWarps = 3;
-constexpr int kQueryTiles = 8;  // row tiles whose score factors are kept: the converting warps are up to
-                                // two of them ahead of the MMAs, and those two steps of the softmax
+constexpr int kQueryTiles = 4;  // row tiles whose score factors are kept: those of two items
 constexpr int kBadItems = 8;    // items whose bad rows are kept
 
 struct State {
@@ -221,8 +219,8 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
       // one arrival a warp where warps arrive
       const bool warps4 = (i >= kKFull && i < kKFull + 2) || (i >= kVFull && i < kVFull + 2) ||
                           (i >= kPFull && i < kPFull + 2) || (i >= kStat && i < kStat + 2);
-      const bool queries = i >= kQFull && i < kQFull + 2;
-      mbar_init(&st->bars[i], queries ? kQueryWarps : warps4 ? 4 : i == kOFree ? 8 : 1);
+      const bool warps8 = i == kOFree || (i >= kQFull && i < kQFull + 2);
+      mbar_init(&st->bars[i], warps8 ? 8 : warps4 ? 4 : 1);
     }
     st->abort = 0;
     fence_barrier_init();
@@ -317,78 +315,22 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
     }
   } else if (warp < 4) {
     less_registers<kRegsControl>();
-    Walk it;
-    it.start(p, sp, rg);
-    // ---- queries: the row tiles of each item, converted to f16, every row scaled by a power of two
-    // of its own; and what the fold needs of an item that goes on in the next block's range ---------
-    constexpr int kLanes = D / 8, kPer = 32 / kLanes, kBatch = 4;  // lanes of a row, rows of a pass, passes
-    const int w = warp == 0 ? 0 : warp - 1, sub = lane / kLanes, col = (lane % kLanes) * 8;
-    int q = 0;
-    bool ok = true;
-    int64_t at = rg->from;
-    TreeSplit::Tail tail = {0, 0, 0, 0};
-    for (; ok && it.valid(); it.next(p, sp, rg)) {
-      float f = p.qk_scale_log2 * (p.k_head_scales ? __ldg(p.k_head_scales + it.kvh) : 1.f);
-      for (int qt = 0; ok && qt < it.nt; ++qt, ++q) {
-        const int qs = q & (nq - 1), use = nq == 2 ? q >> 1 : q;
-        const int node0 = (2 * it.pair + qt) * TQ, rows = min(TQ, it.q.e.n - node0) * g;
-        if (use > 0 && !(ok = wait_warp(st, kQEmpty + qs, uint32_t(use - 1) & 1u))) break;
-        unsigned char* to = smem + oq + qs * C::kOpBytes;
-        for (int r0 = w * kBatch * kPer; r0 < rows; r0 += kQueryWarps * kBatch * kPer) {
-          uint4 x[kBatch];
-#pragma unroll
-          for (int u = 0; u < kBatch; ++u) {
-            const int r = r0 + u * kPer + sub;
-            x[u] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < rows) {
-              const int node = r / g, h = r - node * g;
-              x[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.query) +
-                                                     int64_t(it.q.e.q0 + node0 + node) * p.q_stride_t +
-                                                     int64_t(it.kvh * g + h) * p.q_stride_h + col);
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < kBatch; ++u) {
-            const int r = r0 + u * kPer + sub;
-            float y[8], top = 0.f;
-            Chunk<BF16>::expand(x[u], y);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(y[e]));
-#pragma unroll
-            for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int sh = i8::query_shift(top);
-            const float s = copysignf(i8::power(sh), f);  // (the factor is positive: a row's maximum is that of its sums)
-            if (r < rows) {
-              uint32_t h[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __half2 v = __floats2half2_rn(y[2 * e] * s, y[2 * e + 1] * s);
-                h[e] = *reinterpret_cast<const uint32_t*>(&v);
-              }
-              *reinterpret_cast<uint4*>(to + (col >> 6) * C::kHalfBytes + r * 128 + (((col >> 3) & 7) ^ (r & 7)) * 16) =
-                  make_uint4(h[0], h[1], h[2], h[3]);
-              // (never 0, with which a hidden score of -infinity would be NaN)
-              if (col == 0) st->qf[q % kQueryTiles][r] = fabsf(f) * i8::power(-sh) < 0x1p-149f ? 0x1p-149f : fabsf(f) * i8::power(-sh);
-            }
-          }
+    // ---- what the fold needs of an item that goes on in the next block's range ----------------------
+    if (warp == 0) {
+      Walk it;
+      int64_t at = rg->from;
+      TreeSplit::Tail tail = {0, 0, 0, 0};
+      for (it.start(p, sp, rg); it.valid(); it.next(p, sp, rg)) {
+        if (it.begins() && !it.ends()) {
+          const int node0 = 2 * it.pair * TQ;
+          tail.row0 = it.q.e.q0 + node0;
+          tail.nodes = min(2 * TQ, it.q.e.n - node0);
+          tail.kvh = it.kvh;
+          tail.last = int((at - it.u0 + it.q.tiles + rg->cost - 1) / rg->share);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&st->bars[kQFull + qs]);
+        at += it.u1 - it.u0;
       }
-      if (it.begins() && !it.ends()) {
-        const int node0 = 2 * it.pair * TQ;
-        tail.row0 = it.q.e.q0 + node0;
-        tail.nodes = min(2 * TQ, it.q.e.n - node0);
-        tail.kvh = it.kvh;
-        tail.last = int((at - it.u0 + it.q.tiles + rg->cost - 1) / rg->share);
-      }
-      at += it.u1 - it.u0;
-    }
-    if (warp == 0 && lane == 0) sp.tails[blockIdx.x] = tail;
-    if (!ok && lane == 0) {
-      st->abort = 1;
-      raise_device_error(p.err, kErrTimeout);
+      if (lane == 0) sp.tails[blockIdx.x] = tail;
     }
   } else if (warp >= 12) {
     less_registers<kRegsWiden>();
@@ -437,41 +379,56 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
     constexpr int kCopies = 32 / kRows, kScaleBytes = 32 * C::kGroups;
     const int sbyte = (lane * 16) % kScaleBytes, srow = sbyte / C::kGroups;
     const uint32_t s_in_block = (srow & bs_mask) * C::kGroups;
-    auto copy = [&](uint32_t to) {
-      if (have_next) {
-        ++copied;
-        uint32_t e = e_next;
-        if (e >= uint32_t(p.num_blocks)) {  // (negative ones are large)
-          raise_device_error(p.err, kErrTableEntry);
-          e = 0;
-        }
-        // (the blocks of all copies first: one shuffle after the other, not one behind each copy)
-        uint32_t blk[kCopies];
+    // The addresses of a tile's copies, made before they are needed: a shuffle's and a product's latency
+    // each would hold up the warp behind the copy before.
+    const unsigned char* src[kCopies];
+    const unsigned char* ssrc = nullptr;
+    uint32_t e_now = 0;
+    bool due = false;
+    auto prepare = [&]() {
+      due = have_next;
+      if (!due) return;
+      e_now = e_next;
+      if (e_now >= uint32_t(p.num_blocks)) {  // (negative ones are large)
+        raise_device_error(p.err, kErrTableEntry);
+        e_now = 0;
+      }
+      uint32_t blk[kCopies];
 #pragma unroll
-        for (int c = 0; c < kCopies; ++c) blk[c] = __shfl_sync(0xffffffffu, e, c * kRows + crow);
-        const uint32_t sblk = __shfl_sync(0xffffffffu, e, srow);
-        const unsigned char* src = cache + next_kvh * head_bytes + in_block;
-        const unsigned char* ssrc = scales + next_kvh * head_scales;
+      for (int c = 0; c < kCopies; ++c) blk[c] = __shfl_sync(0xffffffffu, e_now, c * kRows + crow);
+      const uint32_t sblk = __shfl_sync(0xffffffffu, e_now, srow);
+      const unsigned char* const from = cache + next_kvh * head_bytes + in_block;
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c)
+        src[c] = from + blk[c] * block_bytes + (kRows <= bs_mask ? (c * kRows & bs_mask) * C::kRow : 0);
+      ssrc = scales + next_kvh * head_scales + (sp.vec_scales ? sblk * block_scales + s_in_block : 0);
+      lookup();
+    };
+    auto copy = [&](uint32_t to) {
+      if (due) {
+        ++copied;
         const uint32_t dst = to + crow * C::kRow + cbyte;
 #pragma unroll
-        for (int c = 0; c < kCopies; ++c)
-          copy16(dst + c * kRows * C::kRow, src + blk[c] * block_bytes + (kRows <= bs_mask ? (c * kRows & bs_mask) * C::kRow : 0));
+        for (int c = 0; c < kCopies; ++c) copy16(dst + c * kRows * C::kRow, src[c]);
         if (sp.vec_scales) {
-          if (lane < kScaleBytes / 16) copy16(to + 32 * C::kRow + sbyte, ssrc + sblk * block_scales + s_in_block);
-        } else {
+          if (lane < kScaleBytes / 16) copy16(to + 32 * C::kRow + sbyte, ssrc);
+        } else {  // (words of four, at any multiple of them)
 #pragma unroll
           for (int c = 0; c < kScaleBytes; c += 128) {
             const int byte = c + 4 * lane, row = byte / C::kGroups;
-            copy4(to + 32 * C::kRow + byte, ssrc + __shfl_sync(0xffffffffu, e, row) * block_scales +
+            copy4(to + 32 * C::kRow + byte, ssrc + __shfl_sync(0xffffffffu, e_now, row) * block_scales +
                                                 (row & bs_mask) * C::kGroups + byte % C::kGroups);
           }
         }
-        lookup();
       }
       end_copies();
     };
     lookup();
-    for (int s = 0; s < nst; ++s) copy(stage0 + s * C::kStage);
+    for (int s = 0; s < nst; ++s) {
+      prepare();
+      copy(stage0 + s * C::kStage);
+    }
+    prepare();
     bool ok = true;
     State::Item part = {};  // the tile's, and how many of its tiles are left
     int item = 0, k_tile = 0;
@@ -556,6 +513,7 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&st->bars[(isv ? kVFull : kKFull) + buf]);
+      prepare();
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // the copies in flight land before the block may exit
     if (!ok && lane == 0) {
@@ -573,8 +531,70 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
     const uint32_t tO = tmem + C::kO + wg * D + lane_off;
     int x0 = 0, qc = 0, item = 0, steps = 0, folds = 0;  // `steps`: of this warpgroup so far; `folds`: items of one row tile
     bool ok = true;
-    for (; ok && it.valid(); it.next(p, sp, rg), ++item) {
-      const Extent& e = it.q.e;
+    // The walk's item's queries: a row tile by each warpgroup, or half the rows of one by each.  They
+    // are converted to f16, every row scaled by a power of two of its own.  (Between two items, before
+    // the first one's output: the next one's scores are then under way.)
+    auto queries = [&]() {
+      constexpr int kLanes = D / 8, kPer = 32 / kLanes, kBatch = 4;  // lanes of a row, rows of a pass, passes
+      const int sub = lane / kLanes, col = (lane % kLanes) * 8;
+      const int qt = it.nt == 2 ? wg : 0, n = qc + qt, qs = n & (nq - 1), use = nq == 2 ? n >> 1 : n;
+      const int node0 = (2 * it.pair + qt) * TQ, rows = min(TQ, it.q.e.n - node0) * g;
+      const float f = p.qk_scale_log2 * (p.k_head_scales ? __ldg(p.k_head_scales + it.kvh) : 1.f);
+      if (use > 0) ok = ok && wait_warp(st, kQEmpty + qs, uint32_t(use - 1) & 1u);
+      unsigned char* to = smem + oq + qs * C::kOpBytes;
+      const int w = it.nt == 2 ? q : 4 * wg + q, warps = it.nt == 2 ? 4 : 8;
+      if (ok) {
+#pragma unroll 1
+        for (int r0 = w * kBatch * kPer; r0 < rows; r0 += warps * kBatch * kPer) {
+          uint4 x[kBatch];
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) {
+            const int r = r0 + u * kPer + sub;
+            x[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < rows) {
+              const int node = r / g, h = r - node * g;
+              x[u] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.query) +
+                                                     int64_t(it.q.e.q0 + node0 + node) * p.q_stride_t +
+                                                     int64_t(it.kvh * g + h) * p.q_stride_h + col);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) {
+            const int r = r0 + u * kPer + sub;
+            float y[8], top = 0.f;
+            Chunk<BF16>::expand(x[u], y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(y[e]));
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const int sh = i8::query_shift(top);
+            const float s = copysignf(i8::power(sh), f);  // (the factor is positive: a row's maximum is that of its sums)
+            if (r < rows) {
+              uint32_t h[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __half2 v = __floats2half2_rn(y[2 * e] * s, y[2 * e + 1] * s);
+                h[e] = *reinterpret_cast<const uint32_t*>(&v);
+              }
+              *reinterpret_cast<uint4*>(to + (col >> 6) * C::kHalfBytes + r * 128 + (((col >> 3) & 7) ^ (r & 7)) * 16) =
+                  make_uint4(h[0], h[1], h[2], h[3]);
+              // (never 0, with which a hidden score of -infinity would be NaN)
+              const float factor = fabsf(f) * i8::power(-sh);
+              if (col == 0) st->qf[n % kQueryTiles][r] = factor < 0x1p-149f ? 0x1p-149f : factor;
+            }
+          }
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&st->bars[kQFull + qs]);
+        if (it.nt == 2) mbar_arrive(&st->bars[kQFull + qs]);  // (eight arrivals, whoever makes them)
+      }
+    };
+    if (it.valid()) queries();
+    for (; ok && it.valid(); ++item) {
+      const Extent e = it.q.e;
       const int total = (it.j1 - it.j0) * it.nt, qt = it.nt == 2 ? wg : 0;
       const int node = (2 * it.pair + qt) * TQ + r_node;
       const bool row_ok = r < TQ * g && node < e.n;
@@ -641,14 +661,21 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
       if (!ok) break;
       x0 += total;
       qc += it.nt;
+      // (what the output needs of the walk, which goes on to the next item's queries)
+      const int nt = it.nt, j0 = it.j0, j1 = it.j1, base = it.q.base, kvh = it.kvh;
+      const bool begins = it.begins(), whole = begins && it.ends();
+      const int32_t* const table = p.block_tables + int64_t(it.s) * p.bt_stride;
+      it.next(p, sp, rg);
+      if (it.valid()) queries();
+      if (!ok) break;
       // ---- the part's output: this warpgroup's row tile, or half the columns of both results ---------
       const int own = (total - wg + 1) >> 1;  // steps of this warpgroup in the item
       if (own > 0 && !(ok = wait_warp(st, kODone + 2 * wg + ((steps - 1) & 1), uint32_t((steps - 1) >> 1) & 1u))) break;
       // (without a step of its own it might run ahead of the other one by more than a phase)
       if (item > 0 && !(ok = wait_warp(st, kOFree, uint32_t(item - 1) & 1u))) break;
       float f0 = 1.f, f1 = 0.f, m = m_ref, l = l_run;  // the factors on this warpgroup's O and on the other's
-      const bool two = it.nt == 1 && total > 1;        // (both have a result)
-      if (it.nt == 1) {
+      const bool two = nt == 1 && total > 1;        // (both have a result)
+      if (nt == 1) {
         st->stat[folds & 1][wg][r] = make_float2(m_ref, l_run);
         __syncwarp();
         if (lane == 0) mbar_arrive(&st->bars[kStat + wg]);
@@ -664,24 +691,23 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
       }
       tc::fence_after();
       if (warp_ok) {
-        const bool whole = it.begins() && it.ends();
-        const float fv = p.v_head_scales ? __ldg(p.v_head_scales + it.kvh) : p.v_scale;
+        const float fv = p.v_head_scales ? __ldg(p.v_head_scales + kvh) : p.v_scale;
         const float inv = (whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f) * fv;
-        const int64_t prow = int64_t(2 * blockIdx.x + (it.begins() ? 1 : 0)) * sp.rows + qt * kBM + r;
-        if (row_ok && !whole && (it.nt == 2 || wg == 0)) sp.ml[prow] = make_float2(m, l);
-        const int jt = (e.P - it.q.base) / kBN;
+        const int64_t prow = int64_t(2 * blockIdx.x + (begins ? 1 : 0)) * sp.rows + qt * kBM + r;
+        if (row_ok && !whole && (nt == 2 || wg == 0)) sp.ml[prow] = make_float2(m, l);
+        const int jt = (e.P - base) / kBN;
         // (the bytes of this part's tiles; the others are not this item's)
         const unsigned char* bad = st->bad[item % kBadItems];
-        const int b0 = 16 * (max(it.j0, jt) - jt), b1 = 16 * (it.j1 - jt);
+        const int b0 = 16 * (max(j0, jt) - jt), b1 = 16 * (j1 - jt);
         bool any_bad = false;
         if (mask && row_ok)
           for (int b = b0; b < b1; b += 4) any_bad |= *reinterpret_cast<const uint32_t*>(bad + b) != 0u;
-        const int c_first = it.nt == 2 ? 0 : wg * (D / 64), c_last = it.nt == 2 ? D / 32 : c_first + D / 64;
+        const int c_first = nt == 2 ? 0 : wg * (D / 64), c_last = nt == 2 ? D / 32 : c_first + D / 64;
         const uint32_t tA = tmem + C::kO + lane_off, tB = tA + D;  // even and odd tiles' results
 #pragma unroll 1
         for (int c = c_first; c < c_last; ++c) {
           uint32_t w[32];
-          if (it.nt == 2) {
+          if (nt == 2) {
             tc::ld32(tO + 32 * c, w);
             tc::wait_ld();
           } else {
@@ -702,11 +728,11 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
           }
           if (any_bad) {  // the NaN that were taken out of V, to the rows that see them
             for (int k = 8 * b0; k < 8 * b1; ++k) {
-              const int at = it.q.base + jt * kBN + k;
+              const int at = base + jt * kBN + k;
               if (!(bad[k >> 3] >> (k & 7) & 1) || !tree::sees_node(mask, at - e.P)) continue;
-              const int blk = __ldg(p.block_tables + int64_t(it.s) * p.bt_stride + (at >> sp.bs_shift));
+              const int blk = __ldg(table + (at >> sp.bs_shift));
               if (blk < 0 || int64_t(blk) >= p.num_blocks) continue;
-              const unsigned char* s = p.v_group_scales + int64_t(blk) * p.ts_block + int64_t(it.kvh) * p.ts_head +
+              const unsigned char* s = p.v_group_scales + int64_t(blk) * p.ts_block + int64_t(kvh) * p.ts_head +
                                        (at & (p.block_size - 1)) * C::kGroups + 2 * c;
               const bool lo = (s[0] & 0x7f) == 0x7f, hi = (s[1] & 0x7f) == 0x7f;
 #pragma unroll
@@ -717,7 +743,7 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
           if (!row_ok) continue;
           if (whole) {
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + trow * p.out_stride_t +
-                                 int64_t(it.kvh * g + r_head) * p.out_stride_h + 32 * c;
+                                 int64_t(kvh * g + r_head) * p.out_stride_h + 32 * c;
             uint32_t o16[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
