@@ -13,9 +13,9 @@
 // results are folded when the item ends (each warpgroup then writes half of the columns).  So an
 // item's softmax runs in both at once, whatever its rows.
 //
-// K and V are widened by a warpgroup each: a warp brings 32 positions of a tile (asynchronous
-// copies, one to four tiles ahead, as shared memory allows), and code times group scale is an f16
-// number exactly (e2m1_codes.cuh).  A query row is scaled by the power of two that brings its
+// K and V are widened by a warpgroup each: a warp loads 32 positions of a tile into registers, a tile
+// ahead, and code times group scale is an f16 number exactly (e2m1_codes.cuh).  (With asynchronous
+// copies into shared memory a warp spent 500 clocks a tile on issuing them and 150 on reading them.)  A query row is scaled by the power of two that brings its
 // largest element to 2^14, so its bf16 values are exact down to 2^-29 of that.  A weight is rounded
 // to f16, half a step, 2^-11, down to 2^-21 of the row's largest, 2^-32 of that below.  Scores,
 // maximum, sum and output are binary32.
@@ -56,12 +56,9 @@ struct Cfg {
   static constexpr int kHalves = D / 64;             // 64-column halves of an operand (128-byte rows)
   static constexpr uint32_t kHalfBytes = kBM * 128;  // 16 KB
   static constexpr uint32_t kOpBytes = kHalves * kHalfBytes;
-  static constexpr int kRow = D / 2, kGroups = D / 16;        // bytes and scales of a cache row
-  static constexpr uint32_t kStage = 32 * (kRow + kGroups);   // a warp's 32 positions
-  // from the 1024-aligned base: one or two query tiles | two K tiles | two V tiles | the stages of
-  // the eight widening warps | state
-  __host__ __device__ static constexpr int stages(int nq) { return D == 128 ? (nq == 1 ? 3 : 1) : 4; }
-  static constexpr uint32_t kState = D == 128 ? 214 * 1024 : 2 * kOpBytes + 4 * kOpBytes + 8 * 4 * kStage;
+  static constexpr int kRow = D / 2, kGroups = D / 16;  // bytes and scales of a cache row
+  // from the 1024-aligned base: two query tiles | two K tiles | two V tiles | state
+  static constexpr uint32_t kQ = 0, kK = 2 * kOpBytes, kV = 4 * kOpBytes, kState = 6 * kOpBytes;
   static constexpr uint32_t kStateBytes = 11 * 1024;
   static constexpr size_t kSmem = kState + kStateBytes + 1024;  // (+ alignment)
   // tensor memory: S of even and odd steps (128 columns each), then O of the two warpgroups
@@ -87,7 +84,7 @@ struct State {
   // drafted positions with a NaN scale in V, 8 to a byte from the first tile that holds drafted
   // nodes on (1024 nodes touch at most 9 tiles)
   unsigned char bad[kBadItems][144];
-  // What a widening warp of V has to know of an item's part (mod 8: its walk is up to six tiles, so
+  // What a widening warp of V has to know of an item's part (mod 8: its walk is up to three tiles, so
   // items, ahead): tiles, the first one's first position, the context's end, its window's start and
   // its drafted nodes', and the first tile of these counted from the part's first.
   struct Item {
@@ -102,17 +99,20 @@ __device__ __forceinline__ bool wait_warp(State* st, int bar, uint32_t parity) {
   return __all_sync(0xffffffffu, wait(st, bar, parity));
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const unsigned char* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// a lane's D / 4 codes of a row, and their scales (two, or one at D = 64)
+__device__ __forceinline__ void load_codes(const unsigned char* p, uint32_t (&w)[4]) {
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const unsigned char* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void load_codes(const unsigned char* p, uint32_t (&w)[2]) {
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
 }
-__device__ __forceinline__ void end_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void wait_copies(int pending) {  // (at most: 0, 2 or 3)
-  if (pending == 0) asm volatile("cp.async.wait_group 0;" ::: "memory");
-  else if (pending == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-  else asm volatile("cp.async.wait_group 3;" ::: "memory");
+template <int D>
+__device__ __forceinline__ uint32_t load_scales(const unsigned char* p) {
+  uint32_t x;
+  if (D == 128) asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(x) : "l"(p));
+  else asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(x) : "l"(p));
+  return x;
 }
 
 template <int N>
@@ -228,14 +228,12 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
   if (warp == 0) tc::alloc(&st->tmem, kTmemCols);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // nothing of the caller's is read before
   asm volatile("griddepcontrol.launch_dependents;");
-  // (nq: query tiles in shared memory, two where some sequence of the batch has a second row tile)
-  const int nq = find_range<kThreads>(p, sp, &st->range, st->warp_sum, sp.tq) ? 2 : 1;
+  (void)find_range<kThreads>(p, sp, &st->range, st->warp_sum, 0);
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = st->tmem;
   const Range* rg = &st->range;
-  const uint32_t oq = 0, okey = nq * C::kOpBytes, ov = okey + 2 * C::kOpBytes, os = ov + 2 * C::kOpBytes;  // the places
 
   if (warp == 1) {
     less_registers<kRegsControl>();
@@ -247,10 +245,9 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
     constexpr uint32_t idS = idesc_f16(kBM, kBN, 0, 0), idO = idesc_f16(kBM, D, 0, 1);
     constexpr uint64_t kOp = C::kOpBytes >> 4, kHalf = C::kHalfBytes >> 4;  // (descriptors hold addresses / 16)
     auto one = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-    const int nqs = one(nq);
     const uint32_t base = one(int(sbase)), tm = one(int(tmem));
-    const uint64_t qdesc = tc::desc_sw128(base, 16, 1024), kdesc = tc::desc_sw128(base + nqs * C::kOpBytes, 16, 1024);
-    const uint64_t vdesc = tc::desc_sw128(base + (nqs + 2) * C::kOpBytes, C::kHalfBytes, 1024);
+    const uint64_t qdesc = tc::desc_sw128(base + C::kQ, 16, 1024), kdesc = tc::desc_sw128(base + C::kK, 16, 1024);
+    const uint64_t vdesc = tc::desc_sw128(base + C::kV, C::kHalfBytes, 1024);
     int xs = 0, tiles = 0, q = 0, item = 0, steps0 = 0, steps1 = 0;
     // the step whose P V is next: its warpgroup, that one's step and the tile; whether it is the
     // warpgroup's first of the item, and the last of its tile
@@ -275,7 +272,7 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
     for (; ok && it.valid(); it.next(p, sp, rg), ++item) {
       const int nt = one(it.nt), count = one(it.j1 - it.j0) * nt;
       for (int i = 0; ok && i < count; ++i) {
-        const int qt = nt == 2 ? i & 1 : 0, slot = i & 1, qs = (q + qt) & (nqs - 1), use = nqs == 2 ? (q + qt) >> 1 : q + qt;
+        const int qt = nt == 2 ? i & 1 : 0, slot = i & 1, qs = (q + qt) & 1, use = (q + qt) >> 1;
         // (an item's queries may be late: the products do not wait for them)
         if (i == 0 && p_due && !__all_sync(0xffffffffu, test_wait(&st->bars[kQFull + qs], uint32_t(use) & 1u))) products();
         if (qt == 0) ok = ok && wait_warp(st, kKFull + (tiles & 1), uint32_t(tiles >> 1) & 1u);
@@ -339,19 +336,17 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
     // ---- widening: K by one warpgroup, V by the other; a warp has 32 positions of every tile --------
     const bool isv = warp >= 16;
     const int w4 = warp & 3, gr = lane >> 2, t = lane & 3;  // (D = 128: a lane has 16 bytes of a row)
-    const int nst = C::stages(nq), bs_mask = p.block_size - 1;
+    const int bs_mask = p.block_size - 1;
     const uint64_t block_bytes = uint32_t(p.cs_block), block_scales = uint32_t(p.ts_block);  // (32 bits: see the host's check)
     const uint64_t head_bytes = uint32_t(p.cs_head), head_scales = uint32_t(p.ts_head);
-    const unsigned char* cache = static_cast<const unsigned char*>(isv ? p.value_cache : p.key_cache);
-    const unsigned char* scales = isv ? p.v_group_scales : p.k_group_scales;
-    const uint32_t stage0 = sbase + os + (warp - 12) * nst * C::kStage;
-    unsigned char* const tiles = smem + (isv ? ov : okey);
-    constexpr int kLanes = C::kRow / 16, kRows = 32 / kLanes;  // lanes of a row, rows of a copy
-    const int crow = lane / kLanes, cbyte = lane % kLanes * 16;
-    // (a tile's first position is a block's first)
-    const uint32_t in_block = (crow & bs_mask) * C::kRow + cbyte;
-    // the table's entries are looked up a tile ahead of the copies; the walk is theirs, an item ahead
-    int copied = 0, items = 0, t_left = 0, t_pos = 0, t_end = 0, next_kvh = 0;
+    unsigned char* const tiles = smem + (isv ? C::kV : C::kK);
+    constexpr int kW = D / 32, kN = 32 / 8;  // words of a lane, its rows
+    // (a tile's first position is a block's first.)  The lanes of a row's second half take their words in
+    // another order, so that eight lanes never meet a bank twice when they write them.
+    const unsigned char* const cache = static_cast<const unsigned char*>(isv ? p.value_cache : p.key_cache) + 4 * kW * t;
+    const unsigned char* const scales = (isv ? p.v_group_scales : p.k_group_scales) + (D / 64) * t;
+    // the table's entries are looked up a tile ahead of the loads; the walk is theirs, an item ahead
+    int items = 0, t_left = 0, t_pos = 0, t_end = 0, next_kvh = 0;
     const int32_t* t_entry = nullptr;
     bool have_next = false;
     uint32_t e_next = 0;
@@ -376,86 +371,33 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
       t_entry += kBN >> sp.bs_shift;
       --t_left;
     };
-    constexpr int kCopies = 32 / kRows, kScaleBytes = 32 * C::kGroups;
-    const int sbyte = (lane * 16) % kScaleBytes, srow = sbyte / C::kGroups;
-    const uint32_t s_in_block = (srow & bs_mask) * C::kGroups;
-    // The addresses of a tile's copies, made before they are needed: a shuffle's and a product's latency
-    // each would hold up the warp behind the copy before.
-    const unsigned char* src[kCopies];
-    const unsigned char* ssrc = nullptr;
-    uint32_t e_now = 0;
-    bool due = false;
-    auto prepare = [&]() {
-      due = have_next;
-      if (!due) return;
-      e_now = e_next;
-      if (e_now >= uint32_t(p.num_blocks)) {  // (negative ones are large)
+    auto load = [&](uint32_t (&x)[kN][kW], uint32_t (&sc)[kN]) {
+      uint32_t e = e_next;
+      if (e >= uint32_t(p.num_blocks)) {  // (negative ones are large)
         raise_device_error(p.err, kErrTableEntry);
-        e_now = 0;
+        e = 0;
       }
-      uint32_t blk[kCopies];
+      uint32_t blk[kN];
 #pragma unroll
-      for (int c = 0; c < kCopies; ++c) blk[c] = __shfl_sync(0xffffffffu, e_now, c * kRows + crow);
-      const uint32_t sblk = __shfl_sync(0xffffffffu, e_now, srow);
-      const unsigned char* const from = cache + next_kvh * head_bytes + in_block;
+      for (int i = 0; i < kN; ++i) blk[i] = __shfl_sync(0xffffffffu, e, 8 * i + gr);
+      const unsigned char *const from = cache + next_kvh * head_bytes, *const sfrom = scales + next_kvh * head_scales;
 #pragma unroll
-      for (int c = 0; c < kCopies; ++c)
-        src[c] = from + blk[c] * block_bytes + (kRows <= bs_mask ? (c * kRows & bs_mask) * C::kRow : 0);
-      ssrc = scales + next_kvh * head_scales + (sp.vec_scales ? sblk * block_scales + s_in_block : 0);
+      for (int i = 0; i < kN; ++i) load_codes(from + blk[i] * block_bytes + ((8 * i + gr) & bs_mask) * C::kRow, x[i]);
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        sc[i] = load_scales<D>(sfrom + blk[i] * block_scales + ((8 * i + gr) & bs_mask) * C::kGroups);
       lookup();
     };
-    auto copy = [&](uint32_t to) {
-      if (due) {
-        ++copied;
-        const uint32_t dst = to + crow * C::kRow + cbyte;
-#pragma unroll
-        for (int c = 0; c < kCopies; ++c) copy16(dst + c * kRows * C::kRow, src[c]);
-        if (sp.vec_scales) {
-          if (lane < kScaleBytes / 16) copy16(to + 32 * C::kRow + sbyte, ssrc);
-        } else {  // (words of four, at any multiple of them)
-#pragma unroll
-          for (int c = 0; c < kScaleBytes; c += 128) {
-            const int byte = c + 4 * lane, row = byte / C::kGroups;
-            copy4(to + 32 * C::kRow + byte, ssrc + __shfl_sync(0xffffffffu, e_now, row) * block_scales +
-                                                (row & bs_mask) * C::kGroups + byte % C::kGroups);
-          }
-        }
-      }
-      end_copies();
-    };
     lookup();
-    for (int s = 0; s < nst; ++s) {
-      prepare();
-      copy(stage0 + s * C::kStage);
-    }
-    prepare();
-    bool ok = true;
+    bool have = have_next, ok = true;
+    uint32_t x[kN][kW], sc[kN];
+    if (have) load(x, sc);
     State::Item part = {};  // the tile's, and how many of its tiles are left
     int item = 0, k_tile = 0;
-    for (int n = 0, slot = 0; n < copied; ++n, slot = slot + 1 == nst ? 0 : slot + 1) {
-      wait_copies(nst - 1);
-      __syncwarp();
-      // a row's codes of D / 4 columns (one or two groups of 16) and their scales, four or two rows
-      constexpr int kW = D / 32;              // words of a lane
-      constexpr int kN = 32 / 8;              // rows of a lane
-      uint32_t x[kN][kW], sc[kN];
-      const uint32_t from = stage0 + slot * C::kStage;
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        // (the lanes of a row's second half take their words in another order, so that eight lanes never
-        // meet a bank twice when they are written)
-        const uint32_t a = from + (8 * i + gr) * C::kRow + 4 * kW * t, s = from + 32 * C::kRow + (8 * i + gr) * C::kGroups;
-        if constexpr (D == 128) {
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[i][0]), "=r"(x[i][1]) : "r"(a + (t & 2) * 4));
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[i][2]), "=r"(x[i][3]) : "r"(a + 8 - (t & 2) * 4));
-          asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sc[i]) : "r"(s + 2 * t));
-        } else {
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(x[i][0]), "=r"(x[i][1]) : "r"(a));
-          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc[i]) : "r"(s + t));
-        }
-      }
-      __syncwarp();  // (every lane has read the stage)
-      copy(from);
+    for (int n = 0; have; ++n) {
+      const bool more = have_next;
+      uint32_t y[kN][kW], sy[kN];
+      if (more) load(y, sy);
       if (isv) {
         if (k_tile == part.tiles) {
           part = st->item[w4][item & 7];
@@ -501,7 +443,7 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
         for (int c = 0; c < kW; ++c) {
           const __half2 s = c < 2 ? __low2half2(gs) : __high2half2(gs);
           uint32_t h[4];
-          e2m1::widen8(x[i][c], h);
+          e2m1::widen8(D == 128 && swap ? x[i][(c ^ 2) % kW] : x[i][c], h);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h[u]), s);
@@ -513,9 +455,14 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&st->bars[(isv ? kVFull : kKFull) + buf]);
-      prepare();
+      have = more;
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        sc[i] = sy[i];
+#pragma unroll
+        for (int c = 0; c < kW; ++c) x[i][c] = y[i][c];
+      }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");  // the copies in flight land before the block may exit
     if (!ok && lane == 0) {
       st->abort = 1;
       raise_device_error(p.err, kErrTimeout);
@@ -537,11 +484,11 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
     auto queries = [&]() {
       constexpr int kLanes = D / 8, kPer = 32 / kLanes, kBatch = 4;  // lanes of a row, rows of a pass, passes
       const int sub = lane / kLanes, col = (lane % kLanes) * 8;
-      const int qt = it.nt == 2 ? wg : 0, n = qc + qt, qs = n & (nq - 1), use = nq == 2 ? n >> 1 : n;
+      const int qt = it.nt == 2 ? wg : 0, n = qc + qt, qs = n & 1, use = n >> 1;
       const int node0 = (2 * it.pair + qt) * TQ, rows = min(TQ, it.q.e.n - node0) * g;
       const float f = p.qk_scale_log2 * (p.k_head_scales ? __ldg(p.k_head_scales + it.kvh) : 1.f);
       if (use > 0) ok = ok && wait_warp(st, kQEmpty + qs, uint32_t(use - 1) & 1u);
-      unsigned char* to = smem + oq + qs * C::kOpBytes;
+      unsigned char* to = smem + C::kQ + qs * C::kOpBytes;
       const int w = it.nt == 2 ? q : 4 * wg + q, warps = it.nt == 2 ? 4 : 8;
       if (ok) {
 #pragma unroll 1
@@ -796,8 +743,6 @@ cudaError_t launch_tree_e2m1_tpl(const TreeParams& p, const TreeSplit& sp, cudaS
   using C = tree_e2m1::Cfg<D>;
   static_assert(sizeof(tree_e2m1::State) <= C::kStateBytes, "state");
   static_assert(C::kSmem <= 227 * 1024, "shared memory");
-  static_assert(5 * C::kOpBytes + 8 * C::stages(1) * C::kStage <= C::kState &&
-                6 * C::kOpBytes + 8 * C::stages(2) * C::kStage <= C::kState, "operands and stages");
   constexpr int kDevices = 64;
   auto kern = tree_e2m1::tree_e2m1_kernel<D>;
   static std::once_flag once[kDevices];
@@ -838,10 +783,6 @@ bool tree_e2m1_supported(const TreeParams& p) {
 
 cudaError_t launch_tree_e2m1(const TreeParams& p, TreeSplit sp, cudaStream_t stream) {
   sp.item_nodes = 2 * sp.tq;
-  // (16 bytes of scales are two or four tokens of a block)
-  sp.vec_scales = p.block_size * (p.head_dim / 16) >= 16 &&
-                  !((reinterpret_cast<uintptr_t>(p.k_group_scales) | reinterpret_cast<uintptr_t>(p.v_group_scales) |
-                     p.ts_block | p.ts_head) & 15);
   return p.head_dim == 128 ? launch_tree_e2m1_tpl<128>(p, sp, stream) : launch_tree_e2m1_tpl<64>(p, sp, stream);
 }
 
