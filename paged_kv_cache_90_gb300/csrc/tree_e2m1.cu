@@ -8,10 +8,10 @@
 //                      of two tensor-memory buffers, by the step's parity
 //   P = 2^(S c - m)    written back over S as f16 pairs by a softmax warpgroup, a row per thread
 //   O += P V           M 128, N = D, K = 128 keys: P from tensor memory, V from shared memory
-// The steps of an item go to the two softmax warpgroups in turn, each with a reference m, a sum and
-// an O of its own: two row tiles, one each; or the even and the odd key tiles of one, whose two
-// results are folded when the item ends (each warpgroup then writes half of the columns).  So an
-// item's softmax runs in both at once, whatever its rows.
+// Two softmax warpgroups work on an item, each with a reference m, a sum and an O of its own: two row
+// tiles go to one each; of a single one each has half the keys of every tile, and their two results
+// are folded when the item ends (each then writes half of the columns).  A step of one row tile is
+// then half as long in a warpgroup, and so is the chain from its scores to its product.
 //
 // K and V are widened by a warpgroup each: a warp loads 32 positions of a tile into registers, a tile
 // ahead, and code times group scale is an f16 number exactly (e2m1_codes.cuh).  (With asynchronous
@@ -68,7 +68,7 @@ struct Cfg {
 // Barriers.  A wait names a phase by its parity, so its barrier may be at most one phase away:
 // those that a softmax warpgroup waits for count its own steps, two barriers by their parity.
 enum Bar { kQFull = 0, kQEmpty = 2, kKFull = 4, kKEmpty = 6, kVFull = 8, kVEmpty = 10, kSFull = 12, kPFull = 16,
-           kODone = 18, kOFree = 22, kStat = 23, kDrain = 25, kNumBars = 26 };
+           kODone = 20, kOFree = 24, kStat = 25, kDrain = 27, kNumBars = 28 };
 
 constexpr int kQueryTiles = 4;  // row tiles whose score factors are kept: those of two items
 constexpr int kBadItems = 8;    // items whose bad rows are kept
@@ -218,7 +218,7 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
     for (int i = 0; i < kNumBars; ++i) {
       // one arrival a warp where warps arrive
       const bool warps4 = (i >= kKFull && i < kKFull + 2) || (i >= kVFull && i < kVFull + 2) ||
-                          (i >= kPFull && i < kPFull + 2) || (i >= kStat && i < kStat + 2);
+                          (i >= kPFull && i < kPFull + 4) || (i >= kStat && i < kStat + 2);
       const bool warps8 = i == kOFree || (i >= kQFull && i < kQFull + 2);
       mbar_init(&st->bars[i], warps8 ? 8 : warps4 ? 4 : 1);
     }
@@ -248,31 +248,47 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
     const uint32_t base = one(int(sbase)), tm = one(int(tmem));
     const uint64_t qdesc = tc::desc_sw128(base + C::kQ, 16, 1024), kdesc = tc::desc_sw128(base + C::kK, 16, 1024);
     const uint64_t vdesc = tc::desc_sw128(base + C::kV, C::kHalfBytes, 1024);
-    int xs = 0, tiles = 0, q = 0, item = 0, steps0 = 0, steps1 = 0;
-    // the step whose P V is next: its warpgroup, that one's step and the tile; whether it is the
-    // warpgroup's first of the item, and the last of its tile
-    int p_slot = 0, p_step = 0, p_tile = 0, p_item = 0;
+    int xs = 0, tiles = 0, q = 0, item = 0, steps[2] = {0, 0};  // (steps: of the warpgroups)
+    // the step whose P V is next: its tile, and what it is to the one warpgroup that has it, or to both
+    // (-1); whether it is its warpgroup's first of the item, and the last of its tile
+    int p_wg = 0, p_step[2] = {0, 0}, p_tile = 0, p_item = 0;
     bool p_first = false, p_last = false, p_due = false, ok = true;
     auto products = [&]() {
       const int x = xs - 1;
-      ok = wait_warp(st, kVFull + (p_tile & 1), uint32_t(p_tile >> 1) & 1u) &&
-           (!p_first || p_item == 0 || wait_warp(st, kOFree, uint32_t(p_item - 1) & 1u)) &&
-           wait_warp(st, kPFull + (x & 1), uint32_t(x >> 1) & 1u);
-      if (!ok) return;
-      tc::fence_after();
       const uint64_t vd = vdesc + (p_tile & 1) * kOp;
-      const uint32_t ts = tm + C::kS + (x & 1) * kBN, to = tm + C::kO + p_slot * D;
+      const uint32_t ts = tm + C::kS + (x & 1) * kBN;
+      ok = wait_warp(st, kVFull + (p_tile & 1), uint32_t(p_tile >> 1) & 1u) &&
+           (!p_first || p_item == 0 || wait_warp(st, kOFree, uint32_t(p_item - 1) & 1u));
+      if (p_wg >= 0) {
+        const int w = p_wg, n = w ? p_step[1] : p_step[0];
+        ok = ok && wait_warp(st, kPFull + 2 * w + (n & 1), uint32_t(n >> 1) & 1u);
+        if (!ok) return;
+        tc::fence_after();
 #pragma unroll
-      for (int kk = 0; kk < kBN / 16; ++kk)
-        umma::mma_ts(to, ts + 8 * kk, vd + kk * (16 * 128 >> 4), idO, (!p_first || kk > 0) ? 1u : 0u);
-      umma::commit(&st->bars[kODone + 2 * p_slot + (p_step & 1)]);
+        for (int kk = 0; kk < kBN / 16; ++kk)
+          umma::mma_ts(tm + C::kO + w * D, ts + 8 * kk, vd + kk * (16 * 128 >> 4), idO, (!p_first || kk > 0) ? 1u : 0u);
+        umma::commit(&st->bars[kODone + 2 * w + (n & 1)]);
+      } else {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {  // a half of the keys each
+          const int n = p_step[w];
+          ok = ok && wait_warp(st, kPFull + 2 * w + (n & 1), uint32_t(n >> 1) & 1u);
+          if (!ok) return;
+          tc::fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kBN / 32; ++kk)
+            umma::mma_ts(tm + C::kO + w * D, ts + 64 * w + 8 * kk, vd + (4 * w + kk) * (16 * 128 >> 4), idO,
+                         (!p_first || kk > 0) ? 1u : 0u);
+          umma::commit(&st->bars[kODone + 2 * w + (n & 1)]);
+        }
+      }
       if (p_last) umma::commit(&st->bars[kVEmpty + (p_tile & 1)]);
       p_due = false;
     };
     for (; ok && it.valid(); it.next(p, sp, rg), ++item) {
       const int nt = one(it.nt), count = one(it.j1 - it.j0) * nt;
       for (int i = 0; ok && i < count; ++i) {
-        const int qt = nt == 2 ? i & 1 : 0, slot = i & 1, qs = (q + qt) & 1, use = (q + qt) >> 1;
+        const int qt = nt == 2 ? i & 1 : 0, qs = (q + qt) & 1, use = (q + qt) >> 1;
         // (an item's queries may be late: the products do not wait for them)
         if (i == 0 && p_due && !__all_sync(0xffffffffu, test_wait(&st->bars[kQFull + qs], uint32_t(use) & 1u))) products();
         if (qt == 0) ok = ok && wait_warp(st, kKFull + (tiles & 1), uint32_t(tiles >> 1) & 1u);
@@ -284,20 +300,22 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           umma::mma_ss(ts, qd + (kk >> 2) * kHalf + (kk & 3) * 2, kd + (kk >> 2) * kHalf + (kk & 3) * 2, idS, kk > 0 ? 1u : 0u);
-        const int step = slot ? steps1 : steps0;
-        umma::commit(&st->bars[kSFull + 2 * slot + (step & 1)]);
+        if (nt == 1 || qt == 0) umma::commit(&st->bars[kSFull + (steps[0] & 1)]);
+        if (nt == 1 || qt == 1) umma::commit(&st->bars[kSFull + 2 + (steps[1] & 1)]);
         if (qt == nt - 1) umma::commit(&st->bars[kKEmpty + (tiles & 1)]);
         if (i >= count - nt) umma::commit(&st->bars[kQEmpty + qs]);
         if (p_due) products();
         p_due = true;
-        p_slot = slot;
-        p_step = step;
+        p_wg = nt == 1 ? -1 : qt;
+        p_step[0] = steps[0];
+        p_step[1] = steps[1];
         p_tile = tiles;
         p_item = item;
-        p_first = i < 2;
+        p_first = i < nt;
         p_last = qt == nt - 1;
         ++xs;
-        if (slot) ++steps1; else ++steps0;
+        if (nt == 1 || qt == 0) ++steps[0];
+        if (nt == 1 || qt == 1) ++steps[1];
         if (qt == nt - 1) ++tiles;
       }
       q += nt;
@@ -550,20 +568,23 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
       const int64_t* mask = p.tree_mask ? p.tree_mask + (row_ok ? trow : int64_t(e.q0)) * p.mask_stride : nullptr;  // (idle rows: any)
       const uint64_t word0 = mask ? uint64_t(__ldg(mask)) : 0;
       float m_ref = -INFINITY, l_run = 0.f, sl = 0.f;
-      for (int i = wg; i < total; i += 2, ++steps) {
-        const int j = it.j0 + (it.nt == 2 ? i >> 1 : i), x = x0 + i;
+      // this warpgroup's part of a step: its columns of S, 32 at a time
+      const int half = it.nt == 1 ? wg : 0, chunks = it.nt == 1 ? 2 : 4;
+      for (int j = it.j0; j < it.j1; ++j, ++steps) {
+        const int x = x0 + (j - it.j0) * it.nt + qt;
         const int pos = it.q.base + j * kBN;
-        const uint32_t tS = tmem + C::kS + (x & 1) * kBN + lane_off;
+        const uint32_t tS = tmem + C::kS + (x & 1) * kBN + 64 * half + lane_off;
         if (!(ok = wait_warp(st, kSFull + 2 * wg + (steps & 1), uint32_t(steps >> 1) & 1u))) break;
         tc::fence_after();
         if (warp_ok) {
-          if (i == wg) sl = st->qf[(qc + qt) % kQueryTiles][r];
+          if (j == it.j0) sl = st->qf[(qc + qt) % kQueryTiles][r];
           float mx = -INFINITY;
           if (it.cut(j)) {
             uint64_t k[2];
             tile_bits(e, pos, mask, word0, k);
+            if (half) k[0] = k[1];
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < chunks; ++c) {
               mx = fmaxf(mx, row_max<true>(tS + 32 * c, uint32_t(k[0])));
               k[0] = k[0] >> 32 | k[1] << 32;
               k[1] >>= 32;
@@ -571,7 +592,7 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
             tc::wait_st();
           } else {
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) mx = fmaxf(mx, row_max<false>(tS + 32 * c, 0u));
+            for (int c = 0; c < chunks; ++c) mx = fmaxf(mx, row_max<false>(tS + 32 * c, 0u));
           }
           mx *= sl;
           const bool first = m_ref == -INFINITY;
@@ -597,13 +618,13 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
           const float mu = m_ref == -INFINITY ? 0.f : m_ref - kTop;
           float sum = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) sum += weights(tS + 32 * c, tS + 16 * c, sl, mu);
+          for (int c = 0; c < chunks; ++c) sum += weights(tS + 32 * c, tS + 16 * c, sl, mu);
           l_run += sum;
           tc::wait_st();
         }
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&st->bars[kPFull + (x & 1)]);
+        if (lane == 0) mbar_arrive(&st->bars[kPFull + 2 * wg + (steps & 1)]);
       }
       if (!ok) break;
       x0 += total;
@@ -616,12 +637,8 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
       if (it.valid()) queries();
       if (!ok) break;
       // ---- the part's output: this warpgroup's row tile, or half the columns of both results ---------
-      const int own = (total - wg + 1) >> 1;  // steps of this warpgroup in the item
-      if (own > 0 && !(ok = wait_warp(st, kODone + 2 * wg + ((steps - 1) & 1), uint32_t((steps - 1) >> 1) & 1u))) break;
-      // (without a step of its own it might run ahead of the other one by more than a phase)
-      if (item > 0 && !(ok = wait_warp(st, kOFree, uint32_t(item - 1) & 1u))) break;
+      if (!(ok = wait_warp(st, kODone + 2 * wg + ((steps - 1) & 1), uint32_t((steps - 1) >> 1) & 1u))) break;
       float f0 = 1.f, f1 = 0.f, m = m_ref, l = l_run;  // the factors on this warpgroup's O and on the other's
-      const bool two = nt == 1 && total > 1;        // (both have a result)
       if (nt == 1) {
         st->stat[folds & 1][wg][r] = make_float2(m_ref, l_run);
         __syncwarp();
@@ -650,7 +667,7 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
         if (mask && row_ok)
           for (int b = b0; b < b1; b += 4) any_bad |= *reinterpret_cast<const uint32_t*>(bad + b) != 0u;
         const int c_first = nt == 2 ? 0 : wg * (D / 64), c_last = nt == 2 ? D / 32 : c_first + D / 64;
-        const uint32_t tA = tmem + C::kO + lane_off, tB = tA + D;  // even and odd tiles' results
+        const uint32_t tA = tmem + C::kO + lane_off, tB = tA + D;  // the two results
 #pragma unroll 1
         for (int c = c_first; c < c_last; ++c) {
           uint32_t w[32];
@@ -659,19 +676,13 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
             tc::wait_ld();
           } else {
             const float fa = wg ? f1 : f0, fb = wg ? f0 : f1;
+            uint32_t y[32];
             tc::ld32(tA + 32 * c, w);
+            tc::ld32(tB + 32 * c, y);
             tc::wait_ld();
-            if (two) {
-              uint32_t y[32];
-              tc::ld32(tB + 32 * c, y);
-              tc::wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                w[k] = __float_as_uint(fmaf(__uint_as_float(y[k]), fb, __uint_as_float(w[k]) * fa));
-            } else {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * fa);
-            }
+            for (int k = 0; k < 32; ++k)
+              w[k] = __float_as_uint(fmaf(__uint_as_float(y[k]), fb, __uint_as_float(w[k]) * fa));
           }
           if (any_bad) {  // the NaN that were taken out of V, to the rows that see them
             for (int k = 8 * b0; k < 8 * b1; ++k) {
