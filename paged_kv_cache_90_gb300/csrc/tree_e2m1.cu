@@ -157,11 +157,17 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   return r;
 }
 
-// Largest of 32 scores; with `cut` those not kept become -infinity.
-__device__ __forceinline__ float row_max(uint32_t (&w)[32], bool cut, uint32_t keep) {
-  if (cut) {
+// Largest of a row's 32 scores at tensor-memory column `ts`; with kCut those not kept become
+// -infinity there.
+template <bool kCut>
+__device__ __forceinline__ float row_max(uint32_t ts, uint32_t keep) {
+  uint32_t w[32];
+  tc::ld32(ts, w);
+  tc::wait_ld();
+  if (kCut) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) w[i] = keep >> i & 1u ? w[i] : 0xff800000u;
+    tc::st32(ts, w);
   }
   float t[4];
 #pragma unroll
@@ -175,10 +181,12 @@ __device__ __forceinline__ float row_max(uint32_t (&w)[32], bool cut, uint32_t k
   return max3(fmaxf(t[0], t[1]), t[2], t[3]);
 }
 
-// Weights 2^(score * sl - mu) of a row's 32 scores, written as f16 pairs to tensor-memory column `tp`
-// (whose scores have been read); returns their sum.
-__device__ __forceinline__ float weights(const uint32_t (&w)[32], uint32_t tp, float sl, float mu) {
-  uint32_t pk[16];
+// Weights 2^(score * sl - mu) of a row's 32 scores at column `ts`, written as f16 pairs to column
+// `tp` (whose scores have been read); returns their sum.
+__device__ __forceinline__ float weights(uint32_t ts, uint32_t tp, float sl, float mu) {
+  uint32_t w[32], pk[16];
+  tc::ld32(ts, w);
+  tc::wait_ld();
   const uint64_t sl2 = pack2(sl, sl), mu2 = pack2(-mu, -mu);
   uint64_t ps[2] = {0ull, 0ull};
 #pragma unroll
@@ -560,8 +568,8 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
       const int64_t* mask = p.tree_mask ? p.tree_mask + (row_ok ? trow : int64_t(e.q0)) * p.mask_stride : nullptr;  // (idle rows: any)
       const uint64_t word0 = mask ? uint64_t(__ldg(mask)) : 0;
       float m_ref = -INFINITY, l_run = 0.f, sl = 0.f;
-      // this warpgroup's part of a step: half of S's columns, whose scores stay in registers, or all of them
-      const int half = it.nt == 1 ? wg : 0, halves = it.nt;
+      // this warpgroup's part of a step: its columns of S, 32 at a time
+      const int half = it.nt == 1 ? wg : 0, chunks = it.nt == 1 ? 2 : 4;
       for (int j = it.j0; j < it.j1; ++j, ++steps) {
         const int x = x0 + (j - it.j0) * it.nt + qt;
         const int pos = it.q.base + j * kBN;
@@ -571,25 +579,20 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
         if (warp_ok) {
           if (j == it.j0) sl = st->qf[(qc + qt) % kQueryTiles][r];
           float mx = -INFINITY;
-          const bool cut = it.cut(j);
-          uint64_t k[2] = {0ull, 0ull};
-          if (cut) {
+          if (it.cut(j)) {
+            uint64_t k[2];
             tile_bits(e, pos, mask, word0, k);
             if (half) k[0] = k[1];
-          }
-          uint32_t wa[32], wb[32];
 #pragma unroll 1
-          for (int c = 0; c < halves; ++c) {
-            tc::ld32(tS + 64 * c, wa);
-            tc::ld32(tS + 64 * c + 32, wb);
-            tc::wait_ld();
-            mx = max3(mx, row_max(wa, cut, uint32_t(k[0])), row_max(wb, cut, uint32_t(k[0] >> 32)));
-            k[0] = k[1];
-            if (halves == 2 && cut) {
-              tc::st32(tS + 64 * c, wa);
-              tc::st32(tS + 64 * c + 32, wb);
-              tc::wait_st();
+            for (int c = 0; c < chunks; ++c) {
+              mx = fmaxf(mx, row_max<true>(tS + 32 * c, uint32_t(k[0])));
+              k[0] = k[0] >> 32 | k[1] << 32;
+              k[1] >>= 32;
             }
+            tc::wait_st();
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < chunks; ++c) mx = fmaxf(mx, row_max<false>(tS + 32 * c, 0u));
           }
           mx *= sl;
           const bool first = m_ref == -INFINITY;
@@ -615,15 +618,7 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
           const float mu = m_ref == -INFINITY ? 0.f : m_ref - kTop;
           float sum = 0.f;
 #pragma unroll 1
-          for (int c = 0; c < halves; ++c) {
-            if (halves == 2) {
-              tc::ld32(tS + 64 * c, wa);
-              tc::ld32(tS + 64 * c + 32, wb);
-              tc::wait_ld();
-            }
-            sum += weights(wa, tS + 32 * c, sl, mu);
-            sum += weights(wb, tS + 32 * c + 16, sl, mu);
-          }
+          for (int c = 0; c < chunks; ++c) sum += weights(tS + 32 * c, tS + 16 * c, sl, mu);
           l_run += sum;
           tc::wait_st();
         }
