@@ -44,16 +44,23 @@ __device__ __forceinline__ float scale1(uint32_t byte) {
   return __low2float(*reinterpret_cast<const __half2*>(&h));
 }
 
+// A cache's factor f, and division by 6 f.  (Made once where it serves all rows: the reciprocal in it
+// costs more than the rest of a group's scale.)
+struct Factor {
+  float f;
+  DivRn six;
+  __device__ __forceinline__ explicit Factor(float x) : f(x), six(6.f * x) {}
+};
+
 // The scale of a group whose largest magnitude has the bits `top`, and what its elements are
-// multiplied by.  `f`: the cache's factor, `six`: division by 6 f.  A factor that puts the step
-// out of the normal numbers stores zeros.
+// multiplied by.  A factor that puts the step out of the normal numbers stores zeros.
 struct Group {
   uint32_t byte;
   float inverse;  // 0: all codes are 0
-  __device__ __forceinline__ Group(uint32_t top, float f, const DivRn& six) {
-    const float g = fminf(six(__uint_as_float(top)), 448.f);
+  __device__ __forceinline__ Group(uint32_t top, const Factor& x) {
+    const float g = fminf(x.six(__uint_as_float(top)), 448.f);
     byte = __nv_cvt_float_to_fp8(g, __NV_SATFINITE, __NV_E4M3);
-    const float step = __fmul_rn(scale1(byte), f);
+    const float step = __fmul_rn(scale1(byte), x.f);
     const bool number = step >= 0x1p-126f && step <= 0x1p126f;
     inverse = number ? __frcp_rn(step) : 0.f;
     if (!number) byte = 0;

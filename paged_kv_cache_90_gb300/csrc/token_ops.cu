@@ -202,13 +202,11 @@ __device__ __forceinline__ int64_t axis_position(const TokenParams& p, int64_t t
 }
 
 // A row's columns 8 l .. 8 l + 7 to a 4-bit cache: `codes` and `scales` are the row's first bytes,
-// `f` the cache's factor.  All lanes of the row call it (`live`: the row is stored); a group is
-// two lanes', and its scales leave as words of four.
-template <int D>
-__device__ __forceinline__ void store_e2m1(const float (&x)[8], uint32_t top, float f, unsigned char* codes,
+// `top` the bits of its group's largest magnitude.  All lanes of the row call it (`live`: the row is
+// stored); a group is two lanes', and its scales leave as words of four.
+__device__ __forceinline__ void store_e2m1(const float (&x)[8], uint32_t top, const e2m1::Factor& f, unsigned char* codes,
                                            unsigned char* scales, int l, bool live) {
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  const e2m1::Group g(top, f, DivRn(__fmul_rn(6.f, f)));
+  const e2m1::Group g(top, f);
   uint32_t four = g.byte << (8 * ((l >> 1) & 3));
   four |= __shfl_xor_sync(0xffffffffu, four, 2);
   four |= __shfl_xor_sync(0xffffffffu, four, 4);
@@ -217,12 +215,8 @@ __device__ __forceinline__ void store_e2m1(const float (&x)[8], uint32_t top, fl
   if ((l & 7) == 0) *reinterpret_cast<uint32_t*>(scales + (l >> 1)) = four;
 }
 
-__device__ __forceinline__ uint32_t top_bits8(const float (&x)[8]) {
-  uint32_t top = 0u;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-  return top;
-}
+// The bits of a group's largest magnitude: row_top of a lane's pair.
+__device__ __forceinline__ uint32_t group_top(const float (&x)[8]) { return row_top_bits<2>(x); }
 
 __device__ __forceinline__ float cache_factor(const CacheWriteParams& w, bool is_v, int h) {
   const float* hs = is_v ? w.v_head_scales : w.k_head_scales;
@@ -379,10 +373,10 @@ __global__ void __launch_bounds__(32 * kWarps) token_write_kernel(const __grid_c
         __syncwarp();
         const float y[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         const bool stored = live && !is_q && in_cache;
-        store_e2m1<D>(y, top_bits8(y), stored ? cache_factor(p.w, is_v, h) : 1.f,
-                      static_cast<unsigned char*>(dst) + blk * p.w.cs_block + h * p.w.cs_head + off * (D / 2),
-                      (is_v ? p.v_group_scales : p.k_group_scales) + blk * p.ts_block + h * p.ts_head + off * (D / 16), l,
-                      stored);
+        store_e2m1(y, group_top(y), e2m1::Factor(stored ? cache_factor(p.w, is_v, h) : 1.f),
+                   static_cast<unsigned char*>(dst) + blk * p.w.cs_block + h * p.w.cs_head + off * (D / 2),
+                   (is_v ? p.v_group_scales : p.k_group_scales) + blk * p.ts_block + h * p.ts_head + off * (D / 16), l,
+                   stored);
       } else {
         const int64_t at = blk * p.w.cs_block + h * p.w.cs_head + int64_t(off) * D;
         if (p.w.cache_dtype == kI8) {
@@ -426,6 +420,7 @@ __global__ void __launch_bounds__(32 * kWarps) token_quantize_kernel(const __gri
   const int per = (passes + int(gridDim.y) - 1) / int(gridDim.y);
   const int first = int(blockIdx.y) * per, last = min(first + per, passes);
   const int64_t from = t * p.w.src_stride_t;
+  const e2m1::Factor k_factor(type == kE2M1 ? p.w.k_scale : 1.f), v_factor(type == kE2M1 ? p.w.v_scale : 1.f);
   for (int p0 = first; p0 < last; p0 += kBatch) {
     Raw<Src> raw[kBatch];
 #pragma unroll
@@ -450,11 +445,14 @@ __global__ void __launch_bounds__(32 * kWarps) token_quantize_kernel(const __gri
       const bool is_v = p0 + u >= tensor;
       const int h = (p0 + u - (is_v ? tensor : 0)) * kRows + sub;
       if constexpr (type == kE2M1) {
+        const uint32_t top = raw[u].template row_top<2>();  // of the group: a lane's pair
         float x[8];
         raw[u].expand(x);
-        store_e2m1<D>(x, top_bits8(x), h < hk ? cache_factor(p.w, is_v, h) : 1.f,
-                      static_cast<unsigned char*>(is_v ? p.w.value_cache : p.w.key_cache) + to + h * p.w.cs_head,
-                      (is_v ? p.v_group_scales : p.k_group_scales) + scale_to + h * p.ts_head, l, h < hk);
+        e2m1::Factor f = is_v ? v_factor : k_factor;
+        if (is_v ? p.w.v_head_scales != nullptr : p.w.k_head_scales != nullptr)
+          f = e2m1::Factor(h < hk ? cache_factor(p.w, is_v, h) : 1.f);
+        store_e2m1(x, top, f, static_cast<unsigned char*>(is_v ? p.w.value_cache : p.w.key_cache) + to + h * p.w.cs_head,
+                   (is_v ? p.v_group_scales : p.k_group_scales) + scale_to + h * p.ts_head, l, h < hk);
         continue;
       }
       const uint32_t top = raw[u].template row_top<kLanes>();
