@@ -622,12 +622,12 @@ pkv_status pkv_copy_cache_blocks(const pkv_tensor* const* caches, int32_t num_ca
  * outside `keep` PKV_DEVERR_CONTEXT_LEN; table entries out of range (of tokens that move)
  * PKV_DEVERR_TABLE_ENTRY.
  *
- * caches         as for pkv_copy_cache_blocks, none of them twice.  The blocks of drafted
+ * caches         as for pkv_copy_cache_blocks, sharing no memory with each other.  The blocks of drafted
  *                positions belong to their sequence alone (no other table has them).
  * block_tables   [num_seqs, max_blocks_per_seq] int32; context_lens [num_seqs] int32;
  * query_start_loc [num_seqs + 1] int32, contiguous, non-decreasing.
  * keep           [num_tokens] int32, contiguous; keep_counts [num_seqs] int32, contiguous.
- * new_lens       [num_seqs] int32, contiguous, not context_lens itself; or NULL.
+ * new_lens       [num_seqs] int32, contiguous, sharing no memory with the other arrays; or NULL.
  */
 pkv_status pkv_keep_tokens(const pkv_tensor* const* caches, int32_t num_caches, const pkv_tensor* block_tables,
                            const pkv_tensor* context_lens, const pkv_tensor* query_start_loc,

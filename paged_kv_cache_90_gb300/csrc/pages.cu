@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kKeepThreads) keep_tokens_kernel(const __grid_
     return;
   }
   if (first_cache && tid == 0 && k.new_lens) k.new_lens[s] = P + kept;
+  if (int(blockIdx.y) >= p.num_caches) return;
   const PageCache c = p.caches[blockIdx.y];
   const int per_head = c.row_bytes / c.vec, columns = c.heads * per_head;
   for (int i0 = 0; i0 < kept; i0 += kKeepBatch) {
@@ -174,8 +175,8 @@ cudaError_t launch_copy_pages(const PagesParams& p, const int64_t* pairs, int64_
 }
 
 cudaError_t launch_keep_tokens(const PagesParams& p, const KeepParams& k, cudaStream_t stream) {
-  return launch<PagesParams, KeepParams>(keep_tokens_kernel, dim3(unsigned(k.num_seqs), unsigned(p.num_caches)), kKeepThreads,
-                                         stream, p, k);
+  const dim3 grid(unsigned(k.num_seqs), unsigned(p.num_caches ? p.num_caches : 1));
+  return launch<PagesParams, KeepParams>(keep_tokens_kernel, grid, kKeepThreads, stream, p, k);
 }
 
 }  // namespace pkv

@@ -73,6 +73,14 @@ pkv_status check_i32(const pkv_tensor* t, const char* name, int64_t n) {
   return PKV_OK;
 }
 
+// Whether int32 arrays share memory (`a` contiguous; `b` may be a table).
+bool overlap(const pkv_tensor* a, const pkv_tensor* b) {
+  if (a->shape[0] == 0 || b->shape[0] == 0) return false;
+  const int64_t n = (b->shape[0] - 1) * b->stride[0] + (b->ndim == 2 ? b->shape[1] : 1);
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a->data), y = reinterpret_cast<uintptr_t>(b->data);
+  return x < y + 4 * n && y < x + 4 * a->shape[0];
+}
+
 }  // namespace
 }  // namespace pkv
 
@@ -127,8 +135,10 @@ pkv_status pkv_keep_tokens(const pkv_tensor* const* caches, int32_t num_caches, 
   if (caches[0]->shape[2] != block_size) return fail(PKV_ERR_INVALID_ARG, "block_size must match the caches");
   if (block_tables->shape[1] != max_blocks_per_seq || max_blocks_per_seq < 1)
     return fail(PKV_ERR_INVALID_ARG, "block_tables must be [num_seqs, max_blocks_per_seq]");
-  if (new_lens && S > 0 && new_lens->data == context_lens->data)
-    return fail(PKV_ERR_INVALID_ARG, "new_lens must not be context_lens (every block of the launch reads that)");
+  if (new_lens)
+    for (const pkv_tensor* in : {context_lens, query_start_loc, keep, keep_counts, block_tables})
+      if (overlap(new_lens, in))
+        return fail(PKV_ERR_INVALID_ARG, "new_lens must share no memory with an input (all blocks of the launch read them)");
   if (int64_t(max_blocks_per_seq) * block_size > (int64_t(1) << 30))
     return fail(PKV_ERR_UNSUPPORTED, "max context above 2^30 tokens");
   if (S > 65535 || keep->shape[0] > (1 << 28))
@@ -163,7 +173,7 @@ pkv_status pkv_keep_tokens(const pkv_tensor* const* caches, int32_t num_caches, 
   for (int first = 0; first < num_caches && e == cudaSuccess;) {
     first = fill(caches, num_caches, first, &p);
     choose_vectors(&p, true);
-    if (!p.num_caches) continue;
+    if (!p.num_caches && !k.report) continue;  // (caches without heads: new_lens is written all the same)
     e = launch_keep_tokens(p, k, cs);
     k.report = false;
   }

@@ -93,7 +93,8 @@ class FourBit(Case):
         u = 2.0 ** -24
         L = max(self.lens + [1])
         half = self.q.dtype == torch.bfloat16
-        rel = (2.0 ** -11 if half else 0.0) + 2 * ((self.d + 8) * u * dz + 2.0 ** -22) + L * u
+        # a score is off by at most (d + 8) u |scale| sum |q| |K|, whatever the scale's sign (dz has it)
+        rel = (2.0 ** -11 if half else 0.0) + 2 * ((self.d + 8) * u * dz.abs() + 2.0 ** -22) + L * u
         V = torch.where(torch.isfinite(self.V64), self.V64.abs(), 0.0).amax((0, 2, 3))  # [hk]
         floor = L * 2.0 ** -31 * V.repeat_interleave(self.group)[None, :, None] if half else 0.0
         fp = rel * wabs + floor
