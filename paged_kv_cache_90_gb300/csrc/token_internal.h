@@ -77,7 +77,7 @@ struct TreeSplit {
     int nodes, row0, kvh, last;
   };
   static constexpr size_t kMaxSms = 240;
-  static constexpr size_t kMaxGrid = 4 * kMaxSms;                     // blocks
+  static constexpr size_t kMaxGrid = 3 * kMaxSms;                     // blocks
   static constexpr size_t kHeader = kWorkspaceHeader + kMaxGrid * sizeof(Tail);  // (a multiple of 256)
   int grid;
   int rows;     // rows of a part's slot

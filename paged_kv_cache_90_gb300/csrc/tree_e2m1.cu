@@ -380,6 +380,7 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
         next_kvh = it.kvh;
         if (isv && lane == 0)
           st->item[w4][items & 7] = {t_left, pos0, it.q.e.L, it.q.e.lo, it.q.e.P, (it.q.e.P - it.q.base) / kBN - it.j0};
+        __syncwarp();  // (the other lanes read it later)
         ++items;
         it.next(p, sp, rg);
       }
