@@ -458,9 +458,9 @@ pkv_status pkv_rotary_axes_and_cache(const pkv_tensor* query_out, const pkv_tens
  *   G = a / (6 f), at most 448, rounded to e4m3          (the group's scale)
  *   code = x * (1 / (G f)), at most 6 in magnitude, rounded to e2m1
  * both to nearest, ties to even.  An element is off by at most a / 5.  Values beyond 2688 f are
- * cut off there and groups below 0.0058 f vanish (G = 0), so f is set where values are far from 1.  A G f below
- * 2^-126 or above 2^126 is stored as G = 0 with codes of 0, a group holding an infinity or a
- * NaN as G = NaN with codes of 0.
+ * cut off there and groups below 0.0058 f vanish (G = 0), so f is set where values are far from 1.
+ * A G f below 2^-126 or above 2^126 is stored as G = 0 with codes of 0, a group holding an infinity
+ * or a NaN as G = NaN with codes of 0.
  *
  * key, value           as for pkv_reshape_and_cache, f32 or bf16.
  * key_cache,
@@ -479,10 +479,12 @@ pkv_status pkv_quantize_and_cache(const pkv_tensor* key, const pkv_tensor* value
  *
  * For token t with slot = slot_mapping[t] >= 0: key[t, h, :] = the values that the cache
  * holds at the slot (code * scale in binary32 for an 8-bit cache, code * (G * f) for a 4-bit
- * one), rounded once to key's dtype; V alike.  slot < 0 leaves the token's rows as they were.  Reading a token and
- * writing it elsewhere moves it: bit for bit between caches of one 16- or 32-bit type
- * read in that type; for a token-scaled cache read in f32 the codes are the same and the
- * scale within one unit in its last place.  Slots may repeat.
+ * one), rounded once to key's dtype; V alike.  slot < 0 leaves the token's rows as they were.
+ * Reading a token and writing it elsewhere moves it: bit for bit between caches of one 16- or
+ * 32-bit type read in that type; for a token-scaled cache read in f32 the codes are the same and
+ * the scale within one unit in its last place.  (Not for a 4-bit cache, where a group whose largest
+ * code is below 6 gets another scale: its pages and tokens are moved by the copies below.)  Slots
+ * may repeat.
  *
  * key, value           [num_tokens, num_kv_heads, head_dim] f32 or bf16 (written), same
  *                      dtype, shape and strides, last dim contiguous, 16-byte aligned.
@@ -508,10 +510,10 @@ pkv_status pkv_read_cache(const pkv_tensor* key, const pkv_tensor* value, const 
  * Over a 4-bit cache keys and values are taken exactly, and with bf16 queries a softmax weight is
  * rounded once to 16 bits: by at most 2^-11 of itself, or, if it is small, by 2^-31 of the largest
  * in its row.
- * Over an int8 cache, with bf16 queries a softmax weight times its value scale is rounded once to 16 bits: by at
- * most 2^-11 of itself, or, if it is small, by 2^-31 of the largest such product in its row
- * (value scales below 2^-80 count as 2^-80 there; above 2^90 sums lose bits).  With f32 queries
- * it stays in binary32.
+ * Over an int8 cache, with bf16 queries a softmax weight times its value scale is rounded once to
+ * 16 bits: by at most 2^-11 of itself, or, if it is small, by 2^-31 of the largest such product in
+ * its row (value scales below 2^-80 count as 2^-80 there; above 2^90 sums lose bits).  With f32
+ * queries weights stay in binary32.
  */
 pkv_status pkv_paged_attention_decode_quantized(const pkv_tensor* out, const pkv_tensor* query,
                                                 const pkv_tensor* key_cache, const pkv_tensor* value_cache,

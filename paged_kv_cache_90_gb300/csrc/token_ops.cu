@@ -12,7 +12,9 @@
 // 71 us, 5.7 TB/s (a block per token with the cosines in shared memory: 175 us); quantising
 // write of 16384 tokens of 2 x 8 heads 31 us, read back into f32 26 us (168 MB, 6.4 TB/s).  The
 // write is held back by its instructions, 190 for 8 columns of two rows, issued in four of five
-// cycles.
+// cycles.  Into a 4-bit cache the same write takes 21 us (86 MB; instructions in three of four
+// cycles), read back into f32 25 us (153 MB, 6 TB/s); the rotary write with three position axes in
+// turn over the pairs 73 us, 5.6 TB/s.
 #include "device_common.cuh"
 #include "e2m1_codes.cuh"
 #include "token_internal.h"

@@ -1,7 +1,7 @@
 // tree_core.cu — attention of drafted trees and decode over a token-scaled cache on the
 // CUDA cores: the path for what the tensor-core kernels do not take (f32 queries, f32 and
-// e4m3 caches, bf16 caches of block sizes 2 and 4, 4-bit caches whose blocks' scales are not 16
-// aligned bytes a head, groups of more than 128 query heads, a scale that is not above zero, rows
+// e4m3 caches, bf16 caches of block sizes 2 and 4, 4-bit caches with strides of 2^32 bytes and more,
+// groups of more than 128 query heads, a scale that is not above zero over a bf16 cache, rows
 // not aligned to 16 bytes).
 //
 // One thread block per (query row, query head).  Its four warps take 32 keys at a time in

@@ -15,10 +15,18 @@
 //
 // K and V are widened by a warpgroup each: a warp loads 32 positions of a tile into registers, a tile
 // ahead, and code times group scale is an f16 number exactly (e2m1_codes.cuh).  (With asynchronous
-// copies into shared memory a warp spent 500 clocks a tile on issuing them and 150 on reading them.)  A query row is scaled by the power of two that brings its
-// largest element to 2^14, so its bf16 values are exact down to 2^-29 of that.  A weight is rounded
-// to f16, half a step, 2^-11, down to 2^-21 of the row's largest, 2^-32 of that below.  Scores,
-// maximum, sum and output are binary32.
+// copies into shared memory a warp spent 500 clocks a tile on issuing them and 150 on reading them.)
+// A query row is scaled by the power of two that brings its largest element to 2^14, so its bf16
+// values are exact down to 2^-29 of that.  A weight is rounded to f16, half a step, 2^-11, down to
+// 2^-21 of the row's largest, 2^-32 of that below.  Scores, maximum, sum and output are binary32.
+//
+// 32 trees of 8 to 32 nodes over 1000 to 8192 positions, 32 : 8 heads of 128 (182 MB): 108 us; on the
+// CUDA cores 8 ms.  Neither memory (21 % of the time) nor the tensor cores (36 %) bound it but a tile's
+// chain: about 2700 clocks of products (1240), weights (1024 of the exponentials) and widening, of
+// which two tiles' buffers hide no more than a part.  Without the softmax it takes 86 us, without the
+// widening 95, with a single product a step 71.  Two warpgroups on one row tile's keys took 120 us
+// down to 108.  Tried without gain: a second MMA warp (114 us), a half tile's scores kept in
+// registers between maximum and weights (110), waits that spin (129).
 //
 // Nothing that a row does not see reaches it: hidden scores become -infinity, V rows outside the
 // context are widened as zeros, and so are groups of drafted nodes whose scale is a NaN: the rows
@@ -71,7 +79,7 @@ enum Bar { kQFull = 0, kQEmpty = 2, kKFull = 4, kKEmpty = 6, kVFull = 8, kVEmpty
            kODone = 20, kOFree = 24, kStat = 25, kDrain = 27, kNumBars = 28 };
 
 constexpr int kQueryTiles = 4;  // row tiles whose score factors are kept: those of two items
-constexpr int kBadItems = 8;    // items whose bad rows are kept
+constexpr int kBadItems = 8;    // items whose bad rows are kept: the widening is up to three ahead
 
 struct State {
   uint64_t bars[kNumBars];
