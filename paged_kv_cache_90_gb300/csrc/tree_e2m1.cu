@@ -26,7 +26,10 @@
 // which two tiles' buffers hide no more than a part.  Without the softmax it takes 86 us, without the
 // widening 95, with a single product a step 71.  Two warpgroups on one row tile's keys took 120 us
 // down to 108.  Tried without gain: a second MMA warp (114 us), a half tile's scores kept in
-// registers between maximum and weights (110), waits that spin (129).
+// registers between maximum and weights (110) and S given back as soon as they are there (116), waits
+// that spin (129), one lane that waits for its warp (113), a step's waits at once (110), four MMAs an
+// election (110).  The MMA warp's own way through a tile, 2000 to 2500 clocks between the other roles'
+// instructions, is what the others wait for.
 //
 // Nothing that a row does not see reaches it: hidden scores become -infinity, V rows outside the
 // context are widened as zeros, and so are groups of drafted nodes whose scale is a NaN: the rows
