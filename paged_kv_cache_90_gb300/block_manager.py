@@ -100,6 +100,7 @@ class SequenceBlocks:
     blocks: List[int] = field(default_factory=list)
     length: int = 0
     released: int = 0  # leading table entries released after they left a sliding window
+    window: int = 0  # that window's positions (of the latest release)
 
     def slot(self, pos: int, block_size: int) -> int:
         if not 0 <= pos < len(self.blocks) * block_size:
@@ -145,7 +146,7 @@ class BlockManager:
         for b in p.blocks:
             if b != RELEASED:
                 self.alloc.incref(b)
-        self.seqs[child_id] = SequenceBlocks(list(p.blocks), p.length, p.released)
+        self.seqs[child_id] = SequenceBlocks(list(p.blocks), p.length, p.released, p.window)
 
     def free_sequence(self, seq_id) -> None:
         s = self.seqs.pop(seq_id)
@@ -153,14 +154,20 @@ class BlockManager:
             if b != RELEASED:
                 self.alloc.decref(b)
 
-    def release_outside_window(self, seq_id, window: int) -> List[int]:
+    def release_outside_window(self, seq_id, window: int, drafted: int = 0) -> List[int]:
         """Sliding window of ``window`` positions: give back every block whose
         positions all lie before the last ``window`` ones (attention never reads them
         again); their table entries become RELEASED.  Returns the released ids
         (ya.zerocoder.ru, section "Где подход не решает задачу": a limited attention
-        window frees the blocks that have left it)."""
+        window frees the blocks that have left it).  ``drafted``: how many of the last
+        tokens :meth:`truncate` may still take away; the window of a sequence without
+        them starts earlier, and what it reads is kept."""
+        if drafted < 0:
+            raise ValueError("drafted must not be negative")
         s = self.seqs[seq_id]
-        first_kept = max(0, s.length - int(window)) // self.bs  # block holding the window's first position
+        s.window = int(window)
+        # the block holding the window's first position
+        first_kept = max(0, s.length - int(drafted) - int(window)) // self.bs
         out = []
         for i in range(s.released, min(first_kept, len(s.blocks))):
             self.alloc.decref(s.blocks[i])
@@ -171,11 +178,15 @@ class BlockManager:
 
     def truncate(self, seq_id, length: int) -> List[int]:
         """Shorten a sequence to its first ``length`` tokens (drafted tokens that were not
-        accepted) and give back the blocks behind them; returns their ids."""
+        accepted) and give back the blocks behind them; returns their ids.  A shorter
+        sequence's sliding window starts earlier: ValueError where it would reach a block that
+        :meth:`release_outside_window` gave back (its ``drafted`` keeps such blocks)."""
         s = self.seqs[seq_id]
         kept = blocks_needed(length, self.bs)
-        if not 0 <= length <= s.length or (s.released and kept <= s.released):
+        if not 0 <= length <= s.length:
             raise ValueError(f"sequence {seq_id} of {s.length} tokens cannot shrink to {length}")
+        if s.released and (kept <= s.released or max(0, length - s.window) // self.bs < s.released):
+            raise ValueError(f"sequence {seq_id} of {length} tokens would read blocks that left its window")
         out = s.blocks[kept:]
         del s.blocks[kept:]
         s.length = length
