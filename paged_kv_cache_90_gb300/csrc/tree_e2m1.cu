@@ -246,103 +246,103 @@ tree_e2m1_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ T
   const uint32_t tmem = st->tmem;
   const Range* rg = &st->range;
 
-  if (warp == 1) {
+  // (a warpgroup takes its registers together, by one instruction, and its roles part behind it)
+  if (warp < 4) {
     less_registers<kRegsControl>();
-    Walk it;
-    it.start(p, sp, rg);
-    // ---- MMAs (a warp, see umma.cuh): S of a step, then P V of the step before it -------------------
-    // (Counters and descriptors come from values that the compiler knows to be the warp's: a lane's
-    // own would be moved to uniform registers for every MMA.)
-    constexpr uint32_t idS = idesc_f16(kBM, kBN, 0, 0), idO = idesc_f16(kBM, D, 0, 1);
-    constexpr uint64_t kOp = C::kOpBytes >> 4, kHalf = C::kHalfBytes >> 4;  // (descriptors hold addresses / 16)
-    auto one = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-    const uint32_t base = one(int(sbase)), tm = one(int(tmem));
-    const uint64_t qdesc = tc::desc_sw128(base + C::kQ, 16, 1024), kdesc = tc::desc_sw128(base + C::kK, 16, 1024);
-    const uint64_t vdesc = tc::desc_sw128(base + C::kV, C::kHalfBytes, 1024);
-    int xs = 0, tiles = 0, q = 0, item = 0, steps[2] = {0, 0};  // (steps: of the warpgroups)
-    // the step whose P V is next: its tile, and what it is to the one warpgroup that has it, or to both
-    // (-1); whether it is its warpgroup's first of the item, and the last of its tile
-    int p_wg = 0, p_step[2] = {0, 0}, p_tile = 0, p_item = 0;
-    bool p_first = false, p_last = false, p_due = false, ok = true;
-    auto products = [&]() {
-      const int x = xs - 1;
-      const uint64_t vd = vdesc + (p_tile & 1) * kOp;
-      const uint32_t ts = tm + C::kS + (x & 1) * kBN;
-      ok = wait_warp(st, kVFull + (p_tile & 1), uint32_t(p_tile >> 1) & 1u) &&
-           (!p_first || p_item == 0 || wait_warp(st, kOFree, uint32_t(p_item - 1) & 1u));
-      if (p_wg >= 0) {
-        const int w = p_wg, n = w ? p_step[1] : p_step[0];
-        ok = ok && wait_warp(st, kPFull + 2 * w + (n & 1), uint32_t(n >> 1) & 1u);
-        if (!ok) return;
-        tc::fence_after();
-#pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk)
-          umma::mma_ts(tm + C::kO + w * D, ts + 8 * kk, vd + kk * (16 * 128 >> 4), idO, (!p_first || kk > 0) ? 1u : 0u);
-        umma::commit(&st->bars[kODone + 2 * w + (n & 1)]);
-      } else {
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {  // a half of the keys each
-          const int n = p_step[w];
+    if (warp == 1) {
+      Walk it;
+      it.start(p, sp, rg);
+      // ---- MMAs (a warp, see umma.cuh): S of a step, then P V of the step before it -------------------
+      // (Counters and descriptors come from values that the compiler knows to be the warp's: a lane's
+      // own would be moved to uniform registers for every MMA.)
+      constexpr uint32_t idS = idesc_f16(kBM, kBN, 0, 0), idO = idesc_f16(kBM, D, 0, 1);
+      constexpr uint64_t kOp = C::kOpBytes >> 4, kHalf = C::kHalfBytes >> 4;  // (descriptors hold addresses / 16)
+      auto one = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+      const uint32_t base = one(int(sbase)), tm = one(int(tmem));
+      const uint64_t qdesc = tc::desc_sw128(base + C::kQ, 16, 1024), kdesc = tc::desc_sw128(base + C::kK, 16, 1024);
+      const uint64_t vdesc = tc::desc_sw128(base + C::kV, C::kHalfBytes, 1024);
+      int xs = 0, tiles = 0, q = 0, item = 0, steps[2] = {0, 0};  // (steps: of the warpgroups)
+      // the step whose P V is next: its tile, and what it is to the one warpgroup that has it, or to both
+      // (-1); whether it is its warpgroup's first of the item, and the last of its tile
+      int p_wg = 0, p_step[2] = {0, 0}, p_tile = 0, p_item = 0;
+      bool p_first = false, p_last = false, p_due = false, ok = true;
+      auto products = [&]() {
+        const int x = xs - 1;
+        const uint64_t vd = vdesc + (p_tile & 1) * kOp;
+        const uint32_t ts = tm + C::kS + (x & 1) * kBN;
+        ok = wait_warp(st, kVFull + (p_tile & 1), uint32_t(p_tile >> 1) & 1u) &&
+             (!p_first || p_item == 0 || wait_warp(st, kOFree, uint32_t(p_item - 1) & 1u));
+        if (p_wg >= 0) {
+          const int w = p_wg, n = w ? p_step[1] : p_step[0];
           ok = ok && wait_warp(st, kPFull + 2 * w + (n & 1), uint32_t(n >> 1) & 1u);
           if (!ok) return;
           tc::fence_after();
 #pragma unroll
-          for (int kk = 0; kk < kBN / 32; ++kk)
-            umma::mma_ts(tm + C::kO + w * D, ts + 64 * w + 8 * kk, vd + (4 * w + kk) * (16 * 128 >> 4), idO,
-                         (!p_first || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            umma::mma_ts(tm + C::kO + w * D, ts + 8 * kk, vd + kk * (16 * 128 >> 4), idO, (!p_first || kk > 0) ? 1u : 0u);
           umma::commit(&st->bars[kODone + 2 * w + (n & 1)]);
-        }
-      }
-      if (p_last) umma::commit(&st->bars[kVEmpty + (p_tile & 1)]);
-      p_due = false;
-    };
-    for (; ok && it.valid(); it.next(p, sp, rg), ++item) {
-      const int nt = one(it.nt), count = one(it.j1 - it.j0) * nt;
-      for (int i = 0; ok && i < count; ++i) {
-        const int qt = nt == 2 ? i & 1 : 0, qs = (q + qt) & 1, use = (q + qt) >> 1;
-        // (an item's queries may be late: the products do not wait for them)
-        if (i == 0 && p_due && !__all_sync(0xffffffffu, test_wait(&st->bars[kQFull + qs], uint32_t(use) & 1u))) products();
-        if (qt == 0) ok = ok && wait_warp(st, kKFull + (tiles & 1), uint32_t(tiles >> 1) & 1u);
-        if (i < nt) ok = ok && wait_warp(st, kQFull + qs, uint32_t(use) & 1u);
-        if (!ok) break;
-        tc::fence_after();
-        const uint64_t qd = qdesc + qs * kOp, kd = kdesc + (tiles & 1) * kOp;
-        const uint32_t ts = tm + C::kS + (xs & 1) * kBN;
+        } else {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma::mma_ss(ts, qd + (kk >> 2) * kHalf + (kk & 3) * 2, kd + (kk >> 2) * kHalf + (kk & 3) * 2, idS, kk > 0 ? 1u : 0u);
-        if (nt == 1 || qt == 0) umma::commit(&st->bars[kSFull + (steps[0] & 1)]);
-        if (nt == 1 || qt == 1) umma::commit(&st->bars[kSFull + 2 + (steps[1] & 1)]);
-        if (qt == nt - 1) umma::commit(&st->bars[kKEmpty + (tiles & 1)]);
-        if (i >= count - nt) umma::commit(&st->bars[kQEmpty + qs]);
-        if (p_due) products();
-        p_due = true;
-        p_wg = nt == 1 ? -1 : qt;
-        p_step[0] = steps[0];
-        p_step[1] = steps[1];
-        p_tile = tiles;
-        p_item = item;
-        p_first = i < nt;
-        p_last = qt == nt - 1;
-        ++xs;
-        if (nt == 1 || qt == 0) ++steps[0];
-        if (nt == 1 || qt == 1) ++steps[1];
-        if (qt == nt - 1) ++tiles;
+          for (int w = 0; w < 2; ++w) {  // a half of the keys each
+            const int n = p_step[w];
+            ok = ok && wait_warp(st, kPFull + 2 * w + (n & 1), uint32_t(n >> 1) & 1u);
+            if (!ok) return;
+            tc::fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kBN / 32; ++kk)
+              umma::mma_ts(tm + C::kO + w * D, ts + 64 * w + 8 * kk, vd + (4 * w + kk) * (16 * 128 >> 4), idO,
+                           (!p_first || kk > 0) ? 1u : 0u);
+            umma::commit(&st->bars[kODone + 2 * w + (n & 1)]);
+          }
+        }
+        if (p_last) umma::commit(&st->bars[kVEmpty + (p_tile & 1)]);
+        p_due = false;
+      };
+      for (; ok && it.valid(); it.next(p, sp, rg), ++item) {
+        const int nt = one(it.nt), count = one(it.j1 - it.j0) * nt;
+        for (int i = 0; ok && i < count; ++i) {
+          const int qt = nt == 2 ? i & 1 : 0, qs = (q + qt) & 1, use = (q + qt) >> 1;
+          // (an item's queries may be late: the products do not wait for them)
+          if (i == 0 && p_due && !__all_sync(0xffffffffu, test_wait(&st->bars[kQFull + qs], uint32_t(use) & 1u))) products();
+          if (qt == 0) ok = ok && wait_warp(st, kKFull + (tiles & 1), uint32_t(tiles >> 1) & 1u);
+          if (i < nt) ok = ok && wait_warp(st, kQFull + qs, uint32_t(use) & 1u);
+          if (!ok) break;
+          tc::fence_after();
+          const uint64_t qd = qdesc + qs * kOp, kd = kdesc + (tiles & 1) * kOp;
+          const uint32_t ts = tm + C::kS + (xs & 1) * kBN;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma::mma_ss(ts, qd + (kk >> 2) * kHalf + (kk & 3) * 2, kd + (kk >> 2) * kHalf + (kk & 3) * 2, idS, kk > 0 ? 1u : 0u);
+          if (nt == 1 || qt == 0) umma::commit(&st->bars[kSFull + (steps[0] & 1)]);
+          if (nt == 1 || qt == 1) umma::commit(&st->bars[kSFull + 2 + (steps[1] & 1)]);
+          if (qt == nt - 1) umma::commit(&st->bars[kKEmpty + (tiles & 1)]);
+          if (i >= count - nt) umma::commit(&st->bars[kQEmpty + qs]);
+          if (p_due) products();
+          p_due = true;
+          p_wg = nt == 1 ? -1 : qt;
+          p_step[0] = steps[0];
+          p_step[1] = steps[1];
+          p_tile = tiles;
+          p_item = item;
+          p_first = i < nt;
+          p_last = qt == nt - 1;
+          ++xs;
+          if (nt == 1 || qt == 0) ++steps[0];
+          if (nt == 1 || qt == 1) ++steps[1];
+          if (qt == nt - 1) ++tiles;
+        }
+        q += nt;
       }
-      q += nt;
-    }
-    if (ok && p_due) products();
-    // every MMA issued has completed before the tensor memory is freed
-    umma::commit(&st->bars[kDrain]);
-    (void)mbar_wait_bounded(&st->bars[kDrain], 0);
-    if (!ok) {
-      st->abort = 1;
-      if (lane == 0) raise_device_error(p.err, kErrTimeout);
-    }
-  } else if (warp < 4) {
-    less_registers<kRegsControl>();
-    // ---- what the fold needs of an item that goes on in the next block's range ----------------------
-    if (warp == 0) {
+      if (ok && p_due) products();
+      // every MMA issued has completed before the tensor memory is freed
+      umma::commit(&st->bars[kDrain]);
+      (void)mbar_wait_bounded(&st->bars[kDrain], 0);
+      if (!ok) {
+        st->abort = 1;
+        if (lane == 0) raise_device_error(p.err, kErrTimeout);
+      }
+    } else if (warp == 0) {
+      // ---- what the fold needs of an item that goes on in the next block's range ----------------------
       Walk it;
       int64_t at = rg->from;
       TreeSplit::Tail tail = {0, 0, 0, 0};

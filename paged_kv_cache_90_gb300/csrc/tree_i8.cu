@@ -543,113 +543,113 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
   Walk it;
   it.start(p, sp, rg);
 
-  // (each role takes its registers itself: the compiler counts them by branch)
-  if (warp == 0 || warp == 3) {
+  // (a warpgroup takes its registers together, by one instruction, and its roles part behind it; the
+  // compiler counts registers by branch)
+  if (warp < 4) {
     less_registers<kRegsControl>();
-    // ---- codes, K by one warp and V by another, every second tile of the ring each: one bulk copy
-    // per block of the cache (copies issued side by side from one warp go one by one, about 100
-    // clocks each).  The first also copies the tokens' scales, four tokens to a lane ------------
-    const int v = warp == 3, bs = p.block_size;
-    const unsigned char* cache = static_cast<const unsigned char*>(v ? p.value_cache : p.key_cache);
-    const uint32_t bytes = uint32_t(bs) * D;
-    int slot = v, n = v;  // of the ring: tile and tile copies before this one
-    uint32_t phase = 0;
-    // tile j of `it` is looked up one tile before its copies are issued, over items too (up to
-    // 64 blocks of two tokens: two to a lane)
-    int j = it.valid() ? it.j0 : 0, kvh = 0, left = 0, nblk = 0, e0 = 0, e1 = 0;
-    int tiles = 0, sslot = 0;  // of the scales' ring
-    uint32_t sphase = 0;
-    bool have = false;
-    while (true) {
-      const int kvh_now = kvh, left_now = left, nblk_now = nblk;
-      int now[2] = {e0, e1};
-      const bool copy = have;
-      have = it.valid();
-      if (have) {
-        const int pos = it.q.base + j * kBN;
-        kvh = it.kvh;
-        left = max(0, min(kBN, it.q.e.L - pos));
-        nblk = (left + bs - 1) >> sp.bs_shift;
-        const int32_t* row = p.block_tables + int64_t(it.s) * p.bt_stride + (pos >> sp.bs_shift);
-        e0 = lane < nblk ? __ldg(row + lane) : 0;
-        e1 = lane + 32 < nblk ? __ldg(row + lane + 32) : 0;
-        if (++j == it.j1) {
-          it.next(p, sp, rg);
-          j = it.j0;
+    if (warp == 0 || warp == 3) {
+      // ---- codes, K by one warp and V by another, every second tile of the ring each: one bulk copy
+      // per block of the cache (copies issued side by side from one warp go one by one, about 100
+      // clocks each).  The first also copies the tokens' scales, four tokens to a lane ------------
+      const int v = warp == 3, bs = p.block_size;
+      const unsigned char* cache = static_cast<const unsigned char*>(v ? p.value_cache : p.key_cache);
+      const uint32_t bytes = uint32_t(bs) * D;
+      int slot = v, n = v;  // of the ring: tile and tile copies before this one
+      uint32_t phase = 0;
+      // tile j of `it` is looked up one tile before its copies are issued, over items too (up to
+      // 64 blocks of two tokens: two to a lane)
+      int j = it.valid() ? it.j0 : 0, kvh = 0, left = 0, nblk = 0, e0 = 0, e1 = 0;
+      int tiles = 0, sslot = 0;  // of the scales' ring
+      uint32_t sphase = 0;
+      bool have = false;
+      while (true) {
+        const int kvh_now = kvh, left_now = left, nblk_now = nblk;
+        int now[2] = {e0, e1};
+        const bool copy = have;
+        have = it.valid();
+        if (have) {
+          const int pos = it.q.base + j * kBN;
+          kvh = it.kvh;
+          left = max(0, min(kBN, it.q.e.L - pos));
+          nblk = (left + bs - 1) >> sp.bs_shift;
+          const int32_t* row = p.block_tables + int64_t(it.s) * p.bt_stride + (pos >> sp.bs_shift);
+          e0 = lane < nblk ? __ldg(row + lane) : 0;
+          e1 = lane + 32 < nblk ? __ldg(row + lane + 32) : 0;
+          if (++j == it.j1) {
+            it.next(p, sp, rg);
+            j = it.j0;
+          }
         }
-      }
-      if (!copy) {
-        if (!have) break;
-        continue;
-      }
+        if (!copy) {
+          if (!have) break;
+          continue;
+        }
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-        if (now[u] < 0 || int64_t(now[u]) >= p.num_blocks) {
-          raise_device_error(p.err, kErrTableEntry);
-          now[u] = 0;
-        }
-      bool ok = true;
-      if (n >= C::kSlots) ok = wait_warp(st, kCodeEmpty + slot, phase ^ 1u);
-      if (ok) {
-        if (lane == 0) mbar_arrive_expect_tx(&st->bars[kCodeFull + slot], uint32_t(nblk_now) * bytes);
-        __syncwarp();
-        unsigned char* dst = smem + C::kCodes + slot * C::kCodeBytes;
+        for (int u = 0; u < 2; ++u)
+          if (now[u] < 0 || int64_t(now[u]) >= p.num_blocks) {
+            raise_device_error(p.err, kErrTableEntry);
+            now[u] = 0;
+          }
+        bool ok = true;
+        if (n >= C::kSlots) ok = wait_warp(st, kCodeEmpty + slot, phase ^ 1u);
+        if (ok) {
+          if (lane == 0) mbar_arrive_expect_tx(&st->bars[kCodeFull + slot], uint32_t(nblk_now) * bytes);
+          __syncwarp();
+          unsigned char* dst = smem + C::kCodes + slot * C::kCodeBytes;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int b = lane + 32 * u;
-          if (b < nblk_now)
-            bulk_copy_g2s(dst + b * bytes, cache + int64_t(now[u]) * p.cs_block + int64_t(kvh_now) * p.cs_head, bytes,
-                          &st->bars[kCodeFull + slot]);
+          for (int u = 0; u < 2; ++u) {
+            const int b = lane + 32 * u;
+            if (b < nblk_now)
+              bulk_copy_g2s(dst + b * bytes, cache + int64_t(now[u]) * p.cs_block + int64_t(kvh_now) * p.cs_head, bytes,
+                            &st->bars[kCodeFull + slot]);
+          }
         }
-      }
-      n += 2;
-      slot += 2;
-      if (slot >= C::kSlots) {
-        slot -= C::kSlots;
-        phase ^= 1u;
-      }
-      if (v) continue;
-      // the tokens' scales: asynchronous copies of four tokens' 16 bytes where they are aligned
-      // (their block's entry is in lane token / bs), else of each (the upper 32 blocks of two
-      // tokens in the second register)
-      if (tiles >= kScaleSlots) (void)wait_warp(st, kScaleEmpty + sslot, sphase ^ 1u);
-      float* kd = &st->scales[sslot][0][4 * lane];
-      float* vd = &st->scales[sslot][1][4 * lane];
-      const int64_t head = int64_t(kvh_now) * p.ts_head;
-      if (sp.vec_scales) {
-        const int e = __shfl_sync(0xffffffffu, now[0], (4 * lane) >> sp.bs_shift);
-        const bool there = 4 * lane < left_now;
-        const int64_t at = there ? int64_t(e) * p.ts_block + head + ((4 * lane) & (bs - 1)) : 0;
-        copy16(kd, p.k_token_scales + at, there);
-        copy16(vd, p.v_token_scales + at, there);
-      } else {
+        n += 2;
+        slot += 2;
+        if (slot >= C::kSlots) {
+          slot -= C::kSlots;
+          phase ^= 1u;
+        }
+        if (v) continue;
+        // the tokens' scales: asynchronous copies of four tokens' 16 bytes where they are aligned
+        // (their block's entry is in lane token / bs), else of each (the upper 32 blocks of two
+        // tokens in the second register)
+        if (tiles >= kScaleSlots) (void)wait_warp(st, kScaleEmpty + sslot, sphase ^ 1u);
+        float* kd = &st->scales[sslot][0][4 * lane];
+        float* vd = &st->scales[sslot][1][4 * lane];
+        const int64_t head = int64_t(kvh_now) * p.ts_head;
+        if (sp.vec_scales) {
+          const int e = __shfl_sync(0xffffffffu, now[0], (4 * lane) >> sp.bs_shift);
+          const bool there = 4 * lane < left_now;
+          const int64_t at = there ? int64_t(e) * p.ts_block + head + ((4 * lane) & (bs - 1)) : 0;
+          copy16(kd, p.k_token_scales + at, there);
+          copy16(vd, p.v_token_scales + at, there);
+        } else {
 #pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-          const int b = (4 * lane + i) >> sp.bs_shift;
-          const int ea = __shfl_sync(0xffffffffu, now[0], b & 31), eb = __shfl_sync(0xffffffffu, now[1], b & 31);
-          const bool there = 4 * lane + i < left_now;
-          const int64_t at = there ? int64_t(b < 32 ? ea : eb) * p.ts_block + head + ((4 * lane + i) & (bs - 1)) : 0;
-          copy4(kd + i, p.k_token_scales + at, there);
-          copy4(vd + i, p.v_token_scales + at, there);
+          for (int i = 0; i < 4; ++i) {
+            const int b = (4 * lane + i) >> sp.bs_shift;
+            const int ea = __shfl_sync(0xffffffffu, now[0], b & 31), eb = __shfl_sync(0xffffffffu, now[1], b & 31);
+            const bool there = 4 * lane + i < left_now;
+            const int64_t at = there ? int64_t(b < 32 ? ea : eb) * p.ts_block + head + ((4 * lane + i) & (bs - 1)) : 0;
+            copy4(kd + i, p.k_token_scales + at, there);
+            copy4(vd + i, p.v_token_scales + at, there);
+          }
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_addr(&st->bars[kScaleFull + sslot]))
+                     : "memory");
+        ++tiles;
+        if (++sslot == kScaleSlots) {
+          sslot = 0;
+          sphase ^= 1u;
         }
       }
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_addr(&st->bars[kScaleFull + sslot]))
-                   : "memory");
-      ++tiles;
-      if (++sslot == kScaleSlots) {
-        sslot = 0;
-        sphase ^= 1u;
-      }
-    }
-    // the copies in flight land before the block may exit
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    if (lane == 0)
-      for (int k = max(0, n - C::kSlots); k < n; ++k)
-        if ((k & 1) == v) (void)mbar_wait_bounded(&st->bars[kCodeFull + k % C::kSlots], uint32_t(k / C::kSlots) & 1u);
-  } else if (warp == 1) {
-    less_registers<kRegsControl>();
-    // ---- score MMAs (a warp, see umma.cuh; the products' are another's: each waits only for its own) ----
-    {
+      // the copies in flight land before the block may exit
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (lane == 0)
+        for (int k = max(0, n - C::kSlots); k < n; ++k)
+          if ((k & 1) == v) (void)mbar_wait_bounded(&st->bars[kCodeFull + k % C::kSlots], uint32_t(k / C::kSlots) & 1u);
+    } else if (warp == 1) {
+      // ---- score MMAs (a warp, see umma.cuh; the products' are another's: each waits only for its own) ----
       const uint32_t base = smem_addr(smem);
       constexpr uint64_t kUnit = C::kUnitBytes >> 4;  // (descriptors hold addresses / 16)
       const uint64_t kdesc = tc::desc_sw128(base + C::kK, 16, 1024), qdesc = tc::desc_sw128(base + C::kQ, 16, 1024);
@@ -680,11 +680,8 @@ tree_i8_kernel(const __grid_constant__ TreeParams p, const __grid_constant__ Tre
       umma::commit(&st->bars[kDrain]);
       (void)mbar_wait_bounded(&st->bars[kDrain], 0);
       if (!ok && lane == 0) raise_device_error(p.err, kErrTimeout);
-    }
-  } else if (warp == 2) {
-    less_registers<kRegsControl>();
-    // ---- product MMAs (a warp) -------------------------------------------------------------
-    {
+    } else {
+      // ---- product MMAs (a warp) -------------------------------------------------------------
       const uint32_t base = smem_addr(smem);
       constexpr uint64_t kUnit = C::kUnitBytes >> 4;
       // (a head of 64 columns has one chunk of them: the second 64 rows of the MMA repeat it)
