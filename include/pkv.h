@@ -457,8 +457,9 @@ pkv_status pkv_rotary_axes_and_cache(const pkv_tensor* query_out, const pkv_tens
  * factor f (its descriptor's `scale`, or head_scales[h]), all in IEEE binary32:
  *   G = a / (6 f), at most 448, rounded to e4m3          (the group's scale)
  *   code = x * (1 / (G f)), at most 6 in magnitude, rounded to e2m1
- * both to nearest, ties to even.  An element is off by at most a / 5.  Values beyond 2688 f are
- * cut off there and groups below 0.0058 f vanish (G = 0), so f is set where values are far from 1.
+ * both to nearest, ties to even.  An element is off by at most a / 5 where a is 0.0176 f to 2688 f,
+ * and by at most a / 3 below that, down to 0.0059 f; groups below 0.0058 f vanish (G = 0), and values
+ * beyond 2688 f are cut off there.  So f is set where values are far from 1.
  * A G f below 2^-126 or above 2^126 is stored as G = 0 with codes of 0, a group holding an infinity
  * or a NaN as G = NaN with codes of 0.
  *
