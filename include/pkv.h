@@ -395,8 +395,9 @@ pkv_status pkv_rotary_init(pkv_rotary* rotary, int32_t rotary_dim, int32_t inter
  * For token t: query_out[t, h] = rotate(query[t, h], positions[t]) for every query head,
  * and, with slot = slot_mapping[t] >= 0, the cache write of pkv_reshape_and_cache with
  * rotate(key[t, h], positions[t]) in place of the key.  The rotation is computed in
- * binary32 and rounded once, to the query's dtype or to what the cache stores.  A token
- * with slot < 0 has its query rotated and nothing written.
+ * binary32, its cosines and sines within 3e-7 at any position, and rounded once, to the
+ * query's dtype or to what the cache stores.  A token with slot < 0 has its query rotated
+ * and nothing written.
  *
  * query_out, query [num_tokens, num_heads, head_dim] f32 or bf16, last dim contiguous;
  *                  query_out may be query itself (same pointer and strides), otherwise

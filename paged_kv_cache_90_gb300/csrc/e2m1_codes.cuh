@@ -45,7 +45,7 @@ __device__ __forceinline__ float scale1(uint32_t byte) {
 }
 
 // A cache's factor f, and division by 6 f.  (Made once where it serves all rows: the reciprocal in it
-// costs more than the rest of a group's scale.)
+// costs more than the rest of a group's scale; the rotary write makes it for each row.)
 struct Factor {
   float f;
   DivRn six;

@@ -4,7 +4,7 @@
 // Both move bytes and nothing else: HBM bounds the large calls (twice the moved bytes) and the
 // launch the small ones, which is why one launch takes the caches of all layers: their descriptors
 // travel in its parameters.  150 blocks of 16 tokens, 8 heads of 128 in bf16, in 32 caches (157 MB read, as
-// much written): 49 us, 6.4 TB/s.  Three blocks in 8 caches: 1.9 us of the GPU's time, 5.7 of the
+// much written): 49 us, 6.4 TB/s, with one pool or several in turn.  Three blocks in 8 caches: 1.9 us of the GPU's time, 5.7 of the
 // caller's.  48 sequences that keep some of their 8 to 24 drafted tokens in 24 int8 caches and their
 // scales: 5.8 us of the GPU's time (four round trips: lengths, kept nodes, table entries, rows), 10
 // of the caller's.

@@ -12,9 +12,10 @@
 // 71 us, 5.7 TB/s (a block per token with the cosines in shared memory: 175 us); quantising
 // write of 16384 tokens of 2 x 8 heads 31 us, read back into f32 26 us (168 MB, 6.4 TB/s).  The
 // write is held back by its instructions, 190 for 8 columns of two rows, issued in four of five
-// cycles.  Into a 4-bit cache the same write takes 21 us (86 MB; instructions in three of four
-// cycles), read back into f32 25 us (153 MB, 6 TB/s); the rotary write with three position axes in
-// turn over the pairs 73 us, 5.6 TB/s.
+// cycles.  Into a 4-bit cache the same write takes 19 us (86 MB; instructions in three of four
+// cycles), read back into f32 27 us (153 MB, 5.6 TB/s; both over buffers that L2 does not hold); the
+// rotary write with three position axes in turn over the pairs 73 us, 5.5 TB/s, and into a 4-bit
+// cache, with one axis or three, 82 us (354 MB, 4.3 TB/s).
 #include "device_common.cuh"
 #include "e2m1_codes.cuh"
 #include "token_internal.h"
@@ -39,7 +40,9 @@ __device__ __forceinline__ T one_answer(T x) { return __shfl_sync(0xffffffffu, x
 enum Layout { kPairs, kHalves, kOdd };
 
 // What a rotary write does beside the common case, each kind compiled by itself: with the tests for
-// both in one kernel a prefill step's write took 75 us instead of 71.
+// both in one kernel a prefill step's write took 75 us instead of 71.  kFour is held back by its
+// instructions: it makes a row's factor anew in every pass and a group's scale in two lanes, and brings
+// all layouts' columns in order through shared memory (82 us where the bytes take 53).
 enum Kind { kPlain, kAxes, kFour };  // several position axes; a 4-bit cache (with or without them)
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -466,7 +469,7 @@ __global__ void __launch_bounds__(32 * kWarps) token_quantize_kernel(const __gri
 
 // And into a 4-bit cache alone.  A lane has a group's 16 columns: its scale, a division and a
 // reciprocal, is computed once and no lane waits for another's maximum: 15.4 M warp instructions
-// for 16384 tokens of 2 x 8 heads in bf16 and 20.7 us, with eight columns a lane 23.0 M and 26.8 us.
+// for 16384 tokens of 2 x 8 heads in bf16 and 20.7 us (cold), with eight columns a lane 23.0 M and 26.8 us.
 // Eight blocks an SM, for which 7 registers are spilled (write and read back 44.5 us; 45.4 with seven
 // blocks, 45.5 with six; 45.1 with the loads of two passes together).
 template <typename Src, int D>
